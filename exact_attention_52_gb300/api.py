@@ -20,13 +20,20 @@ DEBUG_LIB_PATH = os.path.join(_PKG, "libattn_sm103a_debug.so")
 
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED",
-                -3: "ATTN_ERR_CUDA", -4: "ATTN_ERR_TIMEOUT"}
-
+                -3: "ATTN_ERR_CUDA", -4: "ATTN_ERR_TIMEOUT", -5: "ATTN_ERR_PAGE"}
 
 
 class Strides(ctypes.Structure):
     """attn_strides_t: element strides (b, h, n) of a [B, heads, N, d] view."""
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
+
+
+class Cache(ctypes.Structure):
+    """attn_cache_t: the paged 8-bit key/value cache of a call."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("ks", Strides), ("vs", Strides),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 # Every symbol the header declares, with (restype, argtypes).
@@ -54,6 +61,10 @@ SIGNATURES = {
     "attn_bwd_strided": (_i, [_vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _st, _vp,
                               _st, _vp, _st, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _vp]),
     "attn_fwd_fp8": (_i, [_vp, _vp, _vp, _f, _f, _f, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
+    "attn_cache_append": (_i, [ctypes.POINTER(Cache), _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _vp]),
+    "attn_fwd_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_fwd_cache": (_i, [ctypes.POINTER(Cache), _vp, _st, _vp, _st, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
+                            _i, _i, _vp]),
     "attn_check_device_error": (_i, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
     "attn_set_exp2_offload": (None, [_i]),
@@ -386,3 +397,141 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
         dv.data_ptr(), st(dv), workspace.data_ptr(), B, H, Hk, N, d, scale, int(window[0]),
         int(window[1]), _stream_handle(stream)))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# Paged 8-bit key/value cache
+# ---------------------------------------------------------------------------
+def _check_on(device, name, t, dtype, ndim):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype or t.dim() != ndim:
+        raise ValueError(f"{name} must be {dtype} with {ndim} dimensions, got {t.dtype} {tuple(t.shape)}")
+
+
+def _call_device(t, name):
+    """The device a call runs on: that of its tensors, which has to be the current one."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _on_stream(stream):
+    """Context in which what a call allocates belongs to the stream that the call runs on."""
+    import contextlib
+
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _cache_arg(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens):
+    import torch
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _check_on(device, name, t, torch.uint8, 4)
+    P, heads, page, dim = k_pages.shape
+    if v_pages.shape != k_pages.shape or heads != Hk or dim != d:
+        raise ValueError(f"k_pages and v_pages must be [pages, {Hk}, page_size, {d}], got "
+                         f"{tuple(k_pages.shape)} and {tuple(v_pages.shape)}")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        _check_on(device, name, t, torch.float32, 2)
+        if t.shape != (P, Hk) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{P}, {Hk}]")
+    _check_on(device, "page_table", page_table, torch.int32, 2)
+    if page_table.shape[0] != B or page_table.shape[1] < 1 or page_table.stride(1) != 1:
+        raise ValueError(f"page_table must be [{B}, pages] with contiguous rows")
+    _check_lens(device, "seq_lens", seq_lens, B)
+    ks, vs = k_pages.stride(), v_pages.stride()
+    if ks[3] != 1 or vs[3] != 1:
+        raise ValueError("the last (d) dimension of the pages must be contiguous")
+    return Cache(k_pages.data_ptr(), v_pages.data_ptr(), Strides(*ks[:3]), Strides(*vs[:3]), k_scale.data_ptr(),
+                 v_scale.data_ptr(), page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr(), P, page,
+                 page_table.shape[1])
+
+
+def _check_lens(device, name, t, B):
+    import torch
+    _check_on(device, name, t, torch.int32, 1)
+    if t.shape[0] != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{B}]")
+
+
+def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens=None,
+                 layout: str = "bhnd", stream=None):
+    """Write new tokens into a paged 8-bit cache, in place.
+
+    k, v: bf16 [B, Hk, T, d] (``layout`` "bhnd") or [B, T, Hk, d] ("bnhd"), any strides with
+    a contiguous last dimension.  k_pages, v_pages: uint8 E4M3 codes [pages, Hk, page_size, d],
+    any strides with a contiguous last dimension; k_scale, v_scale: fp32 [pages, Hk].
+    page_table: int32 [B, max_pages]; seq_lens: int32 [B], tokens of each sequence after the
+    call; new_lens: int32 [B], how many of the T tokens are new (default: all): token t goes to
+    position seq_lens - new_lens + t.  A page's scale is a power of two that covers its largest
+    value and grows with it, the codes that are there being rounded again."""
+    import torch
+    device = _call_device(k, "k")
+    _check_on(device, "k", k, torch.bfloat16, 4)
+    _check_on(device, "v", v, torch.bfloat16, 4)
+    if k.shape != v.shape:
+        raise ValueError(f"k and v must have the same shape, got {tuple(k.shape)} and {tuple(v.shape)}")
+    ks, vs = _bhnd_strides(k, layout), _bhnd_strides(v, layout)
+    B, Hk, T, d = _bhnd_shape(k, layout)
+    cache = _cache_arg(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens)
+    if new_lens is not None:
+        _check_lens(device, "new_lens", new_lens, B)
+    _check("attn_cache_append", load_library().attn_cache_append(
+        ctypes.byref(cache), k.data_ptr(), ks, v.data_ptr(), vs,
+        None if new_lens is None else new_lens.data_ptr(), B, Hk, T, d, _stream_handle(stream)))
+
+
+def fwd_cache_workspace_bytes(B: int, H: int, Hk: int, T: int, d: int) -> int:
+    return int(load_library().attn_fwd_cache_workspace_bytes(B, H, Hk, T, d))
+
+
+def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_lens=None,
+              layout: str = "bhnd", scale: float | None = None, window_left: int = -1, sinks: int = 0,
+              o=None, lse=None, workspace=None, stream=None):
+    """Attention of T new queries per sequence over a paged 8-bit cache (see ``cache_append``),
+    their own tokens included; returns (O bf16 like q, LSE fp32 [B, H, T]).
+
+    q: bf16 [B, H, T, d] or, with ``layout`` "bnhd", [B, T, H, d]; H a multiple of the cache's
+    heads.  Query t of q_lens[b] (default T) sits at position p = seq_lens[b] - q_lens[b] + t and
+    sees key j iff j <= p and (window_left is -1, or j >= p - window_left, or j < sinks).  Rows
+    behind q_lens[b] are left as they were; a row that sees nothing gives 0 and LSE +inf.
+    ``workspace``: ``fwd_cache_workspace_bytes`` bytes, one for each call that may overlap."""
+    import torch
+    device = _call_device(q, "q")
+    _check_on(device, "q", q, torch.bfloat16, 4)
+    qs = _bhnd_strides(q, layout)
+    B, H, T, d = _bhnd_shape(q, layout)
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a tensor [pages, Hk, page_size, d]")
+    Hk = k_pages.shape[1]
+    cache = _cache_arg(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens)
+    if q_lens is not None:
+        _check_lens(device, "q_lens", q_lens, B)
+    lib = load_library()
+    need = int(lib.attn_fwd_cache_workspace_bytes(B, H, Hk, T, d))
+    if need == 0:
+        raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, T {T}, d {d}")
+    with _on_stream(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _check_on(device, "o", o, torch.bfloat16, 4)
+    _check_on(device, "lse", lse, torch.float32, 3)
+    if o.shape != q.shape or lse.shape != (B, H, T) or not lse.is_contiguous():
+        raise ValueError(f"o must have q's shape and lse be a contiguous {(B, H, T)}")
+    if workspace.device != device or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace needs {need} bytes on {device}")
+    _check("attn_fwd_cache", lib.attn_fwd_cache(
+        ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), _bhnd_strides(o, layout), lse.data_ptr(),
+        workspace.data_ptr(), None if q_lens is None else q_lens.data_ptr(), B, H, Hk, T, d,
+        1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(sinks),
+        _stream_handle(stream)))
+    return o, lse

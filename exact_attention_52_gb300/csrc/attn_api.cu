@@ -479,6 +479,51 @@ Strides from_abi(const attn_strides_t& s) {
     return r;
 }
 
+attn_status cache_view(const attn_cache_t* c, int B, CacheView* out) {
+    if (c == nullptr || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return ATTN_ERR_INVALID;
+    for (const void* p : {static_cast<const void*>(c->k_scale), static_cast<const void*>(c->v_scale),
+                          static_cast<const void*>(c->page_table), static_cast<const void*>(c->seq_lens)})
+        if (p == nullptr || (reinterpret_cast<uintptr_t>(p) & 3u) != 0) return ATTN_ERR_INVALID;
+    if (c->num_pages < 1 || c->max_pages < 1 || (B > 1 && c->table_stride < c->max_pages) ||
+        c->table_stride < 0 || c->table_stride > kMaxElems)
+        return ATTN_ERR_INVALID;
+    const int ps = c->page_size;
+    if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0 || c->max_pages > (1 << 30) / ps) return ATTN_ERR_INVALID;
+    out->ks = from_abi(c->ks);
+    out->vs = from_abi(c->vs);
+    if (!strides_ok(out->ks, 1) || !strides_ok(out->vs, 1)) return ATTN_ERR_INVALID;
+    out->k_pages = static_cast<uint8_t*>(c->k_pages);
+    out->v_pages = static_cast<uint8_t*>(c->v_pages);
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->table = c->page_table;
+    out->table_stride = c->table_stride;
+    out->seq_lens = c->seq_lens;
+    out->num_pages = c->num_pages;
+    out->page_size = ps;
+    out->max_pages = c->max_pages;
+    out->page_shift = 0;
+    while ((1 << out->page_shift) < ps) ++out->page_shift;
+    return ATTN_OK;
+}
+
+// CTAs that share a cache attention's work on the current device.
+attn_status cache_grid(int* grid) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return ATTN_ERR_CUDA;
+    *grid = sms * cache_decode_ctas_per_sm();
+    return ATTN_OK;
+}
+
+// The workspace is laid out for kCacheGridMax CTAs whatever the device, so that
+// its size needs no device.
+constexpr int kCacheGridMax = 1024;
+constexpr int kCacheRows = 16;
+size_t cache_part_bytes(int d) { return static_cast<size_t>(2) * kCacheGridMax * kCacheRows * d * sizeof(float); }
+
+
 }  // namespace
 
 int check_problem(int B, int H, int N, int d, float scale, int causal) {
@@ -713,6 +758,72 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
                    workspace, B, H, Hk, N, d, scale, window_left, window_right, stream);
 }
 
+attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_strides_t ks, const void* v,
+                              attn_strides_t vs, const int32_t* new_lens, int B, int Hk, int T, int d,
+                              attn_stream_t stream) {
+    attn_status rc = check_sizes(B, Hk, T, d, 1.f, 0);
+    if (rc != ATTN_OK) return rc;
+    CacheAppendParams p;
+    if ((rc = cache_view(cache, B, &p.c)) != ATTN_OK) return rc;
+    if (B > 32767 || Hk > 65535) return ATTN_ERR_INVALID;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(new_lens) & 3u) != 0) return ATTN_ERR_INVALID;
+    p.k = k;
+    p.v = v;
+    p.ks = from_abi(ks);
+    p.vs = from_abi(vs);
+    if (!strides_ok(p.ks, 2) || !strides_ok(p.vs, 2)) return ATTN_ERR_INVALID;
+    p.new_lens = new_lens;
+    p.B = B;
+    p.Hk = Hk;
+    p.T = T;
+    p.D = d;
+    DeviceState ds;
+    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
+    p.st = dev_status(ds);
+    return launch_cache_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d) {
+    if (check_sizes(B, H, T, d, 1.f, 0) != ATTN_OK || check_group(H, Hk) != ATTN_OK) return 0;
+    return cache_part_bytes(d) + static_cast<size_t>(2) * kCacheGridMax * kCacheRows * sizeof(float2);
+}
+
+attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o, attn_strides_t os,
+                           float* lse, void* workspace, const int32_t* q_lens, int B, int H, int Hk, int T, int d,
+                           float scale, int window_left, int sinks, attn_stream_t stream) {
+    attn_status rc = check_sizes(B, H, T, d, scale, 0);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(window_left, sinks - 1)) != ATTN_OK) return rc;
+    CacheFwdParams p;
+    if ((rc = cache_view(cache, B, &p.c)) != ATTN_OK) return rc;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(q_lens) & 3u) != 0)
+        return ATTN_ERR_INVALID;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
+    p.q = q;
+    p.o = o;
+    p.qs = from_abi(qs);
+    p.os = from_abi(os);
+    if (!strides_ok(p.qs, 2) || !strides_ok(p.os, 2)) return ATTN_ERR_INVALID;
+    p.lse = lse;
+    p.q_lens = q_lens;
+    p.B = B;
+    p.H = H;
+    p.Hk = Hk;
+    p.T = T;
+    p.D = d;
+    p.cs = scale * 1.44269504088896340736f;
+    p.left = window_left;
+    p.sinks = sinks;
+    p.part = static_cast<float*>(workspace);
+    p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + cache_part_bytes(d));
+    DeviceState ds;
+    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
+    p.st = dev_status(ds);
+    if ((rc = cache_grid(&p.grid)) != ATTN_OK) return rc;
+    if (p.grid > kCacheGridMax) p.grid = kCacheGridMax;
+    return launch_cache_decode(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
 attn_status attn_check_device_error(attn_stream_t stream, unsigned int* site) {
     if (site) *site = 0;
     DeviceState ds;
@@ -726,6 +837,7 @@ attn_status attn_check_device_error(attn_stream_t stream, unsigned int* site) {
         cudaMemcpy(ds.err, zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
         return ATTN_ERR_CUDA;
     if (site) *site = host[1];
+    if (host[0] == ATTN_DEVERR_PAGE) return ATTN_ERR_PAGE;
     return host[0] ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }
 
@@ -751,6 +863,7 @@ const char* attn_status_string(attn_status s) {
         case ATTN_ERR_UNSUPPORTED: return "ATTN_ERR_UNSUPPORTED";
         case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA";
         case ATTN_ERR_TIMEOUT: return "ATTN_ERR_TIMEOUT";
+        case ATTN_ERR_PAGE: return "ATTN_ERR_PAGE";
     }
     return "ATTN_ERR_UNKNOWN";
 }

@@ -15,6 +15,7 @@ enum : uint32_t {
     ATTN_DEVERR_SMEM_ALIGN = 2u,    // dynamic shared memory was not 1024-byte aligned
     ATTN_DEVERR_RANGE = 4u,         // debug builds: a TMA coordinate or tensor-memory address
                                     // failed its range check (the access was skipped)
+    ATTN_DEVERR_PAGE = 8u,          // a page table entry or a length outside the cache
 };
 
 struct DevStatus {

@@ -111,6 +111,48 @@ struct DqConvertParams {
     float scale;
 };
 
+// Paged 8-bit key/value cache (attn_cache_t, checked and with the page size as a
+// shift).  Code address: pages + page * b + head * h + token * n (bytes).
+struct CacheView {
+    uint8_t* k_pages;
+    uint8_t* v_pages;
+    Strides ks, vs;
+    float* k_scale;  // [num_pages, Hk]
+    float* v_scale;
+    const int* table;  // [B, max_pages], rows table_stride apart
+    long long table_stride;
+    const int* seq_lens;  // [B]
+    int num_pages, page_size, page_shift, max_pages;
+};
+
+struct CacheAppendParams {
+    CacheView c;
+    const void* k;  // bf16 [B, Hk, T, D] with strides ks
+    const void* v;
+    Strides ks, vs;
+    const int* new_lens;  // [B] or null: T
+    int B, Hk, T, D;
+    DevStatus st;
+};
+
+// Segments a CTA of the cache attention can leave unfinished: the one it starts
+// inside and the one it ends inside.
+struct CacheFwdParams {
+    CacheView c;
+    const void* q;  // bf16 [B, H, T, D] with strides qs
+    void* o;        // bf16, strides os
+    Strides qs, os;
+    float* lse;         // fp32 [B, H, T]
+    const int* q_lens;  // [B] or null: T
+    int B, H, Hk, T, D;
+    float cs;  // scale * log2(e)
+    int left, sinks;
+    int grid;      // CTAs that share the work
+    float* part;   // unfinished segments: fp32 [2 * grid][rows][D]
+    float2* stat;  // their maximum (log2 units) and sum: [2 * grid][rows]
+    DevStatus st;
+};
+
 // Launchers (return the launch's cudaError_t; no synchronisation).
 cudaError_t launch_fwd_bf16(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const FwdParams& p, cudaStream_t stream);
@@ -122,6 +164,9 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const CUtensorMap& tdo, const CUtensorMap& tdq,
                             const BwdParams& p, cudaStream_t stream);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
+cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream);
+int cache_decode_ctas_per_sm();
 cudaError_t launch_wait_selftest(DevStatus st, cudaStream_t stream);
 
 // Problem check shared by the entry points (sizes, head dim, scale, causal

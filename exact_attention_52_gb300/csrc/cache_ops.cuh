@@ -1,0 +1,108 @@
+// Building blocks of the kernels over the paged 8-bit key/value cache: which
+// keys a sequence's new queries see, how a page's address is formed, the E4M3
+// conversions and per-thread asynchronous copies.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+
+namespace attn {
+
+// The new queries of one sequence and the keys they see.  Query t of q_len sits
+// at position len - q_len + t; key j is visible to position p iff j <= p and
+// (left < 0, or j >= p - left, or j < sinks).  Keys are walked in blocks of TB
+// tokens: the n_sink first blocks (sinks), then n - n_sink blocks from block lo
+// on (everything between is seen by no query and is not read).
+struct CacheSeq {
+    int len, q_len, n, n_sink, lo;
+    int key_lo;  // first key of the window of the first query
+};
+
+template <int TB>
+__device__ __forceinline__ CacheSeq cache_seq(const CacheView& c, const int* q_lens, int T, int left, int sinks,
+                                              int b) {
+    CacheSeq s;
+    const int cap = c.max_pages * c.page_size;
+    s.len = min(max(c.seq_lens[b], 0), cap);
+    s.q_len = q_lens ? min(max(q_lens[b], 0), T) : T;
+    const int first = max(0, s.len - s.q_len);
+    s.key_lo = left < 0 ? 0 : max(0, first - left);
+    s.lo = s.key_lo / TB;
+    s.n_sink = min((min(sinks, s.key_lo) + TB - 1) / TB, s.lo);
+    s.n = s.len > 0 ? s.n_sink + (s.len - 1) / TB - s.lo + 1 : 1;
+    return s;
+}
+
+// Block v of the walk -> block of the sequence.
+__device__ __forceinline__ int cache_block(const CacheSeq& s, int v) { return v < s.n_sink ? v : s.lo + v - s.n_sink; }
+
+// Page of token `tok` of sequence b.  An entry outside the pool is recorded in
+// the error word and read as page 0, so that no access leaves the pool.
+__device__ __forceinline__ int cache_page(const CacheView& c, const DevStatus& st, int b, int tok) {
+    const int pid = __ldg(c.table + static_cast<long long>(b) * c.table_stride + (tok >> c.page_shift));
+    if (static_cast<unsigned>(pid) >= static_cast<unsigned>(c.num_pages)) {
+        record_device_error(st, ATTN_DEVERR_PAGE, 0x301);
+        return 0;
+    }
+    return pid;
+}
+
+// A thread's own asynchronous copy of 16, 8 or 4 bytes; with `there` false the
+// destination is filled with zeros and nothing is read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(there ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four E4M3 codes (bytes 0-1, bytes 2-3 of w) as two f16 pairs; exact (every
+// E4M3 number is an f16 number).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+// Two floats -> packed f16x2 (round to nearest even); `lo` in bits 15..0.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// D (16x8, fp32) += A (16x16, f16) B (16x8, f16).
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Power of two that brings a row whose largest finite magnitude is `amax` to
+// [2^7, 2^8): bf16 values of the row are then exact in f16 down to 2^-24 of that
+// largest one, and what lies below is off by at most 2^-32 of it.  Its inverse is
+// the power of two with biased exponent 254 minus its own.
+__device__ __forceinline__ float f16_row_scale(float amax) {
+    const int e = static_cast<int>(__float_as_uint(amax) >> 23);  // biased exponent (0: zero or subnormal)
+    return __uint_as_float(static_cast<uint32_t>(min(max(261 - e, 1), 254)) << 23);
+}
+
+}  // namespace attn

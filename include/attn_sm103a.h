@@ -61,7 +61,8 @@ typedef enum {
     ATTN_ERR_INVALID = -1,     /* bad pointer, size, alignment or scale */
     ATTN_ERR_UNSUPPORTED = -2, /* d or dtype not built, or device is not sm_103 */
     ATTN_ERR_CUDA = -3,        /* a CUDA runtime or driver call failed */
-    ATTN_ERR_TIMEOUT = -4      /* a kernel's bounded wait gave up (device error word) */
+    ATTN_ERR_TIMEOUT = -4,     /* a kernel's bounded wait gave up (device error word) */
+    ATTN_ERR_PAGE = -5         /* a page table entry or a length outside the cache (device error word) */
 } attn_status;
 
 /*
@@ -271,10 +272,89 @@ attn_status attn_fwd_fp8(const void* q8, const void* k8, const void* v8, float s
                          int causal, attn_stream_t stream);
 
 /*
+ * Paged key/value cache held in 8 bits.  A page holds page_size tokens of
+ * every key/value head as OCP E4M3 codes (uint8), one fp32 scale per page,
+ * head and tensor: the value is scale * code.  Token j of sequence b lies in
+ * slot j % page_size of page page_table[b * table_stride + j / page_size].
+ *   k_pages, v_pages : device pointers to the codes of [num_pages, Hk,
+ *                  page_size, d] views with strides ks, vs (attn_strides_t: b =
+ *                  page, h = head, n = token; in bytes, multiples of 16, d
+ *                  contiguous), 16-byte aligned.
+ *   k_scale, v_scale : fp32 [num_pages, Hk], dense; finite and > 0.
+ *   page_table   : int32 [B, max_pages], rows table_stride >= max_pages apart.
+ *                  Entries that hold no token a call touches are not read.
+ *   seq_lens     : int32 [B], tokens of each sequence, the new ones included.
+ *   page_size    : a power of two, 16 .. 1024; max_pages * page_size <= 2^30.
+ * The lengths and the table stay on the device: a captured call may be replayed
+ * after they change.  An entry outside [0, num_pages), or a length that leaves
+ * the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE; no
+ * access leaves the pool, attn_cache_append leaves such a page unwritten, and
+ * the rows of attn_fwd_cache that needed it are undefined.
+ */
+typedef struct {
+    void *k_pages, *v_pages;
+    attn_strides_t ks, vs;
+    float *k_scale, *v_scale;
+    const int32_t* page_table;
+    int64_t table_stride;
+    const int32_t* seq_lens;
+    int num_pages, page_size, max_pages;
+} attn_cache_t;
+
+/*
+ * Writes new tokens into the cache.
+ *   k, v     : bf16 [B, Hk, T, d] views with strides ks, vs.
+ *   new_lens : int32 [B], how many of the T tokens of each sequence are new (0
+ *              .. T, clamped), or NULL for T.  Token t goes to position
+ *              seq_lens[b] - new_lens[b] + t (a negative one is not written).
+ * Per page, head and tensor: the scale is the smallest power of two 2^e, e >=
+ * -100, with every finite new magnitude at most 448 * 2^e; a page that holds
+ * older tokens keeps its scale while that is large enough, else the older codes
+ * are rounded again to the new one.  Codes are rounded to nearest even;
+ * infinities become +-448 and NaN the NaN code.  Slots behind the last token are
+ * left as they were.  No two sequences of a call may write to the same page.
+ * Source: ai.engineer item 33 (affine quantisation, Z = 0); no page describes a
+ * cache.  Errors as attn_fwd_strided; B <= 32767 and Hk <= 65535.
+ */
+attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_strides_t ks,
+                              const void* v, attn_strides_t vs, const int32_t* new_lens, int B,
+                              int Hk, int T, int d, attn_stream_t stream);
+
+/*
+ * Attention of new queries over the cache (their own tokens written first).
+ *   q, o     : bf16 [B, H, T, d] views with strides qs, os; H a multiple of Hk,
+ *              query head h reads key/value head h / (H / Hk).
+ *   lse      : fp32 [B, H, T], dense.
+ *   q_lens   : int32 [B], how many of the T queries of each sequence there are
+ *              (0 .. T, clamped), or NULL for T.  Query t sits at position
+ *              p = seq_lens[b] - q_lens[b] + t; rows t >= q_lens[b] of o and lse
+ *              are left as they were.
+ *   window_left, sinks : key j is visible to position p iff j <= p and
+ *              (window_left == -1, or j >= p - window_left, or j < sinks).  Keys
+ *              that no query of a sequence sees are not read, and their pages
+ *              need not exist.
+ *   workspace : attn_fwd_cache_workspace_bytes() bytes, 256-byte aligned,
+ *              overwritten; calls that may overlap need one each.
+ * A row that sees no key gives O = 0 and LSE = +inf.  Scores, softmax and sums
+ * are fp32 on products of f16 operands: codes are exact in f16, Q rows are
+ * brought to it by a power of two each, the softmax weights (times the value
+ * scale) are rounded to it (2^-12 relative).  Results are deterministic.
+ * Source: ai.engineer item 59 (small-query work split across thread blocks plus
+ * a separate combining kernel; causal mask aligned to the last key);
+ * FlashAttention-3 tuning page (window bounds).  Errors as attn_fwd_strided.
+ */
+size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d);
+attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o,
+                           attn_strides_t os, float* lse, void* workspace, const int32_t* q_lens,
+                           int B, int H, int Hk, int T, int d, float scale, int window_left,
+                           int sinks, attn_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device error
  * word on the current device.  Returns ATTN_ERR_TIMEOUT if any kernel's
  * bounded wait gave up since the last check (the results of that launch are
- * undefined), ATTN_ERR_CUDA if synchronisation failed, else ATTN_OK.
+ * undefined), ATTN_ERR_PAGE if a cache call met a page or a length outside its
+ * cache, ATTN_ERR_CUDA if synchronisation failed, else ATTN_OK.
  * `site` (may be NULL) receives the id of the first wait that gave up.
  */
 attn_status attn_check_device_error(attn_stream_t stream, unsigned int* site);

@@ -1,0 +1,376 @@
+"""Paged 8-bit cache: attn_cache_append and attn_fwd_cache against the fp64 oracle.
+
+Codes and scales have to be the oracle's bit for bit (a scale is a power of two, so a
+code carries one rounding).  Outputs of attn_fwd_cache: with M = sum_j P_ij |V_j|,
+  e = (2^-11 + 2^-15) M   weights rounded to f16 (half a step, 2^-11 relative), and 2^-15
+                          for scores and exponentials in fp32 (scores below 32 in log2
+                          units: 128 fp32 additions and one rounding of the exponent stay
+                          under 2^-16, the exponential under 2^-21),
+  |O - ref| <= e + 2^-8 (|ref| + e)   (bf16 store), and |LSE - ref| <= 2^-14."""
+
+import numpy as np
+import pytest
+
+import oracle
+from exact_attention_52_gb300 import api
+from oracle import streaming
+
+from .helpers import device_bf16_to_f64
+
+pytestmark = pytest.mark.gpu
+
+
+class Pool:
+    """A cache of B sequences, its pages dealt out at random, filled with data of its own."""
+
+    def __init__(self, seed, B, Hk, d, page, max_pages, token_major=False, spare=3):
+        import torch
+        self.rng = np.random.default_rng(seed)
+        self.B, self.Hk, self.d, self.page = B, Hk, d, page
+        P = B * max_pages + spare
+        self.table = self.rng.permutation(P)[:B * max_pages].reshape(B, max_pages).astype(np.int32)
+        self.k, self.v = (self.rng.integers(0, 0x7F, (P, Hk, page, d)).astype(np.uint8) |
+                          (self.rng.integers(0, 2, (P, Hk, page, d)).astype(np.uint8) << 7) for _ in range(2))
+        for x in (self.k, self.v):  # magnitudes around 1
+            x[...] = streaming.e4m3_encode(self.rng.standard_normal(x.shape) * 64)
+        self.ks, self.vs = (2.0 ** self.rng.integers(-7, -4, (P, Hk)).astype(np.float64) for _ in range(2))
+        self.token_major = token_major
+        self.torch = torch
+
+    def dev(self):
+        """k_pages, v_pages, k_scale, v_scale, table on the device."""
+        torch = self.torch
+        if self.token_major:  # [P, page, Hk, d] storage seen as [P, Hk, page, d]
+            pages = [torch.from_numpy(np.ascontiguousarray(x.transpose(0, 2, 1, 3))).cuda().transpose(1, 2)
+                     for x in (self.k, self.v)]
+        else:
+            pages = [torch.from_numpy(x.copy()).cuda() for x in (self.k, self.v)]
+        scales = [torch.from_numpy(x.astype(np.float32)).cuda() for x in (self.ks, self.vs)]
+        return [*pages, *scales, torch.from_numpy(self.table).cuda()]
+
+
+def i32(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def bf16(rng, shape, layout="bhnd", amp=1.0):
+    """bf16 data [b, h, t, d] on the device in `layout`, and its values."""
+    import torch
+    x = torch.from_numpy((amp * rng.standard_normal(shape)).astype(np.float32)).bfloat16()
+    vals = x.double().numpy()
+    x = x.cuda()
+    return (x if layout == "bhnd" else x.transpose(1, 2).contiguous()), vals
+
+
+def check_clean():
+    rc, site = api.check_device_error()
+    assert rc == 0, f"device error {rc} at site {site:#x}"
+
+
+def check_out(o, lse, ref, layout="bhnd"):
+    o_ref, lse_ref, mag, there = ref
+    og = device_bf16_to_f64(o if layout == "bhnd" else o.transpose(1, 2))
+    lg = lse.double().cpu().numpy()
+    at = np.broadcast_to(there[:, None, :], lg.shape)
+    assert np.array_equal(np.isnan(og[at]), np.isnan(o_ref[at]))
+    e = (2.0 ** -11 + 2.0 ** -15) * mag
+    bad = np.abs(og - o_ref) > e + 2.0 ** -8 * (np.abs(o_ref) + e)
+    assert not bad[at].any(), (np.argwhere(bad & at[..., None])[:4], np.nanmax(np.abs(og - o_ref)[at]))
+    assert np.array_equal(np.isposinf(lg[at]), np.isposinf(lse_ref[at]))
+    fin = at & np.isfinite(lse_ref)
+    assert np.all(np.abs(lg - lse_ref)[fin] <= 2.0 ** -14)
+
+
+def run_cache(pool, H, T, seq_lens, q_lens, left=-1, sinks=0, layout="bhnd", scale=None, amp=1.0):
+    import torch
+    q, qv = bf16(pool.rng, (pool.B, H, T, pool.d), layout, amp)
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((pool.B, H, T), 7.0, device="cuda")
+    api.fwd_cache(q, *pool.dev(), i32(seq_lens), q_lens=None if q_lens is None else i32(q_lens), layout=layout,
+                  scale=scale, window_left=left, sinks=sinks, o=o, lse=lse)
+    check_clean()
+    ql = [T] * pool.B if q_lens is None else q_lens
+    ref = streaming.cache_forward(qv, pool.k, pool.v, pool.ks, pool.vs, pool.table, seq_lens, ql,
+                                  pool.d ** -0.5 if scale is None else scale, left, sinks)
+    check_out(o, lse, ref, layout)
+    # rows behind a sequence's queries are left as they were
+    gone = ~ref[3]
+    ob = o if layout == "bhnd" else o.transpose(1, 2)
+    for b, t in np.argwhere(gone):
+        assert torch.all(ob[b, :, t] == 7.0) and torch.all(lse[b, :, t] == 7.0)
+
+
+# (B, H, Hk, T, page, seq_lens, q_lens)
+SHAPES = [
+    (1, 1, 1, 1, 16, [1], None),
+    (1, 1, 1, 1, 16, [17], None),
+    (2, 4, 4, 1, 32, [1, 63], None),
+    (3, 8, 2, 1, 64, [200, 0, 65], None),
+    (2, 8, 1, 1, 16, [300, 129], None),
+    (2, 40, 2, 1, 128, [1000, 777], None),    # 20 query heads a group: two row tiles
+    (4, 6, 2, 3, 16, [5, 3, 300, 64], [3, 3, 2, 0]),
+    (2, 8, 4, 7, 64, [130, 2], [7, 7]),       # more queries than tokens: some see nothing
+    (1, 4, 1, 40, 32, [555], None),
+    (1, 2, 1, 1, 64, [20000], None),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("left,sinks", [(-1, 0), (20, 0), (33, 4), (0, 1), (100, 40), (100000, 3)])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_cache_forward_matches_oracle(shape, left, sinks, d):
+    B, H, Hk, T, page, lens, ql = shape
+    pool = Pool(1000 + T + H, B, Hk, d, page, max(1, -(-max(lens) // page)))
+    run_cache(pool, H, T, lens, ql, left, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout,token_major", [("bnhd", False), ("bhnd", True), ("bnhd", True)])
+def test_cache_forward_layouts(layout, token_major, d):
+    pool = Pool(7, 2, 2, d, 32, 5, token_major=token_major)
+    run_cache(pool, 8, 3, [150, 31], [3, 1], 50, 2, layout=layout)
+
+
+def test_cache_forward_many_sequences_share_the_device():
+    """More items than CTAs, lengths from 0 to long: shares begin and end inside items."""
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 400, 150)]
+    lens[7], lens[100] = 3000, 2500
+    pool = Pool(8, 150, 4, 64, 16, 190)
+    run_cache(pool, 8, 1, lens, [0 if n == 0 else 1 for n in lens])
+
+
+def test_cache_forward_large_scores_and_values():
+    """Scores that reach far beyond the first block's maximum, page scales far apart."""
+    pool = Pool(9, 2, 2, 128, 16, 20)
+    pool.vs *= 2.0 ** pool.rng.integers(-40, 41, pool.vs.shape)
+    pool.ks[:] = 2.0 ** -5
+    run_cache(pool, 8, 1, [310, 200], None, amp=2.0)
+
+
+def test_pages_that_no_query_sees_are_not_read():
+    """Table entries outside window and sinks hold nonsense and no error is recorded."""
+    pool = Pool(10, 2, 2, 128, 16, 40)
+    lens, left, sinks = [600, 333], 70, 5
+    for b, n in enumerate(lens):
+        for pg in range(40):
+            lo, hi = pg * 16, pg * 16 + 15
+            if lo >= n or (hi < n - 1 - left and lo >= sinks):
+                pool.table[b, pg] = -1 if pg % 2 else 1 << 30
+    run_cache(pool, 4, 1, lens, None, left, sinks)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_nan_codes_in_hidden_places_do_not_matter(T):
+    """NaN codes behind the sequence, between sinks and window, and (T > 1) in tokens that
+    only later queries see: rows that do not see them are finite, the others NaN as the
+    oracle's."""
+    pool = Pool(11, 1, 1, 128, 16, 10)
+    n, left, sinks = 130, 40, 3
+    first = n - T
+    hidden = [j for j in range(160) if j >= n or (j < first - left and j >= sinks)]
+    for j in hidden + ([n - 1] if T > 1 else []):
+        for x in (pool.k, pool.v):
+            x[pool.table[0, j // 16], 0, j % 16, ::3] = 0x7F if j % 2 else 0xFF
+    if T > 1:  # the last token's key is a number: only its value is NaN
+        pool.k[pool.table[0, (n - 1) // 16], 0, (n - 1) % 16] = 0x30
+    run_cache(pool, 8, T, [n], None, left, sinks)
+
+
+def test_bad_pages_and_lengths_are_reported():
+    import torch
+    pool = Pool(12, 2, 1, 64, 16, 4)
+    good = pool.dev()
+    q, _ = bf16(pool.rng, (2, 2, 1, 64))
+    k, _ = bf16(pool.rng, (2, 1, 1, 64))
+    for entry in (-1, good[0].shape[0], 2 ** 31 - 1):
+        table = good[4].clone()
+        table[1, 2] = entry
+        api.fwd_cache(q, *good[:4], table, i32([64, 40]))
+        assert api.check_device_error()[0] == -5
+        before = [t.clone() for t in good[:4]]
+        api.cache_append(k, k, *good[:4], table, i32([64, 40]), new_lens=i32([0, 1]))
+        assert api.check_device_error()[0] == -5
+        assert all(torch.equal(a, b) for a, b in zip(before, good[:4]))
+    api.cache_append(k, k, *good, i32([64, 65]), new_lens=i32([0, 1]))  # one token behind the table
+    assert api.check_device_error()[0] == -5
+    assert api.check_device_error() == (0, 0)
+
+
+def test_reads_and_writes_past_32_bits():
+    """A pool of 2.1 GB per tensor whose last pages are in use."""
+    import torch
+    P, Hk, page, d = 2080, 8, 1024, 128
+    kp, vp = (torch.zeros((P, Hk, page, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    assert kp.numel() > 1 << 31
+    ks, vs = (torch.ones((P, Hk), device="cuda") for _ in range(2))
+    rng = np.random.default_rng(13)
+    table = np.array([[P - 1, P - 2]], dtype=np.int32)
+    k, kv = bf16(rng, (1, Hk, 1100, d))
+    v, vv = bf16(rng, (1, Hk, 1100, d))
+    q, qv = bf16(rng, (1, 16, 1, d))
+    args = (kp, vp, ks, vs, torch.from_numpy(table).cuda(), i32([1100]))
+    api.cache_append(k, v, *args)
+    o, lse = api.fwd_cache(q, *args)
+    check_clean()
+    small = [np.zeros((2, Hk, page, d), dtype=np.uint8) for _ in range(2)]
+    sc = [np.ones((2, Hk)) for _ in range(2)]
+    streaming.cache_append(kv, vv, *small, *sc, [[1, 0]], [1100], [1100])
+    for dev, ref in ((kp, small[0]), (vp, small[1])):
+        assert np.array_equal(dev[P - 2:].cpu().numpy(), ref)
+        assert int(dev[:P - 2].count_nonzero()) == 0
+    check_out(o, lse, streaming.cache_forward(qv, *small, *sc, [[1, 0]], [1100], [1], d ** -0.5))
+
+
+# (B, Hk, page, T, [(seq_lens, new_lens), ...])
+APPENDS = [
+    (1, 1, 16, 1, [([1], None), ([2], None), ([17], None)]),
+    (2, 2, 16, 40, [([40, 3], [40, 3]), ([41, 30], [1, 27]), ([48, 70], [7, 40])]),
+    (3, 1, 64, 100, [([100, 64, 0], [100, 64, 0]), ([101, 65, 1], [1, 1, 1]), ([190, 128, 2], [89, 63, 1])]),
+    (1, 3, 128, 300, [([300], None), ([450], [150])]),
+    (1, 1, 32, 10, [([4], None)]),  # more new tokens than the sequence has: the last 4 are written
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout,token_major", [("bhnd", False), ("bnhd", True)])
+@pytest.mark.parametrize("case", APPENDS)
+def test_append_matches_oracle(case, layout, token_major, d):
+    B, Hk, page, T, calls = case
+    pool = Pool(20 + T, B, Hk, d, page, -(-max(max(c[0]) for c in calls) // page), token_major=token_major)
+    dev = pool.dev()
+    for n, (lens, new) in enumerate(calls):
+        # later calls bring larger values: scales grow and older codes are rounded again
+        k, kv = bf16(pool.rng, (B, Hk, T, d), layout, amp=2.0 ** (2 * n))
+        v, vv = bf16(pool.rng, (B, Hk, T, d), layout, amp=2.0 ** (-3 * n))
+        api.cache_append(k, v, *dev, i32(lens), new_lens=None if new is None else i32(new), layout=layout)
+        streaming.cache_append(kv, vv, pool.k, pool.v, pool.ks, pool.vs, pool.table, lens,
+                               [T] * B if new is None else new)
+        check_clean()
+        for got, want in zip(dev[:4], (pool.k, pool.v, pool.ks, pool.vs)):
+            assert np.array_equal(got.cpu().numpy(), want.astype(got.cpu().numpy().dtype)), n
+
+
+def test_append_special_values():
+    """Zeros, subnormals, infinities, NaN, the largest numbers, values on a rounding border."""
+    import torch
+    rows = np.zeros((1, 1, 6, 64), dtype=np.float32)
+    rows[0, 0, 1] = 1e-39
+    rows[0, 0, 2, :4] = [np.inf, -np.inf, np.nan, 2.0]
+    rows[0, 0, 3, :6] = [448, 449, -450, 17, 19, 21]
+    rows[0, 0, 4] = 3.3e38
+    rows[0, 0, 5, :3] = [2.0 ** -133, 2.0 ** -126, 1.0]
+    x = torch.from_numpy(rows).bfloat16()
+    for t in range(6):
+        pool = Pool(30, 1, 1, 64, 16, 1)
+        dev = pool.dev()
+        one = x[:, :, t:t + 1].contiguous()
+        api.cache_append(one.cuda(), one.cuda(), *dev, i32([1]))
+        streaming.cache_append(one.double().numpy(), one.double().numpy(), pool.k, pool.v, pool.ks, pool.vs,
+                               pool.table, [1], [1])
+        assert np.array_equal(dev[2].cpu().numpy(), pool.ks.astype(np.float32)), t
+        assert np.array_equal(dev[0].cpu().numpy(), pool.k), t
+    check_clean()
+
+
+def test_refusals():
+    import torch
+    pool = Pool(40, 2, 2, 64, 16, 3)
+    kp, vp, ks, vs, table = pool.dev()
+    lens = i32([20, 30])
+    q, _ = bf16(pool.rng, (2, 4, 1, 64))
+    k, _ = bf16(pool.rng, (2, 2, 1, 64))
+    ok = dict(q=q, k_pages=kp, v_pages=vp, k_scale=ks, v_scale=vs, page_table=table, seq_lens=lens)
+    api.fwd_cache(**ok)
+    bad = [dict(q=q.float()), dict(q=q[:1]), dict(q=q.cpu()), dict(k_pages=kp.to(torch.int32)), dict(v_pages=vp[:-1]),
+           dict(k_scale=ks.half()), dict(v_scale=vs.t()), dict(page_table=table.long()), dict(page_table=table[:1]),
+           dict(page_table=table.t()), dict(seq_lens=lens.long()), dict(seq_lens=lens.cpu()), dict(q_lens=lens[:1]),
+           dict(layout="nbhd"), dict(o=torch.empty_like(q).float()), dict(lse=torch.empty(2, 4, 2, device="cuda")),
+           dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), dict(k_pages=kp[..., ::2], v_pages=vp[..., ::2])]
+    for change in bad:
+        with pytest.raises(ValueError):
+            api.fwd_cache(**{**ok, **change})
+    # three query heads over two, a page of 12 or 8 tokens, bounds below -1, scales that are not positive
+    for change in (dict(q=q[:, :3]), dict(k_pages=kp[:, :, :12], v_pages=vp[:, :, :12]), dict(window_left=-2),
+                   dict(sinks=-1), dict(scale=0.0), dict(scale=float("nan")),
+                   dict(k_pages=kp[:, :, :8], v_pages=vp[:, :, :8])):
+        with pytest.raises((ValueError, api.AttnError)):
+            api.fwd_cache(**{**ok, **change})
+    for args in ((k.float(), k), (k, k[:1]), (k[..., ::2], k[..., ::2]), (k.cpu(), k.cpu()), (q, q)):
+        with pytest.raises((ValueError, api.AttnError)):
+            api.cache_append(*args, kp, vp, ks, vs, table, lens)
+    check_clean()
+
+
+def test_on_another_stream_and_in_a_replayed_graph():
+    """A captured decode step (write, then attend) is replayed with new tokens and lengths in
+    the captured buffers; an eager call on a stream of its own gives the same bits."""
+    import torch
+    pool = Pool(50, 3, 2, 128, 16, 6)
+    dev = pool.dev()
+    q, k, v = (bf16(pool.rng, (3, h, 1, 128))[0] for h in (8, 2, 2))
+    lens = i32([40, 15, 80])
+    o, lse = torch.empty_like(q), torch.empty((3, 8, 1), device="cuda")
+    ws = torch.empty(api.fwd_cache_workspace_bytes(3, 8, 2, 1, 128), dtype=torch.uint8, device="cuda")
+    eager = [t.clone() for t in dev]
+
+    def step():
+        api.cache_append(k, v, *dev, lens)
+        api.fwd_cache(q, *dev, lens, o=o, lse=lse, workspace=ws)
+
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for n in range(3):
+        for t, h in ((q, 8), (k, 2), (v, 2)):
+            t.copy_(bf16(pool.rng, (3, h, 1, 128))[0])
+        lens.add_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        api.cache_append(k, v, *eager, lens, stream=side)
+        o2, lse2 = api.fwd_cache(q, *eager, lens, stream=side)
+        side.synchronize()
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2), n
+        assert all(torch.equal(a, b) for a, b in zip(dev, eager))
+    check_clean()
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    import torch
+    pool = Pool(60, 4, 2, 128, 64, 40)
+    dev = pool.dev()
+    lens = i32([2500, 2000, 1500, 2222])
+    qs = [bf16(pool.rng, (4, 16, 1, 128))[0] for _ in range(2)]
+    alone = [api.fwd_cache(q, *dev, lens) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [api.fwd_cache(q, *dev, lens, stream=s) for q, s in zip(qs, streams)]
+        torch.cuda.synchronize()
+        for (o, lse), (o2, lse2) in zip(alone, got):
+            assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    check_clean()
+
+
+def test_decode_as_it_is_used():
+    """A prompt is written in two pieces, then tokens one by one; after each the attention of
+    the new tokens over what the cache holds is the oracle's."""
+    pool = Pool(70, 2, 2, 64, 32, 5)
+    dev = pool.dev()
+    length = np.array([0, 0])
+    for new in ([50, 33], [20, 1], [1, 1], [1, 1], [1, 0], [3, 2]):
+        T = max(new)
+        length = length + new
+        k, kv = bf16(pool.rng, (2, 2, T, 64))
+        v, vv = bf16(pool.rng, (2, 2, T, 64), amp=1.0 + T)
+        q, qv = bf16(pool.rng, (2, 6, T, 64))
+        lens = length.tolist()
+        api.cache_append(k, v, *dev, i32(lens), new_lens=i32(new))
+        o, lse = api.fwd_cache(q, *dev, i32(lens), q_lens=i32(new), window_left=45, sinks=4)
+        check_clean()
+        streaming.cache_append(kv, vv, pool.k, pool.v, pool.ks, pool.vs, pool.table, lens, new)
+        assert np.array_equal(dev[0].cpu().numpy(), pool.k) and np.array_equal(dev[1].cpu().numpy(), pool.v)
+        check_out(o, lse, streaming.cache_forward(qv, pool.k, pool.v, pool.ks, pool.vs, pool.table, lens, new,
+                                                  64 ** -0.5, 45, 4))
