@@ -507,21 +507,9 @@ attn_status cache_view(const attn_cache_t* c, int B, CacheView* out) {
     return ATTN_OK;
 }
 
-// CTAs that share a cache attention's work on the current device.
-attn_status cache_grid(int* grid) {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return ATTN_ERR_CUDA;
-    *grid = sms * cache_decode_ctas_per_sm();
-    return ATTN_OK;
-}
-
-// The workspace is laid out for kCacheGridMax CTAs whatever the device, so that
-// its size needs no device.
-constexpr int kCacheGridMax = 1024;
-constexpr int kCacheRows = 16;
-size_t cache_part_bytes(int d) { return static_cast<size_t>(2) * kCacheGridMax * kCacheRows * d * sizeof(float); }
+// The workspace is laid out for the largest launch, so that its size needs no device.
+size_t cache_part_bytes(int d) { return static_cast<size_t>(2) * kCacheGridMax * kCacheRowsMax * d * sizeof(float); }
+constexpr size_t kCacheStatBytes = static_cast<size_t>(2) * kCacheGridMax * kCacheRowsMax * sizeof(float2);
 
 
 }  // namespace
@@ -785,7 +773,7 @@ attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_str
 
 size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d) {
     if (check_sizes(B, H, T, d, 1.f, 0) != ATTN_OK || check_group(H, Hk) != ATTN_OK) return 0;
-    return cache_part_bytes(d) + static_cast<size_t>(2) * kCacheGridMax * kCacheRows * sizeof(float2);
+    return cache_part_bytes(d) + kCacheStatBytes + kCacheGridMax * sizeof(CacheBorder);
 }
 
 attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o, attn_strides_t os,
@@ -816,11 +804,11 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     p.sinks = sinks;
     p.part = static_cast<float*>(workspace);
     p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + cache_part_bytes(d));
+    p.border = reinterpret_cast<CacheBorder*>(static_cast<uint8_t*>(workspace) + cache_part_bytes(d) + kCacheStatBytes);
     DeviceState ds;
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
-    if ((rc = cache_grid(&p.grid)) != ATTN_OK) return rc;
-    if (p.grid > kCacheGridMax) p.grid = kCacheGridMax;
+    p.rows = p.grid = 0;
     return launch_cache_decode(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 

@@ -118,23 +118,23 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 // ---------------------------------------------------------------------------
 // Attention of a few queries: work shared out evenly
 // ---------------------------------------------------------------------------
-// An item is (sequence, key/value head, tile of kRows query rows); the rows of a
+// An item is (sequence, key/value head, tile of p.rows query rows); the rows of a
 // key/value head are its H/Hk query heads of every new query, row = t * H/Hk + g.
 // An item's blocks of kBlock tokens are laid end to end over all items, and CTA c
 // of G takes the c-th of G equal shares of that line, whatever the lengths of the
 // sequences are: lengths stay on the device.  A share can begin and end inside
 // an item; such unfinished segments go to the workspace and a second kernel joins
-// them.  At most two per CTA: slot 2c for a segment that does not start its item,
-// or starts it and does not reach its end in slot 2c + 1.
-constexpr int kRows = 16;   // query rows of a tile: M of one mma
-constexpr int kBlock = 16;  // tokens of a block: K of one mma
+// them.  (Where there is a CTA for every item and the longest item is at most a
+// quarter above an equal share, the share is that item: equal items then stay
+// whole.)  At most two per CTA: slot 2c for a segment that does not start its item,
+// slot 2c + 1 for one that starts it and does not reach its end.
+constexpr int kTok = 16;    // tokens of a tile: M of a score product, K of an output product
+constexpr int kBlock = 32;  // tokens of a block: two tiles, which may lie in different pages
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;  // blocks in flight per warp
-constexpr int kCtasPerSm = 3;
 // A share has at least this many blocks: with fewer, joining costs more than the
 // shorter walk gives.
-constexpr int kMinShare = 16;
+constexpr int kMinShare = 8;
 
 struct Share {
     long long total, share;
@@ -144,22 +144,36 @@ struct Share {
 
 struct ShareSmem {
     long long warp_sum[kWarps], b_first;
-    int b;
+    int warp_max[kWarps], warp_items[kWarps], b;
 };
 
+__device__ __forceinline__ int row_tiles(const CacheFwdParams& p, const CacheSeq& s) {
+    return (s.q_len * (p.H / p.Hk) + p.rows - 1) / p.rows;
+}
 __device__ __forceinline__ long long seq_work(const CacheFwdParams& p, const CacheSeq& s) {
-    const int rt = (s.q_len * (p.H / p.Hk) + kRows - 1) / kRows;
-    return static_cast<long long>(s.n) * rt * p.Hk;
+    return static_cast<long long>(s.n) * (row_tiles(p, s) * p.Hk);
+}
+// Quotient of numbers that hardly ever pass 32 bits (a 64-bit division takes some
+// hundred instructions).
+__device__ __forceinline__ long long div_mostly32(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
 // Lays the items of all sequences end to end and finds the sequence at the start
-// of share c (B sequences, a slice of them per thread).
+// of share c (a slice of the sequences per thread).
 __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += seq_work(p, cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b));
+    int longest = 0, items = 0;  // of items
+    for (int b = b0; b < b1; ++b) {
+        const CacheSeq q = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+        mine += seq_work(p, q);
+        items = min(items + row_tiles(p, q) * p.Hk, 1 << 20);
+        if (q.q_len > 0) longest = max(longest, q.n);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    items = __reduce_add_sync(0xffffffffu, items);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long incl = mine;
 #pragma unroll
@@ -167,7 +181,11 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
         const long long up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
     }
-    if (lane == 31) sm->warp_sum[warp] = incl;
+    if (lane == 31) {
+        sm->warp_sum[warp] = incl;
+        sm->warp_max[warp] = longest;
+        sm->warp_items[warp] = items;
+    }
     if (threadIdx.x == 0) sm->b = -1;
     __syncthreads();
     Share s;
@@ -178,7 +196,14 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
         if (w < warp) before += sm->warp_sum[w];
         s.total += sm->warp_sum[w];
     }
-    s.share = max((s.total + p.grid - 1) / p.grid, static_cast<long long>(kMinShare));
+    longest = items = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        longest = max(longest, sm->warp_max[w]);
+        items += sm->warp_items[w];
+    }
+    s.share = max(div_mostly32(s.total + p.grid - 1, p.grid), static_cast<long long>(kMinShare));
+    if (items <= p.grid && 4ll * longest <= 5ll * s.share) s.share = max(s.share, static_cast<long long>(longest));
     const long long x = c * s.share;
     if (x < s.total && before <= x && x < before + mine) {
         for (int b = b0; b < b1; ++b) {
@@ -197,16 +222,16 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     return s;
 }
 
-// Row r (0 .. kRows - 1) of row tile rt of a sequence: query and head of the group.
+// Row r (0 .. p.rows - 1) of row tile rt of a sequence: query and head of the group.
 struct RowAt {
     int t, h;
     bool there;
 };
 __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int hk, int rt, int r) {
-    const int G = p.H / p.Hk, row = rt * kRows + r;
+    const int G = p.H / p.Hk, row = rt * p.rows + r;
     RowAt a;
     a.t = row / G;
-    a.h = hk * G + row % G;
+    a.h = hk * G + row - a.t * G;
     a.there = a.t < q_len;
     return a;
 }
@@ -217,52 +242,91 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // Bound by reading the codes once.  Each warp walks every kWarps-th block of a
 // segment on its own, with its own running maximum, sums and output: a lane
 // copies exactly the bytes that it will turn into its fragments (asynchronous
-// copies into a ring of its own, kStages - 1 blocks ahead), so no barrier stands
-// in the loop.  Codes become f16 exactly and go to f16 matrix products with fp32
-// sums; Q rows are brought to f16 by a power of two each.  A page's scales enter
-// in fp32: the key scale multiplies the scores, the value scale is added, as its
-// log2, to the exponent, so that the weights given to the products are
-// 2^(score + log2 sv - m) with the running maximum m taken over score + log2 sv,
-// and the sum of the probabilities takes them back by 1 / sv.  The weights are
-// scaled by 2^kShift, f16's room above 1, so that one is lost to underflow only
-// below 2^-40 of the largest.
+// copies into a ring of its own), so no barrier stands in the loop.  Codes become
+// f16 exactly and go to f16 matrix products with fp32 sums; Q rows are brought to
+// f16 by a power of two each.  A page's scales enter in fp32: the key scale
+// multiplies the scores, the value scale is added, as its log2, to the exponent,
+// so that the weights given to the products are 2^(score + log2 sv - m) with the
+// running maximum m taken over score + log2 sv, and the sum of the probabilities
+// takes them back by 1 / sv.  m is raised, and the output rescaled, only when a
+// score passes it by more than kSlack; a weight is lost to f16's underflow below
+// 2^-31 of the largest.
 //
-// Fragment layouts (g = lane / 4, q = lane % 4).  Contraction indices may be
-// permuted if both operands are: in K, lane (g, q) holds token g and the 16
-// consecutive d from 64 c + 16 q, of which word s gives the k-pairs (2q, 2q + 1)
-// and (2q + 8, 2q + 9) of product (c, s).  In V, lane (g, q) holds tokens 2q,
-// 2q + 1, 2q + 8, 2q + 9 and the D/8 consecutive d from g D/8, the j-th of which
-// is column g of n-tile j: column n of n-tile j is d = n D/8 + j.
-constexpr int kShift = 15;
+// What belongs to a tile and not to a lane (its page's address and scales, whether
+// all of it is seen) is worked out by one lane per tile for 16 blocks at a time and
+// handed round by shuffles: done by every lane for every tile it took more than
+// half of all instructions.
+//
+// Both products have the keys' side as A: S^T (16 tokens x 8 rows) = K Q^T and
+// O^T (16 d x 8 rows) += V^T P^T, so that the 8 rows of a group of query heads fill
+// the narrow side of the product and codes turned into f16 serve all NT groups of 8
+// rows (with Q as A, 8 rows took as long as 16).  P^T goes from the layout of a
+// result to that of B by an 8x8 transposition between lanes.
+//
+// Fragment layouts (g = lane / 4, q = lane % 4).  Contraction indices, and the order
+// of d in the output, may be permuted.  K: lane (g, q) holds tokens g and g + 8 and
+// the 16 consecutive d from 64 c + 16 q, of which word s gives the k-pairs
+// (2q, 2q + 1) and (2q + 8, 2q + 9) of product (c, s).  V: lane (g, q) holds tokens
+// 2q, 2q + 1, 2q + 8, 2q + 9 and the D/8 consecutive d from g D/8, of which 2j and
+// 2j + 1 are rows g and g + 8 of product j.
+//
+// The copies take whole rows, 512 consecutive bytes an instruction where rows follow
+// each other (each lane copying its own fragments' bytes reached 5.3 TB/s, whole rows
+// 7.0), and the 16-byte pieces of a row are placed so that neither fragment's reads
+// meet in a bank (chunk_at).
+constexpr int kShift = 7;    // weights are 2^(score - m + kShift) and
+constexpr int kSlack = 8;    // m may be up to kSlack below the largest score: at most 2^15
 
-template <int D>
+template <int D, int NT>
 struct DecodeTraits {
+    static constexpr int ROWS = 8 * NT;
+    // Registers (the output takes NT D/4 a lane) admit this many CTAs of four warps to
+    // an SM, and the rings share its memory.
+    static constexpr int CTAS_PER_SM = NT == 1 ? (D == 64 ? 4 : 3) : 2;
+    static constexpr int STAGES = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 6 : 3);  // blocks in a warp's ring
     static constexpr int KC = D / 64;  // 16-byte pieces of a token's K row per lane
     static constexpr int VB = D / 8;   // bytes of a token's V row per lane
-    static constexpr int NJ = D / 8;   // n-tiles of the output
-    static constexpr int K_BYTES = 2 * KC * 512, V_BYTES = 4 * 32 * VB;
-    static constexpr int STAGE = K_BYTES + V_BYTES + 16;  // + the page's two scales
-    static constexpr int RING = kStages * STAGE;
+    static constexpr int NJ = D / 16;  // products of a tile's output
+    static constexpr int ROW = D;             // bytes of a token's row
+    static constexpr int LPR = ROW / 16;      // lanes that copy a row, 16 bytes each
+    static constexpr int RPI = 32 / LPR;      // rows that one copy instruction of the warp takes
+    static constexpr int K_BYTES = kTok * ROW, TILE = 2 * K_BYTES;
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int RING = STAGES * STAGE;
     static constexpr int O_PITCH = D + 4;  // floats between rows of a warp's output in shared memory
-    static constexpr int WARP_BYTES = RING > kRows * O_PITCH * 4 ? RING : kRows * O_PITCH * 4;
-    static constexpr int SMEM = kWarps * WARP_BYTES + kWarps * kRows * 8 + static_cast<int>(sizeof(ShareSmem));
+    static constexpr int WARP_BYTES = RING > ROWS * O_PITCH * 4 ? RING : ROWS * O_PITCH * 4;
+    static constexpr int SMEM = kWarps * WARP_BYTES + kWarps * ROWS * 8 + static_cast<int>(sizeof(ShareSmem));
 };
 
+// Byte offset in a tile of 16-byte piece c of row r.  D = 128: pieces of a row are
+// permuted by a XOR; a quarter warp then finds its eight pieces (K: four pieces of
+// two neighbouring rows; V: two neighbouring pieces of rows 0, 2, 4, 6 or 1, 3, 5, 7)
+// in eight different places of 16 bytes.  D = 64: the same over pairs of rows.
 template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_decode_kernel(const CacheFwdParams p) {
-    using T = DecodeTraits<D>;
+__device__ __forceinline__ int chunk_at(int r, int c) {
+    if constexpr (D == 128) return r * 128 + ((c ^ (r & 6) ^ ((r & 1) << 2)) << 4);
+    else return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) cache_decode_kernel(const CacheFwdParams p) {
+    using T = DecodeTraits<D, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     uint8_t* my = smem + warp * T::WARP_BYTES;
     const uint32_t my_u = smem_u32(my);
-    float2* stat = reinterpret_cast<float2*>(smem + kWarps * T::WARP_BYTES);  // [kWarps][kRows]
-    ShareSmem* ssm = reinterpret_cast<ShareSmem*>(stat + kWarps * kRows);
+    float2* stat = reinterpret_cast<float2*>(smem + kWarps * T::WARP_BYTES);  // [kWarps][ROWS]
+    ShareSmem* ssm = reinterpret_cast<ShareSmem*>(stat + kWarps * T::ROWS);
 
     const Share sh = find_share(p, blockIdx.x, ssm);
     pdl_launch_dependents();
-    if (sh.b < 0) return;  // more CTAs than shares
-    long long x = blockIdx.x * sh.share;
-    const long long x_end = min(x + sh.share, sh.total);
+    if (sh.b < 0) {  // more CTAs than shares
+        if (threadIdx.x == 0) p.border[blockIdx.x].c_first = -1;
+        return;
+    }
+    const long long x_begin = blockIdx.x * sh.share;
+    const long long x_end = min(x_begin + sh.share, sh.total);
+    long long x = x_begin;
     int b = sh.b;
     long long b_first = sh.b_first;
     const int G = p.H / p.Hk;
@@ -274,38 +338,123 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_decode_kernel(cons
             s = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, ++b);
         }
         // segment [v0, v1) of the item's n blocks
-        const int rts = (s.q_len * G + kRows - 1) / kRows;
-        const int item = static_cast<int>((x - b_first) / s.n);
+        const int rts = row_tiles(p, s);
+        const int item = static_cast<int>(div_mostly32(x - b_first, s.n));
         const int v0 = static_cast<int>((x - b_first) - static_cast<long long>(item) * s.n);
         const int v1 = static_cast<int>(min(static_cast<long long>(s.n), v0 + (x_end - x)));
-        const int hk = item / rts, rt = item % rts;
+        const int hk = item / rts, rt = item - hk * rts;
         const int first_pos = s.len - s.q_len;  // may be negative: rows before the first token see nothing
+        if (x == x_begin && threadIdx.x == 0) {
+            CacheBorder bd;
+            bd.b = b;
+            bd.item = item;
+            bd.q_len = s.q_len;
+            bd.c_first = v0 > 0 ? static_cast<int>(div_mostly32(x - v0, sh.share)) + 1 : -1;
+            bd.c_last = static_cast<int>(div_mostly32(x - v0 + s.n - 1, sh.share));
+            p.border[blockIdx.x] = bd;
+        }
 
-        // ---- Q rows g and g + 8 as f16, each times a power of two ----
-        uint32_t qa[T::KC * 4][4];
-        float rq[2];
-        int pos[2];
+        // ---- Q rows on their way while the first blocks are found ----
+        uint4 qw[NT][T::KC][2];  // row g of each group of 8
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const RowAt a = row_at(p, s.q_len, hk, rt, g + 8 * i);
-            pos[i] = first_pos + a.t;
-            uint4 w[T::KC][2];
+        for (int n = 0; n < NT; ++n) {
+            const RowAt a = row_at(p, s.q_len, hk, rt, 8 * n + g);
+            const uint16_t* qrow = static_cast<const uint16_t*>(p.q) + b * p.qs.b + a.h * p.qs.h + a.t * p.qs.n + q * 16;
+#pragma unroll
+            for (int c = 0; c < T::KC; ++c)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    qw[n][c][e] = a.there ? *reinterpret_cast<const uint4*>(qrow + c * 64 + e * 8)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+
+        const int crow = lane / T::LPR, cchunk = lane % T::LPR;  // this lane's piece of a copy instruction
+        const uint8_t* kbase = p.c.k_pages + hk * p.c.ks.h + crow * p.c.ks.n + cchunk * 16;
+        const uint8_t* vbase = p.c.v_pages + hk * p.c.vs.h + crow * p.c.vs.n + cchunk * 16;
+        const long long kn = p.c.ks.n, vn = p.c.vs.n;
+        const int n_my = (v1 - v0 - warp + kWarps - 1) / kWarps;  // blocks of this warp
+        // token of the sequence seen by some query
+        auto seen = [&](int j) { return j < s.len && (j >= s.key_lo || j < p.sinks); };
+
+        // ---- tiles of 16 blocks at a time, one per lane: lane 2i + u holds tile u of block i ----
+        long long koff = 0, voff = 0;          // byte offsets of the tile's first token, for the copies
+        uint32_t loadable = 0;                 // tiles all of whose tokens some query sees
+        float sk_next = 1.f, sv_next = 1.f;    // scales, one batch ahead of their use
+        uint32_t whole_next = 0;
+        auto batch = [&](int i0) {
+            const int i = i0 + (lane >> 1);
+            int tok = 0;
+            bool all = false, whole = false;
+            koff = voff = 0;
+            sk_next = sv_next = 1.f;
+            if (i < n_my) {
+                tok = cache_block(s, v0 + warp + kWarps * i) * kBlock + (lane & 1) * kTok;
+                if (tok < s.len && (tok + kTok > s.key_lo || tok < p.sinks)) {
+                    const int pid = cache_page(p.c, p.st, b, tok);
+                    const int slot = tok & (p.c.page_size - 1);
+                    koff = pid * p.c.ks.b + slot * kn;
+                    voff = pid * p.c.vs.b + slot * vn;
+                    const long long at = static_cast<long long>(pid) * p.Hk + hk;
+                    sk_next = __ldg(p.c.k_scale + at);
+                    sv_next = __ldg(p.c.v_scale + at);
+                    all = tok + kTok <= s.len && (tok >= s.key_lo || tok + kTok <= p.sinks);
+                    // every query sees all of the tile
+                    whole = tok + kTok - 1 <= first_pos &&
+                            (p.left < 0 || tok >= s.len - 1 - p.left || tok + kTok <= p.sinks);
+                }
+            }
+            loadable = __ballot_sync(0xffffffffu, all);
+            whole_next = __ballot_sync(0xffffffffu, whole);
+        };
+        auto issue = [&](int i, int stage) {
+            if (i < n_my) {
+                if ((i & 15) == 0) batch(i);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int src = (2 * i + u) & 31;
+                    const uint8_t* kp = kbase + __shfl_sync(0xffffffffu, koff, src);
+                    const uint8_t* vp = vbase + __shfl_sync(0xffffffffu, voff, src);
+                    const uint32_t dst = my_u + stage * T::STAGE + u * T::TILE;
+                    if ((loadable >> src) & 1u) {
+#pragma unroll
+                        for (int k = 0; k < kTok; k += T::RPI) cp_async16(dst + chunk_at<D>(crow + k, cchunk), kp + k * kn);
+#pragma unroll
+                        for (int k = 0; k < kTok; k += T::RPI)
+                            cp_async16(dst + T::K_BYTES + chunk_at<D>(crow + k, cchunk), vp + k * vn);
+                    } else {  // tokens that no query sees are not read: zeros stand for them
+                        const int tok = cache_block(s, v0 + warp + kWarps * i) * kBlock + u * kTok;
+#pragma unroll
+                        for (int k = 0; k < kTok; k += T::RPI) {
+                            const bool there = seen(tok + crow + k);
+                            const int at = chunk_at<D>(crow + k, cchunk);
+                            cp_async16(dst + at, there ? kp + k * kn : kbase, there);
+                            cp_async16(dst + T::K_BYTES + at, there ? vp + k * vn : vbase, there);
+                        }
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < T::STAGES - 1; ++i) issue(i, i);
+
+        // ---- Q: row g of each group of 8 as f16, times a power of two ----
+        uint32_t qb[NT][T::KC * 4][2];
+        float rq[NT][2];  // rows 2q and 2q + 1: scale * log2 e over that power
+        int pos[NT][2];   // and their positions
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint4 (&w)[T::KC][2] = qw[n];
             float amax = 0.f;
 #pragma unroll
             for (int c = 0; c < T::KC; ++c)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    w[c][e] = make_uint4(0u, 0u, 0u, 0u);
-                    if (a.there)
-                        w[c][e] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + b * p.qs.b +
-                                                                  a.h * p.qs.h + a.t * p.qs.n + c * 64 + q * 16 + e * 8);
+                for (int e = 0; e < 2; ++e)
                     for (uint32_t u : {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w})
                         amax = fmaxf(amax, fmaxf(fabsf(bf16lo(u)), fabsf(bf16hi(u))));
-                }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const float f = f16_row_scale(amax);
-            rq[i] = p.cs * __uint_as_float((254u << 23) - __float_as_uint(f));
 #pragma unroll
             for (int c = 0; c < T::KC; ++c)
 #pragma unroll
@@ -313,237 +462,241 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_decode_kernel(cons
                     const uint32_t u[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)  // elements 8e + 2k, 8e + 2k + 1 of the lane's 16: product 2e + k/2
-                        qa[c * 4 + 2 * e + (k >> 1)][i + 2 * (k & 1)] = pack_f16x2(bf16lo(u[k]) * f, bf16hi(u[k]) * f);
+                        qb[n][c * 4 + 2 * e + (k >> 1)][k & 1] = pack_f16x2(bf16lo(u[k]) * f, bf16hi(u[k]) * f);
                 }
+            const float rf = p.cs * __uint_as_float((254u << 23) - __float_as_uint(f));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                rq[n][e] = __shfl_sync(0xffffffffu, rf, (2 * q + e) * 4);
+                pos[n][e] = first_pos + row_at(p, s.q_len, hk, rt, 8 * n + 2 * q + e).t;
+            }
         }
 
-        float o[T::NJ][4];
+        float o[NT][T::NJ][4];  // (row 2q, 2q + 1 at d 2j; row 2q, 2q + 1 at d 2j + 1) of the lane's D/8
 #pragma unroll
-        for (int j = 0; j < T::NJ; ++j)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int j = 0; j < T::NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][j][e] = 0.f;
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
+        float sk = 1.f, lsv = 0.f, isv = 1.f;  // of this lane's tile of the batch in use
+        uint32_t whole = 0;
+        auto row_sees = [&](int ps, int j) { return j <= ps && (p.left < 0 || j >= ps - p.left || j < p.sinks); };
 
-        const uint8_t* kbase = p.c.k_pages + hk * p.c.ks.h + g * p.c.ks.n + q * 16;
-        const uint8_t* vbase = p.c.v_pages + hk * p.c.vs.h + 2 * q * p.c.vs.n + g * T::VB;
-        const int slot_mask = p.c.page_size - 1;
-        // token of the sequence seen by some query
-        auto seen = [&](int j) { return j < s.len && (j >= s.key_lo || j < p.sinks); };
-        auto issue = [&](int v, int stage) {
-            if (v < v1) {
-                const int tok = cache_block(s, v) * kBlock;
-                const int pid = tok < s.len ? cache_page(p.c, p.st, b, tok) : 0;
-                const uint32_t dst = my_u + stage * T::STAGE;
-                const uint8_t* kp = kbase + pid * p.c.ks.b + (tok & slot_mask) * p.c.ks.n;
-                const uint8_t* vp = vbase + pid * p.c.vs.b + (tok & slot_mask) * p.c.vs.n;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const bool there = seen(tok + 8 * u + g);
-#pragma unroll
-                    for (int c = 0; c < T::KC; ++c)
-                        cp_async16(dst + (u * T::KC + c) * 512 + lane * 16, kp + 8 * u * p.c.ks.n + c * 64, there);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = (k & 1) + 8 * (k >> 1);
-                    const bool there = seen(tok + 2 * q + t);
-                    const uint32_t to = dst + T::K_BYTES + (k * 32 + lane) * T::VB;
-                    if constexpr (T::VB == 16) cp_async16(to, vp + t * p.c.vs.n, there);
-                    else cp_async8(to, vp + t * p.c.vs.n, there);
-                }
-                if (lane < 2)
-                    cp_async4(dst + T::K_BYTES + T::V_BYTES + 4 * lane,
-                              (lane ? p.c.v_scale : p.c.k_scale) + static_cast<long long>(pid) * p.Hk + hk, true);
-            }
-            cp_async_commit();
-        };
-
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(v0 + warp + kWarps * i, i);
         int stage = 0;
-        for (int v = v0 + warp; v < v1; v += kWarps) {
-            issue(v + kWarps * (kStages - 1), stage == 0 ? kStages - 1 : stage - 1);
-            cp_async_wait<kStages - 1>();
-            __syncwarp();  // the scales were copied by lanes 0 and 1
-            const uint8_t* src = my + stage * T::STAGE;
-            const float2 sc = *reinterpret_cast<const float2*>(src + T::K_BYTES + T::V_BYTES);
-
-            // ---- scores of 16 rows and 16 tokens ----
-            float sf[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sf[u][e] = 0.f;
-#pragma unroll
-                for (int c = 0; c < T::KC; ++c) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + (u * T::KC + c) * 512 + lane * 16);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b0, b1;
-                        e4m3x4_to_f16(ww[k], b0, b1);
-                        mma_f16(sf[u], qa[c * 4 + k], b0, b1);
-                    }
-                }
+        for (int i = 0; i < n_my; ++i) {
+            if ((i & 15) == 0) {  // batch i / 16, whose loads went out with its first copies
+                sk = sk_next;
+                lsv = lg2_approx(sv_next);
+                isv = rcp_approx(sv_next);
+                whole = whole_next;
             }
-            const int tok = cache_block(s, v) * kBlock;
-            const float lsv = lg2_approx(sc.y);
-            const float f[2] = {rq[0] * sc.x, rq[1] * sc.x};
+            cp_async_wait<T::STAGES - 2>();
+            __syncwarp();  // block i is there for every lane, and block i - 1 has been read
+            issue(i + T::STAGES - 1, stage == 0 ? T::STAGES - 1 : stage - 1);
+            const uint8_t* src = my + stage * T::STAGE;
+            stage = stage + 1 == T::STAGES ? 0 : stage + 1;
+
+            // ---- scores of 2 x 16 tokens and NT x 8 rows ----
+            float sf[2][NT][4];  // tokens g, g, g + 8, g + 8; rows 2q, 2q + 1, 2q, 2q + 1
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sf[u][e] = fmaf(sf[u][e], f[e >> 1], lsv);
-            // every query sees all 16 tokens, or each score is checked
-            const bool whole = tok + kBlock - 1 <= first_pos &&
-                               (p.left < 0 || tok >= s.len - 1 - p.left || tok + kBlock <= p.sinks);
-            auto row_sees = [&](int ps, int j) { return j <= ps && (p.left < 0 || j >= ps - p.left || j < p.sinks); };
-            if (!whole) {
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sf[u][n][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < T::KC; ++c) {
+                uint4 w[2][2];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!row_sees(pos[e >> 1], tok + 8 * u + 2 * q + (e & 1))) sf[u][e] = -INFINITY;
-            }
-            // ---- running maximum: raised (and the output rescaled) only when a score passes it ----
-            float mx[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                mx[i] = fmaxf(fmaxf(sf[0][2 * i], sf[0][2 * i + 1]), fmaxf(sf[1][2 * i], sf[1][2 * i + 1]));
-            if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float n = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-                    n = fmaxf(m[i], fmaxf(n, __shfl_xor_sync(0xffffffffu, n, 2)));
-                    const float alpha = n == m[i] ? 1.f : ex2_approx(m[i] - n);  // 0 while m is -inf
-                    m[i] = n;
-                    l[i] *= alpha;
-#pragma unroll
-                    for (int j = 0; j < T::NJ; ++j) {
-                        o[j][2 * i] *= alpha;
-                        o[j][2 * i + 1] *= alpha;
-                    }
-                }
-            }
-            const float inv_sv = 1.f / sc.y;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float sub = (m[i] == -INFINITY ? 0.f : m[i]) - kShift;
-                float sum = 0.f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sf[u][2 * i + e] = ex2_approx(sf[u][2 * i + e] - sub);
-                        sum += sf[u][2 * i + e];
-                    }
-                l[i] = fmaf(sum, inv_sv, l[i]);
-            }
-            // weights rounded to f16 (2^-12 relative): finer than the bf16 output
-            const uint32_t pa[4] = {pack_f16x2(sf[0][0], sf[0][1]), pack_f16x2(sf[0][2], sf[0][3]),
-                                    pack_f16x2(sf[1][0], sf[1][1]), pack_f16x2(sf[1][2], sf[1][3])};
-
-            // ---- output += weights V ----
-            uint32_t vw[4][T::VB / 4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint8_t* at = src + T::K_BYTES + (k * 32 + lane) * T::VB;
-                if constexpr (T::VB == 16) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(at);
-                    vw[k][0] = w.x, vw[k][1] = w.y, vw[k][2] = w.z, vw[k][3] = w.w;
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2*>(at);
-                    vw[k][0] = w.x, vw[k][1] = w.y;
-                }
-            }
-            auto add_pv = [&](const uint32_t (&a)[4], const uint32_t (&w)[4][T::VB / 4]) {
-#pragma unroll
-                for (int i = 0; i < T::VB / 4; ++i) {
-                    const uint32_t x01 = __byte_perm(w[0][i], w[1][i], 0x5140), x23 = __byte_perm(w[0][i], w[1][i], 0x7362);
-                    const uint32_t y01 = __byte_perm(w[2][i], w[3][i], 0x5140), y23 = __byte_perm(w[2][i], w[3][i], 0x7362);
-                    uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-                    e4m3x4_to_f16(x01, a0, a1);
-                    e4m3x4_to_f16(x23, a2, a3);
-                    e4m3x4_to_f16(y01, b0, b1);
-                    e4m3x4_to_f16(y23, b2, b3);
-                    mma_f16(o[4 * i], a, a0, b0);
-                    mma_f16(o[4 * i + 1], a, a1, b1);
-                    mma_f16(o[4 * i + 2], a, a2, b2);
-                    mma_f16(o[4 * i + 3], a, a3, b3);
-                }
-            };
-            bool nan_v = false;  // a NaN code that some query of the tile must not see (0 * NaN is NaN)
-            if (!whole && s.q_len > 1) {
+                    for (int k = 0; k < 2; ++k)
+                        w[u][k] = *reinterpret_cast<const uint4*>(src + u * T::TILE + chunk_at<D>(8 * k + g, 4 * c + q));
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
-                    for (int i = 0; i < T::VB / 4; ++i) nan_v |= __vcmpeq4(vw[k][i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
-            }
-            if (__any_sync(0xffffffffu, nan_v)) {
-                // query by query, with only the rows and the tokens that belong to it
-                const int t_lo = rt * kRows / G, t_hi = min(s.q_len - 1, (rt * kRows + kRows - 1) / G);
-                for (int t = t_lo; t <= t_hi; ++t) {
-                    const int ps = first_pos + t;
-                    uint32_t wt[4][T::VB / 4];
+                    for (int u = 0; u < 2; ++u) {
+                        auto word = [&](const uint4& x) { return k == 0 ? x.x : k == 1 ? x.y : k == 2 ? x.z : x.w; };
+                        uint32_t ka[4];
+                        e4m3x4_to_f16(word(w[u][0]), ka[0], ka[2]);
+                        e4m3x4_to_f16(word(w[u][1]), ka[1], ka[3]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const bool vis = row_sees(ps, tok + 2 * q + (k & 1) + 8 * (k >> 1));
-#pragma unroll
-                        for (int i = 0; i < T::VB / 4; ++i) wt[k][i] = vis ? vw[k][i] : 0u;
+                        for (int n = 0; n < NT; ++n) mma_f16(sf[u][n], ka, qb[n][c * 4 + k][0], qb[n][c * 4 + k][1]);
                     }
-                    // a row of another query gets zero weights; 0 * NaN of this query's
-                    // values would reach it, so its output is kept
-                    const uint32_t at[4] = {pos[0] == ps ? pa[0] : 0u, pos[1] == ps ? pa[1] : 0u,
-                                            pos[0] == ps ? pa[2] : 0u, pos[1] == ps ? pa[3] : 0u};
-                    float kept[T::NJ][4];
+            }
+            const int src0 = (2 * i) & 31;
+            const bool all_seen = ((whole >> src0) & 3u) == 3u;
+            const int tok = cache_block(s, v0 + warp + kWarps * i) * kBlock;
+            if (!all_seen) {
 #pragma unroll
-                    for (int j = 0; j < T::NJ; ++j)
+                for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) kept[j][e] = o[j][e];
-                    add_pv(at, wt);
-#pragma unroll
-                    for (int j = 0; j < T::NJ; ++j)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (pos[e >> 1] != ps) o[j][e] = kept[j][e];
-                }
-            } else {
-                add_pv(pa, vw);
+                            if (!row_sees(pos[n][e & 1], tok + u * kTok + g + 8 * (e >> 1))) sf[u][n][e] = -INFINITY;
             }
-            stage = stage + 1 == kStages ? 0 : stage + 1;
+            float t_sk[2], t_lsv[2], t_isv[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                t_sk[u] = __shfl_sync(0xffffffffu, sk, src0 + u);
+                t_lsv[u] = __shfl_sync(0xffffffffu, lsv, src0 + u);
+                t_isv[u] = __shfl_sync(0xffffffffu, isv, src0 + u);
+            }
+            // ---- score + log2 sv, and the running maximum ----
+            bool passes = false;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float f = rq[n][r] * t_sk[u];
+                        sf[u][n][r] = fmaf(sf[u][n][r], f, t_lsv[u]);
+                        sf[u][n][2 + r] = fmaf(sf[u][n][2 + r], f, t_lsv[u]);
+                    }
+                    const float mx = fmaxf(fmaxf(sf[0][n][r], sf[0][n][2 + r]), fmaxf(sf[1][n][r], sf[1][n][2 + r]));
+                    passes |= mx > m[n][r] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, passes)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float mx = fmaxf(fmaxf(sf[0][n][r], sf[0][n][2 + r]), fmaxf(sf[1][n][r], sf[1][n][2 + r]));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                        mx = fmaxf(m[n][r], mx);
+                        const float alpha = mx == m[n][r] ? 1.f : ex2_approx(m[n][r] - mx);  // 0 while m is -inf
+                        m[n][r] = mx;
+                        l[n][r] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < T::NJ; ++j) {
+                            o[n][j][r] *= alpha;
+                            o[n][j][2 + r] *= alpha;
+                        }
+                    }
+            }
+            // ---- weights: f16 (half a step, 2^-11 relative), finer than the bf16 output ----
+            uint32_t pb[2][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float sub0 = kShift - (m[n][0] == -INFINITY ? 0.f : m[n][0]);
+                const float sub1 = kShift - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float e0 = ex2_approx(sf[u][n][0] + sub0), e1 = ex2_approx(sf[u][n][1] + sub1);
+                    const float e2 = ex2_approx(sf[u][n][2] + sub0), e3 = ex2_approx(sf[u][n][3] + sub1);
+                    l[n][0] = fmaf(e0 + e2, t_isv[u], l[n][0]);
+                    l[n][1] = fmaf(e1 + e3, t_isv[u], l[n][1]);
+                    pb[u][n][0] = transpose_b16(pack_f16x2(e0, e1));
+                    pb[u][n][1] = transpose_b16(pack_f16x2(e2, e3));
+                }
+            }
+
+            // ---- output += V^T weights, tile by tile ----
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t vw[4][T::VB / 4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = 2 * q + (k & 1) + 8 * (k >> 1);
+                    const uint8_t* at = src + u * T::TILE + T::K_BYTES + (T::VB == 16 ? chunk_at<D>(row, g) : chunk_at<D>(row, g >> 1) + (g & 1) * 8);
+                    if constexpr (T::VB == 16) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(at);
+                        vw[k][0] = w.x, vw[k][1] = w.y, vw[k][2] = w.z, vw[k][3] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(at);
+                        vw[k][0] = w.x, vw[k][1] = w.y;
+                    }
+                }
+                auto each_pv = [&](const uint32_t (&w)[4][T::VB / 4], auto product) {  // product j, its A words
+#pragma unroll
+                    for (int k = 0; k < T::VB / 4; ++k) {
+                        uint32_t va[4], vb[4];
+                        e4m3x4_to_f16(__byte_perm(w[0][k], w[1][k], 0x5140), va[0], va[1]);
+                        e4m3x4_to_f16(__byte_perm(w[2][k], w[3][k], 0x5140), va[2], va[3]);
+                        product(2 * k, va);
+                        e4m3x4_to_f16(__byte_perm(w[0][k], w[1][k], 0x7362), vb[0], vb[1]);
+                        e4m3x4_to_f16(__byte_perm(w[2][k], w[3][k], 0x7362), vb[2], vb[3]);
+                        product(2 * k + 1, vb);
+                    }
+                };
+                bool nan_v = false;  // a NaN code that some query of the tile must not see (0 * NaN is NaN)
+                if (!all_seen && s.q_len > 1) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int n = 0; n < T::VB / 4; ++n) nan_v |= __vcmpeq4(vw[k][n] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+                }
+                if (__any_sync(0xffffffffu, nan_v)) {
+                    // query by query, with only the tokens that it sees and only its rows:
+                    // rows of other queries take nothing of such a product, 0 * NaN is in it
+                    const int t_lo = rt * T::ROWS / G, t_hi = min(s.q_len - 1, (rt * T::ROWS + T::ROWS - 1) / G);
+#pragma unroll 1
+                    for (int t = t_lo; t <= t_hi; ++t) {
+                        const int ps = first_pos + t;
+                        uint32_t wt[4][T::VB / 4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool vis = row_sees(ps, tok + u * kTok + 2 * q + (k & 1) + 8 * (k >> 1));
+#pragma unroll
+                            for (int n = 0; n < T::VB / 4; ++n) wt[k][n] = vis ? vw[k][n] : 0u;
+                        }
+                        each_pv(wt, [&](int j, const uint32_t (&va)[4]) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float t4[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_f16(t4, va, pb[u][n][0], pb[u][n][1]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (pos[n][e & 1] == ps) o[n][j][e] += t4[e];
+                            }
+                        });
+                    }
+                } else {
+                    each_pv(vw, [&](int j, const uint32_t (&va)[4]) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(o[n][j], va, pb[u][n][0], pb[u][n][1]);
+                    });
+                }
+            }
         }
         cp_async_wait<0>();
 
         // ---- join the warps ----
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-            l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        }
         __syncwarp();  // every lane is done with its ring
         float* ow = reinterpret_cast<float*>(my);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (q == 0) stat[warp * kRows + g + 8 * i] = make_float2(m[i], l[i]);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)  // columns 2q and 2q + 1: D/8 consecutive d each
+            for (int r = 0; r < 2; ++r) {
 #pragma unroll
-                for (int j = 0; j < T::NJ; j += 4)
-                    *reinterpret_cast<float4*>(ow + (g + 8 * i) * T::O_PITCH + (2 * q + n) * T::VB + j) =
-                        make_float4(o[j][2 * i + n], o[j + 1][2 * i + n], o[j + 2][2 * i + n], o[j + 3][2 * i + n]);
-        }
+                for (int x = 4; x < 32; x <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], x);
+                const int row = 8 * n + 2 * q + r;
+                if (g == 0) stat[warp * T::ROWS + row] = make_float2(m[n][r], l[n][r]);
+#pragma unroll
+                for (int j = 0; j < T::NJ; j += 2)
+                    *reinterpret_cast<float4*>(ow + row * T::O_PITCH + g * T::VB + 2 * j) =
+                        make_float4(o[n][j][r], o[n][j][2 + r], o[n][j + 1][r], o[n][j + 1][2 + r]);
+            }
         __syncthreads();
         const bool finished = v0 == 0 && v1 == s.n;
         const int slot = 2 * blockIdx.x + (v0 == 0 ? 1 : 0);
-        constexpr int CPT = D / 8;  // columns per thread: 8 threads a row
-        const int r = threadIdx.x >> 3, c0 = (threadIdx.x & 7) * CPT;
+        constexpr int TPR = kThreads / T::ROWS, CPT = D / TPR;  // threads a row, columns a thread
+        const int r = threadIdx.x / TPR, c0 = threadIdx.x % TPR * CPT;
         const RowAt a = row_at(p, s.q_len, hk, rt, r);
         if (a.there) {
             float mm = -INFINITY, ll = 0.f, wgt[kWarps];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * kRows + r].x);
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, stat[w * T::ROWS + r].x);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 st = stat[w * kRows + r];
+                const float2 st = stat[w * T::ROWS + r];
                 wgt[w] = st.x == -INFINITY ? 0.f : ex2_approx(st.x - mm);
                 ll += st.y * wgt[w];
             }
@@ -569,17 +722,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_decode_kernel(cons
                 for (int e = 0; e < CPT; e += 2) pk[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
                 uint16_t* dst = static_cast<uint16_t*>(p.o) + b * p.os.b + a.h * p.os.h + a.t * p.os.n + c0;
 #pragma unroll
-                for (int e = 0; e < CPT / 8; ++e)
-                    st_global_v4(dst + 8 * e, pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+                for (int e = 0; e < CPT / 4; ++e) *reinterpret_cast<uint2*>(dst + 4 * e) = make_uint2(pk[2 * e], pk[2 * e + 1]);
                 if (c0 == 0)
                     p.lse[(static_cast<long long>(b) * p.H + a.h) * p.T + a.t] =
                         ll != 0.f ? (mm - kShift + log2f(ll)) * kLn2 : INFINITY;
             } else {
-                float* dst = p.part + (static_cast<long long>(slot) * kRows + r) * D + c0;
+                float* dst = p.part + (static_cast<long long>(slot) * T::ROWS + r) * D + c0;
 #pragma unroll
                 for (int e = 0; e < CPT; e += 4)
                     *reinterpret_cast<float4*>(dst + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-                if (c0 == 0) p.stat[slot * kRows + r] = make_float2(mm, ll);
+                if (c0 == 0) p.stat[slot * T::ROWS + r] = make_float2(mm, ll);
             }
         }
         __syncthreads();  // shared memory is free for the next segment
@@ -589,110 +741,143 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) cache_decode_kernel(cons
 
 // Joins an item's unfinished segments, in the order of the keys: with M the
 // largest of their maxima, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  Block
-// (c, r) looks at the border between shares c and c + 1; the first border inside
-// an item joins row r of the whole item.
+// c - 1 stands for the border before share c; the borders inside an item divide its
+// rows among them.  A row is joined by one warp where it has few segments, else by
+// the whole block, the segments divided among the warps.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinAtOnce = 8;  // segments whose loads go out together
+
+// Running join of segments [i0, i1) of row r: maximum, sum and the lane's D/32 columns.
 template <int D>
-__global__ void __launch_bounds__(kThreads) cache_join_kernel(const CacheFwdParams p) {
-    __shared__ ShareSmem ssm;
-    __shared__ float acc_sm[kWarps][D];
-    __shared__ float2 stat_sm[kWarps];
-    const int c = blockIdx.x + 1, r = blockIdx.y;
-    const Share sh = find_share(p, c, &ssm);
-    pdl_wait();
-    if (sh.b < 0) return;
-    const CacheSeq s = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, sh.b);
-    const long long x = c * sh.share;
-    const int G = p.H / p.Hk, rts = (s.q_len * G + kRows - 1) / kRows;
-    const int item = static_cast<int>((x - sh.b_first) / s.n);
-    const long long i0 = sh.b_first + static_cast<long long>(item) * s.n, i1 = i0 + s.n;
-    if (x == i0 || x - sh.share > i0) return;  // no border here, or not the item's first
-    const RowAt a = row_at(p, s.q_len, item / rts, item % rts, r);
-    if (!a.there) return;
-    // segments: share c - 1 (it starts the item), c, c + 1, ... up to the one with block i1 - 1
-    const int c_last = static_cast<int>((i1 - 1) / sh.share);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto slot = [&](int k) { return 2 * k + (k == c - 1 ? 1 : 0); };
-    constexpr int E = D / 32;
-    float M = -INFINITY;
-    for (int k = c - 1 + static_cast<int>(threadIdx.x); k <= c_last; k += kThreads)
-        M = fmaxf(M, p.stat[slot(k) * kRows + r].x);
+struct Joined {
+    static constexpr int E = D / 32;
+    float m = -INFINITY, l = 0.f, o[E] = {};
+    __device__ void add(float sm, float sl, const float (&y)[E]) {
+        const float n = fmaxf(m, sm);
+        const float a = m == -INFINITY ? 0.f : ex2_approx(m - n), w = sm == -INFINITY ? 0.f : ex2_approx(sm - n);
+        m = n;
+        l = l * a + sl * w;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) stat_sm[warp].x = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, stat_sm[w].x);
-    __syncthreads();
-    float acc[E], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    const int n = c_last - (c - 1) + 1, per = (n + kWarps - 1) / kWarps;
-#pragma unroll 4
-    for (int i = warp * per; i < min(n, warp * per + per); ++i) {
-        const int k = slot(c - 1 + i);
-        const float2 st = p.stat[k * kRows + r];
-        const float w = st.x == -INFINITY ? 0.f : ex2_approx(st.x - M);
-        const float* src = p.part + (static_cast<long long>(k) * kRows + r) * D + lane * E;
-        l += w * st.y;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float2 y = *reinterpret_cast<const float2*>(src + e);
-            acc[e] += w * y.x;
-            acc[e + 1] += w * y.y;
-        }
+        for (int e = 0; e < E; ++e) o[e] = o[e] * a + y[e] * w;
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc_sm[warp][lane * E + e] = acc[e];
-    if (lane == 0) stat_sm[warp].y = l;
-    __syncthreads();
-    if (warp != 0) return;
-    l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        l += stat_sm[w].y;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += acc_sm[w][lane * E + e];
-    }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    uint16_t* dst = static_cast<uint16_t*>(p.o) + sh.b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-        p.lse[(static_cast<long long>(sh.b) * p.H + a.h) * p.T + a.t] =
-            l != 0.f ? (M - kShift + log2f(l)) * kLn2 : INFINITY;
-}
+};
 
 template <int D>
-cudaError_t launch_decode_impl(const CacheFwdParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const CacheFwdParams p) {
+    constexpr int E = D / 32;
+    __shared__ float o_sm[kJoinWarps][D];
+    __shared__ float2 stat_sm[kJoinWarps];
+    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const CacheBorder bd = p.border[c];
+    if (bd.c_first < 0) return;  // the share begins with its item
+    const int G = p.H / p.Hk, rts = (bd.q_len * G + p.rows - 1) / p.rows;
+    const int hk = bd.item / rts, rt = bd.item - hk * rts;
+    const int rows = min(p.rows, bd.q_len * G - rt * p.rows);
+    const int n = bd.c_last - bd.c_first + 2;  // segments: of CTAs c_first - 1 (which starts the item) .. c_last
+    auto join = [&](int r, int i0, int i1) {
+        Joined<D> x;
+        for (int i = i0; i < i1; i += kJoinAtOnce) {
+            float2 st[kJoinAtOnce];
+            float y[kJoinAtOnce][E];
+#pragma unroll
+            for (int u = 0; u < kJoinAtOnce; ++u) {
+                st[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[u][e] = 0.f;
+                if (i + u < i1) {
+                    const long long k = 2 * (bd.c_first - 1 + i + u) + (i + u == 0 ? 1 : 0);
+                    st[u] = p.stat[k * p.rows + r];
+                    const float* src = p.part + (k * p.rows + r) * D + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(src + e);
+                        y[u][e] = v.x;
+                        y[u][e + 1] = v.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinAtOnce; ++u) x.add(st[u].x, st[u].y, y[u]);
+        }
+        return x;
+    };
+    auto write = [&](int r, const Joined<D>& x) {
+        const RowAt a = row_at(p, bd.q_len, hk, rt, r);
+        const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
+        uint16_t* dst = static_cast<uint16_t*>(p.o) + bd.b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(x.o[e] * inv, x.o[e + 1] * inv);
+        if (lane == 0)
+            p.lse[(static_cast<long long>(bd.b) * p.H + a.h) * p.T + a.t] =
+                x.l != 0.f ? (x.m - kShift + log2f(x.l)) * kLn2 : INFINITY;
+    };
+    const int mine = c - bd.c_first, borders = n - 1;
+    if (n <= 2 * kJoinAtOnce) {
+        for (int r = mine + borders * warp; r < rows; r += borders * kJoinWarps) write(r, join(r, 0, n));
+        return;
+    }
+    const int per = (n + kJoinWarps - 1) / kJoinWarps;
+    for (int r = mine; r < rows; r += borders) {
+        const Joined<D> x = join(r, min(n, warp * per), min(n, warp * per + per));
+#pragma unroll
+        for (int e = 0; e < E; ++e) o_sm[warp][lane * E + e] = x.o[e];
+        if (lane == 0) stat_sm[warp] = make_float2(x.m, x.l);
+        __syncthreads();
+        if (warp == 0) {
+            Joined<D> z;
+            for (int w = 0; w < kJoinWarps; ++w) {
+                float y[E];
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = o_sm[w][lane * E + e];
+                z.add(stat_sm[w].x, stat_sm[w].y, y);
+            }
+            write(r, z);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
+    using T = DecodeTraits<D, NT>;
     static const cudaError_t attr = cudaFuncSetAttribute(
-        cache_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeTraits<D>::SMEM);
+        cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     if (attr != cudaSuccess) return attr;
-    cache_decode_kernel<D><<<p.grid, kThreads, DecodeTraits<D>::SMEM, stream>>>(p);
+    p.rows = T::ROWS;
+    p.grid = sms * T::CTAS_PER_SM < kCacheGridMax ? sms * T::CTAS_PER_SM : kCacheGridMax;
+    cache_decode_kernel<D, NT><<<p.grid, kThreads, T::SMEM, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.grid == 1) return e;
-    const int rows = p.T * (p.H / p.Hk);  // rows of a tile that exist
     cudaLaunchAttribute pdl;
     pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(rows < kRows ? rows : kRows));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1));
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = stream;
     cfg.attrs = &pdl;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p);
 }
 
+template <int D>
+cudaError_t launch_decode_d(const CacheFwdParams& p, cudaStream_t stream) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long rows = static_cast<long long>(p.T) * (p.H / p.Hk);
+    if (rows <= 8) return launch_decode_impl<D, 1>(p, sms, stream);
+    return launch_decode_impl<D, 2>(p, sms, stream);
+}
+
 }  // namespace
 
-int cache_decode_ctas_per_sm() { return kCtasPerSm; }
-
 cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream) {
-    if (p.D == 64) return launch_decode_impl<64>(p, stream);
-    if (p.D == 128) return launch_decode_impl<128>(p, stream);
+    if (p.D == 64) return launch_decode_d<64>(p, stream);
+    if (p.D == 128) return launch_decode_d<128>(p, stream);
     return cudaErrorInvalidValue;
 }
 

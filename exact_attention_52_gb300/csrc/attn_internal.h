@@ -135,8 +135,15 @@ struct CacheAppendParams {
     DevStatus st;
 };
 
-// Segments a CTA of the cache attention can leave unfinished: the one it starts
-// inside and the one it ends inside.
+// What the joining kernel of the cache attention finds at the border before a CTA's share.
+struct CacheBorder {
+    int b, item, q_len;  // the item that the border splits
+    int c_first, c_last; // first (-1: the border splits nothing) and last border inside that item
+};
+
+constexpr int kCacheGridMax = 1024;
+constexpr int kCacheRowsMax = 16;
+
 struct CacheFwdParams {
     CacheView c;
     const void* q;  // bf16 [B, H, T, D] with strides qs
@@ -147,9 +154,13 @@ struct CacheFwdParams {
     int B, H, Hk, T, D;
     float cs;  // scale * log2(e)
     int left, sinks;
-    int grid;      // CTAs that share the work
+    // Set by the launcher:
+    int rows;      // query rows of a tile
+    int grid;      // CTAs that share the work, at most kCacheGridMax
+    // Workspace, for kCacheGridMax CTAs and kCacheRowsMax rows whatever the launch:
     float* part;   // unfinished segments: fp32 [2 * grid][rows][D]
     float2* stat;  // their maximum (log2 units) and sum: [2 * grid][rows]
+    CacheBorder* border;  // [grid]
     DevStatus st;
 };
 
@@ -166,7 +177,6 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
 cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream);
-int cache_decode_ctas_per_sm();
 cudaError_t launch_wait_selftest(DevStatus st, cudaStream_t stream);
 
 // Problem check shared by the entry points (sizes, head dim, scale, causal
