@@ -60,6 +60,11 @@ SIGNATURES = {
                               _i, _i, _vp]),
     "attn_bwd_strided": (_i, [_vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _st, _vp,
                               _st, _vp, _st, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _vp]),
+    "attn_fwd_sinks": (_i, [_vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _i, _f, _i, _i,
+                            _i, _vp]),
+    "attn_bwd_sinks_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_bwd_sinks": (_i, [_vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _st, _vp, _st,
+                            _vp, _st, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _i, _vp]),
     "attn_fwd_fp8": (_i, [_vp, _vp, _vp, _f, _f, _f, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
     "attn_cache_append": (_i, [ctypes.POINTER(Cache), _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _vp]),
     "attn_fwd_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
@@ -396,6 +401,85 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
         dout.data_ptr(), st(dout), lse.data_ptr(), dq.data_ptr(), st(dq), dk.data_ptr(), st(dk),
         dv.data_ptr(), st(dv), workspace.data_ptr(), B, H, Hk, N, d, scale, int(window[0]),
         int(window[1]), _stream_handle(stream)))
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------
+# Sliding window with sinks
+# ---------------------------------------------------------------------------
+def _sinks_shape(device, q, k, v, layout):
+    import torch
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check_on(device, name, t, torch.bfloat16, 4)
+    B, H, N, d = _bhnd_shape(q, layout)
+    Hk = _bhnd_shape(k, layout)[1]
+    if _bhnd_shape(k, layout) != (B, Hk, N, d) or k.shape != v.shape:
+        raise ValueError(f"k and v must have q's batch, length and d, got {tuple(k.shape)} and {tuple(v.shape)}")
+    return B, H, Hk, N, d
+
+
+def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layout: str = "bhnd",
+              scale: float | None = None, o=None, lse=None, stream=None):
+    """Sliding-window forward whose first ``sinks`` tokens stay visible: key j visible to query i
+    iff j <= i + window_right (-1: no bound) and (window_left is -1, or j >= i - window_left, or
+    j < sinks).  bf16 q [B, H, N, d], k and v [B, Hk, N, d] (``layout`` "bhnd") or [B, N, heads, d]
+    ("bnhd"), any strides with a contiguous last dimension.  Returns (O like q, LSE [B, H, N])."""
+    import torch
+    device = _call_device(q, "q")
+    B, H, Hk, N, d = _sinks_shape(device, q, k, v, layout)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    with _on_stream(stream):
+        o = torch.empty_like(q) if o is None else o
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=device) if lse is None else lse
+    _check_on(device, "o", o, torch.bfloat16, 4)
+    _check_on(device, "lse", lse, torch.float32, 3)
+    if o.shape != q.shape or lse.shape != (B, H, N) or not lse.is_contiguous():
+        raise ValueError(f"o must have q's shape and lse be a contiguous {(B, H, N)}")
+    st = lambda t: _bhnd_strides(t, layout)
+    _check("attn_fwd_sinks", load_library().attn_fwd_sinks(
+        q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o), lse.data_ptr(),
+        B, H, Hk, N, d, scale, int(window_left), int(window_right), int(sinks), _stream_handle(stream)))
+    return o, lse
+
+
+def bwd_sinks_workspace_bytes(B: int, H: int, Hk: int, N: int, d: int, sinks: int) -> int:
+    return int(load_library().attn_bwd_sinks_workspace_bytes(B, H, Hk, N, d, sinks))
+
+
+def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right: int = 0,
+              layout: str = "bhnd", scale: float | None = None, dq=None, dk=None, dv=None,
+              workspace=None, stream=None):
+    """Backward of ``fwd_sinks``: (dQ, dK, dV), each in the layout of its input; dK and dV are
+    summed over the query heads that share them.  ``workspace``: ``bwd_sinks_workspace_bytes``
+    bytes, one for each call that may overlap."""
+    import torch
+    device = _call_device(q, "q")
+    B, H, Hk, N, d = _sinks_shape(device, q, k, v, layout)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    need = bwd_sinks_workspace_bytes(B, H, Hk, N, d, int(sinks))
+    if need == 0:
+        raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, N {N}, d {d}, sinks {sinks}")
+    with _on_stream(stream):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _check_on(device, name, t, torch.bfloat16, 4)
+        if t.shape != like.shape:
+            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    _check_on(device, "lse", lse, torch.float32, 3)
+    if lse.shape != (B, H, N) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous {(B, H, N)}")
+    if workspace.device != device or workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace needs {need} bytes on {device}")
+    st = lambda t: _bhnd_strides(t, layout)
+    _check("attn_bwd_sinks", load_library().attn_bwd_sinks(
+        q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o), dout.data_ptr(),
+        st(dout), lse.data_ptr(), dq.data_ptr(), st(dq), dk.data_ptr(), st(dk), dv.data_ptr(), st(dv),
+        workspace.data_ptr(), B, H, Hk, N, d, scale, int(window_left), int(window_right), int(sinks),
+        _stream_handle(stream)))
     return dq, dk, dv
 
 

@@ -181,18 +181,35 @@ attn_status check_window(int wl, int wr) { return (wl >= -1 && wr >= -1) ? ATTN_
 
 long long npad(int N) { return (static_cast<long long>(N) + kTile - 1) / kTile * kTile; }
 
+int sink_tiles_of(int sinks) { return (sinks + kTile - 1) / kTile; }
+long long sink_items_of(int B, int Hk, int sinks) { return static_cast<long long>(B) * Hk * sink_tiles_of(sinks); }
+
+// Window and sinks of a sequence of N tokens, as the kernels take them: sinks within
+// the sequence, none where the window has no left bound or covers the sequence (which
+// is then the plain causal or unmasked launch).
+attn_status sink_mask(int N, int* left, int* right, int* sinks) {
+    if (*sinks < 0 || check_window(*left, *right) != ATTN_OK) return ATTN_ERR_INVALID;
+    if (*left >= N - 1) *left = -1;
+    if (*right >= N - 1) *right = -1;
+    if (*sinks > N) *sinks = N;
+    if (*left < 0) *sinks = 0;
+    return ATTN_OK;
+}
+
 size_t round256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct BwdLayout {
     size_t dq_acc, lse2, dsum, split_cnt, split_part, total;
     int split_cap;  // parts of split items the workspace holds (0: none)
+    int split_cnt_words;
 };
 
 // fp32 dQ accumulator, -LSE log2 e, D; for d = 128 (split) also the counters and
 // partials of split items: at most min(kBwdSplitCap, items * min(10, ceil(N / 128)))
 // parts, items <= B * H * ceil(N / 128) (an item is split at most ten ways, and
-// never into more parts than its steps).
-BwdLayout bwd_layout(int B, int H, int N, int d, bool split) {
+// never into more parts than its steps); with sinks (sink_items: key tiles of all
+// key/value heads that hold one) at most min(kBwdSinkCap, sink_items * kBwdSinkParts).
+BwdLayout bwd_layout(int B, int H, int N, int d, bool split, long long sink_items) {
     const size_t rows = static_cast<size_t>(B) * H * npad(N);
     BwdLayout L;
     L.dq_acc = 0;
@@ -200,13 +217,16 @@ BwdLayout bwd_layout(int B, int H, int N, int d, bool split) {
     L.dsum = L.lse2 + round256(rows * sizeof(float));
     L.split_cnt = L.split_part = L.dsum + round256(rows * sizeof(float));
     L.total = L.split_cnt;
-    L.split_cap = 0;
+    L.split_cap = L.split_cnt_words = 0;
     if (split && d == 128) {
         const long long tiles = npad(N) / kTile;
-        const long long room = static_cast<long long>(B) * H * tiles * (tiles < 10 ? tiles : 10);
-        L.split_cap = static_cast<int>(room < kBwdSplitCap ? room : kBwdSplitCap);
+        const long long room = sink_items > 0 ? sink_items * kBwdSinkParts
+                                              : static_cast<long long>(B) * H * tiles * (tiles < 10 ? tiles : 10);
+        const long long most = sink_items > 0 ? kBwdSinkCap : kBwdSplitCap;
+        L.split_cap = static_cast<int>(room < most ? room : most);
         if (L.split_cap > 0) {
-            L.split_part = L.split_cnt + round256(kBwdSplitCntWords * sizeof(unsigned));
+            L.split_cnt_words = sink_items > 0 ? L.split_cap * 8 : kBwdSplitCntWords;
+            L.split_part = L.split_cnt + round256(L.split_cnt_words * sizeof(unsigned));
             L.total = L.split_part + round256(static_cast<size_t>(L.split_cap) * 2 * kTile * d * sizeof(float));
         }
     }
@@ -246,7 +266,7 @@ struct SplitArgs {
 attn_status fwd_run(const void* q, const Strides& qs, const void* k, const Strides& ks, const void* v,
                     const Strides& vs, void* o, const Strides& os, float* lse, int B, int H, int Hk,
                     int N, int d, float scale, int win_left, int win_right, attn_stream_t stream,
-                    const SplitArgs& split = SplitArgs()) {
+                    const SplitArgs& split = SplitArgs(), int sinks = 0) {
     const int causal = (win_left == -1 && win_right == 0) ? 1 : 0;
     attn_status rc = check_sizes(B, H, N, d, scale, causal);
     if (rc != ATTN_OK) return rc;
@@ -274,6 +294,7 @@ attn_status fwd_run(const void* q, const Strides& qs, const void* k, const Strid
     p.causal = causal;
     p.win_left = win_left;
     p.win_right = win_right;
+    p.sinks = sinks;
     p.cs = scale * 1.44269504088896340736f;
     p.out_scale = 1.f;
     p.n_splits = split.n_splits;
@@ -316,23 +337,24 @@ struct BwdCall {
     float* dsum = nullptr;
     unsigned* split_cnt = nullptr;
     float* split_part = nullptr;
-    int split_cap = 0;
+    int split_cap = 0, split_cnt_words = 0;
     int BH = 0, Np = 0;
 };
 
 attn_status bwd_prepare(void* workspace, int B, int H, int N, int d, float scale, int causal, bool split,
-                        BwdCall* c) {
+                        long long sink_items, BwdCall* c) {
     attn_status rc = check_sizes(B, H, N, d, scale, causal);
     if (rc != ATTN_OK) return rc;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return ATTN_ERR_INVALID;
     if ((rc = device_state(&c->ds)) != ATTN_OK) return rc;
-    const BwdLayout L = bwd_layout(B, H, N, d, split);
+    const BwdLayout L = bwd_layout(B, H, N, d, split, sink_items);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     c->dq_acc = reinterpret_cast<float*>(ws + L.dq_acc);
     c->lse2 = reinterpret_cast<float*>(ws + L.lse2);
     c->dsum = reinterpret_cast<float*>(ws + L.dsum);
     c->split_cap = L.split_cap;
+    c->split_cnt_words = L.split_cnt_words;
     if (L.split_cap > 0) {
         c->split_cnt = reinterpret_cast<unsigned*>(ws + L.split_cnt);
         c->split_part = reinterpret_cast<float*>(ws + L.split_part);
@@ -344,16 +366,16 @@ attn_status bwd_prepare(void* workspace, int B, int H, int N, int d, float scale
 
 attn_status bwd_pre_run(const void* o, const Strides& os, const void* dout, const Strides& dos,
                         const float* lse, void* workspace, int B, int H, int N, int d, bool split,
-                        attn_stream_t stream) {
+                        long long sink_items, attn_stream_t stream) {
     for (const void* p : {o, dout, static_cast<const void*>(lse)})
         if (!aligned16(p)) return ATTN_ERR_INVALID;
     if (!strides_ok(os, 2) || !strides_ok(dos, 2)) return ATTN_ERR_INVALID;
     BwdCall c;
-    attn_status rc = bwd_prepare(workspace, B, H, N, d, 1.f, 0, split, &c);
+    attn_status rc = bwd_prepare(workspace, B, H, N, d, 1.f, 0, split, sink_items, &c);
     if (rc != ATTN_OK) return rc;
     BwdPreParams pp;
     pp.split_cnt = c.split_cnt;
-    pp.split_cnt_words = c.split_cap > 0 ? kBwdSplitCntWords : 0;
+    pp.split_cnt_words = c.split_cnt_words;
     pp.o = o;
     pp.dout = dout;
     pp.os = os;
@@ -375,7 +397,7 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
                          const void* v, const Strides& vs, const void* dout, const Strides& dos,
                          void* dk, const Strides& dks, void* dv, const Strides& dvs, void* workspace,
                          int B, int H, int Hk, int N, int d, float scale, int win_left, int win_right,
-                         bool split, attn_stream_t stream) {
+                         int sinks, bool split, attn_stream_t stream) {
     for (const void* p : {q, k, v, dout, static_cast<const void*>(dk), static_cast<const void*>(dv)})
         if (!aligned16(p)) return ATTN_ERR_INVALID;
     for (const Strides* st : {&qs, &ks, &vs, &dos, &dks, &dvs})
@@ -385,7 +407,8 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
         return rc;
     const int causal = (win_left == -1 && win_right == 0) ? 1 : 0;
     BwdCall c;
-    if ((rc = bwd_prepare(workspace, B, H, N, d, scale, causal, split, &c)) != ATTN_OK) return rc;
+    if ((rc = bwd_prepare(workspace, B, H, N, d, scale, causal, split, sink_items_of(B, Hk, sinks), &c)) != ATTN_OK)
+        return rc;
     CUtensorMap tq, tk, tv, tdo, tdq;
     if (!make_map(&tq, q, false, d, N, H, B, qs) || !make_map(&tk, k, false, d, N, Hk, B, ks) ||
         !make_map(&tv, v, false, d, N, Hk, B, vs) || !make_map(&tdo, dout, false, d, N, H, B, dos) ||
@@ -408,6 +431,8 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
     bp.causal = causal;
     bp.win_left = win_left;
     bp.win_right = win_right;
+    bp.sinks = sinks;
+    bp.sink_tiles = sink_tiles_of(sinks);
     bp.cs = scale * 1.44269504088896340736f;
     bp.scale = scale;
     bp.split_base = bp.BHk * bp.n_kv;  // the launcher decides on a split
@@ -427,7 +452,7 @@ attn_status dq_convert_run(void* dq, const Strides& dqs, void* workspace, int B,
                            float scale, attn_stream_t stream) {
     if (!aligned16(dq) || !strides_ok(dqs, 2)) return ATTN_ERR_INVALID;
     BwdCall c;
-    attn_status rc = bwd_prepare(workspace, B, H, N, d, scale, 0, false, &c);
+    attn_status rc = bwd_prepare(workspace, B, H, N, d, scale, 0, false, 0, &c);
     if (rc != ATTN_OK) return rc;
     DqConvertParams cp;
     cp.dq_acc = c.dq_acc;
@@ -451,7 +476,7 @@ attn_status bwd_run(const void* q, const Strides& qs, const void* k, const Strid
                     const Strides& dos, const float* lse, void* dq, const Strides& dqs, void* dk,
                     const Strides& dks, void* dv, const Strides& dvs, void* workspace, int B, int H,
                     int Hk, int N, int d, float scale, int win_left, int win_right,
-                    attn_stream_t stream, bool split = true) {
+                    attn_stream_t stream, bool split = true, int sinks = 0) {
     const int causal = (win_left == -1 && win_right == 0) ? 1 : 0;
     attn_status rc = check_sizes(B, H, N, d, scale, causal);
     if (rc != ATTN_OK) return rc;
@@ -464,9 +489,11 @@ attn_status bwd_run(const void* q, const Strides& qs, const void* k, const Strid
         if (!strides_ok(*st, 2)) return ATTN_ERR_INVALID;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return ATTN_ERR_INVALID;
-    if ((rc = bwd_pre_run(o, os, dout, dos, lse, workspace, B, H, N, d, split, stream)) != ATTN_OK) return rc;
+    if ((rc = bwd_pre_run(o, os, dout, dos, lse, workspace, B, H, N, d, split, sink_items_of(B, Hk, sinks),
+                          stream)) != ATTN_OK)
+        return rc;
     if ((rc = bwd_main_run(q, qs, k, ks, v, vs, dout, dos, dk, dks, dv, dvs, workspace, B, H, Hk, N, d,
-                           scale, win_left, win_right, split, stream)) != ATTN_OK)
+                           scale, win_left, win_right, sinks, split, stream)) != ATTN_OK)
         return rc;
     return dq_convert_run(dq, dqs, workspace, B, H, N, d, scale, stream);
 }
@@ -520,7 +547,7 @@ int check_problem(int B, int H, int N, int d, float scale, int causal) {
 
 size_t bwd_workspace_bytes_for(int B, int H, int N, int d, bool split) {
     if (check_sizes(B, H, N, d, 1.f, 0) != ATTN_OK) return 0;
-    return bwd_layout(B, H, N, d, split).total;
+    return bwd_layout(B, H, N, d, split, 0).total;
 }
 
 int bwd_dense(const void* q, const void* k, const void* v, const void* o, const void* dout,
@@ -660,6 +687,7 @@ attn_status attn_fwd_fp8(const void* q8, const void* k8, const void* v8, float s
     p.causal = causal;
     p.win_left = -1;
     p.win_right = causal ? 0 : -1;
+    p.sinks = 0;
     p.cs = scale * sq * sk * 1.44269504088896340736f;
     p.out_scale = sv;
     p.n_splits = 1;
@@ -683,7 +711,7 @@ attn_status attn_bwd_preprocess(const void* o, const void* dout, const float* ls
                                 int B, int H, int N, int d, attn_stream_t stream) {
     if (check_sizes(B, H, N, d, 1.f, 0) != ATTN_OK) return check_sizes(B, H, N, d, 1.f, 0);
     const Strides ds = dense(H, N, d);
-    return bwd_pre_run(o, ds, dout, ds, lse, workspace, B, H, N, d, true, stream);
+    return bwd_pre_run(o, ds, dout, ds, lse, workspace, B, H, N, d, true, 0, stream);
 }
 
 attn_status attn_bwd_main(const void* q, const void* k, const void* v, const void* dout, void* dk,
@@ -693,7 +721,7 @@ attn_status attn_bwd_main(const void* q, const void* k, const void* v, const voi
     if (check_sizes(B, H, N, d, scale, causal) != ATTN_OK) return check_sizes(B, H, N, d, scale, causal);
     const Strides ds = dense(H, N, d);
     return bwd_main_run(q, ds, k, ds, v, ds, dout, ds, dk, ds, dv, ds, workspace, B, H, H, N, d, scale,
-                        -1, causal ? 0 : -1, true, stream);
+                        -1, causal ? 0 : -1, 0, true, stream);
 }
 
 attn_status attn_bwd_dq_convert(void* dq, void* workspace, int B, int H, int N, int d, float scale,
@@ -744,6 +772,33 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
     return bwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), dout,
                    from_abi(dos), lse, dq, from_abi(dqs), dk, from_abi(dks), dv, from_abi(dvs),
                    workspace, B, H, Hk, N, d, scale, window_left, window_right, stream);
+}
+
+attn_status attn_fwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks, const void* v,
+                           attn_strides_t vs, void* o, attn_strides_t os, float* lse, int B, int H, int Hk, int N,
+                           int d, float scale, int window_left, int window_right, int sinks, attn_stream_t stream) {
+    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK) return ATTN_ERR_INVALID;
+    return fwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), lse, B, H, Hk, N, d, scale,
+                   window_left, window_right, stream, SplitArgs(), sinks);
+}
+
+size_t attn_bwd_sinks_workspace_bytes(int B, int H, int Hk, int N, int d, int sinks) {
+    if (check_sizes(B, H, N, d, 1.f, 0) != ATTN_OK || check_group(H, Hk) != ATTN_OK || sinks < 0) return 0;
+    // room for either launch: whether there are sinks to split for depends on the window
+    const size_t plain = bwd_layout(B, H, N, d, true, 0).total;
+    const size_t split = bwd_layout(B, H, N, d, true, sink_items_of(B, Hk, sinks < N ? sinks : N)).total;
+    return plain > split ? plain : split;
+}
+
+attn_status attn_bwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks, const void* v,
+                           attn_strides_t vs, const void* o, attn_strides_t os, const void* dout, attn_strides_t dos,
+                           const float* lse, void* dq, attn_strides_t dqs, void* dk, attn_strides_t dks, void* dv,
+                           attn_strides_t dvs, void* workspace, int B, int H, int Hk, int N, int d, float scale,
+                           int window_left, int window_right, int sinks, attn_stream_t stream) {
+    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK) return ATTN_ERR_INVALID;
+    return bwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), dout, from_abi(dos), lse, dq,
+                   from_abi(dqs), dk, from_abi(dks), dv, from_abi(dvs), workspace, B, H, Hk, N, d, scale, window_left,
+                   window_right, stream, true, sinks);
 }
 
 attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_strides_t ks, const void* v,

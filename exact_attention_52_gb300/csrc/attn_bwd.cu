@@ -182,6 +182,9 @@ __global__ void __launch_bounds__(kAuxThreads) dq_convert_kernel(const DqConvert
 // Work of one backward CTA: one 128-row key tile of one key/value head and the
 // query tiles (of every query head of its group) that see some key of it.
 // ---------------------------------------------------------------------------
+// SINKS (see BwdParams::sinks): a template parameter, so that launches without
+// sinks keep the code they had (its registers are all taken).
+template <bool SINKS>
 struct BwdWork {
     int kv_bh, j;        // (batch, key/value head) index and key tile
     int n_q_total;       // query tiles of a head
@@ -195,7 +198,9 @@ struct BwdWork {
     int parts;           // parts of the item (1: whole)
     int tt0, bh_first;   // (tile step, query head) of the first step
 
-    __device__ explicit BwdWork(const BwdParams& prm) : BwdWork(prm, static_cast<int>(blockIdx.x)) {}
+    // One CTA per item (d = 64): the long sink items first.
+    __device__ explicit BwdWork(const BwdParams& prm)
+        : BwdWork(prm, static_cast<int>(SINKS ? gridDim.x - 1 - blockIdx.x : blockIdx.x)) {}
 
     // Work item `item` of the launch's numbering (items = key tiles of every
     // key/value head), whole.
@@ -205,14 +210,22 @@ struct BwdWork {
         // those heads' Q, dO and fp32 dQ accumulator stay in L2 while every key
         // tile reduces into them.  Causal: low key tiles (longest loops) of every
         // head first, which keeps the tail of the launch short.
-        kv_bh = prm.causal ? item % prm.BHk : item / prm.n_kv;
-        j = prm.causal ? item / prm.BHk : item % prm.n_kv;
+        // With sinks: the key tiles without one head-major, then the sink tiles, whose
+        // loops reach to the last query tile (in parts, where the launch splits them).
+        if constexpr (SINKS) {
+            const int n_plain = prm.n_kv - prm.sink_tiles, sink = item - prm.BHk * n_plain;
+            kv_bh = sink < 0 ? item / n_plain : sink % prm.BHk;
+            j = sink < 0 ? prm.sink_tiles + item % n_plain : sink / prm.BHk;
+        } else {
+            kv_bh = prm.causal ? item % prm.BHk : item / prm.n_kv;
+            j = prm.causal ? item / prm.BHk : item % prm.n_kv;
+        }
         n_q_total = (N + kTile - 1) / kTile;
         // Query tiles holding the rows that see some key of this tile (window
         // i - win_left <= key <= i + win_right; negative = no bound).
         const int kr0 = j * kTile, kr1 = min(N - 1, j * kTile + kTile - 1);
         const int qrow_lo = prm.win_right < 0 ? 0 : max(0, kr0 - prm.win_right);
-        const int qrow_hi = prm.win_left < 0 ? N - 1 : min(N - 1, kr1 + prm.win_left);
+        const int qrow_hi = prm.win_left < 0 || (SINKS && kr0 < prm.sinks) ? N - 1 : min(N - 1, kr1 + prm.win_left);
         q_lo = qrow_lo / kTile;
         n_qh = qrow_lo <= qrow_hi ? qrow_hi / kTile - q_lo + 1 : 0;  // per query head
         full_range = (q_lo == 0 && n_qh == n_q_total);
@@ -232,6 +245,7 @@ struct BwdWork {
     // Item `v` of a launch with a split last round: from split_base on, part
     // (v - split_base) % P of item split_base + (v - split_base) / P, which takes
     // steps [t0, t1) of the item's walk (query head by query head, tile by tile).
+    // (Sinks: the split items are the sink tiles.)
     __device__ static BwdWork split_at(const BwdParams& prm, int v) {
         if (v < prm.split_base) return BwdWork(prm, v);
         const int s = v - prm.split_base, P = prm.split_parts;
@@ -274,7 +288,7 @@ struct BwdWork {
 // own compute warpgroup and its own 128 tensor-memory columns, so that the
 // tensor core computes one half's S^T/dP^T while the other half's P^T/dS^T
 // are being formed, and dV/dK for a half start as soon as that half is ready.
-template <int D>
+template <int D, bool SINKS>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
 
     const int N = prm.N;
-    const BwdWork w(prm);
+    const BwdWork<SINKS> w(prm);
     const int j = w.j, n_qh = w.n_qh, q_bh0 = w.q_bh0, b_idx = w.b_idx, hk_idx = w.hk_idx,
               bH0 = w.bH0, n_steps = w.n_steps;
     auto q_tile = [&](int tt) { return w.q_tile(tt); };
@@ -494,6 +508,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int wq = warp & 3;
         const int r = wq * 32 + lane;  // key row within the tile
         const int kv_row = j * kTile + r;
+        const int win_left = SINKS && kv_row < prm.sinks ? -1 : prm.win_left;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
         const uint32_t tS = tmem + h * T::COL_REGION + lane_off;
         const uint32_t tDP = tS + T::COL_DP;
@@ -522,7 +537,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // warp needs it (boundary tiles of a causal mask or a window)
             const int qc0 = i * kTile + h * 64;
             const int cmin = prm.win_right < 0 ? -kTile : kv_row - prm.win_right - qc0;
-            const int cmax = prm.win_left < 0 ? 2 * kTile : kv_row + prm.win_left - qc0;
+            const int cmax = win_left < 0 ? 2 * kTile : kv_row + win_left - qc0;
             const bool masked = __any_sync(0xffffffffu, cmin > 0 || cmax < 63);
             auto chunk = [&](auto masked_tag, int cc) {
                 constexpr bool kMasked = decltype(masked_tag)::value;
@@ -907,7 +922,8 @@ __device__ __forceinline__ uint2 split3_half_bf16(float v) {
 constexpr unsigned kDqPauseNs = 60;
 
 // MODE 0: items dealt in snake order; 1: the same with a split last round; 2: the
-// per-CTA lists of a BwdDeal (causal launches with long items).  V8: every dK and
+// per-CTA lists of a BwdDeal (causal launches with long items); 3: as 1, with sinks
+// (the split items are the sink tiles').  V8: every dK and
 // dV row starts on a 32-byte boundary (32-byte stores in the epilogue; a runtime
 // choice between the two store widths measured 1-2 % slower than either alone).
 template <int MODE, bool V8>
@@ -917,6 +933,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                          const BwdParams prm, const __grid_constant__ BwdDealArg<MODE> deal) {
     using T = BwdFullTraits;
     constexpr int D = T::D;
+    constexpr bool SINKS = MODE == 3;
+    using Work = BwdWork<SINKS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -954,12 +972,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // epilogue (dV, dK out of tensor memory) overlaps the next item's K/V copy
     // and first products.  item_at returns -1 after the last round and -2 for a
     // round in which this CTA has no item (only the last round can be short).
-    const int n_items = MODE == 1 ? prm.split_base + (prm.BHk * prm.n_kv - prm.split_base) * prm.split_parts
+    const int n_items = MODE == 1 || MODE == 3 ? prm.split_base + (prm.BHk * prm.n_kv - prm.split_base) * prm.split_parts
                                   : prm.BHk * prm.n_kv;
     auto work = [&](int v) {  // the work of item v (a part of a split item from split_base on)
-        if constexpr (MODE == 1) return BwdWork::split_at(prm, v);
-        else if constexpr (MODE == 2) return BwdWork::dealt(prm, v);
-        else return BwdWork(prm, v);
+        if constexpr (MODE == 1 || MODE == 3) return Work::split_at(prm, v);
+        else if constexpr (MODE == 2) return Work::dealt(prm, v);
+        else return Work(prm, v);
     };
     auto item_at = [&](int r) -> int {
         if constexpr (MODE == 2) {  // entry r of this CTA's list
@@ -1055,7 +1073,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const int item = item_at(rr);
                 if (item == -1) return;
                 if (item < 0) continue;
-                const BwdWork w = work(item);
+                const Work w = work(item);
                 if (w.n_steps > 0) {
                     bh = w.bh_first;
                     tile = w.q_tile(w.tt0);
@@ -1124,7 +1142,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int item = item_at(r);
             if (item == -1) break;
             if (item < 0) continue;
-            const BwdWork w = work(item);
+            const Work w = work(item);
             int nx_bh, nx_tile;  // first step of the next item with steps
             first_step(r + 1, nx_bh, nx_tile);
             int tt = w.tt0, bh = w.bh_first;
@@ -1291,7 +1309,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const int item = item_at(r);
                 if (item == -1) break;
                 if (item < 0) continue;
-                const BwdWork w = work(item);
+                const Work w = work(item);
                 if (w.n_steps == 0) {  // nothing sees this key tile: zero dV, dK, release K/V
                     if (!wait_warp(b_kv, k & 1, abort_flag, prm.st, SITE_KV)) break;
                     mma_commit_warp(b_dkv_full);
@@ -1323,8 +1341,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int item = item_at(rr);
         if (item == -1) break;
         if (item < 0) continue;
-        const BwdWork w = work(item);
+        const Work w = work(item);
         const int kv_row = w.j * kTile + r;
+        const int win_left = SINKS && kv_row < prm.sinks ? -1 : prm.win_left;
         for (int t = 0, tt = w.tt0; t < w.n_steps; ++t, ++tt, ++g) {
             if (tt == w.n_qh) tt = 0;
             const int i = w.q_tile(tt);
@@ -1337,7 +1356,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // cmin <= c <= cmax; masked only where some row of the warp needs it
             const int qc0 = i * kTile + h * 64;
             const int cmin = prm.win_right < 0 ? -kTile : kv_row - prm.win_right - qc0;
-            const int cmax = prm.win_left < 0 ? 2 * kTile : kv_row + prm.win_left - qc0;
+            const int cmax = win_left < 0 ? 2 * kTile : kv_row + win_left - qc0;
             const bool masked = __any_sync(0xffffffffu, cmin > 0 || cmax < 63);
             float p[64];  // P^T of this thread's key row and the warpgroup's 64 queries
             // Phase A: P^T = 2^(cs (S^T - LSE log2 e / cs)), the query term already in
@@ -1466,7 +1485,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const int item = item_at(rr);
             if (item == -1) break;
             if (item < 0) continue;
-            const BwdWork w = work(item);
+            const Work w = work(item);
             const bool last_item = item_at(rr + 1) < 0;
             int tt = w.tt0, bh = w.bh_first;
             for (int t = 0; t < w.n_steps; ++t, ++tt, ++g) {
@@ -1671,19 +1690,19 @@ bool bwd_deal_for(const BwdParams& p, int snake_grid, int grid, BwdDealArg<2>* o
     return c.use;
 }
 
-template <int D>
+template <int D, bool SINKS>
 cudaError_t launch_bwd_main_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                  const CUtensorMap& tdo, const CUtensorMap& tdq, const BwdParams& p,
                                  cudaStream_t stream) {
     using T = BwdTraits<D>;
     static const cudaError_t attr = cudaFuncSetAttribute(
-        bwd_main_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+        bwd_main_kernel<D, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
     const long long grid = static_cast<long long>(p.BHk) * p.n_kv;
     const cudaError_t dbg = dbg_set_word(p.st.word, stream);
     if (dbg != cudaSuccess) return dbg;
-    bwd_main_kernel<D><<<static_cast<unsigned>(grid), kBwdThreads, T::SMEM_BYTES, stream>>>(tq, tk, tv, tdo, tdq,
-                                                                                        p);
+    bwd_main_kernel<D, SINKS><<<static_cast<unsigned>(grid), kBwdThreads, T::SMEM_BYTES, stream>>>(tq, tk, tv, tdo,
+                                                                                               tdq, p);
     return cudaGetLastError();
 }
 
@@ -1721,7 +1740,9 @@ cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream) {
 cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& tdo, const CUtensorMap& tdq, const BwdParams& p,
                             cudaStream_t stream) {
-    if (D == 64) return launch_bwd_main_impl<64>(tq, tk, tv, tdo, tdq, p, stream);
+    if (D == 64)
+        return p.sinks > 0 ? launch_bwd_main_impl<64, true>(tq, tk, tv, tdo, tdq, p, stream)
+                           : launch_bwd_main_impl<64, false>(tq, tk, tv, tdo, tdq, p, stream);
     if (D == 128) {
         using T = BwdFullTraits;
         static const cudaError_t attr = [] {
@@ -1731,7 +1752,9 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                                    reinterpret_cast<const void*>(bwd_main_full_kernel<2, false>),
                                    reinterpret_cast<const void*>(bwd_main_full_kernel<0, true>),
                                    reinterpret_cast<const void*>(bwd_main_full_kernel<1, true>),
-                                   reinterpret_cast<const void*>(bwd_main_full_kernel<2, true>)})
+                                   reinterpret_cast<const void*>(bwd_main_full_kernel<2, true>),
+                                   reinterpret_cast<const void*>(bwd_main_full_kernel<3, false>),
+                                   reinterpret_cast<const void*>(bwd_main_full_kernel<3, true>)})
                 if (e == cudaSuccess)
                     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
             return e;
@@ -1767,6 +1790,28 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                 if (items < sms) grid = items * parts;
             }
         }
+        // Sinks: a sink tile's item visits every later query tile (64 steps at N8192 against
+        // 9 of a 1024-key window), so these items are split as well, into parts of a quarter
+        // of the CTAs' mean or less, but of kSplitMinPartSteps at least.
+        if (p.sinks > 0 && p.split_cap > 0) {
+            const long long G = p.H / p.Hk, sink_items = static_cast<long long>(p.BHk) * p.sink_tiles;
+            const long long win_tiles = (static_cast<long long>(p.win_left) + kTile - 1) / kTile + 1;
+            const long long plain = G * (items - sink_items) * (win_tiles < p.n_kv ? win_tiles : p.n_kv);
+            const long long mean = (plain + G * sink_items * p.n_kv) / sms;
+            const long long part = mean / 4 > kSplitMinPartSteps ? mean / 4 : kSplitMinPartSteps;
+            long long parts = (steps + part - 1) / part;
+            if (parts > steps / kSplitMinPartSteps) parts = steps / kSplitMinPartSteps;
+            // the last sink tile has the fewest steps: a part keeps one at least
+            const long long least = G * (p.n_kv - p.sink_tiles + 1);
+            if (parts > least) parts = least;
+            if (parts * sink_items > p.split_cap) parts = p.split_cap / sink_items;
+            if (parts >= 2) {
+                pp.split_base = static_cast<int>(items - sink_items);
+                pp.split_parts = static_cast<int>(parts);
+                const long long all = pp.split_base + sink_items * parts;
+                grid = all < sms ? all : sms;
+            }
+        }
         const cudaError_t dbg = dbg_set_word(p.st.word, stream);
         if (dbg != cudaSuccess) return dbg;
         BwdDealArg<2> deal;
@@ -1789,6 +1834,10 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                       : cudaLaunchKernelEx(&cfg, bwd_main_full_kernel<2, false>, tq, tk, tv, tdo, pp, deal);
         }
         cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        if (p.sinks > 0)
+            return v8 ? cudaLaunchKernelEx(&cfg, bwd_main_full_kernel<3, true>, tq, tk, tv, tdo, pp, BwdDealArg<3>{})
+                      : cudaLaunchKernelEx(&cfg, bwd_main_full_kernel<3, false>, tq, tk, tv, tdo, pp,
+                                           BwdDealArg<3>{});
         if (pp.split_parts > 1)
             return v8 ? cudaLaunchKernelEx(&cfg, bwd_main_full_kernel<1, true>, tq, tk, tv, tdo, pp, BwdDealArg<1>{})
                       : cudaLaunchKernelEx(&cfg, bwd_main_full_kernel<1, false>, tq, tk, tv, tdo, pp,

@@ -84,7 +84,7 @@ enum : uint32_t {
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t f2u(float f) { return __float_as_uint(f); }
 
-template <int D, bool FP8, bool FMAEXP>
+template <int D, bool FP8, bool FMAEXP, bool SINKS>
 __global__ void __launch_bounds__(320, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const FwdParams prm) {
@@ -137,6 +137,13 @@ __global__ void __launch_bounds__(320, 1)
         int lo0, lo1, n0, n1;  // key-tile range [lo_g, lo_g + n_g) of query tile g
         __device__ int lo(int g) const { return g ? lo1 : lo0; }
         __device__ int n(int g) const { return g ? n1 : n0; }
+        // With sinks: the item's first n_sink key tiles are the sequence's first ones, the
+        // others are skip tiles further on.
+        int n_sink, skip;
+        __device__ int tile(int j) const {  // key tile of the item's j-th, from kv_lo or a tile's lo
+            if constexpr (SINKS) return j < n_sink ? j : j + skip;
+            else return j;
+        }
     };
     auto item_info = [&](int item) {
         Item w;
@@ -171,6 +178,18 @@ __global__ void __launch_bounds__(320, 1)
         w.kv_lo = w.n(0) > 0 ? (w.n(1) > 0 ? min(w.lo(0), w.lo(1)) : w.lo(0)) : w.lo(1);
         const int kv_hi = max(w.n(0) > 0 ? w.lo(0) + w.n(0) : 0, w.n(1) > 0 ? w.lo(1) + w.n(1) : 0);
         w.n_kv = (w.n(0) > 0 || w.n(1) > 0) ? kv_hi - w.kv_lo : 0;
+        if constexpr (SINKS) {
+            // The item's key tiles are renumbered from 0: the sink tiles, then its window's
+            // union.  Both query tiles start at 0, so that the aligned schedule runs; the
+            // second one's first window tile is then often wholly masked (one tile in about
+            // 20 at 1024 keys and 128 sinks or fewer).
+            w.n_sink = min((prm.sinks + kTile - 1) / kTile, w.kv_lo);
+            w.skip = w.kv_lo - w.n_sink;
+            if (w.n0 > 0) w.n0 += w.lo0 - w.skip;
+            if (w.n1 > 0) w.n1 += w.lo1 - w.skip;
+            w.lo0 = w.lo1 = w.kv_lo = 0;
+            w.n_kv = max(w.n0, w.n1);
+        }
         // Key/value head of the query head (grouped-query attention: H/Hk query heads
         // share one key/value head; Hk == H is ordinary multi-head attention).
         w.b_idx = w.bh / prm.H;
@@ -250,10 +269,10 @@ __global__ void __launch_bounds__(320, 1)
                     const CUtensorMap* map = v_tile ? &tm_v : &tm_k;
                     for (int blk = 0; blk < T::NBLK; ++blk) {
                         const uint32_t dst = smem_u32(sKV + slot * T::TILE_BYTES + blk * T::BLK_BYTES);
-                        if (dbg_tma(dst, blk * T::BLK_ELEMS, (it.kv_lo + j) * kTile, it.hk_idx, it.b_idx, D, N,
-                                    prm.Hk, prm.BH / prm.H, T::EB, 0x1D1))
-                            tma_load_4d(dst, map, bar, blk * T::BLK_ELEMS, (it.kv_lo + j) * kTile, it.hk_idx,
-                                        it.b_idx);
+                        if (dbg_tma(dst, blk * T::BLK_ELEMS, it.tile(it.kv_lo + j) * kTile, it.hk_idx, it.b_idx, D,
+                                    N, prm.Hk, prm.BH / prm.H, T::EB, 0x1D1))
+                            tma_load_4d(dst, map, bar, blk * T::BLK_ELEMS, it.tile(it.kv_lo + j) * kTile,
+                                        it.hk_idx, it.b_idx);
                     }
                 };
                 auto load_single = [&](int j, bool v_tile) -> bool {
@@ -566,10 +585,21 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
 
-            const int kv0 = (jt0 + j) * kTile;
+            const int kv0 = it.tile(jt0 + j) * kTile;
             const int c_lo = key_min - kv0, c_hi = key_max - kv0;  // visible columns [c_lo, c_hi]
+            const int c_sink = SINKS ? prm.sinks - kv0 : 0;        // and, with sinks, those below c_sink up to c_hi
             auto apply_mask = [&]() {
-                if (c_lo > 0 || c_hi < kTile - 1) {
+                if constexpr (SINKS) {
+                    if ((c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int k = c * 32 + i;
+                                if ((k < c_lo && k >= c_sink) || k > c_hi) s[c][i] = f2u(-INFINITY);
+                            }
+                    }
+                } else if (c_lo > 0 || c_hi < kTile - 1) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -813,12 +843,12 @@ __global__ void __launch_bounds__(256) splitkv_combine_kernel(const CombineParam
     }
 }
 
-template <int D, bool FP8, bool FMAEXP = false>
+template <int D, bool FP8, bool FMAEXP = false, bool SINKS = false>
 cudaError_t launch_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const FwdParams& p, cudaStream_t stream) {
     using T = FwdTraits<D, FP8>;
     static const cudaError_t attr = cudaFuncSetAttribute(
-        fwd_kernel<D, FP8, FMAEXP>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+        fwd_kernel<D, FP8, FMAEXP, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
     // Persistent CTAs, one per SM (shared memory admits one), each looping over
     // items in the snake order of item_at: equal items (no mask) and longest-first
@@ -842,7 +872,7 @@ cudaError_t launch_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk, const 
     if (grid < 1) return cudaSuccess;
     const cudaError_t dbg = dbg_set_word(p.st.word, stream);
     if (dbg != cudaSuccess) return dbg;
-    fwd_kernel<D, FP8, FMAEXP><<<static_cast<unsigned>(grid), 320, T::SMEM_BYTES, stream>>>(tq, tk, tv, pp);
+    fwd_kernel<D, FP8, FMAEXP, SINKS><<<static_cast<unsigned>(grid), 320, T::SMEM_BYTES, stream>>>(tq, tk, tv, pp);
     return cudaGetLastError();
 }
 
@@ -850,6 +880,11 @@ cudaError_t launch_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk, const 
 
 cudaError_t launch_fwd_bf16(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const FwdParams& p, cudaStream_t stream) {
+    if (p.sinks > 0) {
+        if (D == 64) return launch_fwd_impl<64, false, false, true>(tq, tk, tv, p, stream);
+        if (D == 128) return launch_fwd_impl<128, false, false, true>(tq, tk, tv, p, stream);
+        return cudaErrorInvalidValue;
+    }
     if (D == 64) return launch_fwd_impl<64, false>(tq, tk, tv, p, stream);
     if (D == 128) return launch_fwd_impl<128, false>(tq, tk, tv, p, stream);
     return cudaErrorInvalidValue;

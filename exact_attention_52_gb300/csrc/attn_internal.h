@@ -27,6 +27,7 @@ struct FwdParams {
     int causal;       // 1: causal mask (also selects longest-first launch order)
     int win_left;     // key j visible to query i iff i - win_left <= j <= i + win_right;
     int win_right;    // a negative bound is no bound (causal: -1, 0; full: -1, -1)
+    int sinks;        // > 0 (bf16, with win_left >= 0): so are keys j < sinks with j <= i + win_right
     float cs;         // scale * log2(e) (fp8: scale * s_q * s_k * log2(e))
     float out_scale;  // 1 (bf16) or s_v (fp8)
     // Split-KV mode (n_splits > 1): CTA s of a query-tile pair covers key tiles
@@ -74,6 +75,10 @@ struct BwdPreParams {
 // its own and writes the item's dV and dK.  At most kBwdSplitCap parts.
 constexpr int kBwdSplitCap = 160;
 constexpr int kBwdSplitCntWords = kBwdSplitCap * 8;  // [item slot][dV, dK][4 warp slices]
+// With sinks the items of the sink tiles are split the same way, into at most
+// kBwdSinkParts parts each and kBwdSinkCap in all.
+constexpr int kBwdSinkParts = 16;
+constexpr int kBwdSinkCap = 512;
 
 struct BwdParams {
     const float* lse2;  // workspace (-LSE * log2(e)), see BwdPreParams
@@ -89,6 +94,8 @@ struct BwdParams {
     int causal;         // causal mask (also selects longest-first launch order)
     int win_left;       // window bounds as in FwdParams (negative: none)
     int win_right;
+    int sinks;          // > 0 (with win_left >= 0): keys below it are seen past the window too
+    int sink_tiles;     // ceil(sinks / 128); their items come last in the launch's numbering
     float cs;           // scale * log2(e)
     float scale;        // softmax scale (applied to dK here and to dQ at conversion)
     // Split last round (d = 128): virtual items v >= split_base are part v - split_base
@@ -98,7 +105,7 @@ struct BwdParams {
     int split_parts;
     int split_cap;        // parts the workspace has room for (0: no split possible)
     float* split_part;    // fp32 [part][dV, dK][128 rows][D]
-    unsigned* split_cnt;  // kBwdSplitCntWords counters, zero at launch
+    unsigned* split_cnt;  // kBwdSplitCntWords counters (sinks: 8 per part), zero at launch
     int dkv_v8;           // every dK and dV row starts on a 32-byte boundary: 32-byte stores
     DevStatus st;
 };

@@ -258,6 +258,29 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
                              float scale, int window_left, int window_right, attn_stream_t stream);
 
 /*
+ * Sliding window with first tokens that stay visible ("sinks"): key j is visible
+ * to query i iff j <= i + window_right (-1: no bound) and (window_left == -1, or
+ * j >= i - window_left, or j < sinks).  Arguments otherwise as the strided entry
+ * points; sinks >= 0, and sinks = 0 is the plain window.  Key tiles that neither
+ * the window nor the sinks reach are skipped in both passes; the backward's
+ * workspace is attn_bwd_sinks_workspace_bytes() bytes, and its dK and dV are
+ * deterministic as attn_bwd's are.
+ * Source: FlashAttention-3 tuning page (window bounds); no page describes sinks.
+ */
+attn_status attn_fwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks,
+                           const void* v, attn_strides_t vs, void* o, attn_strides_t os, float* lse,
+                           int B, int H, int Hk, int N, int d, float scale, int window_left,
+                           int window_right, int sinks, attn_stream_t stream);
+size_t attn_bwd_sinks_workspace_bytes(int B, int H, int Hk, int N, int d, int sinks);
+attn_status attn_bwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks,
+                           const void* v, attn_strides_t vs, const void* o, attn_strides_t os,
+                           const void* dout, attn_strides_t dos, const float* lse, void* dq,
+                           attn_strides_t dqs, void* dk, attn_strides_t dks, void* dv,
+                           attn_strides_t dvs, void* workspace, int B, int H, int Hk, int N, int d,
+                           float scale, int window_left, int window_right, int sinks,
+                           attn_stream_t stream);
+
+/*
  * FP8 forward pass: OCP E4M3 inputs with per-tensor fp32 scales.
  *   q8, k8, v8 : uint8 E4M3 codes [B, H, N, d]; the value read is s * code
  *                (sq, sk, sv finite and > 0).
