@@ -10,8 +10,11 @@ library is missing, every call raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
+import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libattn_sm103a.so")
@@ -26,14 +29,6 @@ STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED"
 class Strides(ctypes.Structure):
     """attn_strides_t: element strides (b, h, n) of a [B, heads, N, d] view."""
     _fields_ = [("b", ctypes.c_int64), ("h", ctypes.c_int64), ("n", ctypes.c_int64)]
-
-
-class Cache(ctypes.Structure):
-    """attn_cache_t: the paged 8-bit key/value cache of a call."""
-    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("ks", Strides), ("vs", Strides),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64), ("seq_lens", ctypes.c_void_p), ("num_pages", ctypes.c_int),
-                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
 # Every symbol the header declares, with (restype, argtypes).
@@ -66,9 +61,9 @@ SIGNATURES = {
     "attn_bwd_sinks": (_i, [_vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _st, _vp, _st,
                             _vp, _st, _vp, _i, _i, _i, _i, _i, _f, _i, _i, _i, _vp]),
     "attn_fwd_fp8": (_i, [_vp, _vp, _vp, _f, _f, _f, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp]),
-    "attn_cache_append": (_i, [ctypes.POINTER(Cache), _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _vp]),
+    "attn_cache_append": (_i, [_vp, _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _vp]),
     "attn_fwd_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
-    "attn_fwd_cache": (_i, [ctypes.POINTER(Cache), _vp, _st, _vp, _st, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
+    "attn_fwd_cache": (_i, [_vp, _vp, _st, _vp, _st, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
                             _i, _i, _vp]),
     "attn_check_device_error": (_i, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
@@ -405,17 +400,132 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
 
 
 # ---------------------------------------------------------------------------
-# Sliding window with sinks
+# Sliding window with sinks; paged 8-bit key/value cache
 # ---------------------------------------------------------------------------
-def _sinks_shape(device, q, k, v, layout):
+# A decode step runs these for single tokens, where the host's share of a call
+# counts: each function first makes one pass of cheap comparisons, and only when
+# one fails do the functions named _explain_* look for the argument to name.
+def _call_stream(device_index, stream):
+    """Handle of the stream a call runs on (the current one without an argument)."""
     import torch
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def _on_stream(stream):
+    """Context in which what a call allocates belongs to the stream that the call runs on."""
+    import contextlib
+
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+_kept = threading.local()
+
+
+def _call_workspace(dev, stream, handle, need):
+    """Workspace of a call that was given none.  Calls of one thread on one stream run one after
+    the other, so they share one that is kept (an allocation took 7 us of a 22 us call).  A call
+    that is being captured, whose workspace the graph goes on using, and a call on a stream given
+    as an argument get one of their own."""
+    import torch
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        with _on_stream(stream):
+            return torch.empty(need, dtype=torch.uint8, device=dev)
+    kept = _kept.__dict__
+    ws = kept.get((dev, handle))
+    if ws is None or ws.nbytes < need:
+        ws = kept[(dev, handle)] = torch.empty(need, dtype=torch.uint8, device=dev)
+    return ws
+
+
+def _explain_on(device, name, t, dtype, ndim):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dtype != dtype or t.dim() != ndim:
+        raise ValueError(f"{name} must be {dtype} with {ndim} dimensions, got {t.dtype} {tuple(t.shape)}")
+
+
+def _explain_device(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _explain_like(device, name, t, like):
+    import torch
+    _explain_on(device, name, t, torch.bfloat16, 4)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    if t.stride(3) != 1:
+        raise ValueError(f"the last (d) dimension of {name} must be contiguous")
+
+
+def _explain_lse(device, t, shape):
+    import torch
+    _explain_on(device, "lse", t, torch.float32, 3)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"lse must be a contiguous {shape}")
+
+
+def _explain_workspace(device, t, need):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.device != device or t.numel() * t.element_size() < need:
+        raise ValueError(f"workspace needs {need} bytes on {device}")
+
+
+def _strides4(t, layout):
+    """(b, h, n) strides of a 4-D tensor in ``layout``, or None if d is not contiguous."""
+    sb, s1, s2, sd = t.stride()
+    if sd != 1:
+        return None
+    return Strides(sb, s1, s2) if layout == "bhnd" else Strides(sb, s2, s1)
+
+
+def _layout_shape(t, layout):
+    if layout not in ("bhnd", "bnhd"):
+        raise ValueError(f"unknown layout {layout!r}")
+    try:
+        return _bhnd_shape(t, layout)
+    except (AttributeError, ValueError):
+        raise ValueError(f"a 4-dimensional tensor is expected, got {getattr(t, 'shape', type(t))}") from None
+
+
+def _explain_qkv(q, k, v, layout):
+    import torch
+    device = _explain_device(q, "q")
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _check_on(device, name, t, torch.bfloat16, 4)
-    B, H, N, d = _bhnd_shape(q, layout)
-    Hk = _bhnd_shape(k, layout)[1]
-    if _bhnd_shape(k, layout) != (B, Hk, N, d) or k.shape != v.shape:
+        _explain_on(device, name, t, torch.bfloat16, 4)
+        if t.stride(3) != 1:
+            raise ValueError(f"the last (d) dimension of {name} must be contiguous")
+    B, _, N, d = _bhnd_shape(q, layout)
+    Bk, _, Nk, dk = _bhnd_shape(k, layout)
+    if (Bk, Nk, dk) != (B, N, d) or k.shape != v.shape:
         raise ValueError(f"k and v must have q's batch, length and d, got {tuple(k.shape)} and {tuple(v.shape)}")
-    return B, H, Hk, N, d
+    raise ValueError("q, k and v must be bf16 CUDA tensors of one device")
+
+
+def _sinks_args(q, k, v, layout):
+    """Sizes and strides of a whole-sequence call's inputs, checked."""
+    import torch
+    B, H, N, d = _layout_shape(q, layout)
+    Bk, Hk, Nk, dk = _layout_shape(k, layout)
+    try:
+        dev, bf16 = q.get_device(), torch.bfloat16
+        strides = _strides4(q, layout), _strides4(k, layout), _strides4(v, layout)
+        ok = (None not in strides and (Bk, Nk, dk) == (B, N, d) and k.shape == v.shape
+              and q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16
+              and dev == k.get_device() == v.get_device() == torch.cuda.current_device())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain_qkv(q, k, v, layout)
+    return B, H, Hk, N, d, dev, strides
 
 
 def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layout: str = "bhnd",
@@ -425,20 +535,18 @@ def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layo
     j < sinks).  bf16 q [B, H, N, d], k and v [B, Hk, N, d] (``layout`` "bhnd") or [B, N, heads, d]
     ("bnhd"), any strides with a contiguous last dimension.  Returns (O like q, LSE [B, H, N])."""
     import torch
-    device = _call_device(q, "q")
-    B, H, Hk, N, d = _sinks_shape(device, q, k, v, layout)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    B, H, Hk, N, d, dev, (qs, ks, vs) = _sinks_args(q, k, v, layout)
     with _on_stream(stream):
-        o = torch.empty_like(q) if o is None else o
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=device) if lse is None else lse
-    _check_on(device, "o", o, torch.bfloat16, 4)
-    _check_on(device, "lse", lse, torch.float32, 3)
-    if o.shape != q.shape or lse.shape != (B, H, N) or not lse.is_contiguous():
-        raise ValueError(f"o must have q's shape and lse be a contiguous {(B, H, N)}")
-    st = lambda t: _bhnd_strides(t, layout)
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    _explain_like(q.device, "o", o, q)
+    _explain_lse(q.device, lse, (B, H, N))
     _check("attn_fwd_sinks", load_library().attn_fwd_sinks(
-        q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o), lse.data_ptr(),
-        B, H, Hk, N, d, scale, int(window_left), int(window_right), int(sinks), _stream_handle(stream)))
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), _strides4(o, layout), lse.data_ptr(),
+        B, H, Hk, N, d, 1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left),
+        int(window_right), int(sinks), _call_stream(dev, stream)))
     return o, lse
 
 
@@ -453,94 +561,94 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
     summed over the query heads that share them.  ``workspace``: ``bwd_sinks_workspace_bytes``
     bytes, one for each call that may overlap."""
     import torch
-    device = _call_device(q, "q")
-    B, H, Hk, N, d = _sinks_shape(device, q, k, v, layout)
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    B, H, Hk, N, d, dev, (qs, ks, vs) = _sinks_args(q, k, v, layout)
+    device = q.device
     need = bwd_sinks_workspace_bytes(B, H, Hk, N, d, int(sinks))
     if need == 0:
         raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, N {N}, d {d}, sinks {sinks}")
     with _on_stream(stream):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
+        if dq is None:
+            dq = torch.empty_like(q)
+        if dk is None:
+            dk = torch.empty_like(k)
+        if dv is None:
+            dv = torch.empty_like(v)
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
     for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _check_on(device, name, t, torch.bfloat16, 4)
-        if t.shape != like.shape:
-            raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
-    _check_on(device, "lse", lse, torch.float32, 3)
-    if lse.shape != (B, H, N) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous {(B, H, N)}")
-    if workspace.device != device or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace needs {need} bytes on {device}")
-    st = lambda t: _bhnd_strides(t, layout)
+        _explain_like(device, name, t, like)
+    _explain_lse(device, lse, (B, H, N))
+    _explain_workspace(device, workspace, need)
+    st = _strides4
     _check("attn_bwd_sinks", load_library().attn_bwd_sinks(
-        q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o), dout.data_ptr(),
-        st(dout), lse.data_ptr(), dq.data_ptr(), st(dq), dk.data_ptr(), st(dk), dv.data_ptr(), st(dv),
-        workspace.data_ptr(), B, H, Hk, N, d, scale, int(window_left), int(window_right), int(sinks),
-        _stream_handle(stream)))
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), st(o, layout), dout.data_ptr(),
+        st(dout, layout), lse.data_ptr(), dq.data_ptr(), st(dq, layout), dk.data_ptr(), st(dk, layout),
+        dv.data_ptr(), st(dv, layout), workspace.data_ptr(), B, H, Hk, N, d,
+        1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(window_right), int(sinks),
+        _call_stream(dev, stream)))
     return dq, dk, dv
 
 
-# ---------------------------------------------------------------------------
-# Paged 8-bit key/value cache
-# ---------------------------------------------------------------------------
-def _check_on(device, name, t, dtype, ndim):
+# attn_cache_t, packed (native alignment): pages, strides, scales, table, its stride, lengths, sizes
+_CACHE = struct.Struct("@PPqqqqqqPPPqPiii")
+
+
+def _explain_lens(device, name, t, B):
     import torch
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype or t.dim() != ndim:
-        raise ValueError(f"{name} must be {dtype} with {ndim} dimensions, got {t.dtype} {tuple(t.shape)}")
+    _explain_on(device, name, t, torch.int32, 1)
+    if t.shape[0] != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{B}]")
 
 
-def _call_device(t, name):
-    """The device a call runs on: that of its tensors, which has to be the current one."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
-
-
-def _on_stream(stream):
-    """Context in which what a call allocates belongs to the stream that the call runs on."""
-    import contextlib
-
-    import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _cache_arg(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens):
+def _explain_cache(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens, new_name):
     import torch
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _check_on(device, name, t, torch.uint8, 4)
+        _explain_on(device, name, t, torch.uint8, 4)
+        if t.stride(3) != 1:
+            raise ValueError(f"the last (d) dimension of {name} must be contiguous")
     P, heads, page, dim = k_pages.shape
     if v_pages.shape != k_pages.shape or heads != Hk or dim != d:
         raise ValueError(f"k_pages and v_pages must be [pages, {Hk}, page_size, {d}], got "
                          f"{tuple(k_pages.shape)} and {tuple(v_pages.shape)}")
     for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        _check_on(device, name, t, torch.float32, 2)
+        _explain_on(device, name, t, torch.float32, 2)
         if t.shape != (P, Hk) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous [{P}, {Hk}]")
-    _check_on(device, "page_table", page_table, torch.int32, 2)
+    _explain_on(device, "page_table", page_table, torch.int32, 2)
     if page_table.shape[0] != B or page_table.shape[1] < 1 or page_table.stride(1) != 1:
         raise ValueError(f"page_table must be [{B}, pages] with contiguous rows")
-    _check_lens(device, "seq_lens", seq_lens, B)
-    ks, vs = k_pages.stride(), v_pages.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("the last (d) dimension of the pages must be contiguous")
-    return Cache(k_pages.data_ptr(), v_pages.data_ptr(), Strides(*ks[:3]), Strides(*vs[:3]), k_scale.data_ptr(),
-                 v_scale.data_ptr(), page_table.data_ptr(), page_table.stride(0), seq_lens.data_ptr(), P, page,
-                 page_table.shape[1])
+    _explain_lens(device, "seq_lens", seq_lens, B)
+    if new_lens is not None:
+        _explain_lens(device, new_name, new_lens, B)
+    raise ValueError(f"the cache's tensors must all be on {device}, the current device")
 
 
-def _check_lens(device, name, t, B):
+def _cache_arg(dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens, new_name):
+    """attn_cache_t of a call, its tensors checked."""
     import torch
-    _check_on(device, name, t, torch.int32, 1)
-    if t.shape[0] != B or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [{B}]")
+    try:
+        P, heads, page, dim = shape = k_pages.shape
+        i32, u8, f32 = torch.int32, torch.uint8, torch.float32
+        ka, kb, kc, kd = k_pages.stride()
+        va, vb, vc, vd = v_pages.stride()
+        tb, t1 = page_table.stride()
+        rows, cols = page_table.shape
+        ok = (heads == Hk and dim == d and v_pages.shape == shape and kd == 1 and vd == 1
+              and k_pages.dtype is u8 and v_pages.dtype is u8 and k_scale.dtype is f32 and v_scale.dtype is f32
+              and page_table.dtype is i32 and seq_lens.dtype is i32
+              and dev == k_pages.get_device() == v_pages.get_device() == k_scale.get_device()
+              == v_scale.get_device() == page_table.get_device() == seq_lens.get_device()
+              and k_scale.shape == (P, Hk) and v_scale.shape == (P, Hk) and k_scale.is_contiguous()
+              and v_scale.is_contiguous() and rows == B and cols >= 1 and t1 == 1
+              and seq_lens.shape == (B,) and seq_lens.is_contiguous()
+              and (new_lens is None or (new_lens.dtype is i32 and new_lens.get_device() == dev
+                                        and new_lens.shape == (B,) and new_lens.is_contiguous())))
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain_cache(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens, new_name)
+    return _CACHE.pack(k_pages.data_ptr(), v_pages.data_ptr(), ka, kb, kc, va, vb, vc, k_scale.data_ptr(),
+                       v_scale.data_ptr(), page_table.data_ptr(), tb, seq_lens.data_ptr(), P, page, cols)
 
 
 def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens=None,
@@ -555,21 +663,27 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
     position seq_lens - new_lens + t.  A page's scale is a power of two that covers its largest
     value and grows with it, the codes that are there being rounded again."""
     import torch
-    device = _call_device(k, "k")
-    _check_on(device, "k", k, torch.bfloat16, 4)
-    _check_on(device, "v", v, torch.bfloat16, 4)
-    if k.shape != v.shape:
-        raise ValueError(f"k and v must have the same shape, got {tuple(k.shape)} and {tuple(v.shape)}")
-    ks, vs = _bhnd_strides(k, layout), _bhnd_strides(v, layout)
-    B, Hk, T, d = _bhnd_shape(k, layout)
-    cache = _cache_arg(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens)
-    if new_lens is not None:
-        _check_lens(device, "new_lens", new_lens, B)
+    B, Hk, T, d = _layout_shape(k, layout)
+    try:
+        dev, bf16 = k.get_device(), torch.bfloat16
+        ks, vs = _strides4(k, layout), _strides4(v, layout)
+        ok = (ks is not None and vs is not None and k.shape == v.shape and k.dtype is bf16 and v.dtype is bf16
+              and dev == v.get_device() == torch.cuda.current_device())
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain_device(k, "k")
+        _explain_like(k.device, "k", k, k)
+        _explain_like(k.device, "v", v, k)
+        raise ValueError("k and v must be bf16 CUDA tensors of one device")
+    cache = _cache_arg(dev, k.device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+                       new_lens, "new_lens")
     _check("attn_cache_append", load_library().attn_cache_append(
-        ctypes.byref(cache), k.data_ptr(), ks, v.data_ptr(), vs,
-        None if new_lens is None else new_lens.data_ptr(), B, Hk, T, d, _stream_handle(stream)))
+        cache, k.data_ptr(), ks, v.data_ptr(), vs, None if new_lens is None else new_lens.data_ptr(),
+        B, Hk, T, d, _call_stream(dev, stream)))
 
 
+@functools.lru_cache(maxsize=256)
 def fwd_cache_workspace_bytes(B: int, H: int, Hk: int, T: int, d: int) -> int:
     return int(load_library().attn_fwd_cache_workspace_bytes(B, H, Hk, T, d))
 
@@ -584,38 +698,49 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
     heads.  Query t of q_lens[b] (default T) sits at position p = seq_lens[b] - q_lens[b] + t and
     sees key j iff j <= p and (window_left is -1, or j >= p - window_left, or j < sinks).  Rows
     behind q_lens[b] are left as they were; a row that sees nothing gives 0 and LSE +inf.
-    ``workspace``: ``fwd_cache_workspace_bytes`` bytes, one for each call that may overlap."""
+    ``workspace``: ``fwd_cache_workspace_bytes`` bytes, one for each call that may overlap; without
+    one, the calls of a thread on its current stream share a kept one."""
     import torch
-    device = _call_device(q, "q")
-    _check_on(device, "q", q, torch.bfloat16, 4)
-    qs = _bhnd_strides(q, layout)
-    B, H, T, d = _bhnd_shape(q, layout)
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+    B, H, T, d = _layout_shape(q, layout)
+    try:
+        dev, qs, Hk = q.get_device(), _strides4(q, layout), k_pages.shape[1]
+        ok = qs is not None and q.dtype is torch.bfloat16 and dev == torch.cuda.current_device()
+    except (AttributeError, IndexError):
+        ok = False
+    if not ok:
+        _explain_device(q, "q")
+        _explain_like(q.device, "q", q, q)
         raise ValueError("k_pages must be a tensor [pages, Hk, page_size, d]")
-    Hk = k_pages.shape[1]
-    cache = _cache_arg(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens)
-    if q_lens is not None:
-        _check_lens(device, "q_lens", q_lens, B)
-    lib = load_library()
-    need = int(lib.attn_fwd_cache_workspace_bytes(B, H, Hk, T, d))
+    device = q.device
+    cache = _cache_arg(dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+                       q_lens, "q_lens")
+    need = fwd_cache_workspace_bytes(B, H, Hk, T, d)
     if need == 0:
         raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, T {T}, d {d}")
-    with _on_stream(stream):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    _check_on(device, "o", o, torch.bfloat16, 4)
-    _check_on(device, "lse", lse, torch.float32, 3)
-    if o.shape != q.shape or lse.shape != (B, H, T) or not lse.is_contiguous():
-        raise ValueError(f"o must have q's shape and lse be a contiguous {(B, H, T)}")
-    if workspace.device != device or workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace needs {need} bytes on {device}")
-    _check("attn_fwd_cache", lib.attn_fwd_cache(
-        ctypes.byref(cache), q.data_ptr(), qs, o.data_ptr(), _bhnd_strides(o, layout), lse.data_ptr(),
-        workspace.data_ptr(), None if q_lens is None else q_lens.data_ptr(), B, H, Hk, T, d,
-        1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(sinks),
-        _stream_handle(stream)))
+    handle = _call_stream(dev, stream)
+    if o is None or lse is None:
+        with _on_stream(stream):
+            if o is None:
+                o = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = _call_workspace(dev, stream, handle, need)
+    try:
+        os_ = _strides4(o, layout)
+        ok = (os_ is not None and o.dtype is torch.bfloat16 and o.shape == q.shape and lse.shape == (B, H, T)
+              and lse.dtype is torch.float32 and lse.is_contiguous()
+              and dev == o.get_device() == lse.get_device() == workspace.get_device()
+              and workspace.nbytes >= need)
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _explain_like(device, "o", o, q)
+        _explain_lse(device, lse, (B, H, T))
+        _explain_workspace(device, workspace, need)
+        raise ValueError("o, lse and workspace must be tensors of the current device")
+    _check("attn_fwd_cache", load_library().attn_fwd_cache(
+        cache, q.data_ptr(), qs, o.data_ptr(), os_, lse.data_ptr(), workspace.data_ptr(),
+        None if q_lens is None else q_lens.data_ptr(), B, H, Hk, T, d,
+        1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(sinks), handle))
     return o, lse

@@ -156,6 +156,11 @@ bool strides_ok(const Strides& s, int elem_bytes) {
     return true;
 }
 
+// No two elements of an output share a place: no zero stride over more than one.
+bool distinct(const Strides& s, long long nb, long long nh, long long nn) {
+    return (nb == 1 || s.b != 0) && (nh == 1 || s.h != 0) && (nn == 1 || s.n != 0);
+}
+
 constexpr long long kMaxElems = (1ll << 40);  // keeps every byte offset well inside 64 bits
 
 attn_status check_sizes(int B, int H, int N, int d, float scale, int causal) {
@@ -777,7 +782,8 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
 attn_status attn_fwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks, const void* v,
                            attn_strides_t vs, void* o, attn_strides_t os, float* lse, int B, int H, int Hk, int N,
                            int d, float scale, int window_left, int window_right, int sinks, attn_stream_t stream) {
-    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK) return ATTN_ERR_INVALID;
+    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK || !distinct(from_abi(os), B, H, N))
+        return ATTN_ERR_INVALID;
     return fwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), lse, B, H, Hk, N, d, scale,
                    window_left, window_right, stream, SplitArgs(), sinks);
 }
@@ -795,7 +801,9 @@ attn_status attn_bwd_sinks(const void* q, attn_strides_t qs, const void* k, attn
                            const float* lse, void* dq, attn_strides_t dqs, void* dk, attn_strides_t dks, void* dv,
                            attn_strides_t dvs, void* workspace, int B, int H, int Hk, int N, int d, float scale,
                            int window_left, int window_right, int sinks, attn_stream_t stream) {
-    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK) return ATTN_ERR_INVALID;
+    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK || !distinct(from_abi(dqs), B, H, N) ||
+        !distinct(from_abi(dks), B, Hk, N) || !distinct(from_abi(dvs), B, Hk, N))
+        return ATTN_ERR_INVALID;
     return bwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), dout, from_abi(dos), lse, dq,
                    from_abi(dqs), dk, from_abi(dks), dv, from_abi(dvs), workspace, B, H, Hk, N, d, scale, window_left,
                    window_right, stream, true, sinks);
@@ -815,6 +823,8 @@ attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_str
     p.ks = from_abi(ks);
     p.vs = from_abi(vs);
     if (!strides_ok(p.ks, 2) || !strides_ok(p.vs, 2)) return ATTN_ERR_INVALID;
+    if (!distinct(p.c.ks, p.c.num_pages, Hk, p.c.page_size) || !distinct(p.c.vs, p.c.num_pages, Hk, p.c.page_size))
+        return ATTN_ERR_INVALID;
     p.new_lens = new_lens;
     p.B = B;
     p.Hk = Hk;
@@ -846,7 +856,7 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     p.o = o;
     p.qs = from_abi(qs);
     p.os = from_abi(os);
-    if (!strides_ok(p.qs, 2) || !strides_ok(p.os, 2)) return ATTN_ERR_INVALID;
+    if (!strides_ok(p.qs, 2) || !strides_ok(p.os, 2) || !distinct(p.os, B, H, T)) return ATTN_ERR_INVALID;
     p.lse = lse;
     p.q_lens = q_lens;
     p.B = B;

@@ -148,7 +148,7 @@ struct CacheBorder {
     int c_first, c_last; // first (-1: the border splits nothing) and last border inside that item
 };
 
-constexpr int kCacheGridMax = 1024;
+constexpr int kCacheGridMax = 640;  // 160 SMs of four
 constexpr int kCacheRowsMax = 16;
 
 struct CacheFwdParams {

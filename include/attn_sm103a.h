@@ -312,7 +312,8 @@ attn_status attn_fwd_fp8(const void* q8, const void* k8, const void* v8, float s
  * after they change.  An entry outside [0, num_pages), or a length that leaves
  * the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE; no
  * access leaves the pool, attn_cache_append leaves such a page unwritten, and
- * the rows of attn_fwd_cache that needed it are undefined.
+ * the rows of attn_fwd_cache that needed it are undefined.  Tensors that a call
+ * writes have no zero stride over more than one element (ATTN_ERR_INVALID).
  */
 typedef struct {
     void *k_pages, *v_pages;

@@ -292,11 +292,13 @@ def test_refusals():
         with pytest.raises(ValueError):
             api.fwd_cache(**{**ok, **change})
     # three query heads over two, a page of 12 or 8 tokens, bounds below -1, scales that are not positive
-    for change in (dict(q=q[:, :3]), dict(k_pages=kp[:, :, :12], v_pages=vp[:, :, :12]), dict(window_left=-2),
+    for change in (dict(q=q[:, :3]), dict(o=torch.empty_like(q)[:, :1].expand(-1, 4, -1, -1)), dict(k_pages=kp[:, :, :12], v_pages=vp[:, :, :12]), dict(window_left=-2),
                    dict(sinks=-1), dict(scale=0.0), dict(scale=float("nan")),
                    dict(k_pages=kp[:, :, :8], v_pages=vp[:, :, :8])):
         with pytest.raises((ValueError, api.AttnError)):
             api.fwd_cache(**{**ok, **change})
+    with pytest.raises(api.AttnError):  # heads that share their pages' memory
+        api.cache_append(k, k, kp[:, :1].expand(-1, 2, -1, -1), vp[:, :1].expand(-1, 2, -1, -1), ks, vs, table, lens)
     for args in ((k.float(), k), (k, k[:1]), (k[..., ::2], k[..., ::2]), (k.cpu(), k.cpu()), (q, q)):
         with pytest.raises((ValueError, api.AttnError)):
             api.cache_append(*args, kp, vp, ks, vs, table, lens)
@@ -351,6 +353,60 @@ def test_two_calls_at_once_with_a_workspace_each():
         torch.cuda.synchronize()
         for (o, lse), (o2, lse2) in zip(alone, got):
             assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    check_clean()
+
+
+def test_calls_of_two_threads_on_one_stream():
+    """Each thread's calls without a workspace keep one of their own."""
+    import threading
+
+    import torch
+    pool = Pool(61, 4, 2, 128, 64, 40)
+    dev = pool.dev()
+    lens = i32([2500, 2000, 1500, 2222])
+    qs = [bf16(pool.rng, (4, 16, 1, 128))[0] for _ in range(2)]
+    want = [api.fwd_cache(q, *dev, lens)[0] for q in qs]
+    got, start = [[], []], threading.Barrier(2)
+
+    def work(i):
+        start.wait()
+        for _ in range(40):
+            got[i].append(api.fwd_cache(qs[i], *dev, lens)[0])
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o.view(torch.int16), want[i].view(torch.int16)) for o in got[i])
+    check_clean()
+
+
+def test_a_graph_keeps_no_workspace_of_eager_calls():
+    """Two graphs captured without a workspace, replayed at once on two streams."""
+    import torch
+    pool = Pool(62, 4, 2, 128, 64, 40)
+    dev = pool.dev()
+    lens = i32([2500, 2000, 1500, 2222])
+    qs = [bf16(pool.rng, (4, 16, 1, 128))[0] for _ in range(2)]
+    want = [api.fwd_cache(q, *dev, lens) for q in qs]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for q, s in zip(qs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            outs.append(api.fwd_cache(q, *dev, lens))
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        api.fwd_cache(qs[0], *dev, lens)
+    torch.cuda.synchronize()
+    for (o, lse), (o2, lse2) in zip(want, outs):
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
     check_clean()
 
 
