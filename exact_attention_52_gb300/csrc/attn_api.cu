@@ -540,8 +540,19 @@ attn_status cache_view(const attn_cache_t* c, int B, CacheView* out) {
 }
 
 // The workspace is laid out for the largest launch, so that its size needs no device.
-size_t cache_part_bytes(int d) { return static_cast<size_t>(2) * kCacheGridMax * kCacheRowsMax * d * sizeof(float); }
-constexpr size_t kCacheStatBytes = static_cast<size_t>(2) * kCacheGridMax * kCacheRowsMax * sizeof(float2);
+struct CacheLayout {
+    size_t stat, border, total;
+};
+CacheLayout cache_layout(bool prompt, int d) {
+    const size_t rows = prompt ? static_cast<size_t>(2) * kPromptGridMax * kPromptRows
+                               : static_cast<size_t>(2) * kCacheGridMax * kCacheRowsMax;
+    CacheLayout L;
+    L.stat = round256(rows * d * sizeof(float));
+    L.border = L.stat + round256(rows * sizeof(float2));
+    L.total = L.border + round256((prompt ? kPromptGridMax : kCacheGridMax) * sizeof(CacheBorder));
+    return L;
+}
+bool cache_prompt(int H, int Hk, int T) { return static_cast<long long>(T) * (H / Hk) > kPromptMinRows; }
 
 
 }  // namespace
@@ -838,7 +849,7 @@ attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_str
 
 size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d) {
     if (check_sizes(B, H, T, d, 1.f, 0) != ATTN_OK || check_group(H, Hk) != ATTN_OK) return 0;
-    return cache_part_bytes(d) + kCacheStatBytes + kCacheGridMax * sizeof(CacheBorder);
+    return cache_layout(cache_prompt(H, Hk, T), d).total;
 }
 
 attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o, attn_strides_t os,
@@ -868,13 +879,16 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     p.left = window_left;
     p.sinks = sinks;
     p.part = static_cast<float*>(workspace);
-    p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + cache_part_bytes(d));
-    p.border = reinterpret_cast<CacheBorder*>(static_cast<uint8_t*>(workspace) + cache_part_bytes(d) + kCacheStatBytes);
+    const bool prompt = cache_prompt(H, Hk, T);
+    const CacheLayout L = cache_layout(prompt, d);
+    p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + L.stat);
+    p.border = reinterpret_cast<CacheBorder*>(static_cast<uint8_t*>(workspace) + L.border);
     DeviceState ds;
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
     p.rows = p.grid = 0;
-    return launch_cache_decode(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return (prompt ? launch_cache_prompt(p, s) : launch_cache_decode(p, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status attn_check_device_error(attn_stream_t stream, unsigned int* site) {

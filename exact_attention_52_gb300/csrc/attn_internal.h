@@ -150,6 +150,11 @@ struct CacheBorder {
 
 constexpr int kCacheGridMax = 640;  // 160 SMs of four
 constexpr int kCacheRowsMax = 16;
+constexpr int kPromptGridMax = 160;
+constexpr int kPromptRows = 256;
+// More rows per key/value head than this (queries times heads of its group) go to the
+// tensor cores' kernel for prompts.
+constexpr int kPromptMinRows = 64;
 
 struct CacheFwdParams {
     CacheView c;
@@ -164,7 +169,7 @@ struct CacheFwdParams {
     // Set by the launcher:
     int rows;      // query rows of a tile
     int grid;      // CTAs that share the work, at most kCacheGridMax
-    // Workspace, for kCacheGridMax CTAs and kCacheRowsMax rows whatever the launch:
+    // Workspace, for the largest grid of the kernel whatever the launch:
     float* part;   // unfinished segments: fp32 [2 * grid][rows][D]
     float2* stat;  // their maximum (log2 units) and sum: [2 * grid][rows]
     CacheBorder* border;  // [grid]
@@ -183,6 +188,7 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                             const BwdParams& p, cudaStream_t stream);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache_prompt(const CacheFwdParams& p, cudaStream_t stream);
 cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream);
 cudaError_t launch_wait_selftest(DevStatus st, cudaStream_t stream);
 

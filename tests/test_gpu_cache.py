@@ -125,6 +125,46 @@ def test_cache_forward_matches_oracle(shape, left, sinks, d):
     run_cache(pool, H, T, lens, ql, left, sinks)
 
 
+# Queries enough for the kernel of prompts (more than 64 rows a key/value head): tiles
+# that end inside the 128 rows, one and two tiles a pair, several pairs, more queries than
+# tokens, sequences without any, every page size, key tiles that end inside a page.
+PROMPTS = [
+    (1, 1, 1, 65, 16, [65], None),
+    (1, 1, 1, 65, 64, [3], None),              # most rows see nothing
+    (1, 2, 1, 128, 128, [128], None),
+    (2, 6, 2, 100, 32, [1000, 357], [100, 71]),
+    (3, 5, 1, 131, 16, [131, 0, 700], [131, 0, 1]),
+    (1, 16, 1, 300, 1024, [2100], None),
+    (2, 3, 3, 700, 64, [700, 1333], None),
+    (1, 40, 2, 9, 256, [5000], None),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("left,sinks", [(-1, 0), (20, 0), (140, 4), (0, 1), (300, 200), (100000, 3)])
+@pytest.mark.parametrize("shape", PROMPTS)
+def test_cache_forward_of_prompts_matches_oracle(shape, left, sinks, d):
+    B, H, Hk, T, page, lens, ql = shape
+    pool = Pool(2000 + T + H, B, Hk, d, page, max(1, -(-max(lens) // page)))
+    run_cache(pool, H, T, lens, ql, left, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout,token_major", [("bnhd", True), ("bhnd", False)])
+def test_cache_forward_of_prompts_layouts(layout, token_major, d):
+    pool = Pool(17, 2, 2, d, 32, 20, token_major=token_major)
+    run_cache(pool, 8, 90, [611, 305], [90, 43], 333, 2, layout=layout)
+
+
+def test_cache_forward_of_prompts_large_scores_and_values():
+    """Scores that rise far beyond the first tile's maximum (tiles redone, outputs rescaled),
+    page scales far apart."""
+    pool = Pool(19, 1, 2, 128, 16, 80)
+    pool.vs *= 2.0 ** pool.rng.integers(-40, 41, pool.vs.shape)
+    pool.ks[:] = 2.0 ** -5 * (1 + np.arange(len(pool.ks))[:, None] % 2)
+    run_cache(pool, 8, 70, [1250], None, amp=2.0)
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("layout,token_major", [("bnhd", False), ("bhnd", True), ("bnhd", True)])
 def test_cache_forward_layouts(layout, token_major, d):
