@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                 for (int r = 0; r < 2; ++r) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const float f = rq[n][r] * t_sk[u];
+                        const float f = score_factor(rq[n][r], t_sk[u]);
                         sf[u][n][r] = fmaf(sf[u][n][r], f, t_lsv[u]);
                         sf[u][n][2 + r] = fmaf(sf[u][n][2 + r], f, t_lsv[u]);
                     }

@@ -6,16 +6,16 @@
 // g, so that grouped heads fill the tiles and share the keys.  The item's key tiles
 // of 128 tokens stream through a shared-memory ring:
 //
-//   warps 9-11  converters: read the codes of a key or value tile page by page,
+//   warps 12-15 converters: read the codes of a key or value tile page by page,
 //               turn them into f16 (exact) and write them where the tensor core
 //               expects them (128-byte swizzle)
 //   warp 8      MMA issuer: S_g = Q_g K_j^T and O_g += P_g V_j, accumulators in
 //               tensor memory, order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1)
 //   warps 0-3   softmax of query tile 0 (one thread per row), which also bring the
 //   warps 4-7   tile's Q rows to f16; the same for query tile 1
+//   warps 9-11  next to nothing (warps come in fours for the register split)
 //
-// Bound by the tensor cores: 2048 cycles of products a key tile and item, in which
-// the converters' 64 KB of f16 take about 430 issue slots each.  Codes are turned
+// Bound by the tensor cores: 2048 cycles of products a key tile and item.  Codes are turned
 // into f16 and not used as E4M3 operands, because then Q and the weights would have
 // to be E4M3 too (2^-4 relative).  A page's scales enter in fp32 as in the kernel
 // for few queries: score * key scale, + log2 of the value scale in the exponent, and
@@ -36,9 +36,16 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kPairRows = 2 * kTile;
-constexpr int kPromptThreads = 384;
-constexpr int kConvWarps = 3;
-constexpr int kScaleRing = 8;
+constexpr int kPromptThreads = 512;
+constexpr int kConvWarps = 4;
+// Registers a thread: the launch's 128 are dealt out again, 168 for the softmax (a
+// whole score row), 56 for the MMA issuer's four warps, 120 for the converters.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kMmaRegs = 56, kConvRegs = 120;
+static_assert(2 * kSoftmaxRegs + kMmaRegs + kConvRegs <= 4 * kLaunchRegs, "more registers than the launch has");
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 constexpr float kShift = 4.f;           // weights are 2^(score - m + kShift), f16
 constexpr float kRedoBound = 32768.f;   // a row's tile sum that makes it take its own maximum
 
@@ -49,7 +56,7 @@ __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w &
 
 enum : uint32_t {
     SITE_Q = 0x401, SITE_KV_EMPTY = 0x402, SITE_KV_FULL = 0x403, SITE_P_FULL = 0x404, SITE_S_FULL = 0x405,
-    SITE_O_FULL = 0x406, SITE_DRAIN = 0x407, SITE_SCALE = 0x408,
+    SITE_O_FULL = 0x406, SITE_DRAIN = 0x407, SITE_SCALE = 0x408, SITE_MERGE = 0x409,
 };
 
 constexpr uint32_t kFmtF16 = 0;
@@ -60,28 +67,40 @@ struct PromptTraits {
     static constexpr int BLK_BYTES = kTile * 128;
     static constexpr int TILE_BYTES = kTile * D * 2;
     static constexpr int KV_SLOTS = D == 128 ? 5 : 8;
+    static constexpr int SCALES = D == 128 ? 4 : 8;  // ring of the key tiles' scales
     static constexpr int SMEM_Q = 2 * TILE_BYTES;
     static constexpr int OFF_KV = SMEM_Q;
-    static constexpr int OFF_SCALE = OFF_KV + KV_SLOTS * TILE_BYTES;  // float4 [kScaleRing][8]
-    static constexpr int OFF_BAR = OFF_SCALE + kScaleRing * 8 * 16;
-    // q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], scale_full[8], done
-    static constexpr int NBARS = 2 + 2 * KV_SLOTS + 6 + kScaleRing + 1;
-    static constexpr int OFF_SHARE = OFF_BAR + NBARS * 8 + 16;
-    static constexpr int SMEM_BYTES = OFF_SHARE + 256;
+    static constexpr int OFF_SCALE = OFF_KV + KV_SLOTS * TILE_BYTES;  // float4 [SCALES][8]
+    static constexpr int OFF_BAR = OFF_SCALE + SCALES * 8 * 16;
+    // q_full[2], kv_full[S], kv_empty[S], s_full[2], p_full[2], o_full[2], scale_full[SCALES], done,
+    // merge, merged
+    static constexpr int NBARS = 2 + 2 * KV_SLOTS + 6 + SCALES + 3;
+    static constexpr int OFF_WALK = (OFF_BAR + NBARS * 8 + 16 + 15) & ~15;  // a walk per warp; the share's scratch before
+    static constexpr int SMEM_BYTES = OFF_WALK + 14 * 128;  // warps 0-9 and 12-15
     static constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_O0 = 256, COL_O1 = 256 + D;
     static constexpr uint32_t IDESC_S = make_idesc(kFmtF16, kTile, kTile, false, false);
     static constexpr uint32_t IDESC_PV = make_idesc(kFmtF16, kTile, D, false, true);
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-// A pair of query tiles of a sequence and the key tiles it walks: the n_sink first
-// ones of the sequence, then those from lo on; query tile g uses the first n_g of n.
+// wait_warp without its out-of-line half: ptxas deals out registers to parts of a
+// kernel only where they call nothing.
+__device__ __forceinline__ bool wait_in_line(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             const DevStatus& st, uint32_t site) {
+    return wait_warp_loop(bar, parity, abort_flag, st.word, st.wait_limit_ns, site);
+}
+
+// A pair of query tiles of a sequence and the n key tiles it walks: the n_sink first
+// ones of the sequence, then those from lo on.  Query tile g uses the first n_g of
+// them; or, where the pair has rows for one query tile only (dual), the two softmax
+// groups take its key tiles in turn: alone, a query tile's chain of products and
+// softmax would leave the tensor cores idle most of the time.
 struct PromptUnit {
     int len, q_len, rows;
     int first_pos;  // position of query 0 (negative: rows before the first token see nothing)
     int key_lo;     // first key of the window of the pair's first query
-    int n_sink, lo, n, n0, n1;
-    __device__ int tile(int v) const { return v < n_sink ? v : lo + v - n_sink; }
+    int n_sink, lo, dual, n, n0, n1;
+    __device__ int tile(int t) const { return t < n_sink ? t : lo + t - n_sink; }
 };
 
 __device__ PromptUnit prompt_unit(const CacheFwdParams& p, int b, int pair) {
@@ -91,7 +110,7 @@ __device__ PromptUnit prompt_unit(const CacheFwdParams& p, int b, int pair) {
     u.q_len = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
     u.rows = u.q_len * G;
     u.first_pos = u.len - u.q_len;
-    u.n = u.n0 = u.n1 = u.n_sink = u.lo = u.key_lo = 0;
+    u.n = u.n0 = u.n1 = u.n_sink = u.lo = u.key_lo = u.dual = 0;
     const int r0 = pair * kPairRows;
     if (r0 >= u.rows) return u;  // no such pair: no work
     const int pos_lo = max(0, u.first_pos + r0 / G);
@@ -102,15 +121,16 @@ __device__ PromptUnit prompt_unit(const CacheFwdParams& p, int b, int pair) {
         const int pos = u.first_pos + min(u.rows - 1, row_hi) / G;
         return pos < 0 ? 0 : u.n_sink + pos / kTile - u.lo + 1;
     };
+    u.dual = r0 + kTile >= u.rows;
     u.n0 = tiles(r0 + kTile - 1);
-    u.n1 = r0 + kTile < u.rows ? tiles(r0 + kPairRows - 1) : 0;
-    u.n = max(1, max(u.n0, u.n1));
+    u.n1 = u.dual ? u.n0 : tiles(r0 + kPairRows - 1);
+    u.n = max(1, u.n1);  // one that no row sees stands for none
     return u;
 }
 
-// A CTA's share: blocks [x, x_end) of the line on which the units' items lie end to
+// A CTA's share: key tiles [x, x_end) of the line on which the units' items lie end to
 // end (each unit once per key/value head), starting in unit `unit`, before which lie
-// unit_first blocks.  unit < 0: nothing.
+// unit_first key tiles.  unit < 0: nothing.
 struct PromptShare {
     long long share, x, x_end, unit_first;
     int unit;
@@ -168,32 +188,43 @@ __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptSh
     return s;
 }
 
-// Walks the segments of a share, for every role alike.
+// Walks the segments of a share, for every role alike.  Each warp keeps its own walk
+// in shared memory: its fields are read a few times a tile, and the softmax has no
+// registers for them.
 struct PromptWalk {
     PromptShare s;
-    int pairs;
     PromptUnit u;
-    int b, pair, hk, v0, v1, a0, a1;  // segment [v0, v1); query tile g is live in its first a_g tiles
-    __device__ PromptWalk(const PromptShare& share, int pairs_) : s(share), pairs(pairs_) {}
-    __device__ bool next(const CacheFwdParams& p) {
-        if (s.unit < 0 || s.x >= s.x_end) return false;
-        u = prompt_unit(p, s.unit / pairs, s.unit % pairs);
-        for (long long w; s.x >= s.unit_first + (w = static_cast<long long>(u.n) * p.Hk);) {
-            s.unit_first += w;
-            ++s.unit;
-            u = prompt_unit(p, s.unit / pairs, s.unit % pairs);
-        }
-        b = s.unit / pairs;
-        pair = s.unit - b * pairs;
-        hk = static_cast<int>(div_mostly32(s.x - s.unit_first, u.n));
-        v0 = static_cast<int>((s.x - s.unit_first) - static_cast<long long>(hk) * u.n);
-        v1 = static_cast<int>(min(static_cast<long long>(u.n), v0 + (s.x_end - s.x)));
-        a0 = max(0, min(v1, u.n0) - v0);
-        a1 = max(0, min(v1, u.n1) - v0);
-        s.x += v1 - v0;
-        return true;
-    }
+    int pairs, b, pair, hk;
+    int v0, v1;  // key tiles [v0, v1) of the item
+    int a0, a1;  // those that softmax group g takes: the first a_g, or (dual) v0 + g, v0 + g + 2, ...
 };
+// By a whole warp; every lane works out the same step.
+__device__ __forceinline__ bool next_segment(const CacheFwdParams& p, PromptWalk* walk) {
+    PromptWalk w = *walk;
+    __syncwarp();
+    if (w.s.unit < 0 || w.s.x >= w.s.x_end) return false;
+    w.u = prompt_unit(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
+    for (long long n; w.s.x >= w.s.unit_first + (n = static_cast<long long>(w.u.n) * p.Hk);) {
+        w.s.unit_first += n;
+        ++w.s.unit;
+        w.u = prompt_unit(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
+    }
+    w.b = w.s.unit / w.pairs;
+    w.pair = w.s.unit - w.b * w.pairs;
+    w.hk = static_cast<int>(div_mostly32(w.s.x - w.s.unit_first, w.u.n));
+    w.v0 = static_cast<int>((w.s.x - w.s.unit_first) - static_cast<long long>(w.hk) * w.u.n);
+    w.v1 = static_cast<int>(min(static_cast<long long>(w.u.n), w.v0 + (w.s.x_end - w.s.x)));
+    w.a0 = max(0, min(w.v1, w.u.n0) - w.v0);
+    w.a1 = max(0, min(w.v1, w.u.n1) - w.v0);
+    if (w.u.dual) {
+        w.a1 = w.a0 / 2;
+        w.a0 -= w.a1;
+    }
+    w.s.x += w.v1 - w.v0;
+    if ((threadIdx.x & 31) == 0) *walk = w;
+    __syncwarp();
+    return true;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const CacheFwdParams p, const int pairs) {
@@ -211,7 +242,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     auto b_kv_empty = [&](int s) { return bar0 + 8u * (2 + T::KV_SLOTS + s); };
     const uint32_t b_s_full = bar0 + 8u * (2 + 2 * T::KV_SLOTS);  // + 8 g
     const uint32_t b_p_full = b_s_full + 16u, b_o_full = b_p_full + 16u, b_scale = b_o_full + 16u;
-    const uint32_t b_done = b_scale + 8u * kScaleRing;
+    const uint32_t b_done = b_scale + 8u * T::SCALES;
+    const uint32_t b_merge = b_done + 8u, b_merged = b_done + 16u;  // dual items: group 1's part is there / has been read
 
     if ((smem_u32(smem) & 1023u) != 0) {  // swizzle atoms need 1024-byte alignment
         if (threadIdx.x == 0) record_device_error(p.st, ATTN_DEVERR_SMEM_ALIGN, 0x4FF);
@@ -228,8 +260,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             mbar_init(b_kv_full(s), kConvWarps);
             mbar_init(b_kv_empty(s), 1);
         }
-        for (int s = 0; s < kScaleRing; ++s) mbar_init(b_scale + 8u * s, 1);
+        for (int s = 0; s < T::SCALES; ++s) mbar_init(b_scale + 8u * s, kConvWarps);
         mbar_init(b_done, 1);
+        mbar_init(b_merge, 4);
+        mbar_init(b_merged, 4);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -238,123 +272,174 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         tmem_relinquish();
     }
     tc_fence_before();
-    const PromptShare share = prompt_share(p, pairs, reinterpret_cast<PromptShareSmem*>(smem + T::OFF_SHARE));
+    static_assert(sizeof(PromptWalk) <= 128 && sizeof(PromptShareSmem) <= 256, "walk slots");
+    PromptWalk* const walk = reinterpret_cast<PromptWalk*>(smem + T::OFF_WALK + (warp < 10 ? warp : warp - 2) * 128);
+    {
+        const PromptShare share = prompt_share(p, pairs, reinterpret_cast<PromptShareSmem*>(smem + T::OFF_WALK));
+        __syncthreads();  // the scratch has been read
+        if (lane == 0 && (warp < 10 || warp >= 12)) {
+            walk->s = share;
+            walk->pairs = pairs;
+        }
+        __syncwarp();
+    }
+    const PromptWalk& w = *walk;
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = *tmem_slot;
-    PromptWalk w(share, pairs);
     const int G = p.H / p.Hk;
 
-    if (warp >= 9) {
-        // ================= converters =================
-        const int cw = warp - 9;
-        constexpr int LPR = D / 16, RPI = 32 / LPR;                // lanes a row, rows an instruction
-        constexpr int GROUPS = kTile / RPI, PER = (GROUPS + kConvWarps - 1) / kConvWarps;
-        const int crow = lane / LPR, cc = lane % LPR;
+    if (warp >= 12) {
+        // ================= converters: 16-token groups 2 cw and 2 cw + 1 of every tile =================
+        regs_dec<kConvRegs>();
+        const int cw = warp - 12;
+        constexpr int RPI = 512 / D, NI = 16 / RPI;  // rows a warp instruction loads, and those a group
+        // Lane -> row of an instruction and 16-code piece of it: a quarter warp takes two
+        // neighbouring rows, four pieces of one 128-byte block each, so that the f16 pieces it
+        // writes lie in eight different banks.
+        const int crow = D == 128 ? (lane >> 2) & 3 : lane >> 2;
+        const int cc = D == 128 ? (lane & 3) | (lane >> 4 << 2) : lane & 3;
         const long long kn = p.c.ks.n, vn = p.c.vs.n;
-        int idx = 0;   // ring position, over all segments
+        // f16 pieces 2c and 2c + 1 in row crow of this warp's part of a tile
+        const uint32_t row_at = (cc >> 2) * T::BLK_BYTES + cw * 32 * 128 + crow * 128, c2 = (cc & 3) * 2;
+        const uint32_t at0 = row_at + ((c2 ^ crow) << 4), at1 = row_at + (((c2 + 1) ^ crow) << 4);
+        int idx = 0;      // ring position, over all segments
         int tile_no = 0;  // key tiles converted
         bool ok = true;
-        while (ok && w.next(p)) {
-            const uint8_t* kbase = p.c.k_pages + w.hk * p.c.ks.h + cc * 16;
-            const uint8_t* vbase = p.c.v_pages + w.hk * p.c.vs.h + cc * 16;
-            // lanes 0-7 (repeated above): the tile's eight groups of 16 tokens
-            long long koff = 0, voff = 0;
-            float sk = 1.f, sv = 1.f;
-            int tok0 = 0;
-            auto find = [&](int v) {  // pages of the walk's v-th key tile
-                tok0 = w.u.tile(v) * kTile;
-                const int tok = tok0 + (lane & 7) * 16;
-                koff = voff = 0;
-                sk = sv = 1.f;
-                if (tok < w.u.len && (tok + 16 > w.u.key_lo || tok < p.sinks)) {
-                    const int pid = cache_page(p.c, p.st, w.b, tok), slot = tok & (p.c.page_size - 1);
-                    koff = pid * p.c.ks.b + slot * kn;
-                    voff = pid * p.c.vs.b + slot * vn;
-                    const long long at = static_cast<long long>(pid) * p.Hk + w.hk;
-                    sk = __ldg(p.c.k_scale + at);
-                    sv = __ldg(p.c.v_scale + at);
-                }
+        while (ok && next_segment(p, walk)) {
+            const uint8_t* kbase = p.c.k_pages + w.hk * p.c.ks.h + crow * kn + cc * 16;
+            const uint8_t* vbase = p.c.v_pages + w.hk * p.c.vs.h + crow * vn + cc * 16;
+            const int len = w.u.len, key_lo = w.u.key_lo;
+            auto first_tok = [&](int t) { return w.u.tile(t) * kTile + cw * 32; };
+            // some query sees a token of the group from tok on
+            auto needed = [&](int tok) { return tok < len && (tok + 16 > key_lo || tok < p.sinks); };
+            // Page numbers of both groups of 16 tiles at a time, lane 2i + g holding group g of
+            // tile i, fetched 16 tiles before their use (shared memory leaves the L1 no room:
+            // each look at the table goes to the L2).
+            auto fetch = [&](int t) {
+                const int x = t + (lane >> 1), tok = x < w.v1 ? first_tok(x) + 16 * (lane & 1) : len;
+                return needed(tok) ? __ldg(p.c.table + w.b * p.c.table_stride + (tok >> p.c.page_shift)) : 0;
             };
-            uint4 kb[PER], vb[PER];
-            auto load = [&](uint4 (&buf)[PER], const uint8_t* base, long long off, long long n) {
+            auto checked = [&](int pid) {
+                if (static_cast<unsigned>(pid) < static_cast<unsigned>(p.c.num_pages)) return pid;
+                record_device_error(p.st, ATTN_DEVERR_PAGE, 0x401);
+                return 0;
+            };
+            // codes of both groups; tokens that no query sees are not read and count as zeros
+            auto load = [&](uint4 (&buf)[2 * NI], const uint8_t* base, const Strides& st, int tok0, const int (&pid)[2]) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int grp = cw + kConvWarps * i;
-                    const int row = grp * RPI + crow;
-                    const long long o16 = __shfl_sync(0xffffffffu, off, (grp * RPI) >> 4);
-                    const int tok = tok0 + row;
-                    buf[i] = make_uint4(0u, 0u, 0u, 0u);  // tokens that no query sees are zeros
-                    if (grp < GROUPS && tok < w.u.len && (tok >= w.u.key_lo || tok < p.sinks))
-                        buf[i] = __ldg(reinterpret_cast<const uint4*>(base + o16 + (row & 15) * n));
+                for (int i = 0; i < 2; ++i) {
+                    const int tok = tok0 + 16 * i;
+                    const uint8_t* src = base + pid[i] * st.b + (tok & (p.c.page_size - 1)) * st.n;
+                    if (tok + 16 <= len && (tok >= key_lo || tok + 16 <= p.sinks)) {
+#pragma unroll
+                        for (int k = 0; k < NI; ++k) buf[i * NI + k] = __ldg(reinterpret_cast<const uint4*>(src + k * RPI * st.n));
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < NI; ++k) {
+                            const int x = tok + k * RPI + crow;
+                            buf[i * NI + k] = make_uint4(0u, 0u, 0u, 0u);
+                            if (x < len && (x >= key_lo || x < p.sinks))
+                                buf[i * NI + k] = __ldg(reinterpret_cast<const uint4*>(src + k * RPI * st.n));
+                        }
+                    }
                 }
             };
-            auto convert = [&](const uint4 (&buf)[PER], bool keys) -> bool {
-                const int slot = idx % T::KV_SLOTS, round = idx / T::KV_SLOTS;
-                if (round > 0 && !wait_warp(b_kv_empty(slot), (round - 1) & 1, abort_flag, p.st, SITE_KV_EMPTY))
-                    return false;
-                if (keys && cw == 0) {  // the tile's scales: their entry is free now (see the softmax)
-                    if (lane < 8)
-                        scales[(tile_no % kScaleRing) * 8 + lane] = make_float4(sk, lg2_approx(sv), rcp_approx(sv), 0.f);
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_scale + 8u * (tile_no % kScaleRing));
-                }
+            auto claim = [&]() {
+                const int round = idx / T::KV_SLOTS;
+                return round == 0 || wait_in_line(b_kv_empty(idx % T::KV_SLOTS), (round - 1) & 1, abort_flag, p.st, SITE_KV_EMPTY);
+            };
+            auto convert = [&](const uint4 (&buf)[2 * NI]) {
+                const int slot = idx % T::KV_SLOTS;
                 uint8_t* dst = sKV + slot * T::TILE_BYTES;
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int grp = cw + kConvWarps * i;
-                    if (grp >= GROUPS) break;
-                    const int row = grp * RPI + crow;
-                    const uint32_t in[4] = {buf[i].x, buf[i].y, buf[i].z, buf[i].w};
-                    uint32_t h[8];
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) e4m3x4_to_f16(in[k], h[2 * k], h[2 * k + 1]);
-                    // 16-byte pieces 2c and 2c + 1 of the row's 128-byte block; lanes of the
-                    // second block write them the other way round, so that a quarter warp's
-                    // eight pieces lie in different banks
-                    uint8_t* at = dst + (cc >> 2) * T::BLK_BYTES + row * 128;
-                    const int c = (cc & 3) * 2, flip = (cc >> 2) & 1;
-                    const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-                    *reinterpret_cast<uint4*>(at + (((c + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
-                    *reinterpret_cast<uint4*>(at + (((c + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
-                }
+                    for (int k = 0; k < NI; ++k) {
+                        const uint4 x = buf[i * NI + k];
+                        uint32_t h[8];
+                        e4m3x4_to_f16(x.x, h[0], h[1]);
+                        e4m3x4_to_f16(x.y, h[2], h[3]);
+                        e4m3x4_to_f16(x.z, h[4], h[5]);
+                        e4m3x4_to_f16(x.w, h[6], h[7]);
+                        const uint32_t more = (i * 16 + k * RPI) * 128, sw = ((k * RPI) & 7) << 4;  // swizzle of the row
+                        *reinterpret_cast<uint4*>(dst + more + (at0 ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<uint4*>(dst + more + (at1 ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_kv_full(slot));
                 ++idx;
-                return true;
             };
-            find(w.v0);
-            load(kb, kbase, koff, kn);
-            for (int v = w.v0; v < w.v1 && ok; ++v) {
-                load(vb, vbase, voff, vn);
-                ok = convert(kb, true);
-                if (!ok) break;
-                ++tile_no;
-                if (v + 1 < w.v1) {
-                    find(v + 1);
-                    load(kb, kbase, koff, kn);
+            // lanes 0 and 1: the scales of group `lane`
+            float sk = 1.f, sv = 1.f;
+            auto load_scales = [&](int tok0, const int (&pid)[2]) {
+                const int i = lane & 1;
+                if (lane < 2 && needed(tok0 + 16 * i)) {
+                    const long long at = static_cast<long long>(i ? pid[1] : pid[0]) * p.Hk + w.hk;
+                    sk = __ldg(p.c.k_scale + at);
+                    sv = __ldg(p.c.v_scale + at);
                 }
-                ok = convert(vb, false);
+            };
+            // Loads run ahead of their use: V of the tile before K is converted, K of the next
+            // one before V is.
+            uint4 kb[2 * NI], vb[2 * NI];
+            int pages = checked(fetch(w.v0)), pages_next = fetch(w.v0 + 16), pid[2];
+            auto take_pages = [&](int i) {  // of the segment's i-th tile
+                if (i > 0 && (i & 15) == 0) {
+                    pages = checked(pages_next);
+                    pages_next = fetch(w.v0 + i + 16);
+                }
+                pid[0] = __shfl_sync(0xffffffffu, pages, 2 * (i & 15));
+                pid[1] = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + 1);
+            };
+            const int tiles = w.v1 - w.v0;
+            int tok0 = first_tok(w.v0);
+            if (tiles > 0) {
+                take_pages(0);
+                load(kb, kbase, p.c.ks, tok0, pid);
+                load_scales(tok0, pid);
+            }
+            for (int i = 0; i < tiles; ++i) {
+                load(vb, vbase, p.c.vs, tok0, pid);
+                if (!(ok = claim())) break;
+                // the scales' entry of the tile is free now as well (see the softmax)
+                if (lane < 2)
+                    scales[(tile_no % T::SCALES) * 8 + 2 * cw + lane] = make_float4(sk, lg2_approx(sv), rcp_approx(sv), 0.f);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_scale + 8u * (tile_no % T::SCALES));
+                convert(kb);
+                ++tile_no;
+                if (i + 1 < tiles) {
+                    tok0 = first_tok(w.v0 + i + 1);
+                    take_pages(i + 1);
+                    load(kb, kbase, p.c.ks, tok0, pid);
+                    load_scales(tok0, pid);
+                }
+                if (!(ok = claim())) break;
+                convert(vb);
             }
         }
-    } else if (warp == 8) {
+    } else if (warp >= 8) {
+        regs_dec<kMmaRegs>();
+        if (warp == 8) {
         // ================= MMA issuer (the whole warp; one elected lane issues) =================
         const SmemDesc dq0 = sw128_desc_words(smem_u32(smem), 16, 1024);                  // Q, K-major
         const SmemDesc dk0 = sw128_desc_words(smem_u32(sKV), 16, 1024);                   // K tiles, K-major
         const SmemDesc dv0 = sw128_desc_words(smem_u32(sKV), T::BLK_BYTES, 1024);         // V tiles, MN-major
         int ring = 0;                // ring position of the segment's first K tile
-        int pdone[2] = {0, 0};       // P tiles of query tile g consumed in earlier segments
-        int qdone[2] = {0, 0};       // segments in which query tile g was live
+        int pdone0 = 0, pdone1 = 0;  // P tiles of group g consumed in earlier segments
+        int qdone0 = 0, qdone1 = 0;  // segments in which group g was live
         auto slot_desc = [&](SmemDesc base, int i) {
             return desc_add(base, static_cast<uint32_t>((i % T::KV_SLOTS) * T::TILE_BYTES));
         };
         auto wait_kv = [&](int i) {
-            return wait_warp(b_kv_full(i % T::KV_SLOTS), (i / T::KV_SLOTS) & 1, abort_flag, p.st, SITE_KV_FULL);
+            return wait_in_line(b_kv_full(i % T::KV_SLOTS), (i / T::KV_SLOTS) & 1, abort_flag, p.st, SITE_KV_FULL);
         };
-        auto issue_s = [&](int g, int j) {
+        auto release = [&](int i) { mma_commit_warp(b_kv_empty(i % T::KV_SLOTS)); };
+        auto issue_s = [&](int g, int ki) {  // S_g = Q_g K^T, K in ring position ki
             const SmemDesc qa = desc_add(dq0, static_cast<uint32_t>(g * T::TILE_BYTES));
-            const SmemDesc kd = slot_desc(dk0, ring + 2 * j);
+            const SmemDesc kd = slot_desc(dk0, ki);
 #pragma unroll
             for (int q = 0; q < D / 64; ++q)
                 mma_ss_warp4<false, 0, 2, 4, 6, 0, 2, 4, 6>(tmem + (g ? T::COL_S1 : T::COL_S0),
@@ -362,54 +447,122 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                                                             T::IDESC_S, q > 0 ? 1u : 0u);
             mma_commit_warp(b_s_full + 8u * g);
         };
-        auto issue_pv = [&](int g, int j) {
-            const SmemDesc vd = slot_desc(dv0, ring + 2 * j + 1);
+        auto issue_pv = [&](int g, int vi, bool first) {  // O_g += P_g V, V in ring position vi
+            const SmemDesc vd = slot_desc(dv0, vi);
             constexpr uint32_t VS = 16 * 8;  // V rows of one instruction (16), in 16-byte units
 #pragma unroll
             for (int q = 0; q < 2; ++q)
                 mma_ts_warp4<false, 0, 8, 16, 24, 0, VS, 2 * VS, 3 * VS>(
                     tmem + (g ? T::COL_O1 : T::COL_O0), tmem + (g ? T::COL_S1 : T::COL_S0) + 32 * q,
-                    desc_add(vd, static_cast<uint32_t>(4 * q * 16 * 128)), T::IDESC_PV, (j > 0 || q > 0) ? 1u : 0u);
+                    desc_add(vd, static_cast<uint32_t>(4 * q * 16 * 128)), T::IDESC_PV, (!first || q > 0) ? 1u : 0u);
         };
-        auto run = [&]() -> bool {
-            const int a[2] = {w.a0, w.a1}, steps = w.v1 - w.v0;
+        auto wait_q = [&](int g) {
+            const bool ok = wait_in_line(b_q + 8u * g, (g ? qdone1 : qdone0) & 1, abort_flag, p.st, SITE_Q);
+            tc_fence_after();
+            return ok;
+        };
+        auto wait_p = [&](int g, int j) {
+            const bool ok = wait_in_line(b_p_full + 8u * g, ((g ? pdone1 : pdone0) + j) & 1, abort_flag, p.st, SITE_P_FULL);
+            tc_fence_after();
+            return ok;
+        };
+        // Every tile's full barrier is waited for, used or not: a phase that is skipped would
+        // be taken for a later one.
+        auto run_pair = [&](int a0, int a1, int steps) -> bool {
             if (!wait_kv(ring)) return false;
 #pragma unroll
             for (int g = 0; g < 2; ++g)
-                if (a[g] > 0) {
-                    if (!wait_warp(b_q + 8u * g, qdone[g] & 1, abort_flag, p.st, SITE_Q)) return false;
-                    tc_fence_after();
-                    issue_s(g, 0);
+                if ((g ? a1 : a0) > 0) {
+                    if (!wait_q(g)) return false;
+                    issue_s(g, ring);
                 }
-            mma_commit_warp(b_kv_empty(ring % T::KV_SLOTS));
+            release(ring);
             for (int j = 0; j < steps; ++j) {
-                if (!wait_kv(ring + 2 * j + 1)) return false;                       // V_j
-                if (j + 1 < steps && !wait_kv(ring + 2 * j + 2)) return false;      // K_{j+1}
+                const int vi = ring + 2 * j + 1;
+                bool k_ready = j + 1 >= steps;
+                if (!wait_kv(vi)) return false;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    if (j >= a[g]) continue;
-                    if (!wait_warp(b_p_full + 8u * g, (pdone[g] + j) & 1, abort_flag, p.st, SITE_P_FULL)) return false;
-                    tc_fence_after();
-                    issue_pv(g, j);
-                    if (j + 1 < a[g]) issue_s(g, j + 1);
-                    else mma_commit_warp(b_o_full + 8u * g);
+                    const int a = g ? a1 : a0;
+                    if (j >= a) continue;
+                    if (!wait_p(g, j)) return false;
+                    issue_pv(g, vi, j == 0);
+                    if (j + 1 < a) {
+                        if (!k_ready && !wait_kv(vi + 1)) return false;
+                        k_ready = true;
+                        tc_fence_after();
+                        issue_s(g, vi + 1);
+                    } else {
+                        mma_commit_warp(b_o_full + 8u * g);
+                    }
                 }
-                mma_commit_warp(b_kv_empty((ring + 2 * j + 1) % T::KV_SLOTS));
-                if (j + 1 < steps) mma_commit_warp(b_kv_empty((ring + 2 * j + 2) % T::KV_SLOTS));
+                release(vi);
+                if (j + 1 < steps) {
+                    if (!k_ready && !wait_kv(vi + 1)) return false;
+                    release(vi + 1);
+                }
             }
             return true;
         };
-        while (w.next(p)) {
-            if (!run()) break;
+        auto run_dual = [&](int a0, int a1) -> bool {  // group g: tiles g, g + 2, ... of the segment
+            if (a0 == 0) {  // the tile that stands for none
+                if (!wait_kv(ring) || !wait_kv(ring + 1)) return false;
+                release(ring);
+                release(ring + 1);
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+                if ((g ? a1 : a0) > 0) {
+                    if (!wait_kv(ring + 2 * g) || !wait_q(g)) return false;
+                    issue_s(g, ring + 2 * g);
+                    release(ring + 2 * g);
+                }
+            for (int j = 0; j < a0; ++j)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int a = g ? a1 : a0, vi = ring + 4 * j + 2 * g + 1;
+                    if (j >= a) continue;
+                    if (!wait_kv(vi) || !wait_p(g, j)) return false;
+                    issue_pv(g, vi, j == 0);
+                    release(vi);
+                    if (j + 1 < a) {
+                        if (!wait_kv(vi + 3)) return false;
+                        tc_fence_after();
+                        issue_s(g, vi + 3);
+                        release(vi + 3);
+                    } else {
+                        mma_commit_warp(b_o_full + 8u * g);
+                    }
+                }
+            return true;
+        };
+        while (next_segment(p, walk)) {
+            const int a0 = w.a0, a1 = w.a1;
+            if (!(w.u.dual ? run_dual(a0, a1) : run_pair(a0, a1, w.v1 - w.v0))) break;
             ring += 2 * (w.v1 - w.v0);
-            pdone[0] += w.a0;
-            pdone[1] += w.a1;
-            qdone[0] += w.a0 > 0;
-            qdone[1] += w.a1 > 0;
+            pdone0 += a0;
+            pdone1 += a1;
+            qdone0 += a0 > 0;
+            qdone1 += a1 > 0;
         }
         mma_commit_warp(b_done);  // every product has finished before tensor memory is freed
-        wait_drain(b_done, 0, p.st, SITE_DRAIN);
+        wait_drain_loop(b_done, 0, p.st.word, p.st.wait_limit_ns, SITE_DRAIN);
+        } else if (warp == 9) {  // what the joining kernel finds at the border before this share
+            CacheBorder bd;
+            bd.c_first = -1;
+            bd.b = bd.item = bd.q_len = bd.c_last = 0;
+            const long long x = w.s.x;
+            if (next_segment(p, walk) && w.v0 > 0) {
+                bd.b = w.b;
+                bd.item = w.pair * p.Hk + w.hk;
+                bd.q_len = w.u.q_len;
+                bd.c_first = static_cast<int>(div_mostly32(x - w.v0, w.s.share)) + 1;
+                bd.c_last = static_cast<int>(div_mostly32(x - w.v0 + w.u.n - 1, w.s.share));
+            }
+            if (lane == 0) p.border[blockIdx.x] = bd;
+        }
     } else {
+        regs_inc<kSoftmaxRegs>();
         // ================= softmax: one thread per row of query tile g =================
         const int g = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -417,14 +570,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         const uint32_t tO = tmem + (g ? T::COL_O1 : T::COL_O0) + lane_off;
         const uint32_t b_sf = b_s_full + 8u * g, b_pf = b_p_full + 8u * g, b_of = b_o_full + 8u * g;
         uint8_t* q_row = smem + g * T::TILE_BYTES + row * 128;
-        int s_seen = 0, o_seen = 0, tile_no = 0;
+        int s_seen = 0, o_seen = 0, tile_no = 0, merges = 0;
         bool ok = true;
-        while (ok && w.next(p)) {
+        while (ok && next_segment(p, walk)) {
             const int n = g ? w.a1 : w.a0;
-            const int r = w.pair * kPairRows + g * kTile + row;  // row of the key/value head
+            const bool dual = w.u.dual;
+            const int r = w.pair * kPairRows + (dual ? 0 : g * kTile) + row;  // row of the key/value head
             const bool row_ok = r < w.u.rows;
             const int t = row_ok ? r / G : 0, h = w.hk * G + (row_ok ? r - t * G : 0);
-            const int pos = row_ok ? w.u.first_pos + t : -1;
+            // rows behind the last query (zeros, never written) take its place: no mask of their own
+            const int pos = w.u.first_pos + (row_ok ? t : w.u.q_len - 1);
             const int key_min = p.left < 0 ? 0 : pos - p.left;
             float rq = 0.f;
             if (n > 0) {
@@ -456,39 +611,44 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             float m_used = -INFINITY;  // running maximum of score + log2 sv (log2 units), possibly stale
             float l_sum = 0.f;         // sum of 2^(score - m_used + kShift) (value scales taken back out)
             for (int j = 0; j < n; ++j) {
-                // Scales of key tile j.  Its entry is written again for tile j + 8, once that
-                // tile's K slot is free: the one of V(j + 5) (five slots) or K(j + 4) (eight),
-                // read by products that follow this warp's arrival for tile j + 3 at least.
-                const int tn = tile_no + j;
-                if (!wait_warp(b_scale + 8u * (tn % kScaleRing), (tn / kScaleRing) & 1, abort_flag, p.st, SITE_SCALE) ||
-                    !wait_warp(b_sf, (s_seen + j) & 1, abort_flag, p.st, SITE_S_FULL)) {
+                // Scales of key tile j.  Its entry is written again for the tile SCALES further
+                // on, once that tile's K slot is free: the one of V(j + 1) (five slots, four
+                // entries) or K(j + 4) (eight and eight), which products read that were issued
+                // after this warp had arrived for tile j.
+                const int ti = dual ? 2 * j + g : j, tn = tile_no + ti;  // tile of the segment, and of all
+                const int kv0 = w.u.tile(w.v0 + ti) * kTile;
+                const int c_lo = key_min - kv0, c_hi = pos - kv0, c_sink = p.sinks - kv0;
+                const bool masked = __any_sync(0xffffffffu, (c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1);
+                if (!wait_in_line(b_scale + 8u * (tn % T::SCALES), (tn / T::SCALES) & 1, abort_flag, p.st, SITE_SCALE) ||
+                    !wait_in_line(b_sf, (s_seen + j) & 1, abort_flag, p.st, SITE_S_FULL)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float4* sc = scales + (tn % kScaleRing) * 8;
+                const float4* sc = scales + (tn % T::SCALES) * 8;
                 uint32_t s[4][32];
                 auto load_s = [&]() {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
-                    const int kv0 = w.u.tile(w.v0 + j) * kTile;
-                    const int c_lo = key_min - kv0, c_hi = pos - kv0, c_sink = p.sinks - kv0;
-                    if ((c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1) {
+                    if (masked) {
+                        // opaque to the compiler, which otherwise forms all 128 comparisons of every
+                        // tile ahead of this branch (1.5 ms for a call of 0.65 ms)
+                        int lo = c_lo, hi = c_hi, sink = c_sink;
+                        asm volatile("" : "+r"(lo), "+r"(hi), "+r"(sink));
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
                                 const int k = c * 32 + i;
-                                if ((k < c_lo && k >= c_sink) || k > c_hi) s[c][i] = f2u(-INFINITY);
+                                if ((k < lo && k >= sink) || k > hi) s[c][i] = f2u(-INFINITY);
                             }
                     }
                 };
-                load_s();
                 float alpha = 1.f;
                 bool rescale_o = false;
-                auto update_max = [&](float tau) {
+                auto update_max = [&]() {
                     float mx = -INFINITY;
 #pragma unroll
                     for (int grp = 0; grp < 8; ++grp) {
@@ -497,17 +657,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         float a = fmax3(u2f(x[0]), u2f(x[1]), u2f(x[2]));
 #pragma unroll
                         for (int i = 3; i < 15; i += 2) a = fmax3(a, u2f(x[i]), u2f(x[i + 1]));
-                        mx = fmaxf(mx, fmaf(fmaxf(a, u2f(x[15])), rq * e.x, e.y));
+                        mx = fmaxf(mx, fmaf(fmaxf(a, u2f(x[15])), score_factor(rq, e.x), e.y));
                     }
-                    if (mx > m_used + tau) {
-                        alpha = ex2_approx(m_used - mx);  // 0 while m_used is -inf
-                        l_sum *= alpha;
+                    if (mx > m_used) {
+                        const float a = ex2_approx(m_used - mx);  // 0 while m_used is -inf
+                        alpha *= a;
+                        l_sum *= a;
                         m_used = mx;
                         rescale_o = j > 0;
                     }
                 };
-                if (__any_sync(0xffffffffu, m_used == -INFINITY)) update_max(0.f);
-
                 uint32_t pk[2][32];
                 float tile_sum, tile_l;
                 auto exp_pass = [&]() {
@@ -516,7 +675,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
 #pragma unroll
                     for (int grp = 0; grp < 8; ++grp) {
                         const float4 e = sc[grp];  // the same address in every lane
-                        const float f = rq * e.x, add = e.y + sub;
+                        const float f = score_factor(rq, e.x), add = e.y + sub;
                         const uint32_t* x = s[grp >> 1] + (grp & 1) * 16;
                         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
@@ -533,12 +692,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         tile_l = fmaf(a0 + a1, e.z, tile_l);
                     }
                 };
-                exp_pass();
-                if (__any_sync(0xffffffffu, !(tile_sum <= kRedoBound))) {
-                    // scores rose above m_used: redo the tile with its own maximum
+                // Against m_used as it is; a tile whose scores rise far above it is done again
+                // with its own maximum (S is still there: no P has been stored).
+#pragma unroll 1
+                for (int pass = 0;; ++pass) {
                     load_s();
-                    update_max(0.f);
+                    if (pass > 0 || __any_sync(0xffffffffu, m_used == -INFINITY)) update_max();
                     exp_pass();
+                    if (pass > 0 || !__any_sync(0xffffffffu, !(tile_sum <= kRedoBound))) break;
                 }
                 tmem_st32(tS, pk[0]);
                 tmem_st32(tS + 32, pk[1]);
@@ -563,16 +724,51 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             s_seen += n;
             tile_no += w.v1 - w.v0;
             if (ok && n > 0) {
-                ok = wait_warp(b_of, o_seen & 1, abort_flag, p.st, SITE_O_FULL);
+                ok = wait_in_line(b_of, o_seen & 1, abort_flag, p.st, SITE_O_FULL);
                 ++o_seen;
                 tc_fence_after();
             }
             if (!ok) break;
-            const bool finished = w.v0 == 0 && w.v1 == w.u.n;
+            if (dual && w.a1 > 0) {
+                if (g == 1) {
+                    // This group's maximum and sum beside its O in tensor memory, whose lanes the
+                    // other group's warp of the same number can read; the columns are its own P's,
+                    // which the products have read.
+                    uint32_t x[16] = {f2u(l_sum != 0.f ? m_used : -INFINITY), f2u(l_sum)};
+                    tmem_st16(tS, x);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_merge);
+                    // the next segment's Q lets products write there again
+                    ok = wait_in_line(b_merged, merges & 1, abort_flag, p.st, SITE_MERGE);
+                    ++merges;
+                    continue;
+                }
+                ok = wait_in_line(b_merge, merges & 1, abort_flag, p.st, SITE_MERGE);
+                ++merges;
+                if (!ok) break;
+                tc_fence_after();
+            } else if (dual && g == 1) {
+                continue;  // the only tile was group 0's
+            }
+            const bool finished = w.v0 == 0 && w.v1 == w.u.n, merge = dual && w.a1 > 0;
+            // group 0's O and sum times f0, and, merging, group 1's times f1
+            float f0 = 1.f, f1 = 0.f;
+            if (merge) {
+                uint32_t x[32];
+                tmem_ld32(tmem + T::COL_S1 + lane_off, x);
+                tmem_ld_wait(x);
+                const float m1 = u2f(x[0]), l1 = u2f(x[1]), m0 = l_sum != 0.f ? m_used : -INFINITY;
+                m_used = fmaxf(m0, m1);
+                f0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m_used);
+                f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m_used);
+                l_sum = l_sum * f0 + l1 * f1;
+            }
             // without a live key tile: O = 0 and LSE = +inf, or a segment that takes no part
             const float inv = n > 0 && l_sum != 0.f ? 1.f / l_sum : 0.f;  // NaN stays NaN
             const long long part_row =
-                (2ll * blockIdx.x + (w.v0 == 0 ? 1 : 0)) * kPairRows + g * kTile + row;
+                (2ll * blockIdx.x + (w.v0 == 0 ? 1 : 0)) * kPairRows + (dual ? 0 : g * kTile) + row;
             uint16_t* orow = static_cast<uint16_t*>(p.o) + w.b * p.os.b + h * p.os.h + t * p.os.n;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -583,6 +779,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = 0u;
+                }
+                if (merge) {
+                    uint32_t o1[32];
+                    tmem_ld32(tmem + T::COL_O1 + lane_off + 32 * c, o1);
+                    tmem_ld_wait(o1);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * f0 + u2f(o1[i]) * f1);
                 }
                 if (!row_ok) continue;
                 if (finished) {
@@ -603,26 +806,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 else
                     p.stat[part_row] = make_float2(l_sum != 0.f ? m_used : -INFINITY, l_sum);
             }
+            if (merge) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(b_merged);
+            }
             tc_fence_before();  // O_g may be overwritten once this warp arrives on q_full and p_full
         }
     }
 
-    // what the joining kernel finds at the border before this share
-    if (threadIdx.x == 0) {
-        CacheBorder bd;
-        bd.c_first = -1;
-        bd.b = bd.item = bd.q_len = bd.c_last = 0;
-        PromptWalk f(share, pairs);
-        const long long x = share.x;
-        if (f.next(p) && f.v0 > 0) {
-            bd.b = f.b;
-            bd.item = f.pair * p.Hk + f.hk;
-            bd.q_len = f.u.q_len;
-            bd.c_first = static_cast<int>(div_mostly32(x - f.v0, share.share)) + 1;
-            bd.c_last = static_cast<int>(div_mostly32(x - f.v0 + f.u.n - 1, share.share));
-        }
-        p.border[blockIdx.x] = bd;
-    }
     // ---- teardown: all tensor-memory traffic of this CTA is complete ----
     tc_fence_before();
     __syncthreads();
@@ -682,8 +874,15 @@ __global__ void __launch_bounds__(kJoinThreads) cache_prompt_join_kernel(const C
 template <int D>
 cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     using T = PromptTraits<D>;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+    static const cudaError_t attr = [] {
+        cudaFuncAttributes a;
+        cudaError_t e = cudaFuncGetAttributes(&a, cache_prompt_kernel<D>);
+        // the register split draws on what the launch has: with fewer it would wait for ever
+        if (e == cudaSuccess && a.numRegs != kLaunchRegs) e = cudaErrorInvalidKernelImage;
+        return e == cudaSuccess ? cudaFuncSetAttribute(cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       T::SMEM_BYTES)
+                                : e;
+    }();
     if (attr != cudaSuccess) return attr;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

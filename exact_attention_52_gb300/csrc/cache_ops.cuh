@@ -116,4 +116,9 @@ __device__ __forceinline__ float f16_row_scale(float amax) {
     return __uint_as_float(static_cast<uint32_t>(min(max(261 - e, 1), 254)) << 23);
 }
 
+// Row factor times key scale, which turns a product into a score.  Never zero, so
+// that a hidden score of -inf stays one (a row of zeros has a row factor of zero); a
+// product is below 2^24, so the least normal number in place of less moves no score.
+__device__ __forceinline__ float score_factor(float row, float key_scale) { return fmaxf(row * key_scale, 0x1p-126f); }
+
 }  // namespace attn

@@ -145,8 +145,8 @@ __device__ __forceinline__ bool wait_one(uint32_t bar, uint32_t parity, volatile
 
 // Bounded wait that ignores the abort flag: used on the way out to let this
 // thread's own asynchronous copies and MMAs land before the CTA exits.
-static __device__ __noinline__ bool wait_drain_impl(uint32_t bar, uint32_t parity, unsigned int* err,
-                                                     unsigned long long limit, uint32_t site) {
+__device__ __forceinline__ bool wait_drain_loop(uint32_t bar, uint32_t parity, unsigned int* err,
+                                                unsigned long long limit, uint32_t site) {
     const uint64_t t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -155,6 +155,11 @@ static __device__ __noinline__ bool wait_drain_impl(uint32_t bar, uint32_t parit
             return false;
         }
     }
+}
+
+static __device__ __noinline__ bool wait_drain_impl(uint32_t bar, uint32_t parity, unsigned int* err,
+                                                     unsigned long long limit, uint32_t site) {
+    return wait_drain_loop(bar, parity, err, limit, site);
 }
 
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, const DevStatus& st,
@@ -167,9 +172,8 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity, const 
 // leaves only when all lanes saw the phase complete, and a time-out is decided
 // by lane 0 for the whole warp, so the warp never splits before a collective
 // tcgen05.ld/st.
-static __device__ __noinline__ bool wait_warp_impl(uint32_t bar, uint32_t parity,
-                                                    volatile int* abort_flag, unsigned int* err,
-                                                    unsigned long long limit, uint32_t site) {
+__device__ __forceinline__ bool wait_warp_loop(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                               unsigned int* err, unsigned long long limit, uint32_t site) {
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
         const bool ok = mbar_try_wait(bar, parity);
@@ -188,6 +192,12 @@ static __device__ __noinline__ bool wait_warp_impl(uint32_t bar, uint32_t parity
         }
         if (__shfl_sync(0xffffffffu, stop, 0)) return false;
     }
+}
+
+static __device__ __noinline__ bool wait_warp_impl(uint32_t bar, uint32_t parity,
+                                                    volatile int* abort_flag, unsigned int* err,
+                                                    unsigned long long limit, uint32_t site) {
+    return wait_warp_loop(bar, parity, abort_flag, err, limit, site);
 }
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag,

@@ -172,6 +172,29 @@ def test_cache_forward_layouts(layout, token_major, d):
     run_cache(pool, 8, 3, [150, 31], [3, 1], 50, 2, layout=layout)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [2, 70])
+def test_cache_forward_of_zero_and_tiny_rows(T, d):
+    """Query rows of zeros, of subnormals and of one large among tiny numbers; a page whose
+    codes are zeros and whose scale is the least an append writes; hidden scores in all."""
+    import torch
+    pool = Pool(18, 1, 1, d, 16, 12)
+    pool.k[pool.table[0, 3]] = 0
+    pool.ks[pool.table[0, 3]] = 2.0 ** -100
+    q, _ = bf16(pool.rng, (1, 8, T, d))
+    q[:, 0] = 0
+    q[:, 1] *= 2.0 ** -128
+    q[:, 2] *= 2.0 ** -20
+    q[:, 2, :, 5] = 3.0
+    q[:, 3, 1:] = 0
+    qv = q.double().cpu().numpy()
+    for left, sinks in ((-1, 0), (60, 3)):
+        o, lse = api.fwd_cache(q, *pool.dev(), i32([185]), window_left=left, sinks=sinks)
+        check_clean()
+        check_out(o, lse, streaming.cache_forward(qv, pool.k, pool.v, pool.ks, pool.vs, pool.table, [185], [T],
+                                                  d ** -0.5, left, sinks))
+
+
 def test_cache_forward_many_sequences_share_the_device():
     """More items than CTAs, lengths from 0 to long: shares begin and end inside items."""
     rng = np.random.default_rng(5)
