@@ -38,16 +38,16 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kPairRows = 2 * kTile;
 constexpr int kPromptThreads = 512;
 constexpr int kConvWarps = 4;
-// Registers a thread: the launch's 128 are dealt out again, 168 for the softmax (a
-// whole score row), 56 for the MMA issuer's four warps, 120 for the converters.
-constexpr int kLaunchRegs = 128, kSoftmaxRegs = 168, kMmaRegs = 56, kConvRegs = 120;
+// Registers a thread: the launch's 128 are dealt out again, more for the softmax, less
+// for the MMA issuer's four warps.
+constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kMmaRegs = 80, kConvRegs = 128;
 static_assert(2 * kSoftmaxRegs + kMmaRegs + kConvRegs <= 4 * kLaunchRegs, "more registers than the launch has");
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-constexpr float kShift = 4.f;           // weights are 2^(score - m + kShift), f16
-constexpr float kRedoBound = 32768.f;   // a row's tile sum that makes it take its own maximum
+constexpr float kShift = 6.f;  // weights are 2^(score - m + kShift), f16, and
+constexpr float kSlack = 8.f;  // m may be up to kSlack below the largest score: at most 2^14
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t f2u(float f) { return __float_as_uint(f); }
@@ -626,83 +626,81 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 }
                 tc_fence_after();
                 const float4* sc = scales + (tn % T::SCALES) * 8;
-                uint32_t s[4][32];
-                auto load_s = [&]() {
+                // Two passes over the 128 scores, 32 at a time (the next 32 on their way from
+                // tensor memory): the maximum, then the weights.  The loops stay rolled and the
+                // mask is formed from bits: the roles' code does not fit the instruction caches
+                // otherwise (unrolled 1033 us for a call of 700, one pass with the whole row in
+                // registers 715).
+                auto take = [&](int c, uint32_t (&x)[32]) {  // columns 32 c .. 32 c + 31, hidden ones -inf
+                    tmem_ld_wait(x);
+                    if (masked) {  // bit i of `seen`: column 32 c + i
+                        auto below = [&](int n) { n -= 32 * c; return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+                        const uint32_t seen = below(c_hi + 1) & (~below(c_lo) | below(c_sink));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
-                    if (masked) {
-                        // opaque to the compiler, which otherwise forms all 128 comparisons of every
-                        // tile ahead of this branch (1.5 ms for a call of 0.65 ms)
-                        int lo = c_lo, hi = c_hi, sink = c_sink;
-                        asm volatile("" : "+r"(lo), "+r"(hi), "+r"(sink));
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int k = c * 32 + i;
-                                if ((k < lo && k >= sink) || k > hi) s[c][i] = f2u(-INFINITY);
-                            }
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1u)) x[i] = f2u(-INFINITY);
                     }
                 };
+                auto each = [&](auto work) {
+                    uint32_t x[32], y[32];
+                    tmem_ld32(tS, x);
+#pragma unroll 1
+                    for (int c = 0; c < 4; c += 2) {
+                        tmem_ld32(tS + 32 * c + 32, y);
+                        take(c, x);
+                        work(c, x);
+                        if (c == 0) tmem_ld32(tS + 64, x);
+                        take(c + 1, y);
+                        work(c + 1, y);
+                    }
+                };
+                float mx = -INFINITY;
+                each([&](int c, const uint32_t (&x)[32]) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 e = sc[2 * c + h];
+                        float a = fmax3(u2f(x[16 * h]), u2f(x[16 * h + 1]), u2f(x[16 * h + 2]));
+                        float b = fmax3(u2f(x[16 * h + 3]), u2f(x[16 * h + 4]), u2f(x[16 * h + 5]));
+#pragma unroll
+                        for (int i = 6; i < 14; i += 4) {
+                            a = fmax3(a, u2f(x[16 * h + i]), u2f(x[16 * h + i + 1]));
+                            b = fmax3(b, u2f(x[16 * h + i + 2]), u2f(x[16 * h + i + 3]));
+                        }
+                        a = fmaxf(fmax3(a, u2f(x[16 * h + 14]), u2f(x[16 * h + 15])), b);
+                        mx = fmaxf(mx, fmaf(a, score_factor(rq, e.x), e.y));
+                    }
+                });
                 float alpha = 1.f;
                 bool rescale_o = false;
-                auto update_max = [&]() {
-                    float mx = -INFINITY;
+                if (mx > m_used + kSlack) {
+                    alpha = ex2_approx(m_used - mx);  // 0 while m_used is -inf
+                    l_sum *= alpha;
+                    m_used = mx;
+                    rescale_o = j > 0;
+                }
+                float tile_l = 0.f;
+                const float sub = kShift - (m_used == -INFINITY ? 0.f : m_used);
+                each([&](int c, const uint32_t (&x)[32]) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int grp = 0; grp < 8; ++grp) {
-                        const float4 e = sc[grp];
-                        const uint32_t* x = s[grp >> 1] + (grp & 1) * 16;
-                        float a = fmax3(u2f(x[0]), u2f(x[1]), u2f(x[2]));
-#pragma unroll
-                        for (int i = 3; i < 15; i += 2) a = fmax3(a, u2f(x[i]), u2f(x[i + 1]));
-                        mx = fmaxf(mx, fmaf(fmaxf(a, u2f(x[15])), score_factor(rq, e.x), e.y));
-                    }
-                    if (mx > m_used) {
-                        const float a = ex2_approx(m_used - mx);  // 0 while m_used is -inf
-                        alpha *= a;
-                        l_sum *= a;
-                        m_used = mx;
-                        rescale_o = j > 0;
-                    }
-                };
-                uint32_t pk[2][32];
-                float tile_sum, tile_l;
-                auto exp_pass = [&]() {
-                    const float sub = kShift - (m_used == -INFINITY ? 0.f : m_used);
-                    tile_sum = tile_l = 0.f;
-#pragma unroll
-                    for (int grp = 0; grp < 8; ++grp) {
-                        const float4 e = sc[grp];  // the same address in every lane
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 e = sc[2 * c + h];
                         const float f = score_factor(rq, e.x), add = e.y + sub;
-                        const uint32_t* x = s[grp >> 1] + (grp & 1) * 16;
                         float a0 = 0.f, a1 = 0.f;
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             float x0, x1;
-                            ffma2(x0, x1, u2f(x[i]), u2f(x[i + 1]), f, f, add, add);
+                            ffma2(x0, x1, u2f(x[16 * h + i]), u2f(x[16 * h + i + 1]), f, f, add, add);
                             x0 = ex2_approx(x0);
                             x1 = ex2_approx(x1);
-                            // weights rounded to f16 (half a step, 2^-11 relative), finer than the bf16 output
-                            pk[grp >> 2][(grp & 3) * 8 + i / 2] = pack_f16x2(x0, x1);
+                            // f16 (half a step, 2^-11 relative): finer than the bf16 output
+                            pk[8 * h + i / 2] = pack_f16x2(x0, x1);
                             fadd2(a0, a1, a0, a1, x0, x1);
                         }
-                        tile_sum += a0 + a1;
                         tile_l = fmaf(a0 + a1, e.z, tile_l);
                     }
-                };
-                // Against m_used as it is; a tile whose scores rise far above it is done again
-                // with its own maximum (S is still there: no P has been stored).
-#pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    load_s();
-                    if (pass > 0 || __any_sync(0xffffffffu, m_used == -INFINITY)) update_max();
-                    exp_pass();
-                    if (pass > 0 || !__any_sync(0xffffffffu, !(tile_sum <= kRedoBound))) break;
-                }
-                tmem_st32(tS, pk[0]);
-                tmem_st32(tS + 32, pk[1]);
+                    tmem_st16(tS + 16 * c, pk);  // over columns read before
+                });
                 l_sum += tile_l;
                 if (__any_sync(0xffffffffu, rescale_o)) {
                     // PV_g(j-1) has completed: S_g(j) was committed after it
