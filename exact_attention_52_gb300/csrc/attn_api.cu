@@ -223,14 +223,14 @@ BwdLayout bwd_layout(int B, int H, int N, int d, bool split, long long sink_item
     L.split_cnt = L.split_part = L.dsum + round256(rows * sizeof(float));
     L.total = L.split_cnt;
     L.split_cap = L.split_cnt_words = 0;
-    if (split && d == 128) {
+    if (split && (d == 128 || sink_items > 0)) {
         const long long tiles = npad(N) / kTile;
         const long long room = sink_items > 0 ? sink_items * kBwdSinkParts
                                               : static_cast<long long>(B) * H * tiles * (tiles < 10 ? tiles : 10);
         const long long most = sink_items > 0 ? kBwdSinkCap : kBwdSplitCap;
         L.split_cap = static_cast<int>(room < most ? room : most);
         if (L.split_cap > 0) {
-            L.split_cnt_words = sink_items > 0 ? L.split_cap * 8 : kBwdSplitCntWords;
+            L.split_cnt_words = sink_items > 0 ? 0 : kBwdSplitCntWords;
             L.split_part = L.split_cnt + round256(L.split_cnt_words * sizeof(unsigned));
             L.total = L.split_part + round256(static_cast<size_t>(L.split_cap) * 2 * kTile * d * sizeof(float));
         }
@@ -402,7 +402,7 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
                          const void* v, const Strides& vs, const void* dout, const Strides& dos,
                          void* dk, const Strides& dks, void* dv, const Strides& dvs, void* workspace,
                          int B, int H, int Hk, int N, int d, float scale, int win_left, int win_right,
-                         int sinks, bool split, attn_stream_t stream) {
+                         int sinks, bool split, attn_stream_t stream, DqConvertParams* sink = nullptr) {
     for (const void* p : {q, k, v, dout, static_cast<const void*>(dk), static_cast<const void*>(dv)})
         if (!aligned16(p)) return ATTN_ERR_INVALID;
     for (const Strides* st : {&qs, &ks, &vs, &dos, &dks, &dvs})
@@ -440,9 +440,19 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
     bp.sink_tiles = sink_tiles_of(sinks);
     bp.cs = scale * 1.44269504088896340736f;
     bp.scale = scale;
-    bp.split_base = bp.BHk * bp.n_kv;  // the launcher decides on a split
-    bp.split_parts = 1;
     bp.split_cap = c.split_cap;
+    if (bwd_sink_parts(&bp) != cudaSuccess) return ATTN_ERR_CUDA;  // without sinks the launcher decides on a split
+    if (sink != nullptr && bp.split_parts > 1) {  // for the conversion
+        sink->sink_part = c.split_part;
+        sink->parts = bp.split_parts;
+        sink->sink_items = static_cast<int>(sink_items_of(B, Hk, sinks));
+        sink->BHk = bp.BHk;
+        sink->Hk = Hk;
+        sink->dk = dk;
+        sink->dv = dv;
+        sink->dks = dks;
+        sink->dvs = dvs;
+    }
     bp.split_part = c.split_part;
     bp.split_cnt = c.split_cnt;
     bp.dkv_v8 = rows_v8(dk, dks) && rows_v8(dv, dvs);
@@ -454,12 +464,13 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
 }
 
 attn_status dq_convert_run(void* dq, const Strides& dqs, void* workspace, int B, int H, int N, int d,
-                           float scale, attn_stream_t stream) {
+                           float scale, attn_stream_t stream, const DqConvertParams* sink = nullptr) {
     if (!aligned16(dq) || !strides_ok(dqs, 2)) return ATTN_ERR_INVALID;
     BwdCall c;
     attn_status rc = bwd_prepare(workspace, B, H, N, d, scale, 0, false, 0, &c);
     if (rc != ATTN_OK) return rc;
-    DqConvertParams cp;
+    DqConvertParams cp = {};
+    if (sink != nullptr) cp = *sink;
     cp.dq_acc = c.dq_acc;
     cp.dq = dq;
     cp.dqs = dqs;
@@ -494,13 +505,14 @@ attn_status bwd_run(const void* q, const Strides& qs, const void* k, const Strid
         if (!strides_ok(*st, 2)) return ATTN_ERR_INVALID;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return ATTN_ERR_INVALID;
+    DqConvertParams sink = {};
     if ((rc = bwd_pre_run(o, os, dout, dos, lse, workspace, B, H, N, d, split, sink_items_of(B, Hk, sinks),
                           stream)) != ATTN_OK)
         return rc;
     if ((rc = bwd_main_run(q, qs, k, ks, v, vs, dout, dos, dk, dks, dv, dvs, workspace, B, H, Hk, N, d,
-                           scale, win_left, win_right, sinks, split, stream)) != ATTN_OK)
+                           scale, win_left, win_right, sinks, split, stream, &sink)) != ATTN_OK)
         return rc;
-    return dq_convert_run(dq, dqs, workspace, B, H, N, d, scale, stream);
+    return dq_convert_run(dq, dqs, workspace, B, H, N, d, scale, stream, &sink);
 }
 
 Strides from_abi(const attn_strides_t& s) {

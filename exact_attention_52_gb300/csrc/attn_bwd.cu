@@ -151,13 +151,41 @@ __global__ void __launch_bounds__(kAuxThreads) bwd_pre_kernel(const BwdPreParams
 // ---------------------------------------------------------------------------
 // 3. dQ conversion: one block per kAuxRows rows of one head, 8 elements a thread
 // ---------------------------------------------------------------------------
-template <int D>
+// SINKS: further blocks, kAuxRows rows each, add the parts of the sink tiles' dV and dK
+// in their order.
+template <int D, bool SINKS>
 __global__ void __launch_bounds__(kAuxThreads) dq_convert_kernel(const DqConvertParams p) {
     pdl_wait();  // launched as a dependent of the main kernel: its reductions must be done
     constexpr int TPR = D / 8;
     constexpr int RPP = kAuxThreads / TPR;
     constexpr int PASSES = kAuxRows / RPP;
     const int blocks_per_head = p.Npad / kAuxRows;
+    if constexpr (SINKS) {
+        const int extra = static_cast<int>(blockIdx.x) - p.BH * blocks_per_head;
+        if (extra >= 0) {
+            constexpr int PER = kTile / kAuxRows;
+            const int item = extra / (2 * PER), h = extra / PER & 1;  // item: sink tile item / BHk of head item % BHk
+            const int kv_bh = item % p.BHk, j = item / p.BHk, c = threadIdx.x % TPR;
+            const Strides& ds = h ? p.dks : p.dvs;
+            uint16_t* out = static_cast<uint16_t*>(h ? p.dk : p.dv) + (kv_bh / p.Hk) * ds.b + (kv_bh % p.Hk) * ds.h + c * 8;
+            const float f = h ? p.scale : 1.f;
+            for (int r = extra % PER * kAuxRows + threadIdx.x / TPR, k = 0; k < PASSES; ++k, r += RPP) {
+                const int n = j * kTile + r;
+                if (n >= p.N) break;
+                float a[8] = {};
+                const float* src = p.sink_part + ((static_cast<size_t>(item) * p.parts * 2 + h) * kTile + r) * D + c * 8;
+#pragma unroll 4
+                for (int q = 0; q < p.parts; ++q, src += 2 * kTile * D) {
+                    const float4 x = reinterpret_cast<const float4*>(src)[0], y = reinterpret_cast<const float4*>(src)[1];
+                    a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+                    a[4] += y.x, a[5] += y.y, a[6] += y.z, a[7] += y.w;
+                }
+                st_global_v4(out + n * ds.n, pack_bf16x2(a[0] * f, a[1] * f), pack_bf16x2(a[2] * f, a[3] * f),
+                             pack_bf16x2(a[4] * f, a[5] * f), pack_bf16x2(a[6] * f, a[7] * f));
+            }
+            return;
+        }
+    }
     const int bh = static_cast<int>(blockIdx.x / blocks_per_head);
     const int n0 = static_cast<int>(blockIdx.x % blocks_per_head) * kAuxRows;
     const int b = bh / p.H, h = bh - b * p.H;
@@ -198,9 +226,11 @@ struct BwdWork {
     int parts;           // parts of the item (1: whole)
     int tt0, bh_first;   // (tile step, query head) of the first step
 
-    // One CTA per item (d = 64): the long sink items first.
-    __device__ explicit BwdWork(const BwdParams& prm)
-        : BwdWork(prm, static_cast<int>(SINKS ? gridDim.x - 1 - blockIdx.x : blockIdx.x)) {}
+    // One CTA per item (d = 64); with sinks the last ones first: the sink tiles' parts.
+    __device__ static BwdWork of_block(const BwdParams& prm) {
+        if constexpr (SINKS) return split_at(prm, static_cast<int>(gridDim.x - 1 - blockIdx.x));
+        else return BwdWork(prm, static_cast<int>(blockIdx.x));
+    }
 
     // Work item `item` of the launch's numbering (items = key tiles of every
     // key/value head), whole.
@@ -281,6 +311,24 @@ struct BwdWork {
     }
 };
 
+// fp32 rows of dV (h = 0) or unscaled dK (h = 1) of a part of a sink tile's item, to
+// its slot of the workspace: row r of this lane, tensor memory at tsrc.  The
+// conversion kernel adds the parts (by the last part to arrive, as split_part_epilogue
+// does, 16 parts took 64 us).
+template <int D>
+__device__ __noinline__ void sink_part_store(float* part, int slot, int h, int r, uint32_t tsrc) {
+    float* dst = part + ((static_cast<size_t>(slot) * 2 + h) * kTile + r) * D;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tsrc + 32 * c, o);
+        tmem_ld_wait(o);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+            st_global_v4(dst + c * 32 + 4 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // 2. main kernel
 // ---------------------------------------------------------------------------
@@ -320,8 +368,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     }
 
     const int N = prm.N;
-    const BwdWork<SINKS> w(prm);
-    const int j = w.j, n_qh = w.n_qh, q_bh0 = w.q_bh0, b_idx = w.b_idx, hk_idx = w.hk_idx,
+    const BwdWork<SINKS> w = BwdWork<SINKS>::of_block(prm);
+    const int j = w.j, n_qh = w.n_qh, b_idx = w.b_idx, hk_idx = w.hk_idx,
               bH0 = w.bH0, n_steps = w.n_steps;
     auto q_tile = [&](int tt) { return w.q_tile(tt); };
 
@@ -376,7 +424,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 hk_idx, b_idx);
             }
             int t = 0;
-            int tt = 0, bh = q_bh0;  // step t = (head bh - q_bh0) * n_qh + tt
+            int tt = w.tt0, bh = w.bh_first;  // step t = (head bh - q_bh0) * n_qh + tt
             for (; t < n_steps; ++t, ++tt) {
                 if (tt == n_qh) {
                     tt = 0;
@@ -517,7 +565,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int sw = r & 7;
         const uint32_t b_sf = b_s_full + 8u * h, b_pf = b_p_full + 8u * h;
         bool ok = true;
-        for (int t = 0, tt = 0; t < n_steps; ++t, ++tt) {
+        for (int t = 0, tt = w.tt0; t < n_steps; ++t, ++tt) {
             if (tt == n_qh) tt = 0;
             const int s = t % T::STAGES;
             const int i = q_tile(tt);
@@ -605,6 +653,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const uint32_t tsrc = tmem + (h ? T::COL_DK : T::COL_DV) + lane_off;
             uint8_t* dst = static_cast<uint8_t*>(h ? prm.dk : prm.dv) + roff;
             const float f = h ? prm.scale : 1.f;
+            if (SINKS && w.slot >= 0) sink_part_store<D>(prm.split_part, w.slot, h, r, tsrc);
+            else
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -634,7 +684,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool leader = (warp == 8 && lane == 0);
         constexpr int SLOTS_PER_BUF = T::TILE_BYTES / (kTile * 128);  // 16 KB boxes per buffer
         bool ok = true;
-        int tt = 0, bh = q_bh0;
+        int tt = w.tt0, bh = w.bh_first;
         if constexpr (D == 128) {
             // dQ^T_h sits in tensor memory with lane = feature, column = query, so one
             // warp-wide fp32 reduction covers 32 consecutive features of one query row:
@@ -1451,7 +1501,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t tsrc = tmem + (h ? T::COL_DK : T::COL_DV) + lane_off;
         uint8_t* dst = static_cast<uint8_t*>(h ? prm.dk : prm.dv) + roff;
         const float f = h ? prm.scale : 1.f;
-        if (MODE != 0 && w.slot >= 0) {
+        if (MODE == 3 && w.slot >= 0) {
+            sink_part_store<D>(prm.split_part, w.slot, h, r, tsrc);
+        } else if (MODE != 0 && MODE != 3 && w.slot >= 0) {
             split_part_epilogue(prm.split_part, prm.split_cnt, w.slot, w.parts, h, wq, r, tsrc, dst, row_ok, f);
         } else {
             const bool empty = w.n_steps == 0;
@@ -1698,7 +1750,8 @@ cudaError_t launch_bwd_main_impl(const CUtensorMap& tq, const CUtensorMap& tk, c
     static const cudaError_t attr = cudaFuncSetAttribute(
         bwd_main_kernel<D, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
     if (attr != cudaSuccess) return attr;
-    const long long grid = static_cast<long long>(p.BHk) * p.n_kv;
+    long long grid = static_cast<long long>(p.BHk) * p.n_kv;
+    if (SINKS) grid = p.split_base + (grid - p.split_base) * p.split_parts;
     const cudaError_t dbg = dbg_set_word(p.st.word, stream);
     if (dbg != cudaSuccess) return dbg;
     bwd_main_kernel<D, SINKS><<<static_cast<unsigned>(grid), kBwdThreads, T::SMEM_BYTES, stream>>>(tq, tk, tv, tdo,
@@ -1707,6 +1760,36 @@ cudaError_t launch_bwd_main_impl(const CUtensorMap& tq, const CUtensorMap& tk, c
 }
 
 }  // namespace
+
+// Sinks: a sink tile's item visits every later query tile (64 steps a query head at
+// N8192 against 9 of a 1024-key window), so these items are split into parts of a
+// quarter of the SMs' mean or less, but of kSplitMinPartSteps steps at least.
+cudaError_t bwd_sink_parts(BwdParams* p) {
+    p->split_base = p->BHk * p->n_kv;
+    p->split_parts = 1;
+    if (p->sinks == 0 || p->split_cap == 0) return cudaSuccess;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const long long G = p->H / p->Hk, items = static_cast<long long>(p->BHk) * p->n_kv;
+    const long long sink_items = static_cast<long long>(p->BHk) * p->sink_tiles, steps = G * p->n_kv;
+    const long long win_tiles = (static_cast<long long>(p->win_left) + kTile - 1) / kTile + 1;
+    const long long plain = G * (items - sink_items) * (win_tiles < p->n_kv ? win_tiles : p->n_kv);
+    const long long mean = (plain + sink_items * steps) / sms;
+    const long long part = mean / 4 > kSplitMinPartSteps ? mean / 4 : kSplitMinPartSteps;
+    long long parts = (steps + part - 1) / part;
+    if (parts > steps / kSplitMinPartSteps) parts = steps / kSplitMinPartSteps;
+    // the last sink tile has the fewest steps: a part keeps one at least
+    const long long least = G * (p->n_kv - p->sink_tiles + 1);
+    for (long long most : {least, static_cast<long long>(kBwdSinkParts), p->split_cap / sink_items})
+        if (parts > most) parts = most;
+    if (parts >= 2) {
+        p->split_base = static_cast<int>(items - sink_items);
+        p->split_parts = static_cast<int>(parts);
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream) {
     if (p.Npad % kAuxRows != 0) return cudaErrorInvalidValue;
@@ -1732,8 +1815,14 @@ cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (p.D == 64) return cudaLaunchKernelEx(&cfg, dq_convert_kernel<64>, p);
-    if (p.D == 128) return cudaLaunchKernelEx(&cfg, dq_convert_kernel<128>, p);
+    if (p.parts > 1) {
+        cfg.gridDim.x += static_cast<unsigned>(p.sink_items) * 2u * (kTile / kAuxRows);
+        if (p.D == 64) return cudaLaunchKernelEx(&cfg, dq_convert_kernel<64, true>, p);
+        if (p.D == 128) return cudaLaunchKernelEx(&cfg, dq_convert_kernel<128, true>, p);
+        return cudaErrorInvalidValue;
+    }
+    if (p.D == 64) return cudaLaunchKernelEx(&cfg, dq_convert_kernel<64, false>, p);
+    if (p.D == 128) return cudaLaunchKernelEx(&cfg, dq_convert_kernel<128, false>, p);
     return cudaErrorInvalidValue;
 }
 
@@ -1776,8 +1865,13 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
         // splitting 16-step items in two made B1 H4 N2048 19 % slower, 32-step
         // ones (B1 H2 N4096) 7 % faster.
         BwdParams pp = p;
-        pp.split_base = static_cast<int>(items);
-        pp.split_parts = 1;
+        if (p.sinks == 0) {
+            pp.split_base = static_cast<int>(items);
+            pp.split_parts = 1;
+        } else {
+            const long long all = p.split_base + (items - p.split_base) * p.split_parts;
+            grid = all < sms ? all : sms;
+        }
         const long long rem = items < sms ? items : items % grid;
         const long long steps = static_cast<long long>(p.H / p.Hk) * p.n_kv;
         if (rem > 0 && p.causal == 0 && p.win_left < 0 && p.win_right < 0 && p.split_cap > 0) {
@@ -1788,28 +1882,6 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                 pp.split_base = static_cast<int>(items - rem);
                 pp.split_parts = static_cast<int>(parts);
                 if (items < sms) grid = items * parts;
-            }
-        }
-        // Sinks: a sink tile's item visits every later query tile (64 steps at N8192 against
-        // 9 of a 1024-key window), so these items are split as well, into parts of a quarter
-        // of the CTAs' mean or less, but of kSplitMinPartSteps at least.
-        if (p.sinks > 0 && p.split_cap > 0) {
-            const long long G = p.H / p.Hk, sink_items = static_cast<long long>(p.BHk) * p.sink_tiles;
-            const long long win_tiles = (static_cast<long long>(p.win_left) + kTile - 1) / kTile + 1;
-            const long long plain = G * (items - sink_items) * (win_tiles < p.n_kv ? win_tiles : p.n_kv);
-            const long long mean = (plain + G * sink_items * p.n_kv) / sms;
-            const long long part = mean / 4 > kSplitMinPartSteps ? mean / 4 : kSplitMinPartSteps;
-            long long parts = (steps + part - 1) / part;
-            if (parts > steps / kSplitMinPartSteps) parts = steps / kSplitMinPartSteps;
-            // the last sink tile has the fewest steps: a part keeps one at least
-            const long long least = G * (p.n_kv - p.sink_tiles + 1);
-            if (parts > least) parts = least;
-            if (parts * sink_items > p.split_cap) parts = p.split_cap / sink_items;
-            if (parts >= 2) {
-                pp.split_base = static_cast<int>(items - sink_items);
-                pp.split_parts = static_cast<int>(parts);
-                const long long all = pp.split_base + sink_items * parts;
-                grid = all < sms ? all : sms;
             }
         }
         const cudaError_t dbg = dbg_set_word(p.st.word, stream);

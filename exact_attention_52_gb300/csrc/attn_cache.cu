@@ -249,7 +249,7 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // so that the weights given to the products are 2^(score + log2 sv - m) with the
 // running maximum m taken over score + log2 sv, and the sum of the probabilities
 // takes them back by 1 / sv.  m is raised, and the output rescaled, only when a
-// score passes it by more than kSlack; a weight is lost to f16's underflow below
+// score passes it by more than kWeightSlack; a weight is lost to f16's underflow below
 // 2^-31 of the largest.
 //
 // What belongs to a tile and not to a lane (its page's address and scales, whether
@@ -274,9 +274,6 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // each other (each lane copying its own fragments' bytes reached 5.3 TB/s, whole rows
 // 7.0), and the 16-byte pieces of a row are placed so that neither fragment's reads
 // meet in a bank (chunk_at).
-constexpr int kShift = 7;    // weights are 2^(score - m + kShift) and
-constexpr int kSlack = 8;    // m may be up to kSlack below the largest score: at most 2^15
-
 template <int D, int NT>
 struct DecodeTraits {
     static constexpr int ROWS = 8 * NT;
@@ -560,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                         sf[u][n][2 + r] = fmaf(sf[u][n][2 + r], f, t_lsv[u]);
                     }
                     const float mx = fmaxf(fmaxf(sf[0][n][r], sf[0][n][2 + r]), fmaxf(sf[1][n][r], sf[1][n][2 + r]));
-                    passes |= mx > m[n][r] + kSlack;
+                    passes |= mx > m[n][r] + kWeightSlack;
                 }
             if (__any_sync(0xffffffffu, passes)) {
 #pragma unroll
@@ -585,8 +582,8 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float sub0 = kShift - (m[n][0] == -INFINITY ? 0.f : m[n][0]);
-                const float sub1 = kShift - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
+                const float sub0 = kWeightShift - (m[n][0] == -INFINITY ? 0.f : m[n][0]);
+                const float sub1 = kWeightShift - (m[n][1] == -INFINITY ? 0.f : m[n][1]);
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const float e0 = ex2_approx(sf[u][n][0] + sub0), e1 = ex2_approx(sf[u][n][1] + sub1);
@@ -725,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                 for (int e = 0; e < CPT / 4; ++e) *reinterpret_cast<uint2*>(dst + 4 * e) = make_uint2(pk[2 * e], pk[2 * e + 1]);
                 if (c0 == 0)
                     p.lse[(static_cast<long long>(b) * p.H + a.h) * p.T + a.t] =
-                        ll != 0.f ? (mm - kShift + log2f(ll)) * kLn2 : INFINITY;
+                        ll != 0.f ? (mm - kWeightShift + log2f(ll)) * kLn2 : INFINITY;
             } else {
                 float* dst = p.part + (static_cast<long long>(slot) * T::ROWS + r) * D + c0;
 #pragma unroll
@@ -739,11 +736,12 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
     }
 }
 
-// Joins an item's unfinished segments, in the order of the keys: with M the
-// largest of their maxima, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  Block
-// c - 1 stands for the border before share c; the borders inside an item divide its
-// rows among them.  A row is joined by one warp where it has few segments, else by
-// the whole block, the segments divided among the warps.
+// Joins an item's unfinished segments (of either cache attention kernel), in the
+// order of the keys: with M the largest of their maxima, O = sum 2^(m_i - M) O_i /
+// sum 2^(m_i - M) l_i.  Blocks (c - 1, *) stand for the border before share c; the
+// borders inside an item divide its rows among them.  A row is joined by one warp
+// where it has few segments, else by the whole block, the segments divided among the
+// warps.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinAtOnce = 8;  // segments whose loads go out together
 
@@ -753,6 +751,7 @@ struct Joined {
     static constexpr int E = D / 32;
     float m = -INFINITY, l = 0.f, o[E] = {};
     __device__ void add(float sm, float sl, const float (&y)[E]) {
+        if (sm == -INFINITY && sl == 0.f) return;  // a segment in which the row sees no key: no output either
         const float n = fmaxf(m, sm);
         const float a = m == -INFINITY ? 0.f : ex2_approx(m - n), w = sm == -INFINITY ? 0.f : ex2_approx(sm - n);
         m = n;
@@ -811,9 +810,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
             *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(x.o[e] * inv, x.o[e + 1] * inv);
         if (lane == 0)
             p.lse[(static_cast<long long>(bd.b) * p.H + a.h) * p.T + a.t] =
-                x.l != 0.f ? (x.m - kShift + log2f(x.l)) * kLn2 : INFINITY;
+                x.l != 0.f ? (x.m - kWeightShift + log2f(x.l)) * kLn2 : INFINITY;
     };
-    const int mine = c - bd.c_first, borders = n - 1;
+    const int mine = (c - bd.c_first) * static_cast<int>(gridDim.y) + blockIdx.y, borders = (n - 1) * static_cast<int>(gridDim.y);
     if (n <= 2 * kJoinAtOnce) {
         for (int r = mine + borders * warp; r < rows; r += borders * kJoinWarps) write(r, join(r, 0, n));
         return;
@@ -849,17 +848,7 @@ cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
     p.grid = sms * T::CTAS_PER_SM < kCacheGridMax ? sms * T::CTAS_PER_SM : kCacheGridMax;
     cache_decode_kernel<D, NT><<<p.grid, kThreads, T::SMEM, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.grid == 1) return e;
-    cudaLaunchAttribute pdl;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = stream;
-    cfg.attrs = &pdl;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<D>, p);
+    return e != cudaSuccess ? e : launch_cache_join(p, 1, stream);
 }
 
 template <int D>
@@ -874,6 +863,23 @@ cudaError_t launch_decode_d(const CacheFwdParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream) {
+    if (p.grid == 1) return cudaSuccess;  // no border
+    // a programmatic dependent of the attention kernel before it
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cfg.attrs = &pdl;
+    cfg.numAttrs = 1;
+    if (p.D == 64) return cudaLaunchKernelEx(&cfg, cache_join_kernel<64>, p);
+    if (p.D == 128) return cudaLaunchKernelEx(&cfg, cache_join_kernel<128>, p);
+    return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream) {
     if (p.D == 64) return launch_decode_d<64>(p, stream);

@@ -46,8 +46,6 @@ template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-constexpr float kShift = 6.f;  // weights are 2^(score - m + kShift), f16, and
-constexpr float kSlack = 8.f;  // m may be up to kSlack below the largest score: at most 2^14
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t f2u(float f) { return __float_as_uint(f); }
@@ -554,7 +552,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             const long long x = w.s.x;
             if (next_segment(p, walk) && w.v0 > 0) {
                 bd.b = w.b;
-                bd.item = w.pair * p.Hk + w.hk;
+                bd.item = w.hk * ((w.u.rows + kPairRows - 1) / kPairRows) + w.pair;
                 bd.q_len = w.u.q_len;
                 bd.c_first = static_cast<int>(div_mostly32(x - w.v0, w.s.share)) + 1;
                 bd.c_last = static_cast<int>(div_mostly32(x - w.v0 + w.u.n - 1, w.s.share));
@@ -609,7 +607,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             }
 
             float m_used = -INFINITY;  // running maximum of score + log2 sv (log2 units), possibly stale
-            float l_sum = 0.f;         // sum of 2^(score - m_used + kShift) (value scales taken back out)
+            float l_sum = 0.f;         // sum of 2^(score - m_used + kWeightShift) (value scales taken back out)
             for (int j = 0; j < n; ++j) {
                 // Scales of key tile j.  Its entry is written again for the tile SCALES further
                 // on, once that tile's K slot is free: the one of V(j + 1) (five slots, four
@@ -672,14 +670,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 });
                 float alpha = 1.f;
                 bool rescale_o = false;
-                if (mx > m_used + kSlack) {
+                if (mx > m_used + kWeightSlack) {
                     alpha = ex2_approx(m_used - mx);  // 0 while m_used is -inf
                     l_sum *= alpha;
                     m_used = mx;
                     rescale_o = j > 0;
                 }
                 float tile_l = 0.f;
-                const float sub = kShift - (m_used == -INFINITY ? 0.f : m_used);
+                const float sub = kWeightShift - (m_used == -INFINITY ? 0.f : m_used);
                 each([&](int c, const uint32_t (&x)[32]) {
                     uint32_t pk[16];
 #pragma unroll
@@ -800,7 +798,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             if (row_ok) {
                 if (finished)
                     p.lse[(static_cast<long long>(w.b) * p.H + h) * p.T + t] =
-                        l_sum != 0.f ? (m_used - kShift + log2f(l_sum)) * kLn2 : INFINITY;
+                        l_sum != 0.f ? (m_used - kWeightShift + log2f(l_sum)) * kLn2 : INFINITY;
                 else
                     p.stat[part_row] = make_float2(l_sum != 0.f ? m_used : -INFINITY, l_sum);
             }
@@ -819,53 +817,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     if (warp == 8) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
-    }
-}
-
-// Joins unfinished segments row by row (one warp a row), in the order of the keys:
-// with M the largest of their maxima, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
-// The borders inside an item, and gridDim.y blocks each, divide its rows.
-constexpr int kJoinThreads = 256;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) cache_prompt_join_kernel(const CacheFwdParams p) {
-    constexpr int E = D / 32, W = kJoinThreads / 32;
-    const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait();
-    const CacheBorder bd = p.border[c];
-    if (bd.c_first < 0) return;
-    const int G = p.H / p.Hk, pair = bd.item / p.Hk, hk = bd.item - pair * p.Hk;
-    const int rows = min(kPairRows, bd.q_len * G - pair * kPairRows);
-    const int n = bd.c_last - bd.c_first + 2, borders = n - 1;
-    const int first = ((c - bd.c_first) * static_cast<int>(gridDim.y) + blockIdx.y) * W + warp;
-    for (int r = first; r < rows; r += borders * static_cast<int>(gridDim.y) * W) {
-        float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
-        for (int i = 0; i < n; ++i) {
-            const long long at = (2ll * (bd.c_first - 1 + i) + (i == 0 ? 1 : 0)) * kPairRows + r;
-            const float2 st = p.stat[at];
-            if (st.x == -INFINITY && st.y == 0.f) continue;  // no key of it seen
-            const float* src = p.part + at * D + lane * E;
-            const float x = fmaxf(m, st.x), a = m == -INFINITY ? 0.f : ex2_approx(m - x), f = ex2_approx(st.x - x);
-            m = x;
-            l = l * a + st.y * f;
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 y = *reinterpret_cast<const float2*>(src + e);
-                o[e] = o[e] * a + y.x * f;
-                o[e + 1] = o[e + 1] * a + y.y * f;
-            }
-        }
-        const int row = pair * kPairRows + r, t = row / G, h = hk * G + row - t * G;
-        const float inv = l != 0.f ? 1.f / l : 0.f;
-        uint16_t* dst = static_cast<uint16_t*>(p.o) + bd.b * p.os.b + h * p.os.h + t * p.os.n + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-            *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-        if (lane == 0)
-            p.lse[(static_cast<long long>(bd.b) * p.H + h) * p.T + t] =
-                l != 0.f ? (m - kShift + log2f(l)) * kLn2 : INFINITY;
     }
 }
 
@@ -893,17 +844,7 @@ cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     if ((e = dbg_set_word(p.st.word, stream)) != cudaSuccess) return e;
     cache_prompt_kernel<D><<<p.grid, kPromptThreads, T::SMEM_BYTES, stream>>>(p, pairs);
     e = cudaGetLastError();
-    if (e != cudaSuccess || p.grid == 1) return e;
-    cudaLaunchAttribute pdl;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.grid - 1), 8);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &pdl;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_prompt_join_kernel<D>, p);
+    return e != cudaSuccess ? e : launch_cache_join(p, 8, stream);
 }
 
 }  // namespace

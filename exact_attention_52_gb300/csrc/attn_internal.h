@@ -75,9 +75,9 @@ struct BwdPreParams {
 // its own and writes the item's dV and dK.  At most kBwdSplitCap parts.
 constexpr int kBwdSplitCap = 160;
 constexpr int kBwdSplitCntWords = kBwdSplitCap * 8;  // [item slot][dV, dK][4 warp slices]
-// With sinks the items of the sink tiles are split the same way, into at most
-// kBwdSinkParts parts each and kBwdSinkCap in all.
-constexpr int kBwdSinkParts = 16;
+// With sinks the items of the sink tiles are split the same way (d = 64 too), into at
+// most kBwdSinkParts parts each and kBwdSinkCap in all; the conversion kernel adds them.
+constexpr int kBwdSinkParts = 64;
 constexpr int kBwdSinkCap = 512;
 
 struct BwdParams {
@@ -105,7 +105,7 @@ struct BwdParams {
     int split_parts;
     int split_cap;        // parts the workspace has room for (0: no split possible)
     float* split_part;    // fp32 [part][dV, dK][128 rows][D]
-    unsigned* split_cnt;  // kBwdSplitCntWords counters (sinks: 8 per part), zero at launch
+    unsigned* split_cnt;  // kBwdSplitCntWords counters, zero at launch
     int dkv_v8;           // every dK and dV row starts on a 32-byte boundary: 32-byte stores
     DevStatus st;
 };
@@ -116,6 +116,12 @@ struct DqConvertParams {
     Strides dqs;
     int N, Npad, BH, H, D;
     float scale;
+    // Parts of the sink tiles' dV and dK (parts > 1), see BwdParams::split_part
+    const float* sink_part;
+    int parts, sink_items, BHk, Hk;
+    void* dk;
+    void* dv;
+    Strides dks, dvs;
 };
 
 // Paged 8-bit key/value cache (attn_cache_t, checked and with the page size as a
@@ -186,8 +192,11 @@ cudaError_t launch_splitkv_combine(const CombineParams& p, cudaStream_t stream);
 cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const CUtensorMap& tdo, const CUtensorMap& tdq,
                             const BwdParams& p, cudaStream_t stream);
+// Sets split_base and split_parts of a backward with sinks (of any other: none).
+cudaError_t bwd_sink_parts(BwdParams* p);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream);
 cudaError_t launch_cache_prompt(const CacheFwdParams& p, cudaStream_t stream);
 cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream);
 cudaError_t launch_wait_selftest(DevStatus st, cudaStream_t stream);

@@ -11,6 +11,11 @@
 
 namespace attn {
 
+// Softmax weights of the cache attention are 2^(score - m + kWeightShift), rounded to
+// f16; m may be up to kWeightSlack below the largest score, so a weight is at most 2^15,
+// and one is lost to underflow below 2^-31 of the largest.
+constexpr float kWeightShift = 7.f, kWeightSlack = 8.f;
+
 // The new queries of one sequence and the keys they see.  Query t of q_len sits
 // at position len - q_len + t; key j is visible to position p iff j <= p and
 // (left < 0, or j >= p - left, or j < sinks).  Keys are walked in blocks of TB
