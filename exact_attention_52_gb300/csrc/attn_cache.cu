@@ -5,6 +5,8 @@
 // one fp32 scale per page, head and tensor: the value is scale * code.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "attn_internal.h"
 #include "cache_ops.cuh"
 #include "ptx.cuh"
@@ -43,7 +45,7 @@ __device__ __forceinline__ float append_scale(float amax) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const CacheAppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const CacheAppendParams p) {
     constexpr int TPR = D / 8;  // threads per token: 8 elements each
     constexpr int RPP = kAppendThreads / TPR;
     const int hk = blockIdx.y, b = blockIdx.z >> 1;
@@ -72,11 +74,22 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
     float* scale = (is_v ? p.c.v_scale : p.c.k_scale) + static_cast<long long>(pid) * p.Hk + hk;
     const float was = *scale;
 
+    // The first kHeld tokens of each thread stay in registers between the two looks at them.
+    constexpr int kHeld = 8;
+    uint4 held[kHeld];
     float amax = 0.f;
-    for (int pos = lo + rr; pos < hi; pos += RPP) {
-        const uint4 w = *reinterpret_cast<const uint4*>(x + (pos - first) * xs.n);
+    auto look = [&](const uint4& w) {
         for (uint32_t u : {w.x, w.y, w.z, w.w}) amax = fmaxf(amax, fmaxf(finite_abs(bf16lo(u)), finite_abs(bf16hi(u))));
+    };
+    const int n = hi - lo;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        held[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr + k * RPP < n) held[k] = __ldcs(reinterpret_cast<const uint4*>(x + (lo + rr + k * RPP - first) * xs.n));
     }
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) look(held[k]);
+    for (int t = rr + kHeld * RPP; t < n; t += RPP) look(*reinterpret_cast<const uint4*>(x + (lo + t - first) * xs.n));
     // Magnitudes order as their bit patterns: one integer maximum per warp.
     __shared__ uint32_t warp_max[kAppendThreads / 32];
     const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
@@ -84,7 +97,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
     __syncthreads();  // and every thread has read the old scale
     amax = __uint_as_float(max(max(warp_max[0], warp_max[1]), max(warp_max[2], warp_max[3])));
     const int old = lo - pg * page;  // tokens that the page holds already
-    const bool keep = old > 0 && amax <= 448.f * was;
+    const bool keep = old > 0 && was >= __uint_as_float((kMinScaleExp + 127) << 23) && amax <= 448.f * was;
     const float s = keep ? was : append_scale(amax);
     if (old > 0 && !keep) {
         const float f = was > 0.f ? was / s : 0.f;
@@ -106,12 +119,26 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
             *at = make_uint2(r[0], r[1]);
         }
     }
-    for (int pos = lo + rr; pos < hi; pos += RPP) {
-        const uint4 w = *reinterpret_cast<const uint4*>(x + (pos - first) * xs.n);
-        const uint32_t a = pack_e4m3x4(bf16lo(w.x) / s, bf16hi(w.x) / s, bf16lo(w.y) / s, bf16hi(w.y) / s);
-        const uint32_t c = pack_e4m3x4(bf16lo(w.z) / s, bf16hi(w.z) / s, bf16lo(w.w) / s, bf16hi(w.w) / s);
-        *reinterpret_cast<uint2*>(codes + (pos - pg * page) * cs.n) = make_uint2(a, c);
-    }
+    // x / s rounded once: a power of two's inverse is exact; for another scale (one that was
+    // there) the remainder of the product puts it right.  Beyond 448 the code saturates.
+    const float inv = 1.f / s;
+    auto quotient = [&](float v) {
+        const float q = v * inv;
+        return fabsf(q) <= 448.f ? fmaf(fmaf(-q, s, v), inv, q) : q;
+    };
+    auto put = [&](int t, const uint4& w) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t c[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            c[i] = pack_e4m3x4(quotient(bf16lo(u[2 * i])), quotient(bf16hi(u[2 * i])), quotient(bf16lo(u[2 * i + 1])),
+                               quotient(bf16hi(u[2 * i + 1])));
+        *reinterpret_cast<uint2*>(codes + (old + t) * cs.n) = make_uint2(c[0], c[1]);
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+        if (rr + k * RPP < n) put(rr + k * RPP, held[k]);
+    for (int t = rr + kHeld * RPP; t < n; t += RPP) put(t, *reinterpret_cast<const uint4*>(x + (lo + t - first) * xs.n));
     if (threadIdx.x == 0 && !keep) *scale = s;
 }
 
@@ -125,8 +152,7 @@ __global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const Cach
 // sequences are: lengths stay on the device.  A share can begin and end inside
 // an item; such unfinished segments go to the workspace and a second kernel joins
 // them.  (Where there is a CTA for every item and the longest item is at most a
-// quarter above an equal share, the share is that item: equal items then stay
-// whole.)  At most two per CTA: slot 2c for a segment that does not start its item,
+// quarter above an equal share, each CTA takes one item whole.)  At most two per CTA: slot 2c for a segment that does not start its item,
 // slot 2c + 1 for one that starts it and does not reach its end.
 constexpr int kTok = 16;    // tokens of a tile: M of a score product, K of an output product
 constexpr int kBlock = 32;  // tokens of a block: two tiles, which may lie in different pages
@@ -134,24 +160,26 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 // A share has at least this many blocks: with fewer, joining costs more than the
 // shorter walk gives.
-constexpr int kMinShare = 8;
+constexpr int kMinShare = 4;
 
 struct Share {
     long long total, share;
-    int b;              // sequence that holds the start of the share
+    int whole;          // > 0: every item counts as that many blocks and is one share
+    int b;              // sequence that holds the start of the share; -1: there is none
     long long b_first;  // blocks before that sequence
 };
 
 struct ShareSmem {
-    long long warp_sum[kWarps], b_first;
-    int warp_max[kWarps], warp_items[kWarps], b;
+    long long work[kWarps], b_first;
+    int items[kWarps], longest[kWarps], b;
 };
 
 __device__ __forceinline__ int row_tiles(const CacheFwdParams& p, const CacheSeq& s) {
     return (s.q_len * (p.H / p.Hk) + p.rows - 1) / p.rows;
 }
-__device__ __forceinline__ long long seq_work(const CacheFwdParams& p, const CacheSeq& s) {
-    return static_cast<long long>(s.n) * (row_tiles(p, s) * p.Hk);
+// Blocks of a sequence's items (whole: see Share).
+__device__ __forceinline__ long long seq_work(const CacheFwdParams& p, const CacheSeq& s, int whole) {
+    return static_cast<long long>(whole > 0 ? whole : s.n) * (row_tiles(p, s) * p.Hk);
 }
 // Quotient of numbers that hardly ever pass 32 bits (a 64-bit division takes some
 // hundred instructions).
@@ -164,56 +192,61 @@ __device__ __forceinline__ long long div_mostly32(long long a, long long b) {
 __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
-    int longest = 0, items = 0;  // of items
+    long long work = 0;
+    int items = 0, longest = 0;
     for (int b = b0; b < b1; ++b) {
         const CacheSeq q = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
-        mine += seq_work(p, q);
+        work += seq_work(p, q, 0);
         items = min(items + row_tiles(p, q) * p.Hk, 1 << 20);
         if (q.q_len > 0) longest = max(longest, q.n);
     }
     longest = __reduce_max_sync(0xffffffffu, longest);
-    items = __reduce_add_sync(0xffffffffu, items);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long incl = mine;
+    long long work_to = work;
+    int items_to = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
+        const long long w = __shfl_up_sync(0xffffffffu, work_to, o);
+        const int n = __shfl_up_sync(0xffffffffu, items_to, o);
+        if (lane >= o) work_to += w, items_to += n;
     }
     if (lane == 31) {
-        sm->warp_sum[warp] = incl;
-        sm->warp_max[warp] = longest;
-        sm->warp_items[warp] = items;
+        sm->work[warp] = work_to;
+        sm->items[warp] = items_to;
+        sm->longest[warp] = longest;
     }
     if (threadIdx.x == 0) sm->b = -1;
     __syncthreads();
     Share s;
     s.total = 0;
-    long long before = incl - mine;
+    int all_items = 0, items_before = items_to - items;
+    long long work_before = work_to - work;
+    longest = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += sm->warp_sum[w];
-        s.total += sm->warp_sum[w];
-    }
-    longest = items = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        longest = max(longest, sm->warp_max[w]);
-        items += sm->warp_items[w];
+        if (w < warp) work_before += sm->work[w], items_before += sm->items[w];
+        s.total += sm->work[w];
+        all_items += sm->items[w];
+        longest = max(longest, sm->longest[w]);
     }
     s.share = max(div_mostly32(s.total + p.grid - 1, p.grid), static_cast<long long>(kMinShare));
-    if (items <= p.grid && 4ll * longest <= 5ll * s.share) s.share = max(s.share, static_cast<long long>(longest));
+    s.whole = all_items <= p.grid && 4ll * longest <= 5ll * s.share ? longest : 0;
+    if (s.whole > 0) {
+        s.share = s.whole;
+        s.total = static_cast<long long>(all_items) * s.whole;
+        work = static_cast<long long>(items) * s.whole;
+        work_before = static_cast<long long>(items_before) * s.whole;
+    }
     const long long x = c * s.share;
-    if (x < s.total && before <= x && x < before + mine) {
+    if (x < s.total && work_before <= x && x < work_before + work) {
         for (int b = b0; b < b1; ++b) {
-            const long long w = seq_work(p, cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b));
-            if (x < before + w) {
+            const long long w = seq_work(p, cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b), s.whole);
+            if (x < work_before + w) {
                 sm->b = b;
-                sm->b_first = before;
+                sm->b_first = work_before;
                 break;
             }
-            before += w;
+            work_before += w;
         }
     }
     __syncthreads();
@@ -330,14 +363,15 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 
     while (x < x_end) {
         CacheSeq s = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
-        for (long long w; x >= b_first + (w = seq_work(p, s));) {  // next sequence with work
+        for (long long w; x >= b_first + (w = seq_work(p, s, sh.whole));) {  // next sequence with work
             b_first += w;
             s = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, ++b);
         }
         // segment [v0, v1) of the item's n blocks
         const int rts = row_tiles(p, s);
-        const int item = static_cast<int>(div_mostly32(x - b_first, s.n));
-        const int v0 = static_cast<int>((x - b_first) - static_cast<long long>(item) * s.n);
+        const int counts = sh.whole > 0 ? sh.whole : s.n;
+        const int item = static_cast<int>(div_mostly32(x - b_first, counts));
+        const int v0 = static_cast<int>((x - b_first) - static_cast<long long>(item) * counts);
         const int v1 = static_cast<int>(min(static_cast<long long>(s.n), v0 + (x_end - x)));
         const int hk = item / rts, rt = item - hk * rts;
         const int first_pos = s.len - s.q_len;  // may be negative: rows before the first token see nothing
@@ -732,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
             }
         }
         __syncthreads();  // shared memory is free for the next segment
-        x += v1 - v0;
+        x += sh.whole > 0 ? sh.whole : v1 - v0;
     }
 }
 
@@ -743,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 // where it has few segments, else by the whole block, the segments divided among the
 // warps.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinAtOnce = 8;  // segments whose loads go out together
+constexpr int kJoinFew = 16;  // segments that one warp joins alone
 
 // Running join of segments [i0, i1) of row r: maximum, sum and the lane's D/32 columns.
 template <int D>
@@ -774,13 +808,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     const int hk = bd.item / rts, rt = bd.item - hk * rts;
     const int rows = min(p.rows, bd.q_len * G - rt * p.rows);
     const int n = bd.c_last - bd.c_first + 2;  // segments: of CTAs c_first - 1 (which starts the item) .. c_last
-    auto join = [&](int r, int i0, int i1) {
+    auto join = [&](int r, int i0, int i1, auto at_once) {  // so many segments' loads go out together
+        constexpr int U = decltype(at_once)::value;
         Joined<D> x;
-        for (int i = i0; i < i1; i += kJoinAtOnce) {
-            float2 st[kJoinAtOnce];
-            float y[kJoinAtOnce][E];
+        for (int i = i0; i < i1; i += U) {
+            float2 st[U];
+            float y[U][E];
 #pragma unroll
-            for (int u = 0; u < kJoinAtOnce; ++u) {
+            for (int u = 0; u < U; ++u) {
                 st[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
                 for (int e = 0; e < E; ++e) y[u][e] = 0.f;
@@ -797,7 +832,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
                 }
             }
 #pragma unroll
-            for (int u = 0; u < kJoinAtOnce; ++u) x.add(st[u].x, st[u].y, y[u]);
+            for (int u = 0; u < U; ++u) x.add(st[u].x, st[u].y, y[u]);
         }
         return x;
     };
@@ -813,13 +848,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
                 x.l != 0.f ? (x.m - kWeightShift + log2f(x.l)) * kLn2 : INFINITY;
     };
     const int mine = (c - bd.c_first) * static_cast<int>(gridDim.y) + blockIdx.y, borders = (n - 1) * static_cast<int>(gridDim.y);
-    if (n <= 2 * kJoinAtOnce) {
-        for (int r = mine + borders * warp; r < rows; r += borders * kJoinWarps) write(r, join(r, 0, n));
+    if (n <= kJoinFew) {
+        for (int r = mine + borders * warp; r < rows; r += borders * kJoinWarps) write(r, join(r, 0, n, std::integral_constant<int, 4>{}));
         return;
     }
     const int per = (n + kJoinWarps - 1) / kJoinWarps;
     for (int r = mine; r < rows; r += borders) {
-        const Joined<D> x = join(r, min(n, warp * per), min(n, warp * per + per));
+        const Joined<D> x = join(r, min(n, warp * per), min(n, warp * per + per), std::integral_constant<int, 8>{});
 #pragma unroll
         for (int e = 0; e < E; ++e) o_sm[warp][lane * E + e] = x.o[e];
         if (lane == 0) stat_sm[warp] = make_float2(x.m, x.l);

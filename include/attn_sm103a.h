@@ -333,8 +333,9 @@ typedef struct {
  *              seq_lens[b] - new_lens[b] + t (a negative one is not written).
  * Per page, head and tensor: the scale is the smallest power of two 2^e, e >=
  * -100, with every finite new magnitude at most 448 * 2^e; a page that holds
- * older tokens keeps its scale while that is large enough, else the older codes
- * are rounded again to the new one.  Codes are rounded to nearest even;
+ * older tokens keeps its scale while that is large enough (and 2^-100 or more),
+ * else the older codes are rounded again to the new one.  A code is the fp32
+ * quotient value / scale (exact for a power of two) rounded to nearest even;
  * infinities become +-448 and NaN the NaN code.  Slots behind the last token are
  * left as they were.  No two sequences of a call may write to the same page.
  * Source: ai.engineer item 33 (affine quantisation, Z = 0); no page describes a

@@ -10,7 +10,8 @@ TEST INFRASTRUCTURE ONLY, like the rest of this package.  Definitions:
   its value is scale[page, head] * decode(code);
 * append: the scale of a page is 2^e, the smallest e >= -100 with every finite new
   magnitude <= 448 * 2^e, or the one it has where older tokens are in it and that
-  suffices; codes are the nearest E4M3 numbers (ties to even, saturating).
+  suffices; a code is the E4M3 number nearest to the fp32 quotient value / scale (ties to
+  even, saturating), which is exact where the scale is a power of two.
 """
 
 from __future__ import annotations
@@ -64,13 +65,15 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, table, seq_lens, new_
                     amax = float(fin.max()) if fin.size else 0.0
                     s = 2.0 ** append_exponent(amax)
                     old = slots[0][0]
-                    if old and amax <= 448.0 * float(scale[pid, h]):
+                    if old and float(scale[pid, h]) >= 2.0 ** -100 and amax <= 448.0 * float(scale[pid, h]):
                         s = float(scale[pid, h])
                     elif old:
-                        pages[pid, h, :old] = e4m3_encode(_E4M3[pages[pid, h, :old]] * (float(scale[pid, h]) / s))
+                        ratio = np.float32(float(scale[pid, h]) / s)  # not 1 and no power of two only for a user's scale
+                        pages[pid, h, :old] = e4m3_encode(_E4M3[pages[pid, h, :old]].astype(np.float32) * ratio)
                     scale[pid, h] = s
                     for (slot, t), row in zip(slots, new):
-                        pages[pid, h, slot] = e4m3_encode(row / s)
+                        with np.errstate(invalid="ignore", over="ignore"):
+                            pages[pid, h, slot] = e4m3_encode(row.astype(np.float32) / np.float32(s))
 
 
 def sink_visible(pos: np.ndarray, nk: int, left: int, sinks: int, right: int = 0) -> np.ndarray:

@@ -337,6 +337,20 @@ def test_append_special_values():
     check_clean()
 
 
+@pytest.mark.parametrize("scale", [0.3, 0.007, 1.0 / 3.0, 2.0 ** -110, 1e30])
+def test_append_keeps_a_scale_that_is_no_power_of_two(scale):
+    """A page of a user's own scale: codes are the fp32 quotients x / scale, rounded."""
+    pool = Pool(31, 1, 2, 128, 32, 1)
+    pool.ks[:], pool.vs[:] = np.float32(scale), np.float32(scale)
+    dev = pool.dev()
+    k, kv = bf16(pool.rng, (1, 2, 20, 128))
+    api.cache_append(k, k, *dev, i32([29]), new_lens=i32([20]))
+    streaming.cache_append(kv, kv, pool.k, pool.v, pool.ks, pool.vs, pool.table, [29], [20])
+    check_clean()
+    for got, want in zip(dev[:4], (pool.k, pool.v, pool.ks, pool.vs)):
+        assert np.array_equal(got.cpu().numpy(), want.astype(got.cpu().numpy().dtype))
+
+
 def test_refusals():
     import torch
     pool = Pool(40, 2, 2, 64, 16, 3)
