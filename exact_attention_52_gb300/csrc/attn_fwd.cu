@@ -579,27 +579,82 @@ __global__ void __launch_bounds__(320, 1)
                 break;
             }
             tc_fence_after();
+            const int kv0 = it.tile(jt0 + j) * kTile;
+            const int c_lo = key_min - kv0, c_hi = key_max - kv0;  // visible columns [c_lo, c_hi]
+            const int c_sink = SINKS ? prm.sinks - kv0 : 0;        // and, with sinks, those below c_sink up to c_hi
+            float alpha = 1.f;
+            bool rescale_o = false;
+            float ls[4], lr[4];
+            bool done = false;
+            if constexpr (SINKS) {
+                // A tile with a masked element (a sink tile, the window's first, the diagonal), a
+                // quarter at a time: quarters of which no row of the warp sees a column get P = 0
+                // unread.  The tile's maximum comes first, so that nothing is done again; P of a
+                // quarter goes over columns that have been read.
+                done = __any_sync(0xffffffffu, (c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1);
+                if (done) {
+                    uint32_t x[32];
+                    auto quarter = [&](int c) -> bool {  // scores 32 c .. 32 c + 31, masked, in x
+                        if (!__any_sync(0xffffffffu, 32 * c <= c_hi && (32 * c + 31 >= c_lo || 32 * c < c_sink))) return false;
+                        tmem_ld32(tS + 32 * c, x);
+                        tmem_ld_wait(x);
+                        auto below = [&](int n) { n -= 32 * c; return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+                        const uint32_t seen = below(c_hi + 1) & (~below(c_lo) | below(c_sink));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen >> i & 1u)) x[i] = f2u(-INFINITY);
+                        return true;
+                    };
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c)
+                        if (quarter(c)) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) mx = fmax3(mx, u2f(x[i]), u2f(x[i + 1]));
+                        }
+                    if (mx * cs > m_used + kRescaleThreshold) {
+                        alpha = ex2_approx(m_used - mx * cs);  // 0 when m_used is still -inf
+                        l_sum *= alpha;
+                        l_pv *= alpha;
+                        m_used = mx * cs;
+                        rescale_o = j > 0;
+                    }
+                    const float m_sub = (m_used == -INFINITY) ? 0.f : m_used;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) ls[e] = lr[e] = 0.f;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pk[i] = 0u;
+                        if (quarter(c)) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                float x0, x1, x2, x3, a0, a1;
+                                ffma2(x0, x1, u2f(x[i]), u2f(x[i + 1]), cs, cs, -m_sub, -m_sub);
+                                ffma2(x2, x3, u2f(x[i + 2]), u2f(x[i + 3]), cs, cs, -m_sub, -m_sub);
+                                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1), p2 = ex2_approx(x2), p3 = ex2_approx(x3);
+                                pk[i / 2] = pack_bf16x2(p0, p1);
+                                pk[i / 2 + 1] = pack_bf16x2(p2, p3);
+                                lr[0] = add_bf16x2(lr[0], pk[i / 2]);
+                                lr[1] = add_bf16x2(lr[1], pk[i / 2 + 1]);
+                                fadd2(a0, a1, p0, p1, p2, p3);
+                                fadd2(ls[0], ls[1], ls[0], ls[1], a0, a1);
+                            }
+                        }
+                        tmem_st16(tS + 16 * c, pk);
+                    }
+                }
+            }
+            if (!done) {
             uint32_t s[4][32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, s[c]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
 
-            const int kv0 = it.tile(jt0 + j) * kTile;
-            const int c_lo = key_min - kv0, c_hi = key_max - kv0;  // visible columns [c_lo, c_hi]
-            const int c_sink = SINKS ? prm.sinks - kv0 : 0;        // and, with sinks, those below c_sink up to c_hi
             auto apply_mask = [&]() {
-                if constexpr (SINKS) {
-                    if ((c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int k = c * 32 + i;
-                                if ((k < c_lo && k >= c_sink) || k > c_hi) s[c][i] = f2u(-INFINITY);
-                            }
-                    }
-                } else if (c_lo > 0 || c_hi < kTile - 1) {
+                if (!SINKS && (c_lo > 0 || c_hi < kTile - 1)) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
@@ -615,8 +670,6 @@ __global__ void __launch_bounds__(320, 1)
             // E4M3 stops at 448), 2^60 for bf16 (a bf16 value keeps its relative
             // precision at any magnitude; the bound keeps P, O and the sums far inside
             // fp32).  m_used is raised when the tile maximum exceeds it by more than tau.
-            float alpha = 1.f;
-            bool rescale_o = false;
             auto update_max = [&](float tau) {
                 float mx8[8];
 #pragma unroll
@@ -641,7 +694,6 @@ __global__ void __launch_bounds__(320, 1)
 
             // P is kept in registers until the tile is accepted: its bf16 words would
             // overwrite the S columns, which a redo reads again.
-            float ls[4], lr[4];
             uint32_t pk0[32], pk1[32];  // packed P: FP8 all 128 keys in pk0; bf16 keys 0-63, 64-127
             auto exp_pass = [&]() {
                 const float m_sub = (m_used == -INFINITY) ? 0.f : m_used;
@@ -701,6 +753,7 @@ __global__ void __launch_bounds__(320, 1)
             }
             tmem_st32(tS, pk0);
             if constexpr (!FP8) tmem_st32(tS + 32, pk1);
+            }
             l_sum += (ls[0] + ls[1]) + (ls[2] + ls[3]);
             l_pv += (lr[0] + lr[1]) + (lr[2] + lr[3]);
             if (__any_sync(0xffffffffu, rescale_o)) {
