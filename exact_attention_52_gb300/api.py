@@ -698,6 +698,8 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
     heads.  Query t of q_lens[b] (default T) sits at position p = seq_lens[b] - q_lens[b] + t and
     sees key j iff j <= p and (window_left is -1, or j >= p - window_left, or j < sinks).  Rows
     behind q_lens[b] are left as they were; a row that sees nothing gives 0 and LSE +inf.
+    Pages that hold no key a query sees are not read.  Decode (T * H / Hk up to 64) and prompts
+    run different kernels, each with its own split of the keys over the device.
     ``workspace``: ``fwd_cache_workspace_bytes`` bytes, one for each call that may overlap; without
     one, the calls of a thread on its current stream share a kept one."""
     import torch

@@ -875,6 +875,9 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(q_lens) & 3u) != 0)
         return ATTN_ERR_INVALID;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
+    // rows of a key/value head, and pairs of query tiles of all sequences, count in 32 bits
+    const long long rows = static_cast<long long>(T) * (H / Hk);
+    if (rows > (1 << 30) || B * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;
     p.q = q;
     p.o = o;
     p.qs = from_abi(qs);
@@ -888,8 +891,11 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     p.T = T;
     p.D = d;
     p.cs = scale * 1.44269504088896340736f;
-    p.left = window_left;
-    p.sinks = sinks;
+    // A window that covers the longest sequence the table can hold is none, and positions
+    // stay far inside 32 bits.
+    const int cap = cache->max_pages * cache->page_size;
+    p.left = window_left >= cap ? -1 : window_left;
+    p.sinks = p.left < 0 ? 0 : (sinks < cap ? sinks : cap);
     p.part = static_cast<float*>(workspace);
     const bool prompt = cache_prompt(H, Hk, T);
     const CacheLayout L = cache_layout(prompt, d);

@@ -196,6 +196,7 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     int items = 0, longest = 0;
     for (int b = b0; b < b1; ++b) {
         const CacheSeq q = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+        if (blockIdx.x == 0) check_len(p.c, p.st, b);
         work += seq_work(p, q, 0);
         items = min(items + row_tiles(p, q) * p.Hk, 1 << 20);
         if (q.q_len > 0) longest = max(longest, q.n);
@@ -876,8 +877,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
 template <int D, int NT>
 cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
     using T = DecodeTraits<D, NT>;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t attr = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+    });
     if (attr != cudaSuccess) return attr;
     p.rows = T::ROWS;
     p.grid = sms * T::CTAS_PER_SM < kCacheGridMax ? sms * T::CTAS_PER_SM : kCacheGridMax;

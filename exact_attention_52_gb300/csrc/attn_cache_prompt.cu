@@ -149,7 +149,10 @@ __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptSh
     const int u0 = min(units, static_cast<int>(threadIdx.x) * per), u1 = min(units, u0 + per);
     auto work = [&](int u) { return static_cast<long long>(prompt_unit(p, u / pairs, u % pairs).n) * p.Hk; };
     long long mine = 0;
-    for (int u = u0; u < u1; ++u) mine += work(u);
+    for (int u = u0; u < u1; ++u) {
+        if (blockIdx.x == 0 && u % pairs == 0) check_len(p.c, p.st, u / pairs);
+        mine += work(u);
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long incl = mine;
 #pragma unroll
@@ -823,7 +826,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
 template <int D>
 cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     using T = PromptTraits<D>;
-    static const cudaError_t attr = [] {
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t attr = once_per_device(ready, [] {
         cudaFuncAttributes a;
         cudaError_t e = cudaFuncGetAttributes(&a, cache_prompt_kernel<D>);
         // the register split draws on what the launch has: with fewer it would wait for ever
@@ -831,7 +835,7 @@ cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
         return e == cudaSuccess ? cudaFuncSetAttribute(cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        T::SMEM_BYTES)
                                 : e;
-    }();
+    });
     if (attr != cudaSuccess) return attr;
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(320, 1)
         if constexpr (SINKS) {
             // The item's key tiles are renumbered from 0: the sink tiles, then its window's
             // union.  Both query tiles start at 0, so that the aligned schedule runs; the
-            // second one's first window tile is then often wholly masked (one tile in about
-            // 20 at 1024 keys and 128 sinks or fewer).
+            // second one's first window tile is then often wholly masked, and costs its
+            // products but no exponentials.
             w.n_sink = min((prm.sinks + kTile - 1) / kTile, w.kv_lo);
             w.skip = w.kv_lo - w.n_sink;
             if (w.n0 > 0) w.n0 += w.lo0 - w.skip;

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "attn_device_status.cuh"
 
 namespace attn {
@@ -181,6 +183,18 @@ struct CacheFwdParams {
     CacheBorder* border;  // [grid]
     DevStatus st;
 };
+
+// Runs f, which sets up a kernel, once on each device that launches it.
+template <typename F>
+cudaError_t once_per_device(std::atomic<unsigned long long>& done, F f) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if ((e = f()) == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // Launchers (return the launch's cudaError_t; no synchronisation).
 cudaError_t launch_fwd_bf16(int D, const CUtensorMap& tq, const CUtensorMap& tk,

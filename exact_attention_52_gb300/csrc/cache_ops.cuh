@@ -41,6 +41,12 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheView& c, const int* q_l
     return s;
 }
 
+// Records a length that leaves the table (the kernels read as if it ended with it).
+__device__ __forceinline__ void check_len(const CacheView& c, const DevStatus& st, int b) {
+    if (static_cast<unsigned>(c.seq_lens[b]) > static_cast<unsigned>(c.max_pages * c.page_size))
+        record_device_error(st, ATTN_DEVERR_PAGE, 0x304);
+}
+
 // Block v of the walk -> block of the sequence.
 __device__ __forceinline__ int cache_block(const CacheSeq& s, int v) { return v < s.n_sink ? v : s.lo + v - s.n_sink; }
 

@@ -79,7 +79,7 @@ def check_out(o, lse, ref, layout="bhnd"):
     assert not bad[at].any(), (np.argwhere(bad & at[..., None])[:4], np.nanmax(np.abs(og - o_ref)[at]))
     assert np.array_equal(np.isposinf(lg[at]), np.isposinf(lse_ref[at]))
     fin = at & np.isfinite(lse_ref)
-    assert np.all(np.abs(lg - lse_ref)[fin] <= 2.0 ** -14)
+    assert np.all(np.abs(lg[fin] - lse_ref[fin]) <= 2.0 ** -14)
 
 
 def run_cache(pool, H, T, seq_lens, q_lens, left=-1, sinks=0, layout="bhnd", scale=None, amp=1.0):
@@ -224,6 +224,69 @@ def test_pages_that_no_query_sees_are_not_read():
     run_cache(pool, 4, 1, lens, None, left, sinks)
 
 
+def test_pages_that_no_query_of_a_prompt_sees_are_not_read():
+    pool = Pool(15, 2, 2, 64, 16, 40)
+    lens, ql, left, sinks = [600, 333], [90, 70], 70, 5
+    for b, n in enumerate(lens):
+        for pg in range(40):
+            lo, hi = pg * 16, pg * 16 + 15
+            if lo >= n or (hi < n - ql[b] - left and lo >= sinks):
+                pool.table[b, pg] = -1 if pg % 2 else 1 << 30
+                continue
+            for x in (pool.k, pool.v):  # slots behind the sequence or between sinks and window: NaN
+                for j in range(lo, hi + 1):
+                    if j >= n or (j < n - ql[b] - left and j >= sinks):
+                        x[pool.table[b, pg], :, j % 16] = 0x7F
+    run_cache(pool, 4, 90, lens, ql, left, sinks)
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_windows_and_sinks_as_large_as_they_get(T):
+    pool = Pool(16, 1, 1, 64, 16, 12)
+    for left, sinks in ((2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31 - 1, 0), (3, 2 ** 31 - 1), (191, 1), (0, 192)):
+        run_cache(pool, 2, T, [150], None, left, sinks)
+        run_cache(pool, 2, T, [1], None, left, sinks)
+
+
+@pytest.mark.parametrize("T,seq", [(1, 300), (3, 77), (70, 300)])
+def test_cache_in_the_debug_build(T, seq):
+    """The range-checked library gives the oracle's answer with the error word clear."""
+    saved = api._lib
+    api._lib = api.load_library(api.DEBUG_LIB_PATH)
+    try:
+        for d in (64, 128):
+            run_cache(Pool(14, 2, 2, d, 32, 10), 8, T, [seq, 5], None, 60, 3)
+    finally:
+        api._lib = saved
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_first_call_of_a_process_may_be_captured(T):
+    """A fresh process whose first call of the library is made under stream capture."""
+    import subprocess
+    import sys
+    code = f"""
+import torch
+from exact_attention_52_gb300 import api
+q = torch.randn(1, 4, {T}, 64, device="cuda").bfloat16()
+kp, vp = (torch.randint(0, 100, (8, 2, 32, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+ks, vs = (torch.ones(8, 2, device="cuda") for _ in range(2))
+table, lens = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8), torch.tensor([200], dtype=torch.int32, device="cuda")
+k = torch.randn(1, 2, {T}, 64, device="cuda").bfloat16()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(g, stream=s):
+    api.cache_append(k, k, kp, vp, ks, vs, table, lens)
+    o, lse = api.fwd_cache(q, kp, vp, ks, vs, table, lens)
+g.replay()
+torch.cuda.synchronize()
+o2, lse2 = api.fwd_cache(q, kp, vp, ks, vs, table, lens)
+assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+assert api.check_device_error() == (0, 0)
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("T", [1, 4])
 def test_nan_codes_in_hidden_places_do_not_matter(T):
     """NaN codes behind the sequence, between sinks and window, and (T > 1) in tokens that
@@ -258,6 +321,17 @@ def test_bad_pages_and_lengths_are_reported():
         assert all(torch.equal(a, b) for a, b in zip(before, good[:4]))
     api.cache_append(k, k, *good, i32([64, 65]), new_lens=i32([0, 1]))  # one token behind the table
     assert api.check_device_error()[0] == -5
+    many, _ = bf16(pool.rng, (2, 2, 70, 64))
+    for x in (q, many):
+        for lens in ([64, 65], [-1, 3], [2 ** 31 - 1, 64]):
+            api.fwd_cache(x, *good, i32(lens))
+            assert api.check_device_error()[0] == -5
+        table = good[4].clone()
+        table[0, 1] = -7
+        api.fwd_cache(x, *good[:4], table, i32([64, 40]))
+        assert api.check_device_error()[0] == -5
+        api.fwd_cache(x, *good, i32([64, 0]))
+        assert api.check_device_error() == (0, 0)
     assert api.check_device_error() == (0, 0)
 
 
@@ -485,6 +559,33 @@ def test_a_graph_keeps_no_workspace_of_eager_calls():
     for (o, lse), (o2, lse2) in zip(want, outs):
         assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
     check_clean()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_prompt_through_the_cache_is_the_whole_sequence_call(d):
+    """A prompt's own attention over what the cache holds of it against attn_fwd_sinks on the
+    values the codes stand for (four significant bits: exact in bf16), and the next tokens one
+    by one against its later rows.  Both sides are within 1e-2 (beyond their bf16 rounding) of
+    the same numbers; LSE within 1e-3."""
+    import torch
+    B, H, Hk, N, more, left, sinks, page = 2, 8, 2, 333, 3, 90, 5, 32
+    pool = Pool(71, B, Hk, d, page, -(-(N + more) // page))
+    dev = pool.dev()
+    k, v = (bf16(pool.rng, (B, Hk, N + more, d))[0] for _ in range(2))
+    q, _ = bf16(pool.rng, (B, H, N + more, d))
+    outs = []
+    for lo, hi in [(0, N)] + [(n, n + 1) for n in range(N, N + more)]:
+        lens = i32([hi] * B)
+        api.cache_append(k[:, :, lo:hi], v[:, :, lo:hi], *dev, lens)
+        outs.append(api.fwd_cache(q[:, :, lo:hi].contiguous(), *dev, lens, window_left=left, sinks=sinks))
+    table = dev[4].long()
+    kd, vd = ((pages[table].view(torch.float8_e4m3fn).float() * sc[table][..., None, None]).transpose(1, 2)
+              .reshape(B, Hk, -1, d)[:, :, :N + more].bfloat16().contiguous() for pages, sc in zip(dev[:2], dev[2:4]))
+    o, lse = api.fwd_sinks(q, kd, vd, left, sinks)
+    check_clean()
+    got = torch.cat([x for x, _ in outs], 2).double()
+    assert torch.all((got - o.double()).abs() <= 2e-2 + 2.0 ** -7 * o.double().abs())
+    assert torch.all((torch.cat([x for _, x in outs], 2) - lse).abs() <= 2e-3)
 
 
 def test_decode_as_it_is_used():
