@@ -34,6 +34,8 @@
 namespace attn {
 namespace {
 
+// sum of 32 weights from which on they are formed again (a weight in f16 ends at 2^16)
+constexpr float kWeightMax = 32768.f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kPairRows = 2 * kTile;
 constexpr int kPromptThreads = 512;
@@ -627,11 +629,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 }
                 tc_fence_after();
                 const float4* sc = scales + (tn % T::SCALES) * 8;
-                // Two passes over the 128 scores, 32 at a time (the next 32 on their way from
-                // tensor memory): the maximum, then the weights.  The loops stay rolled and the
+                // The 128 scores 32 at a time.  Only while a row has no maximum is there a pass for
+                // the tile's; after it the weights are formed against m_used as it is, and 32
+                // columns whose sum passes kWeightMax are done again with their own maximum, the
+                // tile's weights before them scaled down (2 x 2048 queries over 16384 keys: 596 us,
+                // with a pass for the maximum of each tile 700).  The loops stay rolled and the
                 // mask is formed from bits: the roles' code does not fit the instruction caches
-                // otherwise (unrolled 1033 us for a call of 700, one pass with the whole row in
-                // registers 715).
+                // otherwise (with both passes unrolled 1033 us).
                 auto take = [&](int c, uint32_t (&x)[32]) {  // columns 32 c .. 32 c + 31, hidden ones -inf
                     tmem_ld_wait(x);
                     if (masked) {  // bit i of `seen`: column 32 c + i
@@ -642,21 +646,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                             if (!(seen >> i & 1u)) x[i] = f2u(-INFINITY);
                     }
                 };
-                auto each = [&](auto work) {
-                    uint32_t x[32], y[32];
-                    tmem_ld32(tS, x);
-#pragma unroll 1
-                    for (int c = 0; c < 4; c += 2) {
-                        tmem_ld32(tS + 32 * c + 32, y);
-                        take(c, x);
-                        work(c, x);
-                        if (c == 0) tmem_ld32(tS + 64, x);
-                        take(c + 1, y);
-                        work(c + 1, y);
-                    }
-                };
-                float mx = -INFINITY;
-                each([&](int c, const uint32_t (&x)[32]) {
+                auto largest = [&](int c, const uint32_t (&x)[32]) {
+                    float mx = -INFINITY;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float4 e = sc[2 * c + h];
@@ -670,38 +661,85 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         a = fmaxf(fmax3(a, u2f(x[16 * h + 14]), u2f(x[16 * h + 15])), b);
                         mx = fmaxf(mx, fmaf(a, score_factor(rq, e.x), e.y));
                     }
-                });
-                float alpha = 1.f;
+                    return mx;
+                };
+                float alpha = 1.f, tile_l = 0.f;
                 bool rescale_o = false;
-                if (mx > m_used + kWeightSlack) {
-                    alpha = ex2_approx(m_used - mx);  // 0 while m_used is -inf
-                    l_sum *= alpha;
+                // By whole powers of two, so that weights in f16 scaled down are not rounded twice.
+                auto raise = [&](float mx) -> float {  // factor of what was summed against the old maximum
+                    if (!(mx > m_used)) return 1.f;
+                    if (m_used != -INFINITY) mx = m_used + ceilf(mx - m_used);
+                    const float a = ex2_approx(m_used - mx);  // 0 while m_used is -inf
+                    l_sum *= a;
+                    tile_l *= a;
+                    alpha *= a;
                     m_used = mx;
                     rescale_o = j > 0;
-                }
-                float tile_l = 0.f;
-                const float sub = kWeightShift - (m_used == -INFINITY ? 0.f : m_used);
-                each([&](int c, const uint32_t (&x)[32]) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float4 e = sc[2 * c + h];
-                        const float f = score_factor(rq, e.x), add = e.y + sub;
-                        float a0 = 0.f, a1 = 0.f;
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float x0, x1;
-                            ffma2(x0, x1, u2f(x[16 * h + i]), u2f(x[16 * h + i + 1]), f, f, add, add);
-                            x0 = ex2_approx(x0);
-                            x1 = ex2_approx(x1);
-                            // f16 (half a step, 2^-11 relative): finer than the bf16 output
-                            pk[8 * h + i / 2] = pack_f16x2(x0, x1);
-                            fadd2(a0, a1, a0, a1, x0, x1);
-                        }
-                        tile_l = fmaf(a0 + a1, e.z, tile_l);
+                    return a;
+                };
+                if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tmem_ld32(tS + 32 * c, x);
+                        take(c, x);
+                        mx = fmaxf(mx, largest(c, x));
                     }
+                    raise(mx);
+                }
+                auto work = [&](int c, const uint32_t (&x)[32]) {
+                    uint32_t pk[16];
+                    float sum, l;
+#pragma unroll 1
+                    for (int pass = 0;; ++pass) {
+                        const float sub = kWeightShift - (m_used == -INFINITY ? 0.f : m_used);
+                        sum = l = 0.f;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 e = sc[2 * c + h];
+                            const float f = score_factor(rq, e.x), add = e.y + sub;
+                            float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                float x0, x1;
+                                ffma2(x0, x1, u2f(x[16 * h + i]), u2f(x[16 * h + i + 1]), f, f, add, add);
+                                x0 = ex2_approx(x0);
+                                x1 = ex2_approx(x1);
+                                // f16 (half a step, 2^-11 relative): finer than the bf16 output
+                                pk[8 * h + i / 2] = pack_f16x2(x0, x1);
+                                fadd2(a0, a1, a0, a1, x0, x1);
+                            }
+                            sum += a0 + a1;
+                            l = fmaf(a0 + a1, e.z, l);
+                        }
+                        if (pass > 0 || !__any_sync(0xffffffffu, !(sum <= kWeightMax))) break;
+                        const float a = raise(largest(c, x));
+                        tmem_st_wait();  // the weights stored so far are read back
+#pragma unroll 1
+                        for (int b = 0; b < c; ++b) {
+                            uint32_t w[32], o[16];
+                            tmem_ld32(tS + 16 * b, w);
+                            tmem_ld_wait(w);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float w0, w1;
+                                unpack_f16x2(w[i], w0, w1);
+                                o[i] = pack_f16x2(w0 * a, w1 * a);
+                            }
+                            tmem_st16(tS + 16 * b, o);
+                        }
+                    }
+                    tile_l += l;
                     tmem_st16(tS + 16 * c, pk);  // over columns read before
-                });
+                };
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tmem_ld32(tS + 32 * c, x);
+                    take(c, x);
+                    work(c, x);
+                }
                 l_sum += tile_l;
                 if (__any_sync(0xffffffffu, rescale_o)) {
                     // PV_g(j-1) has completed: S_g(j) was committed after it

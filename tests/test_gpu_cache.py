@@ -166,6 +166,30 @@ def test_cache_forward_of_prompts_large_scores_and_values():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [2, 70, 300])
+@pytest.mark.parametrize("step", [1.0, 4.0, 8.0, 14.0])
+def test_scores_that_grow_along_the_keys(step, T, d):
+    """The running maximum is passed inside a tile, at each of its parts, by little and by
+    far, by some rows of a warp and not by others.  A query has one element that is not
+    zero, so a score is one product: below 2^9 it and its maximum's difference carry two
+    roundings of 2^-16, inside the bound's share for scores."""
+    import torch
+    H, N, page = 2, 700, 64
+    pool = Pool(61 + T, 1, 1, d, page, 11)
+    at = np.minimum(step * (np.arange(704) // 16), 224.0) + np.arange(704) % 16 / 16.0
+    for j in range(11):
+        pool.k[pool.table[0, j], 0, :, 0] = streaming.e4m3_encode(at[page * j:page * j + page])
+    pool.ks[:] = 1.0
+    q = np.zeros((1, H, T, d), np.float32)
+    q[..., 0] = np.array([1.0, -1.0, 0.5, 0.0, 0.25, 1.0, -0.125])[np.arange(H * T).reshape(1, H, T) % 7]
+    q = torch.from_numpy(q).bfloat16()
+    o, lse = api.fwd_cache(q.cuda(), *pool.dev(), i32([N]), scale=1.0)
+    check_clean()
+    check_out(o, lse, streaming.cache_forward(q.double().numpy(), pool.k, pool.v, pool.ks, pool.vs, pool.table,
+                                              [N], [T], 1.0, -1, 0))
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("layout,token_major", [("bnhd", False), ("bhnd", True), ("bnhd", True)])
 def test_cache_forward_layouts(layout, token_major, d):
     pool = Pool(7, 2, 2, d, 32, 5, token_major=token_major)
