@@ -19,7 +19,7 @@
 // about 3700 cycles, of which 2048 are products and 1650 the pass of one tile's softmax;
 // the products' operands (S 128 bytes a cycle, PV 64) and the converters' writes together
 // fill what shared memory gives.  2 x 2048 queries over 16384 keys (32/8 heads, d = 128):
-// 596 us, 1.2 PFLOP/s.  Codes are turned into f16 and not used as E4M3 operands, because
+// 601 us, 1.2 PFLOP/s.  Codes are turned into f16 and not used as E4M3 operands, because
 // then Q and the weights would have to be E4M3 too (2^-4 relative).  A page's scales enter
 // in fp32 as in the kernel for few queries: score * key scale, + log2 of the value scale
 // in the exponent, and 1 / value scale in the sum.
@@ -29,6 +29,8 @@
 // items would leave SMs idle in the last of few rounds (512 equal items on 152 SMs:
 // 16 %).
 #include <cuda_runtime.h>
+
+#include <climits>
 
 #include "attn_internal.h"
 #include "cache_ops.cuh"
@@ -242,6 +244,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + T::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* nan_tiles = reinterpret_cast<int*>(tmem_slot + 2);  // first and last key tile of this CTA with a NaN value
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t b_q = bar0;  // + 8 g
     auto b_kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
@@ -271,6 +274,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         mbar_init(b_merge, 4);
         mbar_init(b_merged, 4);
         *abort_flag = 0;
+        nan_tiles[0] = INT_MAX;
+        nan_tiles[1] = -1;
         fence_mbar_init();
     }
     if (warp == 8) {
@@ -355,9 +360,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 const int round = idx / T::KV_SLOTS;
                 return round == 0 || wait_in_line(b_kv_empty(idx % T::KV_SLOTS), (round - 1) & 1, abort_flag, p.st, SITE_KV_EMPTY);
             };
-            auto convert = [&](const uint4 (&buf)[2 * NI]) {
+            auto convert = [&](const uint4 (&buf)[2 * NI], bool values) {
                 const int slot = idx % T::KV_SLOTS;
                 uint8_t* dst = sKV + slot * T::TILE_BYTES;
+                uint32_t nan[4] = {0u, 0u, 0u, 0u};  // a byte's top bit: a NaN code (7F or FF) in its column
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -368,10 +374,39 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         e4m3x4_to_f16(x.y, h[2], h[3]);
                         e4m3x4_to_f16(x.z, h[4], h[5]);
                         e4m3x4_to_f16(x.w, h[6], h[7]);
+                        if (values) {
+                            nan[0] |= (x.x & 0x7F7F7F7Fu) + 0x01010101u;
+                            nan[1] |= (x.y & 0x7F7F7F7Fu) + 0x01010101u;
+                            nan[2] |= (x.z & 0x7F7F7F7Fu) + 0x01010101u;
+                            nan[3] |= (x.w & 0x7F7F7F7Fu) + 0x01010101u;
+                        }
                         const uint32_t more = (i * 16 + k * RPI) * 128, sw = ((k * RPI) & 7) << 4;  // swizzle of the row
                         *reinterpret_cast<uint4*>(dst + more + (at0 ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
                         *reinterpret_cast<uint4*>(dst + more + (at1 ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
+                // A weight of 0 times NaN is NaN: NaN values stand as 0 in the products, and the
+                // rows that see one get it at the end of the segment.
+                if (values) {
+                    if (__any_sync(0xffffffffu, ((nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u) != 0u)) {
+#pragma unroll 1
+                        for (int i = 0; i < 4 * NI; ++i) {
+                            const int k = (i >> 1) % NI;
+                            uint32_t* at = reinterpret_cast<uint32_t*>(dst + ((i >> 1) / NI * 16 + k * RPI) * 128 +
+                                                                       ((i & 1 ? at1 : at0) ^ (((k * RPI) & 7) << 4)));
+#pragma unroll 1
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t h = at[e];
+                                at[e] = ((h & 0x7FFFu) > 0x7C00u ? 0u : h & 0xFFFFu) |
+                                        ((h & 0x7FFF0000u) > 0x7C000000u ? 0u : h & 0xFFFF0000u);
+                            }
+                        }
+                        if (lane == 0) {
+                            atomicMin(nan_tiles, tile_no - 1);
+                            atomicMax(nan_tiles + 1, tile_no - 1);
+                        }
+                        __syncwarp();
+                    }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_kv_full(slot));
@@ -414,7 +449,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     scales[(tile_no % T::SCALES) * 8 + 2 * cw + lane] = make_float4(sk, lg2_approx(sv), rcp_approx(sv), 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_scale + 8u * (tile_no % T::SCALES));
-                convert(kb);
+                convert(kb, false);
                 ++tile_no;
                 if (i + 1 < tiles) {
                     tok0 = first_tok(w.v0 + i + 1);
@@ -423,7 +458,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     load_scales(tok0, pid);
                 }
                 if (!(ok = claim())) break;
-                convert(vb);
+                convert(vb, true);
             }
         }
     } else if (warp >= 8) {
@@ -485,8 +520,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             release(ring);
             for (int j = 0; j < steps; ++j) {
                 const int vi = ring + 2 * j + 1;
-                bool k_ready = j + 1 >= steps;
-                if (!wait_kv(vi)) return false;
+                // both before P's, off the chain: a look at a barrier takes 250-350 cycles while
+                // products run, and neither tile's slot waits for this step
+                if (!wait_kv(vi) || (j + 1 < steps && !wait_kv(vi + 1))) return false;
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
                     const int a = g ? a1 : a0;
@@ -494,19 +530,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     if (!wait_p(g, j)) return false;
                     issue_pv(g, vi, j == 0);
                     if (j + 1 < a) {
-                        if (!k_ready && !wait_kv(vi + 1)) return false;
-                        k_ready = true;
-                        tc_fence_after();
                         issue_s(g, vi + 1);
                     } else {
                         mma_commit_warp(b_o_full + 8u * g);
                     }
                 }
                 release(vi);
-                if (j + 1 < steps) {
-                    if (!k_ready && !wait_kv(vi + 1)) return false;
-                    release(vi + 1);
-                }
+                if (j + 1 < steps) release(vi + 1);
             }
             return true;
         };
@@ -528,12 +558,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 for (int g = 0; g < 2; ++g) {
                     const int a = g ? a1 : a0, vi = ring + 4 * j + 2 * g + 1;
                     if (j >= a) continue;
-                    if (!wait_kv(vi) || !wait_p(g, j)) return false;
+                    if (!wait_kv(vi) || (j + 1 < a && !wait_kv(vi + 3)) || !wait_p(g, j)) return false;
                     issue_pv(g, vi, j == 0);
                     release(vi);
                     if (j + 1 < a) {
-                        if (!wait_kv(vi + 3)) return false;
-                        tc_fence_after();
                         issue_s(g, vi + 3);
                         release(vi + 3);
                     } else {
@@ -769,6 +797,41 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 tc_fence_after();
             }
             if (!ok) break;
+            if (n > 0 && (!dual || g == 0)) {
+                // NaN values of the segment that the row sees (they stood as 0 in the products)
+                const int t0 = tile_no - (w.v1 - w.v0);
+                const int first = max(t0, *static_cast<volatile int*>(nan_tiles)) - t0 + w.v0;
+                const int last = min(tile_no - 1, *static_cast<volatile int*>(nan_tiles + 1)) - t0 + w.v0;
+                if (first <= last) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t nan = 0u;  // bit i: column 32 c + i
+#pragma unroll 1
+                        for (int x = first * kTile; x < (last + 1) * kTile; ++x) {
+                            const int tok = w.u.tile(x / kTile) * kTile + x % kTile;
+                            if (!row_ok || tok > pos || (tok < key_min && tok >= p.sinks)) continue;
+                            const int pid = __ldg(p.c.table + w.b * p.c.table_stride + (tok >> p.c.page_shift));
+                            if (static_cast<unsigned>(pid) >= static_cast<unsigned>(p.c.num_pages)) continue;
+                            const uint32_t* codes = reinterpret_cast<const uint32_t*>(
+                                p.c.v_pages + pid * p.c.vs.b + w.hk * p.c.vs.h + (tok & (p.c.page_size - 1)) * p.c.vs.n + 32 * c);
+#pragma unroll 1
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t y = ((__ldg(codes + e) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                nan |= (y >> 7 & 1u | y >> 14 & 2u | y >> 21 & 4u | y >> 28 & 8u) << (4 * e);
+                            }
+                        }
+                        if (!__any_sync(0xffffffffu, nan != 0u)) continue;
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * c, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (nan >> i & 1u) o[i] = 0x7FC00000u;
+                        tmem_st32(tO + 32 * c, o);
+                        tmem_st_wait();
+                    }
+                }
+            }
             if (dual && w.a1 > 0) {
                 if (g == 1) {
                     // This group's maximum and sum beside its O in tensor memory, whose lanes the

@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(320, 1)
                 // quarter at a time: quarters of which no row of the warp sees a column get P = 0
                 // unread.  The tile's maximum comes first, so that nothing is done again; P of a
                 // quarter goes over columns that have been read.  B1 H32 Hk8 N8192 d128, 1023
-                // keys back and 4 sinks: 162 us, the window alone 160; what bounds it is the
+                // keys back and 4 sinks: 162 us, the window alone 158; what bounds it is the
                 // window's edge and diagonal tiles, computed whole and seen by half.
                 done = __any_sync(0xffffffffu, (c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1);
                 if (done) {

@@ -361,12 +361,10 @@ attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_str
  *   workspace : attn_fwd_cache_workspace_bytes() bytes, 256-byte aligned,
  *              overwritten; calls that may overlap need one each.
  * A row that sees no key gives O = 0 and LSE = +inf.  What hidden keys and values
- * hold does not matter, NaN codes included; but with more than 64 rows (T * H / Hk)
- * a NaN value reaches every query of the 128-row tile of one that sees it.
- * Scores, softmax and sums
- * are fp32 on products of f16 operands: codes are exact in f16, Q rows are
- * brought to it by a power of two each, the softmax weights (times the value
- * scale) are rounded to it (2^-12 relative).  Results are deterministic.
+ * hold does not matter, NaN codes included.  Scores, softmax and sums are fp32 on
+ * products of f16 operands: codes are exact in f16, Q rows are brought to it by a
+ * power of two each, the softmax weights (times the value scale) are rounded to it
+ * (half a step, 2^-11 relative).  Results are deterministic.
  * Source: ai.engineer item 59 (small-query work split across thread blocks plus
  * a separate combining kernel; causal mask aligned to the last key);
  * FlashAttention-3 tuning page (window bounds).  Errors as attn_fwd_strided.

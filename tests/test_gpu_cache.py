@@ -328,6 +328,23 @@ def test_nan_codes_in_hidden_places_do_not_matter(T):
     run_cache(pool, 8, T, [n], None, left, sinks)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T,n,left,sinks", [(70, 130, -1, 0), (300, 1000, 40, 3), (300, 300, -1, 0), (600, 5000, 700, 20)])
+def test_nan_values_of_a_prompt_reach_the_rows_that_see_them(T, n, left, sinks, d):
+    """NaN codes in a few values of tokens that some queries of a tile see and others do
+    not: NaN in just those rows and columns, as the oracle's, and numbers everywhere else;
+    keys behind the sequence and between sinks and window all NaN."""
+    pool = Pool(13 + T, 1, 2, d, 32, -(-n // 32) + 1)
+    first = n - T
+    at = lambda j: (pool.table[0, j // 32], slice(None), j % 32)
+    for j in range(pool.table.shape[1] * 32):
+        if j >= n or (left >= 0 and sinks <= j < first - left):
+            pool.k[at(j)] = pool.v[at(j)] = 0xFF
+    for j, col in ((first + T // 2, 5), (first + T // 2, d - 1), (n - 1, 33), (first + 40, 0), (0, 17)):
+        pool.v[pool.table[0, j // 32], j % 2, j % 32, col] = 0x7F if col % 2 else 0xFF
+    run_cache(pool, 4, T, [n], None, left, sinks)
+
+
 def test_bad_pages_and_lengths_are_reported():
     import torch
     pool = Pool(12, 2, 1, 64, 16, 4)
