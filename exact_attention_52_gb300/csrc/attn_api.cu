@@ -441,7 +441,7 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
     bp.cs = scale * 1.44269504088896340736f;
     bp.scale = scale;
     bp.split_cap = c.split_cap;
-    if (bwd_sink_parts(&bp) != cudaSuccess) return ATTN_ERR_CUDA;  // without sinks the launcher decides on a split
+    if (bwd_sink_parts(d, &bp) != cudaSuccess) return ATTN_ERR_CUDA;  // without sinks the launcher decides on a split
     if (sink != nullptr && bp.split_parts > 1) {  // for the conversion
         sink->sink_part = c.split_part;
         sink->parts = bp.split_parts;

@@ -1762,12 +1762,45 @@ cudaError_t launch_bwd_main_impl(const CUtensorMap& tq, const CUtensorMap& tk, c
 }  // namespace
 
 // Sinks: a sink tile's item visits every later query tile (64 steps a query head at
-// N8192 against 9 of a 1024-key window), so these items are split into parts of a
-// quarter of the SMs' mean or less, but of kSplitMinPartSteps steps at least.  B1 H4 Hk1
-// N16384, window 1023 and 4 sinks: d = 64 122 us (unsplit 944, the window alone 84), d = 128
-// 152 us (114); B1 H32 Hk8 N8192 d = 128 460 us (428).  Parts joined by the main kernel's
+// N8192 against 9 of a 1024-key window), so these items are split into parts: as many as
+// let the launch end first by the model below, in which every key tile past the sinks
+// takes the same `plain` steps, every part the same share of `steps`, each of them
+// kItemSteps more (set-up, write-out), and parts at all kPartsSteps (their sum).  Over
+// twelve shapes from N1024 to N16384 the choice is within 13 % of the best number of
+// parts, 2 % on average.
+//
+// B1 H4 Hk1 N16384, window 1023 and 4 sinks: d = 64 88 us (unsplit 944, the window alone 84),
+// d = 128 131 us (114); B1 H32 Hk8 N8192 d = 128 459 us (428); parts of a quarter of the
+// SMs' mean, whatever rounds that made: 122, 152, 460.  Parts joined by the main kernel's
 // own epilogue, each after the one before it, spent 64 us of waiting on 16 parts.
-cudaError_t bwd_sink_parts(BwdParams* p) {
+constexpr int kItemSteps = 5, kPartsSteps = 4;
+
+// Steps until `n_plain` items and then n_parts parts are through on `sms` SMs.  d = 64: one
+// CTA an item, parts first, each placed where one has ended; d = 128: dealt out in rounds,
+// every other one backwards, items first.
+long long sink_launch_steps(int D, long long sms, long long n_plain, long long plain, long long n_parts, long long part) {
+    if (D == 64) {
+        // after the parts, `late` SMs are free at a, the others one part earlier
+        const long long late = n_parts % sms, early_at = n_parts / sms * part, late_at = early_at + (late > 0 ? part : 0);
+        if (n_plain == 0) return late_at;
+        // rounds of plain items that the early SMs take before all are through
+        for (long long k = n_plain / sms;; ++k) {
+            auto done = [&](long long t) {
+                return (sms - late) * ((t - early_at) / plain) + (t > late_at ? late * ((t - late_at) / plain) : 0);
+            };
+            if (k > 0 && done(early_at + k * plain) >= n_plain) return std::max(late_at, early_at + k * plain);
+            if (k > 0 && late > 0 && done(late_at + k * plain) >= n_plain) return late_at + k * plain;
+        }
+    }
+    const long long items = n_plain % sms, with_parts = sms - items;  // SMs of the mixed round
+    const long long more = std::max(0ll, n_parts - with_parts), rounds = more / sms, rest = more % sms;
+    const bool backwards = rounds % 2 == 0;  // the last round, seen from the mixed one
+    const bool on_items = backwards ? rest > with_parts : rest > 0, on_parts = backwards ? rest > 0 : rest > items;
+    return n_plain / sms * plain + rounds * part +
+           std::max(items > 0 ? plain + (on_items ? part : 0) : 0, (n_parts > 0 ? part : 0) + (on_parts ? part : 0));
+}
+
+cudaError_t bwd_sink_parts(int D, BwdParams* p) {
     p->split_base = p->BHk * p->n_kv;
     p->split_parts = 1;
     if (p->sinks == 0 || p->split_cap == 0) return cudaSuccess;
@@ -1777,16 +1810,18 @@ cudaError_t bwd_sink_parts(BwdParams* p) {
     if (e != cudaSuccess) return e;
     const long long G = p->H / p->Hk, items = static_cast<long long>(p->BHk) * p->n_kv;
     const long long sink_items = static_cast<long long>(p->BHk) * p->sink_tiles, steps = G * p->n_kv;
-    const long long win_tiles = (static_cast<long long>(p->win_left) + kTile - 1) / kTile + 1;
-    const long long plain = G * (items - sink_items) * (win_tiles < p->n_kv ? win_tiles : p->n_kv);
-    const long long mean = (plain + sink_items * steps) / sms;
-    const long long part = mean / 4 > kSplitMinPartSteps ? mean / 4 : kSplitMinPartSteps;
-    long long parts = (steps + part - 1) / part;
-    if (parts > steps / kSplitMinPartSteps) parts = steps / kSplitMinPartSteps;
+    const long long win_tiles = p->win_right < 0 ? p->n_kv
+                                                 : (static_cast<long long>(p->win_left) + p->win_right + kTile - 1) / kTile + 1;
+    const long long plain = G * std::min<long long>(win_tiles, p->n_kv) + kItemSteps;
     // the last sink tile has the fewest steps: a part keeps one at least
-    const long long least = G * (p->n_kv - p->sink_tiles + 1);
-    for (long long most : {least, static_cast<long long>(kBwdSinkParts), p->split_cap / sink_items})
-        if (parts > most) parts = most;
+    const long long most = std::min({G * (p->n_kv - p->sink_tiles + 1), static_cast<long long>(kBwdSinkParts),
+                                     p->split_cap / sink_items});
+    long long parts = 1, best = 0;
+    for (long long n = 1; n <= most; ++n) {
+        const long long t = (n > 1 ? kPartsSteps : 0) + sink_launch_steps(D, sms, items - sink_items, plain, sink_items * n,
+                                                                          (steps + n - 1) / n + kItemSteps);
+        if (n == 1 || t < best) best = t, parts = n;
+    }
     if (parts >= 2) {
         p->split_base = static_cast<int>(items - sink_items);
         p->split_parts = static_cast<int>(parts);

@@ -207,7 +207,7 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                             const CUtensorMap& tv, const CUtensorMap& tdo, const CUtensorMap& tdq,
                             const BwdParams& p, cudaStream_t stream);
 // Sets split_base and split_parts of a backward with sinks (of any other: none).
-cudaError_t bwd_sink_parts(BwdParams* p);
+cudaError_t bwd_sink_parts(int D, BwdParams* p);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
 cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream);
