@@ -317,9 +317,11 @@ template <int D, int NT>
 struct DecodeTraits {
     static constexpr int ROWS = 8 * NT;
     // Registers (the output takes NT D/4 a lane) admit this many CTAs of four warps to
-    // an SM, and the rings share its memory.
-    static constexpr int CTAS_PER_SM = NT == 1 ? (D == 64 ? 4 : 3) : 2;
-    static constexpr int STAGES = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 6 : 3);  // blocks in a warp's ring
+    // an SM, and the rings share its memory.  NT = 2: with three CTAs an SM d = 64 takes
+    // 33 us for 37 (32 x 4096 tokens, 8 heads, 12 rows), d = 128 spills: 37 us for 35
+    // (16 x 4096, 4 heads, 40 rows).
+    static constexpr int CTAS_PER_SM = NT == 1 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
+    static constexpr int STAGES = NT == 1 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);  // blocks in a warp's ring
     static constexpr int KC = D / 64;  // 16-byte pieces of a token's K row per lane
     static constexpr int VB = D / 8;   // bytes of a token's V row per lane
     static constexpr int NJ = D / 16;  // products of a tile's output
