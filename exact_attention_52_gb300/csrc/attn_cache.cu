@@ -29,16 +29,13 @@ __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w &
 // rounded again to the new scale (exact for a power of two, but for codes that
 // fall below E4M3's normal range).  Dividing by a power of two is exact, so a
 // new code carries one rounding, to nearest even, saturating at 448.
-// Bound by issue (72 % of the slots) beside the reading of the new tokens, which stay in
-// registers between the two looks at them (read twice: 43 us for 33): 4 prompts of up to
-// 8192 tokens, 8 heads, d = 128: 33 us, 4.1 TB/s; one token for 32 sequences 6 us.
+// Bound by reading the new tokens, which stay in registers between the two looks at them
+// (read twice: 43 us for 33), and by issue: magnitudes are compared two at a time as
+// integers, and the quotient's correction is left out where the scale is a power of two (34
+// us for 27 without both).  4 prompts of up to 8192 tokens, 8 heads, d = 128: 27 us, 5.1
+// TB/s; one token for 32 sequences 6 us.
 constexpr int kAppendThreads = 128;
 constexpr int kMinScaleExp = -100;
-
-__device__ __forceinline__ float finite_abs(float x) {
-    const float a = fabsf(x);
-    return a < INFINITY ? a : 0.f;  // NaN compares false
-}
 
 // Smallest power of two s >= 2^kMinScaleExp with amax <= 448 s (448 = 1.75 * 2^8).
 __device__ __forceinline__ float append_scale(float amax) {
@@ -80,25 +77,33 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const C
     // The first kHeld tokens of each thread stay in registers between the two looks at them.
     constexpr int kHeld = 8;
     uint4 held[kHeld];
-    float amax = 0.f;
-    auto look = [&](const uint4& w) {
-        for (uint32_t u : {w.x, w.y, w.z, w.w}) amax = fmaxf(amax, fmaxf(finite_abs(bf16lo(u)), finite_abs(bf16hi(u))));
-    };
     const int n = hi - lo;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) {
         held[k] = make_uint4(0u, 0u, 0u, 0u);
         if (rr + k * RPP < n) held[k] = __ldcs(reinterpret_cast<const uint4*>(x + (lo + rr + k * RPP - first) * xs.n));
     }
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) look(held[k]);
-    for (int t = rr + kHeld * RPP; t < n; t += RPP) look(*reinterpret_cast<const uint4*>(x + (lo + t - first) * xs.n));
-    // Magnitudes order as their bit patterns: one integer maximum per warp.
+    // Magnitudes of bf16 order as their bit patterns: two at a time, one integer maximum a warp.
     __shared__ uint32_t warp_max[kAppendThreads / 32];
-    const uint32_t wm = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = wm;
-    __syncthreads();  // and every thread has read the old scale
-    amax = __uint_as_float(max(max(warp_max[0], warp_max[1]), max(warp_max[2], warp_max[3])));
+    auto largest = [&](auto halves) -> uint32_t {  // of the block's new values, each word's halves given by `halves`
+        uint32_t m = 0u;
+        auto look = [&](const uint4& w) {
+            for (uint32_t u : {w.x, w.y, w.z, w.w}) m = __vmaxu2(m, halves(u & 0x7FFF7FFFu));
+        };
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) look(held[k]);
+        for (int t = rr + kHeld * RPP; t < n; t += RPP) look(*reinterpret_cast<const uint4*>(x + (lo + t - first) * xs.n));
+        const uint32_t wm = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu));
+        if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = wm;
+        __syncthreads();  // and every thread has read the old scale
+        return max(max(warp_max[0], warp_max[1]), max(warp_max[2], warp_max[3]));
+    };
+    uint32_t top = largest([](uint32_t u) { return u; });
+    if (top >= 0x7F80u) {  // infinities or NaN: the largest finite magnitude counts
+        __syncthreads();
+        top = largest([](uint32_t u) { return u & ~__vcmpgeu2(u, 0x7F807F80u); });
+    }
+    const float amax = __uint_as_float(top << 16);
     const int old = lo - pg * page;  // tokens that the page holds already
     const bool keep = old > 0 && was >= __uint_as_float((kMinScaleExp + 127) << 23) && amax <= 448.f * was;
     const float s = keep ? was : append_scale(amax);
@@ -123,25 +128,30 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const C
         }
     }
     // x / s rounded once: a power of two's inverse is exact; for another scale (one that was
-    // there) the remainder of the product puts it right.  Beyond 448 the code saturates.
+    // there) the remainder of the product puts it right, as it would not change the former.  Beyond 448 the code saturates.
     const float inv = 1.f / s;
     auto quotient = [&](float v) {
         const float q = v * inv;
         return fabsf(q) <= 448.f ? fmaf(fmaf(-q, s, v), inv, q) : q;
     };
-    auto put = [&](int t, const uint4& w) {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t c[2];
+    auto put_all = [&](auto code) {
+        auto put = [&](int t, const uint4& w) {
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            uint32_t c[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            c[i] = pack_e4m3x4(quotient(bf16lo(u[2 * i])), quotient(bf16hi(u[2 * i])), quotient(bf16lo(u[2 * i + 1])),
-                               quotient(bf16hi(u[2 * i + 1])));
-        *reinterpret_cast<uint2*>(codes + (old + t) * cs.n) = make_uint2(c[0], c[1]);
+            for (int i = 0; i < 2; ++i)
+                c[i] = pack_e4m3x4(code(bf16lo(u[2 * i])), code(bf16hi(u[2 * i])), code(bf16lo(u[2 * i + 1])),
+                                   code(bf16hi(u[2 * i + 1])));
+            *reinterpret_cast<uint2*>(codes + (old + t) * cs.n) = make_uint2(c[0], c[1]);
+        };
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+            if (rr + k * RPP < n) put(rr + k * RPP, held[k]);
+        for (int t = rr + kHeld * RPP; t < n; t += RPP)
+            put(t, *reinterpret_cast<const uint4*>(x + (lo + t - first) * xs.n));
     };
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-        if (rr + k * RPP < n) put(rr + k * RPP, held[k]);
-    for (int t = rr + kHeld * RPP; t < n; t += RPP) put(t, *reinterpret_cast<const uint4*>(x + (lo + t - first) * xs.n));
+    if ((__float_as_uint(s) & 0x7FFFFFu) == 0u) put_all([&](float v) { return v * inv; });
+    else put_all(quotient);
     if (threadIdx.x == 0 && !keep) *scale = s;
 }
 
