@@ -487,6 +487,25 @@ def _strides4(t, layout):
     return Strides(sb, s1, s2) if layout == "bhnd" else Strides(sb, s2, s1)
 
 
+def _like_strides(dev, t, like, layout):
+    """``_strides4`` of a bf16 tensor of ``like``'s shape on device ``dev``; None for any other."""
+    import torch
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == like.shape and t.get_device() == dev:
+            return _strides4(t, layout)
+    except (AttributeError, ValueError):
+        pass
+    return None
+
+
+def _lse_ok(dev, t, shape):
+    import torch
+    try:
+        return t.dtype is torch.float32 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+    except (AttributeError, ValueError):
+        return False
+
+
 def _layout_shape(t, layout):
     if layout not in ("bhnd", "bnhd"):
         raise ValueError(f"unknown layout {layout!r}")
@@ -536,20 +555,26 @@ def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layo
     ("bnhd"), any strides with a contiguous last dimension.  Returns (O like q, LSE [B, H, N])."""
     import torch
     B, H, Hk, N, d, dev, (qs, ks, vs) = _sinks_args(q, k, v, layout)
-    with _on_stream(stream):
-        if o is None:
-            o = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
-    _explain_like(q.device, "o", o, q)
-    _explain_lse(q.device, lse, (B, H, N))
+    device = q.device
+    if o is None or lse is None:
+        with _on_stream(stream):
+            if o is None:
+                o = torch.empty_like(q)
+            if lse is None:
+                lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
+    os_ = _like_strides(dev, o, q, layout)
+    if os_ is None or not _lse_ok(dev, lse, (B, H, N)):
+        _explain_like(device, "o", o, q)
+        _explain_lse(device, lse, (B, H, N))
+        raise ValueError(f"o and lse must be tensors on {device}")
     _check("attn_fwd_sinks", load_library().attn_fwd_sinks(
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), _strides4(o, layout), lse.data_ptr(),
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), os_, lse.data_ptr(),
         B, H, Hk, N, d, 1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left),
         int(window_right), int(sinks), _call_stream(dev, stream)))
     return o, lse
 
 
+@functools.lru_cache(maxsize=256)
 def bwd_sinks_workspace_bytes(B: int, H: int, Hk: int, N: int, d: int, sinks: int) -> int:
     return int(load_library().attn_bwd_sinks_workspace_bytes(B, H, Hk, N, d, sinks))
 
@@ -566,24 +591,30 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
     need = bwd_sinks_workspace_bytes(B, H, Hk, N, d, int(sinks))
     if need == 0:
         raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, N {N}, d {d}, sinks {sinks}")
-    with _on_stream(stream):
-        if dq is None:
-            dq = torch.empty_like(q)
-        if dk is None:
-            dk = torch.empty_like(k)
-        if dv is None:
-            dv = torch.empty_like(v)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _explain_like(device, name, t, like)
-    _explain_lse(device, lse, (B, H, N))
-    _explain_workspace(device, workspace, need)
-    st = _strides4
+    if dq is None or dk is None or dv is None or workspace is None:
+        with _on_stream(stream):
+            if dq is None:
+                dq = torch.empty_like(q)
+            if dk is None:
+                dk = torch.empty_like(k)
+            if dv is None:
+                dv = torch.empty_like(v)
+            if workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    os_, dos = _like_strides(dev, o, q, layout), _like_strides(dev, dout, q, layout)
+    dqs, dks, dvs = (_like_strides(dev, dq, q, layout), _like_strides(dev, dk, k, layout),
+                     _like_strides(dev, dv, v, layout))
+    if (None in (os_, dos, dqs, dks, dvs) or not _lse_ok(dev, lse, (B, H, N))
+            or not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or workspace.nbytes < need):
+        for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            _explain_like(device, name, t, like)
+        _explain_lse(device, lse, (B, H, N))
+        _explain_workspace(device, workspace, need)
+        raise ValueError(f"the gradients, o, dout, lse and workspace must be tensors on {device}")
     _check("attn_bwd_sinks", load_library().attn_bwd_sinks(
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), st(o, layout), dout.data_ptr(),
-        st(dout, layout), lse.data_ptr(), dq.data_ptr(), st(dq, layout), dk.data_ptr(), st(dk, layout),
-        dv.data_ptr(), st(dv, layout), workspace.data_ptr(), B, H, Hk, N, d,
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), os_, dout.data_ptr(),
+        dos, lse.data_ptr(), dq.data_ptr(), dqs, dk.data_ptr(), dks, dv.data_ptr(), dvs, workspace.data_ptr(), B, H,
+        Hk, N, d,
         1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(window_right), int(sinks),
         _call_stream(dev, stream)))
     return dq, dk, dv
