@@ -649,3 +649,61 @@ def test_decode_as_it_is_used():
         assert np.array_equal(dev[0].cpu().numpy(), pool.k) and np.array_equal(dev[1].cpu().numpy(), pool.v)
         check_out(o, lse, streaming.cache_forward(qv, pool.k, pool.v, pool.ks, pool.vs, pool.table, lens, new,
                                                   64 ** -0.5, 45, 4))
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_calls_that_follow_copies_and_other_streams(T):
+    """What a call reads was written just before it: by a copy, by a kernel of another stream
+    that it waits for, by the call before it; eager and captured, many times over."""
+    import torch
+    torch.manual_seed(5)
+    B, H, Hk, d, page, n = 3, 8, 2, 64, 32, 400
+    kp, vp = (torch.randint(0, 0x70, (40, Hk, page, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((40, Hk), 2.0 ** -6, device="cuda") for _ in range(2))
+    table = torch.randperm(39, device="cuda", dtype=torch.int32).view(3, 13)
+    k, q = (torch.randn(B, h, T, d, device="cuda").bfloat16() for h in (Hk, H))
+    want_lens = [i32([n, 71, 133]), i32([150, n, 70])]
+    lens, q_in = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros_like(q)
+    pages = [x.clone() for x in (kp, vp, ks, vs)]
+    side, o = torch.cuda.Stream(), [torch.empty_like(q) for _ in want_lens]
+    lse = [torch.empty(B, H, T, device="cuda") for _ in want_lens]
+
+    def steps():
+        here = torch.cuda.current_stream()
+        for i, w in enumerate(want_lens):
+            lens.copy_(w)
+            api.cache_append(k, k, *pages, table, lens)
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                q_in.copy_(q)
+                q_in.mul_(1 - 2 * i)
+            here.wait_stream(side)
+            api.fwd_cache(q_in, *pages, table, lens, o=o[i], lse=lse[i])
+            q_in.zero_()
+            lens.zero_()
+
+    def reset():
+        for x, y in zip(pages, (kp, vp, ks, vs)):
+            x.copy_(y)
+
+    # one step at a time
+    want = []
+    reset()
+    for i, w in enumerate(want_lens):
+        api.cache_append(k, k, *pages, table, w)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in api.fwd_cache(q * (1 - 2 * i), *pages, table, w)])
+        torch.cuda.synchronize()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    reset()
+    with torch.cuda.graph(g, stream=s):
+        steps()
+    for run in [steps] * 20 + [g.replay] * 20:
+        reset()
+        for x in (*o, *lse):
+            x.fill_(3.0)
+        run()
+        for (wo, wl), go, gl in zip(want, o, lse):
+            assert torch.equal(wo.view(torch.int16), go.view(torch.int16)) and torch.equal(wl, gl)
+    check_clean()
