@@ -48,7 +48,6 @@ template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const CacheAppendParams p) {
     constexpr int TPR = D / 8;  // threads per token: 8 elements each
     constexpr int RPP = kAppendThreads / TPR;
-    pdl_launch_dependents();
     pdl_wait();
     const int hk = blockIdx.y, b = blockIdx.z >> 1;
     const bool is_v = blockIdx.z & 1;
@@ -823,7 +822,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     __shared__ float o_sm[kJoinWarps][D];
     __shared__ float2 stat_sm[kJoinWarps];
     const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_launch_dependents();
     pdl_wait();
     const CacheBorder bd = p.border[c];
     if (bd.c_first < 0) return;  // the share begins with its item
@@ -896,11 +894,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     }
 }
 
-// Launches a kernel as a programmatic dependent of the one before it in the stream: its
-// CTAs are placed while the last ones of that kernel finish, and wait for all of it
-// (pdl_wait) before they touch memory.  Calls one after the other on a stream: 19.3 -> 17.6
-// us (32 sequences, 1028 keys each of 16 heads, d = 64), 33.0 -> 31.5 (16 x 4096 tokens, 40
-// rows), appended prompts 21.7 -> 19.8; 64 x 8192 tokens 126 -> 127.
+// Launches a kernel as a programmatic dependent of the one before it in the stream: it is
+// placed as that kernel ends, and waits for all of it (pdl_wait) before it touches memory.
+// Calls one after the other on a stream: 19.3 -> 17.7 us (32 sequences, 1028 keys each of
+// 16 heads, d = 64), 33.0 -> 31.5 (16 x 4096 tokens, 40 rows), appended prompts 21.7 ->
+// 19.8, 64 x 8192 tokens 126 -> 120.  Only the attention kernel lets its dependent, the
+// join, start early: where the join let the next call's CTAs in among its own, 64 x 8192
+// tokens took 123 - 129.
 template <typename P>
 cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, int smem, cudaStream_t stream, const P& p) {
     cudaLaunchAttribute pdl;
