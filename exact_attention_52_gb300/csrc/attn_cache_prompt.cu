@@ -797,8 +797,32 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 tc_fence_after();
             }
             if (!ok) break;
-            if (n > 0 && (!dual || g == 0)) {
-                // NaN values of the segment that the row sees (they stood as 0 in the products)
+            if (dual && w.a1 > 0) {
+                if (g == 1) {
+                    // This group's maximum and sum beside its O in tensor memory, whose lanes the
+                    // other group's warp of the same number can read; the columns are its own P's,
+                    // which the products have read.
+                    uint32_t x[16] = {f2u(l_sum != 0.f ? m_used : -INFINITY), f2u(l_sum)};
+                    tmem_st16(tS, x);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(b_merge);
+                    // the next segment's Q lets products write there again
+                    ok = wait_in_line(b_merged, merges & 1, abort_flag, p.st, SITE_MERGE);
+                    ++merges;
+                    continue;
+                }
+                ok = wait_in_line(b_merge, merges & 1, abort_flag, p.st, SITE_MERGE);
+                ++merges;
+                if (!ok) break;
+                tc_fence_after();
+            } else if (dual && g == 1) {
+                continue;  // the only tile was group 0's
+            }
+            if (n > 0) {
+                // NaN values of the segment that the row sees (they stood as 0 in the products); by
+                // now both groups' products are done, so every value of it has been looked at
                 const int t0 = tile_no - (w.v1 - w.v0);
                 const int first = max(t0, *static_cast<volatile int*>(nan_tiles)) - t0 + w.v0;
                 const int last = min(tile_no - 1, *static_cast<volatile int*>(nan_tiles + 1)) - t0 + w.v0;
@@ -831,29 +855,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         tmem_st_wait();
                     }
                 }
-            }
-            if (dual && w.a1 > 0) {
-                if (g == 1) {
-                    // This group's maximum and sum beside its O in tensor memory, whose lanes the
-                    // other group's warp of the same number can read; the columns are its own P's,
-                    // which the products have read.
-                    uint32_t x[16] = {f2u(l_sum != 0.f ? m_used : -INFINITY), f2u(l_sum)};
-                    tmem_st16(tS, x);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(b_merge);
-                    // the next segment's Q lets products write there again
-                    ok = wait_in_line(b_merged, merges & 1, abort_flag, p.st, SITE_MERGE);
-                    ++merges;
-                    continue;
-                }
-                ok = wait_in_line(b_merge, merges & 1, abort_flag, p.st, SITE_MERGE);
-                ++merges;
-                if (!ok) break;
-                tc_fence_after();
-            } else if (dual && g == 1) {
-                continue;  // the only tile was group 0's
             }
             const bool finished = w.v0 == 0 && w.v1 == w.u.n, merge = dual && w.a1 > 0;
             // group 0's O and sum times f0, and, merging, group 1's times f1

@@ -345,6 +345,20 @@ def test_nan_values_of_a_prompt_reach_the_rows_that_see_them(T, n, left, sinks, 
     run_cache(pool, 4, T, [n], None, left, sinks)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [70, 128])
+def test_nan_values_of_a_lone_query_tile(T, d):
+    """One NaN value per sequence and head, in every key tile in turn, where two groups of
+    warps share a query tile's keys: the one that ends later may be the one that met it."""
+    B, Hk, n, page = 10, 4, 1100, 64
+    pool = Pool(17, B, Hk, d, page, 18)
+    for b in range(B):
+        for h in range(Hk):
+            j = min(n - 1, 128 * ((b * Hk + h) % 9) + 97)
+            pool.v[pool.table[b, j // page], h, j % page, (7 * b + h) % d] = 0x7F
+    run_cache(pool, Hk, T, [n] * B, None)
+
+
 def test_bad_pages_and_lengths_are_reported():
     import torch
     pool = Pool(12, 2, 1, 64, 16, 4)
