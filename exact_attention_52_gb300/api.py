@@ -405,12 +405,18 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
 # A decode step runs these for single tokens, where the host's share of a call
 # counts: each function first makes one pass of cheap comparisons, and only when
 # one fails do the functions named _explain_* look for the argument to name.
-def _call_stream(device_index, stream):
+# They are handed `torch`, and ask torch._C, for the same reason: an import statement or a
+# look whether CUDA has been set up costs 0.1 to 0.2 us of a 15 us call.
+def _call_stream(torch, device_index, stream):
     """Handle of the stream a call runs on (the current one without an argument)."""
-    import torch
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(device_index)
+
+
+def _is_current(torch, dev):
+    """Whether ``dev`` is the current device's index (a CPU tensor's is -1)."""
+    return dev >= 0 and dev == torch._C._cuda_getDevice()
 
 
 def _on_stream(stream):
@@ -424,13 +430,12 @@ def _on_stream(stream):
 _kept = threading.local()
 
 
-def _call_workspace(dev, stream, handle, need):
+def _call_workspace(torch, dev, stream, handle, need):
     """Workspace of a call that was given none.  Calls of one thread on one stream run one after
     the other, so they share one that is kept (an allocation took 7 us of a 22 us call).  A call
     that is being captured, whose workspace the graph goes on using, and a call on a stream given
     as an argument get one of their own."""
-    import torch
-    if stream is not None or torch.cuda.is_current_stream_capturing():
+    if stream is not None or torch._C._cuda_isCurrentStreamCapturing():
         with _on_stream(stream):
             return torch.empty(need, dtype=torch.uint8, device=dev)
     kept = _kept.__dict__
@@ -487,9 +492,8 @@ def _strides4(t, layout):
     return Strides(sb, s1, s2) if layout == "bhnd" else Strides(sb, s2, s1)
 
 
-def _like_strides(dev, t, like, layout):
+def _like_strides(torch, dev, t, like, layout):
     """``_strides4`` of a bf16 tensor of ``like``'s shape on device ``dev``; None for any other."""
-    import torch
     try:
         if t.dtype is torch.bfloat16 and t.shape == like.shape and t.get_device() == dev:
             return _strides4(t, layout)
@@ -498,8 +502,7 @@ def _like_strides(dev, t, like, layout):
     return None
 
 
-def _lse_ok(dev, t, shape):
-    import torch
+def _lse_ok(torch, dev, t, shape):
     try:
         return t.dtype is torch.float32 and t.shape == shape and t.get_device() == dev and t.is_contiguous()
     except (AttributeError, ValueError):
@@ -539,7 +542,7 @@ def _sinks_args(q, k, v, layout):
         strides = _strides4(q, layout), _strides4(k, layout), _strides4(v, layout)
         ok = (None not in strides and (Bk, Nk, dk) == (B, N, d) and k.shape == v.shape
               and q.dtype is bf16 and k.dtype is bf16 and v.dtype is bf16
-              and dev == k.get_device() == v.get_device() == torch.cuda.current_device())
+              and dev == k.get_device() == v.get_device() and _is_current(torch, dev))
     except (AttributeError, ValueError):
         ok = False
     if not ok:
@@ -562,15 +565,15 @@ def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layo
                 o = torch.empty_like(q)
             if lse is None:
                 lse = torch.empty((B, H, N), dtype=torch.float32, device=device)
-    os_ = _like_strides(dev, o, q, layout)
-    if os_ is None or not _lse_ok(dev, lse, (B, H, N)):
+    os_ = _like_strides(torch, dev, o, q, layout)
+    if os_ is None or not _lse_ok(torch, dev, lse, (B, H, N)):
         _explain_like(device, "o", o, q)
         _explain_lse(device, lse, (B, H, N))
         raise ValueError(f"o and lse must be tensors on {device}")
     _check("attn_fwd_sinks", load_library().attn_fwd_sinks(
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), os_, lse.data_ptr(),
         B, H, Hk, N, d, 1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left),
-        int(window_right), int(sinks), _call_stream(dev, stream)))
+        int(window_right), int(sinks), _call_stream(torch, dev, stream)))
     return o, lse
 
 
@@ -601,10 +604,10 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
                 dv = torch.empty_like(v)
             if workspace is None:
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    os_, dos = _like_strides(dev, o, q, layout), _like_strides(dev, dout, q, layout)
-    dqs, dks, dvs = (_like_strides(dev, dq, q, layout), _like_strides(dev, dk, k, layout),
-                     _like_strides(dev, dv, v, layout))
-    if (None in (os_, dos, dqs, dks, dvs) or not _lse_ok(dev, lse, (B, H, N))
+    os_, dos = _like_strides(torch, dev, o, q, layout), _like_strides(torch, dev, dout, q, layout)
+    dqs, dks, dvs = (_like_strides(torch, dev, dq, q, layout), _like_strides(torch, dev, dk, k, layout),
+                     _like_strides(torch, dev, dv, v, layout))
+    if (None in (os_, dos, dqs, dks, dvs) or not _lse_ok(torch, dev, lse, (B, H, N))
             or not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or workspace.nbytes < need):
         for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             _explain_like(device, name, t, like)
@@ -616,7 +619,7 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
         dos, lse.data_ptr(), dq.data_ptr(), dqs, dk.data_ptr(), dks, dv.data_ptr(), dvs, workspace.data_ptr(), B, H,
         Hk, N, d,
         1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(window_right), int(sinks),
-        _call_stream(dev, stream)))
+        _call_stream(torch, dev, stream)))
     return dq, dk, dv
 
 
@@ -654,9 +657,8 @@ def _explain_cache(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_ta
     raise ValueError(f"the cache's tensors must all be on {device}, the current device")
 
 
-def _cache_arg(dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens, new_name):
+def _cache_arg(torch, dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens, new_name):
     """attn_cache_t of a call, its tensors checked."""
-    import torch
     try:
         P, heads, page, dim = shape = k_pages.shape
         i32, u8, f32 = torch.int32, torch.uint8, torch.float32
@@ -699,7 +701,7 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
         dev, bf16 = k.get_device(), torch.bfloat16
         ks, vs = _strides4(k, layout), _strides4(v, layout)
         ok = (ks is not None and vs is not None and k.shape == v.shape and k.dtype is bf16 and v.dtype is bf16
-              and dev == v.get_device() == torch.cuda.current_device())
+              and dev == v.get_device() and _is_current(torch, dev))
     except (AttributeError, ValueError):
         ok = False
     if not ok:
@@ -707,11 +709,11 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
         _explain_like(k.device, "k", k, k)
         _explain_like(k.device, "v", v, k)
         raise ValueError("k and v must be bf16 CUDA tensors of one device")
-    cache = _cache_arg(dev, k.device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+    cache = _cache_arg(torch, dev, k.device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
                        new_lens, "new_lens")
     _check("attn_cache_append", load_library().attn_cache_append(
         cache, k.data_ptr(), ks, v.data_ptr(), vs, None if new_lens is None else new_lens.data_ptr(),
-        B, Hk, T, d, _call_stream(dev, stream)))
+        B, Hk, T, d, _call_stream(torch, dev, stream)))
 
 
 @functools.lru_cache(maxsize=256)
@@ -737,7 +739,7 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
     B, H, T, d = _layout_shape(q, layout)
     try:
         dev, qs, Hk = q.get_device(), _strides4(q, layout), k_pages.shape[1]
-        ok = qs is not None and q.dtype is torch.bfloat16 and dev == torch.cuda.current_device()
+        ok = qs is not None and q.dtype is torch.bfloat16 and _is_current(torch, dev)
     except (AttributeError, IndexError):
         ok = False
     if not ok:
@@ -745,12 +747,12 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
         _explain_like(q.device, "q", q, q)
         raise ValueError("k_pages must be a tensor [pages, Hk, page_size, d]")
     device = q.device
-    cache = _cache_arg(dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+    cache = _cache_arg(torch, dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
                        q_lens, "q_lens")
     need = fwd_cache_workspace_bytes(B, H, Hk, T, d)
     if need == 0:
         raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, T {T}, d {d}")
-    handle = _call_stream(dev, stream)
+    handle = _call_stream(torch, dev, stream)
     if o is None or lse is None:
         with _on_stream(stream):
             if o is None:
@@ -758,7 +760,7 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
             if lse is None:
                 lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
     if workspace is None:
-        workspace = _call_workspace(dev, stream, handle, need)
+        workspace = _call_workspace(torch, dev, stream, handle, need)
     try:
         os_ = _strides4(o, layout)
         ok = (os_ is not None and o.dtype is torch.bfloat16 and o.shape == q.shape and lse.shape == (B, H, T)
