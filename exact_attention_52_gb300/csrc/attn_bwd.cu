@@ -1747,8 +1747,10 @@ cudaError_t launch_bwd_main_impl(const CUtensorMap& tq, const CUtensorMap& tk, c
                                  const CUtensorMap& tdo, const CUtensorMap& tdq, const BwdParams& p,
                                  cudaStream_t stream) {
     using T = BwdTraits<D>;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        bwd_main_kernel<D, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t attr = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(bwd_main_kernel<D, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+    });
     if (attr != cudaSuccess) return attr;
     long long grid = static_cast<long long>(p.BHk) * p.n_kv;
     if (SINKS) grid = p.split_base + (grid - p.split_base) * p.split_parts;
@@ -1872,7 +1874,8 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                            : launch_bwd_main_impl<64, false>(tq, tk, tv, tdo, tdq, p, stream);
     if (D == 128) {
         using T = BwdFullTraits;
-        static const cudaError_t attr = [] {
+        static std::atomic<unsigned long long> ready{0};
+        const cudaError_t attr = once_per_device(ready, [] {
             cudaError_t e = cudaSuccess;
             for (const void* fn : {reinterpret_cast<const void*>(bwd_main_full_kernel<0, false>),
                                    reinterpret_cast<const void*>(bwd_main_full_kernel<1, false>),
@@ -1885,7 +1888,7 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
                 if (e == cudaSuccess)
                     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
             return e;
-        }();
+        });
         if (attr != cudaSuccess) return attr;
         // persistent: one CTA per SM (shared memory admits one), items in snake order
         const long long items = static_cast<long long>(p.BHk) * p.n_kv;

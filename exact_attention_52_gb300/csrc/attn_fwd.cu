@@ -902,8 +902,11 @@ template <int D, bool FP8, bool FMAEXP = false, bool SINKS = false>
 cudaError_t launch_fwd_impl(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const FwdParams& p, cudaStream_t stream) {
     using T = FwdTraits<D, FP8>;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        fwd_kernel<D, FP8, FMAEXP, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM_BYTES);
+    static std::atomic<unsigned long long> ready{0};
+    const cudaError_t attr = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(fwd_kernel<D, FP8, FMAEXP, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    T::SMEM_BYTES);
+    });
     if (attr != cudaSuccess) return attr;
     // Persistent CTAs, one per SM (shared memory admits one), each looping over
     // items in the snake order of item_at: equal items (no mask) and longest-first
