@@ -165,9 +165,10 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const C
 // of G takes the c-th of G equal shares of that line, whatever the lengths of the
 // sequences are: lengths stay on the device.  A share can begin and end inside
 // an item; such unfinished segments go to the workspace and a second kernel joins
-// them.  (Where there is a CTA for every item and the longest item is at most a
-// quarter above an equal share, each CTA takes one item whole.)  At most two per CTA: slot 2c for a segment that does not start its item,
-// slot 2c + 1 for one that starts it and does not reach its end.
+// them.  At most two per CTA: slot 2c for a segment that does not start its item,
+// slot 2c + 1 for one that starts it and does not reach its end.  (Where there is a CTA
+// for every item and the longest item is at most a quarter above an equal share, each
+// CTA takes one item whole.)
 constexpr int kTok = 16;    // tokens of a tile: M of a score product, K of an output product
 constexpr int kBlock = 32;  // tokens of a block: two tiles, which may lie in different pages
 constexpr int kWarps = 4;
@@ -201,6 +202,19 @@ __device__ __forceinline__ long long div_mostly32(long long a, long long b) {
     return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
+// Shares of a line of `total` blocks in which all_items items lie; their start is still to be found.
+__device__ __forceinline__ Share equal_shares(const CacheFwdParams& p, long long total, int all_items, int longest) {
+    Share s;
+    s.total = total;
+    s.share = max(div_mostly32(total + p.grid - 1, p.grid), static_cast<long long>(kMinShare));
+    s.whole = all_items <= p.grid && 4ll * longest <= 5ll * s.share ? longest : 0;
+    if (s.whole > 0) {
+        s.share = s.whole;
+        s.total = static_cast<long long>(all_items) * s.whole;
+    }
+    return s;
+}
+
 // Lays the items of all sequences end to end and finds the sequence at the start
 // of share c (a slice of the sequences per thread).
 __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
@@ -232,23 +246,19 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     }
     if (threadIdx.x == 0) sm->b = -1;
     __syncthreads();
-    Share s;
-    s.total = 0;
+    long long total = 0;
     int all_items = 0, items_before = items_to - items;
     long long work_before = work_to - work;
     longest = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) work_before += sm->work[w], items_before += sm->items[w];
-        s.total += sm->work[w];
+        total += sm->work[w];
         all_items += sm->items[w];
         longest = max(longest, sm->longest[w]);
     }
-    s.share = max(div_mostly32(s.total + p.grid - 1, p.grid), static_cast<long long>(kMinShare));
-    s.whole = all_items <= p.grid && 4ll * longest <= 5ll * s.share ? longest : 0;
+    Share s = equal_shares(p, total, all_items, longest);
     if (s.whole > 0) {
-        s.share = s.whole;
-        s.total = static_cast<long long>(all_items) * s.whole;
         work = static_cast<long long>(items) * s.whole;
         work_before = static_cast<long long>(items_before) * s.whole;
     }
@@ -270,6 +280,57 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     return s;
 }
 
+// The same by each warp for itself, without a barrier: 26.8 us for 28.6 and 39.2 for 41.1
+// (16 x 4096 tokens, 24 and 64 rows) with up to 64 sequences; with more the block's threads
+// share the reading of the lengths (1024 sequences: 88 us, each warp for itself 107).
+constexpr int kFewSeqs = 64;
+__device__ __forceinline__ Share find_share_few(const CacheFwdParams& p, int c) {
+    const int lane = threadIdx.x & 31, per = (p.B + 31) >> 5;
+    const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+    long long work = 0;
+    int items = 0, longest = 0;
+    for (int b = b0; b < b1; ++b) {
+        const CacheSeq q = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+        if (blockIdx.x == 0 && threadIdx.x < 32) check_len(p.c, p.st, b);
+        const int n = row_tiles(p, q) * p.Hk;
+        work += static_cast<long long>(q.n) * n;
+        items = min(items + n, 1 << 20);
+        if (q.q_len > 0) longest = max(longest, q.n);
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    long long work_to = work;
+    int items_to = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, work_to, o);
+        const int n = __shfl_up_sync(0xffffffffu, items_to, o);
+        if (lane >= o) work_to += w, items_to += n;
+    }
+    Share s = equal_shares(p, __shfl_sync(0xffffffffu, work_to, 31), __shfl_sync(0xffffffffu, items_to, 31), longest);
+    long long before = work_to - work;
+    if (s.whole > 0) {
+        work = static_cast<long long>(items) * s.whole;
+        before = static_cast<long long>(items_to - items) * s.whole;
+    }
+    const long long x = c * s.share;
+    int found = -1;
+    if (x < s.total && before <= x && x < before + work) {
+        for (int b = b0; b < b1; ++b) {
+            const long long w = seq_work(p, cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b), s.whole);
+            if (x < before + w) {
+                found = b;
+                break;
+            }
+            before += w;
+        }
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, found >= 0);
+    const int src = who ? __ffs(who) - 1 : 0;
+    s.b = __shfl_sync(0xffffffffu, found, src);
+    s.b_first = __shfl_sync(0xffffffffu, before, src);
+    return s;
+}
+
 // Row r (0 .. p.rows - 1) of row tile rt of a sequence: query and head of the group.
 struct RowAt {
     int t, h;
@@ -288,7 +349,7 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // Attention of a few queries: the kernel
 // ---------------------------------------------------------------------------
 // Bound by reading the codes once: 64 sequences of up to 8192 tokens, 32/8 heads, d = 128,
-// one query each: 125 us, 6.3 TB/s.  (With 40 rows a key/value head, 16 x 4096 tokens: 35 us
+// one query each: 122 us, 6.5 TB/s.  (With 40 rows a key/value head, 16 x 4096 tokens: 33 us
 // for 7.5 of reading; three row tiles, latency in 8 warps an SM.)  Each warp walks every
 // kWarps-th block of a segment on its own, with its own running maximum, sums and output;
 // the codes come by asynchronous copies into a ring of its own, so no barrier stands in
@@ -369,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 
     pdl_launch_dependents();
     pdl_wait();
-    const Share sh = find_share(p, blockIdx.x, ssm);
+    const Share sh = p.B <= kFewSeqs ? find_share_few(p, blockIdx.x) : find_share(p, blockIdx.x, ssm);
     if (sh.b < 0) {  // more CTAs than shares
         if (threadIdx.x == 0) p.border[blockIdx.x].c_first = -1;
         return;

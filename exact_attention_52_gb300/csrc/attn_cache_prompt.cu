@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 // The 128 scores 32 at a time.  Only while a row has no maximum is there a pass for
                 // the tile's; after it the weights are formed against m_used as it is, and 32
                 // columns whose sum passes kWeightMax are done again with their own maximum, the
-                // tile's weights before them scaled down (2 x 2048 queries over 16384 keys: 596 us,
+                // tile's weights before them scaled down (2 x 2048 queries over 16384 keys: 600 us,
                 // with a pass for the maximum of each tile 700).  The loops stay rolled and the
                 // mask is formed from bits: the roles' code does not fit the instruction caches
                 // otherwise (with both passes unrolled 1033 us).

@@ -228,6 +228,17 @@ def test_cache_forward_many_sequences_share_the_device():
     run_cache(pool, 8, 1, lens, [0 if n == 0 else 1 for n in lens])
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 64, 65])
+@pytest.mark.parametrize("T,longest", [(1, 60), (1, 900), (3, 300)])
+def test_cache_forward_ragged_batches(T, longest, B):
+    """Shares of ragged batches, whole items and parts, with empty sequences among them."""
+    rng = np.random.default_rng(B + longest)
+    lens = [int(x) for x in rng.integers(0, longest, B)]
+    lens[B // 2], lens[0], lens[-1] = longest, 0, 1
+    pool = Pool(9 + B, B, 2, 64, 16, -(-longest // 16))
+    run_cache(pool, 6, T, lens, [min(n, T) for n in lens])
+
+
 def test_cache_forward_large_scores_and_values():
     """Scores that reach far beyond the first block's maximum, page scales far apart."""
     pool = Pool(9, 2, 2, 128, 16, 20)
