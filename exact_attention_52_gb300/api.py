@@ -1,4 +1,5 @@
-"""Python binding of libattn_sm103a.so (ctypes): argument marshalling only.
+"""Python binding of libattn_sm103a.so (ctypes, and csrc/attn_call.cpp for the streaming
+calls): argument marshalling only.
 
 Every function here checks dtypes, shapes and devices, allocates outputs with
 PyTorch when the caller did not pass them, and calls the C ABI declared in
@@ -20,6 +21,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libattn_sm103a.so")
 # The same library built with device-side range checks (see attn_build_flags).
 DEBUG_LIB_PATH = os.path.join(_PKG, "libattn_sm103a_debug.so")
+CALL_PATH = os.path.join(_PKG, "_attn_call.so")
 
 ATTN_OK = 0
 STATUS_NAMES = {0: "ATTN_OK", -1: "ATTN_ERR_INVALID", -2: "ATTN_ERR_UNSUPPORTED",
@@ -403,9 +405,10 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
 # Sliding window with sinks; paged 8-bit key/value cache
 # ---------------------------------------------------------------------------
 # A decode step runs these for single tokens, where the host's share of a call
-# counts: each function first makes one pass of cheap comparisons, and only when
-# one fails do the functions named _explain_* look for the argument to name.
-# They are handed `torch`, and ask torch._C, for the same reason: an import statement or a
+# counts.  Calls on the current stream are read by csrc/attn_call.cpp, which gives
+# back None for arguments that it does not take: then, or where it is not built,
+# each function here makes one pass of cheap comparisons, and only when one fails
+# do the functions named _explain_* look for the argument to name.  They are handed `torch`, and ask torch._C, for the same reason: an import statement or a
 # look whether CUDA has been set up costs 0.1 to 0.2 us of a 15 us call.
 def _call_stream(torch, device_index, stream):
     """Handle of the stream a call runs on (the current one without an argument)."""
@@ -425,6 +428,39 @@ def _on_stream(stream):
 
     import torch
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+# The compiled half of the binding: (the library that it calls, the module or None).
+_calls = None
+_CALL_FUNCTIONS = ("attn_cache_append", "attn_fwd_cache_workspace_bytes", "attn_fwd_cache", "attn_fwd_sinks",
+                   "attn_bwd_sinks_workspace_bytes", "attn_bwd_sinks")
+
+
+def _compiled_calls():
+    """csrc/attn_call.cpp's module, calling the loaded library; None where it or a GPU is missing."""
+    global _calls
+    lib = load_library()
+    if _calls is None or _calls[0] is not lib:
+        import torch
+        module = None
+        if os.path.exists(CALL_PATH) and torch.cuda.is_available():
+            import importlib.util
+            spec = importlib.util.spec_from_file_location("_attn_call", CALL_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _CALL_FUNCTIONS))
+            torch.cuda.init()
+        _calls = lib, module
+    return _calls[1]
+
+
+def _read(torch, stream, layout):
+    """The compiled half, for a call that it may read (and (device, stream) of the call), or None."""
+    calls = _compiled_calls() if stream is None and layout in ("bhnd", "bnhd") else None
+    if calls is None:
+        return None, None, None
+    dev = torch._C._cuda_getDevice()
+    return calls, dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
 _kept = threading.local()
@@ -557,6 +593,13 @@ def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layo
     j < sinks).  bf16 q [B, H, N, d], k and v [B, Hk, N, d] (``layout`` "bhnd") or [B, N, heads, d]
     ("bnhd"), any strides with a contiguous last dimension.  Returns (O like q, LSE [B, H, N])."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None:
+        done = calls.fwd_sinks(q, k, v, window_left, sinks, window_right, layout == "bnhd", scale, o, lse, dev, handle)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            _check("attn_fwd_sinks", done)
     B, H, Hk, N, d, dev, (qs, ks, vs) = _sinks_args(q, k, v, layout)
     device = q.device
     if o is None or lse is None:
@@ -589,6 +632,14 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
     summed over the query heads that share them.  ``workspace``: ``bwd_sinks_workspace_bytes``
     bytes, one for each call that may overlap."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None:
+        done = calls.bwd_sinks(q, k, v, o, dout, lse, window_left, sinks, window_right, layout == "bnhd", scale, dq, dk,
+                               dv, workspace, dev, handle)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            _check("attn_bwd_sinks", done)
     B, H, Hk, N, d, dev, (qs, ks, vs) = _sinks_args(q, k, v, layout)
     device = q.device
     need = bwd_sinks_workspace_bytes(B, H, Hk, N, d, int(sinks))
@@ -696,6 +747,12 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
     position seq_lens - new_lens + t.  A page's scale is a power of two that covers its largest
     value and grows with it, the codes that are there being rounded again."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None:
+        done = calls.cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens,
+                                  layout == "bnhd", dev, handle)
+        if done is not None:
+            return _check("attn_cache_append", done)
     B, Hk, T, d = _layout_shape(k, layout)
     try:
         dev, bf16 = k.get_device(), torch.bfloat16
@@ -736,6 +793,18 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
     ``workspace``: ``fwd_cache_workspace_bytes`` bytes, one for each call that may overlap; without
     one, the calls of a thread on its current stream share a kept one."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None:
+        ws = workspace
+        if ws is None and not torch._C._cuda_isCurrentStreamCapturing():
+            ws = _kept.__dict__.get((dev, handle))
+        if ws is not None:
+            done = calls.fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_lens, layout == "bnhd",
+                                   scale, window_left, sinks, o, lse, ws, dev, handle)
+            if done.__class__ is tuple:
+                return done
+            if done is not None:
+                _check("attn_fwd_cache", done)
     B, H, T, d = _layout_shape(q, layout)
     try:
         dev, qs, Hk = q.get_device(), _strides4(q, layout), k_pages.shape[1]

@@ -10,6 +10,9 @@ The same sources are also built with ``-DATTN_DEBUG_CHECKS`` into
 is range-checked on the device and a failure is reported through the device
 error word (the stand-in for a memory checker; see attn_build_flags()).
 
+``csrc/attn_call.cpp``, the compiled half of the Python binding, becomes
+``_attn_call.so`` with the host compiler and PyTorch's headers.
+
     python -m exact_attention_52_gb300.build [--verbose]
 """
 
@@ -28,6 +31,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libattn_sm103a.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 DEBUG_LIB_PATH = os.path.join(PKG, "libattn_sm103a_debug.so")
+CALL_PATH = os.path.join(PKG, "_attn_call.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -65,14 +69,36 @@ def _link(objs: list[str], path: str) -> None:
     os.replace(tmp, path)
 
 
+def _build_calls() -> None:
+    """The binding's compiled half (the calls read their arguments in Python where it is missing)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    tmp = CALL_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(root, "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "attn_call.cpp"), "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        if os.path.exists(CALL_PATH):
+            os.remove(CALL_PATH)
+        print(f"{os.path.basename(CALL_PATH)} was not built, calls read their arguments in Python:\n{r.stderr}", file=sys.stderr)
+        return
+    os.replace(tmp, CALL_PATH)
+
+
 def build(verbose: bool = False) -> str:
     """Compile every kernel source twice (release and range-checked debug build),
     link both shared libraries and return the release library's path."""
     os.makedirs(os.path.join(BUILD, "debug"), exist_ok=True)
     srcs = _sources()
     jobs = [(s, False) for s in srcs] + [(s, True) for s in srcs]
-    with cf.ThreadPoolExecutor(max_workers=min(16, len(jobs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, len(jobs) + 1)) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(_compile, jobs))
+        calls.result()
     release, debug = results[:len(srcs)], results[len(srcs):]
     log = "\n".join(err for _, err in release)
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:

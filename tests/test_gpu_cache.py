@@ -732,3 +732,54 @@ def test_calls_that_follow_copies_and_other_streams(T):
         for (wo, wl), go, gl in zip(want, o, lse):
             assert torch.equal(wo.view(torch.int16), go.view(torch.int16)) and torch.equal(wl, gl)
     check_clean()
+
+
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+def test_calls_read_in_python_and_compiled_are_the_same(layout, monkeypatch):
+    """The two halves of the binding make the same call of the same arguments: with outputs
+    and workspaces given and not, and NumPy's integers, which only the one in Python takes."""
+    import torch
+    assert api._compiled_calls() is not None
+    torch.manual_seed(3)
+    B, H, Hk, T, d = 2, 4, 2, 5, 64
+    shape = lambda h, n: (B, h, n, d) if layout == "bhnd" else (B, n, h, d)
+    new = lambda h, n: torch.randn(shape(h, n), device="cuda").bfloat16()
+    kp, vp = (torch.randint(0, 0x70, (12, Hk, 32, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    scales = [torch.full((12, Hk), 2.0 ** -6, device="cuda") for _ in range(2)]
+    table, lens, ql = torch.arange(12, device="cuda", dtype=torch.int32).view(2, 6), i32([100, 7]), i32([5, 3])
+    q, k, v = new(H, T), new(Hk, T), new(Hk, T)
+    qs, ks, vs, do = new(H, 150), new(Hk, 150), new(Hk, 150), new(H, 150)
+    room = torch.empty(max(api.fwd_cache_workspace_bytes(B, H, Hk, T, d), api.bwd_sinks_workspace_bytes(B, H, Hk, 150, d, 3)),
+                       dtype=torch.uint8, device="cuda")
+
+    def run(three, given):
+        pages = [x.clone() for x in (kp, vp, *scales)]
+        o, lse = (torch.empty_like(q), torch.empty(B, H, T, device="cuda")) if given else (None, None)
+        og, lg = (torch.empty_like(qs), torch.empty(B, H, 150, device="cuda")) if given else (None, None)
+        grads = [torch.empty_like(x) if given else None for x in (qs, ks, vs)]
+        ws = room if given else None
+        api.cache_append(k, v, *pages, table, lens, new_lens=ql, layout=layout)
+        if not given:  # makes the kept workspace
+            api.fwd_cache(q, *pages, table, lens, q_lens=ql, layout=layout)
+        # rows behind the last query are left as they were: only those that there are count
+        r = api.fwd_cache(q, *pages, table, lens, q_lens=ql, layout=layout, scale=0.2, window_left=three * 9, sinks=three,
+                          o=o, lse=lse, workspace=ws)
+        assert not given or (r[0] is o and r[1] is lse)
+        there = r[0][1, :, :3] if layout == "bhnd" else r[0][1, :3]
+        s = api.fwd_sinks(qs, ks, vs, three * 9, three, layout=layout, o=og, lse=lg)
+        g = api.bwd_sinks(qs, ks, vs, s[0], do, s[1], three * 9, three, layout=layout, dq=grads[0], dk=grads[1],
+                          dv=grads[2], workspace=ws)
+        assert not given or all(x is y for x, y in zip(g, grads))
+        # dQ is summed by fp32 reductions whose order changes, the others are the same bit for bit
+        return [*pages, r[0][0], r[1][0], there, r[1][1, :, :3], *s, *g[1:]]
+
+    want = run(3, True)
+    for three, given in ((3, False), (np.int64(3), True)):
+        for x, y in zip(want, run(three, given)):
+            assert torch.equal(x, y)
+    monkeypatch.setattr(api, "_compiled_calls", lambda: None)
+    for given in (True, False):
+        for x, y in zip(want, run(3, given)):
+            assert torch.equal(x, y)
+    check_clean()
+
