@@ -1,0 +1,61 @@
+"""csrc/attn_call.cpp without a GPU: it gives back what it does not take, and calls nothing then."""
+
+import ctypes
+import importlib.util
+import os
+
+import pytest
+
+from exact_attention_52_gb300 import api
+
+CALLS = []
+
+
+@pytest.fixture(scope="module")
+def module():
+    pytest.importorskip("torch")
+    if not os.path.exists(api.CALL_PATH):
+        pytest.skip("not built")
+    spec = importlib.util.spec_from_file_location("_attn_call", api.CALL_PATH)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    fake = ctypes.CFUNCTYPE(ctypes.c_size_t)(lambda: CALLS.append(1) or 0)  # stands for every function of the library
+    m.bind(*[ctypes.cast(fake, ctypes.c_void_p).value] * len(api._CALL_FUNCTIONS))
+    yield m
+    lib = api.load_library()
+    m.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in api._CALL_FUNCTIONS))
+
+
+def test_nothing_that_is_no_cuda_tensor_is_taken(module):
+    import torch
+    q = torch.zeros(1, 2, 4, 64).bfloat16()
+    for t in (q, None, 3, "x", q.float(), q[0], torch.zeros(0)):
+        assert module.cache_append(*[t] * 8, None, False, 0, 0) is None
+        assert module.fwd_cache(*[t] * 7, None, False, None, -1, 0, None, None, t, 0, 0) is None
+        assert module.fwd_sinks(t, t, t, 3, 1, 0, True, 0.5, None, None, 0, 0) is None
+        assert module.bwd_sinks(*[t] * 6, 3, 1, 0, False, None, None, None, None, None, 0, 0) is None
+    assert not CALLS
+
+
+def test_a_wrong_number_of_arguments_is_given_back(module):
+    for f in (module.cache_append, module.fwd_cache, module.fwd_sinks, module.bwd_sinks):
+        for n in (0, 1, 11, 13, 16, 18):
+            if n not in (12, 17):
+                assert f(*[None] * n) is None
+    assert not CALLS
+
+
+def test_bind_wants_an_address_for_each_function(module):
+    with pytest.raises(TypeError):
+        module.bind(1, 2)
+
+
+def test_calls_without_a_gpu_name_the_argument():
+    torch = pytest.importorskip("torch")
+    q = torch.zeros(1, 2, 4, 64).bfloat16()
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        api.fwd_sinks(q, q, q, 3, 1)
+    with pytest.raises(ValueError, match="k must be a CUDA tensor"):
+        api.cache_append(q, q, q, q, q, q, q, q)
+    with pytest.raises(ValueError, match="unknown layout"):
+        api.fwd_cache(q, q, q, q, q, q, q, layout="nbhd")
