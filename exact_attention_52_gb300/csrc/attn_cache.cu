@@ -955,28 +955,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     }
 }
 
-// Launches a kernel as a programmatic dependent of the one before it in the stream: it is
-// placed as that kernel ends, and waits for all of it (pdl_wait) before it touches memory.
-// Calls one after the other on a stream: 19.3 -> 17.7 us (32 sequences, 1028 keys each of
-// 16 heads, d = 64), 33.0 -> 31.5 (16 x 4096 tokens, 40 rows), appended prompts 21.7 ->
-// 19.8, 64 x 8192 tokens 126 -> 120.  Only the attention kernel lets its dependent, the
-// join, start early: where the join let the next call's CTAs in among its own, 64 x 8192
-// tokens took 123 - 129.
-template <typename P>
-cudaError_t launch_dependent(void (*kernel)(P), dim3 grid, int threads, int smem, cudaStream_t stream, const P& p) {
-    cudaLaunchAttribute pdl;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cfg.attrs = &pdl;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int D, int NT>
 cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
     using T = DecodeTraits<D, NT>;

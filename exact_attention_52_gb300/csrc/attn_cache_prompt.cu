@@ -237,6 +237,7 @@ __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, PromptWalk
 template <int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const CacheFwdParams p, const int pairs) {
     using T = PromptTraits<D>;
+    pdl_wait();
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* sKV = smem + T::OFF_KV;
@@ -951,8 +952,7 @@ cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.T) * (p.H / p.Hk);
     const int pairs = static_cast<int>((rows + kPairRows - 1) / kPairRows);
     if ((e = dbg_set_word(p.st.word, stream)) != cudaSuccess) return e;
-    cache_prompt_kernel<D><<<p.grid, kPromptThreads, T::SMEM_BYTES, stream>>>(p, pairs);
-    e = cudaGetLastError();
+    e = launch_dependent(cache_prompt_kernel<D>, dim3(static_cast<unsigned>(p.grid)), kPromptThreads, T::SMEM_BYTES, stream, p, pairs);
     return e != cudaSuccess ? e : launch_cache_join(p, 8, stream);
 }
 
