@@ -201,9 +201,9 @@ cudaError_t once_per_device(std::atomic<unsigned long long>& done, F f) {
 // placed as that kernel ends, and waits for all of it (pdl_wait) before it touches memory.
 // Calls one after the other on a stream: 19.3 -> 17.7 us (32 sequences, 1028 keys each of
 // 16 heads, d = 64), 33.0 -> 31.5 (16 x 4096 tokens, 40 rows), appended prompts 21.7 ->
-// 19.8, 64 x 8192 tokens 126 -> 120, prompts of 2 x 100 tokens 18.5 -> 15.9.  Only the attention kernel lets its dependent, the
-// join, start early: where the join let the next call's CTAs in among its own, 64 x 8192
-// tokens took 123 - 129.
+// 19.8, 64 x 8192 tokens 126 -> 120, prompts of 2 x 100 tokens 18.5 -> 15.9.  Only the
+// attention kernel lets its dependent, the join, start early: where the join let the next
+// call's CTAs in among its own, 64 x 8192 tokens took 123 - 129.
 template <typename... P>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream,
                              const std::remove_const_t<P>&... p) {
