@@ -408,8 +408,9 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
 # counts.  Calls on the current stream are read by csrc/attn_call.cpp, which gives
 # back None for arguments that it does not take: then, or where it is not built,
 # each function here makes one pass of cheap comparisons, and only when one fails
-# do the functions named _explain_* look for the argument to name.  They are handed `torch`, and ask torch._C, for the same reason: an import statement or a
-# look whether CUDA has been set up costs 0.1 to 0.2 us of a 15 us call.
+# do the functions named _explain_* look for the argument to name.  They are handed
+# `torch`, and ask torch._C, for the same reason: an import statement or a look
+# whether CUDA has been set up costs 0.1 to 0.2 us.
 def _call_stream(torch, device_index, stream):
     """Handle of the stream a call runs on (the current one without an argument)."""
     if stream is not None:

@@ -717,7 +717,8 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int row = 2 * q + (k & 1) + 8 * (k >> 1);
-                    const uint8_t* at = src + u * T::TILE + T::K_BYTES + (T::VB == 16 ? chunk_at<D>(row, g) : chunk_at<D>(row, g >> 1) + (g & 1) * 8);
+                    const uint8_t* at = src + u * T::TILE + T::K_BYTES +
+                                        (T::VB == 16 ? chunk_at<D>(row, g) : chunk_at<D>(row, g >> 1) + (g & 1) * 8);
                     if constexpr (T::VB == 16) {
                         const uint4 w = *reinterpret_cast<const uint4*>(at);
                         vw[k][0] = w.x, vw[k][1] = w.y, vw[k][2] = w.z, vw[k][3] = w.w;
@@ -931,7 +932,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     };
     const int mine = (c - bd.c_first) * static_cast<int>(gridDim.y) + blockIdx.y, borders = (n - 1) * static_cast<int>(gridDim.y);
     if (n <= kJoinFew) {
-        for (int r = mine + borders * warp; r < rows; r += borders * kJoinWarps) write(r, join(r, 0, n, std::integral_constant<int, 4>{}));
+        for (int r = mine + borders * warp; r < rows; r += borders * kJoinWarps)
+            write(r, join(r, 0, n, std::integral_constant<int, 4>{}));
         return;
     }
     const int per = (n + kJoinWarps - 1) / kJoinWarps;
@@ -965,7 +967,8 @@ cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
     if (attr != cudaSuccess) return attr;
     p.rows = T::ROWS;
     p.grid = sms * T::CTAS_PER_SM < kCacheGridMax ? sms * T::CTAS_PER_SM : kCacheGridMax;
-    const cudaError_t e = launch_dependent(cache_decode_kernel<D, NT>, dim3(static_cast<unsigned>(p.grid)), kThreads, T::SMEM, stream, p);
+    const cudaError_t e = launch_dependent(cache_decode_kernel<D, NT>, dim3(static_cast<unsigned>(p.grid)), kThreads,
+                                           T::SMEM, stream, p);
     return e != cudaSuccess ? e : launch_cache_join(p, 1, stream);
 }
 

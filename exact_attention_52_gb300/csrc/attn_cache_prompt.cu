@@ -952,7 +952,8 @@ cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.T) * (p.H / p.Hk);
     const int pairs = static_cast<int>((rows + kPairRows - 1) / kPairRows);
     if ((e = dbg_set_word(p.st.word, stream)) != cudaSuccess) return e;
-    e = launch_dependent(cache_prompt_kernel<D>, dim3(static_cast<unsigned>(p.grid)), kPromptThreads, T::SMEM_BYTES, stream, p, pairs);
+    e = launch_dependent(cache_prompt_kernel<D>, dim3(static_cast<unsigned>(p.grid)), kPromptThreads, T::SMEM_BYTES,
+                         stream, p, pairs);
     return e != cudaSuccess ? e : launch_cache_join(p, 8, stream);
 }
 

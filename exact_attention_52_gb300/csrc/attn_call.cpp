@@ -261,7 +261,8 @@ PyObject* bwd_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(room > 0);
         Out dq = like_or_given(a[11], q), dk = like_or_given(a[12], k), dv = like_or_given(a[13], v);
         const Rows dqv = rows_like(dq.o, q, dev, bnhd), dkv = rows_like(dk.o, k, dev, bnhd), dvv = rows_like(dv.o, v, dev, bnhd);
-        at::Tensor ws = a[14] == Py_None ? at::empty({static_cast<int64_t>(room)}, q.t->options().dtype(at::kByte)) : tensor(a[14]);
+        const at::Tensor ws = a[14] != Py_None ? tensor(a[14])
+                                               : at::empty({static_cast<int64_t>(room)}, q.t->options().dtype(at::kByte));
         need(ws.is_cuda() && ws.get_device() == dev && ws.nbytes() >= room);
         auto stream = reinterpret_cast<attn_stream_t>(integer(a[16]));
         void* w = ws.data_ptr();
