@@ -72,21 +72,25 @@ def _link(objs: list[str], path: str) -> None:
 def _build_calls() -> None:
     """The binding's compiled half (the calls read their arguments in Python where it is missing)."""
     import sysconfig
-
-    import torch
-    root = os.path.dirname(torch.__file__)
     tmp = CALL_PATH + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(root, "include"),
-           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "attn_call.cpp"), "-o", tmp,
-           "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        if os.path.exists(CALL_PATH):
-            os.remove(CALL_PATH)
-        print(f"{os.path.basename(CALL_PATH)} was not built, calls read their arguments in Python:\n{r.stderr}", file=sys.stderr)
+    try:
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(root, "include"),
+               "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "attn_call.cpp"), "-o", tmp,
+               "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        why = r.stderr if r.returncode != 0 else None
+    except (ImportError, OSError) as e:
+        why = str(e)
+    if why is None:
+        os.replace(tmp, CALL_PATH)
         return
-    os.replace(tmp, CALL_PATH)
+    if os.path.exists(CALL_PATH):
+        os.remove(CALL_PATH)
+    print(f"{os.path.basename(CALL_PATH)} was not built, calls read their arguments in Python:\n{why}", file=sys.stderr)
 
 
 def build(verbose: bool = False) -> str:
