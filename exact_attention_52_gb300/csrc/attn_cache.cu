@@ -51,18 +51,16 @@ __global__ void __launch_bounds__(kAppendThreads, 8) cache_append_kernel(const C
     pdl_wait();
     const int hk = blockIdx.y, b = blockIdx.z >> 1;
     const bool is_v = blockIdx.z & 1;
-    const int page = p.c.page_size, cap = p.c.max_pages * page;
+    const int page = p.c.page_size;
     const int len = p.c.seq_lens[b];
     const int m = p.new_lens ? min(max(p.new_lens[b], 0), p.T) : p.T;
+    if (blockIdx.x == 0 && hk == 0 && !is_v && threadIdx.x == 0) check_len(p.c, p.st, b);
     if (m == 0 || len <= 0) return;
     const int first = len - m;  // position of new token 0 (negative: it is not written)
     const int pg = max(first, 0) / page + static_cast<int>(blockIdx.x);
+    if (pg >= p.c.max_pages) return;  // behind the table; below it positions stay far inside 32 bits
     const int lo = max(first, pg * page), hi = min(len, pg * page + page);  // new positions in this page
     if (lo >= hi) return;
-    if (lo >= cap) {
-        if (threadIdx.x == 0) record_device_error(p.st, ATTN_DEVERR_PAGE, 0x302);
-        return;
-    }
     const int pid = __ldg(p.c.table + b * p.c.table_stride + pg);
     if (static_cast<unsigned>(pid) >= static_cast<unsigned>(p.c.num_pages)) {
         if (threadIdx.x == 0) record_device_error(p.st, ATTN_DEVERR_PAGE, 0x303);

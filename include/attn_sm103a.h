@@ -309,8 +309,9 @@ attn_status attn_fwd_fp8(const void* q8, const void* k8, const void* v8, float s
  *   seq_lens     : int32 [B], tokens of each sequence, the new ones included.
  *   page_size    : a power of two, 16 .. 1024; max_pages * page_size <= 2^30.
  * The lengths and the table stay on the device: a captured call may be replayed
- * after they change.  An entry outside [0, num_pages), or a length that leaves
- * the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE; no
+ * after they change.  An entry outside [0, num_pages), or a length that is
+ * negative or leaves the table (of a sequence without new tokens or queries too),
+ * makes the next attn_check_device_error() return ATTN_ERR_PAGE; no
  * access leaves the pool, attn_cache_append leaves such a page unwritten, and
  * the rows of attn_fwd_cache that needed it are undefined.  Tensors that a call
  * writes have no zero stride over more than one element (ATTN_ERR_INVALID).

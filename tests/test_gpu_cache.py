@@ -401,6 +401,26 @@ def test_bad_pages_and_lengths_are_reported():
     assert api.check_device_error() == (0, 0)
 
 
+@pytest.mark.parametrize("new", [0, 1, 3])
+@pytest.mark.parametrize("length", [-1, -2 ** 31, 65, 67, 68, 2 ** 31 - 1, 2 ** 31 - 16])
+def test_append_reports_lengths_outside_the_table(length, new):
+    """A length that is negative or behind the table is reported, tokens of it or not; what it
+    has inside the table is written, and nothing else; the other sequence as ever."""
+    pool = Pool(41, 2, 1, 64, 16, 4)
+    dev = pool.dev()
+    k, kv = bf16(pool.rng, (2, 1, 3, 64))
+    api.cache_append(k, k, *dev, i32([length, 40]), new_lens=i32([new, 2]))
+    assert api.check_device_error()[0] == -5
+    inside = max(0, 64 - (length - new)) if 64 < length <= 64 + new else 0  # first of the new tokens
+    if inside:
+        streaming.cache_append(kv[:1, :, :inside], kv[:1, :, :inside], pool.k, pool.v, pool.ks, pool.vs, pool.table[:1],
+                               [64], [inside])
+    streaming.cache_append(kv[1:], kv[1:], pool.k, pool.v, pool.ks, pool.vs, pool.table[1:], [40], [2])
+    for got, want in zip(dev[:4], (pool.k, pool.v, pool.ks, pool.vs)):
+        assert np.array_equal(got.cpu().numpy(), want.astype(got.cpu().numpy().dtype))
+    check_clean()
+
+
 def test_reads_and_writes_past_32_bits():
     """A pool of 2.1 GB per tensor whose last pages are in use."""
     import torch
