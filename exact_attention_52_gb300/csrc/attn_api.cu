@@ -869,7 +869,8 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
                            float scale, int window_left, int sinks, attn_stream_t stream) {
     attn_status rc = check_sizes(B, H, T, d, scale, 0);
     if (rc != ATTN_OK) return rc;
-    if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(window_left, sinks - 1)) != ATTN_OK) return rc;
+    if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(window_left, 0)) != ATTN_OK) return rc;
+    if (sinks < 0) return ATTN_ERR_INVALID;
     CacheFwdParams p;
     if ((rc = cache_view(cache, B, &p.c)) != ATTN_OK) return rc;
     if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(q_lens) & 3u) != 0)

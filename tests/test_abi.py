@@ -110,6 +110,18 @@ def test_invalid_arguments_are_rejected_before_launch(lib):
                         None) == INVALID
 
 
+def test_cache_attention_refuses_any_negative_bound(lib):
+    """window_left below -1 and sinks below 0, down to the least integer, are refused before
+    the device is looked at (no GPU here: a device call would fail otherwise)."""
+    fake = ctypes.c_void_p(1 << 20)
+    st = api.Strides(64, 64, 64)
+    cache = api._CACHE.pack(*[1 << 20] * 2, *[64] * 6, *[1 << 20] * 3, 1, 1 << 20, 1, 16, 1)
+    call = lambda left, sinks: lib.attn_fwd_cache(cache, fake, st, fake, st, fake, fake, None, 1, 1, 1, 1, 64, 0.125,
+                                                  left, sinks, None)
+    for left, sinks in ((-2, 0), (-2 ** 31, 0), (3, -1), (3, -2 ** 31), (-1, -2 ** 31)):
+        assert call(left, sinks) == -1, (left, sinks)
+
+
 def test_binding_raises_when_library_missing(tmp_path):
     with pytest.raises(RuntimeError, match="not built"):
         api.load_library(str(tmp_path / "libattn_sm103a.so"))
