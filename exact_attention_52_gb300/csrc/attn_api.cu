@@ -184,6 +184,12 @@ attn_status check_group(int H, int Hk) {
 
 attn_status check_window(int wl, int wr) { return (wl >= -1 && wr >= -1) ? ATTN_OK : ATTN_ERR_INVALID; }
 
+// A bound past the sequence's length is that length: the kernels add it to a position.
+void within_length(int N, int* left, int* right) {
+    if (*left > N) *left = N;
+    if (*right > N) *right = N;
+}
+
 long long npad(int N) { return (static_cast<long long>(N) + kTile - 1) / kTile * kTile; }
 
 int sink_tiles_of(int sinks) { return (sinks + kTile - 1) / kTile; }
@@ -277,6 +283,7 @@ attn_status fwd_run(const void* q, const Strides& qs, const void* k, const Strid
     if (rc != ATTN_OK) return rc;
     if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(win_left, win_right)) != ATTN_OK)
         return rc;
+    within_length(N, &win_left, &win_right);
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse))
         return ATTN_ERR_INVALID;
     if (!strides_ok(qs, 2) || !strides_ok(ks, 2) || !strides_ok(vs, 2) || !strides_ok(os, 2))
@@ -410,6 +417,7 @@ attn_status bwd_main_run(const void* q, const Strides& qs, const void* k, const 
     attn_status rc;
     if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(win_left, win_right)) != ATTN_OK)
         return rc;
+    within_length(N, &win_left, &win_right);
     const int causal = (win_left == -1 && win_right == 0) ? 1 : 0;
     BwdCall c;
     if ((rc = bwd_prepare(workspace, B, H, N, d, scale, causal, split, sink_items_of(B, Hk, sinks), &c)) != ATTN_OK)

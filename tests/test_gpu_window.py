@@ -43,3 +43,25 @@ def test_window_rejects_bounds_below_minus_one():
     q = torch.zeros(1, 1, 128, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(api.AttnError):
         api.fwd_window(q, q, q, -2, 0)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (20, 2 ** 31 - 1), (2 ** 31 - 200, -1)])
+def test_windows_as_large_as_they_get(window, d):
+    """A bound beyond the sequence, up to the largest integer, is the bound of its length: the
+    same bits (but for dQ, whose sums have no fixed order) through both kinds of call."""
+    import torch
+    inp = make_inputs_gqa(1, 2, 1, 333, d, seed=d, with_grad=True)
+    q, k, v, do = (bf16_to_device(x) for x in (inp.q_bits, inp.k_bits, inp.v_bits, inp.do_bits))
+    short = tuple(min(w, 333) for w in window)
+    o, lse = api.fwd_window(q, k, v, *short)
+    grads = api.bwd_window(q, k, v, o, do, lse, *short)
+    o_ref, _ = oracle.forward_gqa(*decoded(inp)[:3], 1.0 / np.sqrt(d), False, window=short)
+    assert bf16_out_err(device_bf16_to_f64(o), o_ref) <= TOL_O_MAXABS
+    for o2, lse2 in (api.fwd_window(q, k, v, *window), api.fwd_strided(q, k, v, layout="bhnd", window=window)):
+        assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(lse, lse2)
+    for g in (api.bwd_window(q, k, v, o, do, lse, *window),
+              api.bwd_strided(q, k, v, o, do, lse, layout="bhnd", window=window)):
+        for x, y in zip(g[1:], grads[1:]):
+            assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    assert api.check_device_error() == (0, 0)
