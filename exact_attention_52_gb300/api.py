@@ -108,6 +108,12 @@ def _check(fn: str, status: int) -> None:
         raise AttnError(fn, status)
 
 
+def _c_int(x) -> int:
+    """A bound or count as a C int.  ctypes would keep the low 32 bits of a larger one, another
+    number; the nearest C int means the same, as no length is above it."""
+    return min(max(int(x), -2 ** 31), 2 ** 31 - 1)
+
+
 def _stream_handle(stream) -> int:
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
@@ -166,7 +172,7 @@ def fwd_splitkv(q, k, v, num_splits: int = 0, scale: float | None = None, causal
     if lse is None:
         lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     lib = load_library()
-    need = int(lib.attn_fwd_splitkv_workspace_bytes(B, H, N, d, int(num_splits)))
+    need = int(lib.attn_fwd_splitkv_workspace_bytes(B, H, N, d, _c_int(num_splits)))
     if need == 0:
         raise ValueError("invalid sizes or num_splits")
     if workspace is None:
@@ -174,7 +180,7 @@ def fwd_splitkv(q, k, v, num_splits: int = 0, scale: float | None = None, causal
     _check("attn_fwd_splitkv", lib.attn_fwd_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                                     o.data_ptr(), lse.data_ptr(),
                                                     workspace.data_ptr(), B, H, N, d, scale,
-                                                    int(bool(causal)), int(num_splits),
+                                                    int(bool(causal)), _c_int(num_splits),
                                                     _stream_handle(stream)))
     return o, lse
 
@@ -195,7 +201,7 @@ def fwd_window(q, k, v, window_left: int, window_right: int, scale: float | None
         lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     _check("attn_fwd_window", load_library().attn_fwd_window(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, Hk, N, d,
-        scale, int(window_left), int(window_right), _stream_handle(stream)))
+        scale, _c_int(window_left), _c_int(window_right), _stream_handle(stream)))
     return o, lse
 
 
@@ -219,7 +225,7 @@ def bwd_window(q, k, v, o, dout, lse, window_left: int, window_right: int,
     _check("attn_bwd_window", load_library().attn_bwd_window(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), B, H, Hk, N, d, scale,
-        int(window_left), int(window_right), _stream_handle(stream)))
+        _c_int(window_left), _c_int(window_right), _stream_handle(stream)))
     return dq, dk, dv
 
 
@@ -373,7 +379,7 @@ def fwd_strided(q, k, v, layout: str = "bnhd", scale: float | None = None, windo
     _check("attn_fwd_strided", load_library().attn_fwd_strided(
         q.data_ptr(), _bhnd_strides(q, layout), k.data_ptr(), _bhnd_strides(k, layout),
         v.data_ptr(), _bhnd_strides(v, layout), o.data_ptr(), _bhnd_strides(o, layout),
-        lse.data_ptr(), B, H, Hk, N, d, scale, int(window[0]), int(window[1]),
+        lse.data_ptr(), B, H, Hk, N, d, scale, _c_int(window[0]), _c_int(window[1]),
         _stream_handle(stream)))
     return o, lse
 
@@ -396,8 +402,8 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
     _check("attn_bwd_strided", load_library().attn_bwd_strided(
         q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o),
         dout.data_ptr(), st(dout), lse.data_ptr(), dq.data_ptr(), st(dq), dk.data_ptr(), st(dk),
-        dv.data_ptr(), st(dv), workspace.data_ptr(), B, H, Hk, N, d, scale, int(window[0]),
-        int(window[1]), _stream_handle(stream)))
+        dv.data_ptr(), st(dv), workspace.data_ptr(), B, H, Hk, N, d, scale, _c_int(window[0]),
+        _c_int(window[1]), _stream_handle(stream)))
     return dq, dk, dv
 
 
@@ -616,14 +622,14 @@ def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layo
         raise ValueError(f"o and lse must be tensors on {device}")
     _check("attn_fwd_sinks", load_library().attn_fwd_sinks(
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), os_, lse.data_ptr(),
-        B, H, Hk, N, d, 1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left),
-        int(window_right), int(sinks), _call_stream(torch, dev, stream)))
+        B, H, Hk, N, d, 1.0 / math.sqrt(d) if scale is None else float(scale), _c_int(window_left),
+        _c_int(window_right), _c_int(sinks), _call_stream(torch, dev, stream)))
     return o, lse
 
 
 @functools.lru_cache(maxsize=256)
 def bwd_sinks_workspace_bytes(B: int, H: int, Hk: int, N: int, d: int, sinks: int) -> int:
-    return int(load_library().attn_bwd_sinks_workspace_bytes(B, H, Hk, N, d, sinks))
+    return int(load_library().attn_bwd_sinks_workspace_bytes(*map(_c_int, (B, H, Hk, N, d, sinks))))
 
 
 def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right: int = 0,
@@ -643,7 +649,7 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
             _check("attn_bwd_sinks", done)
     B, H, Hk, N, d, dev, (qs, ks, vs) = _sinks_args(q, k, v, layout)
     device = q.device
-    need = bwd_sinks_workspace_bytes(B, H, Hk, N, d, int(sinks))
+    need = bwd_sinks_workspace_bytes(B, H, Hk, N, d, _c_int(sinks))
     if need == 0:
         raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, N {N}, d {d}, sinks {sinks}")
     if dq is None or dk is None or dv is None or workspace is None:
@@ -670,7 +676,7 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
         q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, o.data_ptr(), os_, dout.data_ptr(),
         dos, lse.data_ptr(), dq.data_ptr(), dqs, dk.data_ptr(), dks, dv.data_ptr(), dvs, workspace.data_ptr(), B, H,
         Hk, N, d,
-        1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(window_right), int(sinks),
+        1.0 / math.sqrt(d) if scale is None else float(scale), _c_int(window_left), _c_int(window_right), _c_int(sinks),
         _call_stream(torch, dev, stream)))
     return dq, dk, dv
 
@@ -776,7 +782,7 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
 
 @functools.lru_cache(maxsize=256)
 def fwd_cache_workspace_bytes(B: int, H: int, Hk: int, T: int, d: int) -> int:
-    return int(load_library().attn_fwd_cache_workspace_bytes(B, H, Hk, T, d))
+    return int(load_library().attn_fwd_cache_workspace_bytes(*map(_c_int, (B, H, Hk, T, d))))
 
 
 def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_lens=None,
@@ -847,5 +853,5 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
     _check("attn_fwd_cache", load_library().attn_fwd_cache(
         cache, q.data_ptr(), qs, o.data_ptr(), os_, lse.data_ptr(), workspace.data_ptr(),
         None if q_lens is None else q_lens.data_ptr(), B, H, Hk, T, d,
-        1.0 / math.sqrt(d) if scale is None else float(scale), int(window_left), int(sinks), handle))
+        1.0 / math.sqrt(d) if scale is None else float(scale), _c_int(window_left), _c_int(sinks), handle))
     return o, lse

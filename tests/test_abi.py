@@ -122,6 +122,20 @@ def test_cache_attention_refuses_any_negative_bound(lib):
         assert call(left, sinks) == -1, (left, sinks)
 
 
+def test_numbers_past_a_c_int_keep_their_meaning(lib):
+    """More sinks than a C int holds are all tokens, not the low 32 bits' number of them; a
+    size that it does not hold is no size."""
+    for x, want in ((2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1), (-2 ** 32 - 1, -2 ** 31), (-1, -1), (0, 0), (7, 7)):
+        assert api._c_int(x) == want
+    for d in (64, 128):
+        all_of_them = api.bwd_sinks_workspace_bytes(1, 2, 2, 1000, d, 1000)
+        assert all_of_them > api.bwd_sinks_workspace_bytes(1, 2, 2, 1000, d, 1)
+        for sinks in (2 ** 31, 2 ** 32, 2 ** 32 + 1, 10 ** 30):
+            assert api.bwd_sinks_workspace_bytes(1, 2, 2, 1000, d, sinks) == all_of_them
+        assert api.bwd_sinks_workspace_bytes(1, 2, 2, 1000, d, -2 ** 32) == 0
+        assert api.fwd_cache_workspace_bytes(2 ** 32 + 1, 1, 1, 1, d) == 0
+
+
 def test_binding_raises_when_library_missing(tmp_path):
     with pytest.raises(RuntimeError, match="not built"):
         api.load_library(str(tmp_path / "libattn_sm103a.so"))

@@ -237,3 +237,25 @@ def test_sinks_refusals():
     with pytest.raises(ValueError):
         api.bwd_sinks(q, k, k, o, q, lse[:, :2], 10, 2)
     check_clean()
+
+
+@pytest.mark.parametrize("big", [2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 5, 10 ** 20])
+def test_bounds_past_a_c_int(big):
+    """A window or a number of sinks beyond every length, whatever its low 32 bits are: the
+    causal call, in each call that takes one."""
+    import torch
+    inp = make_inputs_gqa(1, 2, 2, 300, 64, seed=6, with_grad=True)
+    q, k, v, do = (bf16_to_device(x) for x in (inp.q_bits, inp.k_bits, inp.v_bits, inp.do_bits))
+    o, lse = api.fwd(q, k, v, causal=True)
+    _, dk, dv = api.bwd(q, k, v, o, do, lse, causal=True)
+    for o2, lse2 in (api.fwd_sinks(q, k, v, big, 3), api.fwd_window(q, k, v, big, 0),
+                     api.fwd_strided(q, k, v, layout="bhnd", window=(big, 0)), api.fwd_sinks(q, k, v, 10, big)):
+        # every key a sink: the mask is the causal one, its sums are in another order
+        assert (o2.double() - o.double()).abs().max() <= 2.0 ** -7 * o.double().abs().max()
+        assert (lse2 - lse).abs().max() <= TOL_LSE_ABS
+    for g in (api.bwd_sinks(q, k, v, o, do, lse, big, 3), api.bwd_window(q, k, v, o, do, lse, big, 0),
+              api.bwd_strided(q, k, v, o, do, lse, layout="bhnd", window=(big, 0)),
+              api.bwd_sinks(q, k, v, o, do, lse, 10, big)):
+        assert rel_fro(device_bf16_to_f64(g[1]), device_bf16_to_f64(dk)) <= TOL_GRAD_RELFRO
+        assert rel_fro(device_bf16_to_f64(g[2]), device_bf16_to_f64(dv)) <= TOL_GRAD_RELFRO
+    check_clean()
