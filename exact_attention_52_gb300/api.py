@@ -362,7 +362,7 @@ def _bhnd_shape(t, layout):
 
 def fwd_strided(q, k, v, layout: str = "bnhd", scale: float | None = None, window=(-1, -1),
                 o=None, lse=None, stream=None):
-    """Forward on bf16 tensors of any strides with a contiguous last dimension.
+    """Forward on bf16 tensors of any strides (multiples of 8) with a contiguous last dimension.
     ``layout`` says how the 4 dimensions are ordered ("bnhd": [B, N, H, d] as
     produced by most projections; "bhnd": [B, H, N, d]).  Returns (O in the same
     layout as q, LSE [B, H, N])."""
@@ -598,7 +598,7 @@ def fwd_sinks(q, k, v, window_left: int, sinks: int, window_right: int = 0, layo
     """Sliding-window forward whose first ``sinks`` tokens stay visible: key j visible to query i
     iff j <= i + window_right (-1: no bound) and (window_left is -1, or j >= i - window_left, or
     j < sinks).  bf16 q [B, H, N, d], k and v [B, Hk, N, d] (``layout`` "bhnd") or [B, N, heads, d]
-    ("bnhd"), any strides with a contiguous last dimension.  Returns (O like q, LSE [B, H, N])."""
+    ("bnhd"), any strides (multiples of 8) with a contiguous last dimension.  Returns (O like q, LSE [B, H, N])."""
     import torch
     calls, dev, handle = _read(torch, stream, layout)
     if calls is not None:
@@ -707,7 +707,7 @@ def _explain_cache(device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_ta
         if t.shape != (P, Hk) or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous [{P}, {Hk}]")
     _explain_on(device, "page_table", page_table, torch.int32, 2)
-    if page_table.shape[0] != B or page_table.shape[1] < 1 or page_table.stride(1) != 1:
+    if page_table.shape[0] != B or page_table.shape[1] < 1 or 1 not in (page_table.shape[1], page_table.stride(1)):
         raise ValueError(f"page_table must be [{B}, pages] with contiguous rows")
     _explain_lens(device, "seq_lens", seq_lens, B)
     if new_lens is not None:
@@ -730,7 +730,7 @@ def _cache_arg(torch, dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale,
               and dev == k_pages.get_device() == v_pages.get_device() == k_scale.get_device()
               == v_scale.get_device() == page_table.get_device() == seq_lens.get_device()
               and k_scale.shape == (P, Hk) and v_scale.shape == (P, Hk) and k_scale.is_contiguous()
-              and v_scale.is_contiguous() and rows == B and cols >= 1 and t1 == 1
+              and v_scale.is_contiguous() and rows == B and cols >= 1 and 1 in (cols, t1)
               and seq_lens.shape == (B,) and seq_lens.is_contiguous()
               and (new_lens is None or (new_lens.dtype is i32 and new_lens.get_device() == dev
                                         and new_lens.shape == (B,) and new_lens.is_contiguous())))
@@ -746,9 +746,10 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
                  layout: str = "bhnd", stream=None):
     """Write new tokens into a paged 8-bit cache, in place.
 
-    k, v: bf16 [B, Hk, T, d] (``layout`` "bhnd") or [B, T, Hk, d] ("bnhd"), any strides with
-    a contiguous last dimension.  k_pages, v_pages: uint8 E4M3 codes [pages, Hk, page_size, d],
-    any strides with a contiguous last dimension; k_scale, v_scale: fp32 [pages, Hk].
+    k, v: bf16 [B, Hk, T, d] (``layout`` "bhnd") or [B, T, Hk, d] ("bnhd"), any strides
+    (multiples of 8) with a contiguous last dimension.  k_pages, v_pages: uint8 E4M3 codes
+    [pages, Hk, page_size, d], any strides (multiples of 16) with a contiguous last dimension;
+    k_scale, v_scale: fp32 [pages, Hk].
     page_table: int32 [B, max_pages]; seq_lens: int32 [B], tokens of each sequence after the
     call; new_lens: int32 [B], how many of the T tokens are new (default: all): token t goes to
     position seq_lens - new_lens + t.  A page's scale is a power of two that covers its largest

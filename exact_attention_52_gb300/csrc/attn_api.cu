@@ -523,15 +523,18 @@ attn_status bwd_run(const void* q, const Strides& qs, const void* k, const Strid
     return dq_convert_run(dq, dqs, workspace, B, H, N, d, scale, stream, &sink);
 }
 
-Strides from_abi(const attn_strides_t& s) {
+// Strides of a [nb, nh, nn, d] view.  A stride over one element is only ever multiplied by 0,
+// and PyTorch may hold any number there: a row's length takes its place, which no check of
+// alignment turns down.
+Strides from_abi(const attn_strides_t& s, int nb, int nh, int nn, int d) {
     Strides r;
-    r.b = s.b;
-    r.h = s.h;
-    r.n = s.n;
+    r.b = nb == 1 ? d : s.b;
+    r.h = nh == 1 ? d : s.h;
+    r.n = nn == 1 ? d : s.n;
     return r;
 }
 
-attn_status cache_view(const attn_cache_t* c, int B, CacheView* out) {
+attn_status cache_view(const attn_cache_t* c, int B, int Hk, int d, CacheView* out) {
     if (c == nullptr || !aligned16(c->k_pages) || !aligned16(c->v_pages)) return ATTN_ERR_INVALID;
     for (const void* p : {static_cast<const void*>(c->k_scale), static_cast<const void*>(c->v_scale),
                           static_cast<const void*>(c->page_table), static_cast<const void*>(c->seq_lens)})
@@ -541,8 +544,8 @@ attn_status cache_view(const attn_cache_t* c, int B, CacheView* out) {
         return ATTN_ERR_INVALID;
     const int ps = c->page_size;
     if (ps < 16 || ps > 1024 || (ps & (ps - 1)) != 0 || c->max_pages > (1 << 30) / ps) return ATTN_ERR_INVALID;
-    out->ks = from_abi(c->ks);
-    out->vs = from_abi(c->vs);
+    out->ks = from_abi(c->ks, c->num_pages, Hk, ps, d);
+    out->vs = from_abi(c->vs, c->num_pages, Hk, ps, d);
     if (!strides_ok(out->ks, 1) || !strides_ok(out->vs, 1)) return ATTN_ERR_INVALID;
     out->k_pages = static_cast<uint8_t*>(c->k_pages);
     out->v_pages = static_cast<uint8_t*>(c->v_pages);
@@ -634,8 +637,10 @@ attn_status attn_fwd_strided(const void* q, attn_strides_t qs, const void* k, at
                              const void* v, attn_strides_t vs, void* o, attn_strides_t os, float* lse,
                              int B, int H, int Hk, int N, int d, float scale, int window_left,
                              int window_right, attn_stream_t stream) {
-    return fwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), lse, B, H, Hk,
-                   N, d, scale, window_left, window_right, stream);
+    const auto of_q = [&](const attn_strides_t& s) { return from_abi(s, B, H, N, d); };
+    const auto of_k = [&](const attn_strides_t& s) { return from_abi(s, B, Hk, N, d); };
+    return fwd_run(q, of_q(qs), k, of_k(ks), v, of_k(vs), o, of_q(os), lse, B, H, Hk, N, d, scale,
+                   window_left, window_right, stream);
 }
 
 size_t attn_fwd_splitkv_workspace_bytes(int B, int H, int N, int d, int num_splits) {
@@ -805,17 +810,21 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
                              attn_strides_t dqs, void* dk, attn_strides_t dks, void* dv,
                              attn_strides_t dvs, void* workspace, int B, int H, int Hk, int N, int d,
                              float scale, int window_left, int window_right, attn_stream_t stream) {
-    return bwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), dout,
-                   from_abi(dos), lse, dq, from_abi(dqs), dk, from_abi(dks), dv, from_abi(dvs),
+    const auto of_q = [&](const attn_strides_t& s) { return from_abi(s, B, H, N, d); };
+    const auto of_k = [&](const attn_strides_t& s) { return from_abi(s, B, Hk, N, d); };
+    return bwd_run(q, of_q(qs), k, of_k(ks), v, of_k(vs), o, of_q(os), dout,
+                   of_q(dos), lse, dq, of_q(dqs), dk, of_k(dks), dv, of_k(dvs),
                    workspace, B, H, Hk, N, d, scale, window_left, window_right, stream);
 }
 
 attn_status attn_fwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks, const void* v,
                            attn_strides_t vs, void* o, attn_strides_t os, float* lse, int B, int H, int Hk, int N,
                            int d, float scale, int window_left, int window_right, int sinks, attn_stream_t stream) {
-    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK || !distinct(from_abi(os), B, H, N))
+    const auto of_q = [&](const attn_strides_t& s) { return from_abi(s, B, H, N, d); };
+    const auto of_k = [&](const attn_strides_t& s) { return from_abi(s, B, Hk, N, d); };
+    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK || !distinct(of_q(os), B, H, N))
         return ATTN_ERR_INVALID;
-    return fwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), lse, B, H, Hk, N, d, scale,
+    return fwd_run(q, of_q(qs), k, of_k(ks), v, of_k(vs), o, of_q(os), lse, B, H, Hk, N, d, scale,
                    window_left, window_right, stream, SplitArgs(), sinks);
 }
 
@@ -832,11 +841,13 @@ attn_status attn_bwd_sinks(const void* q, attn_strides_t qs, const void* k, attn
                            const float* lse, void* dq, attn_strides_t dqs, void* dk, attn_strides_t dks, void* dv,
                            attn_strides_t dvs, void* workspace, int B, int H, int Hk, int N, int d, float scale,
                            int window_left, int window_right, int sinks, attn_stream_t stream) {
-    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK || !distinct(from_abi(dqs), B, H, N) ||
-        !distinct(from_abi(dks), B, Hk, N) || !distinct(from_abi(dvs), B, Hk, N))
+    const auto of_q = [&](const attn_strides_t& s) { return from_abi(s, B, H, N, d); };
+    const auto of_k = [&](const attn_strides_t& s) { return from_abi(s, B, Hk, N, d); };
+    if (sink_mask(N, &window_left, &window_right, &sinks) != ATTN_OK || !distinct(of_q(dqs), B, H, N) ||
+        !distinct(of_k(dks), B, Hk, N) || !distinct(of_k(dvs), B, Hk, N))
         return ATTN_ERR_INVALID;
-    return bwd_run(q, from_abi(qs), k, from_abi(ks), v, from_abi(vs), o, from_abi(os), dout, from_abi(dos), lse, dq,
-                   from_abi(dqs), dk, from_abi(dks), dv, from_abi(dvs), workspace, B, H, Hk, N, d, scale, window_left,
+    return bwd_run(q, of_q(qs), k, of_k(ks), v, of_k(vs), o, of_q(os), dout, of_q(dos), lse, dq,
+                   of_q(dqs), dk, of_k(dks), dv, of_k(dvs), workspace, B, H, Hk, N, d, scale, window_left,
                    window_right, stream, true, sinks);
 }
 
@@ -846,13 +857,13 @@ attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_str
     attn_status rc = check_sizes(B, Hk, T, d, 1.f, 0);
     if (rc != ATTN_OK) return rc;
     CacheAppendParams p;
-    if ((rc = cache_view(cache, B, &p.c)) != ATTN_OK) return rc;
+    if ((rc = cache_view(cache, B, Hk, d, &p.c)) != ATTN_OK) return rc;
     if (B > 32767 || Hk > 65535) return ATTN_ERR_INVALID;
     if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(new_lens) & 3u) != 0) return ATTN_ERR_INVALID;
     p.k = k;
     p.v = v;
-    p.ks = from_abi(ks);
-    p.vs = from_abi(vs);
+    p.ks = from_abi(ks, B, Hk, T, d);
+    p.vs = from_abi(vs, B, Hk, T, d);
     if (!strides_ok(p.ks, 2) || !strides_ok(p.vs, 2)) return ATTN_ERR_INVALID;
     if (!distinct(p.c.ks, p.c.num_pages, Hk, p.c.page_size) || !distinct(p.c.vs, p.c.num_pages, Hk, p.c.page_size))
         return ATTN_ERR_INVALID;
@@ -880,7 +891,7 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(window_left, 0)) != ATTN_OK) return rc;
     if (sinks < 0) return ATTN_ERR_INVALID;
     CacheFwdParams p;
-    if ((rc = cache_view(cache, B, &p.c)) != ATTN_OK) return rc;
+    if ((rc = cache_view(cache, B, Hk, d, &p.c)) != ATTN_OK) return rc;
     if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(q_lens) & 3u) != 0)
         return ATTN_ERR_INVALID;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
@@ -889,8 +900,8 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
     if (rows > (1 << 30) || B * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;
     p.q = q;
     p.o = o;
-    p.qs = from_abi(qs);
-    p.os = from_abi(os);
+    p.qs = from_abi(qs, B, H, T, d);
+    p.os = from_abi(os, B, H, T, d);
     if (!strides_ok(p.qs, 2) || !strides_ok(p.os, 2) || !distinct(p.os, B, H, T)) return ATTN_ERR_INVALID;
     p.lse = lse;
     p.q_lens = q_lens;

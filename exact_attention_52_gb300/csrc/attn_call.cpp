@@ -107,7 +107,7 @@ attn_cache_t cache_of(PyObject* const* a, int dev, int B, int Hk, int D) {  // k
     const at::Tensor& table = tensor(a[4], at::kInt, 2, dev);
     const auto n = k.sizes(), ks = k.strides(), vs = v.strides();
     need(v.sizes() == n && n[1] == Hk && n[3] == D && ks[3] == 1 && vs[3] == 1);
-    need(table.size(0) == B && table.size(1) >= 1 && table.stride(1) == 1);
+    need(table.size(0) == B && table.size(1) >= 1 && (table.stride(1) == 1 || table.size(1) == 1));
     attn_cache_t c;
     c.k_pages = k.data_ptr();
     c.v_pages = v.data_ptr();

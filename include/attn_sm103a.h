@@ -51,7 +51,7 @@ typedef struct CUstream_st* attn_stream_t; /* same type as cudaStream_t */
  * (stride 1).  A dense [B, heads, N, d] tensor has n = d, h = N*d,
  * b = heads*N*d; PyTorch's [B, N, heads, d] layout has n = heads*d, h = d,
  * b = N*heads*d.  Every stride times the element size must be a multiple of
- * 16 bytes. */
+ * 16 bytes; the stride of a dimension of one element is not looked at. */
 typedef struct {
     int64_t b, h, n;
 } attn_strides_t;

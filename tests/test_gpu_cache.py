@@ -421,6 +421,47 @@ def test_append_reports_lengths_outside_the_table(length, new):
     check_clean()
 
 
+def odd_single(t, dims):
+    """t with a stride of 1 or 3 over its dimensions of one element, as PyTorch may hold it."""
+    strides = list(t.stride())
+    for n, i in enumerate(dims):
+        assert t.shape[i] == 1
+        strides[i] = 1 + 2 * (n % 2)
+    return t.as_strided(t.shape, strides)
+
+
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+def test_strides_over_one_element_are_not_looked_at(layout):
+    """One token of one sequence and head, or a single page: the strides of such dimensions are
+    not multiples of anything, and the call is the one of dense tensors."""
+    import torch
+    pool = Pool(42, 1, 1, 64, 16, 1, spare=0)
+    dev, odd = pool.dev(), [odd_single(t, range(t.dim() - 2)) if t.dim() == 4 else t for t in pool.dev()]
+    assert odd[4].shape == (1, 1)
+    odd[4] = odd_single(odd[4], (0, 1))
+    q, k = (bf16(pool.rng, (1, 1, 1, 64), layout)[0] for _ in range(2))
+    lens = i32([5])
+    want = api.fwd_cache(q, *dev, lens, layout=layout)
+    got = api.fwd_cache(odd_single(q, range(3)), *odd, lens, layout=layout, o=odd_single(torch.empty_like(q), range(3)))
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    api.cache_append(k, k, *dev, lens, layout=layout)
+    api.cache_append(odd_single(k, range(3)), odd_single(k, (2, 1, 0)), *odd, lens, layout=layout)
+    assert all(torch.equal(x, y) for x, y in zip(dev, odd))
+    # new tokens as a column, [B, Hk, d, 1] seen as [B, Hk, 1, d]; two sequences of one page each
+    pool = Pool(43, 2, 2, 128, 32, 1)
+    dev, odd = pool.dev(), pool.dev()
+    odd[4] = odd[4].as_strided((2, 1), (1, 2))
+    q, k = (bf16(pool.rng, (2, h, 1, 128))[0] for h in (4, 2))
+    column = lambda t: t.reshape(*t.shape[:2], 128, 1).transpose(2, 3)
+    assert column(k).stride()[2] == 1 and odd[4].stride()[1] == 2
+    lens = i32([7, 30])
+    for args, x, y in ((dev, k, q), (odd, column(k), column(q))):
+        api.cache_append(x, x, *args, lens)
+        want, got = got, api.fwd_cache(y, *args, lens)
+    assert all(torch.equal(x, y) for x, y in zip((*want, *dev), (*got, *odd)))
+    check_clean()
+
+
 def test_reads_and_writes_past_32_bits():
     """A pool of 2.1 GB per tensor whose last pages are in use."""
     import torch

@@ -259,3 +259,22 @@ def test_bounds_past_a_c_int(big):
         assert rel_fro(device_bf16_to_f64(g[1]), device_bf16_to_f64(dk)) <= TOL_GRAD_RELFRO
         assert rel_fro(device_bf16_to_f64(g[2]), device_bf16_to_f64(dv)) <= TOL_GRAD_RELFRO
     check_clean()
+
+
+@pytest.mark.parametrize("N", [1, 150])
+def test_strides_over_one_element_are_not_looked_at(N):
+    """One sequence of one head (and of one token): those dimensions may have any stride."""
+    import torch
+    inp = make_inputs_gqa(1, 1, 1, N, 64, seed=8, with_grad=True)
+    dense = [bf16_to_device(x) for x in (inp.q_bits, inp.k_bits, inp.v_bits, inp.do_bits)]
+    odd = [x.as_strided(x.shape, (3, 1, 5 if N == 1 else 64, 1)) for x in dense]
+    for fwd, bwd in ((lambda q, k, v: api.fwd_sinks(q, k, v, 20, 2), lambda *a: api.bwd_sinks(*a, 20, 2)),
+                     (lambda q, k, v: api.fwd_strided(q, k, v, layout="bhnd", window=(20, 0)),
+                      lambda *a: api.bwd_strided(*a, layout="bhnd", window=(20, 0)))):
+        o, lse = fwd(*dense[:3])
+        g = bwd(*dense[:3], o, dense[3], lse)
+        o2, lse2 = fwd(*odd[:3])
+        g2 = bwd(*odd[:3], o2, odd[3], lse2)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        assert torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
+    check_clean()
