@@ -15,7 +15,9 @@ import functools
 import math
 import os
 import struct
+import sys
 import threading
+import warnings
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libattn_sm103a.so")
@@ -443,19 +445,38 @@ _CALL_FUNCTIONS = ("attn_cache_append", "attn_fwd_cache_workspace_bytes", "attn_
                    "attn_bwd_sinks_workspace_bytes", "attn_bwd_sinks")
 
 
+def _call_tag(torch):
+    """PyTorch and Python that csrc/attn_call.cpp is compiled for: it reads their objects directly."""
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def _load_calls(torch, lib):
+    """csrc/attn_call.cpp's module, calling ``lib``; None, with a warning, where it does not load
+    or was built for another PyTorch or Python: the arguments are then read in Python."""
+    try:
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("_attn_call", CALL_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if module.built_for != _call_tag(torch):
+            raise ImportError(f"it was built for {module.built_for}, this is {_call_tag(torch)}")
+        module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _CALL_FUNCTIONS))
+        return module
+    except (ImportError, OSError, AttributeError, TypeError, SystemError) as e:
+        warnings.warn(f"{os.path.basename(CALL_PATH)} is not used, calls read their arguments in Python: {e}; "
+                      "run `python -m exact_attention_52_gb300.build`", RuntimeWarning, stacklevel=4)
+        return None
+
+
 def _compiled_calls():
-    """csrc/attn_call.cpp's module, calling the loaded library; None where it or a GPU is missing."""
+    """The compiled half of the binding, calling the loaded library; None where it or a GPU is missing."""
     global _calls
     lib = load_library()
     if _calls is None or _calls[0] is not lib:
         import torch
         module = None
         if os.path.exists(CALL_PATH) and torch.cuda.is_available():
-            import importlib.util
-            spec = importlib.util.spec_from_file_location("_attn_call", CALL_PATH)
-            module = importlib.util.module_from_spec(spec)
-            spec.loader.exec_module(module)
-            module.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _CALL_FUNCTIONS))
+            module = _load_calls(torch, lib)
             torch.cuda.init()
         _calls = lib, module
     return _calls[1]

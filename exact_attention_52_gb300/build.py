@@ -75,9 +75,12 @@ def _build_calls() -> None:
     tmp = CALL_PATH + ".tmp"
     try:
         import torch
+
+        from .api import _call_tag
         root = os.path.dirname(torch.__file__)
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f'-DATTN_BUILT_FOR="{_call_tag(torch)}"',
                "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(root, "include"),
                "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "attn_call.cpp"), "-o", tmp,
                "-L" + os.path.join(root, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]

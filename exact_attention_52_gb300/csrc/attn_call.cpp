@@ -301,4 +301,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_call", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__attn_call() { return PyModule_Create(&module); }
+// built_for: the PyTorch and Python whose headers this was compiled with (set by the build),
+// which the binding compares with those that it runs in.
+PyMODINIT_FUNC PyInit__attn_call() {
+    PyObject* m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", ATTN_BUILT_FOR) != 0) Py_CLEAR(m);
+    return m;
+}

@@ -59,3 +59,34 @@ def test_calls_without_a_gpu_name_the_argument():
         api.cache_append(q, q, q, q, q, q, q, q)
     with pytest.raises(ValueError, match="unknown layout"):
         api.fwd_cache(q, q, q, q, q, q, q, layout="nbhd")
+
+
+@pytest.mark.parametrize("what", ["no library", "another library", "another PyTorch"])
+def test_a_module_that_does_not_fit_is_not_used(what, monkeypatch, tmp_path, module):
+    """A file that cannot be loaded, or one built for another PyTorch or Python, leaves the calls
+    to the half in Python, with a warning; what a call then answers is Python's."""
+    torch = pytest.importorskip("torch")
+    path = api.CALL_PATH
+    if what == "no library":
+        path = tmp_path / "_attn_call.so"
+        path.write_bytes(b"not a library")
+    elif what == "another library":
+        path = api.LIB_PATH
+    else:
+        monkeypatch.setattr(torch, "__version__", "1.0")
+    monkeypatch.setattr(api, "CALL_PATH", str(path))
+    monkeypatch.setattr(api, "_calls", None)
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)  # as on a GPU box, but for the device
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    with pytest.warns(RuntimeWarning, match="read their arguments in Python"):
+        assert api._compiled_calls() is None
+    assert api._compiled_calls() is None  # once
+    q = torch.zeros(1, 2, 4, 64).bfloat16()
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+        api.fwd_sinks(q, q, q, 3, 1)
+
+
+def test_the_module_says_what_it_was_built_for(module):
+    import torch
+    assert module.built_for == api._call_tag(torch)
