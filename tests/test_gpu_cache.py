@@ -662,6 +662,31 @@ def test_calls_of_two_threads_on_one_stream():
     check_clean()
 
 
+def test_kept_workspaces_are_given_back():
+    """What calls of this thread keep, on two streams, is back in the allocator after
+    release_workspaces, and the calls' results are not touched."""
+    import torch
+    pool = Pool(63, 2, 2, 128, 64, 10)
+    dev, lens = pool.dev(), i32([600, 500])
+    q = bf16(pool.rng, (2, 16, 70, 128))[0]
+    api.release_workspaces()
+    room = api.fwd_cache_workspace_bytes(2, 16, 2, 70, 128)
+    before, outs = torch.cuda.memory_allocated(), []
+    for s in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append(api.fwd_cache(q, *dev, lens))
+    taken = torch.cuda.memory_allocated() - before
+    assert taken >= 2 * room
+    api.release_workspaces()
+    assert torch.cuda.memory_allocated() - before <= taken - 2 * room
+    outs.append(api.fwd_cache(q, *dev, lens))
+    torch.cuda.synchronize()
+    for o, lse in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(lse, outs[0][1])
+    check_clean()
+
+
 def test_a_graph_keeps_no_workspace_of_eager_calls():
     """Two graphs captured without a workspace, replayed at once on two streams."""
     import torch
