@@ -133,6 +133,16 @@ __device__ PromptUnit prompt_unit(const CacheFwdParams& p, int b, int pair) {
     return u;
 }
 
+// Tiles [first, end) of a segment [v0, v1), tile t0 of its CTA the first, that lie among the
+// CTA's tiles lo .. hi (none: INT_MAX, -1).
+struct TileSpan {
+    int first, end;
+};
+__host__ __device__ __forceinline__ TileSpan segment_span(int lo, int hi, int t0, int v0, int v1) {
+    if (hi < lo || hi < t0 || lo - t0 >= v1 - v0) return {v0, v0};
+    return {v0 + (lo > t0 ? lo - t0 : 0), v0 + (hi - t0 < v1 - v0 ? hi - t0 + 1 : v1 - v0)};
+}
+
 // A CTA's share: key tiles [x, x_end) of the line on which the units' items lie end to
 // end (each unit once per key/value head), starting in unit `unit`, before which lie
 // unit_first key tiles.  unit < 0: nothing.
@@ -824,15 +834,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             if (n > 0) {
                 // NaN values of the segment that the row sees (they stood as 0 in the products); by
                 // now both groups' products are done, so every value of it has been looked at
-                const int t0 = tile_no - (w.v1 - w.v0);
-                const int first = max(t0, *static_cast<volatile int*>(nan_tiles)) - t0 + w.v0;
-                const int last = min(tile_no - 1, *static_cast<volatile int*>(nan_tiles + 1)) - t0 + w.v0;
-                if (first <= last) {
+                const TileSpan span = segment_span(*static_cast<volatile int*>(nan_tiles),
+                                                   *static_cast<volatile int*>(nan_tiles + 1),
+                                                   tile_no - (w.v1 - w.v0), w.v0, w.v1);
+                if (span.first < span.end) {
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t nan = 0u;  // bit i: column 32 c + i
 #pragma unroll 1
-                        for (int x = first * kTile; x < (last + 1) * kTile; ++x) {
+                        for (int x = span.first * kTile; x < span.end * kTile; ++x) {
                             const int tok = w.u.tile(x / kTile) * kTile + x % kTile;
                             if (!row_ok || tok > pos || (tok < key_min && tok >= p.sinks)) continue;
                             const int pid = __ldg(p.c.table + w.b * p.c.table_stride + (tok >> p.c.page_shift));
