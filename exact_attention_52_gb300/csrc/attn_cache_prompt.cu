@@ -834,9 +834,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             if (n > 0) {
                 // NaN values of the segment that the row sees (they stood as 0 in the products); by
                 // now both groups' products are done, so every value of it has been looked at
-                const TileSpan span = segment_span(*static_cast<volatile int*>(nan_tiles),
-                                                   *static_cast<volatile int*>(nan_tiles + 1),
-                                                   tile_no - (w.v1 - w.v0), w.v0, w.v1);
+                // (lane 0's reading counts: the converters may be at the next segment, and all lanes
+                // have to take the same side)
+                const int lo = __shfl_sync(0xffffffffu, *static_cast<volatile int*>(nan_tiles), 0);
+                const int hi = __shfl_sync(0xffffffffu, *static_cast<volatile int*>(nan_tiles + 1), 0);
+                const TileSpan span = segment_span(lo, hi, tile_no - (w.v1 - w.v0), w.v0, w.v1);
                 if (span.first < span.end) {
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
