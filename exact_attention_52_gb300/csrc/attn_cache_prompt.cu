@@ -103,23 +103,31 @@ __device__ __forceinline__ bool wait_in_line(uint32_t bar, uint32_t parity, vola
 struct PromptUnit {
     int len, q_len, rows;
     int first_pos;  // position of query 0 (negative: rows before the first token see nothing)
+    int pos_lo, pos_hi;  // positions of the pair's first and last row
     int key_lo;     // first key of the window of the pair's first query
     int n_sink, lo, dual, n, n0, n1;
-    __device__ int tile(int t) const { return t < n_sink ? t : lo + t - n_sink; }
+    __host__ __device__ int tile(int t) const { return t < n_sink ? t : lo + t - n_sink; }
+    // Every row of the pair sees every token of key tile t.  Those of a walk that it does not
+    // are the few at the diagonal, the window's edge and the last sink.
+    __host__ __device__ bool all_see(int t, int left, int sinks) const {
+        const int kv0 = tile(t) * kTile;
+        return kv0 + kTile - 1 <= pos_lo && (left < 0 || kv0 >= pos_hi - left || kv0 + kTile <= sinks);
+    }
 };
 
-__device__ PromptUnit prompt_unit(const CacheFwdParams& p, int b, int pair) {
+__host__ __device__ inline PromptUnit prompt_unit(const CacheFwdParams& p, int b, int pair) {
     PromptUnit u;
     const int G = p.H / p.Hk, cap = p.c.max_pages * p.c.page_size;
     u.len = min(max(p.c.seq_lens[b], 0), cap);
     u.q_len = p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
     u.rows = u.q_len * G;
     u.first_pos = u.len - u.q_len;
-    u.n = u.n0 = u.n1 = u.n_sink = u.lo = u.key_lo = u.dual = 0;
+    u.n = u.n0 = u.n1 = u.n_sink = u.lo = u.key_lo = u.dual = u.pos_lo = u.pos_hi = 0;
     const int r0 = pair * kPairRows;
     if (r0 >= u.rows) return u;  // no such pair: no work
-    const int pos_lo = max(0, u.first_pos + r0 / G);
-    u.key_lo = p.left < 0 ? 0 : max(0, pos_lo - p.left);
+    u.pos_lo = u.first_pos + r0 / G;
+    u.pos_hi = u.first_pos + min(u.rows - 1, r0 + kPairRows - 1) / G;
+    u.key_lo = p.left < 0 ? 0 : max(0, max(0, u.pos_lo) - p.left);
     u.lo = u.key_lo / kTile;
     u.n_sink = min((min(p.sinks, u.key_lo) + kTile - 1) / kTile, u.lo);
     auto tiles = [&](int row_hi) {  // up to the key tile of the last position of rows .. row_hi
@@ -255,7 +263,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + T::NBARS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* nan_tiles = reinterpret_cast<int*>(tmem_slot + 2);  // first and last key tile of this CTA with a NaN value
+    // first and last key tile of this CTA with a NaN value that not every row of its pair sees
+    int* nan_tiles = reinterpret_cast<int*>(tmem_slot + 2);
     const uint32_t bar0 = smem_u32(bars);
     const uint32_t b_q = bar0;  // + 8 g
     auto b_kv_full = [&](int s) { return bar0 + 8u * (2 + s); };
@@ -371,7 +380,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 const int round = idx / T::KV_SLOTS;
                 return round == 0 || wait_in_line(b_kv_empty(idx % T::KV_SLOTS), (round - 1) & 1, abort_flag, p.st, SITE_KV_EMPTY);
             };
-            auto convert = [&](const uint4 (&buf)[2 * NI], bool values) {
+            auto convert = [&](const uint4 (&buf)[2 * NI], int t, bool values) {
                 const int slot = idx % T::KV_SLOTS;
                 uint8_t* dst = sKV + slot * T::TILE_BYTES;
                 uint32_t nan[4] = {0u, 0u, 0u, 0u};  // a byte's top bit: a NaN code (7F or FF) in its column
@@ -395,10 +404,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         *reinterpret_cast<uint4*>(dst + more + (at0 ^ sw)) = make_uint4(h[0], h[1], h[2], h[3]);
                         *reinterpret_cast<uint4*>(dst + more + (at1 ^ sw)) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
-                // A weight of 0 times NaN is NaN: NaN values stand as 0 in the products, and the
-                // rows that see one get it at the end of the segment.
+                // A weight of 0 times NaN is NaN: right where every row sees the tile, and elsewhere
+                // NaN values stand as 0 in the products, and the rows that see one get it at the end
+                // of the segment.
                 if (values) {
-                    if (__any_sync(0xffffffffu, ((nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u) != 0u)) {
+                    if (__any_sync(0xffffffffu, ((nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u) != 0u) &&
+                        !w.u.all_see(t, p.left, p.sinks)) {
 #pragma unroll 1
                         for (int i = 0; i < 4 * NI; ++i) {
                             const int k = (i >> 1) % NI;
@@ -460,7 +471,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     scales[(tile_no % T::SCALES) * 8 + 2 * cw + lane] = make_float4(sk, lg2_approx(sv), rcp_approx(sv), 0.f);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_scale + 8u * (tile_no % T::SCALES));
-                convert(kb, false);
+                convert(kb, w.v0 + i, false);
                 ++tile_no;
                 if (i + 1 < tiles) {
                     tok0 = first_tok(w.v0 + i + 1);
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     load_scales(tok0, pid);
                 }
                 if (!(ok = claim())) break;
-                convert(vb, true);
+                convert(vb, w.v0 + i, true);
             }
         }
     } else if (warp >= 8) {
@@ -832,38 +843,54 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 continue;  // the only tile was group 0's
             }
             if (n > 0) {
-                // NaN values of the segment that the row sees (they stood as 0 in the products); by
-                // now both groups' products are done, so every value of it has been looked at
+                // NaN values that the row sees in tiles that not every row sees (they stood as 0 in
+                // the products); by now both groups' products are done, so every value of the
+                // segment has been looked at.  Such tiles are few, however long the segment: the
+                // look takes some 0.1 ms each.
                 // (lane 0's reading counts: the converters may be at the next segment, and all lanes
                 // have to take the same side)
                 const int lo = __shfl_sync(0xffffffffu, *static_cast<volatile int*>(nan_tiles), 0);
                 const int hi = __shfl_sync(0xffffffffu, *static_cast<volatile int*>(nan_tiles + 1), 0);
                 const TileSpan span = segment_span(lo, hi, tile_no - (w.v1 - w.v0), w.v0, w.v1);
                 if (span.first < span.end) {
+                    uint32_t nan[D / 32] = {};  // bit i of word c: column 32 c + i
 #pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t nan = 0u;  // bit i: column 32 c + i
+                    for (int t = span.first; t < span.end; ++t) {
+                        if (w.u.all_see(t, p.left, p.sinks)) continue;
+                        const int tile0 = w.u.tile(t) * kTile;
 #pragma unroll 1
-                        for (int x = span.first * kTile; x < span.end * kTile; ++x) {
-                            const int tok = w.u.tile(x / kTile) * kTile + x % kTile;
+                        for (int tok = tile0; tok < tile0 + kTile; ++tok) {
                             if (!row_ok || tok > pos || (tok < key_min && tok >= p.sinks)) continue;
                             const int pid = __ldg(p.c.table + w.b * p.c.table_stride + (tok >> p.c.page_shift));
                             if (static_cast<unsigned>(pid) >= static_cast<unsigned>(p.c.num_pages)) continue;
-                            const uint32_t* codes = reinterpret_cast<const uint32_t*>(
-                                p.c.v_pages + pid * p.c.vs.b + w.hk * p.c.vs.h + (tok & (p.c.page_size - 1)) * p.c.vs.n + 32 * c);
-#pragma unroll 1
-                            for (int e = 0; e < 8; ++e) {
-                                const uint32_t y = ((__ldg(codes + e) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                                nan |= (y >> 7 & 1u | y >> 14 & 2u | y >> 21 & 4u | y >> 28 & 8u) << (4 * e);
+                            const uint4* codes = reinterpret_cast<const uint4*>(
+                                p.c.v_pages + pid * p.c.vs.b + w.hk * p.c.vs.h + (tok & (p.c.page_size - 1)) * p.c.vs.n);
+                            uint4 x[D / 16];
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) x[c] = __ldg(codes + c);
+#pragma unroll
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t bits = 0u;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const uint32_t u = e == 0 ? x[c].x : e == 1 ? x[c].y : e == 2 ? x[c].z : x[c].w;
+                                    const uint32_t y = ((u & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                                    bits |= (y >> 7 & 1u | y >> 14 & 2u | y >> 21 & 4u | y >> 28 & 8u) << (4 * e);
+                                }
+                                nan[c / 2] |= bits << (16 * (c & 1));
                             }
                         }
-                        if (!__any_sync(0xffffffffu, nan != 0u)) continue;
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        if (!__any_sync(0xffffffffu, nan[c] != 0u)) continue;
                         uint32_t o[32];
                         tmem_ld32(tO + 32 * c, o);
                         tmem_ld_wait(o);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (nan >> i & 1u) o[i] = 0x7FC00000u;
+                            if (nan[c] >> i & 1u) o[i] = 0x7FC00000u;
                         tmem_st32(tO + 32 * c, o);
                         tmem_st_wait();
                     }

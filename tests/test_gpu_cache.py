@@ -370,6 +370,46 @@ def test_nan_values_of_a_lone_query_tile(T, d):
     run_cache(pool, Hk, T, [n] * B, None)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_values_far_apart_in_a_long_prompt(d):
+    """Segments of some 800 key tiles, several a CTA, with NaN values in the first and the last
+    key tile and one amid: NaN where a row sees one, and elsewhere the bits of the call on
+    zeros in their place; the look for them is bounded, so the call takes about as long."""
+    import torch
+    torch.manual_seed(d)
+    Hk, T, n, page = 40, 600, 131072 - 5, 1024
+    table = torch.randperm(128, device="cuda", dtype=torch.int32).view(1, 128)
+    kp, vp = (torch.randint(0, 0x78, (128, Hk, page, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((128, Hk), 2.0 ** -8, device="cuda") for _ in range(2))
+    q, lens = torch.randn(1, Hk, T, d, device="cuda").bfloat16(), i32([n])
+    at = [(0, 0, 5), (1, 0, 5), (1, n - 1, 7), (2, n - 1, 0), (3, n - 300, d - 1), (4, 70000, 33), (39, n - 2, 1), (39, 17, 2)]
+
+    def put(code):
+        for h, j, c in at:
+            vp[table[0, j // page], h, j % page, c] = code
+
+    def timed():
+        ends = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+        ends[0].record()
+        out = api.fwd_cache(q, kp, vp, ks, vs, table, lens)
+        ends[1].record()
+        torch.cuda.synchronize()
+        return out, ends[0].elapsed_time(ends[1])
+
+    put(0)
+    timed()
+    (want, lse), clean = timed()
+    put(0x7F)
+    (o, lse2), found = timed()
+    check_clean()
+    nan = torch.zeros_like(want, dtype=torch.bool)
+    for h, j, c in at:
+        nan[0, h, max(0, j - (n - T)):, c] = True
+    assert torch.equal(torch.isnan(o), nan) and not torch.isnan(want).any()
+    assert torch.equal(o[~nan], want[~nan]) and torch.equal(lse, lse2)
+    assert found <= 5 * clean + 20, (clean, found)  # ms: some seven tiles to look through a segment
+
+
 def test_bad_pages_and_lengths_are_reported():
     import torch
     pool = Pool(12, 2, 1, 64, 16, 4)
