@@ -357,7 +357,7 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // multiplies the scores, the value scale is added, as its log2, to the exponent,
 // so that the weights given to the products are 2^(score + log2 sv - m) with the
 // running maximum m taken over score + log2 sv, and the sum of the probabilities
-// takes them back by 1 / sv.  m is raised, and the output rescaled, only when a
+// takes them back by 1 / sv (kScaleReach).  m is raised, and the output rescaled, only when a
 // score passes it by more than kWeightSlack; a weight is lost to f16's underflow below
 // 2^-31 of the largest.
 //
@@ -593,17 +593,21 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 #pragma unroll
         for (int n = 0; n < NT; ++n) m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
         float sk = 1.f, lsv = 0.f, isv = 1.f;  // of this lane's tile of the batch in use
-        uint32_t whole = 0;
+        uint32_t whole = 0, far = 0;           // far: tiles whose value scale is beyond kScaleReach
         auto row_sees = [&](int ps, int j) { return j <= ps && (p.left < 0 || j >= ps - p.left || j < p.sinks); };
 
         int stage = 0;
-        for (int i = 0; i < n_my; ++i) {
-            if ((i & 15) == 0) {  // batch i / 16, whose loads went out with its first copies
-                sk = sk_next;
-                lsv = lg2_approx(sv_next);
-                isv = rcp_approx(sv_next);
-                whole = whole_next;
-            }
+        auto next_batch = [&]() {  // batch i / 16, whose loads went out with its first copies
+            sk = sk_next;
+            lsv = lg2_approx(sv_next);
+            isv = rcp_approx(sv_next);
+            whole = whole_next;
+            far = __ballot_sync(0xffffffffu, !(fabsf(lsv) <= kScaleReach));
+        };
+        // apart_tag: a second copy of the code for walks with far value scales, whose sums (of 2^u)
+        // are in stat, so that the first has nothing more to hold
+        auto step = [&](auto apart_tag, int i) {
+            constexpr bool apart = decltype(apart_tag)::value;
             cp_async_wait<T::STAGES - 2>();
             __syncwarp();  // block i is there for every lane, and block i - 1 has been read
             issue(i + T::STAGES - 1, stage == 0 ? T::STAGES - 1 : stage - 1);
@@ -656,6 +660,29 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                 t_sk[u] = __shfl_sync(0xffffffffu, sk, src0 + u);
                 t_lsv[u] = __shfl_sync(0xffffffffu, lsv, src0 + u);
                 t_isv[u] = __shfl_sync(0xffffffffu, isv, src0 + u);
+            }
+            if constexpr (apart) {  // ---- the sums ----
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float2* const at = stat + warp * T::ROWS + 8 * n + 2 * q + r;
+                        const float2 us = *at;
+                        const float f0 = score_factor(rq[n][r], t_sk[0]), f1 = score_factor(rq[n][r], t_sk[1]);
+                        const float s0 = sf[0][n][r] * f0, s1 = sf[0][n][2 + r] * f0;
+                        const float s2 = sf[1][n][r] * f1, s3 = sf[1][n][2 + r] * f1;
+                        float u = fmaxf(fmaxf(s0, s1), fmaxf(s2, s3));
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, x));
+                        u = fmaxf(u, us.x);
+                        const float sub = u == -INFINITY ? 0.f : u;
+                        float sum = ex2_approx(s0 - sub) + ex2_approx(s1 - sub) + ex2_approx(s2 - sub) + ex2_approx(s3 - sub);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                        __syncwarp();
+                        if (g == 0) *at = make_float2(u, fmaf(us.y, us.x == u ? 1.f : ex2_approx(us.x - u), sum));
+                        __syncwarp();
+                    }
             }
             // ---- score + log2 sv, and the running maximum ----
             bool passes = false;
@@ -776,12 +803,55 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                     });
                 }
             }
+        };
+        int i = 0;
+        for (; i < n_my; ++i) {
+            if ((i & 15) == 0) next_batch();
+            if (((far >> (2 * i & 31)) & 3u) != 0u) break;
+            step(std::false_type{}, i);
+        }
+        const bool apart = i < n_my;
+        if (apart) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {  // what the walk has summed so far
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) l[n][r] += __shfl_xor_sync(0xffffffffu, l[n][r], x);
+                    if (g == 0)
+                        stat[warp * T::ROWS + 8 * n + 2 * q + r] =
+                            make_float2(l[n][r] != 0.f ? m[n][r] - kWeightShift : -INFINITY, l[n][r]);
+                }
+            __syncwarp();
+            for (bool first = true; i < n_my; ++i, first = false) {
+                if ((i & 15) == 0 && !first) next_batch();
+                step(std::true_type{}, i);
+            }
         }
         cp_async_wait<0>();
 
         // ---- join the warps ----
         __syncwarp();  // every lane is done with its ring
         float* ow = reinterpret_cast<float*>(my);
+        if (apart) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float2 us = stat[warp * T::ROWS + 8 * n + 2 * q + r];
+                    float half;
+                    plain_units(m[n][r], l[n][r], us.x, us.y, half);
+                    if (g != 0) l[n][r] = 0.f;  // the lanes' sums are added up
+#pragma unroll
+                    for (int j = 0; j < T::NJ; ++j) {
+                        o[n][j][r] *= half;
+                        o[n][j][r] *= half;
+                        o[n][j][2 + r] *= half;
+                        o[n][j][2 + r] *= half;
+                    }
+                }
+            __syncwarp();  // stat is written again
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll

@@ -22,7 +22,7 @@
 // 601 us, 1.2 PFLOP/s.  Codes are turned into f16 and not used as E4M3 operands, because
 // then Q and the weights would have to be E4M3 too (2^-4 relative).  A page's scales enter
 // in fp32 as in the kernel for few queries: score * key scale, + log2 of the value scale
-// in the exponent, and 1 / value scale in the sum.
+// in the exponent, and 1 / value scale in the sum (kScaleReach).
 //
 // The work is shared out as there: items laid end to end by their key tiles, an
 // equal share for each CTA, unfinished segments joined by a second kernel.  Whole
@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "cache_ops.cuh"
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             float sk = 1.f, sv = 1.f;
             auto load_scales = [&](int tok0, const int (&pid)[2]) {
                 const int i = lane & 1;
+                sv = 1.f;
                 if (lane < 2 && needed(tok0 + 16 * i)) {
                     const long long at = static_cast<long long>(i ? pid[1] : pid[0]) * p.Hk + w.hk;
                     sk = __ldg(p.c.k_scale + at);
@@ -467,8 +469,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 load(vb, vbase, p.c.vs, tok0, pid);
                 if (!(ok = claim())) break;
                 // the scales' entry of the tile is free now as well (see the softmax)
-                if (lane < 2)
-                    scales[(tile_no % T::SCALES) * 8 + 2 * cw + lane] = make_float4(sk, lg2_approx(sv), rcp_approx(sv), 0.f);
+                if (lane < 2) {
+                    const float lsv = lg2_approx(sv);
+                    scales[(tile_no % T::SCALES) * 8 + 2 * cw + lane] =
+                        make_float4(sk, lsv, rcp_approx(sv), fabsf(lsv) <= kScaleReach ? 0.f : 1.f);
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_scale + 8u * (tile_no % T::SCALES));
                 convert(kb, w.v0 + i, false);
@@ -666,22 +671,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
 
             float m_used = -INFINITY;  // running maximum of score + log2 sv (log2 units), possibly stale
             float l_sum = 0.f;         // sum of 2^(score - m_used + kWeightShift) (value scales taken back out)
-            for (int j = 0; j < n; ++j) {
-                // Scales of key tile j.  Its entry is written again for the tile SCALES further
-                // on, once that tile's K slot is free: the one of V(j + 1) (five slots, four
-                // entries) or K(j + 4) (eight and eight), which products read that were issued
-                // after this warp had arrived for tile j.
+            float u = -INFINITY;       // apart (see kScaleReach): l_sum is of 2^(score - u)
+            // Scales of key tile j.  Its entry is written again for the tile SCALES further
+            // on, once that tile's K slot is free: the one of V(j + 1) (five slots, four
+            // entries) or K(j + 4) (eight and eight), which products read that were issued
+            // after this warp had arrived for tile j.
+            auto wait_scales = [&](int j) {
+                const int tn = tile_no + (dual ? 2 * j + g : j);
+                return wait_in_line(b_scale + 8u * (tn % T::SCALES), (tn / T::SCALES) & 1, abort_flag, p.st, SITE_SCALE);
+            };
+            // apart_tag: a second copy of the code, so that the first has nothing more to hold
+            auto step = [&](auto apart_tag, int j) -> bool {
+                constexpr bool apart = decltype(apart_tag)::value;
                 const int ti = dual ? 2 * j + g : j, tn = tile_no + ti;  // tile of the segment, and of all
                 const int kv0 = w.u.tile(w.v0 + ti) * kTile;
                 const int c_lo = key_min - kv0, c_hi = pos - kv0, c_sink = p.sinks - kv0;
                 const bool masked = __any_sync(0xffffffffu, (c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1);
-                if (!wait_in_line(b_scale + 8u * (tn % T::SCALES), (tn / T::SCALES) & 1, abort_flag, p.st, SITE_SCALE) ||
-                    !wait_in_line(b_sf, (s_seen + j) & 1, abort_flag, p.st, SITE_S_FULL)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
                 const float4* sc = scales + (tn % T::SCALES) * 8;
+                if (!wait_in_line(b_sf, (s_seen + j) & 1, abort_flag, p.st, SITE_S_FULL)) return false;
+                tc_fence_after();
                 // The 128 scores 32 at a time.  Only while a row has no maximum is there a pass for
                 // the tile's; after it the weights are formed against m_used as it is, and 32
                 // columns whose sum passes kWeightMax are done again with their own maximum, the
@@ -723,13 +731,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     if (!(mx > m_used)) return 1.f;
                     if (m_used != -INFINITY) mx = m_used + ceilf(mx - m_used);
                     const float a = ex2_approx(m_used - mx);  // 0 while m_used is -inf
-                    l_sum *= a;
+                    if (!apart) l_sum *= a;
                     tile_l *= a;
                     alpha *= a;
                     m_used = mx;
                     rescale_o = j > 0;
                     return a;
                 };
+                if constexpr (apart) {
+#pragma unroll 1
+                    for (int c = 0; c < kTile; c += 8) {
+                        uint32_t x[8];
+                        tmem_ld8(tS + c, x);
+                        const float f = score_factor(rq, sc[c >> 4].x);
+                        float mx = u, sum = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const bool seen = c + i <= c_hi && (c + i >= c_lo || c + i < c_sink);
+                            x[i] = f2u(seen ? u2f(x[i]) * f : -INFINITY);
+                            mx = fmaxf(mx, u2f(x[i]));
+                        }
+                        const float sub = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sum += ex2_approx(u2f(x[i]) - sub);
+                        l_sum = fmaf(l_sum, u == mx ? 1.f : ex2_approx(u - mx), sum);
+                        u = mx;
+                    }
+                }
                 if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
                     float mx = -INFINITY;
 #pragma unroll 1
@@ -793,7 +821,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     take(c, x);
                     work(c, x);
                 }
-                l_sum += tile_l;
+                if (!apart) l_sum += tile_l;
                 if (__any_sync(0xffffffffu, rescale_o)) {
                     // PV_g(j-1) has completed: S_g(j) was committed after it
 #pragma unroll
@@ -810,6 +838,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_pf);
+                return true;
+            };
+            int j = 0;
+            for (; j < n; ++j) {
+                if (!(ok = wait_scales(j))) break;
+                const int tn = tile_no + (dual ? 2 * j + g : j);
+                if (__any_sync(0xffffffffu, scales[(tn % T::SCALES) * 8 + (lane & 7)].w != 0.f)) break;
+                if (!(ok = step(std::false_type{}, j))) break;
+            }
+            const bool apart = ok && j < n;
+            if (apart) {
+                if (l_sum != 0.f) u = m_used - kWeightShift;
+                for (; j < n && ok; ++j) ok = wait_scales(j) && step(std::true_type{}, j);
             }
             s_seen += n;
             tile_no += w.v1 - w.v0;
@@ -819,6 +860,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 tc_fence_after();
             }
             if (!ok) break;
+            if (apart) {
+                float half;
+                plain_units(m_used, l_sum, u, l_sum, half);
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + 32 * c, o);
+                    tmem_ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * half * half);
+                    tmem_st32(tO + 32 * c, o);
+                    tmem_st_wait();
+                }
+            }
             if (dual && w.a1 > 0) {
                 if (g == 1) {
                     // This group's maximum and sum beside its O in tensor memory, whose lanes the

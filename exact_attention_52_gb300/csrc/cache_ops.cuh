@@ -16,6 +16,14 @@ namespace attn {
 // and one is lost to underflow below 2^-31 of the largest.
 constexpr float kWeightShift = 7.f, kWeightSlack = 8.f;
 
+// The weights hold the value scales sv, as 2^(score + log2 sv - m + kWeightShift), and the sum
+// of a row's probabilities takes them back by 1 / sv.  While every page of a walk has |log2 sv|
+// <= kScaleReach, a weight that fp32 flushes (2^-126) is below 2^(-126 + 48) of a sum that is at
+// least 2^(kWeightShift - 48), 2^-37 of it, and nothing overflows.  From the first page beyond
+// (an append gives a page of zeros 2^-100) the rest of the walk sums 2^(score - u) apart, with
+// a maximum u of the plain scores and an exponential more for each of them.
+constexpr float kScaleReach = 48.f;
+
 // The new queries of one sequence and the keys they see.  Query t of q_len sits
 // at position len - q_len + t; key j is visible to position p iff j <= p and
 // (left < 0, or j >= p - left, or j < sinks).  Keys are walked in blocks of TB
@@ -122,6 +130,16 @@ __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// A walk whose sum was taken apart (2^u times s, s >= 1; 0: no key) as one like the others: its
+// maximum and sum become those of plain scores, and its output sum is to be multiplied twice
+// by `half` (the square leaves fp32's range sooner than the product does).
+__device__ __forceinline__ void plain_units(float& m, float& l, float u, float s, float& half) {
+    const float k = s != 0.f ? floorf(lg2_approx(s)) : 0.f;
+    half = s != 0.f ? ex2_approx(0.5f * (m - kWeightShift - u - k)) : 1.f;
+    m = s != 0.f ? u + k + kWeightShift : -INFINITY;
+    l = s * ex2_approx(-k);
 }
 
 // Power of two that brings a row whose largest finite magnitude is `amax` to

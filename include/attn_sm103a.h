@@ -365,7 +365,10 @@ attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_str
  * hold does not matter, NaN codes included.  Scores, softmax and sums are fp32 on
  * products of f16 operands: codes are exact in f16, Q rows are brought to it by a
  * power of two each, the softmax weights (times the value scale) are rounded to it
- * (half a step, 2^-11 relative).  Results are deterministic.
+ * (half a step, 2^-11 relative, and what lies below 2^-31 of a row's largest is lost to
+ * O, not to the sum or LSE).  The scales may be any that the cache allows, however far
+ * apart; walks that meet a value scale beyond 2^+-48 take about twice the exponentials.
+ * Results are deterministic.
  * Source: ai.engineer item 59 (small-query work split across thread blocks plus
  * a separate combining kernel; causal mask aligned to the last key);
  * FlashAttention-3 tuning page (window bounds).  Errors as attn_fwd_strided.

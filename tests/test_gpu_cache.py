@@ -247,6 +247,93 @@ def test_cache_forward_large_scores_and_values():
     run_cache(pool, 8, 1, [310, 200], None, amp=2.0)
 
 
+def run_far(pool, H, T, n, left=-1, sinks=0, amp=1.0):
+    """run_cache for value scales from 2^-126 to 2^126.  Against a score below 32 a sum of score
+    and log2 sv, a maximum and log2 of a sum may all reach 2^8: two roundings of 2^-18 and
+    three of 2^-17 in exponents, 2^-15 log2 units together, beside what the module's bound
+    has: |O - ref| <= e + 2^-8 (|ref| + e) + 2^-134 with e = (2^-11 + 2^-14) M, the last being half
+    a step of bf16 numbers below 2^-126 (their last bit is 2^-126 2^-7); LSE as there."""
+    import torch
+    q, qv = bf16(pool.rng, (pool.B, H, T, pool.d), amp=amp)
+    lens = [n] * pool.B
+    o, lse = api.fwd_cache(q, *pool.dev(), i32(lens), window_left=left, sinks=sinks)
+    check_clean()
+    o_ref, lse_ref, mag, _ = streaming.cache_forward(qv, pool.k, pool.v, pool.ks, pool.vs, pool.table, lens,
+                                                     [T] * pool.B, pool.d ** -0.5, left, sinks)
+    og, lg = device_bf16_to_f64(o), lse.double().cpu().numpy()
+    e = (2.0 ** -11 + 2.0 ** -14) * mag
+    bad = ~(np.abs(og - o_ref) <= e + 2.0 ** -8 * (np.abs(o_ref) + e) + 2.0 ** -134)
+    assert not bad.any(), (np.argwhere(bad)[:4], og[bad][:4], o_ref[bad][:4])
+    assert np.all(np.abs(lg - lse_ref) <= 2.0 ** -14)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 5, 70, 300])
+@pytest.mark.parametrize("exponent", [-126, -122, -110, -100, 100])
+def test_value_scales_that_are_all_small_or_large(exponent, T, d):
+    """Every visible page of one extreme value scale, from one token to thousands of equal scores."""
+    for n, amp in ((max(1, T), 1.0), (T + 8200, 0.0), (T + 500, 2.0)):
+        pool = Pool(80, 1, 2, d, 64, -(-n // 64))
+        pool.vs[:] = 2.0 ** exponent
+        run_far(pool, 4, T, n, amp=amp)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [1, 5, 70, 300])
+@pytest.mark.parametrize("amp", [0.0, 2.0])
+@pytest.mark.parametrize("low,high", [(-100, 40), (-100, -8), (-60, 30), (-126, 100)])
+def test_value_scales_far_apart(low, high, amp, T, d):
+    """Pages of two value scales far apart, at equal scores and at others: one page of the one
+    among the others, first, last or amid; every other page; the whole at random."""
+    n = 1100 + T
+    for which in ("first", "last", "amid", "turns", "random"):
+        for lo, hi in ((low, high), (high, low)):
+            pool = Pool(81, 1, 2, d, 16, -(-n // 16))
+            exps, pages = np.full(pool.table.shape[1], hi), pool.table[0]
+            if which == "turns":
+                exps[::2] = lo
+            elif which == "random":
+                exps = pool.rng.integers(low, high + 1, len(exps))
+            else:
+                exps[{"first": 0, "last": n // 16 - 1, "amid": len(exps) // 2}[which]] = lo
+            pool.vs[pages] = 2.0 ** exps.astype(np.float64)[:, None]
+            run_far(pool, 4, T, n, amp=amp)
+            run_far(pool, 4, T, n, 500, 20, amp=amp)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,T,n", [(40, 1, 900), (24, 5, 900), (6, 300, 1400), (20, 70, 1400)])
+@pytest.mark.parametrize("exponent", [-100, 45, 110])
+def test_a_far_value_scale_within_a_walk(exponent, B, T, n, d):
+    """Enough sequences that a walk has several key tiles: ordinary pages, then one far from
+    them somewhere in each sequence and head, then ordinary ones again."""
+    pool = Pool(83, B, 8, d, 16, -(-n // 16))
+    pool.vs[...] = 2.0 ** pool.rng.integers(-9, -5, pool.vs.shape)
+    for b in range(B):
+        for h in range(8):
+            pool.vs[pool.table[b, pool.rng.integers(0, pool.table.shape[1])], h] = 2.0 ** exponent
+    run_far(pool, 8, T, n, amp=1.5)
+    run_far(pool, 8, T, n, 700, 30, amp=1.5)
+
+
+@pytest.mark.parametrize("T", [1, 70])
+def test_a_page_of_zeros_among_others(T):
+    """What an append makes of values that are all zeros (a scale of 2^-100) beside pages of
+    ordinary and of large values."""
+    import torch
+    pool = Pool(82, 1, 2, 64, 16, 20)
+    dev = pool.dev()
+    k, kv = bf16(pool.rng, (1, 2, 300, 64))
+    v, vv = bf16(pool.rng, (1, 2, 300, 64), amp=2.0 ** 20)
+    v[:, :, 32:80], vv[:, :, 32:80] = 0, 0
+    v[:, :, 100:], vv[:, :, 100:] = v[:, :, 100:] * 2.0 ** -20, vv[:, :, 100:] * 2.0 ** -20
+    api.cache_append(k, v, *dev, i32([300]))
+    streaming.cache_append(kv, vv, pool.k, pool.v, pool.ks, pool.vs, pool.table, [300], [300])
+    assert float(dev[3].min()) == 2.0 ** -100 and np.array_equal(dev[1].cpu().numpy(), pool.v)
+    for amp in (0.0, 1.0):
+        run_far(pool, 4, T, 300, amp=amp)
+
+
 def test_pages_that_no_query_sees_are_not_read():
     """Table entries outside window and sinks hold nonsense and no error is recorded."""
     pool = Pool(10, 2, 2, 128, 16, 40)
