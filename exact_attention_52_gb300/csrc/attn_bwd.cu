@@ -234,7 +234,7 @@ struct BwdWork {
 
     // Work item `item` of the launch's numbering (items = key tiles of every
     // key/value head), whole.
-    __device__ BwdWork(const BwdParams& prm, int item) {
+    __host__ __device__ BwdWork(const BwdParams& prm, int item) {
         const int N = prm.N;
         // Non-causal: head-major order keeps the resident CTAs on a few heads, so
         // those heads' Q, dO and fp32 dQ accumulator stay in L2 while every key
@@ -276,7 +276,7 @@ struct BwdWork {
     // (v - split_base) % P of item split_base + (v - split_base) / P, which takes
     // steps [t0, t1) of the item's walk (query head by query head, tile by tile).
     // (Sinks: the split items are the sink tiles.)
-    __device__ static BwdWork split_at(const BwdParams& prm, int v) {
+    __host__ __device__ static BwdWork split_at(const BwdParams& prm, int v) {
         if (v < prm.split_base) return BwdWork(prm, v);
         const int s = v - prm.split_base, P = prm.split_parts;
         BwdWork w(prm, prm.split_base + s / P);
@@ -291,7 +291,7 @@ struct BwdWork {
         if (e & 0x8000) w.make_part((e >> 14) & 1, 2, 2 * item + ((e >> 14) & 1));
         return w;
     }
-    __device__ void make_part(int part, int P, int part_slot) {
+    __host__ __device__ void make_part(int part, int P, int part_slot) {
         const int t0 = part * n_steps / P;
         n_steps = (part + 1) * n_steps / P - t0;
         slot = part_slot;
@@ -304,7 +304,7 @@ struct BwdWork {
     // run together reduce into different dQ tiles; otherwise (causal, windows)
     // the range is walked upwards, which already starts neighbouring key tiles
     // on different query tiles.
-    __device__ int q_tile(int tt) const {
+    __host__ __device__ int q_tile(int tt) const {
         if (!full_range) return q_lo + tt;
         const int i = j + tt;
         return i < n_q_total ? i : i - n_q_total;
@@ -1802,14 +1802,7 @@ long long sink_launch_steps(int D, long long sms, long long n_plain, long long p
            std::max(items > 0 ? plain + (on_items ? part : 0) : 0, (n_parts > 0 ? part : 0) + (on_parts ? part : 0));
 }
 
-cudaError_t bwd_sink_parts(int D, BwdParams* p) {
-    p->split_base = p->BHk * p->n_kv;
-    p->split_parts = 1;
-    if (p->sinks == 0 || p->split_cap == 0) return cudaSuccess;
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+void sink_parts_for(int D, int sms, BwdParams* p) {
     const long long G = p->H / p->Hk, items = static_cast<long long>(p->BHk) * p->n_kv;
     const long long sink_items = static_cast<long long>(p->BHk) * p->sink_tiles, steps = G * p->n_kv;
     const long long win_tiles = p->win_right < 0 ? p->n_kv
@@ -1828,7 +1821,17 @@ cudaError_t bwd_sink_parts(int D, BwdParams* p) {
         p->split_base = static_cast<int>(items - sink_items);
         p->split_parts = static_cast<int>(parts);
     }
-    return cudaSuccess;
+}
+
+cudaError_t bwd_sink_parts(int D, BwdParams* p) {
+    p->split_base = p->BHk * p->n_kv;
+    p->split_parts = 1;
+    if (p->sinks == 0 || p->split_cap == 0) return cudaSuccess;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) sink_parts_for(D, sms, p);
+    return e;
 }
 
 cudaError_t launch_bwd_pre(const BwdPreParams& p, cudaStream_t stream) {

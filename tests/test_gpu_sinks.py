@@ -278,3 +278,38 @@ def test_strides_over_one_element_are_not_looked_at(N):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
         assert torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
     check_clean()
+
+
+@pytest.mark.parametrize("B,H,Hk,N,left,sinks", [(1, 2, 2, 8192, 200, 4), (1, 8, 1, 2500, 255, 1),
+                                                 (1, 40, 40, 4096, 100, 2), (1, 2, 2, 6000, 130, 513)])
+def test_sinks_split_backward_of_narrow_heads(B, H, Hk, N, left, sinks):
+    """test_sinks_split_backward at d = 64, whose launch is another: a CTA a part, the last ones
+    first, parts that begin in the middle of a query head (test_sink_parts.py says that these
+    shapes are split).  Every key/value head's dK and dV the same bits in three runs."""
+    import torch
+    d = 64
+    inp = make_inputs_gqa(B, H, Hk, N, d, seed=N + H, with_grad=True)
+    q, k, v, do = (bf16_to_device(x) for x in (inp.q_bits, inp.k_bits, inp.v_bits, inp.do_bits))
+    o, lse = api.fwd_sinks(q, k, v, left, sinks)
+    dq, dk, dv = api.bwd_sinks(q, k, v, o, do, lse, left, sinks)
+    for _ in range(2):
+        again = api.bwd_sinks(q, k, v, o, do, lse, left, sinks)
+        assert torch.equal(dk.view(torch.int16), again[1].view(torch.int16))
+        assert torch.equal(dv.view(torch.int16), again[2].view(torch.int16))
+    check_clean()
+    qf, kf, vf, dof = decoded(inp)
+    G = H // Hk
+    for g in {0, Hk - 1}:  # the first and last key/value head and their query heads
+        hs, ks = slice(g * G, g * G + G), slice(g, g + 1)
+        part = (qf[:, hs], kf[:, ks], vf[:, ks])
+        o_ref, lse_ref = streaming.sinks_forward(*part, d ** -0.5, left, sinks)
+        assert bf16_out_err(device_bf16_to_f64(o[:, hs]), o_ref) <= TOL_O_MAXABS
+        assert max_abs(device_f32_to_f64(lse[:, hs]), lse_ref) <= TOL_LSE_ABS
+        ref = streaming.sinks_backward(*part, dof[:, hs], d ** -0.5, left, sinks)
+        for name, x, r in zip(("dq", "dk", "dv"), (dq[:, hs], dk[:, ks], dv[:, ks]), ref):
+            err = grad_rel_err(device_bf16_to_f64(x), r)
+            assert err <= TOL_GRAD_RELFRO, (name, err)
+
+
+def test_many_sink_items_of_narrow_heads_are_not_split():
+    check(5, 52, 52, 300, 64, 100, 4, backward=True)
