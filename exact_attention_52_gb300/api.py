@@ -548,10 +548,16 @@ def _explain_lse(device, t, shape):
         raise ValueError(f"lse must be a contiguous {shape}")
 
 
+def _workspace_ok(torch, dev, t, need):
+    """Whether ``t`` has ``need`` bytes one after the other on device ``dev`` (an expanded tensor
+    counts bytes that it does not have)."""
+    return isinstance(t, torch.Tensor) and t.get_device() == dev and t.nbytes >= need and t.is_contiguous()
+
+
 def _explain_workspace(device, t, need):
     import torch
-    if not isinstance(t, torch.Tensor) or t.device != device or t.numel() * t.element_size() < need:
-        raise ValueError(f"workspace needs {need} bytes on {device}")
+    if not isinstance(t, torch.Tensor) or t.device != device or t.nbytes < need or not t.is_contiguous():
+        raise ValueError(f"workspace needs {need} contiguous bytes on {device}")
 
 
 def _strides4(t, layout):
@@ -693,7 +699,7 @@ def bwd_sinks(q, k, v, o, dout, lse, window_left: int, sinks: int, window_right:
     dqs, dks, dvs = (_like_strides(torch, dev, dq, q, layout), _like_strides(torch, dev, dk, k, layout),
                      _like_strides(torch, dev, dv, v, layout))
     if (None in (os_, dos, dqs, dks, dvs) or not _lse_ok(torch, dev, lse, (B, H, N))
-            or not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or workspace.nbytes < need):
+            or not _workspace_ok(torch, dev, workspace, need)):
         for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
             _explain_like(device, name, t, like)
         _explain_lse(device, lse, (B, H, N))
@@ -869,8 +875,7 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
         os_ = _strides4(o, layout)
         ok = (os_ is not None and o.dtype is torch.bfloat16 and o.shape == q.shape and lse.shape == (B, H, T)
               and lse.dtype is torch.float32 and lse.is_contiguous()
-              and dev == o.get_device() == lse.get_device() == workspace.get_device()
-              and workspace.nbytes >= need)
+              and dev == o.get_device() == lse.get_device() and _workspace_ok(torch, dev, workspace, need))
     except (AttributeError, ValueError):
         ok = False
     if not ok:

@@ -95,6 +95,12 @@ void* dense(PyObject* o, at::ScalarType type, at::IntArrayRef shape, int dev) {
     return t.data_ptr();
 }
 
+// So many bytes one after the other (an expanded tensor counts bytes that it does not have).
+void* workspace(const at::Tensor& t, size_t room, int dev) {
+    need(room > 0 && t.layout() == at::kStrided && t.is_cuda() && t.get_device() == dev && t.nbytes() >= room && t.is_contiguous());
+    return t.data_ptr();
+}
+
 float scale_of(PyObject* o, int D) {
     if (o == Py_None) return static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
     need(PyFloat_CheckExact(o));
@@ -212,13 +218,11 @@ PyObject* fwd_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float scale = scale_of(a[9], q.D);
         const int left = small(a[10]), sinks = small(a[11]);
         const size_t room = lib.fwd_cache_workspace_bytes(q.B, q.H, Hk, q.N, q.D);
-        const at::Tensor& ws = tensor(a[14]);
-        need(room > 0 && ws.is_cuda() && ws.get_device() == dev && ws.nbytes() >= room);
+        void* w = workspace(tensor(a[14]), room, dev);
         Out o = like_or_given(a[12], q), lse = lse_or_given(a[13], q);
         const Rows ov = rows_like(o.o, q, dev, bnhd);
         float* l = static_cast<float*>(dense(lse.o, at::kFloat, {q.B, q.H, q.N}, dev));
         auto stream = reinterpret_cast<attn_stream_t>(integer(a[16]));
-        void* w = ws.data_ptr();
         const attn_status rc = called([&] {
             return lib.fwd_cache(&c, q.p(), q.st, ov.p(), ov.st, l, w, lens, q.B, q.H, Hk, q.N, q.D, scale, left, sinks,
                                  stream);
@@ -263,9 +267,8 @@ PyObject* bwd_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const Rows dqv = rows_like(dq.o, q, dev, bnhd), dkv = rows_like(dk.o, k, dev, bnhd), dvv = rows_like(dv.o, v, dev, bnhd);
         const at::Tensor ws = a[14] != Py_None ? tensor(a[14])
                                                : at::empty({static_cast<int64_t>(room)}, q.t->options().dtype(at::kByte));
-        need(ws.is_cuda() && ws.get_device() == dev && ws.nbytes() >= room);
+        void* w = workspace(ws, room, dev);
         auto stream = reinterpret_cast<attn_stream_t>(integer(a[16]));
-        void* w = ws.data_ptr();
         const attn_status rc = called([&] {
             return lib.bwd_sinks(q.p(), q.st, k.p(), k.st, v.p(), v.st, o.p(), o.st, dout.p(), dout.st, l, dqv.p(), dqv.st,
                                  dkv.p(), dkv.st, dvv.p(), dvv.st, w, q.B, q.H, k.H, q.N, q.D, scale, left, right, sinks,

@@ -90,3 +90,16 @@ def test_a_module_that_does_not_fit_is_not_used(what, monkeypatch, tmp_path, mod
 def test_the_module_says_what_it_was_built_for(module):
     import torch
     assert module.built_for == api._call_tag(torch)
+
+
+def test_a_workspace_is_bytes_one_after_the_other():
+    """Tensors whose bytes are fewer than their elements, or not in a row, are no workspace."""
+    torch = pytest.importorskip("torch")
+    one = torch.empty(1, dtype=torch.uint8)
+    assert api._workspace_ok(torch, -1, torch.empty(512, dtype=torch.uint8), 512)
+    assert api._workspace_ok(torch, -1, torch.empty(2, 64), 512)
+    for t in (one.expand(512), torch.empty(1024, dtype=torch.uint8)[::2], torch.empty(511, dtype=torch.uint8),
+              torch.empty(4, 64).t(), None, 512):
+        assert not api._workspace_ok(torch, -1, t, 512)
+        with pytest.raises(ValueError, match="workspace needs 512 contiguous bytes"):
+            api._explain_workspace(torch.device("cpu"), t, 512)

@@ -710,6 +710,25 @@ def test_refusals():
     check_clean()
 
 
+def test_a_workspace_without_its_bytes_is_refused(monkeypatch):
+    """An expanded or strided tensor as workspace is refused by both halves of the binding."""
+    import torch
+    pool = Pool(44, 2, 2, 64, 16, 3)
+    dev, lens = pool.dev(), i32([20, 30])
+    q, k = (bf16(pool.rng, (2, h, 20, 64))[0] for h in (4, 2))
+    o, lse = api.fwd_sinks(q, k, k, 5, 1)
+    room = max(api.fwd_cache_workspace_bytes(2, 4, 2, 20, 64), api.bwd_sinks_workspace_bytes(2, 4, 2, 20, 64, 1))
+    byte = torch.zeros(1, dtype=torch.uint8, device="cuda")
+    for half in range(2):
+        for ws in (byte.expand(room), torch.empty(2 * room, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError, match="contiguous bytes"):
+                api.fwd_cache(q, *dev, lens, workspace=ws)
+            with pytest.raises(ValueError, match="contiguous bytes"):
+                api.bwd_sinks(q, k, k, o, q, lse, 5, 1, workspace=ws)
+        monkeypatch.setattr(api, "_compiled_calls", lambda: None)
+    check_clean()
+
+
 def test_on_another_stream_and_in_a_replayed_graph():
     """A captured decode step (write, then attend) is replayed with new tokens and lengths in
     the captured buffers; an eager call on a stream of its own gives the same bits."""
