@@ -134,6 +134,15 @@ def _check_qkv(name, t, shape, dtype):
         raise ValueError(f"{name} must be contiguous [B, H, N, d]")
 
 
+def _checked_workspace(t, need, device):
+    """The workspace that a call was given, of ``need`` bytes one after the other, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _explain_workspace(device, t, need)
+    return t
+
+
 def fwd(q, k, v, scale: float | None = None, causal: bool = False, o=None, lse=None,
         stream=None):
     """Forward pass on bf16 CUDA tensors [B, H, N, d]; returns (O bf16, LSE fp32 [B, H, N])."""
@@ -177,8 +186,7 @@ def fwd_splitkv(q, k, v, num_splits: int = 0, scale: float | None = None, causal
     need = int(lib.attn_fwd_splitkv_workspace_bytes(B, H, N, d, _c_int(num_splits)))
     if need == 0:
         raise ValueError("invalid sizes or num_splits")
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _checked_workspace(workspace, need, q.device)
     _check("attn_fwd_splitkv", lib.attn_fwd_splitkv(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                                     o.data_ptr(), lse.data_ptr(),
                                                     workspace.data_ptr(), B, H, N, d, scale,
@@ -222,8 +230,7 @@ def bwd_window(q, k, v, o, dout, lse, window_left: int, window_right: int,
     for name, t in (("k", k), ("v", v), ("dk", dk), ("dv", dv)):
         _check_qkv(name, t, (B, Hk, N, d), torch.bfloat16)
     need = bwd_workspace_bytes(B, H, N, d)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _checked_workspace(workspace, need, q.device)
     _check("attn_bwd_window", load_library().attn_bwd_window(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(), lse.data_ptr(),
         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), B, H, Hk, N, d, scale,
@@ -254,10 +261,7 @@ def bwd(q, k, v, o, dout, lse, scale: float | None = None, causal: bool = False,
     for name, t in (("dk", dk), ("dv", dv)):
         _check_qkv(name, t, (B, Hk, N, d), torch.bfloat16)
     need = bwd_workspace_bytes(B, H, N, d)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace needs {need} bytes")
+    workspace = _checked_workspace(workspace, need, q.device)
     lib = load_library()
     if Hk == H:
         _check("attn_bwd", lib.attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
@@ -398,8 +402,7 @@ def bwd_strided(q, k, v, o, dout, lse, layout: str = "bnhd", scale: float | None
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
     need = bwd_workspace_bytes(B, H, N, d)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    workspace = _checked_workspace(workspace, need, q.device)
     st = lambda t: _bhnd_strides(t, layout)
     _check("attn_bwd_strided", load_library().attn_bwd_strided(
         q.data_ptr(), st(q), k.data_ptr(), st(k), v.data_ptr(), st(v), o.data_ptr(), st(o),

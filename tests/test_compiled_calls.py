@@ -103,3 +103,15 @@ def test_a_workspace_is_bytes_one_after_the_other():
         assert not api._workspace_ok(torch, -1, t, 512)
         with pytest.raises(ValueError, match="workspace needs 512 contiguous bytes"):
             api._explain_workspace(torch.device("cpu"), t, 512)
+
+
+def test_the_other_calls_take_no_smaller_workspace():
+    """fwd_splitkv, bwd, bwd_window and bwd_strided look at the workspace that they are given."""
+    torch = pytest.importorskip("torch")
+    cpu = torch.device("cpu")
+    ws = torch.empty(512, dtype=torch.uint8)
+    assert api._checked_workspace(ws, 512, cpu) is ws
+    assert api._checked_workspace(None, 512, cpu).numel() == 512
+    for t in (ws[:511], ws[:1].expand(512), 3):
+        with pytest.raises(ValueError, match="workspace needs 512"):
+            api._checked_workspace(t, 512, cpu)

@@ -65,3 +65,18 @@ def test_windows_as_large_as_they_get(window, d):
         for x, y in zip(g[1:], grads[1:]):
             assert torch.equal(x.view(torch.int16), y.view(torch.int16))
     assert api.check_device_error() == (0, 0)
+
+
+def test_a_workspace_that_is_too_small_is_refused():
+    import torch
+    inp = make_inputs_gqa(1, 2, 2, 300, 128, seed=4, with_grad=True)
+    q, k, v, do = (bf16_to_device(x) for x in (inp.q_bits, inp.k_bits, inp.v_bits, inp.do_bits))
+    o, lse = api.fwd_window(q, k, v, 50, 0)
+    small = torch.empty(api.bwd_workspace_bytes(1, 2, 300, 128) - 1, dtype=torch.uint8, device="cuda")
+    for ws in (small, small[:1].expand(10 ** 9)):
+        for call in (lambda: api.bwd_window(q, k, v, o, do, lse, 50, 0, workspace=ws), lambda: api.bwd(q, k, v, o, do, lse, workspace=ws),
+                     lambda: api.bwd_strided(q, k, v, o, do, lse, layout="bhnd", window=(50, 0), workspace=ws),
+                     lambda: api.fwd_splitkv(q, k, v, 4, workspace=ws[:100])):
+            with pytest.raises(ValueError, match="workspace needs"):
+                call()
+    assert api.check_device_error() == (0, 0)
