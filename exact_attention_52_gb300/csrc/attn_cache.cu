@@ -14,11 +14,6 @@
 namespace attn {
 namespace {
 
-constexpr float kLn2 = 0.69314718055994530942f;
-
-__device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
 // ---------------------------------------------------------------------------
 // Append
 // ---------------------------------------------------------------------------
@@ -193,11 +188,6 @@ __device__ __forceinline__ int row_tiles(const CacheFwdParams& p, const CacheSeq
 // Blocks of a sequence's items (whole: see Share).
 __device__ __forceinline__ long long seq_work(const CacheFwdParams& p, const CacheSeq& s, int whole) {
     return static_cast<long long>(whole > 0 ? whole : s.n) * (row_tiles(p, s) * p.Hk);
-}
-// Quotient of numbers that hardly ever pass 32 bits (a 64-bit division takes some
-// hundred instructions).
-__device__ __forceinline__ long long div_mostly32(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
 // Shares of a line of `total` blocks in which all_items items lie; their start is still to be found.

@@ -42,7 +42,6 @@ namespace {
 
 // sum of 32 weights from which on they are formed again (a weight in f16 ends at 2^16)
 constexpr float kWeightMax = 32768.f;
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kPairRows = 2 * kTile;
 constexpr int kPromptThreads = 512;
 constexpr int kConvWarps = 4;
@@ -57,8 +56,6 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t f2u(float f) { return __float_as_uint(f); }
-__device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 enum : uint32_t {
     SITE_Q = 0x401, SITE_KV_EMPTY = 0x402, SITE_KV_FULL = 0x403, SITE_P_FULL = 0x404, SITE_S_FULL = 0x405,
@@ -164,10 +161,6 @@ struct PromptShareSmem {
     long long warp_sum[kPromptThreads / 32], unit_first;
     int unit;
 };
-
-__device__ __forceinline__ long long div_mostly32(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
-}
 
 __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptShareSmem* sm) {
     constexpr int W = kPromptThreads / 32;

@@ -24,6 +24,17 @@ constexpr float kWeightShift = 7.f, kWeightSlack = 8.f;
 // a maximum u of the plain scores and an exponential more for each of them.
 constexpr float kScaleReach = 48.f;
 
+__device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Quotient of numbers that hardly ever pass 32 bits (a 64-bit division takes some
+// hundred instructions).
+__device__ __forceinline__ long long div_mostly32(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
 // The new queries of one sequence and the keys they see.  Query t of q_len sits
 // at position len - q_len + t; key j is visible to position p iff j <= p and
 // (left < 0, or j >= p - left, or j < sinks).  Keys are walked in blocks of TB

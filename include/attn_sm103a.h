@@ -264,7 +264,11 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
  * points; sinks >= 0, and sinks = 0 is the plain window.  Key tiles that neither
  * the window nor the sinks reach are skipped in both passes; the backward's
  * workspace is attn_bwd_sinks_workspace_bytes() bytes, and its dK and dV are
- * deterministic as attn_bwd's are.
+ * deterministic as attn_bwd's are.  K and V have to be finite where they are
+ * hidden too, as in the window calls: a weight of 0 times infinity or NaN is NaN.
+ * P and dS are rounded to bf16 for their products, and the backward takes D from
+ * the bf16 O that it is given; where the formula's gradient is 0 (dQ and dK of a
+ * row that sees one key) it gives rounding noise, |dQ| <= 2^-8 scale |dO| |V| |K|.
  * Source: FlashAttention-3 tuning page (window bounds); no page describes sinks.
  */
 attn_status attn_fwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks,
@@ -338,7 +342,8 @@ typedef struct {
  * else the older codes are rounded again to the new one.  A code is the fp32
  * quotient value / scale (exact for a power of two) rounded to nearest even;
  * infinities become +-448 and NaN the NaN code.  Slots behind the last token are
- * left as they were.  No two sequences of a call may write to the same page.
+ * left as they were.  No two sequences of a call may write to the same page, nor
+ * one sequence through two entries of its table.
  * Source: ai.engineer item 33 (affine quantisation, Z = 0); no page describes a
  * cache.  Errors as attn_fwd_strided; B <= 32767 and Hk <= 65535.
  */
