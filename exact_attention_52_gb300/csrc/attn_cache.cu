@@ -25,10 +25,11 @@ namespace {
 // fall below E4M3's normal range).  Dividing by a power of two is exact, so a
 // new code carries one rounding, to nearest even, saturating at 448.
 // Bound by reading the new tokens, which stay in registers between the two looks at them
-// (read twice: 43 us for 33), and by issue: magnitudes are compared two at a time as
-// integers, and the quotient's correction is left out where the scale is a power of two (34
-// us for 27 without both).  4 prompts of up to 8192 tokens, 8 heads, d = 128: 27 us, 5.1
-// TB/s; one token for 32 sequences 6 us.
+// (read twice they cost a quarter more), and by issue: magnitudes are compared two at a time
+// as integers, and the quotient's correction is left out where the scale is a power of two
+// (without both a quarter more again).  4 prompts of up to 8192 tokens, 8 heads, d = 128: 23
+// us among other calls, 5.8 TB/s, 20 in a row; d = 64 16 in a row, 4.2 TB/s; one token for 32
+// sequences 3 us in a row.
 constexpr int kAppendThreads = 128;
 constexpr int kMinScaleExp = -100;
 
@@ -337,7 +338,7 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // Attention of a few queries: the kernel
 // ---------------------------------------------------------------------------
 // Bound by reading the codes once: 64 sequences of up to 8192 tokens, 32/8 heads, d = 128,
-// one query each: 122 us, 6.5 TB/s.  (With 40 rows a key/value head, 16 x 4096 tokens: 33 us
+// one query each: 124 us, 6.4 TB/s.  (With 40 rows a key/value head, 16 x 4096 tokens: 32 us
 // for 7.5 of reading; three row tiles, latency in 8 warps an SM.)  Each warp walks every
 // kWarps-th block of a segment on its own, with its own running maximum, sums and output;
 // the codes come by asynchronous copies into a ring of its own, so no barrier stands in
@@ -347,8 +348,8 @@ __device__ __forceinline__ RowAt row_at(const CacheFwdParams& p, int q_len, int 
 // multiplies the scores, the value scale is added, as its log2, to the exponent,
 // so that the weights given to the products are 2^(score + log2 sv - m) with the
 // running maximum m taken over score + log2 sv, and the sum of the probabilities
-// takes them back by 1 / sv (kScaleReach).  m is raised, and the output rescaled, only when a
-// score passes it by more than kWeightSlack; a weight is lost to f16's underflow below
+// takes them back by 1 / sv (kScaleReach).  m is raised, and the output rescaled, only when
+// a score passes it by more than kWeightSlack; a weight is lost to f16's underflow below
 // 2^-31 of the largest.
 //
 // What belongs to a tile and not to a lane (its page's address and scales, whether

@@ -21,7 +21,10 @@ constexpr float kWeightShift = 7.f, kWeightSlack = 8.f;
 // <= kScaleReach, a weight that fp32 flushes (2^-126) is below 2^(-126 + 48) of a sum that is at
 // least 2^(kWeightShift - 48), 2^-37 of it, and nothing overflows.  From the first page beyond
 // (an append gives a page of zeros 2^-100) the rest of the walk sums 2^(score - u) apart, with
-// a maximum u of the plain scores and an exponential more for each of them.
+// a maximum u of the plain scores and an exponential more for each of them.  All pages at
+// 2^-100: 64 x 4600 tokens 97 us for 95, 40 rows over 16 x 3000 tokens 45 for 34, 2 x 2048
+// queries over 16384 keys 1.68 ms for 0.81 (all in a row).  The check and the second copy of
+// the step's code cost a call without such pages 0 to 3 %.
 constexpr float kScaleReach = 48.f;
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -268,7 +268,7 @@ attn_status attn_bwd_strided(const void* q, attn_strides_t qs, const void* k, at
  * hidden too, as in the window calls: a weight of 0 times infinity or NaN is NaN.
  * P and dS are rounded to bf16 for their products, and the backward takes D from
  * the bf16 O that it is given; where the formula's gradient is 0 (dQ and dK of a
- * row that sees one key) it gives rounding noise, |dQ| <= 2^-8 scale |dO| |V| |K|.
+ * row that sees one key) it gives the rounding noise of fp32 sums.
  * Source: FlashAttention-3 tuning page (window bounds); no page describes sinks.
  */
 attn_status attn_fwd_sinks(const void* q, attn_strides_t qs, const void* k, attn_strides_t ks,
