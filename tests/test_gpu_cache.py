@@ -382,6 +382,25 @@ def test_cache_in_the_debug_build(T, seq):
         api._lib = saved
 
 
+@pytest.mark.parametrize("T,n", [(1, 300), (3, 77), (70, 300), (300, 700)])
+def test_far_value_scales_and_nan_in_the_debug_build(T, n):
+    """The copies of the code for value scales far apart, and the look for NaN values, stay
+    within their tensor-memory columns."""
+    saved = api._lib
+    api._lib = api.load_library(api.DEBUG_LIB_PATH)
+    try:
+        for d in (64, 128):
+            pool = Pool(84, 2, 2, d, 32, -(-n // 32))
+            pool.vs[pool.table[:, 0]] = 2.0 ** -100
+            pool.vs[pool.table[1, -1]] = 2.0 ** 60
+            run_far(pool, 8, T, n)
+            pool = Pool(85, 2, 2, d, 32, -(-n // 32))
+            pool.v[pool.table[0, (n - 2) // 32], 1, (n - 2) % 32, 5] = 0x7F
+            run_cache(pool, 8, T, [n, n], None, 60, 3)
+    finally:
+        api._lib = saved
+
+
 @pytest.mark.parametrize("T", [1, 70])
 def test_first_call_of_a_process_may_be_captured(T):
     """A fresh process whose first call of the library is made under stream capture."""
