@@ -98,7 +98,7 @@ def draw(rng):
     elif op == "append":
         t = rng.choice((1, 1, rng.randint(2, 64), _log(rng, 65, 8192)))
         b = _log(rng, 1, 64) if t <= 64 else _log(rng, 1, 4)
-        while b > 1 and b * t * (2 * h + 3 * hk) * d > 4 * 8192 * 88 * 128:
+        while b > 1 and b * t * (2 * h + 3 * hk) * d > 27000 * 88 * 128:
             b -= 1
         c = _append("", b, h, hk, d, rot, pairs, scaling, norm, rng.choice((16, 32, 64, 128)), t,
                     t + _log(rng, 1, 4096), layout)
