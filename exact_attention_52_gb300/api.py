@@ -11,6 +11,7 @@ library is missing, every call raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import fractions
 import functools
 import math
 import os
@@ -69,6 +70,11 @@ SIGNATURES = {
     "attn_fwd_cache_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "attn_fwd_cache": (_i, [_vp, _vp, _st, _vp, _st, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
                             _i, _i, _vp]),
+    "attn_rope": (_i, [_vp, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, ctypes.c_int64, _i, _i, _i, _i, _i, _vp]),
+    "attn_rope_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_rope_bwd": (_i, [_vp, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _vp,
+                           ctypes.c_int64, _i, _i, _i, _i, _i, _vp]),
+    "attn_cache_append_rope": (_i, [_vp, _vp, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _i, _vp]),
     "attn_check_device_error": (_i, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
     "attn_set_exp2_offload": (None, [_i]),
@@ -891,3 +897,268 @@ def fwd_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, q_len
         None if q_lens is None else q_lens.data_ptr(), B, H, Hk, T, d,
         1.0 / math.sqrt(d) if scale is None else float(scale), _c_int(window_left), _c_int(sinks), handle))
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions and norms of heads, by themselves and in the cache's write
+# ---------------------------------------------------------------------------
+_TWO_PI = 2 * fractions.Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+# attn_rope_t, packed (native alignment): table, weights, their type, rot, interleaved, factor, eps
+_ROPE = struct.Struct("@PPPiiiff")
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Angles per position, in radians, of the rot / 2 pairs of a head, and what the rotated elements
+    are multiplied by: theta_i = base^(-2 i / rot) and 1, or scaled for a context ``factor`` times
+    as long as the trained one:
+
+    "linear"  theta_i / factor: positions are squeezed into the trained range;
+    "ntk"     the base times factor^(rot / (rot - 2)): the slowest pair is stretched by the factor, the
+              fastest not at all;
+    "yarn"    (Peng et al., 2023) pairs that turn more than beta_fast times within original_len tokens
+              stay, those that turn less than beta_slow times are stretched by the factor, those between
+              in proportion; elements are multiplied by 0.1 ln(factor) + 1."""
+    if not isinstance(rot, int) or rot < 2 or rot % 2:
+        raise ValueError(f"rot must be an even number of elements, got {rot!r}")
+    if not (math.isfinite(base) and base > 0):
+        raise ValueError(f"base must be finite and above 0, got {base!r}")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling is not None and not (math.isfinite(factor) and factor > 0):
+        raise ValueError(f"factor must be finite and above 0, got {factor!r}")
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs two pairs at least")
+        base = base * factor ** (rot / (rot - 2))
+    theta = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if scaling == "linear":
+        return [t / factor for t in theta], 1.0
+    if scaling == "yarn":
+        if original_len is None or original_len < 1 or not beta_fast > beta_slow:
+            raise ValueError("yarn scaling needs original_len, and beta_fast above beta_slow")
+        turns = [original_len * t / (2.0 * math.pi) for t in theta]
+        keep = [min(1.0, max(0.0, (x - beta_slow) / (beta_fast - beta_slow))) for x in turns]
+        return [t * (k + (1.0 - k) / factor) for t, k in zip(theta, keep)], 0.1 * math.log(factor) + 1.0
+    return theta, 1.0
+
+
+class RopeTable:
+    """Rotary frequencies as the kernels take them, laid out once for a model (``rope_table``):
+    ``turns``, int64 [rot / 2] on the device, in units of 2^-64 turns a position."""
+    __slots__ = ("turns", "rot", "interleaved", "magnitude")
+
+    def __init__(self, turns, interleaved: bool, magnitude: float):
+        self.turns = turns
+        self.rot = 2 * turns.shape[0]
+        self.interleaved = bool(interleaved)
+        self.magnitude = float(magnitude)
+
+
+def _turns(theta: float) -> int:
+    """theta radians in units of 2^-64 turns, modulo a turn, as a signed number."""
+    t = round(fractions.Fraction(theta) / _TWO_PI * 2 ** 64) % 2 ** 64
+    return t - 2 ** 64 if t >= 2 ** 63 else t
+
+
+def rope_table(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               original_len: int | None = None, beta_fast: float = 32.0, beta_slow: float = 1.0,
+               interleaved: bool = False, frequencies=None, magnitude: float | None = None, device="cuda"):
+    """The table that ``rope`` and ``cache_append_rope`` take, for the first ``rot`` elements of a head
+    (a multiple of 16): the frequencies of ``rope_frequencies``, or ``frequencies``, rot / 2 numbers
+    in radians a position.  ``interleaved``: pairs are elements (2i, 2i + 1), otherwise
+    (i, i + rot / 2).  ``magnitude`` multiplies the rotated elements (default: what the scaling
+    asks for)."""
+    import torch
+    if not isinstance(rot, int) or rot < 16 or rot % 16:
+        raise ValueError(f"rot must be a multiple of 16, got {rot!r}")
+    if frequencies is None:
+        theta, m = rope_frequencies(rot, base, scaling, factor, original_len, beta_fast, beta_slow)
+    else:
+        theta, m = [float(t) for t in frequencies], 1.0
+        if len(theta) != rot // 2 or not all(map(math.isfinite, theta)):
+            raise ValueError(f"frequencies must be {rot // 2} finite numbers")
+    m = m if magnitude is None else float(magnitude)
+    if not math.isfinite(m):
+        raise ValueError(f"magnitude must be finite, got {m!r}")
+    return RopeTable(torch.tensor([_turns(t) for t in theta], dtype=torch.int64, device=device), interleaved, m)
+
+
+def _explain_rope(device, d, table, q_weight, k_weight):
+    import torch
+    if not isinstance(table, RopeTable):
+        raise ValueError("table must be a RopeTable (rope_table)")
+    _explain_on(device, "the table's turns", table.turns, torch.int64, 1)
+    if not table.turns.is_contiguous() or table.rot != 2 * table.turns.shape[0] or table.rot > d:
+        raise ValueError(f"the table must be of at most {d} elements of a head, got {table.rot}")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.device != device or w.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"{name} must be a fp32 or bf16 tensor on {device}")
+        if w.shape != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{d}], got {tuple(w.shape)}")
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must be of one type")
+
+
+def _rope_arg(torch, device, d, table, q_weight, k_weight, eps):
+    """attn_rope_t of a call, its tensors checked."""
+    _explain_rope(device, d, table, q_weight, k_weight)
+    w = q_weight if q_weight is not None else k_weight
+    return _ROPE.pack(table.turns.data_ptr(), 0 if q_weight is None else q_weight.data_ptr(),
+                      0 if k_weight is None else k_weight.data_ptr(), int(w is not None and w.dtype is torch.bfloat16),
+                      table.rot, int(table.interleaved), table.magnitude, float(eps))
+
+
+def _rope_positions(device, positions, B, N):
+    """Address and stride of a call's positions."""
+    import torch
+    if positions is None:
+        return None, 0
+    if not isinstance(positions, torch.Tensor) or positions.device != device or positions.dtype != torch.int32:
+        raise ValueError(f"positions must be an int32 tensor on {device}")
+    if positions.shape not in ((N,), (B, N)) or 1 not in (N, positions.stride(-1)):
+        raise ValueError(f"positions must be [{N}] or [{B}, {N}] with contiguous rows, got {tuple(positions.shape)}")
+    return positions.data_ptr(), positions.stride(0) if positions.dim() == 2 and B > 1 else 0
+
+
+def _rope_heads(device, name, t, layout, like=None):
+    """(shape, strides) of a bf16 tensor of heads, checked; ``like``: of its shape."""
+    import torch
+    _explain_on(device, name, t, torch.bfloat16, 4)
+    st = _strides4(t, layout)
+    if st is None:
+        raise ValueError(f"the last (d) dimension of {name} must be contiguous")
+    if like is not None and t.shape != like.shape:
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    return _bhnd_shape(t, layout), st
+
+
+_NO_STRIDES = Strides(0, 0, 0)
+
+
+def _rope_qk(q, k, layout, names=("q", "k")):
+    """Device, sizes and strides of the queries and keys (which may be None) of a call."""
+    if layout not in ("bhnd", "bnhd"):
+        raise ValueError(f"unknown layout {layout!r}")
+    device = _explain_device(q, names[0])
+    (B, H, N, d), qs = _rope_heads(device, names[0], q, layout)
+    if k is None:
+        return device, B, H, 0, N, d, qs, _NO_STRIDES
+    (Bk, Hk, Nk, dk), ks = _rope_heads(device, names[1], k, layout)
+    if (Bk, Nk, dk) != (B, N, d):
+        raise ValueError(f"{names[1]} must have {names[0]}'s batch, length and d, got {tuple(k.shape)}")
+    return device, B, H, Hk, N, d, qs, ks
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def rope(q, k, table, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6, layout: str = "bhnd",
+         q_out=None, k_out=None, stream=None):
+    """Rotary positions on the heads of q and k (which may be None), each head normed first where its
+    weight is given; returns (q_out, k_out).
+
+    q [B, H, N, d] and k [B, Hk, N, d] (``layout`` "bhnd") or [B, N, heads, d] ("bnhd"), bf16, any
+    strides (multiples of 8) with a contiguous last dimension; an output may be its input.
+    table: ``rope_table``.  positions: int32 [B, N] or [N] (default: token n at n).  With a weight
+    ([d], fp32 or bf16) a head x becomes x / sqrt(mean(x^2) + eps) * weight before its first
+    ``table.rot`` elements are rotated."""
+    import torch
+    device, B, H, Hk, N, d, qs, ks = _rope_qk(q, k, layout)
+    at, step = _rope_positions(device, positions, B, N)
+    arg = _rope_arg(torch, device, d, table, q_weight, None if k is None else k_weight, eps)
+    with _on_stream(stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        if k_out is None and k is not None:
+            k_out = torch.empty_like(k)
+    qos = _rope_heads(device, "q_out", q_out, layout, q)[1]
+    kos = _NO_STRIDES if k is None else _rope_heads(device, "k_out", k_out, layout, k)[1]
+    _check("attn_rope", load_library().attn_rope(
+        arg, q.data_ptr(), qs, q_out.data_ptr(), qos, _ptr(k), ks, None if k is None else k_out.data_ptr(), kos, at, step,
+        B, H, Hk, N, d, _call_stream(torch, device.index, stream)))
+    return q_out, k_out if k is not None else None
+
+
+@functools.lru_cache(maxsize=256)
+def rope_bwd_workspace_bytes(B: int, H: int, Hk: int, N: int, d: int) -> int:
+    return int(load_library().attn_rope_bwd_workspace_bytes(*map(_c_int, (B, H, Hk, N, d))))
+
+
+def rope_bwd(dq_out, dk_out, table, positions=None, q=None, k=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+             layout: str = "bhnd", dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Backward of ``rope``: (dQ, dK, gradient of q_weight, of k_weight), the latter fp32 [d], None
+    without a weight.  dq_out and dk_out (or None) are the gradients of ``rope``'s outputs, q and k its
+    inputs, which only a tensor with a weight needs; dq may be dq_out, dk dk_out.  ``workspace``:
+    ``rope_bwd_workspace_bytes`` bytes, one for each call that may overlap."""
+    import torch
+    device, B, H, Hk, N, d, gqs, gks = _rope_qk(dq_out, dk_out, layout, ("dq_out", "dk_out"))
+    if dk_out is None:
+        k = k_weight = None
+    at, step = _rope_positions(device, positions, B, N)
+    arg = _rope_arg(torch, device, d, table, q_weight, k_weight, eps)
+    strides = []
+    for name, x, w, like in (("q", q, q_weight, dq_out), ("k", k, k_weight, dk_out)):
+        strides.append(_NO_STRIDES if w is None else _rope_heads(device, name, x, layout, like)[1])
+    need = 0
+    if q_weight is not None or k_weight is not None:
+        need = rope_bwd_workspace_bytes(B, H, Hk, N, d)
+        if need == 0:
+            raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, N {N}, d {d}")
+    handle = _call_stream(torch, device.index, stream)
+    with _on_stream(stream):
+        if dq is None:
+            dq = torch.empty_like(dq_out)
+        if dk is None and dk_out is not None:
+            dk = torch.empty_like(dk_out)
+        if dq_weight is None and q_weight is not None:
+            dq_weight = torch.empty(d, dtype=torch.float32, device=device)
+        if dk_weight is None and k_weight is not None:
+            dk_weight = torch.empty(d, dtype=torch.float32, device=device)
+    if workspace is not None and need:
+        _explain_workspace(device, workspace, need)
+    elif need:
+        workspace = _call_workspace(torch, device.index, stream, handle, need)
+    dqs = _rope_heads(device, "dq", dq, layout, dq_out)[1]
+    dks = _NO_STRIDES if dk_out is None else _rope_heads(device, "dk", dk, layout, dk_out)[1]
+    for name, w, g in (("dq_weight", q_weight, dq_weight), ("dk_weight", k_weight, dk_weight)):
+        if w is not None:
+            _explain_on(device, name, g, torch.float32, 1)
+            if g.shape != (d,) or not g.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [{d}]")
+    _check("attn_rope_bwd", load_library().attn_rope_bwd(
+        arg, _ptr(q if q_weight is not None else None), strides[0], dq_out.data_ptr(), gqs, dq.data_ptr(), dqs,
+        _ptr(dq_weight if q_weight is not None else None), _ptr(k if k_weight is not None else None), strides[1],
+        _ptr(dk_out), gks, _ptr(dk if dk_out is not None else None), dks,
+        _ptr(dk_weight if k_weight is not None else None), _ptr(workspace if need else None), at, step, B, H, Hk, N, d, handle))
+    return (dq, dk if dk_out is not None else None, dq_weight if q_weight is not None else None,
+            dk_weight if k_weight is not None else None)
+
+
+def cache_append_rope(q, k, v, table, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens=None,
+                      q_weight=None, k_weight=None, eps: float = 1e-6, layout: str = "bhnd", q_out=None, stream=None):
+    """``cache_append`` of keys that are normed (where k_weight is given) and rotated first, and the
+    same of the new tokens' queries, in one launch; returns q_out, for ``fwd_cache``.
+
+    q: bf16 [B, H, T, d] (``layout`` "bhnd") or [B, T, H, d] ("bnhd"); q_out may be q.  Token t of
+    the new_lens[b] (default T) new ones is rotated at its position in the cache, seq_lens - new_lens
+    + t.  Rows of q_out behind them are left as they were.  The rest as ``rope`` and ``cache_append``."""
+    import torch
+    device, B, H, Hk, T, d, qs, ks = _rope_qk(q, k, layout)
+    if k is None:
+        raise ValueError("k must be a bf16 CUDA tensor")
+    vs = _rope_heads(device, "v", v, layout, k)[1]
+    arg = _rope_arg(torch, device, d, table, q_weight, k_weight, eps)
+    cache = _cache_arg(torch, device.index, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+                       new_lens, "new_lens")
+    if q_out is None:
+        with _on_stream(stream):
+            q_out = torch.empty_like(q)
+    qos = _rope_heads(device, "q_out", q_out, layout, q)[1]
+    _check("attn_cache_append_rope", load_library().attn_cache_append_rope(
+        cache, arg, q.data_ptr(), qs, q_out.data_ptr(), qos, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(new_lens), B, H, Hk,
+        T, d, _call_stream(torch, device.index, stream)))
+    return q_out

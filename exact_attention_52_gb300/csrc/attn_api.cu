@@ -562,6 +562,29 @@ attn_status cache_view(const attn_cache_t* c, int B, int Hk, int d, CacheView* o
     return ATTN_OK;
 }
 
+// The checked arguments of a call that appends; the error word is still to be set.
+attn_status append_params(const attn_cache_t* cache, const void* k, attn_strides_t ks, const void* v, attn_strides_t vs,
+                          const int32_t* new_lens, int B, int Hk, int T, int d, CacheAppendParams* p) {
+    attn_status rc = check_sizes(B, Hk, T, d, 1.f, 0);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = cache_view(cache, B, Hk, d, &p->c)) != ATTN_OK) return rc;
+    if (B > 32767 || Hk > 65535) return ATTN_ERR_INVALID;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(new_lens) & 3u) != 0) return ATTN_ERR_INVALID;
+    p->k = k;
+    p->v = v;
+    p->ks = from_abi(ks, B, Hk, T, d);
+    p->vs = from_abi(vs, B, Hk, T, d);
+    if (!strides_ok(p->ks, 2) || !strides_ok(p->vs, 2)) return ATTN_ERR_INVALID;
+    if (!distinct(p->c.ks, p->c.num_pages, Hk, p->c.page_size) || !distinct(p->c.vs, p->c.num_pages, Hk, p->c.page_size))
+        return ATTN_ERR_INVALID;
+    p->new_lens = new_lens;
+    p->B = B;
+    p->Hk = Hk;
+    p->T = T;
+    p->D = d;
+    return ATTN_OK;
+}
+
 // The workspace is laid out for the largest launch, so that its size needs no device.
 struct CacheLayout {
     size_t stat, border, total;
@@ -575,6 +598,34 @@ CacheLayout cache_layout(bool prompt, int d) {
     L.total = L.border + round256((prompt ? kPromptGridMax : kCacheGridMax) * sizeof(CacheBorder));
     return L;
 }
+attn_status rope_view(const attn_rope_t* r, int d, RopeView* out) {
+    if (r == nullptr || !aligned16(r->turns) || r->rot < 16 || r->rot > d || r->rot % 16 != 0) return ATTN_ERR_INVALID;
+    if ((r->interleaved != 0 && r->interleaved != 1) || (r->weight_bf16 != 0 && r->weight_bf16 != 1)) return ATTN_ERR_INVALID;
+    if (!std::isfinite(r->factor)) return ATTN_ERR_INVALID;
+    for (const void* w : {r->q_weight, r->k_weight})
+        if (w != nullptr && (!aligned16(w) || !(r->eps > 0.f) || !std::isfinite(r->eps))) return ATTN_ERR_INVALID;
+    out->turns = reinterpret_cast<const unsigned long long*>(r->turns);
+    out->q_weight = r->q_weight;
+    out->k_weight = r->k_weight;
+    out->weight_bf16 = r->weight_bf16;
+    out->rot = r->rot;
+    out->interleaved = r->interleaved;
+    out->factor = r->factor;
+    out->eps = r->eps;
+    return ATTN_OK;
+}
+
+// Sizes of Q's and K's heads (Hk = 0: no K) and the positions of a call that rotates them.
+attn_status rope_sizes(int B, int H, int Hk, int N, int d, const int32_t* positions, int64_t position_stride) {
+    attn_status rc = check_sizes(B, H, N, d, 1.f, 0);
+    if (rc != ATTN_OK) return rc;
+    if (Hk < 0 || (Hk > 0 && (rc = check_sizes(B, Hk, N, d, 1.f, 0)) != ATTN_OK)) return ATTN_ERR_INVALID;
+    if (static_cast<long long>(H) + Hk > 65535) return ATTN_ERR_INVALID;  // blocks of a launch's second dimension
+    if ((reinterpret_cast<uintptr_t>(positions) & 3u) != 0 || position_stride < 0 || position_stride > kMaxElems)
+        return ATTN_ERR_INVALID;
+    return ATTN_OK;
+}
+
 bool cache_prompt(int H, int Hk, int T) { return static_cast<long long>(T) * (H / Hk) > kPromptMinRows; }
 
 
@@ -851,31 +902,126 @@ attn_status attn_bwd_sinks(const void* q, attn_strides_t qs, const void* k, attn
                    window_right, stream, true, sinks);
 }
 
+attn_status attn_rope(const attn_rope_t* rope, const void* q, attn_strides_t qs, void* q_out, attn_strides_t qos,
+                      const void* k, attn_strides_t ks, void* k_out, attn_strides_t kos, const int32_t* positions,
+                      int64_t position_stride, int B, int H, int Hk, int N, int d, attn_stream_t stream) {
+    attn_status rc = rope_sizes(B, H, Hk, N, d, positions, position_stride);
+    if (rc != ATTN_OK) return rc;
+    RopeParams p = {};
+    if ((rc = rope_view(rope, d, &p.r)) != ATTN_OK) return rc;
+    const struct { const void* x; attn_strides_t xs; void* y; attn_strides_t ys; int heads; } of[2] = {
+        {q, qs, q_out, qos, H}, {k, ks, k_out, kos, Hk}};
+    for (int i = 0; i < 2; ++i) {
+        if ((p.heads[i] = of[i].heads) == 0) continue;
+        p.xs[i] = from_abi(of[i].xs, B, p.heads[i], N, d);
+        p.ys[i] = from_abi(of[i].ys, B, p.heads[i], N, d);
+        if (!aligned16(p.x[i] = of[i].x) || !aligned16(p.y[i] = of[i].y) || !strides_ok(p.xs[i], 2) ||
+            !strides_ok(p.ys[i], 2) || !distinct(p.ys[i], B, p.heads[i], N))
+            return ATTN_ERR_INVALID;
+    }
+    p.positions = positions;
+    p.position_stride = position_stride;
+    p.tokens = static_cast<long long>(B) * N;
+    p.N = N;
+    p.D = d;
+    p.sign = 1.f;
+    DeviceState ds;
+    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
+    return launch_rope(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+size_t attn_rope_bwd_workspace_bytes(int B, int H, int Hk, int N, int d) {
+    if (rope_sizes(B, H, Hk, N, d, nullptr, 0) != ATTN_OK) return 0;
+    return round256(static_cast<size_t>(kRopeBwdGridMax) * d * sizeof(float));
+}
+
+attn_status attn_rope_bwd(const attn_rope_t* rope, const void* q, attn_strides_t qs, const void* dq_out,
+                          attn_strides_t dqos, void* dq, attn_strides_t dqs, float* dq_weight, const void* k,
+                          attn_strides_t ks, const void* dk_out, attn_strides_t dkos, void* dk, attn_strides_t dks,
+                          float* dk_weight, void* workspace, const int32_t* positions, int64_t position_stride, int B,
+                          int H, int Hk, int N, int d, attn_stream_t stream) {
+    attn_status rc = rope_sizes(B, H, Hk, N, d, positions, position_stride);
+    if (rc != ATTN_OK) return rc;
+    RopeParams p = {};  // tensors without a norm: the transposed rotation
+    RopeBwdParams b = {};
+    if ((rc = rope_view(rope, d, &p.r)) != ATTN_OK) return rc;
+    b.r = p.r;
+    const struct { const void *x, *dy; void* dx; attn_strides_t xs, gs, ys; float* dw; int heads; const void* w; } of[2] = {
+        {q, dq_out, dq, qs, dqos, dqs, dq_weight, H, p.r.q_weight}, {k, dk_out, dk, ks, dkos, dks, dk_weight, Hk, p.r.k_weight}};
+    for (int i = 0; i < 2; ++i) {
+        const auto& a = of[i];
+        if (a.heads == 0) continue;
+        const Strides gs = from_abi(a.gs, B, a.heads, N, d), ys = from_abi(a.ys, B, a.heads, N, d);
+        if (!aligned16(a.dy) || !aligned16(a.dx) || !strides_ok(gs, 2) || !strides_ok(ys, 2) || !distinct(ys, B, a.heads, N))
+            return ATTN_ERR_INVALID;
+        if (a.w == nullptr) {
+            p.heads[i] = a.heads;
+            p.x[i] = a.dy;
+            p.y[i] = a.dx;
+            p.xs[i] = gs;
+            p.ys[i] = ys;
+            continue;
+        }
+        b.xs[i] = from_abi(a.xs, B, a.heads, N, d);
+        if (!aligned16(a.x) || !strides_ok(b.xs[i], 2) || !aligned16(a.dw)) return ATTN_ERR_INVALID;
+        if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
+        b.heads[i] = a.heads;
+        b.x[i] = a.x;
+        b.dy[i] = a.dy;
+        b.dx[i] = a.dx;
+        b.gs[i] = gs;
+        b.ys[i] = ys;
+        b.dw[i] = a.dw;
+    }
+    p.r.q_weight = p.r.k_weight = nullptr;
+    p.positions = b.positions = positions;
+    p.position_stride = b.position_stride = position_stride;
+    p.tokens = b.tokens = static_cast<long long>(B) * N;
+    p.N = b.N = N;
+    p.D = b.D = d;
+    p.sign = -1.f;
+    b.part = static_cast<float*>(workspace);
+    DeviceState ds;
+    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (p.heads[0] + p.heads[1] > 0 && launch_rope(p, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    if (b.heads[0] + b.heads[1] > 0 && launch_rope_norm_bwd(b, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    return ATTN_OK;
+}
+
 attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_strides_t ks, const void* v,
                               attn_strides_t vs, const int32_t* new_lens, int B, int Hk, int T, int d,
                               attn_stream_t stream) {
-    attn_status rc = check_sizes(B, Hk, T, d, 1.f, 0);
-    if (rc != ATTN_OK) return rc;
     CacheAppendParams p;
-    if ((rc = cache_view(cache, B, Hk, d, &p.c)) != ATTN_OK) return rc;
-    if (B > 32767 || Hk > 65535) return ATTN_ERR_INVALID;
-    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(new_lens) & 3u) != 0) return ATTN_ERR_INVALID;
-    p.k = k;
-    p.v = v;
-    p.ks = from_abi(ks, B, Hk, T, d);
-    p.vs = from_abi(vs, B, Hk, T, d);
-    if (!strides_ok(p.ks, 2) || !strides_ok(p.vs, 2)) return ATTN_ERR_INVALID;
-    if (!distinct(p.c.ks, p.c.num_pages, Hk, p.c.page_size) || !distinct(p.c.vs, p.c.num_pages, Hk, p.c.page_size))
-        return ATTN_ERR_INVALID;
-    p.new_lens = new_lens;
-    p.B = B;
-    p.Hk = Hk;
-    p.T = T;
-    p.D = d;
+    attn_status rc = append_params(cache, k, ks, v, vs, new_lens, B, Hk, T, d, &p);
+    if (rc != ATTN_OK) return rc;
     DeviceState ds;
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
     return launch_cache_append(p, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status attn_cache_append_rope(const attn_cache_t* cache, const attn_rope_t* rope, const void* q, attn_strides_t qs,
+                                   void* q_out, attn_strides_t qos, const void* k, attn_strides_t ks, const void* v,
+                                   attn_strides_t vs, const int32_t* new_lens, int B, int H, int Hk, int T, int d,
+                                   attn_stream_t stream) {
+    CacheAppendRopeParams p = {};
+    attn_status rc = append_params(cache, k, ks, v, vs, new_lens, B, Hk, T, d, &p.c);
+    if (rc != ATTN_OK || (rc = check_sizes(B, H, T, d, 1.f, 0)) != ATTN_OK || (rc = rope_view(rope, d, &p.r)) != ATTN_OK)
+        return rc;
+    p.q = q;
+    p.q_out = q_out;
+    p.qs = from_abi(qs, B, H, T, d);
+    p.qos = from_abi(qos, B, H, T, d);
+    p.H = H;
+    if (H > 65535 || !aligned16(q) || !aligned16(q_out) || !strides_ok(p.qs, 2) || !strides_ok(p.qos, 2) ||
+        !distinct(p.qos, B, H, T))
+        return ATTN_ERR_INVALID;
+    DeviceState ds;
+    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
+    p.c.st = dev_status(ds);
+    const cudaError_t e = launch_cache_append_rope(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ATTN_OK : e == cudaErrorInvalidConfiguration ? ATTN_ERR_INVALID : ATTN_ERR_CUDA;
 }
 
 size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d) {

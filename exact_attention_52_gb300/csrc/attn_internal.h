@@ -151,6 +151,60 @@ struct CacheAppendParams {
     DevStatus st;
 };
 
+// Rotary positions and norms of heads (attn_rope_t, checked).
+struct RopeView {
+    const unsigned long long* turns;  // [rot / 2]: angle of a pair per position, in 2^-64 turns
+    const void *q_weight, *k_weight;  // [D] fp32 or bf16, or null: no norm
+    int weight_bf16, rot, interleaved;
+    float factor, eps;
+};
+
+// Heads of Q (index 0) and of K (1); a tensor without heads takes no part.
+struct RopeParams {
+    RopeView r;
+    const void* x[2];  // bf16 [B, heads, N, D] with strides xs
+    void* y[2];
+    Strides xs[2], ys[2];
+    int heads[2];
+    const int* positions;  // [B, N], rows position_stride apart, or null: token n at position n
+    long long position_stride, tokens;  // tokens: B * N
+    int N, D;
+    float sign;  // of the angles: 1, or -1 for the transposed rotation
+    // Set by the launcher:
+    int token_slots, hp, chunks[2];
+};
+
+constexpr int kRopeBwdGridMax = 640;
+
+struct RopeBwdParams {
+    RopeView r;
+    const void* x[2];
+    const void* dy[2];
+    void* dx[2];
+    Strides xs[2], gs[2], ys[2];
+    int heads[2];
+    const int* positions;
+    long long position_stride, tokens;
+    int N, D;
+    float* dw[2];  // fp32 [D]
+    float* part;   // workspace: fp32 [kRopeBwdGridMax][D]
+    // Set by the launcher:
+    long long tiles;
+    int token_slots, blocks[2];
+};
+
+struct CacheAppendRopeParams {
+    CacheAppendParams c;
+    RopeView r;
+    const void* q;  // bf16 [B, H, T, D]
+    void* q_out;
+    Strides qs, qos;
+    int H;
+    // Set by the launcher:
+    int token_slots, hp;
+    unsigned pages, page_blocks, token_tiles, chunks;
+};
+
 // What the joining kernel of the cache attention finds at the border before a CTA's share.
 struct CacheBorder {
     int b, item, q_len;  // the item that the border splits
@@ -234,6 +288,9 @@ cudaError_t launch_bwd_main(int D, const CUtensorMap& tq, const CUtensorMap& tk,
 cudaError_t bwd_sink_parts(int D, BwdParams* p);
 cudaError_t launch_dq_convert(const DqConvertParams& p, cudaStream_t stream);
 cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache_append_rope(const CacheAppendRopeParams& p, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_rope_norm_bwd(const RopeBwdParams& p, cudaStream_t stream);
 cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream);
 cudaError_t launch_cache_prompt(const CacheFwdParams& p, cudaStream_t stream);
 cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream);

@@ -1,0 +1,263 @@
+// Rotary positions on the heads of Q and K, with or without a norm of each head, forward and
+// backward: one pass over the data, bound by reading and writing it.
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "ptx.cuh"
+#include "rope_ops.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kRopeThreads = 128;
+
+// ---------------------------------------------------------------------------
+// Rotation (forward; backward where there is no norm: the transpose, sign = -1)
+// ---------------------------------------------------------------------------
+// A block takes TT tokens and HT * hp heads of Q or of K: thread (slot, t) holds 16 elements of
+// head slot / TT + HT * i of token slot % TT, i = 0 .. hp - 1, so that a token's angles (8 a
+// thread, some 40 instructions each) serve hp heads and four heads' loads are out at a time.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+    constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR, U = 4;
+    pdl_wait();
+    const int which = static_cast<int>(blockIdx.y) >= p.chunks[0] ? 1 : 0;
+    const int chunk = static_cast<int>(blockIdx.y) - (which ? p.chunks[0] : 0);
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int TT = p.token_slots, HT = SLOTS / TT;
+    const long long tok = static_cast<long long>(blockIdx.x) * TT + slot % TT;
+    const bool there = tok < p.tokens;
+    const long long b = there ? div_mostly32(tok, p.N) : 0;
+    const int n = there ? static_cast<int>(tok - b * p.N) : 0;
+    const int nrot = p.r.rot / 16;
+    int lo, hi;
+    rope_pieces<INTER>(t, nrot, lo, hi);
+    const void* weight = which ? p.r.k_weight : p.r.q_weight;
+    float w[16] = {};
+    if (weight) load_weight(p.r, weight, lo, hi, w);
+    const Strides xs = p.xs[which], ys = p.ys[which];
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[which]) + b * xs.b + n * xs.n);
+    uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y[which]) + b * ys.b + n * ys.n);
+    const long long xh = xs.h / 8, yh = ys.h / 8;
+    const int h0 = chunk * HT * p.hp + slot / TT, h1 = min(p.heads[which], (chunk + 1) * HT * p.hp);
+    RopeAngles a;
+    if (there && t < nrot) a.at(p.r, t, p.positions ? __ldg(p.positions + b * p.position_stride + n) : n, p.sign);
+    for (int i = 0; i < p.hp; i += U) {  // (every thread of a warp the same number: norms are sums of several)
+        uint4 vl[U], vh[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + (i + u) * HT;
+            vl[u] = vh[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (there && h < h1) {
+                vl[u] = x[h * xh + lo];
+                vh[u] = x[h * xh + hi];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int h = h0 + (i + u) * HT;
+            float v[16];
+            unpack16(vl[u], vh[u], v);
+            norm_rotate<D, INTER>(v, weight != nullptr, w, p.r.eps, t < nrot, a);
+            if (there && h < h1) {
+                if (weight != nullptr || t < nrot) pack16(v, vl[u], vh[u]);  // else the bits as they are
+                y[h * yh + lo] = vl[u];
+                y[h * yh + hi] = vh[u];
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Backward of norm and rotation
+// ---------------------------------------------------------------------------
+// With u = x r: dn = R^T dy, dw += dn u, g = dn w, dx = r (g - u mean(g u)).  Reads x and dy,
+// writes dx; r is worked out again.  Block c of a tensor's share of the grid takes the c-th of
+// equal ranges of (token tile, HT heads) units, loads one unit ahead, works angles out when the
+// tile changes and keeps dw in registers; a block's sums over its threads go to the workspace,
+// one row a block, and a second kernel adds the rows in their order: no atomics, so the sums are
+// the same every time.
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_norm_bwd_kernel(const RopeBwdParams p) {
+    constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int which = static_cast<int>(blockIdx.x) >= p.blocks[0] ? 1 : 0;
+    const int c = static_cast<int>(blockIdx.x) - (which ? p.blocks[0] : 0);
+    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+    const int TT = p.token_slots, HT = SLOTS / TT, nrot = p.r.rot / 16;
+    int lo, hi;
+    rope_pieces<INTER>(t, nrot, lo, hi);
+    float w[16], dw[16];
+    load_weight(p.r, which ? p.r.k_weight : p.r.q_weight, lo, hi, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+    const Strides xs = p.xs[which], ys = p.ys[which], gs = p.gs[which];
+    const uint4* x = static_cast<const uint4*>(p.x[which]);
+    const uint4* dy = static_cast<const uint4*>(p.dy[which]);
+    uint4* dx = static_cast<uint4*>(p.dx[which]);
+    const int heads = p.heads[which], per_tile = (heads + HT - 1) / HT;
+    const long long units = p.tiles * per_tile;
+    const long long u0 = units * c / p.blocks[which], u1 = units * (c + 1) / p.blocks[which];
+    RopeAngles a;
+
+    struct At {  // a unit's place for this thread
+        long long tile, b;
+        int group, n, h;
+        bool there;
+    };
+    auto place = [&](long long tile, int group) {
+        At k;
+        k.tile = tile;
+        k.group = group;
+        const long long tok = tile * TT + slot % TT;
+        k.h = group * HT + slot / TT;
+        k.there = tok < p.tokens && k.h < heads;
+        k.b = k.there ? div_mostly32(tok, p.N) : 0;
+        k.n = k.there ? static_cast<int>(tok - k.b * p.N) : 0;
+        return k;
+    };
+    uint4 xl, xu, gl, gu;
+    auto load = [&](const At& k) {
+        xl = xu = gl = gu = make_uint4(0u, 0u, 0u, 0u);
+        if (!k.there) return;
+        const uint4* xp = x + (k.b * xs.b + k.n * xs.n + k.h * xs.h) / 8;
+        const uint4* gp = dy + (k.b * gs.b + k.n * gs.n + k.h * gs.h) / 8;
+        xl = xp[lo], xu = xp[hi], gl = gp[lo], gu = gp[hi];
+    };
+    At next = place(u0 / per_tile, static_cast<int>(u0 % per_tile));
+    if (u0 < u1) load(next);
+    long long turned = -1;
+    for (long long u = u0; u < u1; ++u) {
+        const At k = next;
+        float v[16], g[16];
+        unpack16(xl, xu, v);
+        unpack16(gl, gu, g);
+        if (u + 1 < u1) {
+            next = k.group + 1 < per_tile ? place(k.tile, k.group + 1) : place(k.tile + 1, 0);
+            load(next);
+        }
+        if (k.tile != turned) {
+            turned = k.tile;
+            if (t < nrot) a.at(p.r, t, p.positions ? __ldg(p.positions + k.b * p.position_stride + k.n) : k.n, -1.f);
+        }
+        const float r = head_rnorm<D>(v, p.r.eps);
+        if (t < nrot) rotate16<INTER>(a, g);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            v[i] *= r;
+            dw[i] = fmaf(g[i], v[i], dw[i]);  // (rows that are not there are zeros)
+            g[i] *= w[i];
+            (i & 1 ? s1 : s0) += g[i] * v[i];
+        }
+        const float mean = head_sum<D>(s0 + s1) * (1.f / D);
+        if (k.there) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = r * (g[i] - v[i] * mean);
+            uint4 ol, ou;
+            pack16(v, ol, ou);
+            uint4* at = dx + (k.b * ys.b + k.n * ys.n + k.h * ys.h) / 8;
+            at[lo] = ol;
+            at[hi] = ou;
+        }
+    }
+
+    __shared__ float sums[kRopeThreads / 32][D];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+        for (int o = TPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+        if ((threadIdx.x & 31) < TPR) sums[threadIdx.x >> 5][8 * (i < 8 ? lo : hi) + (i & 7)] = dw[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < D; e += kRopeThreads) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRopeThreads / 32; ++i) v += sums[i][e];
+        p.part[static_cast<long long>(blockIdx.x) * D + e] = v;
+    }
+}
+
+// dw of one tensor (blockIdx.y) and 32 elements: its blocks' rows added up, warp w taking rows w, w + 32, ...
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const RopeBwdParams p) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, e = blockIdx.x * 32 + lane;
+    pdl_wait();
+    const float* part = p.part + static_cast<long long>(which ? p.blocks[0] : 0) * p.D + e;
+    float v = 0.f;
+#pragma unroll 8
+    for (int i = warp; i < p.blocks[which]; i += 32) v += part[static_cast<long long>(i) * p.D];
+    sums[warp][lane] = v;
+    __syncthreads();
+    v = sums[lane][warp];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && p.dw[which]) p.dw[which][blockIdx.x * 32 + warp] = v;
+}
+
+int sm_count(cudaError_t* e) {
+    int dev = 0, sms = 0;
+    *e = cudaGetDevice(&dev);
+    if (*e == cudaSuccess) *e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms;
+}
+
+template <int D>
+cudaError_t launch_rope_d(RopeParams p, cudaStream_t stream) {
+    constexpr int SLOTS = kRopeThreads / (D / 16);
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (e != cudaSuccess) return e;
+    p.token_slots = rope_token_slots(p.tokens, SLOTS);
+    const long long tiles = (p.tokens + p.token_slots - 1) / p.token_slots;
+    const int HT = SLOTS / p.token_slots;
+    // As many heads a thread as leave every SM some blocks.
+    for (p.hp = 8;; p.hp /= 2) {
+        for (int i = 0; i < 2; ++i) p.chunks[i] = (p.heads[i] + HT * p.hp - 1) / (HT * p.hp);
+        if (p.hp == 1 || tiles * (p.chunks[0] + p.chunks[1]) >= 8ll * sms) break;
+    }
+    const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.chunks[0] + p.chunks[1]));
+    return p.r.interleaved ? launch_dependent(rope_kernel<D, true>, grid, kRopeThreads, 0, stream, p)
+                           : launch_dependent(rope_kernel<D, false>, grid, kRopeThreads, 0, stream, p);
+}
+
+template <int D>
+cudaError_t launch_rope_norm_bwd_d(RopeBwdParams p, cudaStream_t stream) {
+    constexpr int SLOTS = kRopeThreads / (D / 16);
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (e != cudaSuccess) return e;
+    p.token_slots = rope_token_slots(p.tokens, SLOTS);
+    p.tiles = (p.tokens + p.token_slots - 1) / p.token_slots;
+    const int HT = SLOTS / p.token_slots;
+    const int grid = sms * 4 < kRopeBwdGridMax ? sms * 4 : kRopeBwdGridMax;
+    const int all = p.heads[0] + p.heads[1];
+    for (int i = 0; i < 2; ++i) {
+        const long long units = p.tiles * ((p.heads[i] + HT - 1) / HT);
+        long long n = i == 0 ? (static_cast<long long>(grid) * p.heads[0] + all / 2) / all : grid - p.blocks[0];
+        n = n < units ? n : units;
+        p.blocks[i] = p.heads[i] > 0 ? static_cast<int>(n > 1 ? n : 1) : 0;
+        if (i == 0 && p.blocks[0] == grid && p.heads[1] > 0) --p.blocks[0];
+    }
+    const dim3 blocks(static_cast<unsigned>(p.blocks[0] + p.blocks[1]));
+    e = p.r.interleaved ? launch_dependent(rope_norm_bwd_kernel<D, true>, blocks, kRopeThreads, 0, stream, p)
+                        : launch_dependent(rope_norm_bwd_kernel<D, false>, blocks, kRopeThreads, 0, stream, p);
+    return e != cudaSuccess ? e : launch_dependent(rope_dw_kernel, dim3(D / 32, 2), 1024, 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
+    if (p.D == 64) return launch_rope_d<64>(p, stream);
+    if (p.D == 128) return launch_rope_d<128>(p, stream);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_rope_norm_bwd(const RopeBwdParams& p, cudaStream_t stream) {
+    if (p.D == 64) return launch_rope_norm_bwd_d<64>(p, stream);
+    if (p.D == 128) return launch_rope_norm_bwd_d<128>(p, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace attn

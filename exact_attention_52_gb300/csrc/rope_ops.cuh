@@ -1,0 +1,131 @@
+// Rotary positions and norms of single heads: the arithmetic shared by the kernels that
+// rotate Q and K (attn_rope.cu) and by the cache's write of rotated keys (attn_cache_rope.cu).
+//
+// A pair (x1, x2) of a head at position p becomes
+//   y1 = f (x1 cos a - x2 sin a),  y2 = f (x2 cos a + x1 sin a),  a = p theta_i,
+// and, before that, with a weight w, x becomes x r w with r = (mean of the head's x^2 + eps)^-1/2.
+// A thread holds 16 elements of a head, two pieces of 8 (16 bytes each), and a head takes
+// D / 16 threads side by side, so that both elements of a pair are in one thread, in the half
+// layout (pairs i, i + rot / 2) as in the interleaved one (2i, 2i + 1).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "attn_internal.h"
+#include "cache_ops.cuh"
+#include "ptx.cuh"
+
+namespace attn {
+
+// Pieces of 8 elements of thread t of a head, nrot = rot / 16 threads rotating.  Threads from
+// nrot on hold elements that only pass.
+template <bool INTER>
+__device__ __forceinline__ void rope_pieces(int t, int nrot, int& lo, int& hi) {
+    lo = INTER || t >= nrot ? 2 * t : t;
+    hi = INTER || t >= nrot ? 2 * t + 1 : t + nrot;
+}
+
+// Cosines and sines (times f) of the 8 pairs of thread t at a position: pairs 8t .. 8t + 7 in
+// either layout.  The table holds theta_i in units of 2^-64 turns, and a position times that,
+// modulo 2^64, is the angle within its turn without any error but the table's (2^-65 turns a
+// position): nothing is lost far out.  Its upper 32 bits go to fp32 (2^-25 of half a turn).
+struct RopeAngles {
+    float c[8], s[8];
+    __device__ __forceinline__ void at(const RopeView& r, int t, int pos, float sign) {
+        const ulonglong2* turns = reinterpret_cast<const ulonglong2*>(r.turns + 8 * t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const ulonglong2 w = __ldg(turns + i);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(pos)) * (e ? w.y : w.x);
+                float sn, cs;
+                sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f, &sn, &cs);
+                c[2 * i + e] = cs * r.factor;
+                s[2 * i + e] = sn * (r.factor * sign);
+            }
+        }
+    }
+};
+
+// The thread's elements: x[0 .. 7] of piece lo, x[8 .. 15] of piece hi.
+__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&x)[16]) {
+    const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[2 * i] = bf16lo(u[i]), x[2 * i + 1] = bf16hi(u[i]);
+}
+__device__ __forceinline__ void pack16(const float (&x)[16], uint4& lo, uint4& hi) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    lo = make_uint4(u[0], u[1], u[2], u[3]);
+    hi = make_uint4(u[4], u[5], u[6], u[7]);
+}
+
+template <bool INTER>
+__device__ __forceinline__ void rotate16(const RopeAngles& a, float (&x)[16]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float& x1 = x[INTER ? 2 * i : i];
+        float& x2 = x[INTER ? 2 * i + 1 : i + 8];
+        const float y1 = x1 * a.c[i] - x2 * a.s[i];
+        x2 = x2 * a.c[i] + x1 * a.s[i];
+        x1 = y1;
+    }
+}
+
+// Sum over the D / 16 threads of a head (neighbouring lanes).
+template <int D>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+    for (int o = 1; o < D / 16; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// r of a head, of which x is the thread's part.
+template <int D>
+__device__ __forceinline__ float head_rnorm(const float (&x)[16], float eps) {
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaf(x[2 * i], x[2 * i], a), b = fmaf(x[2 * i + 1], x[2 * i + 1], b);
+    return rsqrtf(fmaf(head_sum<D>(a + b), 1.f / D, eps));
+}
+
+// The thread's 16 weights.
+__device__ __forceinline__ void load_weight(const RopeView& r, const void* w, int lo, int hi, float (&out)[16]) {
+    if (r.weight_bf16) {
+        const uint4* p = static_cast<const uint4*>(w);
+        unpack16(__ldg(p + lo), __ldg(p + hi), out);
+        return;
+    }
+    const float4* p = static_cast<const float4*>(w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float4 v = __ldg(p + 2 * (k < 2 ? lo : hi) + (k & 1));
+        out[4 * k] = v.x, out[4 * k + 1] = v.y, out[4 * k + 2] = v.z, out[4 * k + 3] = v.w;
+    }
+}
+
+// Norm (norm: every thread of a warp alike) and rotation (turns: this thread's pieces rotate) of
+// a head, in fp32.
+template <int D, bool INTER>
+__device__ __forceinline__ void norm_rotate(float (&x)[16], bool norm, const float (&w)[16], float eps, bool turns,
+                                            const RopeAngles& a) {
+    if (norm) {
+        const float r = head_rnorm<D>(x, eps);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+    }
+    if (turns) rotate16<INTER>(a, x);
+}
+
+// How many tokens a block of `slots` heads at a time takes side by side: all, or as few as
+// there are, the rest of the slots taking further heads of the same token.
+__host__ __device__ inline int rope_token_slots(long long tokens, int slots) {
+    int t = 1;
+    while (t < slots && t < tokens) t *= 2;
+    return t;
+}
+
+}  // namespace attn

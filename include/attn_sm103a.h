@@ -285,6 +285,66 @@ attn_status attn_bwd_sinks(const void* q, attn_strides_t qs, const void* k, attn
                            attn_stream_t stream);
 
 /*
+ * Rotary positions on the heads of Q and K, with or without a norm of each head before
+ * them.  With w the tensor's weight (NULL: no norm, n = x) and
+ *   n = x r w,  r = (sum_i x_i^2 / d + eps)^(-1/2),
+ * the first `rot` elements of n are rotated in pairs, y1 = factor (n1 cos a - n2 sin a),
+ * y2 = factor (n2 cos a + n1 sin a), a = position * theta_i, i = 0 .. rot / 2 - 1; the
+ * pairs are elements (i, i + rot / 2), or with `interleaved` (2i, 2i + 1).  The other
+ * elements are n's (factor does not touch them).
+ *   turns       : int64 [rot / 2], 16-byte aligned: theta_i in units of 2^-64 turns (1 turn
+ *                 = 2 pi), modulo 2^64; a negative number is a turn backwards.  An angle is
+ *                 position * turns modulo 2^64, which is exact: far positions lose nothing.
+ *   rot         : a multiple of 16, 16 .. d.
+ *   factor      : finite (1, or the magnitude that a scaled context asks for).
+ *   q_weight, k_weight : [d] fp32 (weight_bf16 = 0) or bf16 (1), 16-byte aligned, or NULL.
+ *   eps         : finite and > 0 where there is a weight.
+ * All of it is fp32 arithmetic on bf16 elements, rounded once; squares have to stay in
+ * fp32's range (magnitudes below 2^60).
+ * Source: the pages describe attention after this step only; the formulas are those of the
+ * rotary embedding (Su et al., 2021) and of the root-mean-square norm (Zhang, Sennrich, 2019).
+ */
+typedef struct {
+    const int64_t* turns;
+    const void *q_weight, *k_weight;
+    int weight_bf16;
+    int rot;
+    int interleaved;
+    float factor, eps;
+} attn_rope_t;
+
+/*
+ *   q, q_out : bf16 [B, H, N, d] views; k, k_out: bf16 [B, Hk, N, d] views (Hk = 0: no K,
+ *              the pointers are not looked at).  An output may be its input, with the same
+ *              strides.
+ *   positions : int32 [B, N], rows position_stride apart (0: the same for every b), any
+ *              values; NULL: token n is at position n.
+ * One launch.  Errors as attn_fwd_strided, and H + Hk <= 65535.
+ */
+attn_status attn_rope(const attn_rope_t* rope, const void* q, attn_strides_t qs, void* q_out, attn_strides_t qos,
+                      const void* k, attn_strides_t ks, void* k_out, attn_strides_t kos, const int32_t* positions,
+                      int64_t position_stride, int B, int H, int Hk, int N, int d, attn_stream_t stream);
+
+/*
+ * Backward of attn_rope: with dn the transposed rotation of dy, u = x r and g = dn w,
+ * dw = sum over tokens and heads of dn u, dx = r (g - u mean(g u)); without a norm dx = dn.
+ *   dq_out, dk_out : bf16 gradients of the outputs; dq, dk: bf16 gradients of the inputs (each
+ *              may be the memory of its output's gradient, with the same strides).
+ *   q, k     : attn_rope's inputs, where the tensor has a weight (else not looked at).
+ *   dq_weight, dk_weight : fp32 [d], 16-byte aligned, written (not added to), where the tensor
+ *              has a weight (else not looked at).
+ *   workspace : attn_rope_bwd_workspace_bytes() bytes, 256-byte aligned, where a tensor has a
+ *              weight (else NULL will do); calls that may overlap need one each.
+ * Sums are fp32 in a fixed order: results are deterministic.
+ */
+size_t attn_rope_bwd_workspace_bytes(int B, int H, int Hk, int N, int d);
+attn_status attn_rope_bwd(const attn_rope_t* rope, const void* q, attn_strides_t qs, const void* dq_out,
+                          attn_strides_t dqos, void* dq, attn_strides_t dqs, float* dq_weight, const void* k,
+                          attn_strides_t ks, const void* dk_out, attn_strides_t dkos, void* dk, attn_strides_t dks,
+                          float* dk_weight, void* workspace, const int32_t* positions, int64_t position_stride, int B,
+                          int H, int Hk, int N, int d, attn_stream_t stream);
+
+/*
  * FP8 forward pass: OCP E4M3 inputs with per-tensor fp32 scales.
  *   q8, k8, v8 : uint8 E4M3 codes [B, H, N, d]; the value read is s * code
  *                (sq, sk, sv finite and > 0).
@@ -350,6 +410,21 @@ typedef struct {
 attn_status attn_cache_append(const attn_cache_t* cache, const void* k, attn_strides_t ks,
                               const void* v, attn_strides_t vs, const int32_t* new_lens, int B,
                               int Hk, int T, int d, attn_stream_t stream);
+
+/*
+ * attn_cache_append of keys that are normed and rotated on their way (see attn_rope), and the
+ * same of the new tokens' queries, for the attention that follows, in one launch.  Token t is
+ * rotated at the position that it has in the cache, seq_lens[b] - new_lens[b] + t.
+ *   q, q_out : bf16 [B, H, T, d] views; q_out may be q with the same strides.  Rows of tokens
+ *              that are not new (t >= new_lens[b]) or have a negative position are left as they
+ *              were.  H need not be a multiple of Hk.
+ * Keys are rotated in fp32 and rounded once, to E4M3; the page's scale covers those values.
+ * Errors as attn_cache_append; H <= 65535, and no more than 2^31 - 1 blocks.
+ */
+attn_status attn_cache_append_rope(const attn_cache_t* cache, const attn_rope_t* rope, const void* q, attn_strides_t qs,
+                                   void* q_out, attn_strides_t qos, const void* k, attn_strides_t ks, const void* v,
+                                   attn_strides_t vs, const int32_t* new_lens, int B, int H, int Hk, int T, int d,
+                                   attn_stream_t stream);
 
 /*
  * Attention of new queries over the cache (their own tokens written first).
