@@ -75,6 +75,8 @@ SIGNATURES = {
     "attn_rope_bwd": (_i, [_vp, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _st, _vp, _st, _vp, _st, _vp, _vp, _vp,
                            ctypes.c_int64, _i, _i, _i, _i, _i, _vp]),
     "attn_cache_append_rope": (_i, [_vp, _vp, _vp, _st, _vp, _st, _vp, _st, _vp, _st, _vp, _i, _i, _i, _i, _i, _vp]),
+    "attn_fwd_cache_prefix_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_fwd_cache_prefix": (_i, [_vp, _vp, _vp, _i, _vp, _st, _vp, _st, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f, _vp]),
     "attn_check_device_error": (_i, [_vp, ctypes.POINTER(ctypes.c_uint)]),
     "attn_set_wait_limit_ns": (None, [ctypes.c_ulonglong]),
     "attn_set_exp2_offload": (None, [_i]),
@@ -1162,3 +1164,60 @@ def cache_append_rope(q, k, v, table, k_pages, v_pages, k_scale, v_scale, page_t
         cache, arg, q.data_ptr(), qs, q_out.data_ptr(), qos, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(new_lens), B, H, Hk,
         T, d, _call_stream(torch, device.index, stream)))
     return q_out
+
+
+# ---------------------------------------------------------------------------
+# Sequences that share their first tokens
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=256)
+def fwd_cache_prefix_workspace_bytes(B: int, H: int, Hk: int, T: int, d: int) -> int:
+    return int(load_library().attn_fwd_cache_prefix_workspace_bytes(*map(_c_int, (B, H, Hk, T, d))))
+
+
+def fwd_cache_prefix(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, prefix_lens, group_first=None,
+                     q_lens=None, layout: str = "bhnd", scale: float | None = None, o=None, lse=None, workspace=None,
+                     stream=None):
+    """``fwd_cache`` for a batch whose sequences share their first tokens, which are read once for all.
+
+    prefix_lens: int32 [groups], tokens whose pages the sequences of a group share (their tables
+    begin with the same pages); every query stands behind them.  group_first: int32 [groups + 1],
+    ascending: group g is sequences group_first[g] .. group_first[g + 1] - 1 (default: one group of
+    all).  Both stay on the device, as the lengths do.  ``workspace``:
+    ``fwd_cache_prefix_workspace_bytes`` bytes, one for each call that may overlap.  The rest, and what
+    is returned, as ``fwd_cache``."""
+    import torch
+    device = _explain_device(q, "q")
+    B, H, T, d = _layout_shape(q, layout)
+    qs = _rope_heads(device, "q", q, layout)[1]
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be a tensor [pages, Hk, page_size, d]")
+    Hk, dev = k_pages.shape[1], device.index
+    cache = _cache_arg(torch, dev, device, B, Hk, d, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
+                       q_lens, "q_lens")
+    _explain_on(device, "prefix_lens", prefix_lens, torch.int32, 1)
+    groups = prefix_lens.shape[0]
+    _explain_lens(device, "prefix_lens", prefix_lens, groups)
+    if group_first is not None:
+        _explain_lens(device, "group_first", group_first, groups + 1)
+    if not 1 <= groups <= B or (group_first is None and groups != 1):
+        raise ValueError(f"prefix_lens must be of 1 .. {B} groups, with group_first where there are several; got {groups}")
+    need = fwd_cache_prefix_workspace_bytes(B, H, Hk, T, d)
+    if need == 0:
+        raise ValueError(f"invalid sizes: B {B}, H {H}, Hk {Hk}, T {T}, d {d}")
+    handle = _call_stream(torch, dev, stream)
+    with _on_stream(stream):
+        if o is None:
+            o = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = _call_workspace(torch, dev, stream, handle, need)
+    _explain_like(device, "o", o, q)
+    _explain_lse(device, lse, (B, H, T))
+    if not _workspace_ok(torch, dev, workspace, need):
+        _explain_workspace(device, workspace, need)
+    _check("attn_fwd_cache_prefix", load_library().attn_fwd_cache_prefix(
+        cache, _ptr(group_first), prefix_lens.data_ptr(), groups, q.data_ptr(), qs, o.data_ptr(), _strides4(o, layout),
+        lse.data_ptr(), workspace.data_ptr(), _ptr(q_lens), B, H, Hk, T, d,
+        1.0 / math.sqrt(d) if scale is None else float(scale), handle))
+    return o, lse

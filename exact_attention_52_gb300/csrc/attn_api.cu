@@ -628,6 +628,73 @@ attn_status rope_sizes(int B, int H, int Hk, int N, int d, const int32_t* positi
 
 bool cache_prompt(int H, int Hk, int T) { return static_cast<long long>(T) * (H / Hk) > kPromptMinRows; }
 
+// The checked arguments of an attention over the cache (without a window's sinks, see left and
+// sinks below); the workspace and the error word are still to be set.
+attn_status cache_fwd_params(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o, attn_strides_t os,
+                             float* lse, const void* workspace, const int32_t* q_lens, int B, int H, int Hk, int T, int d,
+                             float scale, int window_left, int sinks, CacheFwdParams* out) {
+    CacheFwdParams& p = *out;
+    attn_status rc = check_sizes(B, H, T, d, scale, 0);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(window_left, 0)) != ATTN_OK) return rc;
+    if (sinks < 0) return ATTN_ERR_INVALID;
+    if ((rc = cache_view(cache, B, Hk, d, &p.c)) != ATTN_OK) return rc;
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(q_lens) & 3u) != 0)
+        return ATTN_ERR_INVALID;
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
+    // rows of a key/value head, and pairs of query tiles of all sequences, count in 32 bits
+    const long long rows = static_cast<long long>(T) * (H / Hk);
+    if (rows > (1 << 30) || B * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;
+    p.q = q;
+    p.o = o;
+    p.qs = from_abi(qs, B, H, T, d);
+    p.os = from_abi(os, B, H, T, d);
+    if (!strides_ok(p.qs, 2) || !strides_ok(p.os, 2) || !distinct(p.os, B, H, T)) return ATTN_ERR_INVALID;
+    p.lse = lse;
+    p.q_lens = q_lens;
+    p.B = B;
+    p.H = H;
+    p.Hk = Hk;
+    p.T = T;
+    p.D = d;
+    p.cs = scale * 1.44269504088896340736f;
+    // A window that covers the longest sequence the table can hold is none, and positions
+    // stay far inside 32 bits.
+    const int cap = cache->max_pages * cache->page_size;
+    p.left = window_left >= cap ? -1 : window_left;
+    p.sinks = p.left < 0 ? 0 : (sinks < cap ? sinks : cap);
+    p.group_first = p.prefix_lens = nullptr;
+    p.groups = 0;
+    p.start = nullptr;
+    p.pre_o = nullptr;
+    p.pre_stat = nullptr;
+    p.rows = p.grid = 0;
+    return ATTN_OK;
+}
+
+// Where a launch's unfinished segments lie.
+void cache_segments(CacheFwdParams* p, void* workspace, bool prompt) {
+    const CacheLayout L = cache_layout(prompt, p->D);
+    p->part = static_cast<float*>(workspace);
+    p->stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + L.stat);
+    p->border = reinterpret_cast<CacheBorder*>(static_cast<uint8_t*>(workspace) + L.border);
+}
+
+// Attention behind shared prefixes: the segments of both launches, one after the other in the
+// same place, then the prefixes' part of every row.
+struct PrefixLayout {
+    size_t pre_o, pre_stat, start, total;
+};
+PrefixLayout prefix_layout(int B, int H, int Hk, int T, int d) {
+    const size_t rows = static_cast<size_t>(B) * T * H;
+    const size_t prompt = cache_layout(true, d).total, rest = cache_layout(cache_prompt(H, Hk, T), d).total;
+    PrefixLayout L;
+    L.pre_o = prompt > rest ? prompt : rest;
+    L.pre_stat = L.pre_o + round256(rows * d * sizeof(float));
+    L.start = L.pre_stat + round256(rows * sizeof(float2));
+    L.total = L.start + round256(static_cast<size_t>(B) * sizeof(int));
+    return L;
+}
 
 }  // namespace
 
@@ -1029,50 +1096,55 @@ size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d) {
     return cache_layout(cache_prompt(H, Hk, T), d).total;
 }
 
+size_t attn_fwd_cache_prefix_workspace_bytes(int B, int H, int Hk, int T, int d) {
+    if (check_sizes(B, H, T, d, 1.f, 0) != ATTN_OK || check_group(H, Hk) != ATTN_OK) return 0;
+    return prefix_layout(B, H, Hk, T, d).total;
+}
+
 attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o, attn_strides_t os,
                            float* lse, void* workspace, const int32_t* q_lens, int B, int H, int Hk, int T, int d,
                            float scale, int window_left, int sinks, attn_stream_t stream) {
-    attn_status rc = check_sizes(B, H, T, d, scale, 0);
-    if (rc != ATTN_OK) return rc;
-    if ((rc = check_group(H, Hk)) != ATTN_OK || (rc = check_window(window_left, 0)) != ATTN_OK) return rc;
-    if (sinks < 0) return ATTN_ERR_INVALID;
     CacheFwdParams p;
-    if ((rc = cache_view(cache, B, Hk, d, &p.c)) != ATTN_OK) return rc;
-    if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(q_lens) & 3u) != 0)
-        return ATTN_ERR_INVALID;
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return ATTN_ERR_INVALID;
-    // rows of a key/value head, and pairs of query tiles of all sequences, count in 32 bits
-    const long long rows = static_cast<long long>(T) * (H / Hk);
-    if (rows > (1 << 30) || B * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;
-    p.q = q;
-    p.o = o;
-    p.qs = from_abi(qs, B, H, T, d);
-    p.os = from_abi(os, B, H, T, d);
-    if (!strides_ok(p.qs, 2) || !strides_ok(p.os, 2) || !distinct(p.os, B, H, T)) return ATTN_ERR_INVALID;
-    p.lse = lse;
-    p.q_lens = q_lens;
-    p.B = B;
-    p.H = H;
-    p.Hk = Hk;
-    p.T = T;
-    p.D = d;
-    p.cs = scale * 1.44269504088896340736f;
-    // A window that covers the longest sequence the table can hold is none, and positions
-    // stay far inside 32 bits.
-    const int cap = cache->max_pages * cache->page_size;
-    p.left = window_left >= cap ? -1 : window_left;
-    p.sinks = p.left < 0 ? 0 : (sinks < cap ? sinks : cap);
-    p.part = static_cast<float*>(workspace);
+    attn_status rc = cache_fwd_params(cache, q, qs, o, os, lse, workspace, q_lens, B, H, Hk, T, d, scale, window_left, sinks, &p);
+    if (rc != ATTN_OK) return rc;
     const bool prompt = cache_prompt(H, Hk, T);
-    const CacheLayout L = cache_layout(prompt, d);
-    p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + L.stat);
-    p.border = reinterpret_cast<CacheBorder*>(static_cast<uint8_t*>(workspace) + L.border);
+    cache_segments(&p, workspace, prompt);
     DeviceState ds;
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
-    p.rows = p.grid = 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return (prompt ? launch_cache_prompt(p, s) : launch_cache_decode(p, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return (prompt ? launch_cache_prompt(p, kWhole, s) : launch_cache_decode(p, kWhole, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* group_first, const int32_t* prefix_lens,
+                                  int groups, const void* q, attn_strides_t qs, void* o, attn_strides_t os, float* lse,
+                                  void* workspace, const int32_t* q_lens, int B, int H, int Hk, int T, int d, float scale,
+                                  attn_stream_t stream) {
+    CacheFwdParams p;
+    attn_status rc = cache_fwd_params(cache, q, qs, o, os, lse, workspace, q_lens, B, H, Hk, T, d, scale, -1, 0, &p);
+    if (rc != ATTN_OK) return rc;
+    if (groups < 1 || groups > B || (group_first == nullptr && groups != 1) || prefix_lens == nullptr) return ATTN_ERR_INVALID;
+    if (((reinterpret_cast<uintptr_t>(group_first) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3u) != 0) return ATTN_ERR_INVALID;
+    // rows of all sequences of a key/value head, and their pairs of query tiles in each group
+    const long long rows = static_cast<long long>(B) * T * (H / Hk);
+    if (rows > (1 << 30) || groups * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;
+    const PrefixLayout L = prefix_layout(B, H, Hk, T, d);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.group_first = group_first;
+    p.prefix_lens = prefix_lens;
+    p.groups = groups;
+    p.pre_o = reinterpret_cast<float*>(ws + L.pre_o);
+    p.pre_stat = reinterpret_cast<float2*>(ws + L.pre_stat);
+    p.start = reinterpret_cast<int*>(ws + L.start);
+    DeviceState ds;
+    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
+    p.st = dev_status(ds);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cache_segments(&p, workspace, true);
+    if (launch_cache_prompt(p, kPrefix, s) != cudaSuccess) return ATTN_ERR_CUDA;
+    const bool prompt = cache_prompt(H, Hk, T);
+    cache_segments(&p, workspace, prompt);
+    return (prompt ? launch_cache_prompt(p, kRest, s) : launch_cache_decode(p, kRest, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status attn_check_device_error(attn_stream_t stream, unsigned int* site) {

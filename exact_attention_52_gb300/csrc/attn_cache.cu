@@ -84,13 +84,14 @@ __device__ __forceinline__ Share equal_shares(const CacheFwdParams& p, long long
 
 // Lays the items of all sequences end to end and finds the sequence at the start
 // of share c (a slice of the sequences per thread).
+template <CachePart PART>
 __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     const int per = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     long long work = 0;
     int items = 0, longest = 0;
     for (int b = b0; b < b1; ++b) {
-        const CacheSeq q = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+        const CacheSeq q = cache_seq_of<kBlock, PART>(p, b);
         if (blockIdx.x == 0) check_len(p.c, p.st, b);
         work += seq_work(p, q, 0);
         items = min(items + row_tiles(p, q) * p.Hk, 1 << 20);
@@ -132,7 +133,7 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
     const long long x = c * s.share;
     if (x < s.total && work_before <= x && x < work_before + work) {
         for (int b = b0; b < b1; ++b) {
-            const long long w = seq_work(p, cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b), s.whole);
+            const long long w = seq_work(p, cache_seq_of<kBlock, PART>(p, b), s.whole);
             if (x < work_before + w) {
                 sm->b = b;
                 sm->b_first = work_before;
@@ -151,13 +152,14 @@ __device__ Share find_share(const CacheFwdParams& p, int c, ShareSmem* sm) {
 // (16 x 4096 tokens, 24 and 64 rows) with up to 64 sequences; with more the block's threads
 // share the reading of the lengths (1024 sequences: 88 us, each warp for itself 107).
 constexpr int kFewSeqs = 64;
+template <CachePart PART>
 __device__ __forceinline__ Share find_share_few(const CacheFwdParams& p, int c) {
     const int lane = threadIdx.x & 31, per = (p.B + 31) >> 5;
     const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
     long long work = 0;
     int items = 0, longest = 0;
     for (int b = b0; b < b1; ++b) {
-        const CacheSeq q = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+        const CacheSeq q = cache_seq_of<kBlock, PART>(p, b);
         if (blockIdx.x == 0 && threadIdx.x < 32) check_len(p.c, p.st, b);
         const int n = row_tiles(p, q) * p.Hk;
         work += static_cast<long long>(q.n) * n;
@@ -183,7 +185,7 @@ __device__ __forceinline__ Share find_share_few(const CacheFwdParams& p, int c) 
     int found = -1;
     if (x < s.total && before <= x && x < before + work) {
         for (int b = b0; b < b1; ++b) {
-            const long long w = seq_work(p, cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b), s.whole);
+            const long long w = seq_work(p, cache_seq_of<kBlock, PART>(p, b), s.whole);
             if (x < before + w) {
                 found = b;
                 break;
@@ -285,7 +287,21 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
     else return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4);
 }
 
-template <int D, int NT>
+// Joins a row's finished sums (maximum m, sum l) with its group's part: maximum and sum of both, and
+// the outputs y of the two.
+struct PreJoin {
+    float f, g;
+    __device__ __forceinline__ PreJoin(float2 pre, float& m, float& l) {
+        const float n = fmaxf(m, pre.x);
+        f = m == -INFINITY ? 0.f : ex2_approx(m - n);
+        g = pre.x == -INFINITY ? 0.f : ex2_approx(pre.x - n);
+        l = l * f + pre.y * g;
+        m = n;
+    }
+    __device__ __forceinline__ float operator()(float y, float pre) const { return y * f + pre * g; }
+};
+
+template <int D, int NT, CachePart PART>
 __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) cache_decode_kernel(const CacheFwdParams p) {
     using T = DecodeTraits<D, NT>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -297,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 
     pdl_launch_dependents();
     pdl_wait();
-    const Share sh = p.B <= kFewSeqs ? find_share_few(p, blockIdx.x) : find_share(p, blockIdx.x, ssm);
+    const Share sh = p.B <= kFewSeqs ? find_share_few<PART>(p, blockIdx.x) : find_share<PART>(p, blockIdx.x, ssm);
     if (sh.b < 0) {  // more CTAs than shares
         if (threadIdx.x == 0) p.border[blockIdx.x].c_first = -1;
         return;
@@ -310,10 +326,10 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
     const int G = p.H / p.Hk;
 
     while (x < x_end) {
-        CacheSeq s = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+        CacheSeq s = cache_seq_of<kBlock, PART>(p, b);
         for (long long w; x >= b_first + (w = seq_work(p, s, sh.whole));) {  // next sequence with work
             b_first += w;
-            s = cache_seq<kBlock>(p.c, p.q_lens, p.T, p.left, p.sinks, ++b);
+            s = cache_seq_of<kBlock, PART>(p, ++b);
         }
         // segment [v0, v1) of the item's n blocks
         const int rts = row_tiles(p, s);
@@ -766,6 +782,20 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                 }
             }
             if (finished) {
+                if constexpr (PART == kRest) {
+                    if (s.key_lo > 0) {
+                        const long long at = pre_row(p, b, a.t, a.h);
+                        const PreJoin j(p.pre_stat[at], mm, ll);
+#pragma unroll
+                        for (int e = 0; e < CPT; e += 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(p.pre_o + at * D + c0 + e);
+                            acc[e] = j(acc[e], y.x);
+                            acc[e + 1] = j(acc[e + 1], y.y);
+                            acc[e + 2] = j(acc[e + 2], y.z);
+                            acc[e + 3] = j(acc[e + 3], y.w);
+                        }
+                    }
+                }
                 const float inv = ll != 0.f ? 1.f / ll : 0.f;  // NaN stays NaN
                 uint32_t pk[CPT / 2];
 #pragma unroll
@@ -815,7 +845,7 @@ struct Joined {
     }
 };
 
-template <int D>
+template <int D, CachePart PART>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const CacheFwdParams p) {
     constexpr int E = D / 32;
     __shared__ float o_sm[kJoinWarps][D];
@@ -856,15 +886,38 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
         }
         return x;
     };
-    auto write = [&](int r, const Joined<D>& x) {
-        const RowAt a = row_at(p, bd.q_len, hk, rt, r);
+    auto write = [&](int r, Joined<D> x) {
+        RowAt a = row_at(p, bd.q_len, hk, rt, r);
+        int b = bd.b;
+        if constexpr (PART == kPrefix) group_row(p, group_begin(p, bd.b), b, a.t);
+        if constexpr (PART != kWhole) {
+            const long long at = pre_row(p, b, a.t, a.h);
+            float* pre = p.pre_o + at * D + lane * E;
+            if constexpr (PART == kPrefix) {
+#pragma unroll
+                for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(pre + e) = make_float2(x.o[e], x.o[e + 1]);
+                if (lane == 0) p.pre_stat[at] = make_float2(x.m, x.l);
+                return;
+            }
+            if (p.start[b] > 0) {
+                const float2 st = p.pre_stat[at];
+                float y[E];
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 v = *reinterpret_cast<const float2*>(pre + e);
+                    y[e] = v.x;
+                    y[e + 1] = v.y;
+                }
+                x.add(st.x, st.y, y);
+            }
+        }
         const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
-        uint16_t* dst = static_cast<uint16_t*>(p.o) + bd.b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
+        uint16_t* dst = static_cast<uint16_t*>(p.o) + b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2)
             *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(x.o[e] * inv, x.o[e + 1] * inv);
         if (lane == 0)
-            p.lse[(static_cast<long long>(bd.b) * p.H + a.h) * p.T + a.t] =
+            p.lse[(static_cast<long long>(b) * p.H + a.h) * p.T + a.t] =
                 x.l != 0.f ? (x.m - kWeightShift + log2f(x.l)) * kLn2 : INFINITY;
     };
     const int mine = (c - bd.c_first) * static_cast<int>(gridDim.y) + blockIdx.y, borders = (n - 1) * static_cast<int>(gridDim.y);
@@ -894,45 +947,52 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     }
 }
 
-template <int D, int NT>
+template <int D, int NT, CachePart PART>
 cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
     using T = DecodeTraits<D, NT>;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t attr = once_per_device(ready, [] {
-        return cudaFuncSetAttribute(cache_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
+        return cudaFuncSetAttribute(cache_decode_kernel<D, NT, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, T::SMEM);
     });
     if (attr != cudaSuccess) return attr;
     p.rows = T::ROWS;
     p.grid = sms * T::CTAS_PER_SM < kCacheGridMax ? sms * T::CTAS_PER_SM : kCacheGridMax;
-    const cudaError_t e = launch_dependent(cache_decode_kernel<D, NT>, dim3(static_cast<unsigned>(p.grid)), kThreads,
-                                           T::SMEM, stream, p);
-    return e != cudaSuccess ? e : launch_cache_join(p, 1, stream);
+    const cudaError_t e = launch_dependent(cache_decode_kernel<D, NT, PART>, dim3(static_cast<unsigned>(p.grid)),
+                                           kThreads, T::SMEM, stream, p);
+    return e != cudaSuccess ? e : launch_cache_join(p, 1, PART, stream);
 }
 
-template <int D>
+template <int D, CachePart PART>
 cudaError_t launch_decode_d(const CacheFwdParams& p, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const long long rows = static_cast<long long>(p.T) * (p.H / p.Hk);
-    if (rows <= 8) return launch_decode_impl<D, 1>(p, sms, stream);
-    return launch_decode_impl<D, 2>(p, sms, stream);
+    if (rows <= 8) return launch_decode_impl<D, 1, PART>(p, sms, stream);
+    return launch_decode_impl<D, 2, PART>(p, sms, stream);
+}
+
+template <int D>
+cudaError_t launch_join_d(const CacheFwdParams& p, dim3 grid, CachePart part, cudaStream_t stream) {
+    if (part == kPrefix) return launch_dependent(cache_join_kernel<D, kPrefix>, grid, 32 * kJoinWarps, 0, stream, p);
+    if (part == kRest) return launch_dependent(cache_join_kernel<D, kRest>, grid, 32 * kJoinWarps, 0, stream, p);
+    return launch_dependent(cache_join_kernel<D, kWhole>, grid, 32 * kJoinWarps, 0, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream) {
+cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, CachePart part, cudaStream_t stream) {
     if (p.grid == 1) return cudaSuccess;  // no border
     const dim3 grid(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(blocks));
-    if (p.D == 64) return launch_dependent(cache_join_kernel<64>, grid, 32 * kJoinWarps, 0, stream, p);
-    if (p.D == 128) return launch_dependent(cache_join_kernel<128>, grid, 32 * kJoinWarps, 0, stream, p);
+    if (p.D == 64) return launch_join_d<64>(p, grid, part, stream);
+    if (p.D == 128) return launch_join_d<128>(p, grid, part, stream);
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream) {
-    if (p.D == 64) return launch_decode_d<64>(p, stream);
-    if (p.D == 128) return launch_decode_d<128>(p, stream);
+cudaError_t launch_cache_decode(const CacheFwdParams& p, CachePart part, cudaStream_t stream) {
+    if (p.D == 64) return part == kRest ? launch_decode_d<64, kRest>(p, stream) : launch_decode_d<64, kWhole>(p, stream);
+    if (p.D == 128) return part == kRest ? launch_decode_d<128, kRest>(p, stream) : launch_decode_d<128, kWhole>(p, stream);
     return cudaErrorInvalidValue;
 }
 

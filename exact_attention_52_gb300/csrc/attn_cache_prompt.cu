@@ -140,6 +140,36 @@ __host__ __device__ inline PromptUnit prompt_unit(const CacheFwdParams& p, int b
     return u;
 }
 
+// The same of a launch's part of the sequences.  A group's prefix: the rows of all its sequences
+// are one sequence's, all of them behind its last key.  The rest of a sequence: from the first
+// key that its group's part does not cover.
+template <CachePart PART>
+__device__ __forceinline__ PromptUnit unit_of(const CacheFwdParams& p, int b, int pair) {
+    if constexpr (PART == kPrefix) {
+        PromptUnit u;
+        u.len = group_len(p, b);
+        u.q_len = max(0, group_end(p, b) - group_begin(p, b)) * p.T;
+        u.rows = u.q_len * (p.H / p.Hk);
+        u.first_pos = u.pos_lo = u.pos_hi = u.len - 1;
+        const int r0 = pair * kPairRows;
+        u.n = u.n0 = u.n1 = r0 < u.rows ? u.len / kTile : 0;
+        u.dual = r0 + kTile >= u.rows;
+        u.n_sink = u.lo = u.key_lo = 0;
+        return u;
+    }
+    PromptUnit u = prompt_unit(p, b, pair);
+    if constexpr (PART == kRest) {
+        if (u.n > 0) {
+            u.key_lo = p.start[b];
+            u.lo = u.key_lo / kTile;
+            u.n0 = max(0, u.n0 - u.lo);
+            u.n1 = max(0, u.n1 - u.lo);
+            u.n = max(1, u.n1);
+        }
+    }
+    return u;
+}
+
 // Tiles [first, end) of a segment [v0, v1), tile t0 of its CTA the first, that lie among the
 // CTA's tiles lo .. hi (none: INT_MAX, -1).
 struct TileSpan {
@@ -163,14 +193,15 @@ struct PromptShareSmem {
     int unit;
 };
 
+template <CachePart PART>
 __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptShareSmem* sm) {
     constexpr int W = kPromptThreads / 32;
-    const int units = p.B * pairs, per = (units + kPromptThreads - 1) / kPromptThreads;
+    const int units = (PART == kPrefix ? p.groups : p.B) * pairs, per = (units + kPromptThreads - 1) / kPromptThreads;
     const int u0 = min(units, static_cast<int>(threadIdx.x) * per), u1 = min(units, u0 + per);
-    auto work = [&](int u) { return static_cast<long long>(prompt_unit(p, u / pairs, u % pairs).n) * p.Hk; };
+    auto work = [&](int u) { return static_cast<long long>(unit_of<PART>(p, u / pairs, u % pairs).n) * p.Hk; };
     long long mine = 0;
     for (int u = u0; u < u1; ++u) {
-        if (blockIdx.x == 0 && u % pairs == 0) check_len(p.c, p.st, u / pairs);
+        if (PART != kPrefix && blockIdx.x == 0 && u % pairs == 0) check_len(p.c, p.st, u / pairs);
         mine += work(u);
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -220,15 +251,16 @@ struct PromptWalk {
     int a0, a1;  // those that softmax group g takes: the first a_g, or (dual) v0 + g, v0 + g + 2, ...
 };
 // By a whole warp; every lane works out the same step.
+template <CachePart PART>
 __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, PromptWalk* walk) {
     PromptWalk w = *walk;
     __syncwarp();
     if (w.s.unit < 0 || w.s.x >= w.s.x_end) return false;
-    w.u = prompt_unit(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
+    w.u = unit_of<PART>(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
     for (long long n; w.s.x >= w.s.unit_first + (n = static_cast<long long>(w.u.n) * p.Hk);) {
         w.s.unit_first += n;
         ++w.s.unit;
-        w.u = prompt_unit(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
+        w.u = unit_of<PART>(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
     }
     w.b = w.s.unit / w.pairs;
     w.pair = w.s.unit - w.b * w.pairs;
@@ -247,7 +279,7 @@ __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, PromptWalk
     return true;
 }
 
-template <int D>
+template <int D, CachePart PART>
 __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const CacheFwdParams p, const int pairs) {
     using T = PromptTraits<D>;
     pdl_wait();
@@ -301,7 +333,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     static_assert(sizeof(PromptWalk) <= 128 && sizeof(PromptShareSmem) <= 256, "walk slots");
     PromptWalk* const walk = reinterpret_cast<PromptWalk*>(smem + T::OFF_WALK + (warp < 10 ? warp : warp - 2) * 128);
     {
-        const PromptShare share = prompt_share(p, pairs, reinterpret_cast<PromptShareSmem*>(smem + T::OFF_WALK));
+        const PromptShare share = prompt_share<PART>(p, pairs, reinterpret_cast<PromptShareSmem*>(smem + T::OFF_WALK));
         __syncthreads();  // the scratch has been read
         if (lane == 0 && (warp < 10 || warp >= 12)) {
             walk->s = share;
@@ -332,10 +364,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         int idx = 0;      // ring position, over all segments
         int tile_no = 0;  // key tiles converted
         bool ok = true;
-        while (ok && next_segment(p, walk)) {
+        while (ok && next_segment<PART>(p, walk)) {
             const uint8_t* kbase = p.c.k_pages + w.hk * p.c.ks.h + crow * kn + cc * 16;
             const uint8_t* vbase = p.c.v_pages + w.hk * p.c.vs.h + crow * vn + cc * 16;
             const int len = w.u.len, key_lo = w.u.key_lo;
+            // Sequence whose table is read: of a group the first one that has queries (a slot of a
+            // batch that has none may hold any table; a group without queries reads page 0, to no end).
+            int seq = w.b;
+            if constexpr (PART == kPrefix) {
+                const int end = group_end(p, w.b);
+                seq = group_begin(p, w.b);
+                while (seq < end && query_count(p, seq) == 0) ++seq;
+                if (seq == end) seq = -1;
+            }
             auto first_tok = [&](int t) { return w.u.tile(t) * kTile + cw * 32; };
             // some query sees a token of the group from tok on
             auto needed = [&](int tok) { return tok < len && (tok + 16 > key_lo || tok < p.sinks); };
@@ -344,7 +385,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             // each look at the table goes to the L2).
             auto fetch = [&](int t) {
                 const int x = t + (lane >> 1), tok = x < w.v1 ? first_tok(x) + 16 * (lane & 1) : len;
-                return needed(tok) ? __ldg(p.c.table + w.b * p.c.table_stride + (tok >> p.c.page_shift)) : 0;
+                return needed(tok) && seq >= 0 ? __ldg(p.c.table + seq * p.c.table_stride + (tok >> p.c.page_shift)) : 0;
             };
             auto checked = [&](int pid) {
                 if (static_cast<unsigned>(pid) < static_cast<unsigned>(p.c.num_pages)) return pid;
@@ -591,7 +632,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 }
             return true;
         };
-        while (next_segment(p, walk)) {
+        while (next_segment<PART>(p, walk)) {
             const int a0 = w.a0, a1 = w.a1;
             if (!(w.u.dual ? run_dual(a0, a1) : run_pair(a0, a1, w.v1 - w.v0))) break;
             ring += 2 * (w.v1 - w.v0);
@@ -607,7 +648,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             bd.c_first = -1;
             bd.b = bd.item = bd.q_len = bd.c_last = 0;
             const long long x = w.s.x;
-            if (next_segment(p, walk) && w.v0 > 0) {
+            if (next_segment<PART>(p, walk) && w.v0 > 0) {
                 bd.b = w.b;
                 bd.item = w.hk * ((w.u.rows + kPairRows - 1) / kPairRows) + w.pair;
                 bd.q_len = w.u.q_len;
@@ -615,6 +656,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 bd.c_last = static_cast<int>(div_mostly32(x - w.v0 + w.u.n - 1, w.s.share));
             }
             if (lane == 0) p.border[blockIdx.x] = bd;
+        } else if (PART == kPrefix && warp == 10) {  // what the launch for the rest finds
+            const int cap = p.c.max_pages * p.c.page_size;
+            for (int b = static_cast<int>(blockIdx.x) * 32 + lane; b < p.B; b += p.grid * 32) {
+                int lo = 0, hi = p.groups;  // the group: the last one that begins at b or before
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    (group_begin(p, mid) <= b ? lo : hi) = mid;
+                }
+                const int start = group_begin(p, lo) <= b && b < group_end(p, lo) ? group_len(p, lo) : 0;
+                p.start[b] = start;
+                // every new query stands behind its group's prefix
+                if (start > 0 && query_count(p, b) > 0 && min(max(p.c.seq_lens[b], 0), cap) - query_count(p, b) < start)
+                    record_device_error(p.st, ATTN_DEVERR_PAGE, 0x305);
+            }
+            for (int g = static_cast<int>(blockIdx.x) * 32 + lane; g < p.groups; g += p.grid * 32)
+                if (static_cast<unsigned>(p.prefix_lens[g]) > static_cast<unsigned>(cap))
+                    record_device_error(p.st, ATTN_DEVERR_PAGE, 0x306);
         }
     } else {
         regs_inc<kSoftmaxRegs>();
@@ -627,14 +685,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         uint8_t* q_row = smem + g * T::TILE_BYTES + row * 128;
         int s_seen = 0, o_seen = 0, tile_no = 0, merges = 0;
         bool ok = true;
-        while (ok && next_segment(p, walk)) {
+        while (ok && next_segment<PART>(p, walk)) {
             const int n = g ? w.a1 : w.a0;
             const bool dual = w.u.dual;
             const int r = w.pair * kPairRows + (dual ? 0 : g * kTile) + row;  // row of the key/value head
-            const bool row_ok = r < w.u.rows;
-            const int t = row_ok ? r / G : 0, h = w.hk * G + (row_ok ? r - t * G : 0);
+            bool row_ok = r < w.u.rows;
+            int t = row_ok ? r / G : 0, member = 0;  // member: sequence of a group's row
+            const int h = w.hk * G + (row_ok ? r - t * G : 0);
             // rows behind the last query (zeros, never written) take its place: no mask of their own
-            const int pos = w.u.first_pos + (row_ok ? t : w.u.q_len - 1);
+            const int pos = w.u.first_pos + (PART == kPrefix ? 0 : row_ok ? t : w.u.q_len - 1);
+            if constexpr (PART == kPrefix) {
+                if (row_ok) group_row(p, group_begin(p, w.b), member, t);
+                row_ok = row_ok && t < query_count(p, member);
+            }
+            auto seq = [&] { return PART == kPrefix ? member : w.b; };
             const int key_min = p.left < 0 ? 0 : pos - p.left;
             float rq = 0.f;
             if (n > 0) {
@@ -642,7 +706,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 // previous segment's last S_g, read here, came after every product on it.
                 uint4 x[D / 8];
                 float amax = 0.f;
-                const uint16_t* src = static_cast<const uint16_t*>(p.q) + w.b * p.qs.b + h * p.qs.h + t * p.qs.n;
+                const uint16_t* src = static_cast<const uint16_t*>(p.q) + seq() * p.qs.b + h * p.qs.h + t * p.qs.n;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
                     x[c] = row_ok ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
@@ -958,8 +1022,24 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m_used);
                 l_sum = l_sum * f0 + l1 * f1;
             }
+            const float* pre = nullptr;  // the row's part of its group's prefix, times fp
+            float fp = 0.f;
+            if constexpr (PART == kRest) {
+                if (finished && row_ok && w.u.key_lo > 0) {
+                    const long long at = pre_row(p, seq(), t, h);
+                    const float2 st = p.pre_stat[at];
+                    pre = p.pre_o + at * D;
+                    const float m0 = l_sum != 0.f ? m_used : -INFINITY, m = fmaxf(m0, st.x);
+                    const float f = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m);
+                    fp = st.x == -INFINITY ? 0.f : ex2_approx(st.x - m);
+                    l_sum = l_sum * f + st.y * fp;
+                    f0 *= f;
+                    f1 *= f;
+                    m_used = m;
+                }
+            }
             // without a live key tile: O = 0 and LSE = +inf, or a segment that takes no part
-            const float inv = n > 0 && l_sum != 0.f ? 1.f / l_sum : 0.f;  // NaN stays NaN
+            const float inv = (n > 0 || pre) && l_sum != 0.f ? 1.f / l_sum : 0.f;  // NaN stays NaN
             const long long part_row =
                 (2ll * blockIdx.x + (w.v0 == 0 ? 1 : 0)) * kPairRows + (dual ? 0 : g * kTile) + row;
             uint16_t* orow = static_cast<uint16_t*>(p.o) + w.b * p.os.b + h * p.os.h + t * p.os.n;
@@ -979,21 +1059,36 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     tmem_ld_wait(o1);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * f0 + u2f(o1[i]) * f1);
+                } else if (PART == kRest && pre) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * f0);
                 }
                 if (!row_ok) continue;
-                if (finished) {
+                if (PART == kRest && pre) {
+#pragma unroll
+                    for (int v = 0; v < 8; ++v) {
+                        const float4 y = *reinterpret_cast<const float4*>(pre + 32 * c + 4 * v);
+                        o[4 * v] = f2u(fmaf(y.x, fp, u2f(o[4 * v])));
+                        o[4 * v + 1] = f2u(fmaf(y.y, fp, u2f(o[4 * v + 1])));
+                        o[4 * v + 2] = f2u(fmaf(y.z, fp, u2f(o[4 * v + 2])));
+                        o[4 * v + 3] = f2u(fmaf(y.w, fp, u2f(o[4 * v + 3])));
+                    }
+                }
+                if (finished && PART != kPrefix) {
                     uint32_t pkd[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) pkd[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
                     st_global_row64<false>(reinterpret_cast<uint8_t*>(orow + 32 * c), pkd);
                 } else {
-                    float* dst = p.part + part_row * D + 32 * c;
+                    float* dst = (PART == kPrefix && finished ? p.pre_o + pre_row(p, seq(), t, h) * D : p.part + part_row * D) + 32 * c;
 #pragma unroll
                     for (int v = 0; v < 8; ++v) st_global_v4(dst + 4 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
                 }
             }
             if (row_ok) {
-                if (finished)
+                if (PART == kPrefix && finished)
+                    p.pre_stat[pre_row(p, seq(), t, h)] = make_float2(l_sum != 0.f ? m_used : -INFINITY, l_sum);
+                else if (finished)
                     p.lse[(static_cast<long long>(w.b) * p.H + h) * p.T + t] =
                         l_sum != 0.f ? (m_used - kWeightShift + log2f(l_sum)) * kLn2 : INFINITY;
                 else
@@ -1017,16 +1112,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     }
 }
 
-template <int D>
+template <int D, CachePart PART>
 cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     using T = PromptTraits<D>;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t attr = once_per_device(ready, [] {
         cudaFuncAttributes a;
-        cudaError_t e = cudaFuncGetAttributes(&a, cache_prompt_kernel<D>);
+        cudaError_t e = cudaFuncGetAttributes(&a, cache_prompt_kernel<D, PART>);
         // the register split draws on what the launch has: with fewer it would wait for ever
         if (e == cudaSuccess && a.numRegs != kLaunchRegs) e = cudaErrorInvalidKernelImage;
-        return e == cudaSuccess ? cudaFuncSetAttribute(cache_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return e == cudaSuccess ? cudaFuncSetAttribute(cache_prompt_kernel<D, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        T::SMEM_BYTES)
                                 : e;
     });
@@ -1037,20 +1132,21 @@ cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     p.rows = kPairRows;
     p.grid = sms < kPromptGridMax ? sms : kPromptGridMax;
-    const long long rows = static_cast<long long>(p.T) * (p.H / p.Hk);
+    const long long rows = static_cast<long long>(PART == kPrefix ? p.B : 1) * p.T * (p.H / p.Hk);  // at most
     const int pairs = static_cast<int>((rows + kPairRows - 1) / kPairRows);
     if ((e = dbg_set_word(p.st.word, stream)) != cudaSuccess) return e;
-    e = launch_dependent(cache_prompt_kernel<D>, dim3(static_cast<unsigned>(p.grid)), kPromptThreads, T::SMEM_BYTES,
+    e = launch_dependent(cache_prompt_kernel<D, PART>, dim3(static_cast<unsigned>(p.grid)), kPromptThreads, T::SMEM_BYTES,
                          stream, p, pairs);
-    return e != cudaSuccess ? e : launch_cache_join(p, 8, stream);
+    return e != cudaSuccess ? e : launch_cache_join(p, 8, PART, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_prompt(const CacheFwdParams& p, cudaStream_t stream) {
-    if (p.D == 64) return launch_prompt_impl<64>(p, stream);
-    if (p.D == 128) return launch_prompt_impl<128>(p, stream);
-    return cudaErrorInvalidValue;
+cudaError_t launch_cache_prompt(const CacheFwdParams& p, CachePart part, cudaStream_t stream) {
+    if (p.D != 64 && p.D != 128) return cudaErrorInvalidValue;
+    if (part == kPrefix) return p.D == 64 ? launch_prompt_impl<64, kPrefix>(p, stream) : launch_prompt_impl<128, kPrefix>(p, stream);
+    if (part == kRest) return p.D == 64 ? launch_prompt_impl<64, kRest>(p, stream) : launch_prompt_impl<128, kRest>(p, stream);
+    return p.D == 64 ? launch_prompt_impl<64, kWhole>(p, stream) : launch_prompt_impl<128, kWhole>(p, stream);
 }
 
 }  // namespace attn

@@ -219,6 +219,11 @@ constexpr int kPromptRows = 256;
 // tensor cores' kernel for prompts.
 constexpr int kPromptMinRows = 64;
 
+// What a launch of the cache attention's kernels does: whole sequences; the groups' prefixes, the
+// rows of all sequences of a group as those of one; or, after that, the rest of each sequence,
+// joined with its group's part.
+enum CachePart { kWhole = 0, kPrefix = 1, kRest = 2 };
+
 struct CacheFwdParams {
     CacheView c;
     const void* q;  // bf16 [B, H, T, D] with strides qs
@@ -229,6 +234,15 @@ struct CacheFwdParams {
     int B, H, Hk, T, D;
     float cs;  // scale * log2(e)
     int left, sinks;
+    // Groups of sequences with a shared prefix (CachePart): group g is sequences group_first[g] ..
+    // group_first[g + 1] - 1 (null: one group of all), which share the pages of their first
+    // prefix_lens[g] tokens.
+    const int* group_first;
+    const int* prefix_lens;
+    int groups;
+    int* start;        // workspace: [B] tokens of a sequence that its group's part covers
+    float* pre_o;      // workspace: that part of each row, as an unfinished segment: fp32 [B, T, H, D]
+    float2* pre_stat;  // [B, T, H]
     // Set by the launcher:
     int rows;      // query rows of a tile
     int grid;      // CTAs that share the work, at most kCacheGridMax
@@ -291,9 +305,9 @@ cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream)
 cudaError_t launch_cache_append_rope(const CacheAppendRopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope_norm_bwd(const RopeBwdParams& p, cudaStream_t stream);
-cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream);
-cudaError_t launch_cache_prompt(const CacheFwdParams& p, cudaStream_t stream);
-cudaError_t launch_cache_decode(const CacheFwdParams& p, cudaStream_t stream);
+cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, CachePart part, cudaStream_t stream);
+cudaError_t launch_cache_prompt(const CacheFwdParams& p, CachePart part, cudaStream_t stream);
+cudaError_t launch_cache_decode(const CacheFwdParams& p, CachePart part, cudaStream_t stream);
 cudaError_t launch_wait_selftest(DevStatus st, cudaStream_t stream);
 
 // Problem check shared by the entry points (sizes, head dim, scale, causal

@@ -63,6 +63,44 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheView& c, const int* q_l
     return s;
 }
 
+// The same of a launch's part of the sequences: the rest starts with the first key that the
+// group's part does not cover, a multiple of kTile.
+template <int TB, CachePart PART>
+__device__ __forceinline__ CacheSeq cache_seq_of(const CacheFwdParams& p, int b) {
+    CacheSeq s = cache_seq<TB>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+    if constexpr (PART == kRest) {
+        s.key_lo = p.start[b];
+        s.lo = s.key_lo / TB;
+        s.n = max(1, (s.len - 1) / TB - s.lo + 1);
+    }
+    return s;
+}
+
+// Tokens that the part of group g covers: whole tiles of kTile, so that no tile is divided
+// between the parts (the tokens behind them are read for each sequence).
+__device__ __forceinline__ int group_len(const CacheFwdParams& p, int g) {
+    return min(max(p.prefix_lens[g], 0), p.c.max_pages * p.c.page_size) / kTile * kTile;
+}
+__device__ __forceinline__ int group_begin(const CacheFwdParams& p, int g) {
+    return p.group_first ? min(max(p.group_first[g], 0), p.B) : 0;
+}
+__device__ __forceinline__ int group_end(const CacheFwdParams& p, int g) {
+    return p.group_first ? min(max(p.group_first[g + 1], 0), p.B) : p.B;
+}
+// Row (virtual query, head of the group) of a group's part: its sequence and query.
+__device__ __forceinline__ void group_row(const CacheFwdParams& p, int first, int& b, int& t) {
+    const int member = t / p.T;
+    b = first + member;
+    t -= member * p.T;
+}
+__device__ __forceinline__ int query_count(const CacheFwdParams& p, int b) {
+    return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
+}
+// Place of a row in pre_o and pre_stat.
+__device__ __forceinline__ long long pre_row(const CacheFwdParams& p, int b, int t, int h) {
+    return (static_cast<long long>(b) * p.T + t) * p.H + h;
+}
+
 // Records a length that leaves the table (the kernels read as if it ended with it).
 __device__ __forceinline__ void check_len(const CacheView& c, const DevStatus& st, int b) {
     if (static_cast<unsigned>(c.seq_lens[b]) > static_cast<unsigned>(c.max_pages * c.page_size))

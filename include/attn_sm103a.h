@@ -460,6 +460,34 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
                            int sinks, attn_stream_t stream);
 
 /*
+ * attn_fwd_cache (without window and sinks) for a batch whose sequences share their first
+ * tokens: group g is the sequences group_first[g] .. group_first[g + 1] - 1, whose page tables
+ * begin with the same pages for their first prefix_lens[g] tokens.  Those are read once for
+ * the group, for the queries of all its sequences; the rest is read for each sequence, and the
+ * two parts are joined with the softmax rule.  The result is attn_fwd_cache's but for the
+ * rounding of fp32 sums in another order.
+ *   group_first : int32 [groups + 1] on the device, ascending, within [0, B]; NULL with groups =
+ *              1: the whole batch.  Sequences of no group share nothing.
+ *   prefix_lens : int32 [groups] on the device, 0 .. max_pages * page_size, any number (the
+ *              last prefix_lens % 128 tokens are read for each sequence).  The first sequence
+ *              of a group that has queries stands for all: its table is read.
+ *   groups   : 1 .. B.
+ *   workspace : attn_fwd_cache_prefix_workspace_bytes() bytes, 256-byte aligned, overwritten;
+ *              calls that may overlap need one each.
+ * Every query stands behind its group's prefix: a sequence with queries whose seq_lens[b] -
+ * q_lens[b] is smaller (but for the last prefix_lens % 128 tokens), or a prefix length outside
+ * the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE, and its rows are
+ * undefined.  Two launches (and their joins).  Otherwise as attn_fwd_cache, with its errors.
+ * Source: ai.engineer item 59 (small-query work split across thread blocks plus a separate
+ * combining kernel); no page describes shared prefixes.
+ */
+size_t attn_fwd_cache_prefix_workspace_bytes(int B, int H, int Hk, int T, int d);
+attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* group_first, const int32_t* prefix_lens,
+                                  int groups, const void* q, attn_strides_t qs, void* o, attn_strides_t os, float* lse,
+                                  void* workspace, const int32_t* q_lens, int B, int H, int Hk, int T, int d, float scale,
+                                  attn_stream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the library's device error
  * word on the current device.  Returns ATTN_ERR_TIMEOUT if any kernel's
  * bounded wait gave up since the last check (the results of that launch are

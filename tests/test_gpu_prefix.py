@@ -1,0 +1,249 @@
+"""attn_fwd_cache_prefix against the fp64 oracle of the cache attention, which knows nothing of
+shared pages.  Tolerances are those of the cache attention (test_gpu_cache): joining the two parts
+adds a few fp32 roundings, 2^-22 of the sums, to the 2^-15 that scores and exponentials have."""
+
+import numpy as np
+import pytest
+
+from exact_attention_52_gb300 import api
+from oracle import rope as rope_oracle
+from oracle import streaming
+
+from .test_gpu_cache import Pool, bf16, check_clean, check_out, i32
+from .test_gpu_rope import THETA, table_of
+
+pytestmark = pytest.mark.gpu
+
+
+def shared_pool(seed, B, Hk, d, page, firsts, prefixes, lens, token_major=False):
+    """A pool whose groups' tables begin with the same pages."""
+    pool = Pool(seed, B, Hk, d, page, max(1, -(-max(*lens, *prefixes, 1) // page)), token_major)
+    for g, n in enumerate(prefixes):
+        for b in range(firsts[g] + 1, firsts[g + 1]):
+            pool.table[b, :-(-n // page)] = pool.table[firsts[g], :-(-n // page)]
+    return pool
+
+
+def run(pool, H, T, firsts, prefixes, lens, q_lens, layout="bhnd", amp=1.0, table=None, **kw):
+    import torch
+    q, qv = bf16(pool.rng, (pool.B, H, T, pool.d), layout, amp)
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((pool.B, H, T), 7.0, device="cuda")
+    dev = pool.dev()
+    if table is not None:
+        dev[4] = i32(table)
+    args = (q, *dev, i32(lens), i32(prefixes))
+    kw.update(group_first=None if firsts is None else i32(firsts), q_lens=None if q_lens is None else i32(q_lens), layout=layout)
+    api.fwd_cache_prefix(*args, o=o, lse=lse, **kw)
+    check_clean()
+    ql = [T] * pool.B if q_lens is None else q_lens
+    ref = streaming.cache_forward(qv, pool.k, pool.v, pool.ks, pool.vs, pool.table, lens, ql,
+                                  kw.get("scale") or pool.d ** -0.5)
+    check_out(o, lse, ref, layout)
+    ob = o if layout == "bhnd" else o.transpose(1, 2)
+    for b, t in np.argwhere(~ref[3]):
+        assert torch.all(ob[b, :, t] == 7.0) and torch.all(lse[b, :, t] == 7.0)
+    o2, lse2 = api.fwd_cache_prefix(*args, **kw)  # the same bits again, with tensors of its own
+    at = torch.from_numpy(ref[3]).cuda()[:, None]
+    oa, ob = ((x if layout == "bhnd" else x.transpose(1, 2)) for x in (o, o2))
+    assert torch.equal(torch.where(at[..., None], oa, 0).view(torch.int16), torch.where(at[..., None], ob, 0).view(torch.int16))
+    assert torch.equal(torch.where(at, lse, 0).view(torch.int32), torch.where(at, lse2, 0).view(torch.int32))
+    return o, lse
+
+
+# (B, H, Hk, T, page, group_first, prefix_lens, seq_lens, q_lens)
+SHAPES = [
+    (1, 1, 1, 1, 16, [0, 1], [128], [129], None),
+    (1, 4, 4, 1, 64, [0, 1], [0], [1], None),
+    (2, 8, 2, 1, 16, [0, 2], [127], [128, 300], None),               # shorter than a tile: read for each sequence
+    (3, 8, 2, 1, 64, [0, 3], [300], [301, 500, 333], None),          # not a whole tile, nor a whole page
+    (4, 6, 2, 3, 32, [0, 4], [512], [515, 700, 0, 900], [3, 2, 0, 1]),
+    (5, 4, 1, 1, 128, [0, 2, 2, 5], [256, 128, 1280], [300, 257, 1281, 1400, 2000], None),  # an empty group
+    (6, 4, 2, 2, 16, [1, 3, 4], [128, 384], [50, 130, 140, 500, 2, 3], [2, 2, 2, 2, 2, 2]),  # sequences of no group
+    (9, 40, 2, 1, 1024, [0, 9], [2048], [2048 + 3 * i + 1 for i in range(9)], None),
+    (40, 32, 4, 1, 64, [0, 40], [640], [641 + 7 * i for i in range(40)], None),               # more than one pair of query tiles
+    (3, 8, 2, 40, 32, [0, 3], [256], [256 + 40, 700, 300], [40, 33, 1]),                      # prompts behind a prefix
+    (4, 5, 1, 100, 64, [0, 2, 4], [900, 256], [1000, 1300, 356, 999], [100, 0, 100, 71]),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("layout", ["bhnd", "bnhd"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_prefix_matches_oracle(shape, layout, d):
+    B, H, Hk, T, page, firsts, prefixes, lens, ql = shape
+    pool = shared_pool(7 * B + T, B, Hk, d, page, firsts, prefixes, lens, layout == "bnhd")
+    run(pool, H, T, firsts, prefixes, lens, ql, layout)
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_one_group_by_default_and_a_scale(T):
+    pool = shared_pool(3, 4, 2, 128, 32, [0, 4], [384], [500, 600, 414, 900])
+    run(pool, 8, T, None, [384], [500, 600, 414, 900], None, scale=0.3, amp=2.0)
+
+
+def test_long_prefix():
+    lens = [20000 + 40 * i for i in range(6)]
+    pool = shared_pool(4, 6, 1, 64, 64, [0, 6], [19999], lens)
+    run(pool, 8, 1, [0, 6], [19999], lens, None)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_slot_without_queries_may_hold_any_table(T):
+    """The first sequence of a group that has queries stands for it; tables of the others are not read."""
+    lens, ql = [0, 500, 700, 0], [0, T, T, 0]
+    pool = shared_pool(5, 4, 2, 64, 16, [0, 4], [384], [500, 500, 700, 0])
+    junk = pool.table.copy()
+    junk[0], junk[3] = 10 ** 6, -5
+    run(pool, 4, T, [0, 4], [384], lens, ql, table=junk)
+
+
+def test_a_group_without_queries():
+    lens, ql = [0, 0, 300], [0, 0, 1]
+    pool = shared_pool(6, 3, 2, 128, 16, [0, 2, 3], [128, 256], [128, 128, 300])
+    junk = pool.table.copy()
+    junk[:2] = 10 ** 6
+    run(pool, 4, 1, [0, 2, 3], [128, 256], lens, ql, table=junk)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("where", ["prefix", "rest", "both"])
+def test_value_scales_far_apart(where, T):
+    """Parts whose sums are taken apart join with parts whose sums are not."""
+    lens = [400, 512, 700]
+    pool = shared_pool(8, 3, 2, 128, 64, [0, 3], [256], lens)
+    for b in range(3):
+        for pg in range(pool.table.shape[1]):
+            if where == "both" or (pg < 4) == (where == "prefix"):
+                pool.vs[pool.table[b, pg]] = 2.0 ** (-100 if (b + pg) % 2 or pg < 4 else 60)
+    run(pool, 4, T, [0, 3], [256], lens, None)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_nan_values_reach_the_rows_that_see_them(T):
+    lens = [300, 400]
+    for pg, col in ((1, 3), (None, 5)):  # in the prefix; behind the second sequence's last token
+        pool = shared_pool(9, 2, 1, 64, 64, [0, 2], [256], lens)
+        if pg is not None:
+            pool.v[pool.table[0, pg], 0, 10, col] = 0x7F
+        else:
+            pool.v[pool.table[1, 400 // 64], 0, 400 % 64, col] = 0x7F
+            pool.k[pool.table[1, 400 // 64], 0, 400 % 64, col] = 0xFF
+        run(pool, 4, T, [0, 2], [256], lens, None)
+
+
+def test_lengths_that_do_not_fit_are_reported():
+    import torch
+    pool = shared_pool(10, 3, 2, 64, 16, [0, 3], [256], [300, 300, 300])
+    q = torch.randn(3, 4, 2, 64, device="cuda").bfloat16()
+    dev = pool.dev()
+    ok = lambda **kw: api.fwd_cache_prefix(q, *dev, i32(kw.get("lens", [300, 290, 280])), i32([kw.get("prefix", 256)]))
+    ok()
+    check_clean()
+    for kw in (dict(lens=[300, 257, 280]), dict(lens=[300, 0, 280]), dict(lens=[300, -7, 280]), dict(lens=[300, 100000, 280]),
+               dict(prefix=100000), dict(prefix=-1)):
+        ok(**kw)
+        assert api.check_device_error()[0] == -5, kw
+    bad = pool.table.copy()
+    bad[0, 3] = 10 ** 6
+    dev[4] = i32(bad)
+    ok()
+    assert api.check_device_error()[0] == -5
+
+
+def test_captured_calls_follow_their_lengths():
+    """Lengths, prefixes and groups stay on the device; two captured calls have workspaces of their own."""
+    import torch
+    pool = shared_pool(11, 4, 2, 128, 64, [0, 4], [512], [600] * 4)
+    dev = pool.dev()
+    q = torch.randn(4, 8, 1, 128, device="cuda").bfloat16()
+    seq, pre, first = i32([520, 530, 540, 550]), i32([512, 512]), i32([0, 2, 4])
+    call = lambda: api.fwd_cache_prefix(q, *dev, seq, pre, group_first=first)
+    call()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call()
+        graphs.append((g, out))
+    s = torch.cuda.Stream()
+    for step in range(3):
+        graphs[0][0].replay()
+        with torch.cuda.stream(s):
+            s.wait_stream(torch.cuda.current_stream())
+            graphs[1][0].replay()
+        s.synchronize()
+        torch.cuda.synchronize()
+        ref = call()
+        for _, out in graphs:
+            assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+        seq += 9
+        pre.copy_(i32([256, 384]))
+        first.copy_(i32([0, 3, 4]))
+    check_clean()
+    s.wait_stream(torch.cuda.current_stream())
+    o, lse = api.fwd_cache_prefix(q, *dev, seq, pre, group_first=first, stream=s)
+    s.synchronize()
+    ref = call()
+    assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_decoding_behind_a_shared_prompt():
+    """The operators as they are used: a prompt written and rotated once, then steps of a few tokens
+    of three sequences behind it, each written, rotated and attended in two calls."""
+    import torch
+    B, H, Hk, d, page, prompt = 3, 8, 2, 128, 32, 320
+    rng = np.random.default_rng(12)
+    pool = shared_pool(12, B, Hk, d, page, [0, B], [prompt], [prompt + 40] * B)
+    dev, table = pool.dev(), table_of(64)
+    w = torch.from_numpy(rng.uniform(0.5, 1.5, d).astype(np.float32)).cuda()
+    kw = dict(q_weight=w, k_weight=w, layout="bnhd")
+    new = lambda b, t, h: torch.from_numpy(rng.standard_normal((b, t, h, d)).astype(np.float32)).bfloat16().cuda()
+    # the prompt, as the first sequence's
+    one = [*dev[:4], dev[4][:1]]
+    api.cache_append_rope(new(1, prompt, H), new(1, prompt, Hk), new(1, prompt, Hk), table, *one, i32([prompt]), **kw)
+    lens = np.full(B, prompt)
+    for step in range(12):
+        T = 1 + step % 3
+        m = [T, (step + 1) % (T + 1), T]
+        lens = lens + m
+        q, k, v = new(B, T, H), new(B, T, Hk), new(B, T, Hk)
+        seq, nl = i32(lens), i32(m)
+        qr = api.cache_append_rope(q, k, v, table, *dev, seq, new_lens=nl, q_out=torch.zeros_like(q), **kw)
+        o, lse = api.fwd_cache_prefix(qr, *dev, seq, i32([prompt]), q_lens=nl, layout="bnhd")
+        check_clean()
+        # the oracle on what the cache holds now, queries rotated by the oracle
+        kc, vc = (x.cpu().numpy() for x in dev[:2])
+        ks, vs = (x.double().cpu().numpy() for x in dev[2:4])
+        qv = qr.transpose(1, 2).double().cpu().numpy()
+        ref = streaming.cache_forward(qv, kc, vc, ks, vs, pool.table, lens, m, d ** -0.5)
+        check_out(o, lse, ref, "bnhd")
+        x = q.transpose(1, 2).double().cpu().numpy()
+        pos = lens[:, None] - np.asarray(m)[:, None] + np.arange(T)
+        y, size = rope_oracle.forward(x, rope_oracle.angles(pos, THETA[64])[:, None], 1.0, 64, False, w.double().cpu().numpy())
+        there = ref[3][:, None, :, None]
+        assert np.all(np.where(there, np.abs(qv - y) <= 2.0 ** -20 * size + 2.0 ** -8 * (np.abs(y) + size), qv == 0))
+
+
+def test_arguments_that_are_refused():
+    import torch
+    pool = shared_pool(13, 2, 2, 64, 16, [0, 2], [128], [140, 150])
+    dev = pool.dev()
+    q, lens, pre = torch.randn(2, 4, 1, 64, device="cuda").bfloat16(), i32([140, 150]), i32([128])
+    api.fwd_cache_prefix(q, *dev, lens, pre)
+    bad = [dict(q=q.float()), dict(q=q.cpu()), dict(q=q[0]), dict(q=torch.randn(2, 3, 1, 64, device="cuda").bfloat16()),
+           dict(prefix_lens=pre.long()), dict(prefix_lens=pre.cpu()), dict(prefix_lens=i32([[128]])), dict(prefix_lens=i32([])),
+           dict(prefix_lens=i32([128, 128])), dict(prefix_lens=i32([1, 1, 1]), group_first=i32([0, 1, 1, 2])),
+           dict(group_first=i32([0, 1, 2])), dict(group_first=i32([0])), dict(q_lens=i32([1])), dict(layout="nbhd"),
+           dict(o=q.float()), dict(lse=torch.zeros(2, 4, device="cuda")), dict(k_pages=dev[0][0]),
+           dict(workspace=torch.empty(512, dtype=torch.uint8, device="cuda"))]
+    for b in bad:
+        a = dict(q=q, k_pages=dev[0], v_pages=dev[1], k_scale=dev[2], v_scale=dev[3], page_table=dev[4], seq_lens=lens,
+                 prefix_lens=pre)
+        a.update(b)
+        with pytest.raises(ValueError):
+            api.fwd_cache_prefix(**a)
+    with pytest.raises(api.AttnError):
+        api.fwd_cache_prefix(q, *dev, lens, pre, scale=0.0)
+    with pytest.raises(api.AttnError):
+        api.fwd_cache_prefix(q, *dev, lens, pre, o=q[:, :1].expand(2, 4, 1, 64))

@@ -68,3 +68,21 @@ def test_calls_without_a_gpu_name_the_argument():
         api.cache_append_rope(q, q, q, table, q, q, q, q, q, q)
     with pytest.raises(ValueError, match="unknown layout"):
         api.rope(q, q, table, layout="nbhd")
+
+
+def test_a_bad_prefix_is_refused(lib):
+    fake, st = ctypes.c_void_p(1 << 20), api.Strides(64, 64, 64)
+    cache = api._CACHE.pack(*[1 << 20] * 2, *[64] * 6, *[1 << 20] * 3, 1, 1 << 20, 1, 16, 1)
+
+    def call(first=fake, lens=fake, groups=1, B=1, T=1, d=64, scale=0.125, ws=fake, q=fake):
+        return lib.attn_fwd_cache_prefix(cache, first, lens, groups, q, st, fake, st, fake, ws, None, B, 1, 1, T, d, scale, None)
+    for kw in (dict(lens=None), dict(lens=ctypes.c_void_p(2)), dict(first=ctypes.c_void_p((1 << 20) + 2)), dict(groups=0),
+               dict(groups=2), dict(groups=-1), dict(B=0), dict(T=0), dict(scale=0.0), dict(ws=None),
+               dict(ws=ctypes.c_void_p((1 << 20) + 16)), dict(q=None)):
+        assert call(**kw) == -1, kw
+    assert call(d=96) == -2
+    sizes = lib.attn_fwd_cache_prefix_workspace_bytes
+    assert sizes(1, 3, 2, 1, 64) == 0 and sizes(0, 1, 1, 1, 64) == 0 and sizes(1, 1, 1, 1, 96) == 0
+    # the segments of the larger launch, then the prefixes' part: fp32 rows, their statistics, a number a sequence
+    more = sizes(64, 32, 8, 2, 128) - sizes(1, 32, 8, 2, 128)
+    assert more == 63 * 2 * 32 * (128 * 4 + 8) and sizes(1, 32, 8, 2, 128) > lib.attn_fwd_cache_workspace_bytes(1, 32, 8, 200, 128)
