@@ -453,7 +453,9 @@ def _on_stream(stream):
 # The compiled half of the binding: (the library that it calls, the module or None).
 _calls = None
 _CALL_FUNCTIONS = ("attn_cache_append", "attn_fwd_cache_workspace_bytes", "attn_fwd_cache", "attn_fwd_sinks",
-                   "attn_bwd_sinks_workspace_bytes", "attn_bwd_sinks")
+                   "attn_bwd_sinks_workspace_bytes", "attn_bwd_sinks", "attn_rope", "attn_rope_bwd_workspace_bytes",
+                   "attn_rope_bwd", "attn_cache_append_rope", "attn_fwd_cache_prefix_workspace_bytes",
+                   "attn_fwd_cache_prefix")
 
 
 def _call_tag(torch):
@@ -1069,6 +1071,14 @@ def rope(q, k, table, positions=None, q_weight=None, k_weight=None, eps: float =
     ([d], fp32 or bf16) a head x becomes x / sqrt(mean(x^2) + eps) * weight before its first
     ``table.rot`` elements are rotated."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None and table.__class__ is RopeTable:
+        done = calls.rope(q, k, table.turns, table.interleaved, table.magnitude, q_weight, k_weight, eps, positions,
+                          layout == "bnhd", q_out, k_out, dev, handle)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            _check("attn_rope", done)
     device, B, H, Hk, N, d, qs, ks = _rope_qk(q, k, layout)
     at, step = _rope_positions(device, positions, B, N)
     arg = _rope_arg(torch, device, d, table, q_weight, None if k is None else k_weight, eps)
@@ -1097,6 +1107,17 @@ def rope_bwd(dq_out, dk_out, table, positions=None, q=None, k=None, q_weight=Non
     inputs, which only a tensor with a weight needs; dq may be dq_out, dk dk_out.  ``workspace``:
     ``rope_bwd_workspace_bytes`` bytes, one for each call that may overlap."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None and table.__class__ is RopeTable:
+        ws = workspace
+        if ws is None and not torch._C._cuda_isCurrentStreamCapturing():
+            ws = _kept.__dict__.get((dev, handle))
+        done = calls.rope_bwd(dq_out, dk_out, table.turns, table.interleaved, table.magnitude, q_weight, k_weight, eps,
+                              positions, q, k, layout == "bnhd", dq, dk, dq_weight, dk_weight, ws, dev, handle)
+        if done.__class__ is tuple:
+            return done
+        if done is not None:
+            _check("attn_rope_bwd", done)
     device, B, H, Hk, N, d, gqs, gks = _rope_qk(dq_out, dk_out, layout, ("dq_out", "dk_out"))
     if dk_out is None:
         k = k_weight = None
@@ -1149,6 +1170,15 @@ def cache_append_rope(q, k, v, table, k_pages, v_pages, k_scale, v_scale, page_t
     the new_lens[b] (default T) new ones is rotated at its position in the cache, seq_lens - new_lens
     + t.  Rows of q_out behind them are left as they were.  The rest as ``rope`` and ``cache_append``."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None and table.__class__ is RopeTable:
+        done = calls.cache_append_rope(q, k, v, table.turns, table.interleaved, table.magnitude, q_weight, k_weight, eps,
+                                       k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, new_lens,
+                                       layout == "bnhd", q_out, dev, handle)
+        if done.__class__ is int:
+            _check("attn_cache_append_rope", done)
+        elif done is not None:
+            return done
     device, B, H, Hk, T, d, qs, ks = _rope_qk(q, k, layout)
     if k is None:
         raise ValueError("k must be a bf16 CUDA tensor")
@@ -1186,6 +1216,18 @@ def fwd_cache_prefix(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens
     ``fwd_cache_prefix_workspace_bytes`` bytes, one for each call that may overlap.  The rest, and what
     is returned, as ``fwd_cache``."""
     import torch
+    calls, dev, handle = _read(torch, stream, layout)
+    if calls is not None:
+        ws = workspace
+        if ws is None and not torch._C._cuda_isCurrentStreamCapturing():
+            ws = _kept.__dict__.get((dev, handle))
+        if ws is not None:
+            done = calls.fwd_cache_prefix(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, prefix_lens,
+                                          group_first, q_lens, layout == "bnhd", scale, o, lse, ws, dev, handle)
+            if done.__class__ is tuple:
+                return done
+            if done is not None:
+                _check("attn_fwd_cache_prefix", done)
     device = _explain_device(q, "q")
     B, H, T, d = _layout_shape(q, layout)
     qs = _rope_heads(device, "q", q, layout)[1]

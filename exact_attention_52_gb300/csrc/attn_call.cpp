@@ -12,6 +12,7 @@
 
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 #include <ATen/ops/empty.h>
 #include <ATen/ops/empty_like.h>
@@ -28,6 +29,12 @@ struct Library {
     decltype(&attn_fwd_sinks) fwd_sinks = nullptr;
     decltype(&attn_bwd_sinks_workspace_bytes) bwd_sinks_workspace_bytes = nullptr;
     decltype(&attn_bwd_sinks) bwd_sinks = nullptr;
+    decltype(&attn_rope) rope = nullptr;
+    decltype(&attn_rope_bwd_workspace_bytes) rope_bwd_workspace_bytes = nullptr;
+    decltype(&attn_rope_bwd) rope_bwd = nullptr;
+    decltype(&attn_cache_append_rope) cache_append_rope = nullptr;
+    decltype(&attn_fwd_cache_prefix_workspace_bytes) fwd_cache_prefix_workspace_bytes = nullptr;
+    decltype(&attn_fwd_cache_prefix) fwd_cache_prefix = nullptr;
 } lib;
 
 struct Unread {};  // arguments for the Python half
@@ -67,9 +74,9 @@ int small(PyObject* o) {
 
 // [B, heads, N, d] (or [B, N, heads, d]) of bf16, d contiguous.
 struct Rows {
-    const at::Tensor* t;
-    int B, H, N, D;
-    attn_strides_t st;
+    const at::Tensor* t = nullptr;
+    int B = 0, H = 0, N = 0, D = 0;
+    attn_strides_t st = {};
     void* p() const { return t->data_ptr(); }
 };
 Rows rows(PyObject* o, int dev, bool bnhd) {
@@ -278,16 +285,189 @@ PyObject* bwd_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+double number(PyObject* o) {
+    need(PyFloat_CheckExact(o));
+    return PyFloat_AS_DOUBLE(o);
+}
+
+// turns, interleaved, magnitude, q_weight, k_weight, eps
+attn_rope_t rope_of(PyObject* const* a, int dev, int D) {
+    const at::Tensor& turns = tensor(a[0], at::kLong, 1, dev);
+    attn_rope_t r = {};
+    need(turns.is_contiguous() && turns.size(0) <= D / 2);
+    r.turns = static_cast<const int64_t*>(turns.data_ptr());
+    r.rot = size(2 * turns.size(0));
+    r.interleaved = a[1] == Py_True;
+    r.factor = static_cast<float>(number(a[2]));
+    const void** to[2] = {&r.q_weight, &r.k_weight};
+    int types = 0;
+    for (int i = 0; i < 2; ++i) {
+        if (a[3 + i] == Py_None) continue;
+        const at::Tensor& w = tensor(a[3 + i]);
+        const bool bf16 = w.scalar_type() == at::kBFloat16;
+        need((bf16 || w.scalar_type() == at::kFloat) && w.dim() == 1 && w.layout() == at::kStrided && w.is_cuda() &&
+             w.get_device() == dev && w.size(0) == D && w.is_contiguous());
+        *to[i] = w.data_ptr();
+        r.weight_bf16 = bf16;
+        types |= bf16 ? 2 : 1;
+    }
+    need(types != 3);
+    r.eps = static_cast<float>(number(a[5]));
+    return r;
+}
+
+// Address and row stride of [N] or [B, N] positions, or none.
+struct Positions {
+    const int32_t* p = nullptr;
+    int64_t stride = 0;
+};
+Positions positions_of(PyObject* o, int B, int N, int dev) {
+    Positions r;
+    if (o == Py_None) return r;
+    const at::Tensor& t = tensor(o);
+    const int64_t rank = t.dim();
+    need(t.scalar_type() == at::kInt && t.layout() == at::kStrided && t.is_cuda() && t.get_device() == dev &&
+         (rank == 1 || rank == 2) && t.size(rank - 1) == N && (rank == 1 || t.size(0) == B) &&
+         (N == 1 || t.stride(rank - 1) == 1));
+    r.p = static_cast<const int32_t*>(t.data_ptr());
+    r.stride = rank == 2 && B > 1 ? t.stride(0) : 0;
+    return r;
+}
+
+bool same_tokens(const Rows& a, const Rows& b) { return a.B == b.B && a.N == b.N && a.D == b.D; }
+
+// q, k, turns, interleaved, magnitude, q_weight, k_weight, eps, positions, bnhd, q_out, k_out, dev, stream
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n == 14 && lib.rope, [&]() -> PyObject* {
+        const bool bnhd = a[9] == Py_True;
+        const int dev = small(a[12]);
+        const Rows q = rows(a[0], dev, bnhd), k = rows(a[1], dev, bnhd);
+        need(same_tokens(q, k));
+        const attn_rope_t r = rope_of(a + 2, dev, q.D);
+        const Positions pos = positions_of(a[8], q.B, q.N, dev);
+        Out qo = like_or_given(a[10], q), ko = like_or_given(a[11], k);
+        const Rows qv = rows_like(qo.o, q, dev, bnhd), kv = rows_like(ko.o, k, dev, bnhd);
+        auto stream = reinterpret_cast<attn_stream_t>(integer(a[13]));
+        const attn_status rc = called([&] {
+            return lib.rope(&r, q.p(), q.st, qv.p(), qv.st, k.p(), k.st, kv.p(), kv.st, pos.p, pos.stride, q.B, q.H, k.H, q.N,
+                            q.D, stream);
+        });
+        return outputs(rc, qo, ko);
+    });
+}
+
+// dq_out, dk_out, turns, interleaved, magnitude, q_weight, k_weight, eps, positions, q, k, bnhd, dq, dk, dq_weight,
+// dk_weight, workspace, dev, stream
+PyObject* rope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n == 19 && lib.rope_bwd, [&]() -> PyObject* {
+        const bool bnhd = a[11] == Py_True;
+        const int dev = small(a[17]);
+        const Rows gq = rows(a[0], dev, bnhd), gk = rows(a[1], dev, bnhd);
+        need(same_tokens(gq, gk));
+        const attn_rope_t r = rope_of(a + 2, dev, gq.D);
+        const Positions pos = positions_of(a[8], gq.B, gq.N, dev);
+        const Rows q = r.q_weight ? rows_like(a[9], gq, dev, bnhd) : Rows(), k = r.k_weight ? rows_like(a[10], gk, dev, bnhd) : Rows();
+        void* w = nullptr;
+        if (r.q_weight || r.k_weight)
+            w = workspace(tensor(a[16]), lib.rope_bwd_workspace_bytes(gq.B, gq.H, gk.H, gq.N, gq.D), dev);
+        Out dq = like_or_given(a[12], gq), dk = like_or_given(a[13], gk);
+        const Rows dqv = rows_like(dq.o, gq, dev, bnhd), dkv = rows_like(dk.o, gk, dev, bnhd);
+        auto weight_grad = [&](PyObject* o, const void* weight) {
+            if (weight == nullptr) return Out(Py_None, nullptr);
+            if (o != Py_None) return Out(o, nullptr);
+            const at::Tensor t = at::empty({gq.D}, gq.t->options().dtype(at::kFloat));
+            return Out(nullptr, &t);
+        };
+        Out dwq = weight_grad(a[14], r.q_weight), dwk = weight_grad(a[15], r.k_weight);
+        float* wq = r.q_weight ? static_cast<float*>(dense(dwq.o, at::kFloat, {gq.D}, dev)) : nullptr;
+        float* wk = r.k_weight ? static_cast<float*>(dense(dwk.o, at::kFloat, {gq.D}, dev)) : nullptr;
+        auto stream = reinterpret_cast<attn_stream_t>(integer(a[18]));
+        const attn_status rc = called([&] {
+            return lib.rope_bwd(&r, r.q_weight ? q.p() : nullptr, q.st, gq.p(), gq.st, dqv.p(), dqv.st, wq,
+                                r.k_weight ? k.p() : nullptr, k.st, gk.p(), gk.st, dkv.p(), dkv.st, wk, w, pos.p, pos.stride,
+                                gq.B, gq.H, gk.H, gq.N, gq.D, stream);
+        });
+        return outputs(rc, dq, dk, dwq, dwk);
+    });
+}
+
+// q, k, v, turns, interleaved, magnitude, q_weight, k_weight, eps, k_pages, v_pages, k_scale, v_scale, page_table,
+// seq_lens, new_lens, bnhd, q_out, dev, stream
+PyObject* cache_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n == 20 && lib.cache_append_rope, [&]() -> PyObject* {
+        const bool bnhd = a[16] == Py_True;
+        const int dev = small(a[18]);
+        const Rows q = rows(a[0], dev, bnhd), k = rows(a[1], dev, bnhd), v = rows_like(a[2], k, dev, bnhd);
+        need(same_tokens(q, k));
+        const attn_rope_t r = rope_of(a + 3, dev, q.D);
+        const attn_cache_t c = cache_of(a + 9, dev, k.B, k.H, k.D);
+        const int32_t* lens = lens_or_null(a[15], k.B, dev);
+        Out qo = like_or_given(a[17], q);
+        const Rows qv = rows_like(qo.o, q, dev, bnhd);
+        auto stream = reinterpret_cast<attn_stream_t>(integer(a[19]));
+        const attn_status rc = called([&] {
+            return lib.cache_append_rope(&c, &r, q.p(), q.st, qv.p(), qv.st, k.p(), k.st, v.p(), v.st, lens, q.B, q.H, k.H, q.N,
+                                         q.D, stream);
+        });
+        return rc != ATTN_OK ? PyLong_FromLong(rc) : qo.release();
+    });
+}
+
+// q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, prefix_lens, group_first, q_lens, bnhd, scale, o, lse,
+// workspace, dev, stream
+PyObject* fwd_cache_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n == 17 && lib.fwd_cache_prefix, [&]() -> PyObject* {
+        const bool bnhd = a[10] == Py_True;
+        const int dev = small(a[15]);
+        const Rows q = rows(a[0], dev, bnhd);
+        const int Hk = size(tensor(a[1], at::kByte, 4, dev).size(1));
+        const attn_cache_t c = cache_of(a + 1, dev, q.B, Hk, q.D);
+        const int groups = size(tensor(a[7], at::kInt, 1, dev).size(0));
+        need(groups >= 1 && groups <= q.B && (groups == 1 || a[8] != Py_None));
+        const int32_t* prefixes = lens_or_null(a[7], groups, dev);
+        const int32_t* first = lens_or_null(a[8], groups + 1, dev);
+        const int32_t* lens = lens_or_null(a[9], q.B, dev);
+        const float scale = scale_of(a[11], q.D);
+        const size_t room = lib.fwd_cache_prefix_workspace_bytes(q.B, q.H, Hk, q.N, q.D);
+        void* w = workspace(tensor(a[14]), room, dev);
+        Out o = like_or_given(a[12], q), lse = lse_or_given(a[13], q);
+        const Rows ov = rows_like(o.o, q, dev, bnhd);
+        float* l = static_cast<float*>(dense(lse.o, at::kFloat, {q.B, q.H, q.N}, dev));
+        auto stream = reinterpret_cast<attn_stream_t>(integer(a[16]));
+        const attn_status rc = called([&] {
+            return lib.fwd_cache_prefix(&c, first, prefixes, groups, q.p(), q.st, ov.p(), ov.st, l, w, lens, q.B, q.H, Hk, q.N,
+                                        q.D, scale, stream);
+        });
+        return outputs(rc, o, lse);
+    });
+}
+
 // Addresses of the library's functions, in the order of Library.
 PyObject* bind(PyObject*, PyObject* args) {
-    unsigned long long p[6];
-    if (!PyArg_ParseTuple(args, "KKKKKK", p, p + 1, p + 2, p + 3, p + 4, p + 5)) return nullptr;
-    lib.cache_append = reinterpret_cast<decltype(lib.cache_append)>(p[0]);
-    lib.fwd_cache_workspace_bytes = reinterpret_cast<decltype(lib.fwd_cache_workspace_bytes)>(p[1]);
-    lib.fwd_cache = reinterpret_cast<decltype(lib.fwd_cache)>(p[2]);
-    lib.fwd_sinks = reinterpret_cast<decltype(lib.fwd_sinks)>(p[3]);
-    lib.bwd_sinks_workspace_bytes = reinterpret_cast<decltype(lib.bwd_sinks_workspace_bytes)>(p[4]);
-    lib.bwd_sinks = reinterpret_cast<decltype(lib.bwd_sinks)>(p[5]);
+    constexpr Py_ssize_t kFunctions = 12;
+    unsigned long long p[kFunctions];
+    if (PyTuple_GET_SIZE(args) != kFunctions) {
+        PyErr_Format(PyExc_TypeError, "%d addresses are expected", static_cast<int>(kFunctions));
+        return nullptr;
+    }
+    for (Py_ssize_t i = 0; i < kFunctions; ++i) {
+        p[i] = PyLong_AsUnsignedLongLong(PyTuple_GET_ITEM(args, i));
+        if (PyErr_Occurred()) return nullptr;
+    }
+    int i = 0;
+    auto next = [&](auto& f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(p[i++]); };
+    next(lib.cache_append);
+    next(lib.fwd_cache_workspace_bytes);
+    next(lib.fwd_cache);
+    next(lib.fwd_sinks);
+    next(lib.bwd_sinks_workspace_bytes);
+    next(lib.bwd_sinks);
+    next(lib.rope);
+    next(lib.rope_bwd_workspace_bytes);
+    next(lib.rope_bwd);
+    next(lib.cache_append_rope);
+    next(lib.fwd_cache_prefix_workspace_bytes);
+    next(lib.fwd_cache_prefix);
     Py_RETURN_NONE;
 }
 
@@ -299,6 +479,10 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                          {"fwd_cache", fast(fwd_cache), METH_FASTCALL, nullptr},
                          {"fwd_sinks", fast(fwd_sinks), METH_FASTCALL, nullptr},
                          {"bwd_sinks", fast(bwd_sinks), METH_FASTCALL, nullptr},
+                         {"rope", fast(rope), METH_FASTCALL, nullptr},
+                         {"rope_bwd", fast(rope_bwd), METH_FASTCALL, nullptr},
+                         {"cache_append_rope", fast(cache_append_rope), METH_FASTCALL, nullptr},
+                         {"fwd_cache_prefix", fast(fwd_cache_prefix), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
