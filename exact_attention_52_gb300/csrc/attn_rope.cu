@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 // one row a block, and a second kernel adds the rows in their order: no atomics, so the sums are
 // the same every time.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_norm_bwd_kernel(const RopeBwdParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const RopeBwdParams p) {
     constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR;
     pdl_wait();
     pdl_launch_dependents();
