@@ -665,9 +665,9 @@ attn_status cache_fwd_params(const attn_cache_t* cache, const void* q, attn_stri
     p.sinks = p.left < 0 ? 0 : (sinks < cap ? sinks : cap);
     p.group_first = p.prefix_lens = nullptr;
     p.groups = 0;
-    p.start = nullptr;
-    p.pre_o = nullptr;
-    p.pre_stat = nullptr;
+    p.items = nullptr;
+    p.fin_o = nullptr;
+    p.fin_stat = nullptr;
     p.rows = p.grid = 0;
     return ATTN_OK;
 }
@@ -680,20 +680,67 @@ void cache_segments(CacheFwdParams* p, void* workspace, bool prompt) {
     p->border = reinterpret_cast<CacheBorder*>(static_cast<uint8_t*>(workspace) + L.border);
 }
 
-// Attention behind shared prefixes: the segments of both launches, one after the other in the
-// same place, then the prefixes' part of every row.
+// A call's sequences in one part.
+attn_status cache_whole(CacheFwdParams* p, void* workspace, attn_stream_t stream) {
+    const bool prompt = cache_prompt(p->H, p->Hk, p->T);
+    cache_segments(p, workspace, prompt);
+    DeviceState ds;
+    const attn_status rc = device_state(&ds);
+    if (rc != ATTN_OK) return rc;
+    p->st = dev_status(ds);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return (prompt ? launch_cache_prompt(p, kWhole, s) : launch_cache_decode(p, kWhole, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// Whether a batch behind shared prefixes is done in two parts, the prefixes for their groups and the
+// rest, or like any other.  Prompts are bound by their products, which sharing does not lessen (2 x
+// 2048 queries behind 16384 tokens: 1.32 ms in two parts, 0.93 in one); and keys of a small cache
+// come out of the L2 again sooner than the two parts' launches take: in one part 4 x 2300 tokens, 8
+// heads, d = 128 (19 MB) take 14 us for 22, 48 x 4600, 4 heads, d = 64 (113 MB) 30 for 40; 64 x 9200,
+// 8 heads, d = 128 (1.2 GB) 121 for 70.  The lengths are on the device; the longest that the table can
+// hold stands for them.
+constexpr long long kPrefixMinBytes = 256ll << 20;
+bool prefix_parts(const attn_cache_t* c, int B, int H, int Hk, int T, int d) {
+    return !cache_prompt(H, Hk, T) && 2ll * d * Hk * B * c->max_pages * c->page_size >= kPrefixMinBytes;
+}
+
+// Of each of the two parts the unfinished segments, the items' CTAs, and the rows of items that one
+// CTA did.
 struct PrefixLayout {
-    size_t pre_o, pre_stat, start, total;
+    struct Part {
+        size_t segments, items, fin_o, fin_stat;
+    } prefix, rest;
+    size_t total;
 };
 PrefixLayout prefix_layout(int B, int H, int Hk, int T, int d) {
-    const size_t rows = static_cast<size_t>(B) * T * H;
-    const size_t prompt = cache_layout(true, d).total, rest = cache_layout(cache_prompt(H, Hk, T), d).total;
+    const size_t rows = static_cast<size_t>(B) * T * H, group_rows = static_cast<size_t>(T) * (H / Hk);
     PrefixLayout L;
-    L.pre_o = prompt > rest ? prompt : rest;
-    L.pre_stat = L.pre_o + round256(rows * d * sizeof(float));
-    L.start = L.pre_stat + round256(rows * sizeof(float2));
-    L.total = L.start + round256(static_cast<size_t>(B) * sizeof(int));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += round256(bytes);
+        return was;
+    };
+    auto part = [&](bool prompt, size_t items) {
+        PrefixLayout::Part p;
+        p.segments = take(cache_layout(prompt, d).total);
+        p.items = take(items * sizeof(int2));
+        p.fin_o = take(rows * d * sizeof(float));
+        p.fin_stat = take(rows * sizeof(float2));
+        return p;
+    };
+    // tiles of kPromptRows rows of all sequences, one more for each of up to B groups; tiles of at
+    // least 8 rows of each sequence
+    L.prefix = part(true, (B * group_rows / kPromptRows + B + 1) * Hk);
+    L.rest = part(false, static_cast<size_t>(B) * Hk * ((group_rows + 7) / 8));
+    L.total = at;
     return L;
+}
+void prefix_part(CacheFwdParams* p, uint8_t* workspace, const PrefixLayout::Part& L, bool prompt) {
+    cache_segments(p, workspace + L.segments, prompt);
+    p->items = reinterpret_cast<int2*>(workspace + L.items);
+    p->fin_o = reinterpret_cast<float*>(workspace + L.fin_o);
+    p->fin_stat = reinterpret_cast<float2*>(workspace + L.fin_stat);
 }
 
 }  // namespace
@@ -1098,7 +1145,7 @@ size_t attn_fwd_cache_workspace_bytes(int B, int H, int Hk, int T, int d) {
 
 size_t attn_fwd_cache_prefix_workspace_bytes(int B, int H, int Hk, int T, int d) {
     if (check_sizes(B, H, T, d, 1.f, 0) != ATTN_OK || check_group(H, Hk) != ATTN_OK) return 0;
-    return prefix_layout(B, H, Hk, T, d).total;
+    return cache_prompt(H, Hk, T) ? cache_layout(true, d).total : prefix_layout(B, H, Hk, T, d).total;
 }
 
 attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_strides_t qs, void* o, attn_strides_t os,
@@ -1106,14 +1153,7 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
                            float scale, int window_left, int sinks, attn_stream_t stream) {
     CacheFwdParams p;
     attn_status rc = cache_fwd_params(cache, q, qs, o, os, lse, workspace, q_lens, B, H, Hk, T, d, scale, window_left, sinks, &p);
-    if (rc != ATTN_OK) return rc;
-    const bool prompt = cache_prompt(H, Hk, T);
-    cache_segments(&p, workspace, prompt);
-    DeviceState ds;
-    if ((rc = device_state(&ds)) != ATTN_OK) return rc;
-    p.st = dev_status(ds);
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return (prompt ? launch_cache_prompt(p, kWhole, s) : launch_cache_decode(p, kWhole, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    return rc != ATTN_OK ? rc : cache_whole(&p, workspace, stream);
 }
 
 attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* group_first, const int32_t* prefix_lens,
@@ -1125,26 +1165,25 @@ attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* grou
     if (rc != ATTN_OK) return rc;
     if (groups < 1 || groups > B || (group_first == nullptr && groups != 1) || prefix_lens == nullptr) return ATTN_ERR_INVALID;
     if (((reinterpret_cast<uintptr_t>(group_first) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3u) != 0) return ATTN_ERR_INVALID;
+    if (!prefix_parts(cache, B, H, Hk, T, d)) return cache_whole(&p, workspace, stream);
     // rows of all sequences of a key/value head, and their pairs of query tiles in each group
     const long long rows = static_cast<long long>(B) * T * (H / Hk);
     if (rows > (1 << 30) || groups * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;
-    const PrefixLayout L = prefix_layout(B, H, Hk, T, d);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.group_first = group_first;
     p.prefix_lens = prefix_lens;
     p.groups = groups;
-    p.pre_o = reinterpret_cast<float*>(ws + L.pre_o);
-    p.pre_stat = reinterpret_cast<float2*>(ws + L.pre_stat);
-    p.start = reinterpret_cast<int*>(ws + L.start);
     DeviceState ds;
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
+    const PrefixLayout L = prefix_layout(B, H, Hk, T, d);
+    CacheFwdParams rest = p;
+    prefix_part(&p, static_cast<uint8_t*>(workspace), L.prefix, true);
+    prefix_part(&rest, static_cast<uint8_t*>(workspace), L.rest, false);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cache_segments(&p, workspace, true);
-    if (launch_cache_prompt(p, kPrefix, s) != cudaSuccess) return ATTN_ERR_CUDA;
-    const bool prompt = cache_prompt(H, Hk, T);
-    cache_segments(&p, workspace, prompt);
-    return (prompt ? launch_cache_prompt(p, kRest, s) : launch_cache_decode(p, kRest, s)) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+    cudaError_t e = launch_cache_prompt(&p, kPrefix, s);
+    if (e == cudaSuccess) e = launch_cache_decode(&rest, kRest, s);
+    if (e == cudaSuccess) e = launch_cache_merge(p, rest, s);
+    return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
 attn_status attn_check_device_error(attn_stream_t stream, unsigned int* site) {

@@ -200,6 +200,9 @@ __device__ __forceinline__ Share find_share_few(const CacheFwdParams& p, int c) 
     return s;
 }
 
+// Row tiles of a sequence with all T queries.
+__device__ __forceinline__ int most_row_tiles(const CacheFwdParams& p) { return (p.T * (p.H / p.Hk) + p.rows - 1) / p.rows; }
+
 // Row r (0 .. p.rows - 1) of row tile rt of a sequence: query and head of the group.
 struct RowAt {
     int t, h;
@@ -287,20 +290,6 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
     else return (r >> 1) * 128 + ((((r & 1) * 4 + c) ^ (r & 6)) << 4);
 }
 
-// Joins a row's finished sums (maximum m, sum l) with its group's part: maximum and sum of both, and
-// the outputs y of the two.
-struct PreJoin {
-    float f, g;
-    __device__ __forceinline__ PreJoin(float2 pre, float& m, float& l) {
-        const float n = fmaxf(m, pre.x);
-        f = m == -INFINITY ? 0.f : ex2_approx(m - n);
-        g = pre.x == -INFINITY ? 0.f : ex2_approx(pre.x - n);
-        l = l * f + pre.y * g;
-        m = n;
-    }
-    __device__ __forceinline__ float operator()(float y, float pre) const { return y * f + pre * g; }
-};
-
 template <int D, int NT, CachePart PART>
 __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) cache_decode_kernel(const CacheFwdParams p) {
     using T = DecodeTraits<D, NT>;
@@ -312,10 +301,16 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
     ShareSmem* ssm = reinterpret_cast<ShareSmem*>(stat + kWarps * T::ROWS);
 
     pdl_launch_dependents();
-    pdl_wait();
+    // The rest of the sequences does not need the launch before it, which is that of the prefixes:
+    // its CTAs begin as those of the prefixes end, and wait for all of them before they end.  (The
+    // launch of the prefixes let this one begin after everything before it was there; the fence drops
+    // what an SM may have cached from before that.)
+    if constexpr (PART == kRest) __threadfence();
+    else pdl_wait();
     const Share sh = p.B <= kFewSeqs ? find_share_few<PART>(p, blockIdx.x) : find_share<PART>(p, blockIdx.x, ssm);
     if (sh.b < 0) {  // more CTAs than shares
-        if (threadIdx.x == 0) p.border[blockIdx.x].c_first = -1;
+        if constexpr (PART == kRest) pdl_wait();
+        else if (threadIdx.x == 0) p.border[blockIdx.x].c_first = -1;
         return;
     }
     const long long x_begin = blockIdx.x * sh.share;
@@ -339,7 +334,11 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
         const int v1 = static_cast<int>(min(static_cast<long long>(s.n), v0 + (x_end - x)));
         const int hk = item / rts, rt = item - hk * rts;
         const int first_pos = s.len - s.q_len;  // may be negative: rows before the first token see nothing
-        if (x == x_begin && threadIdx.x == 0) {
+        if constexpr (PART == kRest) {
+            if (v0 == 0 && threadIdx.x == 0)
+                p.items[(static_cast<long long>(b) * p.Hk + hk) * most_row_tiles(p) + rt] = make_int2(
+                    static_cast<int>(blockIdx.x), static_cast<int>(div_mostly32(x + s.n - 1, sh.share)));
+        } else if (x == x_begin && threadIdx.x == 0) {
             CacheBorder bd;
             bd.b = b;
             bd.item = item;
@@ -781,21 +780,7 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                     acc[e + 3] += wgt[w] * y.w;
                 }
             }
-            if (finished) {
-                if constexpr (PART == kRest) {
-                    if (s.key_lo > 0) {
-                        const long long at = pre_row(p, b, a.t, a.h);
-                        const PreJoin j(p.pre_stat[at], mm, ll);
-#pragma unroll
-                        for (int e = 0; e < CPT; e += 4) {
-                            const float4 y = *reinterpret_cast<const float4*>(p.pre_o + at * D + c0 + e);
-                            acc[e] = j(acc[e], y.x);
-                            acc[e + 1] = j(acc[e + 1], y.y);
-                            acc[e + 2] = j(acc[e + 2], y.z);
-                            acc[e + 3] = j(acc[e + 3], y.w);
-                        }
-                    }
-                }
+            if (finished && PART != kRest) {
                 const float inv = ll != 0.f ? 1.f / ll : 0.f;  // NaN stays NaN
                 uint32_t pk[CPT / 2];
 #pragma unroll
@@ -808,15 +793,24 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
                         ll != 0.f ? (mm - kWeightShift + log2f(ll)) * kLn2 : INFINITY;
             } else {
                 float* dst = p.part + (static_cast<long long>(slot) * T::ROWS + r) * D + c0;
+                float2* st = p.stat + slot * T::ROWS + r;
+                if constexpr (PART == kRest) {
+                    if (finished) {
+                        const long long at = fin_row(p, b, a.t, a.h);
+                        dst = p.fin_o + at * D + c0;
+                        st = p.fin_stat + at;
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < CPT; e += 4)
                     *reinterpret_cast<float4*>(dst + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-                if (c0 == 0) p.stat[slot * T::ROWS + r] = make_float2(mm, ll);
+                if (c0 == 0) *st = make_float2(mm, ll);
             }
         }
         __syncthreads();  // shared memory is free for the next segment
         x += sh.whole > 0 ? sh.whole : v1 - v0;
     }
+    if constexpr (PART == kRest) pdl_wait();
 }
 
 // Joins an item's unfinished segments (of either cache attention kernel), in the
@@ -845,7 +839,7 @@ struct Joined {
     }
 };
 
-template <int D, CachePart PART>
+template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const CacheFwdParams p) {
     constexpr int E = D / 32;
     __shared__ float o_sm[kJoinWarps][D];
@@ -886,38 +880,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
         }
         return x;
     };
-    auto write = [&](int r, Joined<D> x) {
-        RowAt a = row_at(p, bd.q_len, hk, rt, r);
-        int b = bd.b;
-        if constexpr (PART == kPrefix) group_row(p, group_begin(p, bd.b), b, a.t);
-        if constexpr (PART != kWhole) {
-            const long long at = pre_row(p, b, a.t, a.h);
-            float* pre = p.pre_o + at * D + lane * E;
-            if constexpr (PART == kPrefix) {
-#pragma unroll
-                for (int e = 0; e < E; e += 2) *reinterpret_cast<float2*>(pre + e) = make_float2(x.o[e], x.o[e + 1]);
-                if (lane == 0) p.pre_stat[at] = make_float2(x.m, x.l);
-                return;
-            }
-            if (p.start[b] > 0) {
-                const float2 st = p.pre_stat[at];
-                float y[E];
-#pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(pre + e);
-                    y[e] = v.x;
-                    y[e + 1] = v.y;
-                }
-                x.add(st.x, st.y, y);
-            }
-        }
+    auto write = [&](int r, const Joined<D>& x) {
+        const RowAt a = row_at(p, bd.q_len, hk, rt, r);
         const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
-        uint16_t* dst = static_cast<uint16_t*>(p.o) + b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
+        uint16_t* dst = static_cast<uint16_t*>(p.o) + bd.b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
 #pragma unroll
         for (int e = 0; e < E; e += 2)
             *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(x.o[e] * inv, x.o[e + 1] * inv);
         if (lane == 0)
-            p.lse[(static_cast<long long>(b) * p.H + a.h) * p.T + a.t] =
+            p.lse[(static_cast<long long>(bd.b) * p.H + a.h) * p.T + a.t] =
                 x.l != 0.f ? (x.m - kWeightShift + log2f(x.l)) * kLn2 : INFINITY;
     };
     const int mine = (c - bd.c_first) * static_cast<int>(gridDim.y) + blockIdx.y, borders = (n - 1) * static_cast<int>(gridDim.y);
@@ -947,8 +918,86 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     }
 }
 
+// Puts the parts of a row together, of its group's prefix and of the rest, each in one or more
+// segments: a row a warp.  Bound by latency: what the lengths say is read while the launch before
+// it still runs, then where the segments are, then all statistics (a lane each) and outputs at once.
+struct CacheMergeParams {
+    CacheFwdParams prefix, rest;
+};
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_merge_kernel(const CacheMergeParams m) {
+    constexpr int E = D / 32, U = 8;
+    const int lane = threadIdx.x & 31;
+    const CacheFwdParams& p = m.rest;
+    const int G = p.H / p.Hk;
+    const long long row = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const bool in = row < static_cast<long long>(p.B) * p.T * p.H;
+    const long long bt = in ? div_mostly32(row, p.H) : 0;
+    const int h = in ? static_cast<int>(row - bt * p.H) : 0, b = static_cast<int>(div_mostly32(bt, p.T));
+    const int t = static_cast<int>(bt - static_cast<long long>(b) * p.T), hk = h / G;
+    __threadfence();  // (see the kernel for few queries)
+    const int queries = query_count(p, b), g = group_of(p, b), start = g < 0 ? 0 : group_len(p, g);
+    if (in && t == 0 && h == 0 && lane == 0 && g >= 0) {
+        // every new query stands behind its group's prefix, and that within the table
+        const int cap = p.c.max_pages * p.c.page_size;
+        if (static_cast<unsigned>(p.prefix_lens[g]) > static_cast<unsigned>(cap))
+            record_device_error(p.st, ATTN_DEVERR_PAGE, 0x306);
+        if (start > 0 && queries > 0 && min(max(p.c.seq_lens[b], 0), cap) - queries < start)
+            record_device_error(p.st, ATTN_DEVERR_PAGE, 0x305);
+    }
+    // row of its item, in either part
+    const int group_r = start > 0 ? ((b - group_begin(p, g)) * p.T + t) * G + h - hk * G : 0;
+    const int own_r = t * G + h - hk * G, own_tile = own_r / p.rows, group_tile_r = group_r / m.prefix.rows;
+    const int2* own_item = p.items + (static_cast<long long>(b) * p.Hk + hk) * most_row_tiles(p) + own_tile;
+    const int2* group_item = m.prefix.items + (start > 0 ? (group_tile(m.prefix, g) + group_tile_r) * p.Hk + hk : 0);
+    pdl_wait();
+    if (!in || t >= queries) return;
+    const int2 own = *own_item, shared = start > 0 ? *group_item : make_int2(0, -1);
+    const int n0 = shared.y - shared.x + 1, n = n0 + own.y - own.x + 1;  // segments: the prefix's, then the others
+    Joined<D> x;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        // lane: segment i0 + lane
+        const int i = i0 + lane;
+        const bool of_own = i >= n0;
+        const CacheFwdParams& part = of_own ? m.rest : m.prefix;
+        const int2 c = of_own ? own : shared;
+        const int k = of_own ? i - n0 : i, r = of_own ? own_r - own_tile * p.rows : group_r - group_tile_r * m.prefix.rows;
+        const bool whole = c.x == c.y;
+        const long long at = whole ? row : (2ll * (c.x + k) + (k == 0 ? 1 : 0)) * part.rows + r;
+        float2 st = make_float2(-INFINITY, 0.f);
+        unsigned long long src = 0;
+        if (i < n) {
+            st = (whole ? part.fin_stat : part.stat)[at];
+            src = reinterpret_cast<unsigned long long>((whole ? part.fin_o : part.part) + at * D);
+        }
+        const int here = min(32, n - i0);
+        for (int j0 = 0; j0 < here; j0 += U) {
+            float y[U][E];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, src, j0 + u)) + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {
+                    const float2 v = j0 + u < here ? *reinterpret_cast<const float2*>(from + e) : make_float2(0.f, 0.f);
+                    y[u][e] = v.x;
+                    y[u][e + 1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                x.add(__shfl_sync(0xffffffffu, st.x, j0 + u), __shfl_sync(0xffffffffu, st.y, j0 + u), y[u]);
+        }
+    }
+    const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
+    uint16_t* dst = static_cast<uint16_t*>(p.o) + b * p.os.b + h * p.os.h + t * p.os.n + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(x.o[e] * inv, x.o[e + 1] * inv);
+    if (lane == 0)
+        p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t] = x.l != 0.f ? (x.m - kWeightShift + log2f(x.l)) * kLn2 : INFINITY;
+}
+
 template <int D, int NT, CachePart PART>
-cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
+cudaError_t launch_decode_impl(CacheFwdParams& p, int sms, cudaStream_t stream) {
     using T = DecodeTraits<D, NT>;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t attr = once_per_device(ready, [] {
@@ -959,11 +1008,11 @@ cudaError_t launch_decode_impl(CacheFwdParams p, int sms, cudaStream_t stream) {
     p.grid = sms * T::CTAS_PER_SM < kCacheGridMax ? sms * T::CTAS_PER_SM : kCacheGridMax;
     const cudaError_t e = launch_dependent(cache_decode_kernel<D, NT, PART>, dim3(static_cast<unsigned>(p.grid)),
                                            kThreads, T::SMEM, stream, p);
-    return e != cudaSuccess ? e : launch_cache_join(p, 1, PART, stream);
+    return e != cudaSuccess || PART == kRest ? e : launch_cache_join(p, 1, stream);
 }
 
 template <int D, CachePart PART>
-cudaError_t launch_decode_d(const CacheFwdParams& p, cudaStream_t stream) {
+cudaError_t launch_decode_d(CacheFwdParams& p, cudaStream_t stream) {
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -973,26 +1022,29 @@ cudaError_t launch_decode_d(const CacheFwdParams& p, cudaStream_t stream) {
     return launch_decode_impl<D, 2, PART>(p, sms, stream);
 }
 
-template <int D>
-cudaError_t launch_join_d(const CacheFwdParams& p, dim3 grid, CachePart part, cudaStream_t stream) {
-    if (part == kPrefix) return launch_dependent(cache_join_kernel<D, kPrefix>, grid, 32 * kJoinWarps, 0, stream, p);
-    if (part == kRest) return launch_dependent(cache_join_kernel<D, kRest>, grid, 32 * kJoinWarps, 0, stream, p);
-    return launch_dependent(cache_join_kernel<D, kWhole>, grid, 32 * kJoinWarps, 0, stream, p);
-}
-
 }  // namespace
 
-cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, CachePart part, cudaStream_t stream) {
+cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream) {
     if (p.grid == 1) return cudaSuccess;  // no border
     const dim3 grid(static_cast<unsigned>(p.grid - 1), static_cast<unsigned>(blocks));
-    if (p.D == 64) return launch_join_d<64>(p, grid, part, stream);
-    if (p.D == 128) return launch_join_d<128>(p, grid, part, stream);
+    if (p.D == 64) return launch_dependent(cache_join_kernel<64>, grid, 32 * kJoinWarps, 0, stream, p);
+    if (p.D == 128) return launch_dependent(cache_join_kernel<128>, grid, 32 * kJoinWarps, 0, stream, p);
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_cache_decode(const CacheFwdParams& p, CachePart part, cudaStream_t stream) {
-    if (p.D == 64) return part == kRest ? launch_decode_d<64, kRest>(p, stream) : launch_decode_d<64, kWhole>(p, stream);
-    if (p.D == 128) return part == kRest ? launch_decode_d<128, kRest>(p, stream) : launch_decode_d<128, kWhole>(p, stream);
+cudaError_t launch_cache_merge(const CacheFwdParams& prefix, const CacheFwdParams& rest, cudaStream_t stream) {
+    const long long blocks = (static_cast<long long>(rest.B) * rest.T * rest.H + kJoinWarps - 1) / kJoinWarps;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    const dim3 grid(static_cast<unsigned>(blocks));
+    const CacheMergeParams m{prefix, rest};
+    if (rest.D == 64) return launch_dependent(cache_merge_kernel<64>, grid, 32 * kJoinWarps, 0, stream, m);
+    if (rest.D == 128) return launch_dependent(cache_merge_kernel<128>, grid, 32 * kJoinWarps, 0, stream, m);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_cache_decode(CacheFwdParams* p, CachePart part, cudaStream_t stream) {
+    if (p->D == 64) return part == kRest ? launch_decode_d<64, kRest>(*p, stream) : launch_decode_d<64, kWhole>(*p, stream);
+    if (p->D == 128) return part == kRest ? launch_decode_d<128, kRest>(*p, stream) : launch_decode_d<128, kWhole>(*p, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -46,6 +46,7 @@ constexpr float kWeightMax = 32768.f;
 constexpr int kPairRows = 2 * kTile;
 constexpr int kPromptThreads = 512;
 constexpr int kConvWarps = 4;
+constexpr int kAhead = 3;  // tiles
 // Registers a thread: the launch's 128 are dealt out again, more for the softmax, less
 // for the MMA issuer's four warps.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 152, kMmaRegs = 80, kConvRegs = 128;
@@ -141,10 +142,10 @@ __host__ __device__ inline PromptUnit prompt_unit(const CacheFwdParams& p, int b
 }
 
 // The same of a launch's part of the sequences.  A group's prefix: the rows of all its sequences
-// are one sequence's, all of them behind its last key.  The rest of a sequence: from the first
-// key that its group's part does not cover.
+// are one sequence's, all of them behind its last key.
 template <CachePart PART>
 __device__ __forceinline__ PromptUnit unit_of(const CacheFwdParams& p, int b, int pair) {
+    static_assert(PART != kRest, "the rest of a sequence is for the kernel of few queries");
     if constexpr (PART == kPrefix) {
         PromptUnit u;
         u.len = group_len(p, b);
@@ -157,17 +158,7 @@ __device__ __forceinline__ PromptUnit unit_of(const CacheFwdParams& p, int b, in
         u.n_sink = u.lo = u.key_lo = 0;
         return u;
     }
-    PromptUnit u = prompt_unit(p, b, pair);
-    if constexpr (PART == kRest) {
-        if (u.n > 0) {
-            u.key_lo = p.start[b];
-            u.lo = u.key_lo / kTile;
-            u.n0 = max(0, u.n0 - u.lo);
-            u.n1 = max(0, u.n1 - u.lo);
-            u.n = max(1, u.n1);
-        }
-    }
-    return u;
+    return prompt_unit(p, b, pair);
 }
 
 // Tiles [first, end) of a segment [v0, v1), tile t0 of its CTA the first, that lie among the
@@ -193,15 +184,14 @@ struct PromptShareSmem {
     int unit;
 };
 
-template <CachePart PART>
 __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptShareSmem* sm) {
     constexpr int W = kPromptThreads / 32;
-    const int units = (PART == kPrefix ? p.groups : p.B) * pairs, per = (units + kPromptThreads - 1) / kPromptThreads;
+    const int units = p.B * pairs, per = (units + kPromptThreads - 1) / kPromptThreads;
     const int u0 = min(units, static_cast<int>(threadIdx.x) * per), u1 = min(units, u0 + per);
-    auto work = [&](int u) { return static_cast<long long>(unit_of<PART>(p, u / pairs, u % pairs).n) * p.Hk; };
+    auto work = [&](int u) { return static_cast<long long>(prompt_unit(p, u / pairs, u % pairs).n) * p.Hk; };
     long long mine = 0;
     for (int u = u0; u < u1; ++u) {
-        if (PART != kPrefix && blockIdx.x == 0 && u % pairs == 0) check_len(p.c, p.st, u / pairs);
+        if (blockIdx.x == 0 && u % pairs == 0) check_len(p.c, p.st, u / pairs);
         mine += work(u);
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -237,6 +227,43 @@ __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptSh
     __syncthreads();
     s.unit = sm->unit;
     s.unit_first = sm->unit_first;
+    return s;
+}
+
+// The same for the prefixes' launch, by each warp for itself, without a barrier.
+__device__ __forceinline__ PromptShare prefix_share(const CacheFwdParams& p, int pairs) {
+    const int lane = threadIdx.x & 31, units = p.groups * pairs, per = (units + 31) >> 5;
+    const int u0 = min(units, lane * per), u1 = min(units, u0 + per);
+    auto work = [&](int u) { return static_cast<long long>(unit_of<kPrefix>(p, u / pairs, u % pairs).n) * p.Hk; };
+    long long mine = 0;
+    for (int u = u0; u < u1; ++u) mine += work(u);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+    }
+    const long long total = __shfl_sync(0xffffffffu, incl, 31);
+    PromptShare s;
+    s.share = max(div_mostly32(total + p.grid - 1, p.grid), 1ll);
+    s.x = blockIdx.x * s.share;
+    s.x_end = min(s.x + s.share, total);
+    long long before = incl - mine;
+    int found = -1;
+    if (s.x < total && before <= s.x && s.x < incl) {
+        for (int u = u0; u < u1; ++u) {
+            const long long w = work(u);
+            if (s.x < before + w) {
+                found = u;
+                break;
+            }
+            before += w;
+        }
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, found >= 0);
+    const int src = who ? __ffs(who) - 1 : 0;
+    s.unit = __shfl_sync(0xffffffffu, found, src);
+    s.unit_first = __shfl_sync(0xffffffffu, before, src);
     return s;
 }
 
@@ -333,7 +360,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
     static_assert(sizeof(PromptWalk) <= 128 && sizeof(PromptShareSmem) <= 256, "walk slots");
     PromptWalk* const walk = reinterpret_cast<PromptWalk*>(smem + T::OFF_WALK + (warp < 10 ? warp : warp - 2) * 128);
     {
-        const PromptShare share = prompt_share<PART>(p, pairs, reinterpret_cast<PromptShareSmem*>(smem + T::OFF_WALK));
+        PromptShare share;
+        if constexpr (PART == kPrefix) share = prefix_share(p, pairs);
+        else share = prompt_share(p, pairs, reinterpret_cast<PromptShareSmem*>(smem + T::OFF_WALK));
         __syncthreads();  // the scratch has been read
         if (lane == 0 && (warp < 10 || warp >= 12)) {
             walk->s = share;
@@ -370,13 +399,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             const int len = w.u.len, key_lo = w.u.key_lo;
             // Sequence whose table is read: of a group the first one that has queries (a slot of a
             // batch that has none may hold any table; a group without queries reads page 0, to no end).
-            int seq = w.b;
-            if constexpr (PART == kPrefix) {
-                const int end = group_end(p, w.b);
-                seq = group_begin(p, w.b);
-                while (seq < end && query_count(p, seq) == 0) ++seq;
-                if (seq == end) seq = -1;
-            }
+            int seq = PART == kPrefix ? group_begin(p, w.b) : w.b;
             auto first_tok = [&](int t) { return w.u.tile(t) * kTile + cw * 32; };
             // some query sees a token of the group from tok on
             auto needed = [&](int tok) { return tok < len && (tok + 16 > key_lo || tok < p.sinks); };
@@ -385,7 +408,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             // each look at the table goes to the L2).
             auto fetch = [&](int t) {
                 const int x = t + (lane >> 1), tok = x < w.v1 ? first_tok(x) + 16 * (lane & 1) : len;
-                return needed(tok) && seq >= 0 ? __ldg(p.c.table + seq * p.c.table_stride + (tok >> p.c.page_shift)) : 0;
+                return needed(tok) && (PART != kPrefix || seq >= 0) ? __ldg(p.c.table + seq * p.c.table_stride + (tok >> p.c.page_shift)) : 0;
             };
             auto checked = [&](int pid) {
                 if (static_cast<unsigned>(pid) < static_cast<unsigned>(p.c.num_pages)) return pid;
@@ -484,7 +507,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             // Loads run ahead of their use: V of the tile before K is converted, K of the next
             // one before V is.
             uint4 kb[2 * NI], vb[2 * NI];
-            int pages = checked(fetch(w.v0)), pages_next = fetch(w.v0 + 16), pid[2];
+            int pages = fetch(w.v0), pages_next = fetch(w.v0 + 16), pid[2];
+            if constexpr (PART == kPrefix) {
+                if (query_count(p, seq) == 0) {
+                    const int end = group_end(p, w.b);
+                    do ++seq;
+                    while (seq < end && query_count(p, seq) == 0);
+                    if (seq == end) seq = -1;
+                    pages = fetch(w.v0);
+                    pages_next = fetch(w.v0 + 16);
+                }
+            }
+            pages = checked(pages);
             auto take_pages = [&](int i) {  // of the segment's i-th tile
                 if (i > 0 && (i & 15) == 0) {
                     pages = checked(pages_next);
@@ -494,6 +528,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 pid[1] = __shfl_sync(0xffffffffu, pages, 2 * (i & 15) + 1);
             };
             const int tiles = w.v1 - w.v0;
+            // A prefix's keys are read once, by this CTA: they are called into the L2 kAhead tiles before
+            // their use.  The loads themselves are a half tile ahead, which covers the L2's latency and
+            // not the memory's (32 sequences behind 131072 tokens: 105 us for 115).
+            auto call_in = [&](int i) {  // lane: one of the warp's 32 tokens of the segment's i-th tile
+                if (i >= tiles) return;
+                const int from = (i & ~15) == ((i - kAhead > 0 ? i - kAhead : 0) & ~15) ? pages : pages_next;
+                const int pg = __shfl_sync(0xffffffffu, from, 2 * (i & 15) + (lane >> 4)), tok = first_tok(w.v0 + i) + lane;
+                if (static_cast<unsigned>(pg) >= static_cast<unsigned>(p.c.num_pages)) return;
+                const long long slot = tok & (p.c.page_size - 1);
+                prefetch_l2(p.c.k_pages + pg * p.c.ks.b + w.hk * p.c.ks.h + slot * p.c.ks.n);
+                prefetch_l2(p.c.v_pages + pg * p.c.vs.b + w.hk * p.c.vs.h + slot * p.c.vs.n);
+            };
+            if constexpr (PART == kPrefix) {
+                for (int i = 1; i <= kAhead; ++i) call_in(i);
+            }
             int tok0 = first_tok(w.v0);
             if (tiles > 0) {
                 take_pages(0);
@@ -502,6 +551,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             }
             for (int i = 0; i < tiles; ++i) {
                 load(vb, vbase, p.c.vs, tok0, pid);
+                if constexpr (PART == kPrefix) {
+                    if (i > 0) call_in(i + kAhead);
+                }
                 if (!(ok = claim())) break;
                 // the scales' entry of the tile is free now as well (see the softmax)
                 if (lane < 2) {
@@ -616,7 +668,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     release(ring + 2 * g);
                 }
             for (int j = 0; j < a0; ++j)
-#pragma unroll
+#pragma unroll 1
                 for (int g = 0; g < 2; ++g) {
                     const int a = g ? a1 : a0, vi = ring + 4 * j + 2 * g + 1;
                     if (j >= a) continue;
@@ -643,6 +695,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         }
         mma_commit_warp(b_done);  // every product has finished before tensor memory is freed
         wait_drain_loop(b_done, 0, p.st.word, p.st.wait_limit_ns, SITE_DRAIN);
+        } else if (PART == kPrefix && warp == 9) {  // where the merge finds the items that begin here
+            while (next_segment<PART>(p, walk))
+                if (w.v0 == 0 && lane == 0) {
+                    const long long x = w.s.x - (w.v1 - w.v0);
+                    p.items[(group_tile(p, w.b) + w.pair) * p.Hk + w.hk] =
+                        make_int2(static_cast<int>(blockIdx.x), static_cast<int>(div_mostly32(x + w.u.n - 1, w.s.share)));
+                }
         } else if (warp == 9) {  // what the joining kernel finds at the border before this share
             CacheBorder bd;
             bd.c_first = -1;
@@ -656,23 +715,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 bd.c_last = static_cast<int>(div_mostly32(x - w.v0 + w.u.n - 1, w.s.share));
             }
             if (lane == 0) p.border[blockIdx.x] = bd;
-        } else if (PART == kPrefix && warp == 10) {  // what the launch for the rest finds
-            const int cap = p.c.max_pages * p.c.page_size;
-            for (int b = static_cast<int>(blockIdx.x) * 32 + lane; b < p.B; b += p.grid * 32) {
-                int lo = 0, hi = p.groups;  // the group: the last one that begins at b or before
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) / 2;
-                    (group_begin(p, mid) <= b ? lo : hi) = mid;
-                }
-                const int start = group_begin(p, lo) <= b && b < group_end(p, lo) ? group_len(p, lo) : 0;
-                p.start[b] = start;
-                // every new query stands behind its group's prefix
-                if (start > 0 && query_count(p, b) > 0 && min(max(p.c.seq_lens[b], 0), cap) - query_count(p, b) < start)
-                    record_device_error(p.st, ATTN_DEVERR_PAGE, 0x305);
-            }
-            for (int g = static_cast<int>(blockIdx.x) * 32 + lane; g < p.groups; g += p.grid * 32)
-                if (static_cast<unsigned>(p.prefix_lens[g]) > static_cast<unsigned>(cap))
-                    record_device_error(p.st, ATTN_DEVERR_PAGE, 0x306);
         }
     } else {
         regs_inc<kSoftmaxRegs>();
@@ -682,7 +724,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         const uint32_t tS = tmem + (g ? T::COL_S1 : T::COL_S0) + lane_off;
         const uint32_t tO = tmem + (g ? T::COL_O1 : T::COL_O0) + lane_off;
         const uint32_t b_sf = b_s_full + 8u * g, b_pf = b_p_full + 8u * g, b_of = b_o_full + 8u * g;
-        uint8_t* q_row = smem + g * T::TILE_BYTES + row * 128;
         int s_seen = 0, o_seen = 0, tile_no = 0, merges = 0;
         bool ok = true;
         while (ok && next_segment<PART>(p, walk)) {
@@ -695,33 +736,62 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             // rows behind the last query (zeros, never written) take its place: no mask of their own
             const int pos = w.u.first_pos + (PART == kPrefix ? 0 : row_ok ? t : w.u.q_len - 1);
             if constexpr (PART == kPrefix) {
-                if (row_ok) group_row(p, group_begin(p, w.b), member, t);
+                if (row_ok) {
+                    const int m = t / p.T;
+                    member = group_begin(p, w.b) + m;
+                    t -= m * p.T;
+                }
                 row_ok = row_ok && t < query_count(p, member);
             }
             auto seq = [&] { return PART == kPrefix ? member : w.b; };
             const int key_min = p.left < 0 ? 0 : pos - p.left;
             float rq = 0.f;
             if (n > 0) {
-                // Q row to f16, times a power of two.  The tile's place is free: the
+                // Q rows to f16, times a power of two each.  The tile's place is free: the
                 // previous segment's last S_g, read here, came after every product on it.
-                uint4 x[D / 8];
-                float amax = 0.f;
-                const uint16_t* src = static_cast<const uint16_t*>(p.q) + seq() * p.qs.b + h * p.qs.h + t * p.qs.n;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    x[c] = row_ok ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    for (uint32_t u : {x[c].x, x[c].y, x[c].z, x[c].w})
-                        amax = fmaxf(amax, fmaxf(fabsf(bf16lo(u)), fabsf(bf16hi(u))));
-                const float f = f16_row_scale(amax);
-                rq = p.cs * __uint_as_float((254u << 23) - __float_as_uint(f));
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    auto cv = [&](uint32_t u) { return pack_f16x2(bf16lo(u) * f, bf16hi(u) * f); };
-                    *reinterpret_cast<uint4*>(q_row + (c >> 3) * T::BLK_BYTES + (((c & 7) ^ (row & 7)) << 4)) =
-                        make_uint4(cv(x[c].x), cv(x[c].y), cv(x[c].z), cv(x[c].w));
+                // A row takes D / 8 lanes, the same for the copy and for the conversion in place: all of
+                // the copies are out at once (Q comes after the first keys' loads: 1600 to 3000 cycles),
+                // and the code is short (what runs once a segment runs at the pace at which its
+                // instructions come from the L2).
+                constexpr int LPR = D / 8, RPI = 32 / LPR;
+                const unsigned there = __ballot_sync(0xffffffffu, row_ok);
+                const unsigned long long src = reinterpret_cast<unsigned long long>(
+                    static_cast<const uint16_t*>(p.q) + seq() * p.qs.b + h * p.qs.h + t * p.qs.n);
+                const int sub = lane / LPR, c = lane % LPR;
+                uint8_t* const q_at = smem + g * T::TILE_BYTES + (c >> 3) * T::BLK_BYTES + wq * 32 * 128;
+                auto place = [&](int rr) { return q_at + rr * 128 + (((c & 7) ^ (rr & 7)) << 4); };
+#pragma unroll 4
+                for (int i = 0; i < 32 / RPI; ++i) {
+                    const int rr = i * RPI + sub;
+                    const bool have = there >> rr & 1u;
+                    const unsigned long long at = __shfl_sync(0xffffffffu, src, rr);
+                    cp_async16(smem_u32(place(rr)), have ? reinterpret_cast<const uint4*>(at) + c : p.q, have);
                 }
+                cp_async_commit();
+                cp_async_wait<0>();
+                float f_row = 0.f;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32 / RPI; i0 += 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4*>(place((i0 + k) * RPI + sub));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float amax = 0.f;
+                        for (uint32_t u : {x[k].x, x[k].y, x[k].z, x[k].w})
+                            amax = fmaxf(amax, fmaxf(fabsf(bf16lo(u)), fabsf(bf16hi(u))));
+#pragma unroll
+                        for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        const float f = f16_row_scale(amax);
+                        auto cv = [&](uint32_t u) { return pack_f16x2(bf16lo(u) * f, bf16hi(u) * f); };
+                        x[k] = make_uint4(cv(x[k].x), cv(x[k].y), cv(x[k].z), cv(x[k].w));
+                        const float of_row = __shfl_sync(0xffffffffu, f, lane % RPI * LPR);
+                        if (lane / RPI == i0 + k) f_row = of_row;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(place((i0 + k) * RPI + sub)) = x[k];
+                }
+                rq = p.cs * __uint_as_float((254u << 23) - __float_as_uint(f_row));
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(b_q + 8u * g);
@@ -1022,28 +1092,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 f1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - m_used);
                 l_sum = l_sum * f0 + l1 * f1;
             }
-            const float* pre = nullptr;  // the row's part of its group's prefix, times fp
-            float fp = 0.f;
-            if constexpr (PART == kRest) {
-                if (finished && row_ok && w.u.key_lo > 0) {
-                    const long long at = pre_row(p, seq(), t, h);
-                    const float2 st = p.pre_stat[at];
-                    pre = p.pre_o + at * D;
-                    const float m0 = l_sum != 0.f ? m_used : -INFINITY, m = fmaxf(m0, st.x);
-                    const float f = m0 == -INFINITY ? 0.f : ex2_approx(m0 - m);
-                    fp = st.x == -INFINITY ? 0.f : ex2_approx(st.x - m);
-                    l_sum = l_sum * f + st.y * fp;
-                    f0 *= f;
-                    f1 *= f;
-                    m_used = m;
-                }
-            }
             // without a live key tile: O = 0 and LSE = +inf, or a segment that takes no part
-            const float inv = (n > 0 || pre) && l_sum != 0.f ? 1.f / l_sum : 0.f;  // NaN stays NaN
+            const float inv = n > 0 && l_sum != 0.f ? 1.f / l_sum : 0.f;  // NaN stays NaN
             const long long part_row =
                 (2ll * blockIdx.x + (w.v0 == 0 ? 1 : 0)) * kPairRows + (dual ? 0 : g * kTile) + row;
             uint16_t* orow = static_cast<uint16_t*>(p.o) + w.b * p.os.b + h * p.os.h + t * p.os.n;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 if (n > 0) {
@@ -1059,35 +1113,27 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     tmem_ld_wait(o1);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * f0 + u2f(o1[i]) * f1);
-                } else if (PART == kRest && pre) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * f0);
                 }
                 if (!row_ok) continue;
-                if (PART == kRest && pre) {
-#pragma unroll
-                    for (int v = 0; v < 8; ++v) {
-                        const float4 y = *reinterpret_cast<const float4*>(pre + 32 * c + 4 * v);
-                        o[4 * v] = f2u(fmaf(y.x, fp, u2f(o[4 * v])));
-                        o[4 * v + 1] = f2u(fmaf(y.y, fp, u2f(o[4 * v + 1])));
-                        o[4 * v + 2] = f2u(fmaf(y.z, fp, u2f(o[4 * v + 2])));
-                        o[4 * v + 3] = f2u(fmaf(y.w, fp, u2f(o[4 * v + 3])));
-                    }
-                }
-                if (finished && PART != kPrefix) {
+                if (finished && PART == kWhole) {
                     uint32_t pkd[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) pkd[i] = pack_bf16x2(u2f(o[2 * i]) * inv, u2f(o[2 * i + 1]) * inv);
                     st_global_row64<false>(reinterpret_cast<uint8_t*>(orow + 32 * c), pkd);
                 } else {
-                    float* dst = (PART == kPrefix && finished ? p.pre_o + pre_row(p, seq(), t, h) * D : p.part + part_row * D) + 32 * c;
+                    float* dst = (PART == kPrefix && finished ? p.fin_o + fin_row(p, seq(), t, h) * D : p.part + part_row * D) + 32 * c;
+                    if constexpr (PART == kWhole) {
 #pragma unroll
-                    for (int v = 0; v < 8; ++v) st_global_v4(dst + 4 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                        for (int v = 0; v < 8; ++v) st_global_v4(dst + 4 * v, o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) st_global_v8(dst + 8 * v, o + 8 * v);
+                    }
                 }
             }
             if (row_ok) {
                 if (PART == kPrefix && finished)
-                    p.pre_stat[pre_row(p, seq(), t, h)] = make_float2(l_sum != 0.f ? m_used : -INFINITY, l_sum);
+                    p.fin_stat[fin_row(p, seq(), t, h)] = make_float2(l_sum != 0.f ? m_used : -INFINITY, l_sum);
                 else if (finished)
                     p.lse[(static_cast<long long>(w.b) * p.H + h) * p.T + t] =
                         l_sum != 0.f ? (m_used - kWeightShift + log2f(l_sum)) * kLn2 : INFINITY;
@@ -1113,7 +1159,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
 }
 
 template <int D, CachePart PART>
-cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
+cudaError_t launch_prompt_impl(CacheFwdParams& p, cudaStream_t stream) {
     using T = PromptTraits<D>;
     static std::atomic<unsigned long long> ready{0};
     const cudaError_t attr = once_per_device(ready, [] {
@@ -1137,16 +1183,15 @@ cudaError_t launch_prompt_impl(CacheFwdParams p, cudaStream_t stream) {
     if ((e = dbg_set_word(p.st.word, stream)) != cudaSuccess) return e;
     e = launch_dependent(cache_prompt_kernel<D, PART>, dim3(static_cast<unsigned>(p.grid)), kPromptThreads, T::SMEM_BYTES,
                          stream, p, pairs);
-    return e != cudaSuccess ? e : launch_cache_join(p, 8, PART, stream);
+    return e != cudaSuccess || PART == kPrefix ? e : launch_cache_join(p, 8, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_prompt(const CacheFwdParams& p, CachePart part, cudaStream_t stream) {
-    if (p.D != 64 && p.D != 128) return cudaErrorInvalidValue;
-    if (part == kPrefix) return p.D == 64 ? launch_prompt_impl<64, kPrefix>(p, stream) : launch_prompt_impl<128, kPrefix>(p, stream);
-    if (part == kRest) return p.D == 64 ? launch_prompt_impl<64, kRest>(p, stream) : launch_prompt_impl<128, kRest>(p, stream);
-    return p.D == 64 ? launch_prompt_impl<64, kWhole>(p, stream) : launch_prompt_impl<128, kWhole>(p, stream);
+cudaError_t launch_cache_prompt(CacheFwdParams* p, CachePart part, cudaStream_t stream) {
+    if (p->D == 64) return part == kPrefix ? launch_prompt_impl<64, kPrefix>(*p, stream) : launch_prompt_impl<64, kWhole>(*p, stream);
+    if (p->D == 128) return part == kPrefix ? launch_prompt_impl<128, kPrefix>(*p, stream) : launch_prompt_impl<128, kWhole>(*p, stream);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace attn

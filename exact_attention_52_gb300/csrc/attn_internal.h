@@ -219,9 +219,10 @@ constexpr int kPromptRows = 256;
 // tensor cores' kernel for prompts.
 constexpr int kPromptMinRows = 64;
 
-// What a launch of the cache attention's kernels does: whole sequences; the groups' prefixes, the
-// rows of all sequences of a group as those of one; or, after that, the rest of each sequence,
-// joined with its group's part.
+// What a launch of the cache attention's kernels does: whole sequences; or the groups' prefixes, the
+// rows of all sequences of a group as those of one (the kernel for prompts); or the rest of each
+// sequence (the kernel for few queries).  The latter two leave every row's part in the workspace, for
+// the kernel that merges them.
 enum CachePart { kWhole = 0, kPrefix = 1, kRest = 2 };
 
 struct CacheFwdParams {
@@ -234,15 +235,12 @@ struct CacheFwdParams {
     int B, H, Hk, T, D;
     float cs;  // scale * log2(e)
     int left, sinks;
-    // Groups of sequences with a shared prefix (CachePart): group g is sequences group_first[g] ..
+    // Groups of sequences with a shared prefix: group g is sequences group_first[g] ..
     // group_first[g + 1] - 1 (null: one group of all), which share the pages of their first
     // prefix_lens[g] tokens.
     const int* group_first;
     const int* prefix_lens;
     int groups;
-    int* start;        // workspace: [B] tokens of a sequence that its group's part covers
-    float* pre_o;      // workspace: that part of each row, as an unfinished segment: fp32 [B, T, H, D]
-    float2* pre_stat;  // [B, T, H]
     // Set by the launcher:
     int rows;      // query rows of a tile
     int grid;      // CTAs that share the work, at most kCacheGridMax
@@ -250,6 +248,10 @@ struct CacheFwdParams {
     float* part;   // unfinished segments: fp32 [2 * grid][rows][D]
     float2* stat;  // their maximum (log2 units) and sum: [2 * grid][rows]
     CacheBorder* border;  // [grid]
+    // kPrefix and kRest: where the merge finds the parts
+    int2* items;      // first and last CTA of each item
+    float* fin_o;     // rows of items that one CTA did, as unfinished segments: fp32 [B, T, H, D]
+    float2* fin_stat;  // [B, T, H]
     DevStatus st;
 };
 
@@ -305,9 +307,11 @@ cudaError_t launch_cache_append(const CacheAppendParams& p, cudaStream_t stream)
 cudaError_t launch_cache_append_rope(const CacheAppendRopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_rope_norm_bwd(const RopeBwdParams& p, cudaStream_t stream);
-cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, CachePart part, cudaStream_t stream);
-cudaError_t launch_cache_prompt(const CacheFwdParams& p, CachePart part, cudaStream_t stream);
-cudaError_t launch_cache_decode(const CacheFwdParams& p, CachePart part, cudaStream_t stream);
+cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t stream);
+// (The launch of a part sets its parameters' rows, which the merge needs.)
+cudaError_t launch_cache_prompt(CacheFwdParams* p, CachePart part, cudaStream_t stream);
+cudaError_t launch_cache_decode(CacheFwdParams* p, CachePart part, cudaStream_t stream);
+cudaError_t launch_cache_merge(const CacheFwdParams& prefix, const CacheFwdParams& rest, cudaStream_t stream);
 cudaError_t launch_wait_selftest(DevStatus st, cudaStream_t stream);
 
 // Problem check shared by the entry points (sizes, head dim, scale, causal

@@ -63,19 +63,6 @@ __device__ __forceinline__ CacheSeq cache_seq(const CacheView& c, const int* q_l
     return s;
 }
 
-// The same of a launch's part of the sequences: the rest starts with the first key that the
-// group's part does not cover, a multiple of kTile.
-template <int TB, CachePart PART>
-__device__ __forceinline__ CacheSeq cache_seq_of(const CacheFwdParams& p, int b) {
-    CacheSeq s = cache_seq<TB>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
-    if constexpr (PART == kRest) {
-        s.key_lo = p.start[b];
-        s.lo = s.key_lo / TB;
-        s.n = max(1, (s.len - 1) / TB - s.lo + 1);
-    }
-    return s;
-}
-
 // Tokens that the part of group g covers: whole tiles of kTile, so that no tile is divided
 // between the parts (the tokens behind them are read for each sequence).
 __device__ __forceinline__ int group_len(const CacheFwdParams& p, int g) {
@@ -87,18 +74,42 @@ __device__ __forceinline__ int group_begin(const CacheFwdParams& p, int g) {
 __device__ __forceinline__ int group_end(const CacheFwdParams& p, int g) {
     return p.group_first ? min(max(p.group_first[g + 1], 0), p.B) : p.B;
 }
-// Row (virtual query, head of the group) of a group's part: its sequence and query.
-__device__ __forceinline__ void group_row(const CacheFwdParams& p, int first, int& b, int& t) {
-    const int member = t / p.T;
-    b = first + member;
-    t -= member * p.T;
+// Group of a sequence, the last one that begins at it or before; -1: none.
+__device__ __forceinline__ int group_of(const CacheFwdParams& p, int b) {
+    int lo = 0, hi = p.groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        (group_begin(p, mid) <= b ? lo : hi) = mid;
+    }
+    return group_begin(p, lo) <= b && b < group_end(p, lo) ? lo : -1;
+}
+__device__ __forceinline__ int group_start(const CacheFwdParams& p, int b) {
+    const int g = group_of(p, b);
+    return g < 0 ? 0 : group_len(p, g);
+}
+// Number of a group's first tile of p.rows rows, in which those of several groups do not meet.
+__device__ __forceinline__ long long group_tile(const CacheFwdParams& p, int g) {
+    return static_cast<long long>(group_begin(p, g)) * p.T * (p.H / p.Hk) / p.rows + g;
 }
 __device__ __forceinline__ int query_count(const CacheFwdParams& p, int b) {
     return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
 }
-// Place of a row in pre_o and pre_stat.
-__device__ __forceinline__ long long pre_row(const CacheFwdParams& p, int b, int t, int h) {
+// Place of a row in fin_o and fin_stat.
+__device__ __forceinline__ long long fin_row(const CacheFwdParams& p, int b, int t, int h) {
     return (static_cast<long long>(b) * p.T + t) * p.H + h;
+}
+
+// cache_seq of a launch's part of the sequences: the rest starts with the first key that the
+// group's part does not cover, a multiple of kTile.
+template <int TB, CachePart PART>
+__device__ __forceinline__ CacheSeq cache_seq_of(const CacheFwdParams& p, int b) {
+    CacheSeq s = cache_seq<TB>(p.c, p.q_lens, p.T, p.left, p.sinks, b);
+    if constexpr (PART == kRest) {
+        s.key_lo = group_start(p, b);
+        s.lo = s.key_lo / TB;
+        s.n = max(1, (s.len - 1) / TB - s.lo + 1);
+    }
+    return s;
 }
 
 // Records a length that leaves the table (the kernels read as if it ended with it).
@@ -129,6 +140,7 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool t
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {

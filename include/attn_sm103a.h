@@ -474,10 +474,12 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
  *   groups   : 1 .. B.
  *   workspace : attn_fwd_cache_prefix_workspace_bytes() bytes, 256-byte aligned, overwritten;
  *              calls that may overlap need one each.
- * Every query stands behind its group's prefix: a sequence with queries whose seq_lens[b] -
- * q_lens[b] is smaller (but for the last prefix_lens % 128 tokens), or a prefix length outside
- * the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE, and its rows are
- * undefined.  Two launches (and their joins).  Otherwise as attn_fwd_cache, with its errors.
+ * Every query has to stand behind its group's prefix.  A sequence with queries whose seq_lens[b] -
+ * q_lens[b] is smaller (but for the last prefix_lens % 128 tokens) has undefined rows, and it, or a
+ * prefix length outside the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE.
+ * Where sharing does not pay -- prompts (T * H / Hk above 64), and caches of which the table can
+ * hold less than 256 MB -- the call is attn_fwd_cache: it does not look at groups and prefixes,
+ * and those errors do not occur.  Otherwise three launches.  Errors as attn_fwd_cache.
  * Source: ai.engineer item 59 (small-query work split across thread blocks plus a separate
  * combining kernel); no page describes shared prefixes.
  */

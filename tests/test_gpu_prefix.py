@@ -1,6 +1,9 @@
 """attn_fwd_cache_prefix against the fp64 oracle of the cache attention, which knows nothing of
 shared pages.  Tolerances are those of the cache attention (test_gpu_cache): joining the two parts
-adds a few fp32 roundings, 2^-22 of the sums, to the 2^-15 that scores and exponentials have."""
+adds a few fp32 roundings, 2^-22 of the sums, to the 2^-15 that scores and exponentials have.
+
+A call works in two parts where the table can hold 256 MB; here tables are as wide as that needs,
+the entries behind the sequences' own holding no page, or as narrow as the sequences are."""
 
 import numpy as np
 import pytest
@@ -24,14 +27,28 @@ def shared_pool(seed, B, Hk, d, page, firsts, prefixes, lens, token_major=False)
     return pool
 
 
-def run(pool, H, T, firsts, prefixes, lens, q_lens, layout="bhnd", amp=1.0, table=None, **kw):
+def wide(table, pool):
+    """`table` with entries behind, so many that it can hold 256 MB."""
+    cols = -(-(1 << 28) // (2 * pool.d * pool.Hk * pool.B * pool.page))
+    out = np.full((pool.B, max(cols, table.shape[1])), 10 ** 6, dtype=np.int32)
+    out[:, :table.shape[1]] = table
+    return out
+
+
+def run(*args, **kw):
+    run_with(*args, **kw)
+    run_with(*args, widen=True, **kw)
+
+
+def run_with(pool, H, T, firsts, prefixes, lens, q_lens, layout="bhnd", amp=1.0, table=None, widen=False, **kw):
     import torch
     q, qv = bf16(pool.rng, (pool.B, H, T, pool.d), layout, amp)
     o = torch.full_like(q, 7.0)
     lse = torch.full((pool.B, H, T), 7.0, device="cuda")
     dev = pool.dev()
-    if table is not None:
-        dev[4] = i32(table)
+    if widen or table is not None:
+        table = pool.table if table is None else table
+        dev[4] = i32(wide(table, pool) if widen else table)
     args = (q, *dev, i32(lens), i32(prefixes))
     kw.update(group_first=None if firsts is None else i32(firsts), q_lens=None if q_lens is None else i32(q_lens), layout=layout)
     api.fwd_cache_prefix(*args, o=o, lse=lse, **kw)
@@ -62,7 +79,9 @@ SHAPES = [
     (6, 4, 2, 2, 16, [1, 3, 4], [128, 384], [50, 130, 140, 500, 2, 3], [2, 2, 2, 2, 2, 2]),  # sequences of no group
     (9, 40, 2, 1, 1024, [0, 9], [2048], [2048 + 3 * i + 1 for i in range(9)], None),
     (40, 32, 4, 1, 64, [0, 40], [640], [641 + 7 * i for i in range(40)], None),               # more than one pair of query tiles
-    (3, 8, 2, 40, 32, [0, 3], [256], [256 + 40, 700, 300], [40, 33, 1]),                      # prompts behind a prefix
+    (3, 8, 2, 16, 32, [0, 3], [256], [256 + 16, 700, 300], [16, 13, 1]),                      # as many rows as the part kernels take
+    (2, 5, 1, 12, 16, [0, 2], [1024], [1036, 1999], None),
+    (3, 8, 2, 40, 32, [0, 3], [256], [256 + 40, 700, 300], [40, 33, 1]),                      # prompts behind a prefix: one part
     (4, 5, 1, 100, 64, [0, 2, 4], [900, 256], [1000, 1300, 356, 999], [100, 0, 100, 71]),
 ]
 
@@ -76,7 +95,7 @@ def test_prefix_matches_oracle(shape, layout, d):
     run(pool, H, T, firsts, prefixes, lens, ql, layout)
 
 
-@pytest.mark.parametrize("T", [1, 30])
+@pytest.mark.parametrize("T", [1, 14, 30])
 def test_one_group_by_default_and_a_scale(T):
     pool = shared_pool(3, 4, 2, 128, 32, [0, 4], [384], [500, 600, 414, 900])
     run(pool, 8, T, None, [384], [500, 600, 414, 900], None, scale=0.3, amp=2.0)
@@ -88,7 +107,7 @@ def test_long_prefix():
     run(pool, 8, 1, [0, 6], [19999], lens, None)
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 15, 40])
 def test_a_slot_without_queries_may_hold_any_table(T):
     """The first sequence of a group that has queries stands for it; tables of the others are not read."""
     lens, ql = [0, 500, 700, 0], [0, T, T, 0]
@@ -106,7 +125,7 @@ def test_a_group_without_queries():
     run(pool, 4, 1, [0, 2, 3], [128, 256], lens, ql, table=junk)
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 15, 40])
 @pytest.mark.parametrize("where", ["prefix", "rest", "both"])
 def test_value_scales_far_apart(where, T):
     """Parts whose sums are taken apart join with parts whose sums are not."""
@@ -119,7 +138,7 @@ def test_value_scales_far_apart(where, T):
     run(pool, 4, T, [0, 3], [256], lens, None)
 
 
-@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("T", [1, 15, 40])
 def test_nan_values_reach_the_rows_that_see_them(T):
     lens = [300, 400]
     for pg, col in ((1, 3), (None, 5)):  # in the prefix; behind the second sequence's last token
@@ -136,18 +155,25 @@ def test_lengths_that_do_not_fit_are_reported():
     import torch
     pool = shared_pool(10, 3, 2, 64, 16, [0, 3], [256], [300, 300, 300])
     q = torch.randn(3, 4, 2, 64, device="cuda").bfloat16()
-    dev = pool.dev()
-    ok = lambda **kw: api.fwd_cache_prefix(q, *dev, i32(kw.get("lens", [300, 290, 280])), i32([kw.get("prefix", 256)]))
-    ok()
+    dev, narrow = pool.dev(), pool.dev()
+    dev[4] = i32(wide(pool.table, pool))
+    call = lambda dev, lens=(300, 290, 280), prefix=256: api.fwd_cache_prefix(q, *dev, i32(lens), i32([prefix]))
+    call(dev)
     check_clean()
-    for kw in (dict(lens=[300, 257, 280]), dict(lens=[300, 0, 280]), dict(lens=[300, -7, 280]), dict(lens=[300, 100000, 280]),
-               dict(prefix=100000), dict(prefix=-1)):
-        ok(**kw)
+    for lens in ([300, 257, 280], [300, 0, 280]):
+        call(dev, lens)
+        assert api.check_device_error()[0] == -5
+        # in one part the prefix says nothing
+        got, ref = call(narrow, lens), api.fwd_cache(q, *narrow, i32(lens))
+        check_clean()
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    for kw in (dict(lens=[300, -7, 280]), dict(lens=[300, 2 ** 30, 280]), dict(prefix=2 ** 30), dict(prefix=-1)):
+        call(dev, **kw)
         assert api.check_device_error()[0] == -5, kw
     bad = pool.table.copy()
     bad[0, 3] = 10 ** 6
-    dev[4] = i32(bad)
-    ok()
+    dev[4] = i32(wide(bad, pool))
+    call(dev)
     assert api.check_device_error()[0] == -5
 
 
@@ -156,6 +182,7 @@ def test_captured_calls_follow_their_lengths():
     import torch
     pool = shared_pool(11, 4, 2, 128, 64, [0, 4], [512], [600] * 4)
     dev = pool.dev()
+    dev[4] = i32(wide(pool.table, pool))
     q = torch.randn(4, 8, 1, 128, device="cuda").bfloat16()
     seq, pre, first = i32([520, 530, 540, 550]), i32([512, 512]), i32([0, 2, 4])
     call = lambda: api.fwd_cache_prefix(q, *dev, seq, pre, group_first=first)
@@ -196,6 +223,7 @@ def test_decoding_behind_a_shared_prompt():
     rng = np.random.default_rng(12)
     pool = shared_pool(12, B, Hk, d, page, [0, B], [prompt], [prompt + 40] * B)
     dev, table = pool.dev(), table_of(64)
+    dev[4] = i32(wide(pool.table, pool))
     w = torch.from_numpy(rng.uniform(0.5, 1.5, d).astype(np.float32)).cuda()
     kw = dict(q_weight=w, k_weight=w, layout="bnhd")
     new = lambda b, t, h: torch.from_numpy(rng.standard_normal((b, t, h, d)).astype(np.float32)).bfloat16().cuda()

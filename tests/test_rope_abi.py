@@ -83,6 +83,13 @@ def test_a_bad_prefix_is_refused(lib):
     assert call(d=96) == -2
     sizes = lib.attn_fwd_cache_prefix_workspace_bytes
     assert sizes(1, 3, 2, 1, 64) == 0 and sizes(0, 1, 1, 1, 64) == 0 and sizes(1, 1, 1, 1, 96) == 0
-    # the segments of the larger launch, then the prefixes' part: fp32 rows, their statistics, a number a sequence
-    more = sizes(64, 32, 8, 2, 128) - sizes(1, 32, 8, 2, 128)
-    assert more == 63 * 2 * 32 * (128 * 4 + 8) and sizes(1, 32, 8, 2, 128) > lib.attn_fwd_cache_workspace_bytes(1, 32, 8, 200, 128)
+    # both launches' segments, the items' CTAs, and fp32 rows with their statistics, twice
+    r256 = lambda x: (x + 255) // 256 * 256
+    seg = lambda T: lib.attn_fwd_cache_workspace_bytes(1, 1, 1, T, 128)
+    for B, H, Hk, T in ((64, 32, 8, 2), (3, 40, 2, 3), (1, 1, 1, 1)):
+        G, rows = H // Hk, B * T * H
+        fin = r256(rows * 128 * 4) + r256(rows * 8)
+        want = (seg(200) + r256((B * T * G // 256 + B + 1) * Hk * 8) + fin
+                + seg(1) + r256(B * Hk * ((T * G + 7) // 8) * 8) + fin)
+        assert sizes(B, H, Hk, T, 128) == want
+    assert sizes(3, 40, 2, 70, 128) == lib.attn_fwd_cache_workspace_bytes(3, 40, 2, 70, 128)  # prompts
