@@ -823,10 +823,9 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 constexpr int kJoinWarps = 8;
 constexpr int kJoinFew = 16;  // segments that one warp joins alone
 
-// Running join of segments [i0, i1) of row r: maximum, sum and the lane's D/32 columns.
-template <int D>
+// Running join of segments of a row: maximum, sum and the lane's E columns.
+template <int E>
 struct Joined {
-    static constexpr int E = D / 32;
     float m = -INFINITY, l = 0.f, o[E] = {};
     __device__ void add(float sm, float sl, const float (&y)[E]) {
         if (sm == -INFINITY && sl == 0.f) return;  // a segment in which the row sees no key: no output either
@@ -854,7 +853,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     const int n = bd.c_last - bd.c_first + 2;  // segments: of CTAs c_first - 1 (which starts the item) .. c_last
     auto join = [&](int r, int i0, int i1, auto at_once) {  // so many segments' loads go out together
         constexpr int U = decltype(at_once)::value;
-        Joined<D> x;
+        Joined<E> x;
         for (int i = i0; i < i1; i += U) {
             float2 st[U];
             float y[U][E];
@@ -880,7 +879,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
         }
         return x;
     };
-    auto write = [&](int r, const Joined<D>& x) {
+    auto write = [&](int r, const Joined<E>& x) {
         const RowAt a = row_at(p, bd.q_len, hk, rt, r);
         const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
         uint16_t* dst = static_cast<uint16_t*>(p.o) + bd.b * p.os.b + a.h * p.os.h + a.t * p.os.n + lane * E;
@@ -899,13 +898,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
     }
     const int per = (n + kJoinWarps - 1) / kJoinWarps;
     for (int r = mine; r < rows; r += borders) {
-        const Joined<D> x = join(r, min(n, warp * per), min(n, warp * per + per), std::integral_constant<int, 8>{});
+        const Joined<E> x = join(r, min(n, warp * per), min(n, warp * per + per), std::integral_constant<int, 8>{});
 #pragma unroll
         for (int e = 0; e < E; ++e) o_sm[warp][lane * E + e] = x.o[e];
         if (lane == 0) stat_sm[warp] = make_float2(x.m, x.l);
         __syncthreads();
         if (warp == 0) {
-            Joined<D> z;
+            Joined<E> z;
             for (int w = 0; w < kJoinWarps; ++w) {
                 float y[E];
 #pragma unroll
@@ -921,13 +920,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_join_kernel(const Cache
 // Puts the parts of a row together, of its group's prefix and of the rest, each in one or more
 // segments: a row a warp.  Bound by latency: what the lengths say is read while the launch before
 // it still runs, then where the segments are, then all statistics (a lane each) and outputs at once.
+struct MergePart {  // of CacheFwdParams
+    const int2* items;
+    const float *part, *fin_o;
+    const float2 *stat, *fin_stat;
+    int rows;
+};
 struct CacheMergeParams {
-    CacheFwdParams prefix, rest;
+    CacheFwdParams rest;
+    MergePart parts[2];  // the prefixes', the rest's
 };
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_merge_kernel(const CacheMergeParams m) {
-    constexpr int E = D / 32, U = 8;
-    const int lane = threadIdx.x & 31;
+    constexpr int E = 8, LPR = D / E, S = 32 / LPR, U = 4;  // LPR lanes a segment, S segments at a time, U of those out
+    const int lane = threadIdx.x & 31, col = lane % LPR * E;
     const CacheFwdParams& p = m.rest;
     const int G = p.H / p.Hk;
     const long long row = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
@@ -945,53 +951,63 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_merge_kernel(const Cach
         if (start > 0 && queries > 0 && min(max(p.c.seq_lens[b], 0), cap) - queries < start)
             record_device_error(p.st, ATTN_DEVERR_PAGE, 0x305);
     }
-    // row of its item, in either part
+    // item of the row in either part, and its row there
     const int group_r = start > 0 ? ((b - group_begin(p, g)) * p.T + t) * G + h - hk * G : 0;
-    const int own_r = t * G + h - hk * G, own_tile = own_r / p.rows, group_tile_r = group_r / m.prefix.rows;
-    const int2* own_item = p.items + (static_cast<long long>(b) * p.Hk + hk) * most_row_tiles(p) + own_tile;
-    const int2* group_item = m.prefix.items + (start > 0 ? (group_tile(m.prefix, g) + group_tile_r) * p.Hk + hk : 0);
+    const int own_r = t * G + h - hk * G, own_tile = own_r / p.rows, shared_tile = group_r / kPromptRows;
+    const int2* own_item = m.parts[1].items + (static_cast<long long>(b) * p.Hk + hk) * most_row_tiles(p) + own_tile;
+    const int2* shared_item = m.parts[0].items + (start > 0 ? static_cast<long long>(group_tile(p, g) + shared_tile) * p.Hk + hk : 0);
     pdl_wait();
     if (!in || t >= queries) return;
-    const int2 own = *own_item, shared = start > 0 ? *group_item : make_int2(0, -1);
+    const int2 own = *own_item, shared = start > 0 ? *shared_item : make_int2(0, -1);
     const int n0 = shared.y - shared.x + 1, n = n0 + own.y - own.x + 1;  // segments: the prefix's, then the others
-    Joined<D> x;
+    Joined<E> x;
     for (int i0 = 0; i0 < n; i0 += 32) {
-        // lane: segment i0 + lane
-        const int i = i0 + lane;
-        const bool of_own = i >= n0;
-        const CacheFwdParams& part = of_own ? m.rest : m.prefix;
-        const int2 c = of_own ? own : shared;
-        const int k = of_own ? i - n0 : i, r = of_own ? own_r - own_tile * p.rows : group_r - group_tile_r * m.prefix.rows;
-        const bool whole = c.x == c.y;
-        const long long at = whole ? row : (2ll * (c.x + k) + (k == 0 ? 1 : 0)) * part.rows + r;
+        const int i = i0 + lane;  // this lane's segment
         float2 st = make_float2(-INFINITY, 0.f);
-        unsigned long long src = 0;
-        if (i < n) {
+        const float* src = nullptr;
+        auto find = [&](const MergePart& part, int2 c, int k, int r) {
+            const bool whole = c.x == c.y;
+            const long long at = whole ? row : (2ll * (c.x + k) + (k == 0 ? 1 : 0)) * part.rows + r;
             st = (whole ? part.fin_stat : part.stat)[at];
-            src = reinterpret_cast<unsigned long long>((whole ? part.fin_o : part.part) + at * D);
-        }
+            src = (whole ? part.fin_o : part.part) + at * D;
+        };
+        if (i < n0) find(m.parts[0], shared, i, group_r - shared_tile * kPromptRows);
+        else if (i < n) find(m.parts[1], own, i - n0, own_r - own_tile * p.rows);
         const int here = min(32, n - i0);
-        for (int j0 = 0; j0 < here; j0 += U) {
+        for (int j0 = lane / LPR; j0 - lane / LPR < here; j0 += S * U) {
             float y[U][E];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float* from = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, src, j0 + u)) + lane * E;
+                const int k = j0 + u * S;
+                const float* from = reinterpret_cast<const float*>(
+                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k & 31)) + col;
 #pragma unroll
-                for (int e = 0; e < E; e += 2) {
-                    const float2 v = j0 + u < here ? *reinterpret_cast<const float2*>(from + e) : make_float2(0.f, 0.f);
-                    y[u][e] = v.x;
-                    y[u][e + 1] = v.y;
+                for (int e = 0; e < E; e += 4) {
+                    const float4 v = k < here ? *reinterpret_cast<const float4*>(from + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    y[u][e] = v.x, y[u][e + 1] = v.y, y[u][e + 2] = v.z, y[u][e + 3] = v.w;
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                x.add(__shfl_sync(0xffffffffu, st.x, j0 + u), __shfl_sync(0xffffffffu, st.y, j0 + u), y[u]);
+            for (int u = 0; u < U; ++u) {
+                const int k = j0 + u * S;
+                const float sm = __shfl_sync(0xffffffffu, st.x, k & 31), sl = __shfl_sync(0xffffffffu, st.y, k & 31);
+                x.add(k < here ? sm : -INFINITY, k < here ? sl : 0.f, y[u]);
+            }
         }
     }
-    const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
-    uint16_t* dst = static_cast<uint16_t*>(p.o) + b * p.os.b + h * p.os.h + t * p.os.n + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16x2(x.o[e] * inv, x.o[e + 1] * inv);
+    for (int o = LPR; o < 32; o <<= 1) {
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] = __shfl_xor_sync(0xffffffffu, x.o[e], o);
+        const float sm = __shfl_xor_sync(0xffffffffu, x.m, o), sl = __shfl_xor_sync(0xffffffffu, x.l, o);
+        x.add(sm, sl, y);
+    }
+    const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
+    uint16_t* dst = static_cast<uint16_t*>(p.o) + b * p.os.b + h * p.os.h + t * p.os.n + col;
+    if (lane < LPR)
+        *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x.o[0] * inv, x.o[1] * inv), pack_bf16x2(x.o[2] * inv, x.o[3] * inv),
+                                                    pack_bf16x2(x.o[4] * inv, x.o[5] * inv), pack_bf16x2(x.o[6] * inv, x.o[7] * inv));
     if (lane == 0)
         p.lse[(static_cast<long long>(b) * p.H + h) * p.T + t] = x.l != 0.f ? (x.m - kWeightShift + log2f(x.l)) * kLn2 : INFINITY;
 }
@@ -1036,7 +1052,8 @@ cudaError_t launch_cache_merge(const CacheFwdParams& prefix, const CacheFwdParam
     const long long blocks = (static_cast<long long>(rest.B) * rest.T * rest.H + kJoinWarps - 1) / kJoinWarps;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks));
-    const CacheMergeParams m{prefix, rest};
+    auto part = [](const CacheFwdParams& p) { return MergePart{p.items, p.part, p.fin_o, p.stat, p.fin_stat, p.rows}; };
+    const CacheMergeParams m{rest, {part(prefix), part(rest)}};
     if (rest.D == 64) return launch_dependent(cache_merge_kernel<64>, grid, 32 * kJoinWarps, 0, stream, m);
     if (rest.D == 128) return launch_dependent(cache_merge_kernel<128>, grid, 32 * kJoinWarps, 0, stream, m);
     return cudaErrorInvalidValue;

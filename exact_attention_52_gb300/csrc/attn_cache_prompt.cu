@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             while (next_segment<PART>(p, walk))
                 if (w.v0 == 0 && lane == 0) {
                     const long long x = w.s.x - (w.v1 - w.v0);
-                    p.items[(group_tile(p, w.b) + w.pair) * p.Hk + w.hk] =
+                    p.items[static_cast<long long>(group_tile(p, w.b) + w.pair) * p.Hk + w.hk] =
                         make_int2(static_cast<int>(blockIdx.x), static_cast<int>(div_mostly32(x + w.u.n - 1, w.s.share)));
                 }
         } else if (warp == 9) {  // what the joining kernel finds at the border before this share

@@ -73,13 +73,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 // ---------------------------------------------------------------------------
 // With u = x r: dn = R^T dy, dw += dn u, g = dn w, dx = r (g - u mean(g u)).  Reads x and dy,
 // writes dx; r is worked out again.  Block c of a tensor's share of the grid takes the c-th of
-// equal ranges of (token tile, HT heads) units, loads one unit ahead, works angles out when the
-// tile changes and keeps dw in registers; a block's sums over its threads go to the workspace,
-// one row a block, and a second kernel adds the rows in their order: no atomics, so the sums are
-// the same every time.
+// equal ranges of (token tile, HT heads) units, works angles out when the tile changes and keeps dw
+// in registers; a block's sums over its threads go to the workspace, one row a block, and a second
+// kernel adds the rows in their order: no atomics, so the sums are the same every time.
+// Bound by the memory: each thread copies its own elements kBwdStages - 1 units ahead into its own
+// places in shared memory, which takes no registers and no barrier.
+constexpr int kBwdStages = 4;
+
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const RopeBwdParams p) {
     constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR;
+    __shared__ uint4 ring[kBwdStages][4][kRopeThreads];
     pdl_wait();
     pdl_launch_dependents();
     const int which = static_cast<int>(blockIdx.x) >= p.blocks[0] ? 1 : 0;
@@ -92,53 +96,69 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
     load_weight(p.r, which ? p.r.k_weight : p.r.q_weight, lo, hi, w);
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[i] = 0.f;
-    const Strides xs = p.xs[which], ys = p.ys[which], gs = p.gs[which];
-    const uint4* x = static_cast<const uint4*>(p.x[which]);
-    const uint4* dy = static_cast<const uint4*>(p.dy[which]);
-    uint4* dx = static_cast<uint4*>(p.dx[which]);
+    const long long xh = p.xs[which].h / 8, gh = p.gs[which].h / 8, yh = p.ys[which].h / 8;
     const int heads = p.heads[which], per_tile = (heads + HT - 1) / HT;
     const long long units = p.tiles * per_tile;
     const long long u0 = units * c / p.blocks[which], u1 = units * (c + 1) / p.blocks[which];
-    RopeAngles a;
 
-    struct At {  // a unit's place for this thread
-        long long tile, b;
-        int group, n, h;
-        bool there;
+    // A unit's token and head for this thread; walked twice, by the copies and behind them.
+    struct Walk {
+        long long tile;
+        int group, b, n;
+        bool there;  // the token
     };
-    auto place = [&](long long tile, int group) {
-        At k;
-        k.tile = tile;
-        k.group = group;
+    auto at_tile = [&](Walk& k, long long tile) {
         const long long tok = tile * TT + slot % TT;
-        k.h = group * HT + slot / TT;
-        k.there = tok < p.tokens && k.h < heads;
-        k.b = k.there ? div_mostly32(tok, p.N) : 0;
-        k.n = k.there ? static_cast<int>(tok - k.b * p.N) : 0;
-        return k;
+        k.tile = tile;
+        k.there = tok < p.tokens;
+        k.b = k.there ? static_cast<int>(div_mostly32(tok, p.N)) : 0;
+        k.n = k.there ? static_cast<int>(tok - static_cast<long long>(k.b) * p.N) : 0;
     };
-    uint4 xl, xu, gl, gu;
-    auto load = [&](const At& k) {
-        xl = xu = gl = gu = make_uint4(0u, 0u, 0u, 0u);
-        if (!k.there) return;
-        const uint4* xp = x + (k.b * xs.b + k.n * xs.n + k.h * xs.h) / 8;
-        const uint4* gp = dy + (k.b * gs.b + k.n * gs.n + k.h * gs.h) / 8;
-        xl = xp[lo], xu = xp[hi], gl = gp[lo], gu = gp[hi];
+    const uint4 *x = nullptr, *dy = nullptr;  // of the copies' token
+    auto copy_tile = [&](Walk& k, long long tile) {
+        at_tile(k, tile);
+        x = static_cast<const uint4*>(p.x[which]) + (k.b * p.xs[which].b + k.n * p.xs[which].n) / 8;
+        dy = static_cast<const uint4*>(p.dy[which]) + (k.b * p.gs[which].b + k.n * p.gs[which].n) / 8;
     };
-    At next = place(u0 / per_tile, static_cast<int>(u0 % per_tile));
-    if (u0 < u1) load(next);
-    long long turned = -1;
-    for (long long u = u0; u < u1; ++u) {
-        const At k = next;
-        float v[16], g[16];
-        unpack16(xl, xu, v);
-        unpack16(gl, gu, g);
-        if (u + 1 < u1) {
-            next = k.group + 1 < per_tile ? place(k.tile, k.group + 1) : place(k.tile + 1, 0);
-            load(next);
+    Walk ahead, k;
+    long long copied = u0;
+    auto copy = [&] {
+        if (copied < u1) {
+            const int h = ahead.group * HT + slot / TT;
+            const bool there = ahead.there && h < heads;  // else zeros
+            uint4(*to)[kRopeThreads] = ring[(copied - u0) % kBwdStages];
+            const uint4 *xp = there ? x + h * xh : static_cast<const uint4*>(p.x[which]);
+            const uint4 *gp = there ? dy + h * gh : static_cast<const uint4*>(p.dy[which]);
+            cp_async16(smem_u32(&to[0][threadIdx.x]), xp + lo, there);
+            cp_async16(smem_u32(&to[1][threadIdx.x]), xp + hi, there);
+            cp_async16(smem_u32(&to[2][threadIdx.x]), gp + lo, there);
+            cp_async16(smem_u32(&to[3][threadIdx.x]), gp + hi, there);
+            if (++ahead.group == per_tile) {
+                ahead.group = 0;
+                copy_tile(ahead, ahead.tile + 1);
+            }
         }
-        if (k.tile != turned) {
-            turned = k.tile;
+        ++copied;
+        cp_async_commit();
+    };
+    copy_tile(ahead, u0 / per_tile);
+    k.group = ahead.group = static_cast<int>(u0 % per_tile);
+    at_tile(k, ahead.tile);
+#pragma unroll
+    for (int i = 0; i < kBwdStages - 1; ++i) copy();
+    RopeAngles a;
+    uint4* dx = nullptr;
+    bool turned = false;  // angles and dx are this tile's
+    for (long long u = u0; u < u1; ++u) {
+        cp_async_wait<kBwdStages - 2>();
+        const uint4(*from)[kRopeThreads] = ring[(u - u0) % kBwdStages];
+        float v[16], g[16];
+        unpack16(from[0][threadIdx.x], from[1][threadIdx.x], v);
+        unpack16(from[2][threadIdx.x], from[3][threadIdx.x], g);
+        copy();  // over what was read a unit ago
+        if (!turned) {
+            turned = true;
+            dx = static_cast<uint4*>(p.dx[which]) + (k.b * p.ys[which].b + k.n * p.ys[which].n) / 8;
             if (t < nrot) a.at(p.r, t, p.positions ? __ldg(p.positions + k.b * p.position_stride + k.n) : k.n, -1.f);
         }
         const float r = head_rnorm<D>(v, p.r.eps);
@@ -152,14 +172,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
             (i & 1 ? s1 : s0) += g[i] * v[i];
         }
         const float mean = head_sum<D>(s0 + s1) * (1.f / D);
-        if (k.there) {
+        const int h = k.group * HT + slot / TT;
+        if (k.there && h < heads) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = r * (g[i] - v[i] * mean);
             uint4 ol, ou;
             pack16(v, ol, ou);
-            uint4* at = dx + (k.b * ys.b + k.n * ys.n + k.h * ys.h) / 8;
-            at[lo] = ol;
-            at[hi] = ou;
+            dx[h * yh + lo] = ol;
+            dx[h * yh + hi] = ou;
+        }
+        if (++k.group == per_tile) {
+            k.group = 0;
+            at_tile(k, k.tile + 1);
+            turned = false;
         }
     }
 
@@ -179,21 +204,25 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
     }
 }
 
-// dw of one tensor (blockIdx.y) and 32 elements: its blocks' rows added up, warp w taking rows w, w + 32, ...
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const RopeBwdParams p) {
-    __shared__ float sums[32][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, which = blockIdx.y, e = blockIdx.x * 32 + lane;
+// dw of one tensor (blockIdx.y) and 8 elements: its blocks' rows added up, thread group i taking rows
+// i, i + 64, ...
+__global__ void __launch_bounds__(512) rope_dw_kernel(const RopeBwdParams p) {
+    __shared__ float sums[8][65];
+    const int e = threadIdx.x & 7, from = threadIdx.x >> 3, which = blockIdx.y;
     pdl_wait();
-    const float* part = p.part + static_cast<long long>(which ? p.blocks[0] : 0) * p.D + e;
+    const float* part = p.part + static_cast<long long>(which ? p.blocks[0] : 0) * p.D + blockIdx.x * 8 + e;
     float v = 0.f;
-#pragma unroll 8
-    for (int i = warp; i < p.blocks[which]; i += 32) v += part[static_cast<long long>(i) * p.D];
-    sums[warp][lane] = v;
+#pragma unroll
+    for (int i = 0; i < kRopeBwdGridMax / 64; ++i)
+        if (from + 64 * i < p.blocks[which]) v += part[(from + 64ll * i) * p.D];
+    sums[e][from] = v;
     __syncthreads();
-    v = sums[lane][warp];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= 8) return;
+    v = sums[warp][lane] + sums[warp][lane + 32];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0 && p.dw[which]) p.dw[which][blockIdx.x * 32 + warp] = v;
+    if (lane == 0 && p.dw[which]) p.dw[which][blockIdx.x * 8 + warp] = v;
 }
 
 int sm_count(cudaError_t* e) {
@@ -243,7 +272,7 @@ cudaError_t launch_rope_norm_bwd_d(RopeBwdParams p, cudaStream_t stream) {
     const dim3 blocks(static_cast<unsigned>(p.blocks[0] + p.blocks[1]));
     e = p.r.interleaved ? launch_dependent(rope_norm_bwd_kernel<D, true>, blocks, kRopeThreads, 0, stream, p)
                         : launch_dependent(rope_norm_bwd_kernel<D, false>, blocks, kRopeThreads, 0, stream, p);
-    return e != cudaSuccess ? e : launch_dependent(rope_dw_kernel, dim3(D / 32, 2), 1024, 0, stream, p);
+    return e != cudaSuccess ? e : launch_dependent(rope_dw_kernel, dim3(D / 8, 2), 512, 0, stream, p);
 }
 
 }  // namespace

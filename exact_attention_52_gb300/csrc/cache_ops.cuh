@@ -87,9 +87,9 @@ __device__ __forceinline__ int group_start(const CacheFwdParams& p, int b) {
     const int g = group_of(p, b);
     return g < 0 ? 0 : group_len(p, g);
 }
-// Number of a group's first tile of p.rows rows, in which those of several groups do not meet.
-__device__ __forceinline__ long long group_tile(const CacheFwdParams& p, int g) {
-    return static_cast<long long>(group_begin(p, g)) * p.T * (p.H / p.Hk) / p.rows + g;
+// Number of a group's first tile of kPromptRows rows; tiles of several groups have numbers of their own.
+__device__ __forceinline__ int group_tile(const CacheFwdParams& p, int g) {
+    return group_begin(p, g) * p.T * (p.H / p.Hk) / kPromptRows + g;  // rows count in 32 bits
 }
 __device__ __forceinline__ int query_count(const CacheFwdParams& p, int b) {
     return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;
