@@ -165,17 +165,20 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
         if (t < nrot) rotate16<INTER>(a, g);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            v[i] *= r;
-            dw[i] = fmaf(g[i], v[i], dw[i]);  // (rows that are not there are zeros)
-            g[i] *= w[i];
-            (i & 1 ? s1 : s0) += g[i] * v[i];
+        for (int i = 0; i < 16; i += 2) {
+            fmul2(v[i], v[i + 1], v[i], v[i + 1], r, r);
+            ffma2(dw[i], dw[i + 1], g[i], g[i + 1], v[i], v[i + 1], dw[i], dw[i + 1]);  // (rows that are not there are zeros)
+            fmul2(g[i], g[i + 1], g[i], g[i + 1], w[i], w[i + 1]);
+            ffma2(s0, s1, g[i], g[i + 1], v[i], v[i + 1], s0, s1);
         }
         const float mean = head_sum<D>(s0 + s1) * (1.f / D);
         const int h = k.group * HT + slot / TT;
         if (k.there && h < heads) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = r * (g[i] - v[i] * mean);
+            for (int i = 0; i < 16; i += 2) {
+                fmul2(g[i], g[i + 1], g[i], g[i + 1], r, r);
+                ffma2(v[i], v[i + 1], v[i], v[i + 1], -r * mean, -r * mean, g[i], g[i + 1]);
+            }
             uint4 ol, ou;
             pack16(v, ol, ou);
             dx[h * yh + lo] = ol;

@@ -66,12 +66,15 @@ __device__ __forceinline__ void pack16(const float (&x)[16], uint4& lo, uint4& h
 template <bool INTER>
 __device__ __forceinline__ void rotate16(const RopeAngles& a, float (&x)[16]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float& x1 = x[INTER ? 2 * i : i];
-        float& x2 = x[INTER ? 2 * i + 1 : i + 8];
-        const float y1 = x1 * a.c[i] - x2 * a.s[i];
-        x2 = x2 * a.c[i] + x1 * a.s[i];
-        x1 = y1;
+    for (int i = 0; i < 8; i += 2) {  // two pairs at a time, in packed operations
+        float &p1 = x[INTER ? 2 * i : i], &p2 = x[INTER ? 2 * i + 1 : i + 8];
+        float &q1 = x[INTER ? 2 * i + 2 : i + 1], &q2 = x[INTER ? 2 * i + 3 : i + 9];
+        float a0, a1, b0, b1, c0, c1;
+        fmul2(a0, a1, p2, q2, a.s[i], a.s[i + 1]);
+        fmul2(b0, b1, p1, q1, a.s[i], a.s[i + 1]);
+        fmul2(c0, c1, p1, q1, a.c[i], a.c[i + 1]);
+        fsub2(p1, q1, c0, c1, a0, a1);
+        ffma2(p2, q2, p2, q2, a.c[i], a.c[i + 1], b0, b1);
     }
 }
 
@@ -88,7 +91,7 @@ template <int D>
 __device__ __forceinline__ float head_rnorm(const float (&x)[16], float eps) {
     float a = 0.f, b = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a = fmaf(x[2 * i], x[2 * i], a), b = fmaf(x[2 * i + 1], x[2 * i + 1], b);
+    for (int i = 0; i < 16; i += 2) ffma2(a, b, x[i], x[i + 1], x[i], x[i + 1], a, b);
     return rsqrtf(fmaf(head_sum<D>(a + b), 1.f / D, eps));
 }
 
@@ -115,7 +118,10 @@ __device__ __forceinline__ void norm_rotate(float (&x)[16], bool norm, const flo
     if (norm) {
         const float r = head_rnorm<D>(x, eps);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+        for (int i = 0; i < 16; i += 2) {
+            fmul2(x[i], x[i + 1], x[i], x[i + 1], r, r);
+            fmul2(x[i], x[i + 1], x[i], x[i + 1], w[i], w[i + 1]);
+        }
     }
     if (turns) rotate16<INTER>(a, x);
 }
