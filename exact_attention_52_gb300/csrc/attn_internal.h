@@ -174,7 +174,7 @@ struct RopeParams {
     int token_slots, hp, chunks[2];
 };
 
-constexpr int kRopeBwdGridMax = 640;
+constexpr int kRopeBwdGridMax = 640;  // 160 SMs of four
 
 struct RopeBwdParams {
     RopeView r;
@@ -201,8 +201,8 @@ struct CacheAppendRopeParams {
     Strides qs, qos;
     int H;
     // Set by the launcher:
-    int token_slots, hp;
-    unsigned pages, page_blocks, token_tiles, chunks;
+    int token_slots, hp, hk;
+    unsigned pages, k_parts, k_blocks, page_blocks, token_tiles, chunks;
 };
 
 // What the joining kernel of the cache attention finds at the border before a CTA's share.

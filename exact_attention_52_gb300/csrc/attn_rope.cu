@@ -9,63 +9,31 @@
 namespace attn {
 namespace {
 
-constexpr int kRopeThreads = 128;
-
 // ---------------------------------------------------------------------------
 // Rotation (forward; backward where there is no norm: the transpose, sign = -1)
 // ---------------------------------------------------------------------------
 // A block takes TT tokens and HT * hp heads of Q or of K: thread (slot, t) holds 16 elements of
 // head slot / TT + HT * i of token slot % TT, i = 0 .. hp - 1, so that a token's angles (8 a
-// thread, some 40 instructions each) serve hp heads and four heads' loads are out at a time.
+// thread, some 50 instructions each) serve hp heads.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-    constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR, U = 4;
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeParams p) {
+    constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR;
+    __shared__ RopeRing ring;
     pdl_wait();
     const int which = static_cast<int>(blockIdx.y) >= p.chunks[0] ? 1 : 0;
     const int chunk = static_cast<int>(blockIdx.y) - (which ? p.chunks[0] : 0);
-    const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-    const int TT = p.token_slots, HT = SLOTS / TT;
+    const int slot = threadIdx.x / TPR, TT = p.token_slots, HT = SLOTS / TT;
     const long long tok = static_cast<long long>(blockIdx.x) * TT + slot % TT;
     const bool there = tok < p.tokens;
     const long long b = there ? div_mostly32(tok, p.N) : 0;
     const int n = there ? static_cast<int>(tok - b * p.N) : 0;
-    const int nrot = p.r.rot / 16;
-    int lo, hi;
-    rope_pieces<INTER>(t, nrot, lo, hi);
-    const void* weight = which ? p.r.k_weight : p.r.q_weight;
-    float w[16] = {};
-    if (weight) load_weight(p.r, weight, lo, hi, w);
     const Strides xs = p.xs[which], ys = p.ys[which];
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.x[which]) + b * xs.b + n * xs.n);
-    uint4* y = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y[which]) + b * ys.b + n * ys.n);
-    const long long xh = xs.h / 8, yh = ys.h / 8;
-    const int h0 = chunk * HT * p.hp + slot / TT, h1 = min(p.heads[which], (chunk + 1) * HT * p.hp);
-    RopeAngles a;
-    if (there && t < nrot) a.at(p.r, t, p.positions ? __ldg(p.positions + b * p.position_stride + n) : n, p.sign);
-    for (int i = 0; i < p.hp; i += U) {  // (every thread of a warp the same number: norms are sums of several)
-        uint4 vl[U], vh[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + (i + u) * HT;
-            vl[u] = vh[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (there && h < h1) {
-                vl[u] = x[h * xh + lo];
-                vh[u] = x[h * xh + hi];
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int h = h0 + (i + u) * HT;
-            float v[16];
-            unpack16(vl[u], vh[u], v);
-            norm_rotate<D, INTER>(v, weight != nullptr, w, p.r.eps, t < nrot, a);
-            if (there && h < h1) {
-                if (weight != nullptr || t < nrot) pack16(v, vl[u], vh[u]);  // else the bits as they are
-                y[h * yh + lo] = vl[u];
-                y[h * yh + hi] = vh[u];
-            }
-        }
-    }
+    const int first = chunk * HT * p.hp, heads = min(p.heads[which] - first, HT * p.hp);
+    rotate_heads<D, INTER>(p.r, which ? p.r.k_weight : p.r.q_weight, p.sign, there,
+                           there && p.positions ? __ldg(p.positions + b * p.position_stride + n) : n,
+                           static_cast<const uint4*>(p.x[which]) + (b * xs.b + n * xs.n) / 8, xs.h / 8,
+                           static_cast<uint4*>(p.y[which]) + (b * ys.b + n * ys.n) / 8, ys.h / 8, first + slot / TT, HT,
+                           first + heads, (heads + HT - 1) / HT, ring);
 }
 
 // ---------------------------------------------------------------------------
@@ -78,10 +46,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 // kernel adds the rows in their order: no atomics, so the sums are the same every time.
 // Bound by the memory: each thread copies its own elements kBwdStages - 1 units ahead into its own
 // places in shared memory, which takes no registers and no barrier.
-constexpr int kBwdStages = 4;
+constexpr int kBwdStages = 4, kBwdBlocks = 4;  // stages; blocks an SM
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const RopeBwdParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kBwdBlocks) rope_norm_bwd_kernel(const RopeBwdParams p) {
     constexpr int TPR = D / 16, SLOTS = kRopeThreads / TPR;
     __shared__ uint4 ring[kBwdStages][4][kRopeThreads];
     pdl_wait();
@@ -92,8 +60,16 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
     const int TT = p.token_slots, HT = SLOTS / TT, nrot = p.r.rot / 16;
     int lo, hi;
     rope_pieces<INTER>(t, nrot, lo, hi);
-    float w[16], dw[16];
-    load_weight(p.r, which ? p.r.k_weight : p.r.q_weight, lo, hi, w);
+    // the head's weights, in the order of the pieces that its threads hold
+    __shared__ float4 weights[4][TPR];
+    if (slot == 0) {
+        float w[16];
+        load_weight(p.r, which ? p.r.k_weight : p.r.q_weight, lo, hi, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) weights[i][t] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __syncthreads();
+    float dw[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) dw[i] = 0.f;
     const long long xh = p.xs[which].h / 8, gh = p.gs[which].h / 8, yh = p.ys[which].h / 8;
@@ -104,7 +80,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
     // A unit's token and head for this thread; walked twice, by the copies and behind them.
     struct Walk {
         long long tile;
-        int group, b, n;
+        int b, n, h;
         bool there;  // the token
     };
     auto at_tile = [&](Walk& k, long long tile) {
@@ -114,66 +90,78 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
         k.b = k.there ? static_cast<int>(div_mostly32(tok, p.N)) : 0;
         k.n = k.there ? static_cast<int>(tok - static_cast<long long>(k.b) * p.N) : 0;
     };
-    const uint4 *x = nullptr, *dy = nullptr;  // of the copies' token
-    auto copy_tile = [&](Walk& k, long long tile) {
+    const int h_last = (per_tile - 1) * HT + slot / TT;  // this thread's head in a tile's last unit
+    const uint4 *x = nullptr, *dy = nullptr;  // of the copies' token and head
+    auto copy_tile = [&](Walk& k, long long tile, int group) {
         at_tile(k, tile);
-        x = static_cast<const uint4*>(p.x[which]) + (k.b * p.xs[which].b + k.n * p.xs[which].n) / 8;
-        dy = static_cast<const uint4*>(p.dy[which]) + (k.b * p.gs[which].b + k.n * p.gs[which].n) / 8;
+        k.h = group * HT + slot / TT;
+        x = static_cast<const uint4*>(p.x[which]) + (k.b * p.xs[which].b + k.n * p.xs[which].n) / 8 + k.h * xh;
+        dy = static_cast<const uint4*>(p.dy[which]) + (k.b * p.gs[which].b + k.n * p.gs[which].n) / 8 + k.h * gh;
     };
     Walk ahead, k;
     long long copied = u0;
+    int to_slot = 0;
     auto copy = [&] {
         if (copied < u1) {
-            const int h = ahead.group * HT + slot / TT;
-            const bool there = ahead.there && h < heads;  // else zeros
-            uint4(*to)[kRopeThreads] = ring[(copied - u0) % kBwdStages];
-            const uint4 *xp = there ? x + h * xh : static_cast<const uint4*>(p.x[which]);
-            const uint4 *gp = there ? dy + h * gh : static_cast<const uint4*>(p.dy[which]);
-            cp_async16(smem_u32(&to[0][threadIdx.x]), xp + lo, there);
-            cp_async16(smem_u32(&to[1][threadIdx.x]), xp + hi, there);
-            cp_async16(smem_u32(&to[2][threadIdx.x]), gp + lo, there);
-            cp_async16(smem_u32(&to[3][threadIdx.x]), gp + hi, there);
-            if (++ahead.group == per_tile) {
-                ahead.group = 0;
-                copy_tile(ahead, ahead.tile + 1);
+            uint4(*to)[kRopeThreads] = ring[to_slot];
+            to_slot = to_slot + 1 == kBwdStages ? 0 : to_slot + 1;
+            if (ahead.there && ahead.h < heads) {
+                cp_async16(smem_u32(&to[0][threadIdx.x]), x + lo);
+                cp_async16(smem_u32(&to[1][threadIdx.x]), x + hi);
+                cp_async16(smem_u32(&to[2][threadIdx.x]), dy + lo);
+                cp_async16(smem_u32(&to[3][threadIdx.x]), dy + hi);
+            } else {
+                to[0][threadIdx.x] = to[1][threadIdx.x] = to[2][threadIdx.x] = to[3][threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (ahead.h == h_last) {
+                copy_tile(ahead, ahead.tile + 1, 0);
+            } else {
+                ahead.h += HT;
+                x += HT * xh;
+                dy += HT * gh;
             }
         }
         ++copied;
         cp_async_commit();
     };
-    copy_tile(ahead, u0 / per_tile);
-    k.group = ahead.group = static_cast<int>(u0 % per_tile);
-    at_tile(k, ahead.tile);
-#pragma unroll
+    copy_tile(ahead, u0 / per_tile, static_cast<int>(u0 % per_tile));
+    k = ahead;
+#pragma unroll 1
     for (int i = 0; i < kBwdStages - 1; ++i) copy();
     RopeAngles a;
     uint4* dx = nullptr;
     bool turned = false;  // angles and dx are this tile's
+    int from_slot = 0;
     for (long long u = u0; u < u1; ++u) {
         cp_async_wait<kBwdStages - 2>();
-        const uint4(*from)[kRopeThreads] = ring[(u - u0) % kBwdStages];
+        const uint4(*from)[kRopeThreads] = ring[from_slot];
+        from_slot = from_slot + 1 == kBwdStages ? 0 : from_slot + 1;
         float v[16], g[16];
         unpack16(from[0][threadIdx.x], from[1][threadIdx.x], v);
         unpack16(from[2][threadIdx.x], from[3][threadIdx.x], g);
         copy();  // over what was read a unit ago
         if (!turned) {
             turned = true;
-            dx = static_cast<uint4*>(p.dx[which]) + (k.b * p.ys[which].b + k.n * p.ys[which].n) / 8;
+            dx = static_cast<uint4*>(p.dx[which]) + (k.b * p.ys[which].b + k.n * p.ys[which].n) / 8 + k.h * yh;
             if (t < nrot) a.at(p.r, t, p.positions ? __ldg(p.positions + k.b * p.position_stride + k.n) : k.n, -1.f);
         }
         const float r = head_rnorm<D>(v, p.r.eps);
         if (t < nrot) rotate16<INTER>(a, g);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < 16; i += 4) {
+            const float4 w = weights[i / 4][t];
             fmul2(v[i], v[i + 1], v[i], v[i + 1], r, r);
+            fmul2(v[i + 2], v[i + 3], v[i + 2], v[i + 3], r, r);
             ffma2(dw[i], dw[i + 1], g[i], g[i + 1], v[i], v[i + 1], dw[i], dw[i + 1]);  // (rows that are not there are zeros)
-            fmul2(g[i], g[i + 1], g[i], g[i + 1], w[i], w[i + 1]);
+            ffma2(dw[i + 2], dw[i + 3], g[i + 2], g[i + 3], v[i + 2], v[i + 3], dw[i + 2], dw[i + 3]);
+            fmul2(g[i], g[i + 1], g[i], g[i + 1], w.x, w.y);
+            fmul2(g[i + 2], g[i + 3], g[i + 2], g[i + 3], w.z, w.w);
             ffma2(s0, s1, g[i], g[i + 1], v[i], v[i + 1], s0, s1);
+            ffma2(s0, s1, g[i + 2], g[i + 3], v[i + 2], v[i + 3], s0, s1);
         }
         const float mean = head_sum<D>(s0 + s1) * (1.f / D);
-        const int h = k.group * HT + slot / TT;
-        if (k.there && h < heads) {
+        if (k.there && k.h < heads) {
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
                 fmul2(g[i], g[i + 1], g[i], g[i + 1], r, r);
@@ -181,13 +169,16 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_norm_bwd_kernel(const Ro
             }
             uint4 ol, ou;
             pack16(v, ol, ou);
-            dx[h * yh + lo] = ol;
-            dx[h * yh + hi] = ou;
+            dx[lo] = ol;
+            dx[hi] = ou;
         }
-        if (++k.group == per_tile) {
-            k.group = 0;
+        if (k.h == h_last) {
             at_tile(k, k.tile + 1);
+            k.h = slot / TT;
             turned = false;
+        } else {
+            k.h += HT;
+            dx += HT * yh;
         }
     }
 
@@ -216,7 +207,7 @@ __global__ void __launch_bounds__(512) rope_dw_kernel(const RopeBwdParams p) {
     const float* part = p.part + static_cast<long long>(which ? p.blocks[0] : 0) * p.D + blockIdx.x * 8 + e;
     float v = 0.f;
 #pragma unroll
-    for (int i = 0; i < kRopeBwdGridMax / 64; ++i)
+    for (int i = 0; i < (kRopeBwdGridMax + 63) / 64; ++i)
         if (from + 64 * i < p.blocks[which]) v += part[(from + 64ll * i) * p.D];
     sums[e][from] = v;
     __syncthreads();
@@ -263,7 +254,7 @@ cudaError_t launch_rope_norm_bwd_d(RopeBwdParams p, cudaStream_t stream) {
     p.token_slots = rope_token_slots(p.tokens, SLOTS);
     p.tiles = (p.tokens + p.token_slots - 1) / p.token_slots;
     const int HT = SLOTS / p.token_slots;
-    const int grid = sms * 4 < kRopeBwdGridMax ? sms * 4 : kRopeBwdGridMax;
+    const int grid = sms * kBwdBlocks < kRopeBwdGridMax ? sms * kBwdBlocks : kRopeBwdGridMax;
     const int all = p.heads[0] + p.heads[1];
     for (int i = 0; i < 2; ++i) {
         const long long units = p.tiles * ((p.heads[i] + HT - 1) / HT);

@@ -126,6 +126,68 @@ __device__ __forceinline__ void norm_rotate(float (&x)[16], bool norm, const flo
     if (turns) rotate16<INTER>(a, x);
 }
 
+constexpr int kRopeThreads = 128;
+// Heads that a thread copies ahead into its own places in shared memory, which takes no registers
+// and no barrier: 32 bytes each.
+constexpr int kRopeStages = 6;
+struct RopeRing {
+    uint4 at[kRopeStages][2][kRopeThreads];
+};
+
+// Norm (weight not null) and rotation of heads h, h + step, ... (count of them, the same for every
+// thread of a block) below h_end of one token (there: it exists) at a position: x and y point to its
+// head 0, whose heads are xh and yh pieces apart.
+template <int D, bool INTER>
+__device__ __forceinline__ void rotate_heads(const RopeView& r, const void* weight, float sign, bool there, int pos,
+                                             const uint4* x, long long xh, uint4* y, long long yh, int h, int step, int h_end,
+                                             int count, RopeRing& ring) {
+    const int tid = threadIdx.x, t = tid % (D / 16), nrot = r.rot / 16;
+    int lo, hi;
+    rope_pieces<INTER>(t, nrot, lo, hi);
+    x += h * xh;
+    y += h * yh;
+    int copied = 0, slot = 0, h_ahead = h;
+    auto copy = [&] {
+        if (copied < count) {
+            if (there && h_ahead < h_end) {
+                cp_async16(smem_u32(&ring.at[slot][0][tid]), x + lo);
+                cp_async16(smem_u32(&ring.at[slot][1][tid]), x + hi);
+            } else {  // zeros, which take part in a norm's shuffles
+                ring.at[slot][0][tid] = ring.at[slot][1][tid] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            x += step * xh;
+            h_ahead += step;
+            ++copied;
+            slot = slot + 1 == kRopeStages ? 0 : slot + 1;
+        }
+        cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kRopeStages - 1; ++i) copy();
+    float w[16] = {};
+    if (weight) load_weight(r, weight, lo, hi, w);
+    RopeAngles a;
+    if (there && t < nrot) a.at(r, t, pos, sign);
+    int from = 0;
+#pragma unroll 1
+    for (int i = 0; i < count; ++i) {
+        cp_async_wait<kRopeStages - 2>();
+        uint4 vl = ring.at[from][0][tid], vh = ring.at[from][1][tid];
+        from = from + 1 == kRopeStages ? 0 : from + 1;
+        copy();  // over what was read a head ago
+        float v[16];
+        unpack16(vl, vh, v);
+        norm_rotate<D, INTER>(v, weight != nullptr, w, r.eps, t < nrot, a);
+        if (there && h < h_end) {
+            if (weight || t < nrot) pack16(v, vl, vh);  // else the bits as they are
+            y[lo] = vl;
+            y[hi] = vh;
+        }
+        y += step * yh;
+        h += step;
+    }
+}
+
 // How many tokens a block of `slots` heads at a time takes side by side: all, or as few as
 // there are, the rest of the slots taking further heads of the same token.
 __host__ __device__ inline int rope_token_slots(long long tokens, int slots) {
