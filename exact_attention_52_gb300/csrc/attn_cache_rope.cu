@@ -235,7 +235,7 @@ cudaError_t launch_append_rope_d(CacheAppendRopeParams p, cudaStream_t stream) {
     const int HT = SLOTS / p.token_slots;
     for (p.hp = 8;; p.hp /= 2) {  // as many heads a thread as leave every SM some blocks
         p.chunks = static_cast<unsigned>((p.H + HT * p.hp - 1) / (HT * p.hp));
-        if (p.hp == 1 || static_cast<long long>(p.token_tiles) * p.chunks * c.B >= 8ll * sms) break;
+        if (p.hp == 1 || static_cast<long long>(p.token_tiles) * p.chunks * c.B >= 3ll * sms) break;
     }
     for (p.hk = c.Hk < 4 ? c.Hk : 4;; p.hk = (p.hk + 1) / 2) {  // and as many heads of K a block
         p.k_parts = static_cast<unsigned>((c.Hk + p.hk - 1) / p.hk);

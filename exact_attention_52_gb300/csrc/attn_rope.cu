@@ -238,7 +238,7 @@ cudaError_t launch_rope_d(RopeParams p, cudaStream_t stream) {
     // As many heads a thread as leave every SM some blocks.
     for (p.hp = 8;; p.hp /= 2) {
         for (int i = 0; i < 2; ++i) p.chunks[i] = (p.heads[i] + HT * p.hp - 1) / (HT * p.hp);
-        if (p.hp == 1 || tiles * (p.chunks[0] + p.chunks[1]) >= 8ll * sms) break;
+        if (p.hp == 1 || tiles * (p.chunks[0] + p.chunks[1]) >= 3ll * sms) break;
     }
     const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(p.chunks[0] + p.chunks[1]));
     return p.r.interleaved ? launch_dependent(rope_kernel<D, true>, grid, kRopeThreads, 0, stream, p)
