@@ -621,6 +621,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             tc_fence_after();
             return ok;
         };
+        // One copy of the products' code for both groups: it competes for the instruction cache with the
+        // other roles' (2 x 2048 queries over 16384 keys 599 us for 611, 149 -> 131 with a window of 1023;
+        // d = 64, whose code is shorter, 488 with two copies and 499 with one).
+        constexpr int kRolled = D == 64 ? 2 : 1;
         // Every tile's full barrier is waited for, used or not: a phase that is skipped would
         // be taken for a later one.
         auto run_pair = [&](int a0, int a1, int steps) -> bool {
@@ -637,7 +641,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 // both before P's, off the chain: a look at a barrier takes 250-350 cycles while
                 // products run, and neither tile's slot waits for this step
                 if (!wait_kv(vi) || (j + 1 < steps && !wait_kv(vi + 1))) return false;
-#pragma unroll
+#pragma unroll kRolled
                 for (int g = 0; g < 2; ++g) {
                     const int a = g ? a1 : a0;
                     if (j >= a) continue;
@@ -777,11 +781,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                     for (int k = 0; k < 4; ++k) x[k] = *reinterpret_cast<const uint4*>(place((i0 + k) * RPI + sub));
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float amax = 0.f;
-                        for (uint32_t u : {x[k].x, x[k].y, x[k].z, x[k].w})
-                            amax = fmaxf(amax, fmaxf(fabsf(bf16lo(u)), fabsf(bf16hi(u))));
+                        // magnitudes of bf16 order as their bit patterns (a row with NaN is NaN whatever its power)
+                        uint32_t top = 0u;
+                        for (uint32_t u : {x[k].x, x[k].y, x[k].z, x[k].w}) top = __vmaxu2(top, u & 0x7FFF7FFFu);
+                        top = max(top >> 16, top & 0xFFFFu);
 #pragma unroll
-                        for (int o = 1; o < LPR; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const float amax = __uint_as_float(top << 16);
                         const float f = f16_row_scale(amax);
                         auto cv = [&](uint32_t u) { return pack_f16x2(bf16lo(u) * f, bf16hi(u) * f); };
                         x[k] = make_uint4(cv(x[k].x), cv(x[k].y), cv(x[k].z), cv(x[k].w));
