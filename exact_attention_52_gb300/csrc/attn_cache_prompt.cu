@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             int seq = PART == kPrefix ? group_begin(p, w.b) : w.b;
             auto first_tok = [&](int t) { return w.u.tile(t) * kTile + cw * 32; };
             // some query sees a token of the group from tok on
-            auto needed = [&](int tok) { return tok < len && (tok + 16 > key_lo || tok < p.sinks); };
+            auto needed = [&](int tok) { return tok < len && (PART == kPrefix || tok + 16 > key_lo || tok < p.sinks); };
             // Page numbers of both groups of 16 tiles at a time, lane 2i + g holding group g of
             // tile i, fetched 16 tiles before their use (shared memory leaves the L1 no room:
             // each look at the table goes to the L2).
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 for (int i = 0; i < 2; ++i) {
                     const int tok = tok0 + 16 * i;
                     const uint8_t* src = base + pid[i] * st.b + (tok & (p.c.page_size - 1)) * st.n;
-                    if (tok + 16 <= len && (tok >= key_lo || tok + 16 <= p.sinks)) {
+                    if (PART == kPrefix || (tok + 16 <= len && (tok >= key_lo || tok + 16 <= p.sinks))) {
 #pragma unroll
                         for (int k = 0; k < NI; ++k) buf[i * NI + k] = __ldg(reinterpret_cast<const uint4*>(src + k * RPI * st.n));
                     } else {
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         e4m3x4_to_f16(x.y, h[2], h[3]);
                         e4m3x4_to_f16(x.z, h[4], h[5]);
                         e4m3x4_to_f16(x.w, h[6], h[7]);
-                        if (values) {
+                        if (values && PART == kWhole) {  // (every row sees all of a prefix)
                             nan[0] |= (x.x & 0x7F7F7F7Fu) + 0x01010101u;
                             nan[1] |= (x.y & 0x7F7F7F7Fu) + 0x01010101u;
                             nan[2] |= (x.z & 0x7F7F7F7Fu) + 0x01010101u;
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 // A weight of 0 times NaN is NaN: right where every row sees the tile, and elsewhere
                 // NaN values stand as 0 in the products, and the rows that see one get it at the end
                 // of the segment.
-                if (values) {
+                if (values && PART == kWhole) {
                     if (__any_sync(0xffffffffu, ((nan[0] | nan[1] | nan[2] | nan[3]) & 0x80808080u) != 0u) &&
                         !w.u.all_see(t, p.left, p.sinks)) {
 #pragma unroll 1
@@ -820,7 +820,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 const int ti = dual ? 2 * j + g : j, tn = tile_no + ti;  // tile of the segment, and of all
                 const int kv0 = w.u.tile(w.v0 + ti) * kTile;
                 const int c_lo = key_min - kv0, c_hi = pos - kv0, c_sink = p.sinks - kv0;
-                const bool masked = __any_sync(0xffffffffu, (c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1);
+                const bool masked = PART == kWhole && __any_sync(0xffffffffu, (c_lo > 0 && c_sink < c_lo) || c_hi < kTile - 1);
                 const float4* sc = scales + (tn % T::SCALES) * 8;
                 if (!wait_in_line(b_sf, (s_seen + j) & 1, abort_flag, p.st, SITE_S_FULL)) return false;
                 tc_fence_after();
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                         float mx = u, sum = 0.f;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const bool seen = c + i <= c_hi && (c + i >= c_lo || c + i < c_sink);
+                            const bool seen = PART == kPrefix || (c + i <= c_hi && (c + i >= c_lo || c + i < c_sink));
                             x[i] = f2u(seen ? u2f(x[i]) * f : -INFINITY);
                             mx = fmaxf(mx, u2f(x[i]));
                         }
@@ -1031,7 +1031,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
             } else if (dual && g == 1) {
                 continue;  // the only tile was group 0's
             }
-            if (n > 0) {
+            if (n > 0 && PART == kWhole) {
                 // NaN values that the row sees in tiles that not every row sees (they stood as 0 in
                 // the products); by now both groups' products are done, so every value of the
                 // segment has been looked at.  Such tiles are seven a walk at most, however long
