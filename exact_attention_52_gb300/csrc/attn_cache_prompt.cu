@@ -230,13 +230,18 @@ __device__ PromptShare prompt_share(const CacheFwdParams& p, int pairs, PromptSh
     return s;
 }
 
-// The same for the prefixes' launch, by each warp for itself, without a barrier.
+// The same for the prefixes' launch, by each warp for itself, without a barrier; a group's units are
+// numbered as if each had as many as all rows fill.
 __device__ __forceinline__ PromptShare prefix_share(const CacheFwdParams& p, int pairs) {
-    const int lane = threadIdx.x & 31, units = p.groups * pairs, per = (units + 31) >> 5;
-    const int u0 = min(units, lane * per), u1 = min(units, u0 + per);
-    auto work = [&](int u) { return static_cast<long long>(unit_of<kPrefix>(p, u / pairs, u % pairs).n) * p.Hk; };
+    const int lane = threadIdx.x & 31, per = (p.groups + 31) >> 5;
+    const int g0 = min(p.groups, lane * per), g1 = min(p.groups, g0 + per);
+    auto unit_work = [&](const PromptUnit& u) { return static_cast<long long>(u.n) * p.Hk; };
+    auto work = [&](int g) {
+        const PromptUnit u = unit_of<kPrefix>(p, g, 0);
+        return unit_work(u) * ((u.rows + kPairRows - 1) / kPairRows);
+    };
     long long mine = 0;
-    for (int u = u0; u < u1; ++u) mine += work(u);
+    for (int g = g0; g < g1; ++g) mine += work(g);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -251,10 +256,13 @@ __device__ __forceinline__ PromptShare prefix_share(const CacheFwdParams& p, int
     long long before = incl - mine;
     int found = -1;
     if (s.x < total && before <= s.x && s.x < incl) {
-        for (int u = u0; u < u1; ++u) {
-            const long long w = work(u);
+        for (int g = g0; g < g1; ++g) {
+            const long long w = work(g);
             if (s.x < before + w) {
-                found = u;
+                const long long each = unit_work(unit_of<kPrefix>(p, g, 0));
+                const int pair = static_cast<int>(div_mostly32(s.x - before, each));
+                found = g * pairs + pair;
+                before += pair * each;
                 break;
             }
             before += w;
@@ -286,7 +294,8 @@ __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, PromptWalk
     w.u = unit_of<PART>(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
     for (long long n; w.s.x >= w.s.unit_first + (n = static_cast<long long>(w.u.n) * p.Hk);) {
         w.s.unit_first += n;
-        ++w.s.unit;
+        // (the units of a group behind its last rows are passed over at once)
+        w.s.unit = PART == kPrefix && n == 0 ? (w.s.unit / w.pairs + 1) * w.pairs : w.s.unit + 1;
         w.u = unit_of<PART>(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
     }
     w.b = w.s.unit / w.pairs;

@@ -107,6 +107,21 @@ def test_long_prefix():
     run(pool, 8, 1, [0, 6], [19999], lens, None)
 
 
+def test_many_groups():
+    """Groups of a few sequences each among many rows, some of them empty or with nothing shared."""
+    rng = np.random.default_rng(21)
+    B, T = 60, 4
+    cuts = sorted(int(x) for x in rng.integers(0, B + 1, 25))
+    firsts = [0] + cuts + [B]
+    prefixes = [int(x) for x in rng.choice([0, 128, 256, 300, 700], len(firsts) - 1)]
+    lens = [0] * B
+    for g, n in enumerate(prefixes):
+        for b in range(firsts[g], firsts[g + 1]):
+            lens[b] = n + T + int(rng.integers(0, 90))
+    pool = shared_pool(22, B, 2, 64, 32, firsts, prefixes, lens)
+    run(pool, 32, T, firsts, prefixes, lens, [int(x) for x in rng.integers(0, T + 1, B)])
+
+
 @pytest.mark.parametrize("T", [1, 15, 40])
 def test_a_slot_without_queries_may_hold_any_table(T):
     """The first sequence of a group that has queries stands for it; tables of the others are not read."""
