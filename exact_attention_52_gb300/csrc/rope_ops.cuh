@@ -29,7 +29,8 @@ __device__ __forceinline__ void rope_pieces(int t, int nrot, int& lo, int& hi) {
 // Cosines and sines (times f) of the 8 pairs of thread t at a position: pairs 8t .. 8t + 7 in
 // either layout.  The table holds theta_i in units of 2^-64 turns, and a position times that,
 // modulo 2^64, is the angle within its turn without any error but the table's (2^-65 turns a
-// position): nothing is lost far out.  Its upper 32 bits go to fp32 (2^-25 of half a turn).
+// position): nothing is lost far out.  What it is off the nearest quarter turn, at most pi / 4, goes
+// to fp32 (2^-25 of it).
 struct RopeAngles {
     float c[8], s[8];
     __device__ __forceinline__ void at(const RopeView& r, int t, int pos, float sign) {
@@ -40,10 +41,14 @@ struct RopeAngles {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(pos)) * (e ? w.y : w.x);
+                const unsigned quarter = (static_cast<unsigned>(a >> 32) + (1u << 29)) >> 30;  // 0 .. 3; 4 of 4 is 0
+                const int off = static_cast<int>(static_cast<long long>(a - (static_cast<unsigned long long>(quarter) << 62)) >> 30);
                 float sn, cs;
-                sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f, &sn, &cs);
-                c[2 * i + e] = cs * r.factor;
-                s[2 * i + e] = sn * (r.factor * sign);
+                sincospif(static_cast<float>(off) * 0x1p-33f, &sn, &cs);  // off: 2^-34 turns
+                const float x = quarter & 1u ? -sn : cs, y = quarter & 1u ? cs : sn;
+                const float f = quarter & 2u ? -r.factor : r.factor;
+                c[2 * i + e] = x * f;
+                s[2 * i + e] = y * (f * sign);
             }
         }
     }

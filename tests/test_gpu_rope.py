@@ -1,8 +1,8 @@
 """attn_rope, attn_rope_bwd and attn_cache_append_rope against the fp64 oracle.
 
-Tolerances.  A cosine or sine is off by at most 2^-22.3: the angle's upper 32 bits go to fp32 (half
-a step of a number up to 1, 2^-25, times pi), the function and the factor add a step each (2^-24 of
-at most 1, twice).  A normed element is off by 2^-21 of itself: the sum of up to 128 squares in a
+Tolerances.  A cosine or sine is off by at most 2^-22.3: the angle off the nearest quarter turn goes
+to fp32 (2^-25 of at most pi / 4), the function and the factor add a step each (2^-24 of at most 1,
+twice).  A normed element is off by 2^-21 of itself: the sum of up to 128 squares in a
 tree (2^-24 times 12 additions, halved by the square root), the inverse root (two steps) and two
 products.  So a rotated element is off by e = 2^-20 (|n1| + |n2|) f before it is rounded to bf16,
   |y - ref| <= e + 2^-8 (|ref| + e);
