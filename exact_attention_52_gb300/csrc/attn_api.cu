@@ -694,14 +694,17 @@ attn_status cache_whole(CacheFwdParams* p, void* workspace, attn_stream_t stream
 
 // Whether a batch behind shared prefixes is done in two parts, the prefixes for their groups and the
 // rest, or like any other.  Prompts are bound by their products, which sharing does not lessen (2 x
-// 2048 queries behind 16384 tokens: 1.32 ms in two parts, 0.93 in one); and keys of a small cache
-// come out of the L2 again sooner than the two parts' launches take: in one part 4 x 2300 tokens, 8
-// heads, d = 128 (19 MB) take 14 us for 22, 48 x 4600, 4 heads, d = 64 (113 MB) 30 for 40; 64 x 9200,
-// 8 heads, d = 128 (1.2 GB) 121 for 70.  The lengths are on the device; the longest that the table can
-// hold stands for them.
+// 2048 queries behind 16384 tokens: 1.32 ms in two parts, 0.93 in one).  Keys of a small cache come
+// out of the L2 again sooner than the two parts' launches take, and the kernel of the prefixes takes a
+// key in the time in which the other one reads it five times.  One part and two, 8 heads, d = 128,
+// 300 tokens of their own: 8 x 4096 tokens (68 MB) 18 and 29 us, 32 x 4096 (274) 37 and 34, 8 x 16384
+// (260) 33 and 37, 32 x 16384 108 and 41, 128 x 16384 412 and 89; 2 x 65536 (257) 42 and 76, 8 x 65536
+// 99 and 78.  The lengths are on the device; the longest that the table can hold stands for them.
 constexpr long long kPrefixMinBytes = 256ll << 20;
-bool prefix_parts(const attn_cache_t* c, int B, int H, int Hk, int T, int d) {
-    return !cache_prompt(H, Hk, T) && 2ll * d * Hk * B * c->max_pages * c->page_size >= kPrefixMinBytes;
+constexpr int kPrefixMinMembers = 6;  // sequences of a group, on average
+bool prefix_parts(const attn_cache_t* c, int groups, int B, int H, int Hk, int T, int d) {
+    return !cache_prompt(H, Hk, T) && B / groups >= kPrefixMinMembers &&
+           2ll * d * Hk * B * c->max_pages * c->page_size >= kPrefixMinBytes;
 }
 
 // Of each of the two parts the unfinished segments, the items' CTAs, and the rows of items that one
@@ -1165,7 +1168,7 @@ attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* grou
     if (rc != ATTN_OK) return rc;
     if (groups < 1 || groups > B || (group_first == nullptr && groups != 1) || prefix_lens == nullptr) return ATTN_ERR_INVALID;
     if (((reinterpret_cast<uintptr_t>(group_first) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3u) != 0) return ATTN_ERR_INVALID;
-    if (!prefix_parts(cache, B, H, Hk, T, d)) return cache_whole(&p, workspace, stream);
+    if (!prefix_parts(cache, groups, B, H, Hk, T, d)) return cache_whole(&p, workspace, stream);
     // rows of all sequences of a key/value head, and their pairs of query tiles in each group
     const long long rows = static_cast<long long>(B) * T * (H / Hk);
     if (rows > (1 << 30) || groups * ((rows + kPromptRows - 1) / kPromptRows) > (1 << 30)) return ATTN_ERR_INVALID;

@@ -477,9 +477,10 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
  * Every query has to stand behind its group's prefix.  A sequence with queries whose seq_lens[b] -
  * q_lens[b] is smaller (but for the last prefix_lens % 128 tokens) has undefined rows, and it, or a
  * prefix length outside the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE.
- * Where sharing does not pay -- prompts (T * H / Hk above 64), and caches of which the table can
- * hold less than 256 MB -- the call is attn_fwd_cache: it does not look at groups and prefixes,
- * and those errors do not occur.  Otherwise three launches.  Errors as attn_fwd_cache.
+ * Where sharing does not pay -- prompts (T * H / Hk above 64), groups of fewer than six sequences
+ * on average, and caches of which the table can hold less than 256 MB -- the call is
+ * attn_fwd_cache: it does not look at groups and prefixes, and those errors do not occur.
+ * Otherwise three launches.  Errors as attn_fwd_cache.
  * Source: ai.engineer item 59 (small-query work split across thread blocks plus a separate
  * combining kernel); no page describes shared prefixes.
  */

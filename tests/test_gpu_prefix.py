@@ -2,8 +2,9 @@
 shared pages.  Tolerances are those of the cache attention (test_gpu_cache): joining the two parts
 adds a few fp32 roundings, 2^-22 of the sums, to the 2^-15 that scores and exponentials have.
 
-A call works in two parts where the table can hold 256 MB; here tables are as wide as that needs,
-the entries behind the sequences' own holding no page, or as narrow as the sequences are."""
+A call works in two parts where groups have six sequences on average and the table can hold 256 MB;
+here tables are as wide as that needs, the entries behind the sequences' own holding no page, or as
+narrow as the sequences are."""
 
 import numpy as np
 import pytest
@@ -71,17 +72,19 @@ def run_with(pool, H, T, firsts, prefixes, lens, q_lens, layout="bhnd", amp=1.0,
 # (B, H, Hk, T, page, group_first, prefix_lens, seq_lens, q_lens)
 SHAPES = [
     (1, 1, 1, 1, 16, [0, 1], [128], [129], None),
-    (1, 4, 4, 1, 64, [0, 1], [0], [1], None),
-    (2, 8, 2, 1, 16, [0, 2], [127], [128, 300], None),               # shorter than a tile: read for each sequence
-    (3, 8, 2, 1, 64, [0, 3], [300], [301, 500, 333], None),          # not a whole tile, nor a whole page
-    (4, 6, 2, 3, 32, [0, 4], [512], [515, 700, 0, 900], [3, 2, 0, 1]),
-    (5, 4, 1, 1, 128, [0, 2, 2, 5], [256, 128, 1280], [300, 257, 1281, 1400, 2000], None),  # an empty group
-    (6, 4, 2, 2, 16, [1, 3, 4], [128, 384], [50, 130, 140, 500, 2, 3], [2, 2, 2, 2, 2, 2]),  # sequences of no group
+    (6, 1, 1, 1, 16, [0, 6], [128], [129, 129, 130, 128 + 16, 300, 129], None),
+    (6, 4, 4, 1, 64, [0, 6], [0], [1, 2, 64, 65, 300, 7], None),
+    (7, 8, 2, 1, 16, [0, 7], [127], [128, 300, 129, 128, 200, 512, 140], None),   # shorter than a tile: read for each sequence
+    (6, 8, 2, 1, 64, [0, 6], [300], [301, 500, 333, 301, 320, 1000], None),       # not a whole tile, nor a whole page
+    (6, 6, 2, 3, 32, [0, 6], [512], [515, 700, 0, 900, 514, 512 + 33], [3, 2, 0, 1, 2, 3]),
+    (19, 4, 1, 1, 128, [0, 4, 4, 19], [256, 128, 1280], [257 + 9 * i for i in range(4)] + [1281 + 50 * i for i in range(15)], None),  # an empty group
+    (14, 4, 2, 2, 16, [1, 3, 12], [128, 384], [50, 130, 140] + [386 + 7 * i for i in range(9)] + [2, 3], [2] * 14),  # sequences of no group
     (9, 40, 2, 1, 1024, [0, 9], [2048], [2048 + 3 * i + 1 for i in range(9)], None),
-    (40, 32, 4, 1, 64, [0, 40], [640], [641 + 7 * i for i in range(40)], None),               # more than one pair of query tiles
-    (3, 8, 2, 16, 32, [0, 3], [256], [256 + 16, 700, 300], [16, 13, 1]),                      # as many rows as the part kernels take
-    (2, 5, 1, 12, 16, [0, 2], [1024], [1036, 1999], None),
-    (3, 8, 2, 40, 32, [0, 3], [256], [256 + 40, 700, 300], [40, 33, 1]),                      # prompts behind a prefix: one part
+    (40, 32, 4, 1, 64, [0, 40], [640], [641 + 7 * i for i in range(40)], None),   # more than one pair of query tiles
+    (6, 8, 2, 16, 32, [0, 6], [256], [256 + 16, 700, 300, 272, 280, 256], [16, 13, 1, 16, 9, 0]),  # as many rows as the part kernels take
+    (8, 5, 1, 12, 16, [0, 8], [1024], [1036 + 120 * i for i in range(8)], None),
+    (5, 4, 1, 1, 128, [0, 2, 2, 5], [256, 128, 1280], [300, 257, 1281, 1400, 2000], None),    # few in a group: one part
+    (3, 8, 2, 40, 32, [0, 3], [256], [256 + 40, 700, 300], [40, 33, 1]),                      # prompts: one part
     (4, 5, 1, 100, 64, [0, 2, 4], [900, 256], [1000, 1300, 356, 999], [100, 0, 100, 71]),
 ]
 
@@ -97,8 +100,9 @@ def test_prefix_matches_oracle(shape, layout, d):
 
 @pytest.mark.parametrize("T", [1, 14, 30])
 def test_one_group_by_default_and_a_scale(T):
-    pool = shared_pool(3, 4, 2, 128, 32, [0, 4], [384], [500, 600, 414, 900])
-    run(pool, 8, T, None, [384], [500, 600, 414, 900], None, scale=0.3, amp=2.0)
+    lens = [500, 600, 414, 900, 450, 417]
+    pool = shared_pool(3, 6, 2, 128, 32, [0, 6], [384], lens)
+    run(pool, 8, T, None, [384], lens, None, scale=0.3, amp=2.0)
 
 
 def test_long_prefix():
@@ -111,7 +115,7 @@ def test_many_groups():
     """Groups of a few sequences each among many rows, some of them empty or with nothing shared."""
     rng = np.random.default_rng(21)
     B, T = 60, 4
-    cuts = sorted(int(x) for x in rng.integers(0, B + 1, 25))
+    cuts = sorted(int(x) for x in rng.integers(0, B + 1, 9))
     firsts = [0] + cuts + [B]
     prefixes = [int(x) for x in rng.choice([0, 128, 256, 300, 700], len(firsts) - 1)]
     lens = [0] * B
@@ -125,64 +129,67 @@ def test_many_groups():
 @pytest.mark.parametrize("T", [1, 15, 40])
 def test_a_slot_without_queries_may_hold_any_table(T):
     """The first sequence of a group that has queries stands for it; tables of the others are not read."""
-    lens, ql = [0, 500, 700, 0], [0, T, T, 0]
-    pool = shared_pool(5, 4, 2, 64, 16, [0, 4], [384], [500, 500, 700, 0])
+    lens, ql = [0, 500, 700, 0, 450, 431], [0, T, T, 0, T, 1]
+    pool = shared_pool(5, 6, 2, 64, 16, [0, 6], [384], lens)
     junk = pool.table.copy()
     junk[0], junk[3] = 10 ** 6, -5
-    run(pool, 4, T, [0, 4], [384], lens, ql, table=junk)
+    run(pool, 4, T, [0, 6], [384], lens, ql, table=junk)
 
 
 def test_a_group_without_queries():
-    lens, ql = [0, 0, 300], [0, 0, 1]
-    pool = shared_pool(6, 3, 2, 128, 16, [0, 2, 3], [128, 256], [128, 128, 300])
+    lens, ql = [0, 0] + [257 + 20 * i for i in range(10)], [0, 0] + [1] * 10
+    pool = shared_pool(6, 12, 2, 128, 16, [0, 2, 12], [128, 256], lens)
     junk = pool.table.copy()
     junk[:2] = 10 ** 6
-    run(pool, 4, 1, [0, 2, 3], [128, 256], lens, ql, table=junk)
+    run(pool, 4, 1, [0, 2, 12], [128, 256], lens, ql, table=junk)
 
 
 @pytest.mark.parametrize("T", [1, 15, 40])
 @pytest.mark.parametrize("where", ["prefix", "rest", "both"])
 def test_value_scales_far_apart(where, T):
     """Parts whose sums are taken apart join with parts whose sums are not."""
-    lens = [400, 512, 700]
-    pool = shared_pool(8, 3, 2, 128, 64, [0, 3], [256], lens)
-    for b in range(3):
+    lens = [400, 512, 700, 333, 296, 450]
+    pool = shared_pool(8, 6, 2, 128, 64, [0, 6], [256], lens)
+    for b in range(6):
         for pg in range(pool.table.shape[1]):
             if where == "both" or (pg < 4) == (where == "prefix"):
                 pool.vs[pool.table[b, pg]] = 2.0 ** (-100 if (b + pg) % 2 or pg < 4 else 60)
-    run(pool, 4, T, [0, 3], [256], lens, None)
+    run(pool, 4, T, [0, 6], [256], lens, None)
 
 
 @pytest.mark.parametrize("T", [1, 15, 40])
 def test_nan_values_reach_the_rows_that_see_them(T):
-    lens = [300, 400]
+    lens = [300, 400, 310, 297, 500, 450]
     for pg, col in ((1, 3), (None, 5)):  # in the prefix; behind the second sequence's last token
-        pool = shared_pool(9, 2, 1, 64, 64, [0, 2], [256], lens)
+        pool = shared_pool(9, 6, 1, 64, 64, [0, 6], [256], lens)
         if pg is not None:
             pool.v[pool.table[0, pg], 0, 10, col] = 0x7F
         else:
             pool.v[pool.table[1, 400 // 64], 0, 400 % 64, col] = 0x7F
             pool.k[pool.table[1, 400 // 64], 0, 400 % 64, col] = 0xFF
-        run(pool, 4, T, [0, 2], [256], lens, None)
+        run(pool, 4, T, [0, 6], [256], lens, None)
 
 
 def test_lengths_that_do_not_fit_are_reported():
     import torch
-    pool = shared_pool(10, 3, 2, 64, 16, [0, 3], [256], [300, 300, 300])
-    q = torch.randn(3, 4, 2, 64, device="cuda").bfloat16()
+    pool = shared_pool(10, 6, 2, 64, 16, [0, 6], [256], [300] * 6)
+    q = torch.randn(6, 4, 2, 64, device="cuda").bfloat16()
     dev, narrow = pool.dev(), pool.dev()
     dev[4] = i32(wide(pool.table, pool))
-    call = lambda dev, lens=(300, 290, 280), prefix=256: api.fwd_cache_prefix(q, *dev, i32(lens), i32([prefix]))
+    good = [300, 290, 280, 258, 300, 270]
+    call = lambda dev, lens=good, prefix=256: api.fwd_cache_prefix(q, *dev, i32(lens), i32([prefix]))
     call(dev)
     check_clean()
-    for lens in ([300, 257, 280], [300, 0, 280]):
+    for short in (257, 2, 0):
+        lens = good[:1] + [short] + good[2:]
         call(dev, lens)
         assert api.check_device_error()[0] == -5
         # in one part the prefix says nothing
         got, ref = call(narrow, lens), api.fwd_cache(q, *narrow, i32(lens))
         check_clean()
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
-    for kw in (dict(lens=[300, -7, 280]), dict(lens=[300, 2 ** 30, 280]), dict(prefix=2 ** 30), dict(prefix=-1)):
+    for kw in (dict(lens=[300, -7, 280, 270, 300, 290]), dict(lens=[300, 2 ** 30, 280, 270, 300, 290]), dict(prefix=2 ** 30),
+               dict(prefix=-1)):
         call(dev, **kw)
         assert api.check_device_error()[0] == -5, kw
     bad = pool.table.copy()
@@ -195,11 +202,11 @@ def test_lengths_that_do_not_fit_are_reported():
 def test_captured_calls_follow_their_lengths():
     """Lengths, prefixes and groups stay on the device; two captured calls have workspaces of their own."""
     import torch
-    pool = shared_pool(11, 4, 2, 128, 64, [0, 4], [512], [600] * 4)
+    pool = shared_pool(11, 12, 2, 128, 64, [0, 12], [512], [600] * 12)
     dev = pool.dev()
     dev[4] = i32(wide(pool.table, pool))
-    q = torch.randn(4, 8, 1, 128, device="cuda").bfloat16()
-    seq, pre, first = i32([520, 530, 540, 550]), i32([512, 512]), i32([0, 2, 4])
+    q = torch.randn(12, 8, 1, 128, device="cuda").bfloat16()
+    seq, pre, first = i32([520 + 4 * i for i in range(12)]), i32([512, 512]), i32([0, 5, 12])
     call = lambda: api.fwd_cache_prefix(q, *dev, seq, pre, group_first=first)
     call()
     graphs = []
@@ -221,7 +228,7 @@ def test_captured_calls_follow_their_lengths():
             assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
         seq += 9
         pre.copy_(i32([256, 384]))
-        first.copy_(i32([0, 3, 4]))
+        first.copy_(i32([0, 7, 12]))
     check_clean()
     s.wait_stream(torch.cuda.current_stream())
     o, lse = api.fwd_cache_prefix(q, *dev, seq, pre, group_first=first, stream=s)
@@ -232,9 +239,9 @@ def test_captured_calls_follow_their_lengths():
 
 def test_decoding_behind_a_shared_prompt():
     """The operators as they are used: a prompt written and rotated once, then steps of a few tokens
-    of three sequences behind it, each written, rotated and attended in two calls."""
+    of six sequences behind it, each written, rotated and attended in two calls."""
     import torch
-    B, H, Hk, d, page, prompt = 3, 8, 2, 128, 32, 320
+    B, H, Hk, d, page, prompt = 6, 8, 2, 128, 32, 320
     rng = np.random.default_rng(12)
     pool = shared_pool(12, B, Hk, d, page, [0, B], [prompt], [prompt + 40] * B)
     dev, table = pool.dev(), table_of(64)
@@ -248,7 +255,7 @@ def test_decoding_behind_a_shared_prompt():
     lens = np.full(B, prompt)
     for step in range(12):
         T = 1 + step % 3
-        m = [T, (step + 1) % (T + 1), T]
+        m = [T, (step + 1) % (T + 1), T, T, step % (T + 1), T]
         lens = lens + m
         q, k, v = new(B, T, H), new(B, T, Hk), new(B, T, Hk)
         seq, nl = i32(lens), i32(m)
