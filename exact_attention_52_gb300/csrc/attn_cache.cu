@@ -930,13 +930,14 @@ struct CacheMergeParams {
     CacheFwdParams rest;
     MergePart parts[2];  // the prefixes', the rest's
 };
+constexpr int kMergeWarps = 2;
 template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) cache_merge_kernel(const CacheMergeParams m) {
-    constexpr int E = 8, LPR = D / E, S = 32 / LPR, U = 4;  // LPR lanes a segment, S segments at a time, U of those out
+__global__ void __launch_bounds__(32 * kMergeWarps) cache_merge_kernel(const CacheMergeParams m) {
+    constexpr int E = 8, LPR = D / E, S = 32 / LPR, U = 8;  // LPR lanes a segment, S segments at a time, U of those out
     const int lane = threadIdx.x & 31, col = lane % LPR * E;
     const CacheFwdParams& p = m.rest;
     const int G = p.H / p.Hk;
-    const long long row = static_cast<long long>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
     const bool in = row < static_cast<long long>(p.B) * p.T * p.H;
     const long long bt = in ? div_mostly32(row, p.H) : 0;
     const int h = in ? static_cast<int>(row - bt * p.H) : 0, b = static_cast<int>(div_mostly32(bt, p.T));
@@ -1049,13 +1050,13 @@ cudaError_t launch_cache_join(const CacheFwdParams& p, int blocks, cudaStream_t 
 }
 
 cudaError_t launch_cache_merge(const CacheFwdParams& prefix, const CacheFwdParams& rest, cudaStream_t stream) {
-    const long long blocks = (static_cast<long long>(rest.B) * rest.T * rest.H + kJoinWarps - 1) / kJoinWarps;
+    const long long blocks = (static_cast<long long>(rest.B) * rest.T * rest.H + kMergeWarps - 1) / kMergeWarps;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>(blocks));
     auto part = [](const CacheFwdParams& p) { return MergePart{p.items, p.part, p.fin_o, p.stat, p.fin_stat, p.rows}; };
     const CacheMergeParams m{rest, {part(prefix), part(rest)}};
-    if (rest.D == 64) return launch_dependent(cache_merge_kernel<64>, grid, 32 * kJoinWarps, 0, stream, m);
-    if (rest.D == 128) return launch_dependent(cache_merge_kernel<128>, grid, 32 * kJoinWarps, 0, stream, m);
+    if (rest.D == 64) return launch_dependent(cache_merge_kernel<64>, grid, 32 * kMergeWarps, 0, stream, m);
+    if (rest.D == 128) return launch_dependent(cache_merge_kernel<128>, grid, 32 * kMergeWarps, 0, stream, m);
     return cudaErrorInvalidValue;
 }
 
