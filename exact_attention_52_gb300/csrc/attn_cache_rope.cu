@@ -190,7 +190,10 @@ __device__ __forceinline__ void rotate_queries(const CacheAppendRopeParams& p, i
 }
 
 // Blocks [0, k_blocks): a touched page of a sequence and p.hk heads of K; [k_blocks, page_blocks): one
-// and a head of V; the others: tokens and heads of Q.
+// and a head of V; the others: tokens and heads of Q.  Bound by the memory: 4 prompts of up to 8192
+// tokens, 32/8 heads, d = 128, norms: 92 us, 5.4 TB/s (angles worked out for each head of K and Q's
+// loads in registers: 109); one token for 32 sequences 4.9 us in a row, the chain length, table, page,
+// scale.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_rope_kernel(const CacheAppendRopeParams p) {
     __shared__ union Shared {

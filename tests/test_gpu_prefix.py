@@ -237,6 +237,28 @@ def test_captured_calls_follow_their_lengths():
     assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
 
+def test_two_calls_at_once():
+    """Calls on two streams, each with the workspace kept for its stream."""
+    import torch
+    pool = shared_pool(31, 8, 2, 128, 64, [0, 8], [1024], [1100 + 9 * i for i in range(8)])
+    dev = pool.dev()
+    dev[4] = i32(wide(pool.table, pool))
+    lens, pre = i32([1100 + 9 * i for i in range(8)]), i32([1024])
+    qs = [torch.randn(8, 16, 2, 128, device="cuda").bfloat16() for _ in range(2)]
+    call = lambda q: api.fwd_cache_prefix(q, *dev, lens, pre)
+    ref = [call(q) for q in qs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = call(qs[i])
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check_clean()
+
+
 def test_decoding_behind_a_shared_prompt():
     """The operators as they are used: a prompt written and rotated once, then steps of a few tokens
     of six sequences behind it, each written, rotated and attended in two calls."""

@@ -201,6 +201,43 @@ def test_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(o, new))
 
 
+def test_two_calls_at_once():
+    """Calls on two streams have workspaces of their own."""
+    import torch
+    B, H, Hk, N, d = 1, 8, 2, 3001, 128
+    w, table, streams = torch.rand(d, device="cuda") + 0.5, table_of(128), [torch.cuda.Stream() for _ in range(2)]
+    data = [[torch.randn(B, x, N, d, device="cuda").bfloat16() for x in (H, Hk, H, Hk)] for _ in streams]
+    call = lambda q, k, gq, gk: api.rope_bwd(gq, gk, table, q=q, k=k, q_weight=w, k_weight=w)
+    ref = [call(*x) for x in data]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = call(*data[i])
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_offsets_past_32_bits():
+    """Heads 2^32 elements apart, and an output whose tokens are far apart."""
+    import torch
+    far = (1 << 32) + 64
+    room = torch.zeros(far + 40 * 64, dtype=torch.bfloat16, device="cuda")
+    x = torch.randn(1, 2, 33, 64, device="cuda").bfloat16()
+    view = room.as_strided((1, 2, 33, 64), (8, far, 64, 1))
+    view.copy_(x)
+    w, table = torch.rand(64, device="cuda") + 0.5, table_of(32)
+    ref = api.rope(x, x, table, q_weight=w)
+    got = api.rope(view, x, table, q_weight=w, k_out=room.as_strided((1, 2, 33, 64), (8, 64 * 40, 64, 1), (1 << 31) + 8))
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    g = torch.randn_like(x)
+    ref = api.rope_bwd(g, None, table, q=x, q_weight=w)
+    got = api.rope_bwd(g, None, table, q=view, q_weight=w, dq=view)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[2], ref[2])
+
+
 # ---------------------------------------------------------------------------
 # The cache's write
 # ---------------------------------------------------------------------------
@@ -280,6 +317,8 @@ APPENDS = [
     (1, 5, 1, 131, 128, [333], None),            # tokens of a page beyond those held in registers
     (2, 3, 3, 600, 1024, [700, 2000], [600, 599]),
     (1, 4, 2, 300, 256, [300], None),
+    (2, 5, 3, 20, 32, [50, 20], [20, 17]),       # query heads need not be shared evenly
+    (1, 9, 5, 700, 64, [1000], [700]),           # several heads of K a block, not a multiple of them
 ]
 
 
@@ -300,6 +339,25 @@ def test_append_where_scales_grow_and_vanish():
     for amp in (1e4, 1e-4, 1e-38):
         pool = Pool(7, 2, 2, 128, 16, 4)
         run_append(pool, 4, 5, [21, 40], [5, 4], 128, False, "", amp=amp)
+
+
+def test_append_through_a_wider_table():
+    """A table that is a part of a wider one, and new tokens that are slices of a packed projection."""
+    import torch
+    pool = Pool(17, 3, 2, 64, 32, 4)
+    dev, ref = pool.dev(), pool.dev()
+    outer = torch.full((3, 9), -1, dtype=torch.int32, device="cuda")
+    outer[:, 2:6] = dev[4]
+    dev[4] = outer[:, 2:6]
+    packed = torch.randn(3, 5, 4 + 2 + 2, 64, device="cuda").bfloat16()
+    q, k, v = packed[:, :, :4], packed[:, :, 4:6], packed[:, :, 6:]
+    w, lens = torch.rand(64, device="cuda") + 0.5, i32([40, 128, 5])
+    want = api.cache_append_rope(q.contiguous(), k.contiguous(), v.contiguous(), table_of(48, True), *ref, lens, q_weight=w,
+                                 k_weight=w, layout="bnhd")
+    got = api.cache_append_rope(q, k, v, table_of(48, True), *dev, lens, q_weight=w, k_weight=w, layout="bnhd", q_out=q)
+    check_clean()
+    assert torch.equal(got, want) and got.data_ptr() == q.data_ptr()
+    assert all(torch.equal(x, y) for x, y in zip(dev[:4], ref[:4]))
 
 
 def test_append_of_values_that_are_not_finite():

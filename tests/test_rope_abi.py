@@ -8,6 +8,7 @@ import pytest
 
 from exact_attention_52_gb300 import api
 
+from .test_compiled_calls import CALLS, module  # noqa: F401
 
 @pytest.fixture(scope="module")
 def lib():
@@ -93,3 +94,15 @@ def test_a_bad_prefix_is_refused(lib):
                 + seg(1) + r256(B * Hk * ((T * G + 7) // 8) * 8) + fin)
         assert sizes(B, H, Hk, T, 128) == want
     assert sizes(3, 40, 2, 70, 128) == lib.attn_fwd_cache_workspace_bytes(3, 40, 2, 70, 128)  # prompts
+
+
+def test_the_compiled_half_gives_back_what_it_does_not_take(module):
+    import torch
+    functions = ((module.rope, 14), (module.rope_bwd, 19), (module.cache_append_rope, 20), (module.fwd_cache_prefix, 17))
+    q = torch.zeros(1, 2, 4, 64).bfloat16()
+    for f, n in functions:
+        for t in (q, None, 3, "x", q.float(), q[0], torch.zeros(0)):
+            assert f(*[t] * (n - 2), 0, 0) is None
+        for m in (0, 1, n - 1, n + 1):
+            assert f(*[None] * m) is None
+    assert not CALLS
