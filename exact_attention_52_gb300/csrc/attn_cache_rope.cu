@@ -12,12 +12,14 @@
 namespace attn {
 namespace {
 
-// A thread's angles of its held tokens, in shared memory (a place of its own): 32 KB a block; and the
-// head's weights, in the order of the pieces that its threads hold.
-constexpr int kHeld = 4;
+// Tokens of a page go by rounds of kAppendThreads / (D / 16), one a thread and round.  The first
+// kHeld rounds' rotated elements stay in registers and their angles in shared memory (a place for each
+// thread, 8 KB a round), for all of a block's up to kPageHeads heads.  (Room for the angles of eight
+// rounds leaves an SM three blocks: pages of 128 tokens at d = 128, 133 us for 115.)
+constexpr int kHeld = 4, kPageHeads = 8;
 struct KeyShared {
+    float4 weight[4][8];  // the head's, in the order of the pieces that its threads hold
     float4 at[kHeld][4][kAppendThreads];
-    float4 weight[4][8];
     __device__ __forceinline__ void put_weight(const RopeView& r, int t, int row, int lo, int hi) {
         if (row != 0) return;
         float w[16];
@@ -41,11 +43,9 @@ struct KeyShared {
         }
     }
 };
-
 // K of the page of AppendPage a, heads [hk, hk_end): rotated in fp32 and rounded once, to E4M3.  A
-// thread holds 16 elements of its tokens as fp32 between the two looks at them, and their angles for
-// all heads; tokens beyond the ones held (pages of more than 64 tokens at d = 128, 128 at d = 64)
-// are read and rotated again.
+// thread holds 16 elements of its tokens as fp32 between the two looks at them; tokens beyond the ones
+// held (pages of more than 64 tokens at d = 128, 128 at d = 64) are read and rotated again.
 template <int D, bool INTER>
 __device__ __forceinline__ void append_rotated(const CacheAppendRopeParams& p, const AppendPage& a, int b, int hk, int hk_end,
                                                KeyShared& sm) {
@@ -96,7 +96,7 @@ __device__ __forceinline__ void append_rotated(const CacheAppendRopeParams& p, c
             if (h == hk) {  // while those are on their way
                 if (norm) sm.put_weight(p.r, t, rr, lo, hi);
 #pragma unroll 1
-                for (int k = 0; k < kHeld; ++k) {
+                for (int k = 0; k < kHeld && k * RPP < n; ++k) {
                     RopeAngles ang;
                     if (rr + k * RPP < n && t < nrot) {
                         ang.at(p.r, t, a.lo + rr + k * RPP, 1.f);
@@ -108,7 +108,7 @@ __device__ __forceinline__ void append_rotated(const CacheAppendRopeParams& p, c
 #pragma unroll
             for (int k = 0; k < kHeld; ++k) {  // (zeros stay zeros)
                 unpack16(l[k], u[k], held[k]);
-                turn(held[k], rr + k * RPP < n && t < nrot, [&](RopeAngles& ang) { sm.get(k, ang); });
+                if (k * RPP < n) turn(held[k], rr + k * RPP < n && t < nrot, [&](RopeAngles& ang) { sm.get(k, ang); });
             }
         }
         // Rounds of further tokens are the same for every thread: a norm's sum takes several.
@@ -190,10 +190,11 @@ __device__ __forceinline__ void rotate_queries(const CacheAppendRopeParams& p, i
 }
 
 // Blocks [0, k_blocks): a touched page of a sequence and p.hk heads of K; [k_blocks, page_blocks): one
-// and a head of V; the others: tokens and heads of Q.  Bound by the memory: 4 prompts of up to 8192
-// tokens, 32/8 heads, d = 128, norms: 92 us, 5.4 TB/s (angles worked out for each head of K and Q's
-// loads in registers: 109); one token for 32 sequences 4.9 us in a row, the chain length, table, page,
-// scale.
+// and p.hk heads of V; the others: tokens and heads of Q.  Bound by the memory: 4 prompts of up to 8192
+// tokens, 32/8 heads, d = 128, norms: 90 us, 5.5 TB/s, in pages of 16 126, of 128 115 (angles worked out for each head of K and Q's
+// loads in registers: 109; Q in a launch of its own with six blocks an SM: 93; a head of K and of V a
+// block, pages of 16: 154); one token for 32
+// sequences 4.9 us in a row, the chain length, table, page, scale.
 template <int D, bool INTER>
 __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_rope_kernel(const CacheAppendRopeParams p) {
     __shared__ union Shared {
@@ -207,17 +208,20 @@ __global__ void __launch_bounds__(kAppendThreads, 4) cache_append_rope_kernel(co
     if (x < p.page_blocks) {
         const bool is_v = x >= p.k_blocks;
         const unsigned y = is_v ? x - p.k_blocks : x, of_page = y / p.pages, slot = y - of_page * p.pages;
-        const unsigned parts = is_v ? p.c.Hk : p.k_parts, b = of_page / parts, part = of_page - b * parts;
+        const unsigned b = of_page / p.parts, part = of_page - b * p.parts;
         if (slot == 0 && part == 0 && !is_v && threadIdx.x == 0) check_len(p.c.c, p.c.st, static_cast<int>(b));
         AppendPage a;
         if (!append_page(p.c, static_cast<int>(b), static_cast<int>(slot), a)) return;
-        if (is_v) {
-            append_plain<D>(p.c, a, static_cast<int>(b), static_cast<int>(part), true);
-        } else {
-            const int hk = static_cast<int>(part) * p.hk;
-            append_rotated<D, INTER>(p, a, static_cast<int>(b), hk, min(hk + p.hk, p.c.Hk), sm.keys);
+        const int hk = static_cast<int>(part) * p.hk, hk_end = min(hk + p.hk, p.c.Hk);
+        if (!is_v) {
+            append_rotated<D, INTER>(p, a, static_cast<int>(b), hk, hk_end, sm.keys);
+            return;
         }
-        return;
+        for (int h = hk;;) {
+            append_plain<D>(p.c, a, static_cast<int>(b), h, true);
+            if (++h == hk_end) return;
+            __syncthreads();  // the head's largest magnitudes have been read
+        }
     }
     const unsigned y = x - p.page_blocks, rest = y / p.token_tiles, tile = y - rest * p.token_tiles;
     const unsigned b = rest / p.chunks, chunk = rest - b * p.chunks;
@@ -240,16 +244,15 @@ cudaError_t launch_append_rope_d(CacheAppendRopeParams p, cudaStream_t stream) {
         p.chunks = static_cast<unsigned>((p.H + HT * p.hp - 1) / (HT * p.hp));
         if (p.hp == 1 || static_cast<long long>(p.token_tiles) * p.chunks * c.B >= 3ll * sms) break;
     }
-    for (p.hk = c.Hk < 4 ? c.Hk : 4;; p.hk = (p.hk + 1) / 2) {  // and as many heads of K a block
-        p.k_parts = static_cast<unsigned>((c.Hk + p.hk - 1) / p.hk);
-        if (p.hk == 1 || static_cast<long long>(p.pages) * p.k_parts * c.B >= 4ll * sms) break;
+    for (p.hk = c.Hk < kPageHeads ? c.Hk : kPageHeads;; p.hk = (p.hk + 1) / 2) {  // and as many heads of K and V a block
+        p.parts = static_cast<unsigned>((c.Hk + p.hk - 1) / p.hk);
+        if (p.hk == 1 || static_cast<long long>(p.pages) * p.parts * c.B >= 4ll * sms) break;
     }
-    const long long k_blocks = static_cast<long long>(p.pages) * p.k_parts * c.B;
-    const long long page_blocks = k_blocks + static_cast<long long>(p.pages) * c.Hk * c.B;
-    const long long blocks = page_blocks + static_cast<long long>(p.token_tiles) * p.chunks * c.B;
+    const long long k_blocks = static_cast<long long>(p.pages) * p.parts * c.B;
+    const long long blocks = 2 * k_blocks + static_cast<long long>(p.token_tiles) * p.chunks * c.B;
     if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     p.k_blocks = static_cast<unsigned>(k_blocks);
-    p.page_blocks = static_cast<unsigned>(page_blocks);
+    p.page_blocks = 2 * p.k_blocks;
     const dim3 grid(static_cast<unsigned>(blocks));
     return p.r.interleaved ? launch_dependent(cache_append_rope_kernel<D, true>, grid, kAppendThreads, 0, stream, p)
                            : launch_dependent(cache_append_rope_kernel<D, false>, grid, kAppendThreads, 0, stream, p);

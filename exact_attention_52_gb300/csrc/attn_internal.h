@@ -202,7 +202,7 @@ struct CacheAppendRopeParams {
     int H;
     // Set by the launcher:
     int token_slots, hp, hk;
-    unsigned pages, k_parts, k_blocks, page_blocks, token_tiles, chunks;
+    unsigned pages, parts, k_blocks, page_blocks, token_tiles, chunks;
 };
 
 // What the joining kernel of the cache attention finds at the border before a CTA's share.
