@@ -284,6 +284,7 @@ struct PromptWalk {
     PromptShare s;
     PromptUnit u;
     int pairs, b, pair, hk;
+    int known;   // u is that of (b, pair)
     int v0, v1;  // key tiles [v0, v1) of the item
     int a0, a1;  // those that softmax group g takes: the first a_g, or (dual) v0 + g, v0 + g + 2, ...
 };
@@ -293,15 +294,17 @@ __device__ __forceinline__ bool next_segment(const CacheFwdParams& p, PromptWalk
     PromptWalk w = *walk;
     __syncwarp();
     if (w.s.unit < 0 || w.s.x >= w.s.x_end) return false;
-    w.u = unit_of<PART>(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
+    if (!w.known) w.u = unit_of<PART>(p, w.b, w.pair);
+    w.known = 1;
     for (long long n; w.s.x >= w.s.unit_first + (n = static_cast<long long>(w.u.n) * p.Hk);) {
         w.s.unit_first += n;
         // (the units of a group behind its last rows are passed over at once)
-        w.s.unit = PART == kPrefix && n == 0 ? (w.s.unit / w.pairs + 1) * w.pairs : w.s.unit + 1;
-        w.u = unit_of<PART>(p, w.s.unit / w.pairs, w.s.unit % w.pairs);
+        if (++w.pair == w.pairs || (PART == kPrefix && n == 0)) {
+            w.pair = 0;
+            ++w.b;
+        }
+        w.u = unit_of<PART>(p, w.b, w.pair);
     }
-    w.b = w.s.unit / w.pairs;
-    w.pair = w.s.unit - w.b * w.pairs;
     w.hk = static_cast<int>(div_mostly32(w.s.x - w.s.unit_first, w.u.n));
     w.v0 = static_cast<int>((w.s.x - w.s.unit_first) - static_cast<long long>(w.hk) * w.u.n);
     w.v1 = static_cast<int>(min(static_cast<long long>(w.u.n), w.v0 + (w.s.x_end - w.s.x)));
@@ -378,6 +381,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
         if (lane == 0 && (warp < 10 || warp >= 12)) {
             walk->s = share;
             walk->pairs = pairs;
+            walk->b = share.unit / pairs;
+            walk->pair = share.unit - walk->b * pairs;
+            walk->known = 0;
         }
         __syncwarp();
     }
