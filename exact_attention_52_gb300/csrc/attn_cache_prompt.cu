@@ -19,7 +19,7 @@
 // about 3700 cycles, of which 2048 are products and 1650 the pass of one tile's softmax;
 // the products' operands (S 128 bytes a cycle, PV 64) and the converters' writes together
 // fill what shared memory gives.  2 x 2048 queries over 16384 keys (32/8 heads): d = 128
-// 600 us, 1.2 PFLOP/s; d = 64 488 us, 0.73 (the same softmax, half the products).  Codes are
+// 596 us, 1.2 PFLOP/s; d = 64 485 us, 0.74 (the same softmax, half the products).  Codes are
 // turned into f16 and not used as E4M3 operands, because then Q and the weights would have to
 // be E4M3 too (2^-4 relative).  A page's scales enter in fp32 as in the kernel for few
 // queries: score * key scale, + log2 of the value scale in the exponent, and 1 / value scale in
