@@ -14,6 +14,7 @@ from oracle import rope as rope_oracle
 from oracle import streaming
 
 from .test_gpu_cache import Pool, bf16, check_clean, check_out, i32
+from .test_gpu_debug_checks import debug_library
 from .test_gpu_rope import THETA, table_of
 
 pytestmark = pytest.mark.gpu
@@ -96,6 +97,15 @@ def test_prefix_matches_oracle(shape, layout, d):
     B, H, Hk, T, page, firsts, prefixes, lens, ql = shape
     pool = shared_pool(7 * B + T, B, Hk, d, page, firsts, prefixes, lens, layout == "bnhd")
     run(pool, H, T, firsts, prefixes, lens, ql, layout)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_range_checked_build(d):
+    """The library whose tensor-memory accesses and product operands are checked finds nothing."""
+    with debug_library():
+        for shape in (SHAPES[4], SHAPES[9], SHAPES[10]):
+            B, H, Hk, T, page, firsts, prefixes, lens, ql = shape
+            run(shared_pool(B + d, B, Hk, d, page, firsts, prefixes, lens), H, T, firsts, prefixes, lens, ql)
 
 
 @pytest.mark.parametrize("T", [1, 14, 30])
