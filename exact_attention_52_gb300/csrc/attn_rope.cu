@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdBlocks) rope_norm_bwd_kernel
         x = static_cast<const uint4*>(p.x[which]) + (k.b * p.xs[which].b + k.n * p.xs[which].n) / 8 + k.h * xh;
         dy = static_cast<const uint4*>(p.dy[which]) + (k.b * p.gs[which].b + k.n * p.gs[which].n) / 8 + k.h * gh;
     };
-    Walk ahead, k;
+    Walk ahead = {}, k;
     long long copied = u0;
     int to_slot = 0;
     auto copy = [&] {
