@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -668,6 +669,8 @@ attn_status cache_fwd_params(const attn_cache_t* cache, const void* q, attn_stri
     p.items = nullptr;
     p.fin_o = nullptr;
     p.fin_stat = nullptr;
+    p.open = nullptr;
+    p.call = 0;
     p.rows = p.grid = 0;
     return ATTN_OK;
 }
@@ -713,7 +716,7 @@ struct PrefixLayout {
     struct Part {
         size_t segments, items, fin_o, fin_stat;
     } prefix, rest;
-    size_t total;
+    size_t open, total;
 };
 PrefixLayout prefix_layout(int B, int H, int Hk, int T, int d) {
     const size_t rows = static_cast<size_t>(B) * T * H, group_rows = static_cast<size_t>(T) * (H / Hk);
@@ -736,8 +739,15 @@ PrefixLayout prefix_layout(int B, int H, int Hk, int T, int d) {
     // least 8 rows of each sequence
     L.prefix = part(true, (B * group_rows / kPromptRows + B + 1) * Hk);
     L.rest = part(false, static_cast<size_t>(B) * Hk * ((group_rows + 7) / 8));
+    L.open = take(sizeof(unsigned long long));
     L.total = at;
     return L;
+}
+// A call's number, which no data of a workspace holds by chance: its upper half is a NaN that no
+// arithmetic gives, as fp32 and as bf16.
+unsigned long long call_number() {
+    static std::atomic<unsigned long long> calls{0};
+    return 0x7FA97FA900000000ull ^ calls.fetch_add(1, std::memory_order_relaxed);
 }
 void prefix_part(CacheFwdParams* p, uint8_t* workspace, const PrefixLayout::Part& L, bool prompt) {
     cache_segments(p, workspace + L.segments, prompt);
@@ -1179,6 +1189,8 @@ attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* grou
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
     const PrefixLayout L = prefix_layout(B, H, Hk, T, d);
+    p.open = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + L.open);
+    p.call = call_number();
     CacheFwdParams rest = p;
     prefix_part(&p, static_cast<uint8_t*>(workspace), L.prefix, true);
     prefix_part(&rest, static_cast<uint8_t*>(workspace), L.rest, false);

@@ -302,11 +302,8 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
 
     pdl_launch_dependents();
     // The rest of the sequences does not need the launch before it, which is that of the prefixes:
-    // its CTAs begin as those of the prefixes end, and wait for all of them before they end.  (The
-    // launch of the prefixes let this one begin after everything before it was there; the fence drops
-    // what an SM may have cached from before that.)
-    if constexpr (PART == kRest) __threadfence();
-    else pdl_wait();
+    // its CTAs begin as those of the prefixes end, and wait for all of them before they end.
+    if (PART != kRest || !opened(p)) pdl_wait();
     const Share sh = p.B <= kFewSeqs ? find_share_few<PART>(p, blockIdx.x) : find_share<PART>(p, blockIdx.x, ssm);
     if (sh.b < 0) {  // more CTAs than shares
         if constexpr (PART == kRest) pdl_wait();
@@ -384,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, DecodeTraits<D, NT>::CTAS_PER_SM) ca
             if (i < n_my) {
                 tok = cache_block(s, v0 + warp + kWarps * i) * kBlock + (lane & 1) * kTok;
                 if (tok < s.len && (tok + kTok > s.key_lo || tok < p.sinks)) {
-                    const int pid = cache_page(p.c, p.st, b, tok);
+                    const int pid = cache_page<PART>(p.c, p.st, b, tok);
                     const int slot = tok & (p.c.page_size - 1);
                     koff = pid * p.c.ks.b + slot * kn;
                     voff = pid * p.c.vs.b + slot * vn;
                     const long long at = static_cast<long long>(pid) * p.Hk + hk;
-                    sk_next = __ldg(p.c.k_scale + at);
-                    sv_next = __ldg(p.c.v_scale + at);
+                    sk_next = load_cache<PART>(p.c.k_scale + at);
+                    sv_next = load_cache<PART>(p.c.v_scale + at);
                     all = tok + kTok <= s.len && (tok >= s.key_lo || tok + kTok <= p.sinks);
                     // every query sees all of the tile
                     whole = tok + kTok - 1 <= first_pos &&
@@ -944,7 +941,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) cache_merge_kernel(const Cac
     const long long bt = in ? div_mostly32(row, p.H) : 0;
     const int h = in ? static_cast<int>(row - bt * p.H) : 0, b = static_cast<int>(div_mostly32(bt, p.T));
     const int t = static_cast<int>(bt - static_cast<long long>(b) * p.T), hk = h / G;
-    __threadfence();  // (see the kernel for few queries)
+    if (!opened(p)) pdl_wait();
     const int queries = query_count(p, b), g = group_of(p, b), start = g < 0 ? 0 : group_len(p, g);
     if (in && t == 0 && h == 0 && lane == 0 && g >= 0) {
         // every new query stands behind its group's prefix, and that within the table
@@ -960,6 +957,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) cache_merge_kernel(const Cac
     const int2* own_item = m.parts[1].items + (static_cast<long long>(b) * p.Hk + hk) * most_row_tiles(p) + own_tile;
     const int2* shared_item = m.parts[0].items + (start > 0 ? static_cast<long long>(group_tile(p, g) + shared_tile) * p.Hk + hk : 0);
     pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) shut_rest(p);
     if (!in || t >= queries) return;
     const int2 own = *own_item, shared = start > 0 ? *shared_item : make_int2(0, -1);
     const int n0 = shared.y - shared.x + 1, n = n0 + own.y - own.x + 1;  // segments: the prefix's, then the others

@@ -324,6 +324,7 @@ template <int D, CachePart PART>
 __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const CacheFwdParams p, const int pairs) {
     using T = PromptTraits<D>;
     pdl_wait();
+    if (PART == kPrefix && blockIdx.x == 0 && threadIdx.x == 0) open_rest(p);
     extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* sKV = smem + T::OFF_KV;

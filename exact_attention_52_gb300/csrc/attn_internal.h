@@ -252,6 +252,8 @@ struct CacheFwdParams {
     int2* items;      // first and last CTA of each item
     float* fin_o;     // rows of items that one CTA did, as unfinished segments: fp32 [B, T, H, D]
     float2* fin_stat;  // [B, T, H]
+    unsigned long long* open;  // holds `call` once what was written before the call is there
+    unsigned long long call;
     DevStatus st;
 };
 

@@ -1,0 +1,120 @@
+"""attn_fwd_cache_prefix in two parts as a server runs it: what the call reads is written just before it.
+Results are compared bit for bit with those of calls that have the device to themselves, or with the
+fp64 oracle (tolerances: test_gpu_cache)."""
+
+import numpy as np
+import pytest
+
+from exact_attention_52_gb300 import api
+
+from .test_gpu_cache import check_clean, i32
+from .test_gpu_prefix import shared_pool, wide
+
+pytestmark = pytest.mark.gpu
+
+
+def versions(n):
+    """Inputs of n calls of the same sizes, and the pools' tensors on the device."""
+    import torch
+    B, H, Hk, T, d, page = 12, 16, 2, 2, 128, 64
+    out = []
+    for i in range(n):
+        rng = np.random.default_rng(100 + i)
+        firsts = [0, 5 + i % 3, 12]
+        prefixes = [256 + 128 * (i % 3), 512 - 128 * (i % 2)]
+        lens = [prefixes[b >= firsts[1]] + T + int(rng.integers(0, 200)) for b in range(B)]
+        pool = shared_pool(200 + i, B, Hk, d, page, firsts, prefixes, lens)
+        table = np.full((B, 16), 10 ** 6, dtype=np.int32)
+        table[:, :pool.table.shape[1]] = pool.table
+        pages = 16 * B + 3
+        k, v = (np.zeros((pages, Hk, page, d), dtype=np.uint8) for _ in range(2))
+        ks, vs = (np.ones((pages, Hk)) for _ in range(2))
+        for big, small in ((k, pool.k), (v, pool.v), (ks, pool.ks), (vs, pool.vs)):
+            big[:small.shape[0]] = small
+        pool.table = table
+        ql = [int(x) for x in rng.integers(1, T + 1, B)]
+        out.append([torch.randn(B, H, T, d, device="cuda").bfloat16(), *(torch.from_numpy(x).cuda() for x in (k, v)),
+                    *(torch.from_numpy(x).float().cuda() for x in (ks, vs)), i32(wide(table, pool)), i32(lens), i32(prefixes),
+                    i32(firsts), i32(ql)])
+    return out
+
+
+def call(x, **kw):
+    return api.fwd_cache_prefix(*x[:8], group_first=x[8], q_lens=x[9], **kw)
+
+
+def outputs(like):
+    import torch
+    return torch.zeros_like(like[0]), torch.zeros(like[0].shape[:3], device="cuda")
+
+
+def check_same(got, ref):
+    import torch
+    assert torch.equal(got[0].view(torch.int16), ref[0].view(torch.int16))
+    assert torch.equal(got[1].view(torch.int32), ref[1].view(torch.int32))
+
+
+def references(data):
+    import torch
+    refs = []
+    for x in data:
+        o, lse = outputs(x)
+        torch.cuda.synchronize()
+        call(x, o=o, lse=lse)
+        torch.cuda.synchronize()
+        refs.append((o, lse))
+    check_clean()
+    return refs
+
+
+def test_a_call_sees_what_was_written_just_before_it():
+    """Every input changes between calls that follow each other without a pause, and calls of another
+    kind share the workspace that is kept for the stream."""
+    import torch
+    data = versions(4)
+    refs = references(data)
+    live, got = [t.clone() for t in data[0]], []
+    for step in range(40):
+        for t, new in zip(live, data[step % 4]):
+            t.copy_(new)
+        o, lse = outputs(live)
+        call(live, o=o, lse=lse)
+        got.append((o, lse))
+        if step % 3 == 0:
+            api.fwd_cache(*live[:7], q_lens=live[9])
+    for step, x in enumerate(got):
+        check_same(x, refs[step % 4])
+    check_clean()
+
+
+def test_captured_calls_that_share_a_workspace():
+    """Two graphs, each of copies and calls, replayed in turn with one workspace, which other calls write
+    over in between; a replayed call is the same call again."""
+    import torch
+    data = versions(4)
+    refs = references(data)
+    B, H, T, d = data[0][0].shape
+    ws = torch.full((api.fwd_cache_prefix_workspace_bytes(B, H, 2, T, d),), 255, dtype=torch.uint8, device="cuda")
+    live, graphs = [t.clone() for t in data[0]], []
+    call(live, workspace=ws)
+    torch.cuda.synchronize()
+    for pair in ((0, 1), (2, 3)):
+        g, outs = torch.cuda.CUDAGraph(), [outputs(live) for _ in pair]
+        with torch.cuda.graph(g):
+            for i, (o, lse) in zip(pair, outs):
+                for t, new in zip(live, data[i]):
+                    t.copy_(new)
+                call(live, o=o, lse=lse, workspace=ws)
+        graphs.append((g, pair, outs))
+    for step in range(12):
+        g, pair, outs = graphs[step % 2]
+        for o, lse in outs:
+            o.zero_(), lse.zero_()
+        g.replay()
+        for i, out in zip(pair, outs):
+            check_same(out, refs[i])
+        if step % 3 == 0:
+            ws.fill_(step)
+        elif step % 3 == 1:
+            call(data[step % 4], workspace=ws)
+    check_clean()
