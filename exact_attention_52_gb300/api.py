@@ -799,7 +799,8 @@ def cache_append(k, v, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens,
     page_table: int32 [B, max_pages]; seq_lens: int32 [B], tokens of each sequence after the
     call; new_lens: int32 [B], how many of the T tokens are new (default: all): token t goes to
     position seq_lens - new_lens + t.  A page's scale is a power of two that covers its largest
-    value and grows with it, the codes that are there being rounded again."""
+    value and grows with it, the codes that are there being rounded again: a page that is written to
+    belongs to one sequence."""
     import torch
     calls, dev, handle = _read(torch, stream, layout)
     if calls is not None:
@@ -1210,7 +1211,11 @@ def fwd_cache_prefix(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens
     """``fwd_cache`` for a batch whose sequences share their first tokens, which are read once for all.
 
     prefix_lens: int32 [groups], tokens whose pages the sequences of a group share (their tables
-    begin with the same pages); every query stands behind them.  group_first: int32 [groups + 1],
+    begin with the same pages); every query stands behind them.  A page that is still to be appended
+    to is no shared one: where a prompt ends inside a page, each sequence has a copy of that page (codes
+    and scales), and prefix_lens ends with the page before it (with pages of up to 128 tokens it may
+    be the whole prompt: the last prefix_lens % 128 tokens are read through each sequence's own
+    table).  group_first: int32 [groups + 1],
     ascending: group g is sequences group_first[g] .. group_first[g + 1] - 1 (default: one group of
     all).  Both stay on the device, as the lengths do.  ``workspace``:
     ``fwd_cache_prefix_workspace_bytes`` bytes, one for each call that may overlap.  The rest, and what

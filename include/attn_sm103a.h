@@ -469,8 +469,13 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
  *   group_first : int32 [groups + 1] on the device, ascending, within [0, B]; NULL with groups =
  *              1: the whole batch.  Sequences of no group share nothing.
  *   prefix_lens : int32 [groups] on the device, 0 .. max_pages * page_size, any number (the
- *              last prefix_lens % 128 tokens are read for each sequence).  The first sequence
- *              of a group that has queries stands for all: its table is read.
+ *              last prefix_lens % 128 tokens are read for each sequence, through its own table).
+ *              The first sequence of a group that has queries stands for all: its table is read.
+ *              A page that is still to be appended to belongs to one sequence (see
+ *              attn_cache_append), so full pages are shared: where a shared prompt ends inside a
+ *              page, each sequence gets a copy of that page, its codes and scales, and prefix_lens
+ *              is the tokens of the full pages before it (with pages of up to 128 tokens the whole
+ *              prompt will do: the copies lie behind its last whole 128).
  *   groups   : 1 .. B.
  *   workspace : attn_fwd_cache_prefix_workspace_bytes() bytes, 256-byte aligned, overwritten;
  *              calls that may overlap need one each.

@@ -7,7 +7,9 @@ import pytest
 
 from exact_attention_52_gb300 import api
 
-from .test_gpu_cache import check_clean, i32
+from oracle import streaming
+
+from .test_gpu_cache import bf16, check_clean, check_out, i32
 from .test_gpu_prefix import shared_pool, wide
 
 pytestmark = pytest.mark.gpu
@@ -118,3 +120,42 @@ def test_captured_calls_that_share_a_workspace():
         elif step % 3 == 1:
             call(data[step % 4], workspace=ws)
     check_clean()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,prompt,shared", [(16, 300, 300), (64, 200, 200), (128, 320, 320), (128, 320, 256),
+                                                (256, 400, 256), (512, 1100, 1024), (1024, 900, 0)])
+def test_decoding_behind_a_prompt_that_ends_inside_a_page(page, prompt, shared, d):
+    """Full pages are shared; of the page in which the prompt ends each sequence has a copy, which its own
+    tokens go to, with values that make the page's scale grow at another step in each."""
+    import torch
+    B, H, Hk, steps = 6, 8, 2, 6
+    rng = np.random.default_rng(prompt + d)
+    full = prompt // page
+    pool = shared_pool(page + d, B, Hk, d, page, [0, B], [full * page], [prompt + 2 * steps] * B)
+    dev = pool.dev()
+    dev[4] = i32(wide(pool.table, pool))
+    new = lambda b, t, amp=1.0: torch.from_numpy((amp * rng.standard_normal((b, Hk, t, d))).astype(np.float32)).bfloat16().cuda()
+    # the prompt, as the first sequence's, and the copies of its last page
+    api.cache_append(new(1, prompt), new(1, prompt), *dev[:4], dev[4][:1], i32([prompt]))
+    for x in dev[:4]:
+        for b in range(1, B):
+            x[int(pool.table[b, full])] = x[int(pool.table[0, full])]
+    start = [x.clone() for x in dev[:4]]
+    lens = np.full(B, prompt)
+    for step in range(steps):
+        T = 1 + step % 2
+        k, v = new(B, T), new(B, T)
+        k[step] *= 1000.0
+        v[(step + 3) % B] *= 1000.0
+        lens = lens + T
+        seq = i32(lens)
+        api.cache_append(k, v, *dev, seq)
+        q, qv = bf16(rng, (B, H, T, d), amp=2.0 ** -10)  # scores of the large keys stay below 32
+        o, lse = api.fwd_cache_prefix(q, *dev, seq, i32([shared]))
+        check_clean()
+        kc, vc = (x.cpu().numpy() for x in dev[:2])
+        ks, vs = (x.double().cpu().numpy() for x in dev[2:4])
+        check_out(o, lse, streaming.cache_forward(qv, kc, vc, ks, vs, pool.table, lens, [T] * B, d ** -0.5))
+    for pid in pool.table[0, :full]:  # what is shared has stayed as it was
+        assert all(torch.equal(x[int(pid)], y[int(pid)]) for x, y in zip(dev[:4], start))
