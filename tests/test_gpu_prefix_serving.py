@@ -10,7 +10,7 @@ from exact_attention_52_gb300 import api
 from oracle import streaming
 
 from .test_gpu_cache import bf16, check_clean, check_out, i32
-from .test_gpu_prefix import shared_pool, wide
+from .test_gpu_prefix import run, shared_pool, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +159,39 @@ def test_decoding_behind_a_prompt_that_ends_inside_a_page(page, prompt, shared, 
         check_out(o, lse, streaming.cache_forward(qv, kc, vc, ks, vs, pool.table, lens, [T] * B, d ** -0.5))
     for pid in pool.table[0, :full]:  # what is shared has stayed as it was
         assert all(torch.equal(x[int(pid)], y[int(pid)]) for x, y in zip(dev[:4], start))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,T", [(65, 8, 1), (70, 4, 2), (200, 8, 1), (200, 32, 3)])
+def test_more_sequences_than_a_warp_takes(B, H, T, d):
+    """Above 64 sequences a block's threads find its share together, above 128 with several sequences
+    each; lengths are ragged, slots are empty, a group may be."""
+    rng = np.random.default_rng(B + T + d)
+    cuts = sorted(int(x) for x in rng.integers(0, B + 1, 4))
+    firsts = [0, *cuts, cuts[-1], B]  # an empty group
+    prefixes = [int(x) for x in rng.choice([128, 256, 300, 640], len(firsts) - 1)]
+    ql = [int(x) for x in rng.integers(0, T + 1, B)]
+    lens = [0] * B
+    for g, n in enumerate(prefixes):
+        for b in range(firsts[g], firsts[g + 1]):
+            lens[b] = n + T + int(rng.integers(0, 250)) if ql[b] or rng.integers(0, 2) else 0
+    pool = shared_pool(B, B, 2, d, 32, firsts, prefixes, lens)
+    run(pool, H, T, firsts, prefixes, lens, ql)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("groups,B", [(33, 240), (64, 400), (100, 610)])
+def test_more_groups_than_lanes(groups, B, d):
+    """More than 32 groups: a lane of the prefixes' launch adds several up.  Some are empty, some share
+    nothing, some have more than a pair of query tiles."""
+    rng = np.random.default_rng(groups + d)
+    inner = sorted(int(x) for x in rng.integers(0, B - 130, groups - 2))
+    firsts = [0, *inner, B - 129, B]  # 129 sequences of 2 rows in the last group
+    prefixes = [int(x) for x in rng.choice([0, 100, 128, 200, 384], groups - 1)] + [256]
+    ql = [int(x) for x in rng.integers(0, 2, B)]
+    lens = [0] * B
+    for g, n in enumerate(prefixes):
+        for b in range(firsts[g], firsts[g + 1]):
+            lens[b] = n + 1 + int(rng.integers(0, 40))
+    pool = shared_pool(groups, B, 1, d, 16, firsts, prefixes, lens)
+    run(pool, 2, 1, firsts, prefixes, lens, ql)
