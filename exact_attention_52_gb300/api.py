@@ -1208,7 +1208,11 @@ def fwd_cache_prefix_workspace_bytes(B: int, H: int, Hk: int, T: int, d: int) ->
 def fwd_cache_prefix(q, k_pages, v_pages, k_scale, v_scale, page_table, seq_lens, prefix_lens, group_first=None,
                      q_lens=None, layout: str = "bhnd", scale: float | None = None, o=None, lse=None, workspace=None,
                      stream=None):
-    """``fwd_cache`` for a batch whose sequences share their first tokens, which are read once for all.
+    """``fwd_cache`` for a batch whose sequences share their first tokens, which are read once for all
+    where that pays: with at most 64 rows a sequence and key/value head (T * H / Hk), groups of six
+    sequences or more on average, and a table that can hold 256 MB of keys and values.  Elsewhere the call
+    is ``fwd_cache``.  Unused columns of the table count: hand in page_table[:, :n] with the columns that
+    the longest sequence needs.
 
     prefix_lens: int32 [groups], tokens whose pages the sequences of a group share (their tables
     begin with the same pages); every query stands behind them.  A page that is still to be appended

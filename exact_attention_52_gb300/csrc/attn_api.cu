@@ -696,13 +696,19 @@ attn_status cache_whole(CacheFwdParams* p, void* workspace, attn_stream_t stream
 }
 
 // Whether a batch behind shared prefixes is done in two parts, the prefixes for their groups and the
-// rest, or like any other.  Prompts are bound by their products, which sharing does not lessen (2 x
-// 2048 queries behind 16384 tokens: 1.32 ms in two parts, 0.93 in one).  Keys of a small cache come
+// rest, or like any other.  The rest is for the kernel of few queries, so calls with more rows than that
+// takes are done in one part.  To prompts that is no loss: they are bound by their products, which
+// sharing does not lessen (2 x 2048 queries behind 16384 tokens: 1.32 ms in two parts, 0.93 in one).  Rows
+// that fill a part of a tile would gain by sharing tiles and the keys' conversion, too: a step that is open
+// (4 heads, d = 128, behind 32768 tokens: 8 sequences of 64 rows, in two parts, 59 us, of 72 and 128 rows, in one,
+// 109 and 111; 32 sequences 159, 357 and 363; 64 sequences 283, 694 and 700).  Keys of a small cache come
 // out of the L2 again sooner than the two parts' launches take, and the kernel of the prefixes takes a
-// key in the time in which the other one reads it five times.  One part and two, 8 heads, d = 128,
-// 300 tokens of their own: 8 x 4096 tokens (68 MB) 18 and 29 us, 32 x 4096 (274) 37 and 34, 8 x 16384
-// (260) 33 and 37, 32 x 16384 108 and 41, 128 x 16384 412 and 89; 2 x 65536 (257) 42 and 76, 8 x 65536
-// 99 and 78.  The lengths are on the device; the longest that the table can hold stands for them.
+// key in the time in which the other one reads it five times.  One part and two, 8 heads of 4 queries, d = 128,
+// 300 tokens of their own: 8 x 4096 tokens (72 MB with those) 18 and 30 us, 32 x 4096 (288) 38 and 34, 8 x 16384
+// (273) 36 and 36, 32 x 16384 111 and 40, 128 x 16384 416 and 89; 2 x 65536 (270) 46 and 74, 5 x 65536
+// 75 and 74, 6 x 65536 88 and 74, 8 x 65536 111 and 75.  The lengths are on the device; the longest that the
+// table can hold stands for them, so unused columns of a table count (8 x 4096 with a table four times as
+// wide: 29 us), as does a prefix of less than a tile (64 x 64 tokens: 16 and 21 us).
 constexpr long long kPrefixMinBytes = 256ll << 20;
 constexpr int kPrefixMinMembers = 6;  // sequences of a group, on average
 bool prefix_parts(const attn_cache_t* c, int groups, int B, int H, int Hk, int T, int d) {

@@ -773,8 +773,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) cache_prompt_kernel(const C
                 // previous segment's last S_g, read here, came after every product on it.
                 // A row takes D / 8 lanes, the same for the copy and for the conversion in place: all of
                 // the copies are out at once (Q comes after the first keys' loads: 1600 to 3000 cycles),
-                // and the code is short (what runs once a segment runs at the pace at which its
-                // instructions come from the L2).
+                // and the code is short (unrolled, what runs once a segment took longer).
                 constexpr int LPR = D / 8, RPI = 32 / LPR;
                 const unsigned there = __ballot_sync(0xffffffffu, row_ok);
                 const unsigned long long src = reinterpret_cast<unsigned long long>(

@@ -482,10 +482,13 @@ attn_status attn_fwd_cache(const attn_cache_t* cache, const void* q, attn_stride
  * Every query has to stand behind its group's prefix.  A sequence with queries whose seq_lens[b] -
  * q_lens[b] is smaller (but for the last prefix_lens % 128 tokens) has undefined rows, and it, or a
  * prefix length outside the table, makes the next attn_check_device_error() return ATTN_ERR_PAGE.
- * Where sharing does not pay -- prompts (T * H / Hk above 64), groups of fewer than six sequences
- * on average, and caches of which the table can hold less than 256 MB -- the call is
+ * Three cases share nothing: more than 64 rows a sequence and key/value head (T * H / Hk),
+ * groups of fewer than six sequences on average, and caches of which the table can hold less
+ * than 256 MB (2 * d * Hk * B * max_pages * page_size).  There the call is
  * attn_fwd_cache: it does not look at groups and prefixes, and those errors do not occur.
- * Otherwise three launches.  Errors as attn_fwd_cache.
+ * Otherwise three launches, also where the prefixes turn out to be short.  max_pages stands for
+ * the lengths, which are on the device: give the columns that the sequences need, not the width
+ * of a table laid out for longer ones (table_stride keeps that).  Errors as attn_fwd_cache.
  * Source: ai.engineer item 59 (small-query work split across thread blocks plus a separate
  * combining kernel); no page describes shared prefixes.
  */
