@@ -923,7 +923,10 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
               fastest not at all;
     "yarn"    (Peng et al., 2023) pairs that turn more than beta_fast times within original_len tokens
               stay, those that turn less than beta_slow times are stretched by the factor, those between
-              in proportion; elements are multiplied by 0.1 ln(factor) + 1."""
+              in proportion to their turns, as the paper's formula has it; elements are multiplied by
+              0.1 ln(factor) + 1.  Published models are often run with another ramp, over the pair's
+              index between two bounds rounded to whole pairs: the pairs between differ.  For such a
+              model give its own numbers to ``rope_table`` (frequencies, magnitude)."""
     if not isinstance(rot, int) or rot < 2 or rot % 2:
         raise ValueError(f"rot must be an even number of elements, got {rot!r}")
     if not (math.isfinite(base) and base > 0):
