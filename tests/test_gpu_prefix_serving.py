@@ -195,3 +195,21 @@ def test_more_groups_than_lanes(groups, B, d):
             lens[b] = n + 1 + int(rng.integers(0, 40))
     pool = shared_pool(groups, B, 1, d, 16, firsts, prefixes, lens)
     run(pool, 2, 1, firsts, prefixes, lens, ql)
+
+
+@pytest.mark.parametrize("compiled", [True, False])
+def test_the_columns_in_use_of_a_wide_table(compiled, monkeypatch):
+    """A view of a wide table's first columns is the narrow table: the same path and the same bits."""
+    import torch
+    if not compiled:
+        monkeypatch.setattr(api, "_read", lambda *a: (None, None, None))
+    lens = [300 + 11 * b for b in range(8)]
+    pool = shared_pool(41, 8, 2, 128, 64, [0, 8], [256], lens)
+    q, dev = torch.randn(8, 16, 1, 128, device="cuda").bfloat16(), pool.dev()
+    ref = api.fwd_cache(q, *dev, i32(lens))
+    whole = i32(wide(pool.table, pool))
+    check_same(api.fwd_cache_prefix(q, *dev[:4], whole[:, :dev[4].shape[1]], i32(lens), i32([256])), ref)
+    o, lse = api.fwd_cache_prefix(q, *dev[:4], whole, i32(lens), i32([256]))  # in two parts
+    check_clean()
+    host = [x.cpu().numpy() for x in dev[:2]] + [x.double().cpu().numpy() for x in dev[2:4]]
+    check_out(o, lse, streaming.cache_forward(q.double().cpu().numpy(), *host, pool.table, lens, [1] * 8, 128 ** -0.5))
