@@ -722,7 +722,7 @@ struct PrefixLayout {
     struct Part {
         size_t segments, items, fin_o, fin_stat;
     } prefix, rest;
-    size_t open, total;
+    size_t total;
 };
 PrefixLayout prefix_layout(int B, int H, int Hk, int T, int d) {
     const size_t rows = static_cast<size_t>(B) * T * H, group_rows = static_cast<size_t>(T) * (H / Hk);
@@ -745,7 +745,6 @@ PrefixLayout prefix_layout(int B, int H, int Hk, int T, int d) {
     // least 8 rows of each sequence
     L.prefix = part(true, (B * group_rows / kPromptRows + B + 1) * Hk);
     L.rest = part(false, static_cast<size_t>(B) * Hk * ((group_rows + 7) / 8));
-    L.open = take(sizeof(unsigned long long));
     L.total = at;
     return L;
 }
@@ -1195,11 +1194,12 @@ attn_status attn_fwd_cache_prefix(const attn_cache_t* cache, const int32_t* grou
     if ((rc = device_state(&ds)) != ATTN_OK) return rc;
     p.st = dev_status(ds);
     const PrefixLayout L = prefix_layout(B, H, Hk, T, d);
-    p.open = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + L.open);
     p.call = call_number();
     CacheFwdParams rest = p;
     prefix_part(&p, static_cast<uint8_t*>(workspace), L.prefix, true);
     prefix_part(&rest, static_cast<uint8_t*>(workspace), L.rest, false);
+    // (a part's launch writes no borders)
+    p.open = rest.open = reinterpret_cast<unsigned long long*>(p.border);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = launch_cache_prompt(&p, kPrefix, s);
     if (e == cudaSuccess) e = launch_cache_decode(&rest, kRest, s);
